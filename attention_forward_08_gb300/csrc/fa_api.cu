@@ -19,6 +19,7 @@
 
 #include "fa.h"
 #include "fa_bwd_launch.h"
+#include "fa_device.h"
 #include "fa_launch.cuh"
 
 namespace fa {
@@ -290,6 +291,24 @@ EncodeTiledFn get_encode_tiled() {
   }
   return g_encode;
 }
+
+int current_device(DeviceInfo* info) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) {
+    set_error("cudaGetDevice: %s", cudaGetErrorString(e));
+    return FA_ERR_CUDA;
+  }
+  const int rc = device_setup(dev);
+  if (rc != FA_OK) return rc;
+  info->dev = dev;
+  info->num_sms = g_num_sms[dev];
+  info->status = g_status_ptr[dev];
+  info->timeout_cycles = timeout_cycles();
+  return FA_OK;
+}
+
+void clear_error() { g_err[0] = '\0'; }
 
 int validate_bwd(const fa_bwd_args* a) {
   if (!(a->dropout_p >= 0.0f && a->dropout_p <= 1.0f)) {
@@ -622,6 +641,10 @@ int fa_sync_status(void* stream) {
   if (word & kStatusTimeout) {
     set_error("a kernel reached its wait bound and stopped early (status 0x%x)", word);
     return FA_ERR_DEVICE_TIMEOUT;
+  }
+  if (word & kStatusBadIndex) {
+    set_error("a cache call met a length or a table entry out of range and skipped the tokens behind it");
+    return FA_ERR_INVALID_ARGUMENT;
   }
   return FA_OK;
 }

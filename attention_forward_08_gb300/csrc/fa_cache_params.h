@@ -1,0 +1,81 @@
+// fa_cache_params.h -- parameter blocks of the 8-bit cache kernels (by value,
+// as kernel arguments) and the host functions that launch them.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "fa_params.h"
+
+namespace fa {
+
+// Pools, scales and the page table, as fa_cache.h describes them.
+struct CacheView {
+  uint8_t *k, *v;
+  float *k_scale, *v_scale;
+  long long ks[3], vs[3];  // byte strides: block, head, token
+  int P, H, page, D;
+  int page_log2;
+  const int* table;
+  long long table_stride;
+  int M;
+  unsigned int* status;
+};
+
+struct AppendParams {
+  CacheView c;
+  const void *k, *v;
+  long long ks[3], vs[3];  // element strides: batch, head, token
+  const int *lens, *n_new, *seen;
+  float* weights;
+  int* positions;
+  int B, n, W;
+  int spans;  // blocks that n tokens can touch
+};
+
+struct CacheAttnParams {
+  CacheView c;
+  const void* q;
+  void* o;
+  float* lse;
+  float* weights;
+  long long qs[3], os[3];  // element strides: batch, head, row
+  const int *lens, *n_q;
+  int B, Hq, group, n, W;
+  int causal, window;
+  float scale_log2;             // scale * log2(e)
+  float cap_in, cap_out;        // softcap: scale / cap and cap * log2(e); cap_out 0: off
+  long long timeout_cycles;
+  uint8_t* ws;                  // workspace
+};
+
+struct EvictParams {
+  CacheView c;
+  const int* lens;
+  float* weights;
+  int* positions;
+  const int* into;
+  long long into_stride;
+  float* weights_out;
+  int* positions_out;
+  int* lens_out;
+  int B, W, M_into, W_out;
+  int keep, recent;
+  // Workspace: what the choice tells the moves.
+  int* src;         // [B, H, keep]: the slot whose token ends in slot j; -1 - i: that of mover i (in place)
+  int* mover;       // [B, H, keep]: kept slots at `keep` and behind, in order (in place)
+  int* count;       // [B, H]: tokens kept; -1 - n: all n stay in place
+  float* edge;      // [B, H, 2]: scales, before the call, of the block that holds slot `keep`
+};
+
+struct LaunchCtx {
+  cudaStream_t stream;
+  int num_sms;
+};
+
+int launch_cache_append(const AppendParams& p, int kind, int dtype, const LaunchCtx& ctx);
+int launch_cache_attn(const CacheAttnParams& p, int kind, int dtype, const LaunchCtx& ctx);
+int launch_cache_evict(const EvictParams& p, int kind, const LaunchCtx& ctx);
+long long cache_attn_workspace(const CacheAttnParams& p, int num_sms);
+
+}  // namespace fa

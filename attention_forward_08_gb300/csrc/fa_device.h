@@ -1,0 +1,18 @@
+// fa_device.h -- what a host launcher needs to know about the current device,
+// and the calling thread's error message (both kept in fa_api.cu).
+#pragma once
+
+namespace fa {
+
+struct DeviceInfo {
+  int dev;
+  int num_sms;
+  unsigned int* status;      // the device status word (kStatus* bits)
+  long long timeout_cycles;  // bound on every wait, in SM clock cycles
+};
+
+int current_device(DeviceInfo* info);  // an fa_status; the message is set on error
+void set_error(const char* fmt, ...);
+void clear_error();
+
+}  // namespace fa
