@@ -1,0 +1,84 @@
+// fa_cache_decode_launch.cuh -- host side of cache_decode_kernel for one head
+// dim: tensor maps, grid, workspace.
+#pragma once
+
+#include <atomic>
+
+#include "fa.h"
+#include "fa_cache.h"
+#include "fa_cache_decode.cuh"
+#include "fa_cache_maps.h"
+#include "fa_device.h"
+
+namespace fa {
+
+template <class C>
+long long decode_workspace(int num_sms) {
+  const long long slots = 2LL * num_sms * C::kCtas * C::kRows;
+  return slots * C::kD * 4 + slots * 8;
+}
+
+template <class C>
+int launch_decode(const CacheAttnParams& a, const LaunchCtx& ctx) {
+  CUtensorMap tk, tv;
+  const int sub = a.c.page < C::kTile ? a.c.page : C::kTile;
+  if (!encode_pool(&tk, a.c, false, sub) || !encode_pool(&tv, a.c, true, sub)) return FA_ERR_CUDA;
+  auto kern = cache_decode_kernel<C>;
+  static std::atomic<unsigned long long> configured{0};
+  if (!((configured.load(std::memory_order_acquire) >> ctx.dev) & 1ull)) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) {
+      set_error("cudaFuncSetAttribute(max dynamic smem = %d): %s", C::kSmem, cudaGetErrorString(e));
+      return FA_ERR_CUDA;
+    }
+    configured.fetch_or(1ull << ctx.dev, std::memory_order_release);
+  }
+  DecParams p;
+  p.a = a;
+  p.rows = a.n * a.group;
+  p.row_groups = (p.rows + C::kRows - 1) / C::kRows;
+  p.max_ctas = ctx.num_sms * C::kCtas;
+  p.part_o = reinterpret_cast<float*>(a.ws);
+  p.part_ml = reinterpret_cast<float2*>(a.ws + 2LL * p.max_ctas * C::kRows * C::kD * 4);
+  kern<<<p.max_ctas, C::kThreads, C::kSmem, ctx.stream>>>(tk, tv, p);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) {
+    cache_join_kernel<C><<<dim3((unsigned)p.row_groups, (unsigned)a.c.H, (unsigned)a.B), 128, 0, ctx.stream>>>(p);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) {
+    set_error("cache attention launch failed: %s", cudaGetErrorString(e));
+    return FA_ERR_CUDA;
+  }
+  return FA_OK;
+}
+
+// 32 rows a block where 16 would not hold them (and the registers do).
+template <int kD, int kKind, bool kF16>
+int launch_decode_rows(const CacheAttnParams& a, const LaunchCtx& ctx) {
+  if constexpr (kD <= 128) {
+    if (a.n * a.group > 16) return launch_decode<DecCfg<kKind, kF16, kD, 2>>(a, ctx);
+  }
+  return launch_decode<DecCfg<kKind, kF16, kD, 1>>(a, ctx);
+}
+
+template <int kD>
+int launch_decode_d(const CacheAttnParams& a, int kind, bool f16, const LaunchCtx& ctx) {
+  if (kind == FA_CACHE_E4M3)
+    return f16 ? launch_decode_rows<kD, kKindE4m3, true>(a, ctx) : launch_decode_rows<kD, kKindE4m3, false>(a, ctx);
+  return f16 ? launch_decode_rows<kD, kKindInt8, true>(a, ctx) : launch_decode_rows<kD, kKindInt8, false>(a, ctx);
+}
+
+template <int kD>
+long long decode_workspace_d(const CacheAttnParams& a, int num_sms) {
+  if constexpr (kD <= 128) {
+    if (a.n * a.group > 16) return decode_workspace<DecCfg<0, false, kD, 2>>(num_sms);
+  }
+  return decode_workspace<DecCfg<0, false, kD, 1>>(num_sms);
+}
+
+int launch_decode_d64(const CacheAttnParams& a, int kind, bool f16, const LaunchCtx& ctx);
+int launch_decode_d128(const CacheAttnParams& a, int kind, bool f16, const LaunchCtx& ctx);
+int launch_decode_d256(const CacheAttnParams& a, int kind, bool f16, const LaunchCtx& ctx);
+
+}  // namespace fa

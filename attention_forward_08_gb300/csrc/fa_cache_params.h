@@ -71,6 +71,7 @@ struct EvictParams {
 struct LaunchCtx {
   cudaStream_t stream;
   int num_sms;
+  int dev;
 };
 
 int launch_cache_append(const AppendParams& p, int kind, int dtype, const LaunchCtx& ctx);
