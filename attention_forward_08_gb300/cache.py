@@ -189,8 +189,8 @@ def _foreign(device, stream):
 def _call(device, stream, work):
     """Run ``work(raw stream)`` on the cache's device and on the given or the current stream."""
     import torch
-    if stream is None and torch.cuda.current_device() == device.index:
-        return work(torch.cuda.current_stream(device).cuda_stream)
+    if stream is None and torch._C._cuda_getDevice() == device.index:
+        return work(torch._C._cuda_getCurrentRawStream(device.index))
     with _foreign(device, stream):
         return work(torch.cuda.current_stream(device).cuda_stream)
 

@@ -15,9 +15,10 @@
 // rescaling.  P is rounded to f16 (2^-11; the output has 2^-8 or 2^-11), its
 // sum is not.
 //
-// Work.  Every warp runs on its own: it takes tiles of 32 tokens, TMA brings
-// them into the warp's own ring, and running maximum, sum and output stay in
-// the warp's registers, so that no barrier stands between two tiles.  The
+// Work.  A producer warp brings tiles of 32 tokens into a ring by TMA, with
+// their scales; the other warps take turns at the tiles, and each keeps a
+// running maximum, sum and output of its own in registers, so that no barrier
+// stands between two tiles.  The
 // tiles of all (sequence, head, row group) segments form one line that is cut
 // into equal parts, one for each thread block, wherever the cuts fall:
 // sequences of any lengths load the machine evenly, and nothing is planned on
@@ -51,22 +52,36 @@ struct DecCfg {
   static constexpr bool kF16 = kF16_;  // type of q and o
   static constexpr int kD = kD_, kMT = kMT_;
   static constexpr int kTile = 32;  // tokens
-  static constexpr int kWarps = 4, kThreads = 32 * kWarps;
-  static constexpr int kCtas = kD == 256 ? 1 : 2;           // per SM
+  // Consumer warps a block, and blocks an SM: as many warps as the outputs
+  // that each holds (kMT * D / 2 registers a lane) leave room for.
+  static constexpr bool kWide = kMT * kD > 128;
+  static constexpr int kWarps = kWide ? 7 : 5;
+  static constexpr int kCtas = kWide ? 1 : 2;
+  static constexpr int kThreads = 32 * (kWarps + 1);        // and the producer warp
   static constexpr int kCols = kD >= 128 ? kD / 128 : 1;    // 128-byte column blocks of a row
   static constexpr int kRowBytes = kD >= 128 ? 128 : 64;    // of one column block
   static constexpr int kTileBytes = kTile * kD;             // K; V alike
-  static constexpr int kStages = kD == 64 ? 4 : 3;
   static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kStages = (kWide ? 196608 : 98304) / kStageBytes;  // ring of all warps; tile k goes to warp k % kWarps
   static constexpr int kRows = 16 * kMT;
   static constexpr int kKSteps = kD / 16, kNTiles = kD / 8;
   static constexpr int kQBytes = kRows * kD * 2;
-  static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-  // The warps join through the ring's memory: kWarps x (rows x D fp32), then maxima and sums.
+  static constexpr int kRingBytes = kStages * kStageBytes;
+  // The warps join through the ring's memory: kWarps x (rows x D fp32).
   static constexpr int kJoinBytes = kWarps * kRows * kD * 4;
-  static constexpr int kBulk = kRingBytes > kJoinBytes ? kRingBytes : kJoinBytes;
-  static_assert(kD != 256 || kMT == 1, "32 rows of 256 columns do not fit the registers");
-  static constexpr int kSmem = 1024 + kBulk + kQBytes + kWarps * kRows * 8 + kRows * 4 + kWarps * kStages * 8 + 128;
+  static_assert(kJoinBytes <= kRingBytes && kWarps < kStages && kStages <= 64, "ring size");
+  static_assert(kMT * kD <= 256, "32 rows of 256 columns do not fit the registers");
+  static constexpr int kOffQ = kRingBytes, kOffMl = kOffQ + kQBytes, kOffMeta = kOffMl + kWarps * kRows * 8;
+  static constexpr int kOffBar = kOffMeta + kStages * 32, kOffRs = kOffBar + kStages * 16;
+  static constexpr int kOffTmp = kOffRs + kRows * 4;
+  static constexpr int kSmem = 1024 + kOffTmp + 128;
+};
+
+// What a consumer needs beside a tile's bytes.
+struct DecMeta {
+  float ks[2], vs[2];  // scales of its two halves of 16 tokens
+  int ok;              // bit i: half i is there
+  int pad[3];
 };
 
 struct DecParams {
@@ -218,32 +233,66 @@ __device__ __forceinline__ int dec_col(int i, int n) {
 
 // ------------------------------------------------------------------ the kernel
 
+// Eight columns of one output row, and its L.
+template <class C>
+__device__ __forceinline__ void dec_write(const CacheAttnParams& a, int b, int h, int row, int d, const float (&x)[8],
+                                          float top, float sum) {
+  const int i = row / a.group, head = h * a.group + row % a.group;
+  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  uint4 y;
+  uint32_t* u = &y.x;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    u[e] = C::kF16 ? pack_f16x2(x[2 * e] * inv, x[2 * e + 1] * inv) : pack_bf16x2(x[2 * e] * inv, x[2 * e + 1] * inv);
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + b * a.os[0] + head * a.os[1] + i * a.os[2] + d) = y;
+  if (d == 0) a.lse[((long long)b * a.Hq + head) * a.n + i] = sum > 0.0f ? (top + log2f(sum)) * kDecLn2 : -INFINITY;
+}
+
+// A bounded wait by a whole warp; false once it ran out (or another did).
+__device__ __forceinline__ bool dec_wait(uint64_t* bar, uint32_t parity, volatile int* abort, const CacheAttnParams& a) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    const long long begin = clock64_now();
+    while (!ok) {
+      ok = mbar_try_wait(bar, parity);
+      if (!ok && (*abort || clock64_now() - begin > a.timeout_cycles)) break;
+    }
+  }
+  if (__all_sync(0xFFFFFFFFu, ok)) return true;
+  if (!*abort && (threadIdx.x & 31) == 0) atomicOr(a.c.status, kStatusTimeout);
+  *abort = 1;
+  return false;
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     cache_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                         const __grid_constant__ DecParams p) {
   const CacheAttnParams& a = p.a;
   const CacheView& c = a.c;
+  constexpr int kW = C::kWarps, kS = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  uint8_t* s_q = smem + C::kBulk;
-  float2* s_ml = reinterpret_cast<float2*>(s_q + C::kQBytes);             // [warp][row]
-  float* s_rs = reinterpret_cast<float*>(s_ml + C::kWarps * C::kRows);    // [row]: 2^-(scaling of the query row)
-  uint64_t* s_bar = reinterpret_cast<uint64_t*>(s_rs + C::kRows);         // [warp][stage]
-  long long* s_tmp = reinterpret_cast<long long*>(s_bar + C::kWarps * C::kStages);  // [4 warps], then the search
+  uint8_t* s_q = smem + C::kOffQ;
+  float2* s_ml = reinterpret_cast<float2*>(smem + C::kOffMl);        // [warp][row]: maximum, sum
+  DecMeta* s_meta = reinterpret_cast<DecMeta*>(smem + C::kOffMeta);  // [stage]
+  uint64_t* s_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* s_empty = s_full + kS;
+  float* s_rs = reinterpret_cast<float*>(smem + C::kOffRs);  // [row]: 2^-(scaling of the query row)
+  long long* s_tmp = reinterpret_cast<long long*>(smem + C::kOffTmp);  // one a warp, then the search's answer
+  volatile int* s_abort = reinterpret_cast<int*>(s_tmp + 12);
   float* s_join = reinterpret_cast<float*>(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  uint8_t* ring = smem + warp * C::kStages * C::kStageBytes;
-  uint64_t* bars = s_bar + warp * C::kStages;
-  if (lane == 0) {
-    for (int s = 0; s < C::kStages; ++s) mbar_init(bars + s, 1);
-    fence_barrier_init();
-  }
   if (tid == 0) {
+    for (int s = 0; s < kS; ++s) {
+      mbar_init(s_full + s, 1);
+      mbar_init(s_empty + s, 1);
+    }
+    fence_barrier_init();
+    *s_abort = 0;
     tma_prefetch_desc(&tk);
     tma_prefetch_desc(&tv);
   }
-  uint32_t phases = 0;  // parity of each stage's next wait
 
   // This block's part of the line, and where it begins.
   const long long total = dec_tiles_before<C>(p, a.B, s_tmp);
@@ -252,53 +301,53 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   const long long t0 = dec_start(total, ctas, blockIdx.x), t1 = dec_start(total, ctas, blockIdx.x + 1);
   int b = 0;
   long long before = 0;  // tiles before sequence b
-  for (int base = 0;; base += C::kThreads) {  // chunks of sequences, then inside the chunk
+  for (int base = 0;; base += C::kThreads) {  // a block of sequences at a time
     const int i = base + tid;
-    long long mine = i < a.B ? dec_seq_tiles<C>(p, i) : 0, upto = mine;
+    const long long mine = i < a.B ? dec_seq_tiles<C>(p, i) : 0;
+    long long upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long u = __shfl_up_sync(0xFFFFFFFFu, upto, o);
       if (lane >= o) upto += u;
     }
     if (lane == 31) s_tmp[warp] = upto;
-    if (tid == 0) s_tmp[4] = -1;
+    if (tid == 0) s_tmp[9] = -1;
     __syncthreads();
     long long off = before, all = before;
-    for (int w = 0; w < C::kWarps; ++w) {
+    for (int w = 0; w <= kW; ++w) {
       if (w < warp) off += s_tmp[w];
       all += s_tmp[w];
     }
     upto += off;
     if (mine > 0 && upto - mine <= t0 && t0 < upto) {
-      s_tmp[4] = i;
-      s_tmp[5] = upto - mine;
+      s_tmp[9] = i;
+      s_tmp[10] = upto - mine;
     }
     __syncthreads();
-    const long long hit = s_tmp[4];
+    const long long hit = s_tmp[9];
     if (hit >= 0) {
       b = (int)hit;
-      before = s_tmp[5];
+      before = s_tmp[10];
       break;
     }
     before = all;
     __syncthreads();
     if (base + C::kThreads >= a.B) return;  // not reached: t0 < total
   }
-
-  const int sub = min(c.page, C::kTile), subs = C::kTile / sub, sub_log2 = min(c.page_log2, 5);
   DecSeq seq = dec_seq(a, b);
-  if (blockIdx.x == 0 || before >= t0) {  // one block per sequence tells about lengths
-    if (tid == 0) (void)checked_len(c, a.lens[b]);
-  }
+  if (tid == 0 && before >= t0) (void)checked_len(c, a.lens[b]);  // one block a sequence tells about its length
   long long seg0 = before;  // first tile of the current segment
   int h = 0, rg = 0;
-  {  // advance to the segment of t0
+  {  // the segment of t0
     long long per_head = 0;
     for (int r = 0; r < p.row_groups; ++r) per_head += dec_tiles<C>(p, seq, r);
     h = (int)((t0 - seg0) / per_head);
     seg0 += h * per_head;
     while (seg0 + dec_tiles<C>(p, seq, rg) <= t0) seg0 += dec_tiles<C>(p, seq, rg++);
   }
+  const int sub = min(c.page, C::kTile), sub_log2 = min(c.page_log2, 5);  // a block's part of a tile
+  const int subs = C::kTile >> sub_log2;                                  // parts a tile: 1 or 2
+  int tile0 = 0;  // tiles of this block's earlier pieces: tile k of all uses stage k % kS
 
   for (long long at = t0; at < t1;) {
     const int r0 = rg * C::kRows, r1 = min(p.rows, r0 + C::kRows);
@@ -308,353 +357,319 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     const int n_tiles = (int)(min(t1, seg0 + tiles) - at);
     const bool whole = n_tiles == tiles;
 
-    // This warp's tiles: first_tile + warp, + kWarps, ...  Lane l looks up the
-    // sub-blocks (a block's part of a tile) of the tiles to come, 32 / subs
-    // tiles at a time, and their scales.
-    const int mine = n_tiles > warp ? (n_tiles - warp + C::kWarps - 1) / C::kWarps : 0;
-    const int per_batch = 32 / subs;
-    int look_blk = -1;
-    float look_ks = 0.0f, look_vs = 0.0f;
-    auto look_up = [&](int k0) {  // tiles k0 .. of this warp
-      const int k = k0 + (lane >> (subs - 1));
-      const int tok = (first_tile + warp + k * C::kWarps) * C::kTile + (lane & (subs - 1)) * sub;
-      look_blk = -1;
-      look_ks = look_vs = 0.0f;
-      if (k < mine && tok < span.y && tok + sub > span.x) {
-        look_blk = checked_block(c, c.table, c.table_stride, b, tok >> c.page_log2);
-        if (look_blk >= 0) {
-          look_ks = __ldg(c.k_scale + (long long)look_blk * c.H + h);
-          look_vs = __ldg(c.v_scale + (long long)look_blk * c.H + h);
+    if (warp == kW) {
+      // ---------------------------------------------------------- producer
+      // Lane l looks up part l of the next 32: its block, and the scales.
+      int stage = tile0 % kS;
+      uint32_t phase = (uint32_t)(tile0 / kS) & 1u;
+      const int per_batch = 32 / subs;
+      int blk = -1, issued = 0;
+      bool ok = true;
+      float ks = 0.0f, vs = 0.0f;
+      for (; issued < n_tiles && ok; ++issued) {
+        const int from = issued % per_batch * subs;
+        if (from == 0) {
+          const int k = issued + (lane >> (subs - 1));
+          const int tok = (first_tile + k) * C::kTile + (lane & (subs - 1)) * sub;
+          blk = -1;
+          ks = vs = 0.0f;
+          if (k < n_tiles && tok < span.y && tok + sub > span.x) {
+            blk = checked_block(c, c.table, c.table_stride, b, tok >> c.page_log2);
+            if (blk >= 0) {
+              ks = __ldg(c.k_scale + (long long)blk * c.H + h);
+              vs = __ldg(c.v_scale + (long long)blk * c.H + h);
+            }
+          }
         }
+        const int b0 = __shfl_sync(0xFFFFFFFFu, blk, from), b1 = __shfl_sync(0xFFFFFFFFu, blk, from + subs - 1);
+        const float k0 = __shfl_sync(0xFFFFFFFFu, ks, from), k1 = __shfl_sync(0xFFFFFFFFu, ks, from + subs - 1);
+        const float v0 = __shfl_sync(0xFFFFFFFFu, vs, from), v1 = __shfl_sync(0xFFFFFFFFu, vs, from + subs - 1);
+        if (tile0 + issued >= kS) ok = dec_wait(s_empty + stage, phase ^ 1u, s_abort, a);
+        if (!ok) break;
+        if (lane == 0) {
+          DecMeta* meta = s_meta + stage;
+          *reinterpret_cast<float4*>(meta) = make_float4(k0, k1, v0, v1);
+          meta->ok = (b0 >= 0 ? 1 : 0) | (b1 >= 0 ? 2 : 0);
+          const int boxes = (b0 >= 0) + (subs == 2 && b1 >= 0);
+          uint64_t* bar = s_full + stage;
+          if (boxes == 0) {
+            mbar_arrive(bar);
+          } else {
+            mbar_arrive_expect_tx(bar, (uint32_t)(boxes * sub * C::kD * 2));
+            uint8_t* dst = smem + stage * C::kStageBytes;
+            const int y = ((first_tile + issued) * C::kTile) & (c.page - 1);  // 0 where blocks are no longer than a tile
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int from_blk = u ? b1 : b0;
+              if (u < subs && from_blk >= 0) {
+#pragma unroll
+                for (int col = 0; col < C::kCols; ++col) {
+                  uint8_t* d = dst + (col * C::kTile + u * sub) * C::kRowBytes;
+                  tma_load_4d(d, &tk, bar, col * 128, y, h, from_blk);
+                  tma_load_4d(d + C::kTileBytes, &tv, bar, col * 128, y, h, from_blk);
+                }
+              }
+            }
+          }
+        }
+        if (++stage == kS) stage = 0, phase ^= 1u;
       }
-    };
-    // Sub-block `u` of this warp's tile k: its block (-1: none), by shuffle.
-    auto issue = [&](int k, int blk0, int blk1) {  // lane 0 only
-      const int s = k % C::kStages;
-      uint8_t* dst = ring + s * C::kStageBytes;
-      const int boxes = (blk0 >= 0) + (subs == 2 && blk1 >= 0);
-      if (boxes == 0) {
-        mbar_arrive(bars + s);
+      // After an expired wait: the copies in flight land first (a bounded wait
+      // again), then the block ends.
+      if (__syncthreads_or(0)) {
+        for (int k = max(0, tile0 + issued - kS); k < tile0 + issued; ++k) {
+          const long long begin = clock64_now();
+          while (!mbar_try_wait(s_full + k % kS, (uint32_t)(k / kS) & 1u) && clock64_now() - begin < kDecDrainCycles) {
+          }
+        }
         return;
       }
-      mbar_arrive_expect_tx(bars + s, (uint32_t)(boxes * sub * C::kD * 2));
-      const int row = ((first_tile + warp + k * C::kWarps) * C::kTile) & (c.page - 1);
+    } else {
+      // ---------------------------------------------------------- consumers
+      // The query rows, scaled to f16 and laid out as the tensor core's operand.
+      for (int r = warp; r < C::kRows; r += kW) {
+        constexpr int kE = C::kD / 32;  // elements a lane
+        float f[kE];
+        const int row = r0 + r, i = row / a.group, head = h * a.group + row % a.group;
+        const bool in = row < r1 && i < seq.nq;
+        if (in) {
+          const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + b * a.qs[0] +
+                                                                head * a.qs[1] + i * a.qs[2]) + lane * (kE / 2);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int blk = u ? blk1 : blk0;
-        if (u < subs && blk >= 0) {
-          const int y = sub < C::kTile ? 0 : row;  // blocks shorter than a tile start inside it
-#pragma unroll
-          for (int col = 0; col < C::kCols; ++col) {
-            uint8_t* d = dst + col * C::kTile * C::kRowBytes + u * sub * C::kRowBytes;
-            tma_load_4d(d, &tk, bars + s, col * 128, y, h, blk);
-            tma_load_4d(d + C::kTileBytes, &tv, bars + s, col * 128, y, h, blk);
+          for (int e = 0; e < kE; e += 2) {
+            const uint32_t w = __ldg(q + e / 2);
+            f[e] = half_bits_to_f32<C::kF16>(w);
+            f[e + 1] = half_bits_to_f32<C::kF16>(w >> 16);
           }
+        } else {
+#pragma unroll
+          for (int e = 0; e < kE; ++e) f[e] = 0.0f;
+        }
+        float up = 1.0f;
+        if constexpr (!C::kF16) {
+          float top = 0.0f;
+#pragma unroll
+          for (int e = 0; e < kE; ++e) top = fmaxf(top, fabsf(f[e]));
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+          // 2^(9 - exponent), kept inside the normal numbers
+          const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -110), 127);
+          up = __uint_as_float((uint32_t)(9 - ex + 127) << 23);
+          if (lane == 0) s_rs[r] = __uint_as_float((uint32_t)(ex - 9 + 127) << 23);
+        } else if (lane == 0) {
+          s_rs[r] = 1.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < kE; e += 2) {
+          const int d = lane * kE + e;
+          const int tt = C::kD == 64 ? d / 16 : (d & 127) / 32;
+          const int kk = C::kD == 64 ? (d & 15) / 4 : 8 * (d / 128) + (d & 31) / 4;
+          const int reg = ((d & 3) / 2) * 2 + ((r & 15) >> 3);
+          const uint32_t at2 = (uint32_t)((((r >> 4) * C::kKSteps + kk) * 32 + (r & 7) * 4 + tt) * 16 + reg * 4);
+          *reinterpret_cast<uint32_t*>(s_q + at2) = pack_f16x2(f[e] * up, f[e + 1] * up);
         }
       }
-    };
-    int looked = 0;  // the batch in the lanes begins at this tile
-    look_up(0);
-    int issued = 0;
-    // The scales of tiles that were looked up in an earlier batch than the one
-    // in the lanes: tiles are consumed in order, at most kStages behind.
-    float ring_ks[C::kStages][2], ring_vs[C::kStages][2];
-    int ring_ok[C::kStages];
-    auto advance = [&]() {  // issue the next tile, by the whole warp
-      if (issued - looked >= per_batch) {
-        looked = issued;
-        look_up(issued);
-      }
-      const int from = (issued - looked) * subs;
-      const int b0 = __shfl_sync(0xFFFFFFFFu, look_blk, from);
-      const int b1 = __shfl_sync(0xFFFFFFFFu, look_blk, from + subs - 1);
-      const float k0 = __shfl_sync(0xFFFFFFFFu, look_ks, from), k1 = __shfl_sync(0xFFFFFFFFu, look_ks, from + subs - 1);
-      const float v0 = __shfl_sync(0xFFFFFFFFu, look_vs, from), v1 = __shfl_sync(0xFFFFFFFFu, look_vs, from + subs - 1);
-      if (lane == 0) issue(issued, b0, b1);
-      // a ring kept in registers: the newest entry is last
-#pragma unroll
-      for (int s = 0; s + 1 < C::kStages; ++s) {
-        ring_ks[s][0] = ring_ks[s + 1][0], ring_ks[s][1] = ring_ks[s + 1][1];
-        ring_vs[s][0] = ring_vs[s + 1][0], ring_vs[s][1] = ring_vs[s + 1][1];
-        ring_ok[s] = ring_ok[s + 1];
-      }
-      ring_ks[C::kStages - 1][0] = k0, ring_ks[C::kStages - 1][1] = k1;
-      ring_vs[C::kStages - 1][0] = v0, ring_vs[C::kStages - 1][1] = v1;
-      ring_ok[C::kStages - 1] = (b0 >= 0 ? 1 : 0) | (b1 >= 0 ? 2 : 0);
-      ++issued;
-    };
-    auto advance_none = [&]() {  // past the last tile: the register ring moves on
-#pragma unroll
-      for (int s = 0; s + 1 < C::kStages; ++s) {
-        ring_ks[s][0] = ring_ks[s + 1][0], ring_ks[s][1] = ring_ks[s + 1][1];
-        ring_vs[s][0] = ring_vs[s + 1][0], ring_vs[s][1] = ring_vs[s + 1][1];
-        ring_ok[s] = ring_ok[s + 1];
-      }
-    };
-#pragma unroll
-    for (int s = 0; s < C::kStages; ++s) {
-      if (s < mine)
-        advance();
-      else
-        advance_none();
-    }
+      named_bar_sync(1, 32 * kW);
 
-    // The query rows, scaled to f16 and laid out as the tensor core's operand.
-    for (int r = warp; r < C::kRows; r += C::kWarps) {
-      constexpr int kE = C::kD / 32;  // elements a lane
-      float f[kE];
-      const int row = r0 + r, i = row / a.group, head = h * a.group + row % a.group;
-      const bool in = row < r1 && i < seq.nq;
-      float top = 0.0f;
-      if (in) {
-        const uint16_t* q = static_cast<const uint16_t*>(a.q) + b * a.qs[0] + head * a.qs[1] + i * a.qs[2] + lane * kE;
-#pragma unroll
-        for (int e = 0; e < kE; ++e) f[e] = half_bits_to_f32<C::kF16>(q[e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < kE; ++e) f[e] = 0.0f;
-      }
-      float up = 1.0f;
-      if constexpr (!C::kF16) {
-#pragma unroll
-        for (int e = 0; e < kE; ++e) top = fmaxf(top, fabsf(f[e]));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        // 2^(9 - exponent), kept inside the normal numbers
-        const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -110), 127);
-        up = __uint_as_float((uint32_t)(9 - ex + 127) << 23);
-        if (lane == 0) s_rs[r] = __uint_as_float((uint32_t)(ex - 9 + 127) << 23);
-      } else if (lane == 0) {
-        s_rs[r] = 1.0f;
-      }
-#pragma unroll
-      for (int e = 0; e < kE; e += 2) {
-        const int d = lane * kE + e;
-        const int tt = C::kD == 64 ? d / 16 : (d & 127) / 32;
-        const int kk = C::kD == 64 ? (d & 15) / 4 : 8 * (d / 128) + (d & 31) / 4;
-        const int reg = ((d & 3) / 2) * 2 + ((r & 15) >> 3);
-        const uint32_t at2 = (uint32_t)((((r >> 4) * C::kKSteps + kk) * 32 + (r & 7) * 4 + tt) * 16 + reg * 4);
-        *reinterpret_cast<uint32_t*>(s_q + at2) = pack_f16x2(f[e] * up, f[e + 1] * up);
-      }
-    }
-    __syncthreads();
-
-    float o[C::kMT][C::kNTiles][4];
-    float m[C::kMT][2], l[C::kMT][2], rs[C::kMT][2];
-    int hi_row[C::kMT][2], lo_row[C::kMT][2];  // the tokens that this lane's two rows see
-    float vs_unit = 1.0f;                      // O is in units of this scale
-#pragma unroll
-    for (int mt = 0; mt < C::kMT; ++mt) {
-#pragma unroll
-      for (int i = 0; i < C::kNTiles; ++i) o[mt][i][0] = o[mt][i][1] = o[mt][i][2] = o[mt][i][3] = 0.0f;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        m[mt][x] = -INFINITY;
-        l[mt][x] = 0.0f;
-        const int r = mt * 16 + g + 8 * x, row = r0 + r;
-        rs[mt][x] = s_rs[r];
-        const int2 v = row < r1 ? dec_span(a, seq, row, row + 1) : make_int2(0, 0);
-        lo_row[mt][x] = v.x;
-        hi_row[mt][x] = v.y;
-      }
-    }
-
-    int k = 0;
-    bool dead = false;
-    for (; k < mine; ++k) {
-      const int s = k % C::kStages;
-      {
-        const uint32_t par = (phases >> s) & 1u;
-        bool ok = mbar_try_wait(bars + s, par);
-        const long long begin = clock64_now();
-        while (!ok) {
-          ok = mbar_try_wait(bars + s, par);
-          if (!ok && clock64_now() - begin > a.timeout_cycles) break;
-        }
-        if (!__all_sync(0xFFFFFFFFu, ok)) {
-          dead = true;
-          if (lane == 0) atomicOr(c.status, kStatusTimeout);
-          break;
-        }
-        phases ^= 1u << s;
-      }
-      const uint32_t tile_k = smem_u32(ring + s * C::kStageBytes), tile_v = tile_k + C::kTileBytes;
-      const int tok0 = (first_tile + warp + k * C::kWarps) * C::kTile;
-      const float ks0 = ring_ks[0][0], ks1 = ring_ks[0][1], vs0 = ring_vs[0][0], vs1 = ring_vs[0][1];
-      const int ok_blk = ring_ok[0];
-      // Whole: every row of the warp sees every token, and every block is there.
-      bool full = ok_blk == 3;
-#pragma unroll
-      for (int mt = 0; mt < C::kMT; ++mt)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) full = full && lo_row[mt][x] <= tok0 && tok0 + C::kTile <= hi_row[mt][x];
-      full = __all_sync(0xFFFFFFFFu, full);
-
-      // S = Q K^T: 4 column tiles of 8 tokens
-      float sc[C::kMT][4][4];
-#pragma unroll
-      for (int mt = 0; mt < C::kMT; ++mt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sc[mt][j][0] = sc[mt][j][1] = sc[mt][j][2] = sc[mt][j][3] = 0.0f;
-#pragma unroll
-      for (int jj = 0; jj < 4; jj += 2) {
-        uint32_t w0[C::kKSteps], w1[C::kKSteps];
-        dec_key_words<C>(tile_k, jj * 8 + g, t, w0);
-        dec_key_words<C>(tile_k, jj * 8 + 8 + g, t, w1);
-#pragma unroll
-        for (int kk = 0; kk < C::kKSteps; ++kk) {
-          uint32_t x0, x1, y0, y1;
-          to_f16x4<C::kKind>(w0[kk], x0, x1);
-          to_f16x4<C::kKind>(w1[kk], y0, y1);
-#pragma unroll
-          for (int mt = 0; mt < C::kMT; ++mt) {
-            const uint4 q = lds128(smem_u32(s_q) + (uint32_t)(((mt * C::kKSteps + kk) * 32 + lane) * 16));
-            const uint32_t qa[4] = {q.x, q.y, q.z, q.w};
-            mma_f16(sc[mt][jj], qa, x0, x1);
-            mma_f16(sc[mt][jj + 1], qa, y0, y1);
-          }
-        }
-      }
-
-      // Scores in base 2; masks; the running maximum.
-      uint32_t pa[C::kMT][2][4];  // P as the A operand of the two k-steps of PV
-      float grow = 0.0f;          // rescaling wanted by some row
-      float mx[C::kMT][2];
+      float o[C::kMT][C::kNTiles][4];
+      float m[C::kMT][2], l[C::kMT][2], rs[C::kMT][2];
+      int hi_row[C::kMT][2], lo_row[C::kMT][2];  // the tokens that this lane's two rows see
+      int lo_all = 0, hi_all = 0x7fffffff;       // ... that every row of the warp sees
+      float vs_unit = 1.0f;                      // O is in units of this scale
 #pragma unroll
       for (int mt = 0; mt < C::kMT; ++mt) {
-        const float f00 = ks0 * rs[mt][0], f01 = ks0 * rs[mt][1], f10 = ks1 * rs[mt][0], f11 = ks1 * rs[mt][1];
-        if (a.cap_out > 0.0f) {  // cap * tanh(x) = cap * (1 - 2 / (2^(2 x log2 e) + 1))
-          const float ci = a.cap_in * 2.8853900817779268f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float f = (j < 2 ? (e < 2 ? f00 : f01) : (e < 2 ? f10 : f11)) * ci;
-              sc[mt][j][e] = fmaf(-2.0f * a.cap_out, rcp_approx(ex2(sc[mt][j][e] * f) + 1.0f), a.cap_out);
-            }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              sc[mt][j][e] *= (j < 2 ? (e < 2 ? f00 : f01) : (e < 2 ? f10 : f11)) * a.scale_log2;
-        }
-        if (!full) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int tok = tok0 + j * 8 + 2 * t + (e & 1), x = e >> 1;
-              if (tok < lo_row[mt][x] || tok >= hi_row[mt][x] || !(ok_blk & (j < 2 ? 1 : 2)))
-                sc[mt][j][e] = -INFINITY;
-            }
-        }
+        for (int i = 0; i < C::kNTiles; ++i) o[mt][i][0] = o[mt][i][1] = o[mt][i][2] = o[mt][i][3] = 0.0f;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          float v = fmaxf(fmaxf(sc[mt][0][2 * x], sc[mt][0][2 * x + 1]), fmaxf(sc[mt][1][2 * x], sc[mt][1][2 * x + 1]));
-          v = fmaxf(v, fmaxf(fmaxf(sc[mt][2][2 * x], sc[mt][2][2 * x + 1]),
-                             fmaxf(sc[mt][3][2 * x], sc[mt][3][2 * x + 1])));
-          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
-          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
-          mx[mt][x] = v;
-          if (v > m[mt][x] + kDecLazy) grow = 1.0f;
+          m[mt][x] = -INFINITY;
+          l[mt][x] = 0.0f;
+          const int r = mt * 16 + g + 8 * x, row = r0 + r;
+          rs[mt][x] = s_rs[r];
+          const bool real = row < r1 && row / a.group < seq.nq;
+          const int2 v = real ? dec_span(a, seq, row, row + 1) : make_int2(0, 0x7fffffff);
+          // a row of the tile that is no query row may see anything: nothing of it is written
+          lo_row[mt][x] = v.x;
+          hi_row[mt][x] = row < r1 && !real ? 0 : v.y;
+          lo_all = max(lo_all, lo_row[mt][x]);
+          hi_all = min(hi_all, hi_row[mt][x]);
         }
       }
-      const bool move = __any_sync(0xFFFFFFFFu, grow > 0.0f);
-      // Two halves of 16 tokens, each inside one block: O in that block's units.
+      lo_all = __reduce_max_sync(0xFFFFFFFFu, lo_all);
+      hi_all = __reduce_min_sync(0xFFFFFFFFu, hi_all);
+      // Scores stay raw where one positive factor a row and block brings them
+      // to base 2; a softcap, or a scale that is not positive, is applied first.
+      const bool raw = a.cap_out == 0.0f && a.scale_log2 > 0.0f;
+
+      int stage = (tile0 + warp) % kS;
+      uint32_t phase = (uint32_t)((tile0 + warp) / kS) & 1u;
+      bool dead = false;
+      for (int k = warp; k < n_tiles; k += kW) {
+        if (!dec_wait(s_full + stage, phase, s_abort, a)) {
+          dead = true;
+          break;
+        }
+        const uint32_t tile_k = smem_u32(smem + stage * C::kStageBytes), tile_v = tile_k + C::kTileBytes;
+        const int tok0 = (first_tile + k) * C::kTile;
+        const float4 meta = *reinterpret_cast<const float4*>(s_meta + stage);
+        const int ok_blk = s_meta[stage].ok;
+        const bool full = ok_blk == 3 && lo_all <= tok0 && tok0 + C::kTile <= hi_all;
+
+        // S = Q K^T: 4 column tiles of 8 tokens
+        float sc[C::kMT][4][4];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const float vs = half ? vs1 : vs0;
-        const float unit = vs > 0.0f ? vs : vs_unit;  // a zero scale: stored values are zeros, or do not matter
-        const bool first = half == 0 && move;
-        if (first || unit != vs_unit) {
-          // (finite, so that an output of 0 stays 0)
-          const float by_unit = unit != vs_unit ? fminf(__fdividef(vs_unit, unit), 1e38f) : 1.0f;
+        for (int mt = 0; mt < C::kMT; ++mt)
 #pragma unroll
-          for (int mt = 0; mt < C::kMT; ++mt) {
-            float al[2] = {by_unit, by_unit};
-            if (first) {
+          for (int j = 0; j < 4; ++j) sc[mt][j][0] = sc[mt][j][1] = sc[mt][j][2] = sc[mt][j][3] = 0.0f;
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const float m2 = fmaxf(m[mt][x], mx[mt][x]);
-                const float f = m2 == -INFINITY ? 1.0f : ex2(m[mt][x] - m2);
-                l[mt][x] *= f;
-                al[x] *= f;
-                m[mt][x] = m2;
-              }
-            }
+        for (int jj = 0; jj < 4; jj += 2) {
+          uint32_t w0[C::kKSteps], w1[C::kKSteps];
+          dec_key_words<C>(tile_k, jj * 8 + g, t, w0);
+          dec_key_words<C>(tile_k, jj * 8 + 8 + g, t, w1);
 #pragma unroll
-            for (int i = 0; i < C::kNTiles; ++i) {
-              o[mt][i][0] *= al[0], o[mt][i][1] *= al[0];
-              o[mt][i][2] *= al[1], o[mt][i][3] *= al[1];
+          for (int kk = 0; kk < C::kKSteps; ++kk) {
+            uint32_t x0, x1, y0, y1;
+            to_f16x4<C::kKind>(w0[kk], x0, x1);
+            to_f16x4<C::kKind>(w1[kk], y0, y1);
+#pragma unroll
+            for (int mt = 0; mt < C::kMT; ++mt) {
+              const uint4 q = lds128(smem_u32(s_q) + (uint32_t)(((mt * C::kKSteps + kk) * 32 + lane) * 16));
+              const uint32_t qa[4] = {q.x, q.y, q.z, q.w};
+              mma_f16(sc[mt][jj], qa, x0, x1);
+              mma_f16(sc[mt][jj + 1], qa, y0, y1);
             }
           }
-          vs_unit = unit;
         }
+
+        // Masks, and the running maximum in base 2.
+        float fa[C::kMT][2][2];  // [row][half]: score to base 2
+        float mx[C::kMT][2];
+        bool grow = false;
 #pragma unroll
         for (int mt = 0; mt < C::kMT; ++mt) {
-          const float m0 = m[mt][0] == -INFINITY ? 0.0f : m[mt][0], m1 = m[mt][1] == -INFINITY ? 0.0f : m[mt][1];
-          float pv[2][4];
 #pragma unroll
-          for (int jj = 0; jj < 2; ++jj) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              pv[jj][e] = ex2(sc[mt][2 * half + jj][e] - (e < 2 ? m0 : m1));
-              l[mt][e >> 1] += pv[jj][e];
-            }
+          for (int x = 0; x < 2; ++x) {
+            // (not 0, so that a hidden score stays -inf; stored values times a zero scale are as good as 0)
+            fa[mt][x][0] = fmaxf(meta.x * rs[mt][x] * a.scale_log2, 1e-37f);
+            fa[mt][x][1] = fmaxf(meta.y * rs[mt][x] * a.scale_log2, 1e-37f);
           }
-          const float z = vs > 0.0f ? 1.0f : 0.0f;
-          pa[mt][half][0] = pack_f16x2(pv[0][0] * z, pv[0][1] * z);
-          pa[mt][half][1] = pack_f16x2(pv[0][2] * z, pv[0][3] * z);
-          pa[mt][half][2] = pack_f16x2(pv[1][0] * z, pv[1][1] * z);
-          pa[mt][half][3] = pack_f16x2(pv[1][2] * z, pv[1][3] * z);
+          if (!raw) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float v = sc[mt][j][e] * (j < 2 ? meta.x : meta.y) * rs[mt][e >> 1];
+                // cap * tanh(x) = cap * (1 - 2 / (2^(2 x log2 e) + 1))
+                sc[mt][j][e] = a.cap_out > 0.0f
+                                   ? fmaf(-2.0f * a.cap_out, rcp_approx(ex2(v * a.cap_in * 2.8853900817779268f) + 1.0f), a.cap_out)
+                                   : v * a.scale_log2;
+              }
+            fa[mt][0][0] = fa[mt][0][1] = fa[mt][1][0] = fa[mt][1][1] = 1.0f;
+          }
+          if (!full) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int tok = tok0 + j * 8 + 2 * t + (e & 1), x = e >> 1;
+                if (tok < lo_row[mt][x] || tok >= hi_row[mt][x] || !(ok_blk & (j < 2 ? 1 : 2)))
+                  sc[mt][j][e] = -INFINITY;
+              }
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float va = fmaxf(fmax3(sc[mt][0][2 * x], sc[mt][0][2 * x + 1], sc[mt][1][2 * x]), sc[mt][1][2 * x + 1]);
+            const float vb = fmaxf(fmax3(sc[mt][2][2 * x], sc[mt][2][2 * x + 1], sc[mt][3][2 * x]), sc[mt][3][2 * x + 1]);
+            float v = fmaxf(va * fa[mt][x][0], vb * fa[mt][x][1]);
+            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
+            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
+            mx[mt][x] = v;
+            grow = grow || v > m[mt][x] + kDecLazy;
+          }
         }
-        // O += P V over these 16 tokens: lane t takes tokens 2t, 2t+1, 2t+8, 2t+9
-        const int row = half * 16 + 2 * t;
-        uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
-        if (!full) {  // bytes that no row may see could be NaN
+        const bool move = __any_sync(0xFFFFFFFFu, grow);
+        // Two halves of 16 tokens, each inside one block: O in that block's units.
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int tok = tok0 + row + (e & 1) + 8 * (e >> 1);
-            if (tok < span.x || tok >= span.y || !(ok_blk & (half ? 2 : 1))) keep[e] = 0u;
-          }
-        }
-        if constexpr (C::kD == 64) {
-          uint2 v[4];
+        for (int half = 0; half < 2; ++half) {
+          const float vs = half ? meta.w : meta.z;
+          const float unit = vs > 0.0f ? vs : vs_unit;  // a zero scale: its values do not count
+          const bool first = half == 0 && move;
+          if (first || unit != vs_unit) {
+            // (finite, so that an output of 0 stays 0)
+            const float by_unit = unit != vs_unit ? fminf(__fdividef(vs_unit, unit), 1e38f) : 1.0f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = row + (e & 1) + 8 * (e >> 1);
-            v[e] = lds64(dec_unit<C>(tile_v, r, g >> 1) + (g & 1) * 8);
-            v[e].x &= keep[e], v[e].y &= keep[e];
-          }
+            for (int mt = 0; mt < C::kMT; ++mt) {
+              float al[2] = {by_unit, by_unit};
+              if (first) {
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const uint32_t x0 = w ? v[0].y : v[0].x, x1 = w ? v[1].y : v[1].x, x2 = w ? v[2].y : v[2].x,
-                           x3 = w ? v[3].y : v[3].x;
+                for (int x = 0; x < 2; ++x) {
+                  const float m2 = fmaxf(m[mt][x], mx[mt][x]);
+                  const float f = m2 == -INFINITY ? 1.0f : ex2(m[mt][x] - m2);
+                  l[mt][x] *= f;
+                  al[x] *= f;
+                  m[mt][x] = m2;
+                }
+              }
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              uint32_t a0, a1, b0, b1;
-              to_f16x4<C::kKind>(__byte_perm(x0, x1, hh ? 0x7362 : 0x5140), a0, a1);
-              to_f16x4<C::kKind>(__byte_perm(x2, x3, hh ? 0x7362 : 0x5140), b0, b1);
-#pragma unroll
-              for (int mt = 0; mt < C::kMT; ++mt) {
-                mma_f16(o[mt][4 * w + 2 * hh], pa[mt][half], a0, b0);
-                mma_f16(o[mt][4 * w + 2 * hh + 1], pa[mt][half], a1, b1);
+              for (int i = 0; i < C::kNTiles; ++i) {
+                fmul2(o[mt][i][0], o[mt][i][1], o[mt][i][0], o[mt][i][1], al[0], al[0]);
+                fmul2(o[mt][i][2], o[mt][i][3], o[mt][i][2], o[mt][i][3], al[1], al[1]);
               }
             }
+            vs_unit = unit;
           }
-        } else {
+          uint32_t pa[C::kMT][4];  // P as the A operand
+#pragma unroll
+          for (int mt = 0; mt < C::kMT; ++mt) {
+            const float m0 = m[mt][0] == -INFINITY ? 0.0f : m[mt][0], m1 = m[mt][1] == -INFINITY ? 0.0f : m[mt][1];
+            const float f0 = fa[mt][0][half], f1 = fa[mt][1][half];
+            float pv[2][4];
+#pragma unroll
+            for (int jj = 0; jj < 2; ++jj) {
+              const float* x = sc[mt][2 * half + jj];
+              ffma2(pv[jj][0], pv[jj][1], x[0], x[1], f0, f0, -m0, -m0);
+              ffma2(pv[jj][2], pv[jj][3], x[2], x[3], f1, f1, -m1, -m1);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) pv[jj][e] = ex2(pv[jj][e]);
+            }
+            l[mt][0] += (pv[0][0] + pv[0][1]) + (pv[1][0] + pv[1][1]);
+            l[mt][1] += (pv[0][2] + pv[0][3]) + (pv[1][2] + pv[1][3]);
+            pa[mt][0] = pack_f16x2(pv[0][0], pv[0][1]);
+            pa[mt][1] = pack_f16x2(pv[0][2], pv[0][3]);
+            pa[mt][2] = pack_f16x2(pv[1][0], pv[1][1]);
+            pa[mt][3] = pack_f16x2(pv[1][2], pv[1][3]);
+            if (!(vs > 0.0f)) pa[mt][0] = pa[mt][1] = pa[mt][2] = pa[mt][3] = 0u;
+          }
+          // O += P V over these 16 tokens: lane t takes tokens 2t, 2t+1, 2t+8, 2t+9
+          const int row = half * 16 + 2 * t;
+          constexpr int kWords = C::kD == 64 ? 2 : 4;
 #pragma unroll
           for (int col = 0; col < C::kCols; ++col) {
-            const uint32_t base = tile_v + col * C::kTile * 128;
-            uint32_t v[4][4];
+            const uint32_t base = tile_v + col * C::kTile * C::kRowBytes;
+            uint32_t v[4][kWords];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const uint4 x = lds128(dec_unit<C>(base, row + (e & 1) + 8 * (e >> 1), g));
-              v[e][0] = x.x & keep[e], v[e][1] = x.y & keep[e], v[e][2] = x.z & keep[e], v[e][3] = x.w & keep[e];
+              const int r = row + (e & 1) + 8 * (e >> 1);
+              if constexpr (C::kD == 64) {
+                const uint2 x = lds64(dec_unit<C>(base, r, g >> 1) + (g & 1) * 8);
+                v[e][0] = x.x, v[e][1] = x.y;
+              } else {
+                const uint4 x = lds128(dec_unit<C>(base, r, g));
+                v[e][0] = x.x, v[e][1] = x.y, v[e][2] = x.z, v[e][3] = x.w;
+              }
+            }
+            if (!full) {  // bytes that no row may see could be NaN
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int tok = tok0 + row + (e & 1) + 8 * (e >> 1);
+                if (tok < span.x || tok >= span.y || !(ok_blk & (half ? 2 : 1))) {
+#pragma unroll
+                  for (int w = 0; w < kWords; ++w) v[e][w] = 0u;
+                }
+              }
             }
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
+            for (int w = 0; w < kWords; ++w) {
 #pragma unroll
               for (int hh = 0; hh < 2; ++hh) {
                 uint32_t a0, a1, b0, b1;
@@ -662,93 +677,73 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
                 to_f16x4<C::kKind>(__byte_perm(v[2][w], v[3][w], hh ? 0x7362 : 0x5140), b0, b1);
 #pragma unroll
                 for (int mt = 0; mt < C::kMT; ++mt) {
-                  mma_f16(o[mt][16 * col + 4 * w + 2 * hh], pa[mt][half], a0, b0);
-                  mma_f16(o[mt][16 * col + 4 * w + 2 * hh + 1], pa[mt][half], a1, b1);
+                  mma_f16(o[mt][4 * kWords * col + 4 * w + 2 * hh], pa[mt], a0, b0);
+                  mma_f16(o[mt][4 * kWords * col + 4 * w + 2 * hh + 1], pa[mt], a1, b1);
                 }
               }
             }
           }
         }
+        __syncwarp();  // every lane has read the stage: it may be filled again
+        if (lane == 0) mbar_arrive(s_empty + stage);
+        stage += kW;
+        if (stage >= kS) stage -= kS, phase ^= 1u;
       }
-      __syncwarp();  // every lane has read the stage: it may be filled again
-      if (issued < mine)
-        advance();
-      else
-        advance_none();
-    }
-    // Join the warps: O in units of 1, at the block's common maximum.
+
+      // Join the warps: O in units of 1, at the block's common maximum.
 #pragma unroll
-    for (int mt = 0; mt < C::kMT; ++mt)
+      for (int mt = 0; mt < C::kMT; ++mt)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        l[mt][x] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][x], 1);
-        l[mt][x] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][x], 2);
-        if (t == 0) s_ml[warp * C::kRows + mt * 16 + g + 8 * x] = make_float2(m[mt][x], l[mt][x]);
-      }
-    // Every warp is done with its ring, and the maxima are there.  After an
-    // expired wait the block ends, once its copies in flight have landed (a
-    // bounded wait again).
-    if (__syncthreads_or(dead)) {
-      for (; k < issued; ++k) {
-        const int s = k % C::kStages;
-        const long long begin = clock64_now();
-        while (!mbar_try_wait(bars + s, (phases >> s) & 1u) && clock64_now() - begin < kDecDrainCycles) {
+        for (int x = 0; x < 2; ++x) {
+          l[mt][x] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][x], 1);
+          l[mt][x] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][x], 2);
+          if (t == 0) s_ml[warp * C::kRows + mt * 16 + g + 8 * x] = make_float2(m[mt][x], l[mt][x]);
         }
-        phases ^= 1u << s;
-      }
-      return;
-    }
+      // Every warp is done with the ring, and the maxima are there.
+      if (__syncthreads_or(dead)) return;
 #pragma unroll
-    for (int mt = 0; mt < C::kMT; ++mt)
+      for (int mt = 0; mt < C::kMT; ++mt)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int r = mt * 16 + g + 8 * x;
-        float top = -INFINITY;
-        for (int w = 0; w < C::kWarps; ++w) top = fmaxf(top, s_ml[w * C::kRows + r].x);
-        const float f = m[mt][x] == -INFINITY ? 0.0f : ex2(m[mt][x] - top) * vs_unit;
-        float* dst = s_join + (long long)(warp * C::kRows + r) * C::kD;
+        for (int x = 0; x < 2; ++x) {
+          const int r = mt * 16 + g + 8 * x;
+          float top = -INFINITY;
+          for (int w = 0; w < kW; ++w) top = fmaxf(top, s_ml[w * C::kRows + r].x);
+          const float f = m[mt][x] == -INFINITY ? 0.0f : ex2(m[mt][x] - top) * vs_unit;
+          float* dst = s_join + (warp * C::kRows + r) * C::kD;
 #pragma unroll
-        for (int i = 0; i < C::kNTiles; ++i) {
-          dst[dec_col<C>(i, 2 * t)] = o[mt][i][2 * x] * f;
-          dst[dec_col<C>(i, 2 * t + 1)] = o[mt][i][2 * x + 1] * f;
+          for (int i = 0; i < C::kNTiles; ++i) {
+            dst[dec_col<C>(i, 2 * t)] = o[mt][i][2 * x] * f;
+            dst[dec_col<C>(i, 2 * t + 1)] = o[mt][i][2 * x + 1] * f;
+          }
+        }
+      named_bar_sync(1, 32 * kW);
+      const int slot = 2 * blockIdx.x + (at > seg0 ? 0 : 1);
+      for (int v = tid; v < C::kRows * (C::kD / 8); v += 32 * kW) {
+        const int r = v / (C::kD / 8), d = (v % (C::kD / 8)) * 8;
+        if (r0 + r >= r1) break;
+        float top = -INFINITY, sum = 0.0f, x[8] = {};
+        for (int w = 0; w < kW; ++w) top = fmaxf(top, s_ml[w * C::kRows + r].x);
+        for (int w = 0; w < kW; ++w) {
+          const float2 ml = s_ml[w * C::kRows + r];
+          if (ml.x > -INFINITY) sum += ml.y * ex2(ml.x - top);
+          const float4* q = reinterpret_cast<const float4*>(s_join + (w * C::kRows + r) * C::kD + d);
+          const float4 y0 = q[0], y1 = q[1];
+          x[0] += y0.x, x[1] += y0.y, x[2] += y0.z, x[3] += y0.w;
+          x[4] += y1.x, x[5] += y1.y, x[6] += y1.z, x[7] += y1.w;
+        }
+        if (whole) {
+          dec_write<C>(a, b, h, r0 + r, d, x, top, sum);
+        } else {
+          float4* q = reinterpret_cast<float4*>(p.part_o + ((long long)slot * C::kRows + r) * C::kD + d);
+          q[0] = make_float4(x[0], x[1], x[2], x[3]);
+          q[1] = make_float4(x[4], x[5], x[6], x[7]);
+          if (d == 0) p.part_ml[(long long)slot * C::kRows + r] = make_float2(top, sum);
         }
       }
-    __syncthreads();
-    const bool head_cut = at > seg0;
-    const int slot = 2 * blockIdx.x + (head_cut ? 0 : 1);
-    for (int v = tid; v < C::kRows * (C::kD / 8); v += C::kThreads) {
-      const int r = v / (C::kD / 8), d = (v % (C::kD / 8)) * 8;
-      if (r0 + r >= r1) break;
-      float top = -INFINITY, sum = 0.0f, x[8] = {};
-      for (int w = 0; w < C::kWarps; ++w) top = fmaxf(top, s_ml[w * C::kRows + r].x);
-      for (int w = 0; w < C::kWarps; ++w) {
-        const float2 ml = s_ml[w * C::kRows + r];
-        if (ml.x > -INFINITY) sum += ml.y * ex2(ml.x - top);
-        const float4* q = reinterpret_cast<const float4*>(s_join + (long long)(w * C::kRows + r) * C::kD + d);
-        const float4 y0 = q[0], y1 = q[1];
-        x[0] += y0.x, x[1] += y0.y, x[2] += y0.z, x[3] += y0.w;
-        x[4] += y1.x, x[5] += y1.y, x[6] += y1.z, x[7] += y1.w;
-      }
-      if (whole) {
-        const int row = r0 + r, i = row / a.group, head = h * a.group + row % a.group;
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-        uint4 y;
-        uint32_t* u = &y.x;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          u[e] = C::kF16 ? pack_f16x2(x[2 * e] * inv, x[2 * e + 1] * inv) : pack_bf16x2(x[2 * e] * inv, x[2 * e + 1] * inv);
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + b * a.os[0] + head * a.os[1] + i * a.os[2] + d) = y;
-        if (d == 0)
-          a.lse[((long long)b * a.Hq + head) * a.n + i] = sum > 0.0f ? (top + log2f(sum)) * kDecLn2 : -INFINITY;
-      } else {
-        float4* q = reinterpret_cast<float4*>(p.part_o + ((long long)slot * C::kRows + r) * C::kD + d);
-        q[0] = make_float4(x[0], x[1], x[2], x[3]);
-        q[1] = make_float4(x[4], x[5], x[6], x[7]);
-        if (d == 0) p.part_ml[(long long)slot * C::kRows + r] = make_float2(top, sum);
-      }
+      fence_proxy_async_smem();  // what was written into the ring's memory goes before the next copies into it
     }
-    fence_proxy_async_smem();  // what was written into the ring's memory goes before the next copies into it
-    __syncthreads();           // the ring's memory and the maxima are free again
+    __syncthreads();  // the ring's memory and the maxima are free again
+    tile0 += n_tiles;
     at = min(t1, seg0 + tiles);
     seg0 += tiles;
     if (++rg == p.row_groups) {
@@ -807,15 +802,7 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
       x[0] = fmaf(y0.x, f, x[0]), x[1] = fmaf(y0.y, f, x[1]), x[2] = fmaf(y0.z, f, x[2]), x[3] = fmaf(y0.w, f, x[3]);
       x[4] = fmaf(y1.x, f, x[4]), x[5] = fmaf(y1.y, f, x[5]), x[6] = fmaf(y1.z, f, x[6]), x[7] = fmaf(y1.w, f, x[7]);
     }
-    const int row = r0 + r, i = row / a.group, head = h * a.group + row % a.group;
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    uint4 y;
-    uint32_t* u = &y.x;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      u[e] = C::kF16 ? pack_f16x2(x[2 * e] * inv, x[2 * e + 1] * inv) : pack_bf16x2(x[2 * e] * inv, x[2 * e + 1] * inv);
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + b * a.os[0] + head * a.os[1] + i * a.os[2] + d) = y;
-    if (d == 0) a.lse[((long long)b * a.Hq + head) * a.n + i] = sum > 0.0f ? (top + log2f(sum)) * kDecLn2 : -INFINITY;
+    dec_write<C>(a, b, h, r0 + r, d, x, top, sum);
   }
 }
 
