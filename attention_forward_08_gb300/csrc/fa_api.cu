@@ -305,6 +305,8 @@ int current_device(DeviceInfo* info) {
   info->num_sms = g_num_sms[dev];
   info->status = g_status_ptr[dev];
   info->timeout_cycles = timeout_cycles();
+  std::lock_guard<std::mutex> lk(g_mu);
+  info->max_ctas = g_max_ctas;
   return FA_OK;
 }
 

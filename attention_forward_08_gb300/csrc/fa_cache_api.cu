@@ -296,7 +296,7 @@ int fa_cache_append(const fa_cache_append_args* a) {
   p.W = a->W;
   // n tokens that start at any slot touch at most this many blocks.
   p.spans = (int)(((long long)a->n + a->cache.page - 2) / a->cache.page + 1);
-  return launch_cache_append(p, a->cache.kind, a->dtype, {static_cast<cudaStream_t>(a->stream), dev.num_sms, dev.dev});
+  return launch_cache_append(p, a->cache.kind, a->dtype, {static_cast<cudaStream_t>(a->stream), dev.num_sms, dev.dev, dev.max_ctas});
 }
 
 int fa_cache_attn(const fa_cache_attn_args* a) {
@@ -311,7 +311,7 @@ int fa_cache_attn(const fa_cache_attn_args* a) {
   rc = check_workspace(a->workspace, a->workspace_bytes, cache_attn_workspace(p, dev.num_sms),
                        "fa_cache_attn_workspace_bytes");
   if (rc != FA_OK) return rc;
-  return launch_cache_attn(p, a->cache.kind, a->dtype, {static_cast<cudaStream_t>(a->stream), dev.num_sms, dev.dev});
+  return launch_cache_attn(p, a->cache.kind, a->dtype, {static_cast<cudaStream_t>(a->stream), dev.num_sms, dev.dev, dev.max_ctas});
 }
 
 long long fa_cache_attn_workspace_bytes(const fa_cache_attn_args* a) {
@@ -355,7 +355,7 @@ int fa_cache_evict(const fa_cache_evict_args* a) {
   p.mover = reinterpret_cast<int*>(ws + slots);
   p.count = reinterpret_cast<int*>(ws + 2 * slots);
   p.edge = reinterpret_cast<float*>(ws + 2 * slots + align256(heads * 4));
-  return launch_cache_evict(p, a->cache.kind, {static_cast<cudaStream_t>(a->stream), dev.num_sms, dev.dev});
+  return launch_cache_evict(p, a->cache.kind, {static_cast<cudaStream_t>(a->stream), dev.num_sms, dev.dev, dev.max_ctas});
 }
 
 long long fa_cache_evict_workspace_bytes(const fa_cache_evict_args* a) {

@@ -55,14 +55,19 @@ struct DecCfg {
   // Consumer warps a block, and blocks an SM: as many warps as the outputs
   // that each holds (kMT * D / 2 registers a lane) leave room for.
   static constexpr bool kWide = kMT * kD > 128;
-  static constexpr int kWarps = kWide ? 7 : 5;
+  static constexpr int kWarps = kD == 256 ? 6 : kWide ? 7 : 5;
   static constexpr int kCtas = kWide ? 1 : 2;
   static constexpr int kThreads = 32 * (kWarps + 1);        // and the producer warp
   static constexpr int kCols = kD >= 128 ? kD / 128 : 1;    // 128-byte column blocks of a row
   static constexpr int kRowBytes = kD >= 128 ? 128 : 64;    // of one column block
   static constexpr int kTileBytes = kTile * kD;             // K; V alike
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kStages = (kWide ? 196608 : 98304) / kStageBytes;  // ring of all warps; tile k goes to warp k % kWarps
+  // The ring: a whole number of stages for each warp.  Tile k takes stage k %
+  // kStages and warp k % kWarps, so that a stage's tiles all belong to one
+  // warp: copies land in any order, and a warp that waited for one tile of a
+  // stage cannot mistake its phase for the next one's.
+  static constexpr int kStages = (kWide ? 196608 : 98304) / kStageBytes / kWarps * kWarps;
+  static constexpr int kMinTiles = 2 * kWarps;  // of one block
   static constexpr int kRows = 16 * kMT;
   static constexpr int kKSteps = kD / 16, kNTiles = kD / 8;
   static constexpr int kQBytes = kRows * kD * 2;
@@ -74,7 +79,7 @@ struct DecCfg {
   static constexpr int kOffQ = kRingBytes, kOffMl = kOffQ + kQBytes, kOffMeta = kOffMl + kWarps * kRows * 8;
   static constexpr int kOffBar = kOffMeta + kStages * 32, kOffRs = kOffBar + kStages * 16;
   static constexpr int kOffTmp = kOffRs + kRows * 4;
-  static constexpr int kSmem = 1024 + kOffTmp + 128;
+  static constexpr int kSmem = 1024 + kOffTmp + 16;
 };
 
 // What a consumer needs beside a tile's bytes.
@@ -130,34 +135,65 @@ __device__ __forceinline__ long long dec_seq_tiles(const DecParams& p, int b) { 
   return n * p.a.c.H;
 }
 
-// Sum over the block of one value a thread; `tmp` holds one value a warp.
-__device__ __forceinline__ long long block_sum(long long v, long long* tmp) {
+__device__ __forceinline__ long long warp_sum_ll(long long v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = v;
-  __syncthreads();
-  long long s = 0;
-  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s += tmp[w];
-  __syncthreads();
-  return s;
+  return v;
+}
+__device__ __forceinline__ long long warp_scan_ll(long long v, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+// a / b for a, b >= 0 (64-bit divisions are long; these numbers are small).
+__device__ __forceinline__ long long div_ll(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// Tiles before sequence `b` (all of them: b = B), by the whole block.
+// Every warp finds its place for itself: there is no barrier in it, and up to
+// 32 sequences take one load.
+// All tiles, and those before sequence `b`.
 template <class C>
-__device__ __forceinline__ long long dec_tiles_before(const DecParams& p, int b, long long* tmp) {
-  long long n = 0;
-  for (int i = threadIdx.x; i < b; i += blockDim.x) n += dec_seq_tiles<C>(p, i);
-  return block_sum(n, tmp);
+__device__ __forceinline__ void dec_count(const DecParams& p, int b, long long& before, long long& total) {
+  const int lane = threadIdx.x & 31;
+  long long all = 0, lower = 0;
+  for (int i = lane; i < p.a.B; i += 32) {
+    const long long n = dec_seq_tiles<C>(p, i);
+    all += n;
+    if (i < b) lower += n;
+  }
+  total = warp_sum_ll(all);
+  before = warp_sum_ll(lower);
 }
 
-// Thread blocks that share the line: all, or fewer when some would get less
-// than two tiles a warp.
+// The sequence that holds tile `t` of the line, and the tiles before it.
 template <class C>
-__device__ __forceinline__ int dec_ctas(const DecParams& p, long long total) {
-  const long long want = (total + 2 * C::kWarps - 1) / (2 * C::kWarps);
-  return (int)min((long long)p.max_ctas, max(1LL, want));
+__device__ __forceinline__ int dec_find(const DecParams& p, long long t, long long& before) {
+  const int lane = threadIdx.x & 31;
+  before = 0;
+  for (int base = 0; base < p.a.B; base += 32) {
+    const long long mine = base + lane < p.a.B ? dec_seq_tiles<C>(p, base + lane) : 0;
+    const long long upto = before + warp_scan_ll(mine, lane);
+    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, t < upto);
+    if (hit) {
+      const int at = __ffs(hit) - 1;
+      before = __shfl_sync(0xFFFFFFFFu, upto - mine, at);
+      return base + at;
+    }
+    before = __shfl_sync(0xFFFFFFFFu, upto, 31);
+  }
+  return p.a.B - 1;  // not reached: t < total
 }
-__device__ __forceinline__ long long dec_start(long long total, int ctas, int c) { return total * c / ctas; }
+
+// Tiles of one thread block's part of the line: an equal share of the grid's,
+// and no less than two tiles a warp.
+template <class C>
+__device__ __forceinline__ long long dec_part(const DecParams& p, long long total) {
+  return max((long long)C::kMinTiles, div_ll(total + p.max_ctas - 1, p.max_ctas));
+}
 
 // ------------------------------------------------------------------ tensor-core pieces
 
@@ -279,8 +315,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   uint64_t* s_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* s_empty = s_full + kS;
   float* s_rs = reinterpret_cast<float*>(smem + C::kOffRs);  // [row]: 2^-(scaling of the query row)
-  long long* s_tmp = reinterpret_cast<long long*>(smem + C::kOffTmp);  // one a warp, then the search's answer
-  volatile int* s_abort = reinterpret_cast<int*>(s_tmp + 12);
+  volatile int* s_abort = reinterpret_cast<int*>(smem + C::kOffTmp);
   float* s_join = reinterpret_cast<float*>(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   if (tid == 0) {
@@ -294,46 +329,15 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     tma_prefetch_desc(&tv);
   }
 
+  // The join kernel may take its place on the machine as soon as there is room.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
   // This block's part of the line, and where it begins.
-  const long long total = dec_tiles_before<C>(p, a.B, s_tmp);
-  const int ctas = dec_ctas<C>(p, total);
-  if ((int)blockIdx.x >= ctas) return;
-  const long long t0 = dec_start(total, ctas, blockIdx.x), t1 = dec_start(total, ctas, blockIdx.x + 1);
-  int b = 0;
-  long long before = 0;  // tiles before sequence b
-  for (int base = 0;; base += C::kThreads) {  // a block of sequences at a time
-    const int i = base + tid;
-    const long long mine = i < a.B ? dec_seq_tiles<C>(p, i) : 0;
-    long long upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-      if (lane >= o) upto += u;
-    }
-    if (lane == 31) s_tmp[warp] = upto;
-    if (tid == 0) s_tmp[9] = -1;
-    __syncthreads();
-    long long off = before, all = before;
-    for (int w = 0; w <= kW; ++w) {
-      if (w < warp) off += s_tmp[w];
-      all += s_tmp[w];
-    }
-    upto += off;
-    if (mine > 0 && upto - mine <= t0 && t0 < upto) {
-      s_tmp[9] = i;
-      s_tmp[10] = upto - mine;
-    }
-    __syncthreads();
-    const long long hit = s_tmp[9];
-    if (hit >= 0) {
-      b = (int)hit;
-      before = s_tmp[10];
-      break;
-    }
-    before = all;
-    __syncthreads();
-    if (base + C::kThreads >= a.B) return;  // not reached: t0 < total
-  }
+  long long before, total;
+  dec_count<C>(p, 0, before, total);
+  const long long part = dec_part<C>(p, total), t0 = part * blockIdx.x, t1 = min(total, t0 + part);
+  if (t0 >= total) return;
+  int b = dec_find<C>(p, t0, before);
   DecSeq seq = dec_seq(a, b);
   if (tid == 0 && before >= t0) (void)checked_len(c, a.lens[b]);  // one block a sequence tells about its length
   long long seg0 = before;  // first tile of the current segment
@@ -341,10 +345,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   {  // the segment of t0
     long long per_head = 0;
     for (int r = 0; r < p.row_groups; ++r) per_head += dec_tiles<C>(p, seq, r);
-    h = (int)((t0 - seg0) / per_head);
+    h = (int)div_ll(t0 - seg0, per_head);
     seg0 += h * per_head;
     while (seg0 + dec_tiles<C>(p, seq, rg) <= t0) seg0 += dec_tiles<C>(p, seq, rg++);
   }
+  __syncthreads();  // the barriers are ready
   const int sub = min(c.page, C::kTile), sub_log2 = min(c.page_log2, 5);  // a block's part of a tile
   const int subs = C::kTile >> sub_log2;                                  // parts a tile: 1 or 2
   int tile0 = 0;  // tiles of this block's earlier pieces: tile k of all uses stage k % kS
@@ -501,10 +506,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       // to base 2; a softcap, or a scale that is not positive, is applied first.
       const bool raw = a.cap_out == 0.0f && a.scale_log2 > 0.0f;
 
-      int stage = (tile0 + warp) % kS;
-      uint32_t phase = (uint32_t)((tile0 + warp) / kS) & 1u;
+      const int k_first = (warp + kW - tile0 % kW) % kW;  // this warp's first tile of the piece
+      int stage = (tile0 + k_first) % kS;
+      uint32_t phase = (uint32_t)((tile0 + k_first) / kS) & 1u;
       bool dead = false;
-      for (int k = warp; k < n_tiles; k += kW) {
+      for (int k = k_first; k < n_tiles; k += kW) {
         if (!dec_wait(s_full + stage, phase, s_abort, a)) {
           dead = true;
           break;
@@ -760,13 +766,16 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 }
 
 // Joins the parts of segments that lie in more than one thread block.  One
-// block per (head, sequence); rows of all row groups.
+// block per (row group and piece of its rows, head, sequence); a thread sums
+// four columns of a row over the parts.
 template <class C>
 __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__ DecParams p) {
   const CacheAttnParams& a = p.a;
-  __shared__ long long tmp[4];
-  const int rg = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  const long long before = dec_tiles_before<C>(p, b, tmp), total = dec_tiles_before<C>(p, a.B, tmp);
+  constexpr int kRowsHere = 512 / C::kD;  // rows a block
+  const int rg = blockIdx.x / (C::kRows / kRowsHere), piece = blockIdx.x % (C::kRows / kRowsHere);
+  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+  long long before, total;
+  dec_count<C>(p, b, before, total);
   const DecSeq seq = dec_seq(a, b);
   long long per_head = 0, u0 = 0;
   for (int r = 0; r < p.row_groups; ++r) {
@@ -775,35 +784,31 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
     per_head += n;
   }
   u0 += before + h * per_head;
-  const long long u1 = u0 + dec_tiles<C>(p, seq, rg);
-  const int ctas = dec_ctas<C>(p, total);
-  auto owner = [&](long long u) {
-    int c = (int)min((long long)ctas - 1, u * ctas / total);
-    while (c > 0 && dec_start(total, ctas, c) > u) --c;
-    while (c + 1 < ctas && dec_start(total, ctas, c + 1) <= u) ++c;
-    return c;
-  };
-  const int c0 = owner(u0), c1 = owner(u1 - 1);
-  if (c0 == c1) return;
-  const int r0 = rg * C::kRows, r1 = min(p.rows, r0 + C::kRows);
-  for (int v = tid; v < C::kRows * (C::kD / 8); v += 128) {
-    const int r = v / (C::kD / 8), d = (v % (C::kD / 8)) * 8;
-    if (r0 + r >= r1) break;
-    float top = -INFINITY, sum = 0.0f, x[8] = {};
-    for (int c = c0; c <= c1; ++c) top = fmaxf(top, p.part_ml[(long long)(2 * c + (c == c0)) * C::kRows + r].x);
-    for (int c = c0; c <= c1; ++c) {
-      const long long slot = (long long)(2 * c + (c == c0)) * C::kRows + r;
-      const float2 ml = p.part_ml[slot];
-      if (ml.x == -INFINITY) continue;
-      const float f = ex2(ml.x - top);
-      sum = fmaf(ml.y, f, sum);
-      const float4* q = reinterpret_cast<const float4*>(p.part_o + slot * C::kD + d);
-      const float4 y0 = q[0], y1 = q[1];
-      x[0] = fmaf(y0.x, f, x[0]), x[1] = fmaf(y0.y, f, x[1]), x[2] = fmaf(y0.z, f, x[2]), x[3] = fmaf(y0.w, f, x[3]);
-      x[4] = fmaf(y1.x, f, x[4]), x[5] = fmaf(y1.y, f, x[5]), x[6] = fmaf(y1.z, f, x[6]), x[7] = fmaf(y1.w, f, x[7]);
-    }
-    dec_write<C>(a, b, h, r0 + r, d, x, top, sum);
+  const long long u1 = u0 + dec_tiles<C>(p, seq, rg), part = dec_part<C>(p, total);
+  const int c0 = (int)div_ll(u0, part), c1 = (int)div_ll(u1 - 1, part);
+  const int r = piece * kRowsHere + tid / (C::kD / 4), row = rg * C::kRows + r, d = tid % (C::kD / 4) * 4;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
+  if (c0 == c1 || row >= p.rows) return;
+  float top = -INFINITY, sum = 0.0f;
+  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int i = c0; i <= c1; ++i) {
+    const long long slot = (long long)(2 * i + (i == c0)) * C::kRows + r;
+    const float2 ml = __ldcg(p.part_ml + slot);
+    const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part_o + slot * C::kD + d));
+    const float m2 = fmaxf(top, ml.x), z = m2 == -INFINITY ? 0.0f : m2;
+    const float f = ex2(top - z), g = ex2(ml.x - z);
+    top = m2;
+    sum = fmaf(sum, f, ml.y * g);
+    x.x = fmaf(x.x, f, y.x * g), x.y = fmaf(x.y, f, y.y * g), x.z = fmaf(x.z, f, y.z * g), x.w = fmaf(x.w, f, y.w * g);
   }
+  const int i = row / a.group, head = h * a.group + row % a.group;
+  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  uint2 y;
+  y.x = C::kF16 ? pack_f16x2(x.x * inv, x.y * inv) : pack_bf16x2(x.x * inv, x.y * inv);
+  y.y = C::kF16 ? pack_f16x2(x.z * inv, x.w * inv) : pack_bf16x2(x.z * inv, x.w * inv);
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + b * a.os[0] + head * a.os[1] + i * a.os[2] + d) = y;
+  if (d == 0) a.lse[((long long)b * a.Hq + head) * a.n + i] = sum > 0.0f ? (top + log2f(sum)) * kDecLn2 : -INFINITY;
 }
 
 }  // namespace fa

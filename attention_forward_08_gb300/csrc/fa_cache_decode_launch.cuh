@@ -38,13 +38,24 @@ int launch_decode(const CacheAttnParams& a, const LaunchCtx& ctx) {
   p.rows = a.n * a.group;
   p.row_groups = (p.rows + C::kRows - 1) / C::kRows;
   p.max_ctas = ctx.num_sms * C::kCtas;
+  if (ctx.max_ctas > 0 && ctx.max_ctas < p.max_ctas) p.max_ctas = ctx.max_ctas;
   p.part_o = reinterpret_cast<float*>(a.ws);
   p.part_ml = reinterpret_cast<float2*>(a.ws + 2LL * p.max_ctas * C::kRows * C::kD * 4);
   kern<<<p.max_ctas, C::kThreads, C::kSmem, ctx.stream>>>(tk, tv, p);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) {
-    cache_join_kernel<C><<<dim3((unsigned)p.row_groups, (unsigned)a.c.H, (unsigned)a.B), 128, 0, ctx.stream>>>(p);
-    e = cudaGetLastError();
+    // Programmatic launch: the blocks come up while the first kernel ends, and
+    // wait for it before they read its parts.
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.row_groups * (C::kRows * C::kD / 512)), (unsigned)a.c.H, (unsigned)a.B);
+    cfg.blockDim = dim3(128);
+    cfg.stream = ctx.stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, cache_join_kernel<C>, p);
   }
   if (e != cudaSuccess) {
     set_error("cache attention launch failed: %s", cudaGetErrorString(e));

@@ -72,6 +72,7 @@ struct LaunchCtx {
   cudaStream_t stream;
   int num_sms;
   int dev;
+  int max_ctas;  // 0: no cap (fa_set_max_ctas)
 };
 
 int launch_cache_append(const AppendParams& p, int kind, int dtype, const LaunchCtx& ctx);

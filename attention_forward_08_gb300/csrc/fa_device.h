@@ -7,6 +7,7 @@ namespace fa {
 struct DeviceInfo {
   int dev;
   int num_sms;
+  int max_ctas;              // fa_set_max_ctas (0: no cap)
   unsigned int* status;      // the device status word (kStatus* bits)
   long long timeout_cycles;  // bound on every wait, in SM clock cycles
 };

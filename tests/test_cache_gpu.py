@@ -281,6 +281,28 @@ def test_long_cache_and_long_offsets(fa):
         check_attention(fa, ref, q, table, lens, got)
 
 
+@pytest.mark.parametrize("ctas", [1, 2, 7])
+@pytest.mark.parametrize("kind,io,D,page,Hq,Hkv,n", [
+    (E4M3, BF16, 128, 64, 8, 2, 1), (I8, F16, 64, 16, 6, 3, 1), (E4M3, F16, 256, 128, 4, 2, 1),
+    (E4M3, BF16, 128, 16, 8, 2, 6), (I8, BF16, 64, 32, 8, 1, 40), (I8, BF16, 256, 16, 8, 1, 4),
+])
+def test_long_parts(fa, ctas, kind, io, D, page, Hq, Hkv, n):
+    """Few thread blocks: each runs round its ring many times, over parts of several sequences and heads."""
+    fa.fa_set_max_ctas(ctas)
+    try:
+        attention_case(fa, kind=kind, io=io, D=D, page=page, Hq=Hq, Hkv=Hkv, n=n, lens=(2500, n, 777, 0 if n == 1 else n, 1300),
+                       track=True)
+        attention_case(fa, kind=kind, io=io, D=D, page=page, Hq=Hq, Hkv=Hkv, n=n, lens=(4000,) * 3, window=900)
+    finally:
+        fa.fa_set_max_ctas(0)
+
+
+def test_full_machine(fa):
+    """Every thread block gets parts longer than its ring."""
+    attention_case(fa, Hq=16, Hkv=8, lens=(6000, 5000, 7001, 6500))
+    attention_case(fa, Hq=32, Hkv=8, n=5, lens=(4000, 5000, 3001, 2500))
+
+
 @pytest.mark.parametrize("n", [1, 5, 150])
 def test_attention_strided(fa, n):
     """Token-major q and output, pools interleaved, a table that is a slice of a wider one."""
