@@ -74,10 +74,10 @@ struct DecCfg {
   static constexpr int kRingBytes = kStages * kStageBytes;
   // The warps join through the ring's memory: kWarps x (rows x D fp32).
   static constexpr int kJoinBytes = kWarps * kRows * kD * 4;
-  static_assert(kJoinBytes <= kRingBytes && kWarps < kStages && kStages <= 64, "ring size");
+  static_assert(kJoinBytes <= kRingBytes && kWarps < kStages && kStages <= 24, "ring size");
   static_assert(kMT * kD <= 256, "32 rows of 256 columns do not fit the registers");
   static constexpr int kOffQ = kRingBytes, kOffMl = kOffQ + kQBytes, kOffMeta = kOffMl + kWarps * kRows * 8;
-  static constexpr int kOffBar = kOffMeta + kStages * 32, kOffRs = kOffBar + kStages * 16;
+  static constexpr int kOffBar = kOffMeta + 64 * 32, kOffRs = kOffBar + kStages * 16;
   static constexpr int kOffTmp = kOffRs + kRows * 4;
   static constexpr int kSmem = 1024 + kOffTmp + 16;
 };
@@ -85,8 +85,8 @@ struct DecCfg {
 // What a consumer needs beside a tile's bytes.
 struct DecMeta {
   float ks[2], vs[2];  // scales of its two halves of 16 tokens
-  int ok;              // bit i: half i is there
-  int pad[3];
+  int ok[2];           // whether they are there
+  int pad[2];
 };
 
 struct DecParams {
@@ -111,88 +111,112 @@ __device__ __forceinline__ DecSeq dec_seq(const CacheAttnParams& a, int b) {
   return s;
 }
 
-// Tokens that rows r0 .. r1-1 of a K/V head see: [lo, hi), empty as {0, 0}.
-__device__ __forceinline__ int2 dec_span(const CacheAttnParams& a, const DecSeq& s, int r0, int r1) {
-  const int i0 = r0 / a.group, i1 = min((r1 - 1) / a.group, s.nq - 1);
+// Tokens that query rows i0 .. i1 see: [lo, hi), empty as {0, 0}.
+__device__ __forceinline__ int2 dec_span(const CacheAttnParams& a, const DecSeq& s, int i0, int i1) {
+  i1 = min(i1, s.nq - 1);
   if (i0 > i1) return make_int2(0, 0);
   const int p0 = s.len - s.nq + i0, p1 = s.len - s.nq + i1;
   const int hi = a.causal ? min(s.len, p1 + 1) : s.len;
   const int lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
   return lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
 }
+// ... and the query rows of row group rg.
+template <class C>
+__device__ __forceinline__ int2 dec_group_span(const DecParams& p, const DecSeq& s, int rg) {
+  if (p.row_groups == 1) return dec_span(p.a, s, 0, p.a.n - 1);
+  return dec_span(p.a, s, rg * C::kRows / p.a.group, (min(p.rows, (rg + 1) * C::kRows) - 1) / p.a.group);
+}
 
 // Tiles of one segment: at least one, so that empty rows are written too.
 template <class C>
 __device__ __forceinline__ int dec_tiles(const DecParams& p, const DecSeq& s, int rg) {
-  const int2 v = dec_span(p.a, s, rg * C::kRows, min(p.rows, (rg + 1) * C::kRows));
+  const int2 v = dec_group_span<C>(p, s, rg);
   return max(1, (v.y + C::kTile - 1) / C::kTile - v.x / C::kTile);
 }
+// (A call, not inlined: kernels this short run once through most of their
+// instructions, and fetching code costs more than calling it.)
 template <class C>
-__device__ __forceinline__ long long dec_seq_tiles(const DecParams& p, int b) {  // all heads
-  const DecSeq s = dec_seq(p.a, b);
-  long long n = 0;
-  for (int rg = 0; rg < p.row_groups; ++rg) n += dec_tiles<C>(p, s, rg);
-  return n * p.a.c.H;
+__device__ __noinline__ int dec_many_groups(const DecParams& p, DecSeq s, int groups) {
+  int n = 0;
+#pragma unroll 1
+  for (int rg = 0; rg < groups; ++rg) n += dec_tiles<C>(p, s, rg);
+  return n;
+}
+template <class C>
+__device__ __forceinline__ int dec_head_tiles(const DecParams& p, const DecSeq& s) {  // of all row groups
+  return p.row_groups == 1 ? dec_tiles<C>(p, s, 0) : dec_many_groups<C>(p, s, p.row_groups);
 }
 
-__device__ __forceinline__ long long warp_sum_ll(long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
-}
-__device__ __forceinline__ long long warp_scan_ll(long long v, int lane) {  // inclusive
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xFFFFFFFFu, v, o);
-    if (lane >= o) v += u;
-  }
-  return v;
-}
-// a / b for a, b >= 0 (64-bit divisions are long; these numbers are small).
-__device__ __forceinline__ long long div_ll(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
-// Every warp finds its place for itself: there is no barrier in it, and up to
-// 32 sequences take one load.
-// All tiles, and those before sequence `b`.
+// The line's length, and where tile `part * nth` lies (part: tiles a thread
+// block, below): its sequence, and the tiles before that.  Every warp finds it
+// for itself, without a barrier; up to 32 sequences take one load.  (The host
+// keeps all counts below 2^31.)
+struct DecPlace {
+  int total, part, b, before;
+};
 template <class C>
-__device__ __forceinline__ void dec_count(const DecParams& p, int b, long long& before, long long& total) {
+__device__ __forceinline__ int dec_part(const DecParams& p, int total);
+
+template <class C>
+__device__ __forceinline__ DecPlace dec_find(const DecParams& p, unsigned nth) {
   const int lane = threadIdx.x & 31;
-  long long all = 0, lower = 0;
+  DecPlace at;
+  int mine = 0, all = 0;
+#pragma unroll 1
   for (int i = lane; i < p.a.B; i += 32) {
-    const long long n = dec_seq_tiles<C>(p, i);
+    mine = dec_head_tiles<C>(p, dec_seq(p.a, i)) * p.a.c.H;
+    all += mine;
+  }
+  at.total = __reduce_add_sync(0xFFFFFFFFu, all);
+  at.part = dec_part<C>(p, at.total);
+  at.b = at.before = 0;
+  const long long t = (long long)at.part * nth;
+  if (t >= at.total) return at;
+#pragma unroll 1
+  for (int base = 0;; base += 32) {
+    if (p.a.B > 32) mine = base + lane < p.a.B ? dec_head_tiles<C>(p, dec_seq(p.a, base + lane)) * p.a.c.H : 0;
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += u;
+    }
+    upto += at.before;
+    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, t < upto);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      at.before = __shfl_sync(0xFFFFFFFFu, upto - mine, l);
+      at.b = base + l;
+      return at;
+    }
+    at.before = __shfl_sync(0xFFFFFFFFu, upto, 31);
+  }
+}
+
+// The line's length, and the tiles before sequence b.
+template <class C>
+__device__ __forceinline__ DecPlace dec_before(const DecParams& p, int b) {
+  const int lane = threadIdx.x & 31;
+  int all = 0, lower = 0;
+#pragma unroll 1
+  for (int i = lane; i < p.a.B; i += 32) {
+    const int n = dec_head_tiles<C>(p, dec_seq(p.a, i)) * p.a.c.H;
     all += n;
     if (i < b) lower += n;
   }
-  total = warp_sum_ll(all);
-  before = warp_sum_ll(lower);
-}
-
-// The sequence that holds tile `t` of the line, and the tiles before it.
-template <class C>
-__device__ __forceinline__ int dec_find(const DecParams& p, long long t, long long& before) {
-  const int lane = threadIdx.x & 31;
-  before = 0;
-  for (int base = 0; base < p.a.B; base += 32) {
-    const long long mine = base + lane < p.a.B ? dec_seq_tiles<C>(p, base + lane) : 0;
-    const long long upto = before + warp_scan_ll(mine, lane);
-    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, t < upto);
-    if (hit) {
-      const int at = __ffs(hit) - 1;
-      before = __shfl_sync(0xFFFFFFFFu, upto - mine, at);
-      return base + at;
-    }
-    before = __shfl_sync(0xFFFFFFFFu, upto, 31);
-  }
-  return p.a.B - 1;  // not reached: t < total
+  DecPlace at;
+  at.total = __reduce_add_sync(0xFFFFFFFFu, all);
+  at.part = dec_part<C>(p, at.total);
+  at.b = b;
+  at.before = __reduce_add_sync(0xFFFFFFFFu, lower);
+  return at;
 }
 
 // Tiles of one thread block's part of the line: an equal share of the grid's,
 // and no less than two tiles a warp.
 template <class C>
-__device__ __forceinline__ long long dec_part(const DecParams& p, long long total) {
-  return max((long long)C::kMinTiles, div_ll(total + p.max_ctas - 1, p.max_ctas));
+__device__ __forceinline__ int dec_part(const DecParams& p, int total) {
+  return max(C::kMinTiles, (int)(((unsigned)total + p.max_ctas - 1) / (unsigned)p.max_ctas));
 }
 
 // ------------------------------------------------------------------ tensor-core pieces
@@ -269,19 +293,23 @@ __device__ __forceinline__ int dec_col(int i, int n) {
 
 // ------------------------------------------------------------------ the kernel
 
-// Eight columns of one output row, and its L.
+// Where the warps leave column d (a multiple of 4) of their row `r` to be joined.
 template <class C>
-__device__ __forceinline__ void dec_write(const CacheAttnParams& a, int b, int h, int row, int d, const float (&x)[8],
+__device__ __forceinline__ float* dec_join_at(float* base, int r, int d) {
+  return base + r * C::kD + (d & ~31) + ((((d >> 2) & 7) + 2 * (d >> 5) + r) & 7) * 4;
+}
+
+// Four columns of one output row, and its L.
+template <class C>
+__device__ __forceinline__ void dec_write(const CacheAttnParams& a, int b, int h, int row, int d, const float4& x,
                                           float top, float sum) {
   const int i = row / a.group, head = h * a.group + row % a.group;
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-  uint4 y;
-  uint32_t* u = &y.x;
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    u[e] = C::kF16 ? pack_f16x2(x[2 * e] * inv, x[2 * e + 1] * inv) : pack_bf16x2(x[2 * e] * inv, x[2 * e + 1] * inv);
-  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + b * a.os[0] + head * a.os[1] + i * a.os[2] + d) = y;
-  if (d == 0) a.lse[((long long)b * a.Hq + head) * a.n + i] = sum > 0.0f ? (top + log2f(sum)) * kDecLn2 : -INFINITY;
+  const float inv = sum > 0.0f ? rcp_approx(sum) : 0.0f;
+  uint2 y;
+  y.x = C::kF16 ? pack_f16x2(x.x * inv, x.y * inv) : pack_bf16x2(x.x * inv, x.y * inv);
+  y.y = C::kF16 ? pack_f16x2(x.z * inv, x.w * inv) : pack_bf16x2(x.z * inv, x.w * inv);
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + b * a.os[0] + head * a.os[1] + i * a.os[2] + d) = y;
+  if (d == 0) a.lse[((long long)b * a.Hq + head) * a.n + i] = sum > 0.0f ? (top + lg2(sum)) * kDecLn2 : -INFINITY;
 }
 
 // A bounded wait by a whole warp; false once it ran out (or another did).
@@ -311,7 +339,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* s_q = smem + C::kOffQ;
   float2* s_ml = reinterpret_cast<float2*>(smem + C::kOffMl);        // [warp][row]: maximum, sum
-  DecMeta* s_meta = reinterpret_cast<DecMeta*>(smem + C::kOffMeta);  // [stage]
+  DecMeta* s_meta = reinterpret_cast<DecMeta*>(smem + C::kOffMeta);  // [tile % 64]
   uint64_t* s_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* s_empty = s_full + kS;
   float* s_rs = reinterpret_cast<float*>(smem + C::kOffRs);  // [row]: 2^-(scaling of the query row)
@@ -333,91 +361,110 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // This block's part of the line, and where it begins.
-  long long before, total;
-  dec_count<C>(p, 0, before, total);
-  const long long part = dec_part<C>(p, total), t0 = part * blockIdx.x, t1 = min(total, t0 + part);
-  if (t0 >= total) return;
-  int b = dec_find<C>(p, t0, before);
+  const DecPlace place = dec_find<C>(p, blockIdx.x);
+  if ((long long)place.part * blockIdx.x >= place.total) return;
+  const int t0 = place.part * (int)blockIdx.x, t1 = (int)min((long long)place.total, (long long)t0 + place.part);
+  int b = place.b;
   DecSeq seq = dec_seq(a, b);
-  if (tid == 0 && before >= t0) (void)checked_len(c, a.lens[b]);  // one block a sequence tells about its length
-  long long seg0 = before;  // first tile of the current segment
+  if (tid == 0 && place.before >= t0) (void)checked_len(c, a.lens[b]);  // one block a sequence tells about its length
+  int seg0 = place.before;  // first tile of the current segment
   int h = 0, rg = 0;
   {  // the segment of t0
-    long long per_head = 0;
-    for (int r = 0; r < p.row_groups; ++r) per_head += dec_tiles<C>(p, seq, r);
-    h = (int)div_ll(t0 - seg0, per_head);
+    const int per_head = dec_head_tiles<C>(p, seq);
+    h = (int)((unsigned)(t0 - seg0) / (unsigned)per_head);
     seg0 += h * per_head;
-    while (seg0 + dec_tiles<C>(p, seq, rg) <= t0) seg0 += dec_tiles<C>(p, seq, rg++);
+    if (p.row_groups > 1) {
+      int tiles;
+#pragma unroll 1
+      while (seg0 + (tiles = dec_many_groups<C>(p, seq, rg + 1) - dec_many_groups<C>(p, seq, rg)) <= t0) {
+        seg0 += tiles;
+        ++rg;
+      }
+    }
   }
   __syncthreads();  // the barriers are ready
   const int sub = min(c.page, C::kTile), sub_log2 = min(c.page_log2, 5);  // a block's part of a tile
   const int subs = C::kTile >> sub_log2;                                  // parts a tile: 1 or 2
   int tile0 = 0;  // tiles of this block's earlier pieces: tile k of all uses stage k % kS
 
-  for (long long at = t0; at < t1;) {
+#pragma unroll 1
+  for (int at = t0; at < t1;) {
     const int r0 = rg * C::kRows, r1 = min(p.rows, r0 + C::kRows);
     const int tiles = dec_tiles<C>(p, seq, rg);
-    const int2 span = dec_span(a, seq, r0, r1);
-    const int first_tile = span.x / C::kTile + (int)(at - seg0);
-    const int n_tiles = (int)(min(t1, seg0 + tiles) - at);
+    const int2 span = dec_group_span<C>(p, seq, rg);
+    const int first_tile = span.x / C::kTile + at - seg0;
+    const int n_tiles = min(t1, seg0 + tiles) - at;
     const bool whole = n_tiles == tiles;
 
     if (warp == kW) {
       // ---------------------------------------------------------- producer
-      // Lane l looks up part l of the next 32: its block, and the scales.
+      // Parts of 32 tiles' (or 16) blocks at a time: lane l looks up part l's
+      // block, one batch ahead, and writes its scales where the consumers of
+      // tile k find them (entry k % 64: the ring is shorter than a batch, so
+      // that nobody reads the batch before the last any more).
+      const int shift = subs - 1, per_batch = 32 >> shift, sub_at = lane & shift;
       int stage = tile0 % kS;
       uint32_t phase = (uint32_t)(tile0 / kS) & 1u;
-      const int per_batch = 32 / subs;
-      int blk = -1, issued = 0;
+      int issued = 0, next_blk = -1;
       bool ok = true;
-      float ks = 0.0f, vs = 0.0f;
-      for (; issued < n_tiles && ok; ++issued) {
-        const int from = issued % per_batch * subs;
-        if (from == 0) {
-          const int k = issued + (lane >> (subs - 1));
-          const int tok = (first_tile + k) * C::kTile + (lane & (subs - 1)) * sub;
-          blk = -1;
-          ks = vs = 0.0f;
-          if (k < n_tiles && tok < span.y && tok + sub > span.x) {
-            blk = checked_block(c, c.table, c.table_stride, b, tok >> c.page_log2);
-            if (blk >= 0) {
-              ks = __ldg(c.k_scale + (long long)blk * c.H + h);
-              vs = __ldg(c.v_scale + (long long)blk * c.H + h);
-            }
-          }
+      auto look_up = [&](int k0) {
+        const int k = k0 + (lane >> shift), tok = (first_tile + k) * C::kTile + sub_at * sub;
+        return k < n_tiles && tok < span.y && tok + sub > span.x
+                   ? checked_block(c, c.table, c.table_stride, b, tok >> c.page_log2)
+                   : -1;
+      };
+      next_blk = look_up(0);
+      int y = (first_tile * C::kTile) & (c.page - 1);  // 0 where blocks are no longer than a tile
+#pragma unroll 1
+      for (int k0 = 0; k0 < n_tiles && ok; k0 += per_batch) {
+        const int blk = next_blk;
+        float ks = 0.0f, vs = 0.0f;
+        if (blk >= 0) {
+          ks = __ldg(c.k_scale + (long long)blk * c.H + h);
+          vs = __ldg(c.v_scale + (long long)blk * c.H + h);
         }
-        const int b0 = __shfl_sync(0xFFFFFFFFu, blk, from), b1 = __shfl_sync(0xFFFFFFFFu, blk, from + subs - 1);
-        const float k0 = __shfl_sync(0xFFFFFFFFu, ks, from), k1 = __shfl_sync(0xFFFFFFFFu, ks, from + subs - 1);
-        const float v0 = __shfl_sync(0xFFFFFFFFu, vs, from), v1 = __shfl_sync(0xFFFFFFFFu, vs, from + subs - 1);
-        if (tile0 + issued >= kS) ok = dec_wait(s_empty + stage, phase ^ 1u, s_abort, a);
-        if (!ok) break;
-        if (lane == 0) {
-          DecMeta* meta = s_meta + stage;
-          *reinterpret_cast<float4*>(meta) = make_float4(k0, k1, v0, v1);
-          meta->ok = (b0 >= 0 ? 1 : 0) | (b1 >= 0 ? 2 : 0);
-          const int boxes = (b0 >= 0) + (subs == 2 && b1 >= 0);
-          uint64_t* bar = s_full + stage;
-          if (boxes == 0) {
-            mbar_arrive(bar);
-          } else {
-            mbar_arrive_expect_tx(bar, (uint32_t)(boxes * sub * C::kD * 2));
+        next_blk = look_up(k0 + per_batch);
+        if (k0 + (lane >> shift) < n_tiles) {
+          DecMeta* meta = s_meta + ((tile0 + k0 + (lane >> shift)) & 63);
+          meta->ks[sub_at] = ks;
+          meta->vs[sub_at] = vs;
+          meta->ok[sub_at] = blk >= 0;
+          if (subs == 1) meta->ks[1] = ks, meta->vs[1] = vs, meta->ok[1] = blk >= 0;
+        }
+        __syncwarp();
+        const int n = min(per_batch, n_tiles - k0);
+#pragma unroll 1
+        for (int i = 0; i < n; ++i, ++issued) {
+          const int b0 = __shfl_sync(0xFFFFFFFFu, blk, i << shift);
+          const int b1 = subs == 2 ? __shfl_sync(0xFFFFFFFFu, blk, 2 * i + 1) : -1;
+          if (tile0 + issued >= kS && !dec_wait(s_empty + stage, phase ^ 1u, s_abort, a)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            uint64_t* bar = s_full + stage;
             uint8_t* dst = smem + stage * C::kStageBytes;
-            const int y = ((first_tile + issued) * C::kTile) & (c.page - 1);  // 0 where blocks are no longer than a tile
+            const int boxes = (b0 >= 0) + (b1 >= 0);
+            if (boxes == 0)
+              mbar_arrive(bar);
+            else
+              mbar_arrive_expect_tx(bar, (uint32_t)(boxes * sub * C::kD * 2));
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              const int from_blk = u ? b1 : b0;
-              if (u < subs && from_blk >= 0) {
+              const int from = u ? b1 : b0;
+              if (from >= 0) {
 #pragma unroll
                 for (int col = 0; col < C::kCols; ++col) {
                   uint8_t* d = dst + (col * C::kTile + u * sub) * C::kRowBytes;
-                  tma_load_4d(d, &tk, bar, col * 128, y, h, from_blk);
-                  tma_load_4d(d + C::kTileBytes, &tv, bar, col * 128, y, h, from_blk);
+                  tma_load_4d(d, &tk, bar, col * 128, y, h, from);
+                  tma_load_4d(d + C::kTileBytes, &tv, bar, col * 128, y, h, from);
                 }
               }
             }
           }
+          y = (y + C::kTile) & (c.page - 1);
+          if (++stage == kS) stage = 0, phase ^= 1u;
         }
-        if (++stage == kS) stage = 0, phase ^= 1u;
       }
       // After an expired wait: the copies in flight land first (a bounded wait
       // again), then the block ends.
@@ -432,6 +479,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     } else {
       // ---------------------------------------------------------- consumers
       // The query rows, scaled to f16 and laid out as the tensor core's operand.
+#pragma unroll 1
       for (int r = warp; r < C::kRows; r += kW) {
         constexpr int kE = C::kD / 32;  // elements a lane
         float f[kE];
@@ -491,8 +539,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           l[mt][x] = 0.0f;
           const int r = mt * 16 + g + 8 * x, row = r0 + r;
           rs[mt][x] = s_rs[r];
-          const bool real = row < r1 && row / a.group < seq.nq;
-          const int2 v = real ? dec_span(a, seq, row, row + 1) : make_int2(0, 0x7fffffff);
+          const int i = row / a.group;
+          const bool real = row < r1 && i < seq.nq;
+          const int2 v = real ? dec_span(a, seq, i, i) : make_int2(0, 0x7fffffff);
           // a row of the tile that is no query row may see anything: nothing of it is written
           lo_row[mt][x] = v.x;
           hi_row[mt][x] = row < r1 && !real ? 0 : v.y;
@@ -517,8 +566,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         }
         const uint32_t tile_k = smem_u32(smem + stage * C::kStageBytes), tile_v = tile_k + C::kTileBytes;
         const int tok0 = (first_tile + k) * C::kTile;
-        const float4 meta = *reinterpret_cast<const float4*>(s_meta + stage);
-        const int ok_blk = s_meta[stage].ok;
+        const DecMeta* meta_at = s_meta + ((tile0 + k) & 63);
+        const float4 meta = *reinterpret_cast<const float4*>(meta_at);
+        const int2 here = *reinterpret_cast<const int2*>(meta_at->ok);
+        const int ok_blk = here.x + 2 * here.y;
         const bool full = ok_blk == 3 && lo_all <= tok0 && tok0 + C::kTile <= hi_all;
 
         // S = Q K^T: 4 column tiles of 8 tokens
@@ -714,35 +765,38 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           const int r = mt * 16 + g + 8 * x;
           float top = -INFINITY;
           for (int w = 0; w < kW; ++w) top = fmaxf(top, s_ml[w * C::kRows + r].x);
-          const float f = m[mt][x] == -INFINITY ? 0.0f : ex2(m[mt][x] - top) * vs_unit;
-          float* dst = s_join + (warp * C::kRows + r) * C::kD;
+          const float f = m[mt][x] == -INFINITY ? 0.0f : ex2(m[mt][x] - top), fo = f * vs_unit;
+          if (t == 0) s_ml[warp * C::kRows + r].y = l[mt][x] * f;
+          // four columns at a time, units rotated so that no two lanes meet in a bank
 #pragma unroll
-          for (int i = 0; i < C::kNTiles; ++i) {
-            dst[dec_col<C>(i, 2 * t)] = o[mt][i][2 * x] * f;
-            dst[dec_col<C>(i, 2 * t + 1)] = o[mt][i][2 * x + 1] * f;
+          for (int q = 0; q < C::kNTiles / 2; ++q) {  // 2 * D / 8 values a row: columns of n = 2t, then 2t + 1
+            constexpr int kRun = C::kD == 64 ? 8 : 16;
+            const int i = (q * 4) % C::kNTiles, e = 2 * x + (q * 4) / C::kNTiles;
+            const int d = dec_col<C>(i, 2 * t + (e & 1));
+            static_assert(kRun % 4 == 0, "four neighbouring columns");
+            *reinterpret_cast<float4*>(dec_join_at<C>(s_join, warp * C::kRows + r, d)) =
+                make_float4(o[mt][i][e] * fo, o[mt][i + 1][e] * fo, o[mt][i + 2][e] * fo, o[mt][i + 3][e] * fo);
           }
         }
       named_bar_sync(1, 32 * kW);
       const int slot = 2 * blockIdx.x + (at > seg0 ? 0 : 1);
-      for (int v = tid; v < C::kRows * (C::kD / 8); v += 32 * kW) {
-        const int r = v / (C::kD / 8), d = (v % (C::kD / 8)) * 8;
-        if (r0 + r >= r1) break;
-        float top = -INFINITY, sum = 0.0f, x[8] = {};
-        for (int w = 0; w < kW; ++w) top = fmaxf(top, s_ml[w * C::kRows + r].x);
+#pragma unroll 1
+      for (int v = tid; v < (r1 - r0) * (C::kD / 4); v += 32 * kW) {
+        const int r = v / (C::kD / 4), d = (v % (C::kD / 4)) * 4;
+        float top = -INFINITY, sum = 0.0f;
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
         for (int w = 0; w < kW; ++w) {
           const float2 ml = s_ml[w * C::kRows + r];
-          if (ml.x > -INFINITY) sum += ml.y * ex2(ml.x - top);
-          const float4* q = reinterpret_cast<const float4*>(s_join + (w * C::kRows + r) * C::kD + d);
-          const float4 y0 = q[0], y1 = q[1];
-          x[0] += y0.x, x[1] += y0.y, x[2] += y0.z, x[3] += y0.w;
-          x[4] += y1.x, x[5] += y1.y, x[6] += y1.z, x[7] += y1.w;
+          const float4 y = *reinterpret_cast<const float4*>(dec_join_at<C>(s_join, w * C::kRows + r, d));
+          top = fmaxf(top, ml.x);
+          sum += ml.y;
+          x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
         }
         if (whole) {
           dec_write<C>(a, b, h, r0 + r, d, x, top, sum);
         } else {
-          float4* q = reinterpret_cast<float4*>(p.part_o + ((long long)slot * C::kRows + r) * C::kD + d);
-          q[0] = make_float4(x[0], x[1], x[2], x[3]);
-          q[1] = make_float4(x[4], x[5], x[6], x[7]);
+          *reinterpret_cast<float4*>(p.part_o + ((long long)slot * C::kRows + r) * C::kD + d) = x;
           if (d == 0) p.part_ml[(long long)slot * C::kRows + r] = make_float2(top, sum);
         }
       }
@@ -774,18 +828,11 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
   constexpr int kRowsHere = 512 / C::kD;  // rows a block
   const int rg = blockIdx.x / (C::kRows / kRowsHere), piece = blockIdx.x % (C::kRows / kRowsHere);
   const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  long long before, total;
-  dec_count<C>(p, b, before, total);
+  const DecPlace place = dec_before<C>(p, b);
   const DecSeq seq = dec_seq(a, b);
-  long long per_head = 0, u0 = 0;
-  for (int r = 0; r < p.row_groups; ++r) {
-    const int n = dec_tiles<C>(p, seq, r);
-    if (r < rg) u0 += n;
-    per_head += n;
-  }
-  u0 += before + h * per_head;
-  const long long u1 = u0 + dec_tiles<C>(p, seq, rg), part = dec_part<C>(p, total);
-  const int c0 = (int)div_ll(u0, part), c1 = (int)div_ll(u1 - 1, part);
+  const int u0 = place.before + h * dec_head_tiles<C>(p, seq) + (rg > 0 ? dec_many_groups<C>(p, seq, rg) : 0);
+  const int u1 = u0 + dec_tiles<C>(p, seq, rg);
+  const int c0 = u0 / place.part, c1 = (u1 - 1) / place.part;
   const int r = piece * kRowsHere + tid / (C::kD / 4), row = rg * C::kRows + r, d = tid % (C::kD / 4) * 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
   if (c0 == c1 || row >= p.rows) return;
@@ -802,13 +849,7 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
     sum = fmaf(sum, f, ml.y * g);
     x.x = fmaf(x.x, f, y.x * g), x.y = fmaf(x.y, f, y.y * g), x.z = fmaf(x.z, f, y.z * g), x.w = fmaf(x.w, f, y.w * g);
   }
-  const int i = row / a.group, head = h * a.group + row % a.group;
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-  uint2 y;
-  y.x = C::kF16 ? pack_f16x2(x.x * inv, x.y * inv) : pack_bf16x2(x.x * inv, x.y * inv);
-  y.y = C::kF16 ? pack_f16x2(x.z * inv, x.w * inv) : pack_bf16x2(x.z * inv, x.w * inv);
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + b * a.os[0] + head * a.os[1] + i * a.os[2] + d) = y;
-  if (d == 0) a.lse[((long long)b * a.Hq + head) * a.n + i] = sum > 0.0f ? (top + log2f(sum)) * kDecLn2 : -INFINITY;
+  dec_write<C>(a, b, h, row, d, x, top, sum);
 }
 
 }  // namespace fa

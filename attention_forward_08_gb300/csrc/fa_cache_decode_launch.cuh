@@ -37,6 +37,12 @@ int launch_decode(const CacheAttnParams& a, const LaunchCtx& ctx) {
   p.a = a;
   p.rows = a.n * a.group;
   p.row_groups = (p.rows + C::kRows - 1) / C::kRows;
+  // The line's counts are 32-bit numbers.
+  if ((double)a.B * a.c.H * p.row_groups * ((double)a.c.M * a.c.page / C::kTile + 1) >= 2147483648.0) {
+    set_error("B * H_kv * row groups (%d) * table width (%d tokens) is beyond the kernel's index range", p.row_groups,
+              a.c.M * a.c.page);
+    return FA_ERR_UNSUPPORTED;
+  }
   p.max_ctas = ctx.num_sms * C::kCtas;
   if (ctx.max_ctas > 0 && ctx.max_ctas < p.max_ctas) p.max_ctas = ctx.max_ctas;
   p.part_o = reinterpret_cast<float*>(a.ws);
