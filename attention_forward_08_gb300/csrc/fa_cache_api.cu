@@ -228,6 +228,12 @@ CacheAttnParams attn_params(const fa_cache_attn_args* a, unsigned int* status, l
   return p;
 }
 
+long long attn_workspace(const CacheAttnParams& p, int num_sms) {
+  return p.c.D == 64    ? cache_attn_workspace_d64(p, num_sms)
+         : p.c.D == 128 ? cache_attn_workspace_d128(p, num_sms)
+                        : cache_attn_workspace_d256(p, num_sms);
+}
+
 int check_evict(const fa_cache_evict_args* a) {
   if (!a) return invalid("args is NULL");
   int rc = check_cache(a->cache);
@@ -308,10 +314,14 @@ int fa_cache_attn(const fa_cache_attn_args* a) {
   rc = current_device(&dev);
   if (rc != FA_OK) return rc;
   const CacheAttnParams p = attn_params(a, dev.status, dev.timeout_cycles);
-  rc = check_workspace(a->workspace, a->workspace_bytes, cache_attn_workspace(p, dev.num_sms),
+  rc = check_workspace(a->workspace, a->workspace_bytes, attn_workspace(p, dev.num_sms),
                        "fa_cache_attn_workspace_bytes");
   if (rc != FA_OK) return rc;
-  return launch_cache_attn(p, a->cache.kind, a->dtype, {static_cast<cudaStream_t>(a->stream), dev.num_sms, dev.dev, dev.max_ctas});
+  const LaunchCtx ctx = {static_cast<cudaStream_t>(a->stream), dev.num_sms, dev.dev, dev.max_ctas};
+  const bool f16 = a->dtype == FA_DTYPE_F16;
+  return p.c.D == 64    ? launch_cache_attn_d64(p, a->cache.kind, f16, ctx)
+         : p.c.D == 128 ? launch_cache_attn_d128(p, a->cache.kind, f16, ctx)
+                        : launch_cache_attn_d256(p, a->cache.kind, f16, ctx);
 }
 
 long long fa_cache_attn_workspace_bytes(const fa_cache_attn_args* a) {
@@ -320,7 +330,7 @@ long long fa_cache_attn_workspace_bytes(const fa_cache_attn_args* a) {
   if (check_attn(a) != FA_OK) return -1;
   DeviceInfo dev;
   if (current_device(&dev) != FA_OK) return -1;
-  return cache_attn_workspace(attn_params(a, dev.status, dev.timeout_cycles), dev.num_sms);
+  return attn_workspace(attn_params(a, dev.status, dev.timeout_cycles), dev.num_sms);
 }
 
 int fa_cache_evict(const fa_cache_evict_args* a) {

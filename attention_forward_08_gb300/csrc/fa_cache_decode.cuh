@@ -42,7 +42,7 @@
 
 namespace fa {
 
-constexpr float kDecLn2 = 0.6931471805599453f;
+constexpr float kDecLn2 = 0.6931471805599453f, kLog2eF = 1.4426950408889634f;
 constexpr float kDecLazy = 8.0f;  // the running maximum moves when it grows by more than 2^8: p stays below 2^8 in f16
 constexpr long long kDecDrainCycles = 1LL << 33;
 
@@ -284,6 +284,23 @@ __device__ __forceinline__ void dec_key_words(uint32_t tile, int r, int t, uint3
   }
 }
 
+// A power of two that brings a query row whose largest entry is `top` into
+// [2^9, 2^10), kept inside the normal numbers, and its inverse.
+__device__ __forceinline__ void dec_row_scale(float top, float& up, float& down) {
+  const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -110), 127);
+  up = __uint_as_float((uint32_t)(9 - ex + 127) << 23);
+  down = __uint_as_float((uint32_t)(ex - 9 + 127) << 23);
+}
+
+// The 32-bit word, in the A operand [k-step, lane, 4] of 16 query rows, of
+// row r's elements d and d + 1 (d even).
+template <int kD>
+__device__ __forceinline__ int dec_q_word(int r, int d) {
+  const int t = kD == 64 ? d / 16 : (d & 127) / 32;
+  const int kk = kD == 64 ? (d & 15) / 4 : 8 * (d / 128) + (d & 31) / 4;
+  return (kk * 32 + (r & 7) * 4 + t) * 4 + ((d & 3) / 2) * 2 + (r >> 3);
+}
+
 // Output columns.  Value n of PV's column tile i is column dec_col(i, n).
 template <class C>
 __device__ __forceinline__ int dec_col(int i, int n) {
@@ -505,21 +522,16 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           for (int e = 0; e < kE; ++e) top = fmaxf(top, fabsf(f[e]));
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-          // 2^(9 - exponent), kept inside the normal numbers
-          const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -110), 127);
-          up = __uint_as_float((uint32_t)(9 - ex + 127) << 23);
-          if (lane == 0) s_rs[r] = __uint_as_float((uint32_t)(ex - 9 + 127) << 23);
+          float down;
+          dec_row_scale(top, up, down);
+          if (lane == 0) s_rs[r] = down;
         } else if (lane == 0) {
           s_rs[r] = 1.0f;
         }
 #pragma unroll
         for (int e = 0; e < kE; e += 2) {
-          const int d = lane * kE + e;
-          const int tt = C::kD == 64 ? d / 16 : (d & 127) / 32;
-          const int kk = C::kD == 64 ? (d & 15) / 4 : 8 * (d / 128) + (d & 31) / 4;
-          const int reg = ((d & 3) / 2) * 2 + ((r & 15) >> 3);
-          const uint32_t at2 = (uint32_t)((((r >> 4) * C::kKSteps + kk) * 32 + (r & 7) * 4 + tt) * 16 + reg * 4);
-          *reinterpret_cast<uint32_t*>(s_q + at2) = pack_f16x2(f[e] * up, f[e + 1] * up);
+          const int at_word = (r >> 4) * C::kKSteps * 128 + dec_q_word<C::kD>(r & 15, lane * kE + e);
+          reinterpret_cast<uint32_t*>(s_q)[at_word] = pack_f16x2(f[e] * up, f[e + 1] * up);
         }
       }
       named_bar_sync(1, 32 * kW);
@@ -828,6 +840,7 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
   constexpr int kRowsHere = 512 / C::kD;  // rows a block
   const int rg = blockIdx.x / (C::kRows / kRowsHere), piece = blockIdx.x % (C::kRows / kRowsHere);
   const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const DecPlace place = dec_before<C>(p, b);
   const DecSeq seq = dec_seq(a, b);
   const int u0 = place.before + h * dec_head_tiles<C>(p, seq) + (rg > 0 ? dec_many_groups<C>(p, seq, rg) : 0);

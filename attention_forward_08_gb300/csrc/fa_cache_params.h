@@ -76,8 +76,13 @@ struct LaunchCtx {
 };
 
 int launch_cache_append(const AppendParams& p, int kind, int dtype, const LaunchCtx& ctx);
-int launch_cache_attn(const CacheAttnParams& p, int kind, int dtype, const LaunchCtx& ctx);
+// One head dim each (fa_cache_attn_d*.cu).
+int launch_cache_attn_d64(const CacheAttnParams& p, int kind, bool f16, const LaunchCtx& ctx);
+int launch_cache_attn_d128(const CacheAttnParams& p, int kind, bool f16, const LaunchCtx& ctx);
+int launch_cache_attn_d256(const CacheAttnParams& p, int kind, bool f16, const LaunchCtx& ctx);
+long long cache_attn_workspace_d64(const CacheAttnParams& p, int num_sms);
+long long cache_attn_workspace_d128(const CacheAttnParams& p, int num_sms);
+long long cache_attn_workspace_d256(const CacheAttnParams& p, int num_sms);
 int launch_cache_evict(const EvictParams& p, int kind, const LaunchCtx& ctx);
-long long cache_attn_workspace(const CacheAttnParams& p, int num_sms);
 
 }  // namespace fa

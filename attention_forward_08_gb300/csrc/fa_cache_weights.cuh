@@ -1,0 +1,173 @@
+// fa_cache_weights.cuh -- the attention weight that every cached token got:
+//
+//   weights[b, kvh, j] += sum over rows r of the K/V head of 2^(s_rj - L2_r)
+//
+// with L2 the row's logsumexp in base 2, known once the attention itself has
+// run.  A warp owns 32 tokens, holds their keys in registers and goes over the
+// rows, 16 at a time; sums stay in its lanes, so that nothing is added twice
+// or in an order that changes.  Scores are computed again from the keys: to
+// keep them would take 4 bytes a row and token (and a workspace as wide as
+// the table), while a key is 1 byte an element for all rows of its head.
+//
+// The query rows are brought into the tensor core's order once, by a small
+// kernel before this one, together with each row's two factors.
+//
+// Bound: the second reading of K (from L2 where it still is there) for few
+// rows, the tensor cores for many.
+#pragma once
+
+#include "fa_cache_decode.cuh"
+
+namespace fa {
+
+struct WeightParams {
+  CacheAttnParams a;
+  int rows, row_groups;  // rows of a K/V head, and groups of 16 of them
+  uint32_t* q;           // [B, H, row group, k-step, lane, 4]: A operands
+  float2* row;           // [B, H, row group * 16]: score to base 2 (without k_scale), L2 (+inf: a row that sees nothing)
+};
+
+// One warp a row (the grid has 16 warps a row group).
+template <bool kF16, int kD>
+__global__ void __launch_bounds__(256) cache_rows_kernel(const __grid_constant__ WeightParams p) {
+  const CacheAttnParams& a = p.a;
+  constexpr int kE = kD / 32;
+  const int lane = threadIdx.x & 31, r = blockIdx.x * 8 + (threadIdx.x >> 5), h = blockIdx.y, b = blockIdx.z;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int i = r / a.group, head = h * a.group + r % a.group;
+  const bool in = r < p.rows;
+  float f[kE], up = 1.0f, down = 1.0f;
+#pragma unroll
+  for (int e = 0; e < kE; ++e) f[e] = 0.0f;
+  if (in) {
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + b * a.qs[0] +
+                                                          head * a.qs[1] + i * a.qs[2]) + lane * (kE / 2);
+#pragma unroll
+    for (int e = 0; e < kE; e += 2) {
+      const uint32_t w = __ldg(q + e / 2);
+      f[e] = half_bits_to_f32<kF16>(w);
+      f[e + 1] = half_bits_to_f32<kF16>(w >> 16);
+    }
+  }
+  if constexpr (!kF16) {
+    float top = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) top = fmaxf(top, fabsf(f[e]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    dec_row_scale(top, up, down);
+  }
+  const long long bh = (long long)b * a.c.H + h;
+  uint32_t* out = p.q + (bh * p.row_groups + (r >> 4)) * (kD / 16) * 128;
+#pragma unroll
+  for (int e = 0; e < kE; e += 2) out[dec_q_word<kD>(r & 15, lane * kE + e)] = pack_f16x2(f[e] * up, f[e + 1] * up);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // L is written
+  if (lane == 0) {
+    const float lse = in ? a.lse[((long long)b * a.Hq + head) * a.n + i] : -INFINITY;
+    p.row[bh * p.row_groups * 16 + r] = make_float2(down, lse == -INFINITY ? INFINITY : lse * kLog2eF);
+  }
+}
+
+template <int kKind, int kD>
+__global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constant__ WeightParams p) {
+  const CacheAttnParams& a = p.a;
+  const CacheView& c = a.c;
+  constexpr int kK = kD / 16;  // k-steps
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int h = blockIdx.y, b = blockIdx.z, tok0 = (blockIdx.x * 4 + warp) * 32;
+  const DecSeq seq = dec_seq(a, b);
+  // the query rows that see one of these tokens
+  int i0 = 0, i1 = seq.nq - 1;
+  const int pos0 = seq.len - seq.nq;
+  if (a.causal) i0 = max(0, tok0 - pos0);
+  if (a.window > 0) i1 = (int)min((long long)i1, (long long)tok0 + 31 + a.window - 1 - pos0);
+  if (tok0 >= seq.len || i0 > i1) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // a grid ends no earlier than the one before it
+    return;
+  }
+  const int rg0 = i0 * a.group / 16, rg1 = (i1 * a.group + a.group - 1) / 16;
+
+  // keys: lane (g, t) holds the bytes of token 8j + g that it multiplies
+  uint32_t w[4][kK];
+  float ks[2];
+  bool here[2];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int tok = tok0 + 16 * half;
+    int blk = -1;
+    if (tok < seq.len) blk = checked_block(c, c.table, c.table_stride, b, tok >> c.page_log2);
+    here[half] = blk >= 0;
+    ks[half] = here[half] ? __ldg(c.k_scale + (long long)blk * c.H + h) : 0.0f;
+#pragma unroll
+    for (int j = 2 * half; j < 2 * half + 2; ++j) {
+      const uint8_t* k = c.k + blk * c.ks[0] + h * c.ks[1] + (((tok0 + 8 * j) & (c.page - 1)) + g) * c.ks[2];
+#pragma unroll
+      for (int u = 0; u < kK / 4; ++u) {  // 16-byte units: t of the row (D 64), 2t and 2t + 1 of each 128 bytes
+        const int at = kD == 64 ? 16 * t : 128 * (u / 2) + 32 * t + 16 * (u & 1);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (here[half]) v = __ldg(reinterpret_cast<const uint4*>(k + at));
+        w[j][4 * u] = v.x, w[j][4 * u + 1] = v.y, w[j][4 * u + 2] = v.z, w[j][4 * u + 3] = v.w;
+      }
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows are there
+  const long long bh = (long long)b * c.H + h;
+  const uint4* q = reinterpret_cast<const uint4*>(p.q) + bh * p.row_groups * kK * 32 + lane;
+  const float2* row = p.row + bh * p.row_groups * 16;
+  const bool raw = a.cap_out == 0.0f;
+  float sum[4][2] = {};
+#pragma unroll 1
+  for (int rg = rg0; rg <= rg1; ++rg) {
+    float sc[4][4] = {};
+#pragma unroll
+    for (int kk = 0; kk < kK; ++kk) {
+      const uint4 x = __ldcg(q + ((long long)rg * kK + kk) * 32);
+      const uint32_t qa[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t b0, b1;
+        to_f16x4<kKind>(w[j][kk], b0, b1);
+        mma_f16(sc[j], qa, b0, b1);
+      }
+    }
+    const float2 r0 = __ldcg(row + rg * 16 + g), r1 = __ldcg(row + rg * 16 + g + 8);
+    const int ia = (rg * 16 + g) / a.group, ib = (rg * 16 + g + 8) / a.group;
+    // tokens that rows g and g + 8 see (a row that is none has L2 = +inf)
+    const int2 va = dec_span(a, seq, ia, ia), vb = dec_span(a, seq, ib, ib);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 r = e < 2 ? r0 : r1;
+        const int2 v = e < 2 ? va : vb;
+        float s = sc[j][e] * (ks[j >> 1] * r.x);
+        s = raw ? s * a.scale_log2
+                : fmaf(-2.0f * a.cap_out, rcp_approx(ex2(s * a.cap_in * 2.8853900817779268f) + 1.0f), a.cap_out);
+        const int tok = tok0 + 8 * j + 2 * t + (e & 1);
+        if (tok >= v.x && tok < v.y) sum[j][e & 1] += ex2(s - r.y);
+      }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) sum[j][e] += __shfl_xor_sync(0xFFFFFFFFu, sum[j][e], o);
+    }
+  if (g == 0) {
+    float* out = a.weights + bh * a.W;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int tok = tok0 + 8 * j + 2 * t + e;
+        if (tok >= seq.len || !here[j >> 1]) continue;
+        if (tok >= a.W)
+          flag_bad_index(c);
+        else
+          out[tok] += sum[j][e];
+      }
+  }
+}
+
+}  // namespace fa
