@@ -1,5 +1,5 @@
 // Cache attention, head dim 64.
-#include "fa_cache_decode_launch.cuh"
+#include "fa_cache_attn_launch.cuh"
 
 namespace fa {
 int launch_cache_attn_d64(const CacheAttnParams& a, int kind, bool f16, const LaunchCtx& ctx) {

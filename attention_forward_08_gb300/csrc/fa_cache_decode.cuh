@@ -1,8 +1,7 @@
 // fa_cache_decode.cuh -- attention of few query rows over the 8-bit cache.
 //
-// Rows.  The R = n * group rows of a K/V head (row r: query row r / group,
-// head r % group of the group) share every key and value that is read; a
-// thread block takes up to 16 * kMT of them (a "row group").
+// The rows of a K/V head share every key and value that is read; a thread
+// block takes up to 16 * kMT of them at a time (fa_cache_line.cuh).
 //
 // Mathematics.  S = Q K^T and O += P V on the tensor cores (m16n8k16, f16 in,
 // fp32 out), with an online softmax in base 2.  Nothing is lost on the way to
@@ -18,12 +17,8 @@
 // Work.  A producer warp brings tiles of 32 tokens into a ring by TMA, with
 // their scales; the other warps take turns at the tiles, and each keeps a
 // running maximum, sum and output of its own in registers, so that no barrier
-// stands between two tiles.  The
-// tiles of all (sequence, head, row group) segments form one line that is cut
-// into equal parts, one for each thread block, wherever the cuts fall:
-// sequences of any lengths load the machine evenly, and nothing is planned on
-// the host.  A block that holds a whole segment writes the output; the parts
-// of a cut segment go to the workspace and a second, small kernel joins them.
+// stands between two tiles.  Tiles are shared out evenly over the machine
+// (fa_cache_line.cuh).
 //
 // Layout.  Neither product cares about the order of its summed index, nor
 // about the order of the columns it produces: lane (g, t) takes the bytes
@@ -35,16 +30,9 @@
 // Bound: memory; 2 * D bytes a token and K/V head, read once per row group.
 #pragma once
 
-#include <cuda.h>
-
-#include "fa_cache_ops.cuh"
-#include "fa_ptx.cuh"
+#include "fa_cache_line.cuh"
 
 namespace fa {
-
-constexpr float kDecLn2 = 0.6931471805599453f, kLog2eF = 1.4426950408889634f;
-constexpr float kDecLazy = 8.0f;  // the running maximum moves when it grows by more than 2^8: p stays below 2^8 in f16
-constexpr long long kDecDrainCycles = 1LL << 33;
 
 template <int kKind_, bool kF16_, int kD_, int kMT_>
 struct DecCfg {
@@ -89,136 +77,6 @@ struct DecMeta {
   int pad[2];
 };
 
-struct DecParams {
-  CacheAttnParams a;
-  int rows, row_groups;   // rows of a K/V head; groups of kRows
-  int max_ctas;
-  float* part_o;          // [2 * max_ctas, kRows, D]
-  float2* part_ml;        // [2 * max_ctas, kRows]: maximum, sum
-};
-
-// ------------------------------------------------------------------ the line of tiles
-
-struct DecSeq {
-  int len, nq;
-};
-__device__ __forceinline__ DecSeq dec_seq(const CacheAttnParams& a, int b) {
-  DecSeq s;
-  const long long most = (long long)a.c.M * a.c.page;
-  const int len = a.lens[b];
-  s.len = len < 0 ? 0 : (int)min((long long)len, most);
-  s.nq = a.n_q ? min(max(a.n_q[b], 0), a.n) : a.n;
-  return s;
-}
-
-// Tokens that query rows i0 .. i1 see: [lo, hi), empty as {0, 0}.
-__device__ __forceinline__ int2 dec_span(const CacheAttnParams& a, const DecSeq& s, int i0, int i1) {
-  i1 = min(i1, s.nq - 1);
-  if (i0 > i1) return make_int2(0, 0);
-  const int p0 = s.len - s.nq + i0, p1 = s.len - s.nq + i1;
-  const int hi = a.causal ? min(s.len, p1 + 1) : s.len;
-  const int lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
-  return lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
-}
-// ... and the query rows of row group rg.
-template <class C>
-__device__ __forceinline__ int2 dec_group_span(const DecParams& p, const DecSeq& s, int rg) {
-  if (p.row_groups == 1) return dec_span(p.a, s, 0, p.a.n - 1);
-  return dec_span(p.a, s, rg * C::kRows / p.a.group, (min(p.rows, (rg + 1) * C::kRows) - 1) / p.a.group);
-}
-
-// Tiles of one segment: at least one, so that empty rows are written too.
-template <class C>
-__device__ __forceinline__ int dec_tiles(const DecParams& p, const DecSeq& s, int rg) {
-  const int2 v = dec_group_span<C>(p, s, rg);
-  return max(1, (v.y + C::kTile - 1) / C::kTile - v.x / C::kTile);
-}
-// (A call, not inlined: kernels this short run once through most of their
-// instructions, and fetching code costs more than calling it.)
-template <class C>
-__device__ __noinline__ int dec_many_groups(const DecParams& p, DecSeq s, int groups) {
-  int n = 0;
-#pragma unroll 1
-  for (int rg = 0; rg < groups; ++rg) n += dec_tiles<C>(p, s, rg);
-  return n;
-}
-template <class C>
-__device__ __forceinline__ int dec_head_tiles(const DecParams& p, const DecSeq& s) {  // of all row groups
-  return p.row_groups == 1 ? dec_tiles<C>(p, s, 0) : dec_many_groups<C>(p, s, p.row_groups);
-}
-
-// The line's length, and where tile `part * nth` lies (part: tiles a thread
-// block, below): its sequence, and the tiles before that.  Every warp finds it
-// for itself, without a barrier; up to 32 sequences take one load.  (The host
-// keeps all counts below 2^31.)
-struct DecPlace {
-  int total, part, b, before;
-};
-template <class C>
-__device__ __forceinline__ int dec_part(const DecParams& p, int total);
-
-template <class C>
-__device__ __forceinline__ DecPlace dec_find(const DecParams& p, unsigned nth) {
-  const int lane = threadIdx.x & 31;
-  DecPlace at;
-  int mine = 0, all = 0;
-#pragma unroll 1
-  for (int i = lane; i < p.a.B; i += 32) {
-    mine = dec_head_tiles<C>(p, dec_seq(p.a, i)) * p.a.c.H;
-    all += mine;
-  }
-  at.total = __reduce_add_sync(0xFFFFFFFFu, all);
-  at.part = dec_part<C>(p, at.total);
-  at.b = at.before = 0;
-  const long long t = (long long)at.part * nth;
-  if (t >= at.total) return at;
-#pragma unroll 1
-  for (int base = 0;; base += 32) {
-    if (p.a.B > 32) mine = base + lane < p.a.B ? dec_head_tiles<C>(p, dec_seq(p.a, base + lane)) * p.a.c.H : 0;
-    int upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-      if (lane >= o) upto += u;
-    }
-    upto += at.before;
-    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, t < upto);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      at.before = __shfl_sync(0xFFFFFFFFu, upto - mine, l);
-      at.b = base + l;
-      return at;
-    }
-    at.before = __shfl_sync(0xFFFFFFFFu, upto, 31);
-  }
-}
-
-// The line's length, and the tiles before sequence b.
-template <class C>
-__device__ __forceinline__ DecPlace dec_before(const DecParams& p, int b) {
-  const int lane = threadIdx.x & 31;
-  int all = 0, lower = 0;
-#pragma unroll 1
-  for (int i = lane; i < p.a.B; i += 32) {
-    const int n = dec_head_tiles<C>(p, dec_seq(p.a, i)) * p.a.c.H;
-    all += n;
-    if (i < b) lower += n;
-  }
-  DecPlace at;
-  at.total = __reduce_add_sync(0xFFFFFFFFu, all);
-  at.part = dec_part<C>(p, at.total);
-  at.b = b;
-  at.before = __reduce_add_sync(0xFFFFFFFFu, lower);
-  return at;
-}
-
-// Tiles of one thread block's part of the line: an equal share of the grid's,
-// and no less than two tiles a warp.
-template <class C>
-__device__ __forceinline__ int dec_part(const DecParams& p, int total) {
-  return max(C::kMinTiles, (int)(((unsigned)total + p.max_ctas - 1) / (unsigned)p.max_ctas));
-}
-
 // ------------------------------------------------------------------ tensor-core pieces
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -227,25 +85,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Four stored bytes -> two f16x2 (bytes 0, 1 and bytes 2, 3), exact.  int8: a
-// byte u = x + 128 in the low mantissa bits of 1024 is the number 1024 + u.
-template <int kKind>
-__device__ __forceinline__ void to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if constexpr (kKind == kKindE4m3) {
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-  } else {
-    const uint32_t u = w ^ 0x80808080u;
-    const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
-    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-    __half2 ha = __hsub2(*reinterpret_cast<__half2*>(&a), off), hb = __hsub2(*reinterpret_cast<__half2*>(&b), off);
-    lo = *reinterpret_cast<uint32_t*>(&ha);
-    hi = *reinterpret_cast<uint32_t*>(&hb);
-  }
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -284,14 +123,6 @@ __device__ __forceinline__ void dec_key_words(uint32_t tile, int r, int t, uint3
   }
 }
 
-// A power of two that brings a query row whose largest entry is `top` into
-// [2^9, 2^10), kept inside the normal numbers, and its inverse.
-__device__ __forceinline__ void dec_row_scale(float top, float& up, float& down) {
-  const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -110), 127);
-  up = __uint_as_float((uint32_t)(9 - ex + 127) << 23);
-  down = __uint_as_float((uint32_t)(ex - 9 + 127) << 23);
-}
-
 // The 32-bit word, in the A operand [k-step, lane, 4] of 16 query rows, of
 // row r's elements d and d + 1 (d even).
 template <int kD>
@@ -314,19 +145,6 @@ __device__ __forceinline__ int dec_col(int i, int n) {
 template <class C>
 __device__ __forceinline__ float* dec_join_at(float* base, int r, int d) {
   return base + r * C::kD + (d & ~31) + ((((d >> 2) & 7) + 2 * (d >> 5) + r) & 7) * 4;
-}
-
-// Four columns of one output row, and its L.
-template <class C>
-__device__ __forceinline__ void dec_write(const CacheAttnParams& a, int b, int h, int row, int d, const float4& x,
-                                          float top, float sum) {
-  const int i = row / a.group, head = h * a.group + row % a.group;
-  const float inv = sum > 0.0f ? rcp_approx(sum) : 0.0f;
-  uint2 y;
-  y.x = C::kF16 ? pack_f16x2(x.x * inv, x.y * inv) : pack_bf16x2(x.x * inv, x.y * inv);
-  y.y = C::kF16 ? pack_f16x2(x.z * inv, x.w * inv) : pack_bf16x2(x.z * inv, x.w * inv);
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + b * a.os[0] + head * a.os[1] + i * a.os[2] + d) = y;
-  if (d == 0) a.lse[((long long)b * a.Hq + head) * a.n + i] = sum > 0.0f ? (top + lg2(sum)) * kDecLn2 : -INFINITY;
 }
 
 // A bounded wait by a whole warp; false once it ran out (or another did).
@@ -378,39 +196,24 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // This block's part of the line, and where it begins.
-  const DecPlace place = dec_find<C>(p, blockIdx.x);
-  if ((long long)place.part * blockIdx.x >= place.total) return;
-  const int t0 = place.part * (int)blockIdx.x, t1 = (int)min((long long)place.total, (long long)t0 + place.part);
-  int b = place.b;
-  DecSeq seq = dec_seq(a, b);
-  if (tid == 0 && place.before >= t0) (void)checked_len(c, a.lens[b]);  // one block a sequence tells about its length
-  int seg0 = place.before;  // first tile of the current segment
-  int h = 0, rg = 0;
-  {  // the segment of t0
-    const int per_head = dec_head_tiles<C>(p, seq);
-    h = (int)((unsigned)(t0 - seg0) / (unsigned)per_head);
-    seg0 += h * per_head;
-    if (p.row_groups > 1) {
-      int tiles;
-#pragma unroll 1
-      while (seg0 + (tiles = dec_many_groups<C>(p, seq, rg + 1) - dec_many_groups<C>(p, seq, rg)) <= t0) {
-        seg0 += tiles;
-        ++rg;
-      }
-    }
-  }
+  DecPlace at;
+  if (!dec_find<C>(p, blockIdx.x, at)) return;
+  const int t0 = at.part * (int)blockIdx.x, t1 = (int)min((long long)at.total, (long long)t0 + at.part);
   __syncthreads();  // the barriers are ready
   const int sub = min(c.page, C::kTile), sub_log2 = min(c.page_log2, 5);  // a block's part of a tile
   const int subs = C::kTile >> sub_log2;                                  // parts a tile: 1 or 2
   int tile0 = 0;  // tiles of this block's earlier pieces: tile k of all uses stage k % kS
 
 #pragma unroll 1
-  for (int at = t0; at < t1;) {
-    const int r0 = rg * C::kRows, r1 = min(p.rows, r0 + C::kRows);
-    const int tiles = dec_tiles<C>(p, seq, rg);
-    const int2 span = dec_group_span<C>(p, seq, rg);
-    const int first_tile = span.x / C::kTile + at - seg0;
-    const int n_tiles = min(t1, seg0 + tiles) - at;
+  for (int pos = t0; pos < t1;) {
+    const int b = at.b, h = at.h, r0 = at.rg * C::kRows, r1 = min(p.rows, r0 + C::kRows);
+    const DecSeq seq = at.seq;
+    // the first tile of a sequence tells about its length
+    if (tid == 0 && h == 0 && at.rg == 0 && pos == at.seg0) (void)checked_len(c, a.lens[b]);
+    const int tiles = dec_tiles<C>(p, seq, at.rg);
+    const int2 span = dec_group_span<C>(p, seq, at.rg);
+    const int first_tile = span.x / C::kTile + pos - at.seg0;
+    const int n_tiles = min(t1, at.seg0 + tiles) - pos;
     const bool whole = n_tiles == tiles;
 
     if (warp == kW) {
@@ -791,7 +594,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           }
         }
       named_bar_sync(1, 32 * kW);
-      const int slot = 2 * blockIdx.x + (at > seg0 ? 0 : 1);
+      const int slot = 2 * blockIdx.x + (pos > at.seg0 ? 0 : 1);
 #pragma unroll 1
       for (int v = tid; v < (r1 - r0) * (C::kD / 4); v += 32 * kW) {
         const int r = v / (C::kD / 4), d = (v % (C::kD / 4)) * 4;
@@ -816,53 +619,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     }
     __syncthreads();  // the ring's memory and the maxima are free again
     tile0 += n_tiles;
-    at = min(t1, seg0 + tiles);
-    seg0 += tiles;
-    if (++rg == p.row_groups) {
-      rg = 0;
-      if (++h == c.H) {
-        h = 0;
-        if (++b < a.B) {
-          seq = dec_seq(a, b);
-          if (tid == 0) (void)checked_len(c, a.lens[b]);
-        }
-      }
-    }
+    pos += n_tiles;
+    dec_next(p, at, tiles);
   }
-}
-
-// Joins the parts of segments that lie in more than one thread block.  One
-// block per (row group and piece of its rows, head, sequence); a thread sums
-// four columns of a row over the parts.
-template <class C>
-__global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__ DecParams p) {
-  const CacheAttnParams& a = p.a;
-  constexpr int kRowsHere = 512 / C::kD;  // rows a block
-  const int rg = blockIdx.x / (C::kRows / kRowsHere), piece = blockIdx.x % (C::kRows / kRowsHere);
-  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const DecPlace place = dec_before<C>(p, b);
-  const DecSeq seq = dec_seq(a, b);
-  const int u0 = place.before + h * dec_head_tiles<C>(p, seq) + (rg > 0 ? dec_many_groups<C>(p, seq, rg) : 0);
-  const int u1 = u0 + dec_tiles<C>(p, seq, rg);
-  const int c0 = u0 / place.part, c1 = (u1 - 1) / place.part;
-  const int r = piece * kRowsHere + tid / (C::kD / 4), row = rg * C::kRows + r, d = tid % (C::kD / 4) * 4;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
-  if (c0 == c1 || row >= p.rows) return;
-  float top = -INFINITY, sum = 0.0f;
-  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-  for (int i = c0; i <= c1; ++i) {
-    const long long slot = (long long)(2 * i + (i == c0)) * C::kRows + r;
-    const float2 ml = __ldcg(p.part_ml + slot);
-    const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part_o + slot * C::kD + d));
-    const float m2 = fmaxf(top, ml.x), z = m2 == -INFINITY ? 0.0f : m2;
-    const float f = ex2(top - z), g = ex2(ml.x - z);
-    top = m2;
-    sum = fmaf(sum, f, ml.y * g);
-    x.x = fmaf(x.x, f, y.x * g), x.y = fmaf(x.y, f, y.y * g), x.z = fmaf(x.z, f, y.z * g), x.w = fmaf(x.w, f, y.w * g);
-  }
-  dec_write<C>(a, b, h, row, d, x, top, sum);
 }
 
 }  // namespace fa

@@ -19,6 +19,25 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
   return r;
 }
 
+// Four stored bytes -> two f16x2 (bytes 0, 1 and bytes 2, 3), exact.  int8: a
+// byte u = x + 128 in the low mantissa bits of 1024 is the number 1024 + u.
+template <int kKind>
+__device__ __forceinline__ void to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (kKind == kKindE4m3) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  } else {
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    __half2 ha = __hsub2(*reinterpret_cast<__half2*>(&a), off), hb = __hsub2(*reinterpret_cast<__half2*>(&b), off);
+    lo = *reinterpret_cast<uint32_t*>(&ha);
+    hi = *reinterpret_cast<uint32_t*>(&hb);
+  }
+}
+
 // Round to the stored type, to nearest even.  e4m3 saturates infinities and
 // keeps NaN; int8 clamps to +-127 and stores NaN as 0.
 template <int kKind>

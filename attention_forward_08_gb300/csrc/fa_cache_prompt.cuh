@@ -1,0 +1,564 @@
+// fa_cache_prompt.cuh -- attention of many query rows over the 8-bit cache.
+//
+// The same operation as fa_cache_decode.cuh, for rows enough to fill the
+// tensor core's 128-row tiles (a piece of a prompt, or many drafts): tcgen05
+// MMAs with accumulators in tensor memory, two row tiles a thread block taking
+// turns at the tensor core (one where D = 256).
+//
+// Mathematics.  All products in f16 with fp32 accumulation: a stored value is
+// an f16 number, a bf16 query row is scaled by a power of two.  With k_scale
+// and v_scale constant over 16 tokens (ks, vs), row i's weights are kept as
+//
+//   P'_ij = 2^(s_ij + log2 vs_j - m_i),   O = sum_j P'_ij v8_j / l_i,   l_i = sum_j P'_ij / vs_j
+//
+// with m_i the running maximum of s + log2 vs: one FMA and one exponential a
+// score, the scales cost an operation per 16 scores, and what counts most in O
+// always has P' near 1, whatever the scales of other blocks.  P' is rounded to
+// f16 (2^-11), the sums are not.
+//
+// Roles.  Warps 0 and 1 issue MMAs, one per row tile (strict turns: PV0 S0 PV1
+// S1, as in fa_kernel.cuh); the converter warps load stored bytes straight
+// from global memory into registers, one block of 128 keys ahead, widen them
+// to f16 and write them in the tensor core's 128-byte-swizzled layout; one
+// softmax warpgroup per row tile owns a row a thread, loads and scales its
+// query row itself, and writes its output.
+//
+// Bound: the tensor cores; the widened K and V tiles are written once for 256
+// rows (64 KB of shared-memory writes beside 192 KB of operand reads a block).
+#pragma once
+
+#include "fa_cache_line.cuh"
+
+namespace fa {
+
+template <int kKind_, bool kF16_, int kD_>
+struct PromptCfg {
+  static constexpr int kKind = kKind_;
+  static constexpr bool kF16 = kF16_;
+  static constexpr int kD = kD_;
+  static constexpr int kTiles = kD <= 128 ? 2 : 1;   // 128-row tiles a block
+  static constexpr int kRows = 128 * kTiles;
+  static constexpr int kTile = 128;                  // keys a block of the line
+  static constexpr int kMinTiles = 4;
+  static constexpr int kStages = kD == 64 ? 3 : kD == 128 ? 2 : 1;  // of K; of V alike
+  static constexpr int kIssuers = kTiles;
+  static constexpr int kConvWarps = kTiles == 2 ? 4 : 8;
+  static constexpr int kThreads = 128 + 32 * kConvWarps + 128 * kTiles;  // 512
+  static constexpr int kQBytes = 128 * kD * 2;       // one row tile
+  static constexpr int kKvBytes = 128 * kD * 2;
+  static constexpr int kOffK = kTiles * kQBytes, kOffV = kOffK + kStages * kKvBytes;
+  static constexpr int kOffMeta = kOffV + kStages * kKvBytes, kOffCtl = kOffMeta + 4 * 8 * 16;
+  static constexpr int kSmem = 1024 + kOffCtl + 512;
+  static constexpr int kColO = 256;                  // S: two buffers of 128 columns; P over S
+  // Registers: 512 threads x 128 at launch; control and converters give theirs
+  // to the softmax warps (128 * 40 + 128 * 72 + 256 * 200 = 512 * 128 with two
+  // tiles, 128 * 40 + 256 * 128 + 128 * 208 <= 512 * 128 with one).
+  static constexpr int kRegsCtrl = 40, kRegsConv = kTiles == 2 ? 72 : 128, kRegsSoft = kTiles == 2 ? 200 : 208;
+  static_assert(128 * kRegsCtrl + 32 * kConvWarps * kRegsConv + 128 * kTiles * kRegsSoft <= 512 * 128,
+                "register split exceeds the launch allocation");
+  static_assert(kThreads == 512 && kSmem <= 232448, "thread block shape");
+};
+
+struct PromptCtl {
+  uint64_t q_full[2];              // 4 softmax warps: query tile written
+  uint64_t k_full[3], k_empty[3];  // converters / MMAs (one arrival an issuer)
+  uint64_t v_full[3], v_empty[3];
+  uint64_t s_full[2];              // S computed (two tiles: of tile t; one tile: in buffer j & 1)
+  uint64_t p_ready[2];             // softmax wrote P (and rescaled O)
+  uint64_t o_ready[2];             // two tiles: a piece's last PV done; one tile: each PV done
+  uint64_t turn[2];
+  uint64_t drain[2];
+  uint32_t tmem;
+  int abort;
+};
+
+__device__ __forceinline__ bool prompt_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                            const CacheAttnParams& a) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long begin = clock64_now();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort) return false;
+    if (clock64_now() - begin > a.timeout_cycles) {
+      *abort = 1;
+      atomicOr(a.c.status, kStatusTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool prompt_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                                 const CacheAttnParams& a) {
+  return __all_sync(0xFFFFFFFFu, prompt_wait(bar, parity, abort, a));
+}
+
+// 16 stored bytes -> 16 f16.
+template <int kKind>
+__device__ __forceinline__ void widen16(const uint4& w, uint4& lo, uint4& hi) {
+  to_f16x4<kKind>(w.x, lo.x, lo.y);
+  to_f16x4<kKind>(w.y, lo.z, lo.w);
+  to_f16x4<kKind>(w.z, hi.x, hi.y);
+  to_f16x4<kKind>(w.w, hi.z, hi.w);
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __grid_constant__ DecParams p) {
+  const CacheAttnParams& a = p.a;
+  const CacheView& c = a.c;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  float4* s_meta = reinterpret_cast<float4*>(smem + C::kOffMeta);  // [block % 4][16 tokens]: ks, log2 vs, 1 / vs, there
+  PromptCtl* ctl = reinterpret_cast<PromptCtl*>(smem + C::kOffCtl);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  DecPlace at;
+  if (!dec_find<C>(p, blockIdx.x, at)) return;  // the whole block: nothing is set up yet
+  const int t0 = at.part * (int)blockIdx.x, t1 = (int)min((long long)at.total, (long long)t0 + at.part);
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->q_full[i], 4);
+      mbar_init(&ctl->s_full[i], 1);
+      mbar_init(&ctl->p_ready[i], 4);
+      mbar_init(&ctl->o_ready[i], 1);
+      mbar_init(&ctl->turn[i], 1);
+      mbar_init(&ctl->drain[i], 1);
+    }
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&ctl->k_full[i], C::kConvWarps);
+      mbar_init(&ctl->v_full[i], C::kConvWarps);
+      mbar_init(&ctl->k_empty[i], C::kIssuers);
+      mbar_init(&ctl->v_empty[i], C::kIssuers);
+    }
+    ctl->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl->tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+  volatile int* abort = &ctl->abort;
+
+  if (warp < 4) {
+    // ============================================================ control
+    regs_dec<C::kRegsCtrl>();
+    if (warp < C::kIssuers) {
+      const int t = warp;  // row tile
+      constexpr uint32_t idS = make_idesc_fmt(kFmtF16, 128, 128, false, false);
+      constexpr uint32_t idPV = make_idesc_fmt(kFmtF16, 128, C::kD, false, true);
+      const uint64_t dQ = make_sdesc_sw128(smem_u32(smem + t * C::kQBytes), 16, 1024);
+      const uint64_t dK = make_sdesc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
+      const uint64_t dV = make_sdesc_sw128(smem_u32(smem + C::kOffV), 128 * 128, 1024);
+      const uint32_t q_lo = (uint32_t)dQ, q_hi = (uint32_t)(dQ >> 32), k_lo = (uint32_t)dK, k_hi = (uint32_t)(dK >> 32),
+                     v_lo = (uint32_t)dV, v_hi = (uint32_t)(dV >> 32);
+      auto issue_S = [&](int buf, int stage) {
+        const uint32_t ka = k_lo + ((stage * C::kKvBytes) >> 4), dst = tmem + buf * 128;
+        mma_ss_lh<false, 0>(dst, q_lo, q_hi, ka, k_hi, idS, 0u);
+#pragma unroll
+        for (int kk = 1; kk < C::kD / 16; ++kk) {
+          const uint32_t off = (kk / 4) * ((128 * 128) >> 4) + (kk % 4) * 2;
+          mma_ss_lh<false, 1>(dst, q_lo + off, q_hi, ka + off, k_hi, idS, 1u);
+        }
+      };
+      auto issue_PV = [&](int buf, int stage, bool first) {
+        const uint32_t va = v_lo + ((stage * C::kKvBytes) >> 4), src = tmem + buf * 128;
+        const uint32_t dst = tmem + C::kColO + (C::kTiles == 2 ? t * C::kD : 0);
+        mma_ts_lh<false, 0>(dst, src, va, v_hi, idPV, first ? 0u : 1u);
+#pragma unroll
+        for (int kk = 1; kk < 8; ++kk) mma_ts_lh<false, 1>(dst, src + kk * 8, va + ((kk * 16 * 128) >> 4), v_hi, idPV, 1u);
+      };
+      int groups = 0;
+      auto wait_turn = [&]() -> bool {
+        if (C::kIssuers == 1 || (t == 0 && groups == 0)) return true;
+        return prompt_wait(&ctl->turn[t], (t == 0 ? groups - 1 : groups) & 1, abort, a);
+      };
+      auto pass_turn = [&]() {
+        if (C::kIssuers == 2) {
+          mbar_arrive(&ctl->turn[1 - t]);
+          ++groups;
+        }
+      };
+      int blocks = 0, pieces = 0;  // blocks and pieces before this one
+      bool ok = true;
+#pragma unroll 1
+      for (int pos = t0; pos < t1 && ok; ++pieces) {
+        const int tiles = dec_tiles<C>(p, at.seq, at.rg), n = min(t1, at.seg0 + tiles) - pos;
+        if (lane == 0) {
+          auto k_at = [&](int j) { return (blocks + j) % C::kStages; };
+          auto par = [&](int j) { return (uint32_t)((blocks + j) / C::kStages) & 1u; };
+          ok = prompt_wait(&ctl->q_full[t], pieces & 1, abort, a) && prompt_wait(&ctl->k_full[k_at(0)], par(0), abort, a) &&
+               wait_turn();
+          if (ok) {
+            tc_fence_after();
+            // buffers: two tiles: tile t's; one: alternating over all blocks
+            auto buf = [&](int j) { return C::kTiles == 2 ? t : (blocks + j) & 1; };
+            issue_S(buf(0), k_at(0));
+            mma_commit(&ctl->s_full[buf(0)]);
+            pass_turn();
+            mma_commit(&ctl->k_empty[k_at(0)]);
+#pragma unroll 1
+            for (int j = 0; j < n && ok; ++j) {
+              if constexpr (C::kTiles == 1) {  // the next S goes before this PV
+                if (j + 1 < n) {
+                  ok = prompt_wait(&ctl->k_full[k_at(j + 1)], par(j + 1), abort, a);
+                  if (!ok) break;
+                  tc_fence_after();
+                  issue_S(buf(j + 1), k_at(j + 1));
+                  mma_commit(&ctl->s_full[buf(j + 1)]);
+                  mma_commit(&ctl->k_empty[k_at(j + 1)]);
+                }
+              }
+              ok = prompt_wait(&ctl->v_full[k_at(j)], par(j), abort, a) &&
+                   prompt_wait(&ctl->p_ready[t], (uint32_t)(blocks + j) & 1u, abort, a);
+              if (ok && C::kTiles == 2 && j + 1 < n) ok = prompt_wait(&ctl->k_full[k_at(j + 1)], par(j + 1), abort, a);
+              if (ok) ok = wait_turn();
+              if (!ok) break;
+              tc_fence_after();
+              issue_PV(buf(j), k_at(j), j == 0);
+              if (C::kTiles == 1 || j + 1 == n) mma_commit(&ctl->o_ready[t]);
+              if constexpr (C::kTiles == 2) {
+                if (j + 1 < n) {
+                  issue_S(t, k_at(j + 1));
+                  mma_commit(&ctl->s_full[t]);
+                }
+              }
+              pass_turn();
+              mma_commit(&ctl->v_empty[k_at(j)]);
+              if (C::kTiles == 2 && j + 1 < n) mma_commit(&ctl->k_empty[k_at(j + 1)]);
+            }
+          }
+        }
+        ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+        blocks += n;
+        pos += n;
+        dec_next(p, at, tiles);
+      }
+      // Every MMA issued here has completed before the block lets go of its
+      // memory (after an expired wait too; bounded).
+      if (lane == 0) {
+        mma_commit(&ctl->drain[t]);
+        const long long begin = clock64_now();
+        while (!mbar_try_wait(&ctl->drain[t], 0) && clock64_now() - begin < kDecDrainCycles) {
+        }
+      }
+      __syncwarp();
+    }
+  } else if (warp < 4 + C::kConvWarps) {
+    // ============================================================ converters
+    if constexpr (C::kRegsConv < 128) regs_dec<C::kRegsConv>();
+    const int cw = warp - 4;
+    constexpr int kUnits = C::kD / 16;                  // 16-byte units a key
+    constexpr int kPer = 128 * kUnits / (32 * C::kConvWarps);  // units a thread and tile: 4 (D = 64) or 8
+    // Lane bits 0-1: unit, 2: key, then units, then keys: eight neighbours
+    // write eight different 16-byte columns of the swizzled rows.
+    constexpr int kHigh = kUnits / 4;                   // 1, 2 or 4
+    const int unit = (lane & 3) + 4 * ((lane >> 3) % kHigh);
+    const int key_in = ((lane >> 2) & 1) + 2 * ((lane >> 3) / kHigh);  // of the warp's keys
+    constexpr int kKeysWarp = 32 / kUnits;              // keys a warp takes at once: 8, 4, 2
+    constexpr int kKeysStep = kKeysWarp * C::kConvWarps;  // 32 (D = 64) or 16
+    const int key0 = cw * kKeysWarp + key_in;
+    const uint32_t col = (uint32_t)(unit / 4) * (128 * 128);
+    int blocks = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int pos = t0; pos < t1 && ok;) {
+      if (cw == 0 && lane == 0 && at.h == 0 && at.rg == 0 && pos == at.seg0) (void)checked_len(c, a.lens[at.b]);
+      const int tiles = dec_tiles<C>(p, at.seq, at.rg), n = min(t1, at.seg0 + tiles) - pos;
+      const int2 span = dec_group_span<C>(p, at.seq, at.rg);
+      const int first = span.x / 128 + pos - at.seg0;
+      const int b = at.b, h = at.h;
+      // lane g (of 8) looks up tokens 16g .. of a block: its cache block and scales
+      int blk = -1;
+      float ks = 0.0f, vs = 0.0f;
+      auto look_up = [&](int j) {
+        const int tok = (first + j) * 128 + 16 * (lane & 7);
+        blk = -1;
+        ks = vs = 0.0f;
+        if (j < n && tok < span.y && tok + 16 > span.x)
+          blk = checked_block(c, c.table, c.table_stride, b, tok >> c.page_log2);
+        if (blk >= 0) {
+          ks = __ldg(c.k_scale + (long long)blk * c.H + h);
+          vs = __ldg(c.v_scale + (long long)blk * c.H + h);
+        }
+      };
+      uint4 xk[kPer], xv[kPer];
+      // Keys (or values) of block j: zero where nobody sees them or nothing is stored.
+      auto load = [&](uint4(&x)[kPer], int j, const uint8_t* pool, const long long* st, bool values) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int key = key0 + i * kKeysStep, tok = (first + j) * 128 + key;
+          const int at_blk = __shfl_sync(0xFFFFFFFFu, blk, key >> 4);
+          const float v = __shfl_sync(0xFFFFFFFFu, vs, key >> 4);
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (at_blk >= 0 && tok >= span.x && tok < span.y && (!values || v > 0.0f))
+            x[i] = __ldg(reinterpret_cast<const uint4*>(pool + at_blk * st[0] + h * st[1] + (tok & (c.page - 1)) * st[2] + unit * 16));
+        }
+      };
+      auto store = [&](const uint4(&x)[kPer], uint8_t* tile) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int key = key0 + i * kKeysStep;
+          uint4 lo, hi;
+          widen16<C::kKind>(x[i], lo, hi);
+          uint8_t* row = tile + col + key * 128;
+          const int u = (unit % 4) * 2;
+          *reinterpret_cast<uint4*>(row + ((u ^ (key & 7)) << 4)) = lo;
+          *reinterpret_cast<uint4*>(row + (((u + 1) ^ (key & 7)) << 4)) = hi;
+        }
+      };
+      look_up(0);
+      load(xk, 0, c.k, c.ks, false);
+      load(xv, 0, c.v, c.vs, true);
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        const int stage = (blocks + j) % C::kStages;
+        const uint32_t use = (uint32_t)((blocks + j) / C::kStages);
+        if (use > 0 && !(ok = prompt_warp_wait(&ctl->k_empty[stage], (use - 1) & 1, abort, a))) break;
+        if (cw == 0 && lane < 8)
+          s_meta[((blocks + j) & 3) * 8 + lane] =
+              make_float4(ks, vs > 0.0f ? log2f(vs) : 0.0f, vs > 0.0f ? 1.0f / vs : 1.0f, blk >= 0 ? 1.0f : 0.0f);
+        store(xk, smem + C::kOffK + stage * C::kKvBytes);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->k_full[stage]);
+        look_up(j + 1);
+        load(xk, j + 1, c.k, c.ks, false);
+        if (use > 0 && !(ok = prompt_warp_wait(&ctl->v_empty[stage], (use - 1) & 1, abort, a))) break;
+        store(xv, smem + C::kOffV + stage * C::kKvBytes);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->v_full[stage]);
+        load(xv, j + 1, c.v, c.vs, true);
+      }
+      blocks += n;
+      pos += n;
+      dec_next(p, at, tiles);
+    }
+  } else {
+    // ============================================================ softmax
+    regs_inc<C::kRegsSoft>();
+    const int t = C::kTiles == 2 ? (warp - 8) >> 2 : 0;
+    const int tl = tid - (512 - 128 * C::kTiles) - 128 * t;  // row of the tile = TMEM lane
+    const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tO = tmem + lane_addr + C::kColO + (C::kTiles == 2 ? t * C::kD : 0);
+    uint8_t* q_tile = smem + t * C::kQBytes;
+    const bool raw = a.cap_out == 0.0f && a.scale_log2 > 0.0f;
+    int blocks = 0, pieces = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int pos = t0; pos < t1 && ok; ++pieces) {
+      const int tiles = dec_tiles<C>(p, at.seq, at.rg), n = min(t1, at.seg0 + tiles) - pos;
+      const int2 span = dec_group_span<C>(p, at.seq, at.rg);
+      const int first = span.x / 128 + pos - at.seg0;
+      const bool whole = n == tiles, head_cut = pos > at.seg0;
+      const int row = at.rg * C::kRows + t * 128 + tl, i = row / a.group, head = at.h * a.group + row % a.group;
+      const bool real = row < p.rows;
+      const int2 see = real ? dec_span(a, at.seq, i, i) : make_int2(0, 0);
+      // The query row, twice over: its largest entry, then its f16 form.  (S of
+      // the piece before is done: the tile may be written.)
+      float rs = 1.0f;
+      {
+        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at.b * a.qs[0] +
+                                                        head * a.qs[1] + i * a.qs[2]);
+        const bool in = see.x < see.y;
+        float up = 1.0f;
+        if constexpr (!C::kF16) {
+          float top = 0.0f;
+          if (in) {
+#pragma unroll 4
+            for (int u = 0; u < C::kD / 8; ++u) {
+              const uint4 w = __ldg(q + u);
+              const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                top = fmax3(top, fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xFFFF0000u)));
+            }
+          }
+          dec_row_scale(top, up, rs);
+        }
+#pragma unroll 4
+        for (int u = 0; u < C::kD / 8; ++u) {
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (in) w = __ldg(q + u);
+          if constexpr (!C::kF16) {
+            uint32_t* x = &w.x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[e] = pack_f16x2(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xFFFF0000u) * up);
+          }
+          *reinterpret_cast<uint4*>(q_tile + (u / 8) * (128 * 128) + tl * 128 + (((u % 8) ^ (tl & 7)) << 4)) = w;
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->q_full[t]);
+
+      const float f_row = rs * a.scale_log2;
+      float m = -INFINITY, l = 0.0f;
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        const int nth = blocks + j, buf = C::kTiles == 2 ? t : nth & 1;
+        const uint32_t s_par = (uint32_t)(C::kTiles == 2 ? nth : nth >> 1) & 1u;
+        ok = prompt_warp_wait(&ctl->s_full[buf], s_par, abort, a);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t tS = tmem + lane_addr + buf * 128;
+        float s[128];
+        {
+          uint32_t rr[128];
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) tmem_ld32(tS + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&rr[cc * 32]));
+          tmem_wait_ld();
+          reg_fence(rr);
+#pragma unroll
+          for (int k = 0; k < 128; ++k) s[k] = __uint_as_float(rr[k]);
+        }
+        const float4* meta = s_meta + (nth & 3) * 8;
+        const int key0 = (first + j) * 128, lo = see.x - key0, hi = see.y - key0;
+        if (!raw) {  // scores to base 2 first
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            const float ks = meta[g].x * rs;
+            if (a.cap_out > 0.0f) {
+              const float ci = ks * a.cap_in * 2.8853900817779268f;
+#pragma unroll
+              for (int k = 16 * g; k < 16 * g + 16; ++k)
+                s[k] = fmaf(-2.0f * a.cap_out, rcp_approx(ex2(s[k] * ci) + 1.0f), a.cap_out);
+            } else {
+#pragma unroll
+              for (int k = 16 * g; k < 16 * g + 16; ++k) s[k] *= ks * a.scale_log2;
+            }
+          }
+        }
+        if (lo > 0 || hi < 128) {
+#pragma unroll
+          for (int k = 0; k < 128; ++k)
+            if (k < lo || k >= hi) s[k] = -INFINITY;
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          const float4 q = meta[g];
+          const float* x = s + 16 * g;
+          float v = fmax3(fmax3(x[0], x[1], x[2]), x[3], x[4]), w = fmax3(fmax3(x[5], x[6], x[7]), x[8], x[9]);
+          v = fmax3(v, x[10], x[11]);
+          w = fmax3(w, x[12], x[13]);
+          v = fmax3(fmaxf(v, w), x[14], x[15]);
+          if (q.w == 0.0f) v = -INFINITY;  // nothing stored there
+          mx = fmaxf(mx, fmaf(v, raw ? fmaxf(q.x * f_row, 1e-37f) : 1.0f, q.y));
+        }
+        float corr = 1.0f;
+        const bool resc = mx > m + kDecLazy;
+        if (resc) {
+          corr = ex2(m - mx);  // 0 when m = -inf
+          m = mx;
+          l *= corr;
+        }
+        const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int gg = 0; gg < 2; ++gg) {
+            const float4 q = meta[2 * cc + gg];
+            const float f = raw ? fmaxf(q.x * f_row, 1e-37f) : 1.0f, off = q.w == 0.0f ? -INFINITY : q.y - base;
+            float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int k = 32 * cc + 16 * gg + 2 * e;
+              float x0, x1;
+              ffma2(x0, x1, s[k], s[k + 1], f, f, off, off);
+              x0 = ex2(x0), x1 = ex2(x1);
+              fadd2(sum[0], sum[1], x0, x1);
+              pk[8 * gg + e] = pack_f16x2(x0, x1);
+            }
+            l = fmaf(sum[0] + sum[1], q.z, l);
+          }
+          tmem_st16(tS + cc * 16, pk);
+        }
+        if constexpr (C::kTiles == 1) {  // PV of the block before has landed (each phase is consumed, in order)
+          if (nth > 0) {
+            ok = prompt_warp_wait(&ctl->o_ready[0], (uint32_t)(nth - 1) & 1u, abort, a);
+            if (!ok) break;
+          }
+        }
+        if (j > 0 && __any_sync(0xFFFFFFFFu, resc)) {
+          tc_fence_after();
+#pragma unroll
+          for (int cc = 0; cc < C::kD / 32; ++cc) {
+            uint32_t rr[32];
+            tmem_ld32(tO + cc * 32, rr);
+            tmem_wait_ld();
+            reg_fence(rr);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float o0, o1;
+              fmul2(o0, o1, __uint_as_float(rr[e]), __uint_as_float(rr[e + 1]), corr, corr);
+              rr[e] = __float_as_uint(o0);
+              rr[e + 1] = __float_as_uint(o1);
+            }
+            tmem_st32(tO + cc * 32, rr);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->p_ready[t]);
+      }
+      if (!ok) break;
+      blocks += n;
+      if constexpr (C::kTiles == 2)
+        ok = prompt_warp_wait(&ctl->o_ready[t], pieces & 1, abort, a);
+      else
+        ok = prompt_warp_wait(&ctl->o_ready[0], (uint32_t)(blocks - 1) & 1u, abort, a);
+      if (!ok) break;
+      tc_fence_after();
+      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      const long long slot = (long long)(2 * blockIdx.x + (head_cut ? 0 : 1)) * C::kRows + t * 128 + tl;
+      uint8_t* dst = static_cast<uint8_t*>(a.o) + (at.b * a.os[0] + head * a.os[1] + i * a.os[2]) * 2;
+#pragma unroll 1
+      for (int cc = 0; cc < C::kD / 32; ++cc) {
+        uint32_t rr[32];
+        tmem_ld32(tO + cc * 32, rr);
+        tmem_wait_ld();
+        reg_fence(rr);
+        if (real && whole) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float o0 = __uint_as_float(rr[8 * u + 2 * e]) * inv, o1 = __uint_as_float(rr[8 * u + 2 * e + 1]) * inv;
+              y[e] = C::kF16 ? pack_f16x2(o0, o1) : pack_bf16x2(o0, o1);
+            }
+            *reinterpret_cast<uint4*>(dst + cc * 64 + u * 16) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        } else if (real) {
+          uint4* part = reinterpret_cast<uint4*>(p.part_o + slot * C::kD + cc * 32);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) part[u] = make_uint4(rr[4 * u], rr[4 * u + 1], rr[4 * u + 2], rr[4 * u + 3]);
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      if (real) {
+        if (whole)
+          a.lse[((long long)at.b * a.Hq + head) * a.n + i] = l > 0.0f ? (m + lg2(l)) * kDecLn2 : -INFINITY;
+        else
+          p.part_ml[slot] = make_float2(m, l);
+      }
+      pos += n;
+      dec_next(p, at, tiles);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace fa

@@ -37,14 +37,11 @@ def synced(fa):
     assert fa.fa_sync_status(None) == 0, fa.fa_last_error()
 
 
-def check_attention(fa, ref, q, table, lens, got, got_w=None, w0=None, n_q=None, p_half=None, **kw):
-    """O: half a step of the output, and of the weights' 16-bit form (p_half) times sum of p |v|; L: fp32 sums of D
+def check_attention(fa, ref, q, table, lens, got, got_w=None, w0=None, n_q=None, **kw):
+    """O: half a step of the output, and of the weights' f16 form times sum of p |v|; L: fp32 sums of D
     products, D steps of 2^-24 of the largest sum of |q k| at worst, taken as 2^-18 of it."""
     o, lse = (t.double().cpu().numpy() for t in got)
     ro, rl, rw, a, sabs = R.attention(ref, q, table, lens, n_q=n_q, **kw)
-    G = q.shape[1] // ref.pool["k"].shape[1]
-    if p_half is None:
-        p_half = HALF[F16] if q.shape[2] * G <= 32 else HALF[BF16]
     tol_l = (2.0 ** -18 * sabs + 1e-6)[:, None, None]
     empty = np.isneginf(rl)
     np.testing.assert_array_equal(np.isneginf(lse), empty)
@@ -52,7 +49,7 @@ def check_attention(fa, ref, q, table, lens, got, got_w=None, w0=None, n_q=None,
     assert np.all(np.isfinite(o))
     d = np.abs(np.where(empty, 0.0, lse) - np.where(empty, 0.0, rl))
     assert np.all(d <= tol_l), f"max |dL| {d.max():.3e}, allowed {tol_l.max():.3e}"
-    tol_o = HALF[q.dtype] * np.abs(ro) + (p_half + 2 * tol_l[..., None]) * a + 1e-7
+    tol_o = HALF[q.dtype] * np.abs(ro) + (HALF[F16] + 2 * tol_l[..., None]) * a + 1e-7
     d = np.abs(o - ro)
     assert np.all(d <= tol_o), f"max |dO| {d.max():.3e} at {np.unravel_index(d.argmax(), d.shape)}, {(d / tol_o).max():.2f} of the tolerance"
     if got_w is not None:
