@@ -128,7 +128,7 @@ int launch_prompt(const CacheAttnParams& a, const LaunchCtx& ctx) {
   static std::atomic<unsigned long long> configured{0};
   if (!((configured.load(std::memory_order_acquire) >> ctx.dev) & 1ull)) {
     // The register split inside the kernel assumes 128 a thread at launch; a
-    // smaller allocation would make its increase wait forever.
+    // smaller allocation would make its increases wait forever.
     cudaFuncAttributes attr;
     const cudaError_t e = cudaFuncGetAttributes(&attr, kern);
     if (e != cudaSuccess || attr.numRegs != 128) {

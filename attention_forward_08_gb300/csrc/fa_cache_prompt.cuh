@@ -50,10 +50,9 @@ struct PromptCfg {
   static constexpr int kOffMeta = kOffV + kStages * kKvBytes, kOffCtl = kOffMeta + 4 * 8 * 16;
   static constexpr int kSmem = 1024 + kOffCtl + 512;
   static constexpr int kColO = 256;                  // S: two buffers of 128 columns; P over S
-  // Registers: 512 threads x 128 at launch; control and converters give theirs
-  // to the softmax warps (128 * 40 + 128 * 72 + 256 * 200 = 512 * 128 with two
-  // tiles, 128 * 40 + 256 * 128 + 128 * 208 <= 512 * 128 with one).
-  static constexpr int kRegsCtrl = 40, kRegsConv = kTiles == 2 ? 72 : 128, kRegsSoft = kTiles == 2 ? 200 : 208;
+  // Registers: 512 threads x 128 at launch; the control warps give theirs to
+  // the converters, which keep a block of K and V in flight.
+  static constexpr int kRegsCtrl = 80, kRegsConv = kTiles == 2 ? 152 : 144, kRegsSoft = kTiles == 2 ? 136 : 144;
   static_assert(128 * kRegsCtrl + 32 * kConvWarps * kRegsConv + 128 * kTiles * kRegsSoft <= 512 * 128,
                 "register split exceeds the launch allocation");
   static_assert(kThreads == 512 && kSmem <= 232448, "thread block shape");
@@ -98,6 +97,28 @@ __device__ __forceinline__ void widen16(const uint4& w, uint4& lo, uint4& hi) {
   to_f16x4<kKind>(w.y, lo.z, lo.w);
   to_f16x4<kKind>(w.z, hi.x, hi.y);
   to_f16x4<kKind>(w.w, hi.z, hi.w);
+}
+
+// Scores of 32 keys (two groups of 16) to base 2 where a factor cannot do it,
+// and -inf outside [lo, hi).
+__device__ __forceinline__ void prompt_fix(uint32_t (&x)[32], const CacheAttnParams& a, const float4* meta, float rs,
+                                           bool raw, int lo, int hi) {
+  if (!raw) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const float ks = meta[g].x * rs, ci = ks * a.cap_in * 2.8853900817779268f;
+#pragma unroll
+      for (int k = 16 * g; k < 16 * g + 16; ++k) {
+        const float v = __uint_as_float(x[k]);
+        // cap * tanh(y) = cap * (1 - 2 / (2^(2 y log2 e) + 1))
+        x[k] = __float_as_uint(a.cap_out > 0.0f ? fmaf(-2.0f * a.cap_out, rcp_approx(ex2(v * ci) + 1.0f), a.cap_out)
+                                                : v * (ks * a.scale_log2));
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 32; ++k)
+    if (k < lo || k >= hi) x[k] = 0xFF800000u;
 }
 
 template <class C>
@@ -247,7 +268,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
     }
   } else if (warp < 4 + C::kConvWarps) {
     // ============================================================ converters
-    if constexpr (C::kRegsConv < 128) regs_dec<C::kRegsConv>();
+    regs_inc<C::kRegsConv>();
     const int cw = warp - 4;
     constexpr int kUnits = C::kD / 16;                  // 16-byte units a key
     constexpr int kPer = 128 * kUnits / (32 * C::kConvWarps);  // units a thread and tile: 4 (D = 64) or 8
@@ -269,31 +290,37 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
       const int2 span = dec_group_span<C>(p, at.seq, at.rg);
       const int first = span.x / 128 + pos - at.seg0;
       const int b = at.b, h = at.h;
-      // lane g (of 8) looks up tokens 16g .. of a block: its cache block and scales
-      int blk = -1;
+      // Four blocks at a time, and one batch ahead: lane 8q + g looks up tokens
+      // 16g .. of block q (its cache block), then that block's scales.
+      int blk = -1, next_blk;
       float ks = 0.0f, vs = 0.0f;
-      auto look_up = [&](int j) {
-        const int tok = (first + j) * 128 + 16 * (lane & 7);
-        blk = -1;
+      auto look_up = [&](int j0) {
+        const int j = j0 + (lane >> 3), tok = (first + j) * 128 + 16 * (lane & 7);
+        return j < n && tok < span.y && tok + 16 > span.x
+                   ? checked_block(c, c.table, c.table_stride, b, tok >> c.page_log2)
+                   : -1;
+      };
+      next_blk = look_up(0);
+      auto turn_over = [&](int j0) {  // the batch of blocks j0 .. becomes the one in the lanes
+        blk = next_blk;
         ks = vs = 0.0f;
-        if (j < n && tok < span.y && tok + 16 > span.x)
-          blk = checked_block(c, c.table, c.table_stride, b, tok >> c.page_log2);
         if (blk >= 0) {
           ks = __ldg(c.k_scale + (long long)blk * c.H + h);
           vs = __ldg(c.v_scale + (long long)blk * c.H + h);
         }
+        next_blk = look_up(j0 + 4);
       };
       uint4 xk[kPer], xv[kPer];
       // Keys (or values) of block j: zero where nobody sees them or nothing is stored.
-      auto load = [&](uint4(&x)[kPer], int j, const uint8_t* pool, const long long* st, bool values) {
+      auto load = [&](uint4(&x)[kPer], int j, const uint8_t* pool, const long long* st) {
+        const uint8_t* base = pool + h * st[1] + unit * 16;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int key = key0 + i * kKeysStep, tok = (first + j) * 128 + key;
-          const int at_blk = __shfl_sync(0xFFFFFFFFu, blk, key >> 4);
-          const float v = __shfl_sync(0xFFFFFFFFu, vs, key >> 4);
+          const int at_blk = __shfl_sync(0xFFFFFFFFu, blk, (j & 3) * 8 + (key >> 4));
           x[i] = make_uint4(0, 0, 0, 0);
-          if (at_blk >= 0 && tok >= span.x && tok < span.y && (!values || v > 0.0f))
-            x[i] = __ldg(reinterpret_cast<const uint4*>(pool + at_blk * st[0] + h * st[1] + (tok & (c.page - 1)) * st[2] + unit * 16));
+          if (at_blk >= 0 && tok >= span.x && tok < span.y)
+            x[i] = __ldg(reinterpret_cast<const uint4*>(base + at_blk * st[0] + (tok & (c.page - 1)) * st[2]));
         }
       };
       auto store = [&](const uint4(&x)[kPer], uint8_t* tile) {
@@ -308,29 +335,38 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
           *reinterpret_cast<uint4*>(row + (((u + 1) ^ (key & 7)) << 4)) = hi;
         }
       };
-      look_up(0);
-      load(xk, 0, c.k, c.ks, false);
-      load(xv, 0, c.v, c.vs, true);
+      turn_over(0);
+      load(xk, 0, c.k, c.ks);
+      load(xv, 0, c.v, c.vs);
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
         const int stage = (blocks + j) % C::kStages;
         const uint32_t use = (uint32_t)((blocks + j) / C::kStages);
         if (use > 0 && !(ok = prompt_warp_wait(&ctl->k_empty[stage], (use - 1) & 1, abort, a))) break;
-        if (cw == 0 && lane < 8)
-          s_meta[((blocks + j) & 3) * 8 + lane] =
-              make_float4(ks, vs > 0.0f ? log2f(vs) : 0.0f, vs > 0.0f ? 1.0f / vs : 1.0f, blk >= 0 ? 1.0f : 0.0f);
+        // (values of a zero scale are stored zeros for all that counts: they are
+        // cleared below, and count with the scale 1)
+        const bool none = !(vs > 0.0f);
+        if (cw == 0 && (lane >> 3) == (j & 3))
+          s_meta[((blocks + j) & 3) * 8 + (lane & 7)] =
+              make_float4(ks, none ? 0.0f : lg2(vs), none ? 1.0f : 1.0f / vs, blk >= 0 ? 1.0f : 0.0f);
+        const uint32_t zero = __ballot_sync(0xFFFFFFFFu, none) >> (8 * (j & 3));  // groups of this block
         store(xk, smem + C::kOffK + stage * C::kKvBytes);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->k_full[stage]);
-        look_up(j + 1);
-        load(xk, j + 1, c.k, c.ks, false);
+        if ((j & 3) == 3) turn_over(j + 1);
+        load(xk, j + 1, c.k, c.ks);
+        if (zero & 0xFFu) {
+#pragma unroll
+          for (int i = 0; i < kPer; ++i)
+            if ((zero >> ((key0 + i * kKeysStep) >> 4)) & 1u) xv[i] = make_uint4(0, 0, 0, 0);
+        }
         if (use > 0 && !(ok = prompt_warp_wait(&ctl->v_empty[stage], (use - 1) & 1, abort, a))) break;
         store(xv, smem + C::kOffV + stage * C::kKvBytes);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->v_full[stage]);
-        load(xv, j + 1, c.v, c.vs, true);
+        load(xv, j + 1, c.v, c.vs);
       }
       blocks += n;
       pos += n;
@@ -405,50 +441,40 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
         if (!ok) break;
         tc_fence_after();
         const uint32_t tS = tmem + lane_addr + buf * 128;
-        float s[128];
-        {
-          uint32_t rr[128];
-#pragma unroll
-          for (int cc = 0; cc < 4; ++cc) tmem_ld32(tS + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&rr[cc * 32]));
-          tmem_wait_ld();
-          reg_fence(rr);
-#pragma unroll
-          for (int k = 0; k < 128; ++k) s[k] = __uint_as_float(rr[k]);
-        }
+        // Two passes over the row in chunks of 32 scores, the next chunk on its
+        // way while one is worked on: the maximum, then P.  A row held in
+        // registers instead would take 200 of them, and leave the converters too
+        // few to keep a block of K and V in flight.
         const float4* meta = s_meta + (nth & 3) * 8;
         const int key0 = (first + j) * 128, lo = see.x - key0, hi = see.y - key0;
-        if (!raw) {  // scores to base 2 first
+        const bool edge = __any_sync(0xFFFFFFFFu, lo > 0 || hi < 128);
+        uint32_t ra[32], rb[32];
+        float mx = -INFINITY;
+        tmem_ld32(tS, ra);
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            const float ks = meta[g].x * rs;
-            if (a.cap_out > 0.0f) {
-              const float ci = ks * a.cap_in * 2.8853900817779268f;
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t(&x)[32] = cc & 1 ? rb : ra;
+          tmem_wait_ld();
+          reg_fence(x);
+          if (cc < 3) tmem_ld32(tS + (cc + 1) * 32, cc & 1 ? ra : rb);
+          if (!raw || edge) {
+            prompt_fix(x, a, meta + 2 * cc, rs, raw, lo - 32 * cc, hi - 32 * cc);
+            tmem_st32(tS + cc * 32, x);  // for the second pass
+          }
 #pragma unroll
-              for (int k = 16 * g; k < 16 * g + 16; ++k)
-                s[k] = fmaf(-2.0f * a.cap_out, rcp_approx(ex2(s[k] * ci) + 1.0f), a.cap_out);
-            } else {
-#pragma unroll
-              for (int k = 16 * g; k < 16 * g + 16; ++k) s[k] *= ks * a.scale_log2;
-            }
+          for (int g = 0; g < 2; ++g) {
+            const float4 q = meta[2 * cc + g];
+            auto f = [&](int i) { return __uint_as_float(x[16 * g + i]); };
+            float v = fmax3(fmax3(f(0), f(1), f(2)), f(3), f(4)), w = fmax3(fmax3(f(5), f(6), f(7)), f(8), f(9));
+            v = fmax3(v, f(10), f(11));
+            w = fmax3(w, f(12), f(13));
+            v = fmax3(fmaxf(v, w), f(14), f(15));
+            if (q.w == 0.0f) v = -INFINITY;  // nothing stored there
+            mx = fmaxf(mx, fmaf(v, raw ? fmaxf(q.x * f_row, 1e-37f) : 1.0f, q.y));
           }
         }
-        if (lo > 0 || hi < 128) {
-#pragma unroll
-          for (int k = 0; k < 128; ++k)
-            if (k < lo || k >= hi) s[k] = -INFINITY;
-        }
-        float mx = -INFINITY;
-#pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          const float4 q = meta[g];
-          const float* x = s + 16 * g;
-          float v = fmax3(fmax3(x[0], x[1], x[2]), x[3], x[4]), w = fmax3(fmax3(x[5], x[6], x[7]), x[8], x[9]);
-          v = fmax3(v, x[10], x[11]);
-          w = fmax3(w, x[12], x[13]);
-          v = fmax3(fmaxf(v, w), x[14], x[15]);
-          if (q.w == 0.0f) v = -INFINITY;  // nothing stored there
-          mx = fmaxf(mx, fmaf(v, raw ? fmaxf(q.x * f_row, 1e-37f) : 1.0f, q.y));
-        }
+        if (!raw || edge) tmem_wait_st();
+        tmem_ld32(tS, ra);
         float corr = 1.0f;
         const bool resc = mx > m + kDecLazy;
         if (resc) {
@@ -459,23 +485,27 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
         const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
         for (int cc = 0; cc < 4; ++cc) {
+          uint32_t(&x)[32] = cc & 1 ? rb : ra;
+          tmem_wait_ld();
+          reg_fence(x);
+          if (cc < 3) tmem_ld32(tS + (cc + 1) * 32, cc & 1 ? ra : rb);
           uint32_t pk[16];
 #pragma unroll
-          for (int gg = 0; gg < 2; ++gg) {
-            const float4 q = meta[2 * cc + gg];
+          for (int g = 0; g < 2; ++g) {
+            const float4 q = meta[2 * cc + g];
             const float f = raw ? fmaxf(q.x * f_row, 1e-37f) : 1.0f, off = q.w == 0.0f ? -INFINITY : q.y - base;
             float sum[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const int k = 32 * cc + 16 * gg + 2 * e;
               float x0, x1;
-              ffma2(x0, x1, s[k], s[k + 1], f, f, off, off);
+              ffma2(x0, x1, __uint_as_float(x[16 * g + 2 * e]), __uint_as_float(x[16 * g + 2 * e + 1]), f, f, off, off);
               x0 = ex2(x0), x1 = ex2(x1);
               fadd2(sum[0], sum[1], x0, x1);
-              pk[8 * gg + e] = pack_f16x2(x0, x1);
+              pk[8 * g + e] = pack_f16x2(x0, x1);
             }
             l = fmaf(sum[0] + sum[1], q.z, l);
           }
+          // over scores that were read before: columns 16cc .. of the 32cc + 32 done
           tmem_st16(tS + cc * 16, pk);
         }
         if constexpr (C::kTiles == 1) {  // PV of the block before has landed (each phase is consumed, in order)
