@@ -166,7 +166,7 @@ AttnPlan attn_plan(const CacheAttnParams& a) {
 template <int kD>
 long long plan_workspace(const CacheAttnParams& a, int num_sms) {
   switch (attn_plan<kD>(a)) {
-    case AttnPlan::kPrompt: return line_workspace<PromptCfg<0, false, kD>>(num_sms);
+    case AttnPlan::kPrompt: return line_workspace<PromptCfg<0, false, kD, 16>>(num_sms);
     case AttnPlan::kRows32:
       if constexpr (kD <= 128) return line_workspace<DecCfg<0, false, kD, 2>>(num_sms * DecCfg<0, false, kD, 2>::kCtas);
     default: return line_workspace<DecCfg<0, false, kD, 1>>(num_sms * DecCfg<0, false, kD, 1>::kCtas);
@@ -176,7 +176,9 @@ long long plan_workspace(const CacheAttnParams& a, int num_sms) {
 template <int kD, int kKind, bool kF16>
 int launch_plan(const CacheAttnParams& a, const LaunchCtx& ctx) {
   switch (attn_plan<kD>(a)) {
-    case AttnPlan::kPrompt: return launch_prompt<PromptCfg<kKind, kF16, kD>>(a, ctx);
+    case AttnPlan::kPrompt:
+      return a.c.page >= 64 ? launch_prompt<PromptCfg<kKind, kF16, kD, 64>>(a, ctx)
+                            : launch_prompt<PromptCfg<kKind, kF16, kD, 16>>(a, ctx);
     case AttnPlan::kRows32:
       if constexpr (kD <= 128) return launch_decode<DecCfg<kKind, kF16, kD, 2>>(a, ctx);
     default: return launch_decode<DecCfg<kKind, kF16, kD, 1>>(a, ctx);

@@ -7,12 +7,12 @@
 //
 // Mathematics.  All products in f16 with fp32 accumulation: a stored value is
 // an f16 number, a bf16 query row is scaled by a power of two.  With k_scale
-// and v_scale constant over 16 tokens (ks, vs), row i's weights are kept as
+// and v_scale constant over groups of 16 or 64 tokens (ks, vs), row i's weights are kept as
 //
 //   P'_ij = 2^(s_ij + log2 vs_j - m_i),   O = sum_j P'_ij v8_j / l_i,   l_i = sum_j P'_ij / vs_j
 //
 // with m_i the running maximum of s + log2 vs: one FMA and one exponential a
-// score, the scales cost an operation per 16 scores, and what counts most in O
+// score, the scales cost an operation per group, and what counts most in O
 // always has P' near 1, whatever the scales of other blocks.  P' is rounded to
 // f16 (2^-11), the sums are not.
 //
@@ -31,8 +31,12 @@
 
 namespace fa {
 
-template <int kKind_, bool kF16_, int kD_>
+// kGroup_: tokens that surely share a cache block, and so a scale: 16, or 64
+// where blocks have 64 tokens and more (a quarter of the operations by group:
+// TIMES).
+template <int kKind_, bool kF16_, int kD_, int kGroup_>
 struct PromptCfg {
+  static constexpr int kGroup = kGroup_, kGroups = 128 / kGroup;  // groups a block of keys
   static constexpr int kKind = kKind_;
   static constexpr bool kF16 = kF16_;
   static constexpr int kD = kD_;
@@ -47,12 +51,13 @@ struct PromptCfg {
   static constexpr int kQBytes = 128 * kD * 2;       // one row tile
   static constexpr int kKvBytes = 128 * kD * 2;
   static constexpr int kOffK = kTiles * kQBytes, kOffV = kOffK + kStages * kKvBytes;
-  static constexpr int kOffMeta = kOffV + kStages * kKvBytes, kOffCtl = kOffMeta + 4 * 8 * 16;
+  static constexpr int kOffMeta = kOffV + kStages * kKvBytes, kOffCtl = kOffMeta + 4 * kGroups * 16;
   static constexpr int kSmem = 1024 + kOffCtl + 512;
   static constexpr int kColO = 256;                  // S: two buffers of 128 columns; P over S
-  // Registers: 512 threads x 128 at launch; the control warps give theirs to
-  // the converters, which keep a block of K and V in flight.
-  static constexpr int kRegsCtrl = 80, kRegsConv = kTiles == 2 ? 152 : 144, kRegsSoft = kTiles == 2 ? 136 : 144;
+  // Registers: 512 threads x 128 at launch; the softmax warps, which hold a
+  // row of scores each, take the others'.
+  static constexpr int kRegsCtrl = 40, kRegsConv = kTiles == 2 ? 72 : 104, kRegsSoft = kTiles == 2 ? 200 : 208;
+  static_assert(kRegsCtrl < 128 && kRegsConv < 128 && kRegsSoft > 128, "which warps give, which take");
   static_assert(128 * kRegsCtrl + 32 * kConvWarps * kRegsConv + 128 * kTiles * kRegsSoft <= 512 * 128,
                 "register split exceeds the launch allocation");
   static_assert(kThreads == 512 && kSmem <= 232448, "thread block shape");
@@ -67,6 +72,7 @@ struct PromptCtl {
   uint64_t o_ready[2];             // two tiles: a piece's last PV done; one tile: each PV done
   uint64_t turn[2];
   uint64_t drain[2];
+  int n[2][2];                     // [tile][piece & 1]: blocks of a piece (0: no more), beside q_full
   uint32_t tmem;
   int abort;
 };
@@ -99,26 +105,20 @@ __device__ __forceinline__ void widen16(const uint4& w, uint4& lo, uint4& hi) {
   to_f16x4<kKind>(w.w, hi.z, hi.w);
 }
 
-// Scores of 32 keys (two groups of 16) to base 2 where a factor cannot do it,
-// and -inf outside [lo, hi).
-__device__ __forceinline__ void prompt_fix(uint32_t (&x)[32], const CacheAttnParams& a, const float4* meta, float rs,
-                                           bool raw, int lo, int hi) {
-  if (!raw) {
+// A row's scores to base 2 where one positive factor cannot do it.
+template <class C>
+__device__ __forceinline__ void prompt_scale(uint32_t (&x)[128], const CacheAttnParams& a, const float4* meta, float rs) {
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const float ks = meta[g].x * rs, ci = ks * a.cap_in * 2.8853900817779268f;
+  for (int g = 0; g < C::kGroups; ++g) {
+    const float ks = meta[g].x * rs, ci = ks * a.cap_in * 2.8853900817779268f;
 #pragma unroll
-      for (int k = 16 * g; k < 16 * g + 16; ++k) {
-        const float v = __uint_as_float(x[k]);
-        // cap * tanh(y) = cap * (1 - 2 / (2^(2 y log2 e) + 1))
-        x[k] = __float_as_uint(a.cap_out > 0.0f ? fmaf(-2.0f * a.cap_out, rcp_approx(ex2(v * ci) + 1.0f), a.cap_out)
-                                                : v * (ks * a.scale_log2));
-      }
+    for (int k = C::kGroup * g; k < C::kGroup * (g + 1); ++k) {
+      const float v = __uint_as_float(x[k]);
+      // cap * tanh(y) = cap * (1 - 2 / (2^(2 y log2 e) + 1))
+      x[k] = __float_as_uint(a.cap_out > 0.0f ? fmaf(-2.0f * a.cap_out, rcp_approx(ex2(v * ci) + 1.0f), a.cap_out)
+                                              : v * (ks * a.scale_log2));
     }
   }
-#pragma unroll
-  for (int k = 0; k < 32; ++k)
-    if (k < lo || k >= hi) x[k] = 0xFF800000u;
 }
 
 template <class C>
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
   const CacheView& c = a.c;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  float4* s_meta = reinterpret_cast<float4*>(smem + C::kOffMeta);  // [block % 4][16 tokens]: ks, log2 vs, 1 / vs, there
+  float4* s_meta = reinterpret_cast<float4*>(smem + C::kOffMeta);  // [block % 4][group]: ks, log2 vs, 1 / vs, there
   PromptCtl* ctl = reinterpret_cast<PromptCtl*>(smem + C::kOffCtl);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -201,61 +201,59 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
           ++groups;
         }
       };
-      int blocks = 0, pieces = 0;  // blocks and pieces before this one
-      bool ok = true;
+      if (lane == 0) {
+        int nth = 0, stage = 0;  // blocks done, and the next one's stage
+        uint32_t par = 0;        // parity of the stage's use
+        bool ok = true;
 #pragma unroll 1
-      for (int pos = t0; pos < t1 && ok; ++pieces) {
-        const int tiles = dec_tiles<C>(p, at.seq, at.rg), n = min(t1, at.seg0 + tiles) - pos;
-        if (lane == 0) {
-          auto k_at = [&](int j) { return (blocks + j) % C::kStages; };
-          auto par = [&](int j) { return (uint32_t)((blocks + j) / C::kStages) & 1u; };
-          ok = prompt_wait(&ctl->q_full[t], pieces & 1, abort, a) && prompt_wait(&ctl->k_full[k_at(0)], par(0), abort, a) &&
-               wait_turn();
-          if (ok) {
-            tc_fence_after();
-            // buffers: two tiles: tile t's; one: alternating over all blocks
-            auto buf = [&](int j) { return C::kTiles == 2 ? t : (blocks + j) & 1; };
-            issue_S(buf(0), k_at(0));
-            mma_commit(&ctl->s_full[buf(0)]);
-            pass_turn();
-            mma_commit(&ctl->k_empty[k_at(0)]);
+        for (int pieces = 0; ok; ++pieces) {
+          ok = prompt_wait(&ctl->q_full[t], pieces & 1, abort, a);
+          if (!ok) break;
+          const int n = ctl->n[t][pieces & 1];
+          if (n == 0) break;
+          ok = prompt_wait(&ctl->k_full[stage], par, abort, a) && wait_turn();
+          if (!ok) break;
+          tc_fence_after();
+          // buffers: two tiles: tile t's; one: alternating over all blocks
+          issue_S(C::kTiles == 2 ? t : nth & 1, stage);
+          mma_commit(&ctl->s_full[C::kTiles == 2 ? t : nth & 1]);
+          pass_turn();
+          mma_commit(&ctl->k_empty[stage]);
 #pragma unroll 1
-            for (int j = 0; j < n && ok; ++j) {
-              if constexpr (C::kTiles == 1) {  // the next S goes before this PV
-                if (j + 1 < n) {
-                  ok = prompt_wait(&ctl->k_full[k_at(j + 1)], par(j + 1), abort, a);
-                  if (!ok) break;
-                  tc_fence_after();
-                  issue_S(buf(j + 1), k_at(j + 1));
-                  mma_commit(&ctl->s_full[buf(j + 1)]);
-                  mma_commit(&ctl->k_empty[k_at(j + 1)]);
-                }
+          for (int j = 0; j < n; ++j, ++nth) {
+            const int next = stage + 1 == C::kStages ? 0 : stage + 1;
+            const uint32_t next_par = par ^ (next == 0 ? 1u : 0u);
+            const bool more = j + 1 < n;
+            if constexpr (C::kTiles == 1) {  // the next S goes before this PV
+              if (more) {
+                ok = prompt_wait(&ctl->k_full[next], next_par, abort, a);
+                if (!ok) break;
+                tc_fence_after();
+                issue_S((nth + 1) & 1, next);
+                mma_commit(&ctl->s_full[(nth + 1) & 1]);
+                mma_commit(&ctl->k_empty[next]);
               }
-              ok = prompt_wait(&ctl->v_full[k_at(j)], par(j), abort, a) &&
-                   prompt_wait(&ctl->p_ready[t], (uint32_t)(blocks + j) & 1u, abort, a);
-              if (ok && C::kTiles == 2 && j + 1 < n) ok = prompt_wait(&ctl->k_full[k_at(j + 1)], par(j + 1), abort, a);
-              if (ok) ok = wait_turn();
-              if (!ok) break;
-              tc_fence_after();
-              issue_PV(buf(j), k_at(j), j == 0);
-              if (C::kTiles == 1 || j + 1 == n) mma_commit(&ctl->o_ready[t]);
-              if constexpr (C::kTiles == 2) {
-                if (j + 1 < n) {
-                  issue_S(t, k_at(j + 1));
-                  mma_commit(&ctl->s_full[t]);
-                }
-              }
-              pass_turn();
-              mma_commit(&ctl->v_empty[k_at(j)]);
-              if (C::kTiles == 2 && j + 1 < n) mma_commit(&ctl->k_empty[k_at(j + 1)]);
             }
+            ok = prompt_wait(&ctl->v_full[stage], par, abort, a) &&
+                 (C::kTiles == 1 || !more || prompt_wait(&ctl->k_full[next], next_par, abort, a)) &&
+                 prompt_wait(&ctl->p_ready[t], (uint32_t)nth & 1u, abort, a) && wait_turn();
+            if (!ok) break;
+            tc_fence_after();
+            issue_PV(C::kTiles == 2 ? t : nth & 1, stage, j == 0);
+            if (C::kTiles == 1 || !more) mma_commit(&ctl->o_ready[t]);
+            if (C::kTiles == 2 && more) {
+              issue_S(t, next);
+              mma_commit(&ctl->s_full[t]);
+            }
+            pass_turn();
+            mma_commit(&ctl->v_empty[stage]);
+            if (C::kTiles == 2 && more) mma_commit(&ctl->k_empty[next]);
+            stage = next;
+            par = next_par;
           }
         }
-        ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
-        blocks += n;
-        pos += n;
-        dec_next(p, at, tiles);
       }
+      __syncwarp();
       // Every MMA issued here has completed before the block lets go of its
       // memory (after an expired wait too; bounded).
       if (lane == 0) {
@@ -268,7 +266,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
     }
   } else if (warp < 4 + C::kConvWarps) {
     // ============================================================ converters
-    regs_inc<C::kRegsConv>();
+    regs_dec<C::kRegsConv>();
     const int cw = warp - 4;
     constexpr int kUnits = C::kD / 16;                  // 16-byte units a key
     constexpr int kPer = 128 * kUnits / (32 * C::kConvWarps);  // units a thread and tile: 4 (D = 64) or 8
@@ -281,7 +279,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
     constexpr int kKeysStep = kKeysWarp * C::kConvWarps;  // 32 (D = 64) or 16
     const int key0 = cw * kKeysWarp + key_in;
     const uint32_t col = (uint32_t)(unit / 4) * (128 * 128);
-    int blocks = 0;
+    int nth = 0, stage = 0;  // blocks done; the next one's stage, and the parity of its use
+    uint32_t par = 0;
     bool ok = true;
 #pragma unroll 1
     for (int pos = t0; pos < t1 && ok;) {
@@ -290,13 +289,15 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
       const int2 span = dec_group_span<C>(p, at.seq, at.rg);
       const int first = span.x / 128 + pos - at.seg0;
       const int b = at.b, h = at.h;
-      // Four blocks at a time, and one batch ahead: lane 8q + g looks up tokens
-      // 16g .. of block q (its cache block), then that block's scales.
+      // A batch of blocks at a time, and one batch ahead: lane kGroups * q + g
+      // looks up group g of the batch's block q (its cache block), then the
+      // scales.
+      constexpr int kG = C::kGroups, kBatch = 32 / kG;
       int blk = -1, next_blk;
       float ks = 0.0f, vs = 0.0f;
       auto look_up = [&](int j0) {
-        const int j = j0 + (lane >> 3), tok = (first + j) * 128 + 16 * (lane & 7);
-        return j < n && tok < span.y && tok + 16 > span.x
+        const int j = j0 + lane / kG, tok = (first + j) * 128 + C::kGroup * (lane % kG);
+        return j < n && tok < span.y && tok + C::kGroup > span.x
                    ? checked_block(c, c.table, c.table_stride, b, tok >> c.page_log2)
                    : -1;
       };
@@ -308,67 +309,87 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
           ks = __ldg(c.k_scale + (long long)blk * c.H + h);
           vs = __ldg(c.v_scale + (long long)blk * c.H + h);
         }
-        next_blk = look_up(j0 + 4);
+        next_blk = look_up(j0 + kBatch);
       };
-      uint4 xk[kPer], xv[kPer];
-      // Keys (or values) of block j: zero where nobody sees them or nothing is stored.
-      auto load = [&](uint4(&x)[kPer], int j, const uint8_t* pool, const long long* st) {
-        const uint8_t* base = pool + h * st[1] + unit * 16;
+      // One set of registers, always on its way: as soon as a unit of K_j is
+      // widened and stored, its register takes that unit of V_j, and then of
+      // K_{j+1}, so that every load has half a block's time to arrive.
+      uint4 x[kPer];
+      // Where this thread's keys of a block lie: by unit where groups are as
+      // short as a step between units, else by group.
+      auto load_at = [&](int i, int j, const uint8_t* from, long long row) {
+        const int tok = (first + j) * 128 + key0 + i * kKeysStep;
+        x[i] = make_uint4(0, 0, 0, 0);  // where nobody sees them or nothing is stored
+        if (from && tok >= span.x && tok < span.y)
+          x[i] = __ldg(reinterpret_cast<const uint4*>(from + ((key0 + i * kKeysStep) & (c.page - 1)) * row));
+      };
+      const uint8_t* from[kG];
+      auto find = [&](int j, const uint8_t* pool, const long long* st) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int key = key0 + i * kKeysStep, tok = (first + j) * 128 + key;
-          const int at_blk = __shfl_sync(0xFFFFFFFFu, blk, (j & 3) * 8 + (key >> 4));
-          x[i] = make_uint4(0, 0, 0, 0);
-          if (at_blk >= 0 && tok >= span.x && tok < span.y)
-            x[i] = __ldg(reinterpret_cast<const uint4*>(base + at_blk * st[0] + (tok & (c.page - 1)) * st[2]));
+        for (int g = 0; g < kG; ++g) {
+          const int at_blk = __shfl_sync(0xFFFFFFFFu, blk, (j % kBatch) * kG + g);
+          from[g] = at_blk >= 0 ? pool + at_blk * st[0] : nullptr;
         }
       };
-      auto store = [&](const uint4(&x)[kPer], uint8_t* tile) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int key = key0 + i * kKeysStep;
-          uint4 lo, hi;
-          widen16<C::kKind>(x[i], lo, hi);
-          uint8_t* row = tile + col + key * 128;
-          const int u = (unit % 4) * 2;
-          *reinterpret_cast<uint4*>(row + ((u ^ (key & 7)) << 4)) = lo;
-          *reinterpret_cast<uint4*>(row + (((u + 1) ^ (key & 7)) << 4)) = hi;
+      auto load = [&](int i, int j, const uint8_t* pool, const long long* st) {
+        if constexpr (C::kGroup == 64) {
+          load_at(i, j, from[i * kKeysStep / 64], st[2]);
+        } else {
+          const int at_blk = __shfl_sync(0xFFFFFFFFu, blk, (j % kBatch) * kG + ((key0 + i * kKeysStep) >> 4));
+          load_at(i, j, at_blk >= 0 ? pool + at_blk * st[0] : nullptr, st[2]);
         }
       };
+      auto store = [&](int i, uint8_t* tile) {
+        const int key = key0 + i * kKeysStep;
+        uint4 lo, hi;
+        widen16<C::kKind>(x[i], lo, hi);
+        uint8_t* row = tile + col + key * 128;
+        const int u = (unit % 4) * 2;
+        *reinterpret_cast<uint4*>(row + ((u ^ (key & 7)) << 4)) = lo;
+        *reinterpret_cast<uint4*>(row + (((u + 1) ^ (key & 7)) << 4)) = hi;
+      };
+      const uint8_t* const k_pool = c.k + h * c.ks[1] + unit * 16;
+      const uint8_t* const v_pool = c.v + h * c.vs[1] + unit * 16;
       turn_over(0);
-      load(xk, 0, c.k, c.ks);
-      load(xv, 0, c.v, c.vs);
+      if constexpr (C::kGroup == 64) find(0, k_pool, c.ks);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) load(i, 0, k_pool, c.ks);
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
-        const int stage = (blocks + j) % C::kStages;
-        const uint32_t use = (uint32_t)((blocks + j) / C::kStages);
-        if (use > 0 && !(ok = prompt_warp_wait(&ctl->k_empty[stage], (use - 1) & 1, abort, a))) break;
+        if (nth >= C::kStages && !(ok = prompt_warp_wait(&ctl->k_empty[stage], par ^ 1u, abort, a))) break;
         // (values of a zero scale are stored zeros for all that counts: they are
         // cleared below, and count with the scale 1)
         const bool none = !(vs > 0.0f);
-        if (cw == 0 && (lane >> 3) == (j & 3))
-          s_meta[((blocks + j) & 3) * 8 + (lane & 7)] =
+        if (cw == 0 && lane / kG == j % kBatch)
+          s_meta[(nth & 3) * kG + lane % kG] =
               make_float4(ks, none ? 0.0f : lg2(vs), none ? 1.0f : 1.0f / vs, blk >= 0 ? 1.0f : 0.0f);
-        const uint32_t zero = __ballot_sync(0xFFFFFFFFu, none) >> (8 * (j & 3));  // groups of this block
-        store(xk, smem + C::kOffK + stage * C::kKvBytes);
+        const uint32_t zero = (__ballot_sync(0xFFFFFFFFu, none) >> (kG * (j % kBatch))) & ((1u << kG) - 1u);  // groups of this block
+        uint8_t* tile = smem + C::kOffK + stage * C::kKvBytes;
+        if constexpr (C::kGroup == 64) find(j, v_pool, c.vs);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          store(i, tile);
+          load(i, j, v_pool, c.vs);
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->k_full[stage]);
-        if ((j & 3) == 3) turn_over(j + 1);
-        load(xk, j + 1, c.k, c.ks);
-        if (zero & 0xFFu) {
+        if (j % kBatch == kBatch - 1) turn_over(j + 1);
+        if (nth >= C::kStages && !(ok = prompt_warp_wait(&ctl->v_empty[stage], par ^ 1u, abort, a))) break;
+        tile = smem + C::kOffV + stage * C::kKvBytes;
+        if constexpr (C::kGroup == 64) find(j + 1, k_pool, c.ks);
 #pragma unroll
-          for (int i = 0; i < kPer; ++i)
-            if ((zero >> ((key0 + i * kKeysStep) >> 4)) & 1u) xv[i] = make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kPer; ++i) {
+          if ((zero >> ((key0 + i * kKeysStep) / C::kGroup)) & 1u) x[i] = make_uint4(0, 0, 0, 0);
+          store(i, tile);
+          load(i, j + 1, k_pool, c.ks);
         }
-        if (use > 0 && !(ok = prompt_warp_wait(&ctl->v_empty[stage], (use - 1) & 1, abort, a))) break;
-        store(xv, smem + C::kOffV + stage * C::kKvBytes);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->v_full[stage]);
-        load(xv, j + 1, c.v, c.vs);
+        ++nth;
+        if (++stage == C::kStages) stage = 0, par ^= 1u;
       }
-      blocks += n;
       pos += n;
       dec_next(p, at, tiles);
     }
@@ -429,7 +450,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->q_full[t]);
+      if (lane == 0) {
+        if ((warp & 3) == 0) ctl->n[t][pieces & 1] = n;
+        mbar_arrive(&ctl->q_full[t]);
+      }
 
       const float f_row = rs * a.scale_log2;
       float m = -INFINITY, l = 0.0f;
@@ -441,40 +465,37 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
         if (!ok) break;
         tc_fence_after();
         const uint32_t tS = tmem + lane_addr + buf * 128;
-        // Two passes over the row in chunks of 32 scores, the next chunk on its
-        // way while one is worked on: the maximum, then P.  A row held in
-        // registers instead would take 200 of them, and leave the converters too
-        // few to keep a block of K and V in flight.
-        const float4* meta = s_meta + (nth & 3) * 8;
+        const float4* meta = s_meta + (nth & 3) * C::kGroups;
         const int key0 = (first + j) * 128, lo = see.x - key0, hi = see.y - key0;
-        const bool edge = __any_sync(0xFFFFFFFFu, lo > 0 || hi < 128);
-        uint32_t ra[32], rb[32];
-        float mx = -INFINITY;
-        tmem_ld32(tS, ra);
+        uint32_t x[128];  // the row's scores (fp32 bits)
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          uint32_t(&x)[32] = cc & 1 ? rb : ra;
-          tmem_wait_ld();
-          reg_fence(x);
-          if (cc < 3) tmem_ld32(tS + (cc + 1) * 32, cc & 1 ? ra : rb);
-          if (!raw || edge) {
-            prompt_fix(x, a, meta + 2 * cc, rs, raw, lo - 32 * cc, hi - 32 * cc);
-            tmem_st32(tS + cc * 32, x);  // for the second pass
-          }
+        for (int cc = 0; cc < 4; ++cc) tmem_ld32(tS + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[cc * 32]));
+        tmem_wait_ld();
+        reg_fence(x);
+        if (!raw) prompt_scale<C>(x, a, meta, rs);
+        if (lo > 0 || hi < 128) {
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const float4 q = meta[2 * cc + g];
-            auto f = [&](int i) { return __uint_as_float(x[16 * g + i]); };
-            float v = fmax3(fmax3(f(0), f(1), f(2)), f(3), f(4)), w = fmax3(fmax3(f(5), f(6), f(7)), f(8), f(9));
-            v = fmax3(v, f(10), f(11));
-            w = fmax3(w, f(12), f(13));
-            v = fmax3(fmaxf(v, w), f(14), f(15));
-            if (q.w == 0.0f) v = -INFINITY;  // nothing stored there
-            mx = fmaxf(mx, fmaf(v, raw ? fmaxf(q.x * f_row, 1e-37f) : 1.0f, q.y));
-          }
+          for (int k = 0; k < 128; ++k)
+            if (k < lo || k >= hi) x[k] = 0xFF800000u;
         }
-        if (!raw || edge) tmem_wait_st();
-        tmem_ld32(tS, ra);
+        // Group by group: a raw score times f plus y is the score's weight in
+        // base 2 (s + log2 vs); y = -inf where nothing is stored.
+        float f[C::kGroups], y[C::kGroups], mx = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < C::kGroups; ++g) {
+          const float4 q = meta[g];
+          f[g] = raw ? fmaxf(q.x * f_row, 1e-37f) : 1.0f;  // (not 0: a hidden score stays -inf)
+          y[g] = q.w == 0.0f ? -INFINITY : q.y;
+        }
+#pragma unroll
+        for (int g = 0; g < C::kGroups; ++g) {
+          float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int k = 0; k < C::kGroup; k += 2)
+            v[(k >> 1) & 3] = fmax3(v[(k >> 1) & 3], __uint_as_float(x[C::kGroup * g + k]),
+                                    __uint_as_float(x[C::kGroup * g + k + 1]));
+          mx = fmaxf(mx, fmaf(fmax3(fmaxf(v[0], v[1]), v[2], v[3]), f[g], y[g]));
+        }
         float corr = 1.0f;
         const bool resc = mx > m + kDecLazy;
         if (resc) {
@@ -484,29 +505,24 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
         }
         const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          uint32_t(&x)[32] = cc & 1 ? rb : ra;
-          tmem_wait_ld();
-          reg_fence(x);
-          if (cc < 3) tmem_ld32(tS + (cc + 1) * 32, cc & 1 ? ra : rb);
-          uint32_t pk[16];
+        for (int g = 0; g < C::kGroups; ++g) {
+          const float off = y[g] - base;
+          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const float4 q = meta[2 * cc + g];
-            const float f = raw ? fmaxf(q.x * f_row, 1e-37f) : 1.0f, off = q.w == 0.0f ? -INFINITY : q.y - base;
-            float sum[2] = {0.0f, 0.0f};
+          for (int c0 = 0; c0 < C::kGroup; c0 += 16) {
+            uint32_t pk[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
+              const int k = C::kGroup * g + c0 + 2 * e;
               float x0, x1;
-              ffma2(x0, x1, __uint_as_float(x[16 * g + 2 * e]), __uint_as_float(x[16 * g + 2 * e + 1]), f, f, off, off);
+              ffma2(x0, x1, __uint_as_float(x[k]), __uint_as_float(x[k + 1]), f[g], f[g], off, off);
               x0 = ex2(x0), x1 = ex2(x1);
-              fadd2(sum[0], sum[1], x0, x1);
-              pk[8 * g + e] = pack_f16x2(x0, x1);
+              fadd2(sum[(e & 1) * 2], sum[(e & 1) * 2 + 1], x0, x1);
+              pk[e] = pack_f16x2(x0, x1);
             }
-            l = fmaf(sum[0] + sum[1], q.z, l);
+            tmem_st8(tS + (C::kGroup * g + c0) / 2, pk);
           }
-          // over scores that were read before: columns 16cc .. of the 32cc + 32 done
-          tmem_st16(tS + cc * 16, pk);
+          l = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), meta[g].z, l);
         }
         if constexpr (C::kTiles == 1) {  // PV of the block before has landed (each phase is consumed, in order)
           if (nth > 0) {
@@ -581,6 +597,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
       }
       pos += n;
       dec_next(p, at, tiles);
+    }
+    if (ok && lane == 0) {
+      if ((warp & 3) == 0) ctl->n[t][pieces & 1] = 0;
+      mbar_arrive(&ctl->q_full[t]);
     }
   }
   tc_fence_before();
