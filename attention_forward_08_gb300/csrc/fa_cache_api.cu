@@ -267,11 +267,11 @@ int check_evict(const fa_cache_evict_args* a) {
   return FA_OK;
 }
 
-// Slots that eviction names per head (src, mover), counts, edge scales.
+// Slots that eviction names per head (src, mover), and counts.
 long long evict_slots(const fa_cache_evict_args* a) { return (long long)a->B * a->cache.H_kv * a->keep; }
 long long evict_workspace(const fa_cache_evict_args* a) {
   const long long heads = (long long)a->B * a->cache.H_kv;
-  return 2 * align256(evict_slots(a) * 4) + align256(heads * 4) + align256(heads * 8);
+  return 2 * align256(evict_slots(a) * 4) + align256(heads * 4);
 }
 
 }  // namespace
@@ -360,11 +360,10 @@ int fa_cache_evict(const fa_cache_evict_args* a) {
   p.keep = a->keep;
   p.recent = a->recent;
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
-  const long long slots = align256(evict_slots(a) * 4), heads = (long long)a->B * a->cache.H_kv;
+  const long long slots = align256(evict_slots(a) * 4);
   p.src = reinterpret_cast<int*>(ws);
   p.mover = reinterpret_cast<int*>(ws + slots);
   p.count = reinterpret_cast<int*>(ws + 2 * slots);
-  p.edge = reinterpret_cast<float*>(ws + 2 * slots + align256(heads * 4));
   return launch_cache_evict(p, a->cache.kind, {static_cast<cudaStream_t>(a->stream), dev.num_sms, dev.dev, dev.max_ctas});
 }
 

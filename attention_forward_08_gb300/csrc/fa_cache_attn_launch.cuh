@@ -7,6 +7,7 @@
 #include "fa.h"
 #include "fa_cache.h"
 #include "fa_cache_decode.cuh"
+#include "fa_cache_launch.cuh"
 #include "fa_cache_prompt.cuh"
 #include "fa_cache_weights.cuh"
 #include "fa_cache_maps.h"
@@ -38,44 +39,17 @@ bool line_params(DecParams& p, const CacheAttnParams& a, int max_ctas, const Lau
   return true;
 }
 
-// Once per kernel and device: its shared memory.
-template <class K>
-bool allow_smem(K kern, int bytes, int dev, std::atomic<unsigned long long>& configured) {
-  if ((configured.load(std::memory_order_acquire) >> dev) & 1ull) return true;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) {
-    set_error("cudaFuncSetAttribute(max dynamic smem = %d): %s", bytes, cudaGetErrorString(e));
-    return false;
-  }
-  configured.fetch_or(1ull << dev, std::memory_order_release);
-  return true;
-}
 
 // Rows of a K/V head behind which a call is a prompt's.
 template <int kD>
 constexpr int kPromptRows = 64;
 
-// Programmatic launch: the blocks come up while the kernel before ends, and
-// wait for it (griddepcontrol.wait) before they read what it wrote.
-template <class P>
-cudaError_t launch_after(void (*kern)(P), dim3 grid, unsigned threads, cudaStream_t stream, const P& p) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
-}
 
 // The accumulated weights, after the attention; workspace behind `used` bytes.
 template <int kD>
 long long weights_workspace(const CacheAttnParams& a) {
   const long long groups = (long long)a.B * a.c.H * ((a.n * (long long)a.group + 15) / 16);
-  return a.weights ? groups * 16 * (kD * 2 + 8) : 0;
+  return a.weights && a.n * (long long)a.group > 16 ? groups * 16 * (kD * 2 + 8) : 0;
 }
 template <int kD>
 int launch_weights(const CacheAttnParams& a, int kind, bool f16, long long used, const LaunchCtx& ctx) {
@@ -113,8 +87,18 @@ int launch_decode(const CacheAttnParams& a, const LaunchCtx& ctx) {
   if (!line_params<C>(p, a, ctx.num_sms * C::kCtas, ctx)) return FA_ERR_UNSUPPORTED;
   kern<<<p.max_ctas, C::kThreads, C::kSmem, ctx.stream>>>(tk, tv, p);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && p.max_ctas > 1)
+  if (e == cudaSuccess && a.weights && C::kMT == 1 && p.row_groups == 1) {
+    const int joins = (p.max_ctas - 1) * (C::kRows * C::kD / 512);
+    const long long chunks = ((long long)a.c.M * a.c.page + 127) / 128;
+    if (chunks * a.c.H * a.B > 0x7fffffffLL - joins) {
+      set_error("B * H_kv * table width (%lld tokens) is beyond the weights' index range", (long long)a.c.M * a.c.page);
+      return FA_ERR_UNSUPPORTED;
+    }
+    e = launch_after(cache_finish_kernel<C>, dim3((unsigned)(joins + chunks * a.c.H * a.B)), 128, ctx.stream, p, joins,
+                     (int)chunks);
+  } else if (e == cudaSuccess && p.max_ctas > 1) {
     e = launch_after(cache_join_kernel<C>, dim3(C::kRows * C::kD / 512, (unsigned)p.max_ctas - 1), 128, ctx.stream, p);
+  }
   if (e != cudaSuccess) {
     set_error("cache attention launch failed: %s", cudaGetErrorString(e));
     return FA_ERR_CUDA;
@@ -192,7 +176,8 @@ int launch_attn_d(const CacheAttnParams& a, int kind, bool f16, const LaunchCtx&
     rc = f16 ? launch_plan<kD, kKindE4m3, true>(a, ctx) : launch_plan<kD, kKindE4m3, false>(a, ctx);
   else
     rc = f16 ? launch_plan<kD, kKindInt8, true>(a, ctx) : launch_plan<kD, kKindInt8, false>(a, ctx);
-  if (rc != FA_OK || !a.weights) return rc;
+  // (16 rows at most: cache_finish_kernel has weighed the tokens)
+  if (rc != FA_OK || !a.weights || a.n * (long long)a.group <= 16) return rc;
   return launch_weights<kD>(a, kind, f16, plan_workspace<kD>(a, ctx.num_sms), ctx);
 }
 

@@ -204,18 +204,39 @@ __device__ __forceinline__ void dec_write(const CacheAttnParams& a, int b, int h
   if (d == 0) a.lse[((long long)b * a.Hq + head) * a.n + i] = sum > 0.0f ? (top + lg2(sum)) * kDecLn2 : -INFINITY;
 }
 
-// Joins the parts of a cut segment: the block of the first cut inside it sums
-// them, in order, four columns of a row a thread.
+// The line's length, and the first tile (seg0) of sequence b; one row group.
 template <class C>
-__global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__ DecParams p) {
+__device__ __forceinline__ DecPlace dec_before(const DecParams& p, int b) {
+  const int lane = threadIdx.x & 31;
+  int all = 0, lower = 0;
+#pragma unroll 1
+  for (int i = lane; i < p.a.B; i += 32) {
+    const int n = dec_tiles<C>(p, dec_seq(p.a, i), 0) * p.a.c.H;
+    all += n;
+    if (i < b) lower += n;
+  }
+  DecPlace at;
+  at.total = __reduce_add_sync(0xFFFFFFFFu, all);
+  at.part = dec_part<C>(p, at.total);
+  at.b = b;
+  at.h = at.rg = 0;
+  at.seg0 = __reduce_add_sync(0xFFFFFFFFu, lower);
+  return at;
+}
+
+// Joins the parts of a cut segment: the block of the first cut inside it sums
+// them, in order, four columns of a row a thread (128 threads: 512 / D rows,
+// `piece` of the segment's).
+template <class C>
+__device__ __forceinline__ void join_parts(const DecParams& p, int piece, int cut) {
   const CacheAttnParams& a = p.a;
   constexpr int kRowsHere = 512 / C::kD;  // rows a block
-  const int tid = threadIdx.x, cut = blockIdx.y + 1;
+  const int tid = threadIdx.x;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   DecPlace at;
   const bool in = dec_find<C>(p, cut, at);
   const int t = at.part * cut;
-  const int r = blockIdx.x * kRowsHere + tid / (C::kD / 4), row = at.rg * C::kRows + r, d = tid % (C::kD / 4) * 4;
+  const int r = piece * kRowsHere + tid / (C::kD / 4), row = at.rg * C::kRows + r, d = tid % (C::kD / 4) * 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
   if (!in || at.seg0 == t || at.seg0 < t - at.part || row >= p.rows) return;
   const int c1 = (at.seg0 + dec_tiles<C>(p, at.seq, at.rg) - 1) / at.part;
@@ -233,6 +254,10 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
     x.x = fmaf(x.x, f, y.x * g), x.y = fmaf(x.y, f, y.y * g), x.z = fmaf(x.z, f, y.z * g), x.w = fmaf(x.w, f, y.w * g);
   }
   dec_write<C>(a, at.b, at.h, row, d, x, top, sum);
+}
+template <class C>
+__global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__ DecParams p) {
+  join_parts<C>(p, blockIdx.x, blockIdx.y + 1);
 }
 
 }  // namespace fa

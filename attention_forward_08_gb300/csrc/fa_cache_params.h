@@ -64,8 +64,7 @@ struct EvictParams {
   // Workspace: what the choice tells the moves.
   int* src;         // [B, H, keep]: the slot whose token ends in slot j; -1 - i: that of mover i (in place)
   int* mover;       // [B, H, keep]: kept slots at `keep` and behind, in order (in place)
-  int* count;       // [B, H]: tokens kept; -1 - n: all n stay in place
-  float* edge;      // [B, H, 2]: scales, before the call, of the block that holds slot `keep`
+  int* count;       // [B, H]: tokens kept
 };
 
 struct LaunchCtx {

@@ -68,23 +68,21 @@ __global__ void __launch_bounds__(256) cache_rows_kernel(const __grid_constant__
   }
 }
 
-template <int kKind, int kD>
-__global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constant__ WeightParams p) {
-  const CacheAttnParams& a = p.a;
+// The weights of 32 tokens of a head, by one warp.  `q` (A operands) and `row`
+// hold the row groups' rows, in shared memory (kShared: one group) or global;
+// ready() returns once they are there, and is called with the keys on their way.
+template <int kKind, int kD, bool kShared, class Ready>
+__device__ __forceinline__ void weigh_tokens(const CacheAttnParams& a, const DecSeq& seq, int b, int h, int tok0,
+                                             const uint4* q, const float2* row, Ready ready) {
   const CacheView& c = a.c;
   constexpr int kK = kD / 16;  // k-steps
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int h = blockIdx.y, b = blockIdx.z, tok0 = (blockIdx.x * 4 + warp) * 32;
-  const DecSeq seq = dec_seq(a, b);
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   // the query rows that see one of these tokens
   int i0 = 0, i1 = seq.nq - 1;
   const int pos0 = seq.len - seq.nq;
   if (a.causal) i0 = max(0, tok0 - pos0);
   if (a.window > 0) i1 = (int)min((long long)i1, (long long)tok0 + 31 + a.window - 1 - pos0);
-  if (tok0 >= seq.len || i0 > i1) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // a grid ends no earlier than the one before it
-    return;
-  }
+  const bool none = tok0 >= seq.len || i0 > i1;
   const int rg0 = i0 * a.group / 16, rg1 = (i1 * a.group + a.group - 1) / 16;
 
   // keys: lane (g, t) holds the bytes of token 8j + g that it multiplies
@@ -95,7 +93,7 @@ __global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constan
   for (int half = 0; half < 2; ++half) {
     const int tok = tok0 + 16 * half;
     int blk = -1;
-    if (tok < seq.len) blk = checked_block(c, c.table, c.table_stride, b, tok >> c.page_log2);
+    if (!none && tok < seq.len) blk = checked_block(c, c.table, c.table_stride, b, tok >> c.page_log2);
     here[half] = blk >= 0;
     ks[half] = here[half] ? __ldg(c.k_scale + (long long)blk * c.H + h) : 0.0f;
 #pragma unroll
@@ -110,10 +108,8 @@ __global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constan
       }
     }
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows are there
-  const long long bh = (long long)b * c.H + h;
-  const uint4* q = reinterpret_cast<const uint4*>(p.q) + bh * p.row_groups * kK * 32 + lane;
-  const float2* row = p.row + bh * p.row_groups * 16;
+  ready();
+  if (none) return;
   const bool raw = a.cap_out == 0.0f;
   float sum[4][2] = {};
 #pragma unroll 1
@@ -121,7 +117,7 @@ __global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constan
     float sc[4][4] = {};
 #pragma unroll
     for (int kk = 0; kk < kK; ++kk) {
-      const uint4 x = __ldcg(q + ((long long)rg * kK + kk) * 32);
+      const uint4 x = kShared ? q[kk * 32 + lane] : __ldcg(q + ((long long)rg * kK + kk) * 32 + lane);
       const uint32_t qa[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -130,7 +126,7 @@ __global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constan
         mma_f16(sc[j], qa, b0, b1);
       }
     }
-    const float2 r0 = __ldcg(row + rg * 16 + g), r1 = __ldcg(row + rg * 16 + g + 8);
+    const float2 r0 = kShared ? row[g] : __ldcg(row + rg * 16 + g), r1 = kShared ? row[g + 8] : __ldcg(row + rg * 16 + g + 8);
     const int ia = (rg * 16 + g) / a.group, ib = (rg * 16 + g + 8) / a.group;
     // tokens that rows g and g + 8 see (a row that is none has L2 = +inf)
     const int2 va = dec_span(a, seq, ia, ia), vb = dec_span(a, seq, ib, ib);
@@ -155,7 +151,7 @@ __global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constan
       for (int o = 4; o < 32; o <<= 1) sum[j][e] += __shfl_xor_sync(0xFFFFFFFFu, sum[j][e], o);
     }
   if (g == 0) {
-    float* out = a.weights + bh * a.W;
+    float* out = a.weights + ((long long)b * c.H + h) * a.W;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -168,6 +164,102 @@ __global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constan
           out[tok] += sum[j][e];
       }
   }
+}
+
+// Many rows: their operands come from cache_rows_kernel.
+template <int kKind, int kD>
+__global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constant__ WeightParams p) {
+  const CacheAttnParams& a = p.a;
+  const int h = blockIdx.y, b = blockIdx.z, tok0 = (blockIdx.x * 4 + (threadIdx.x >> 5)) * 32;
+  const long long bh = (long long)b * a.c.H + h;
+  weigh_tokens<kKind, kD, false>(a, dec_seq(a, b), b, h, tok0,
+                                 reinterpret_cast<const uint4*>(p.q) + bh * p.row_groups * (kD / 16) * 32,
+                                 p.row + bh * p.row_groups * 16, [] {
+                                   // (by every block, also one that has nothing to do: a grid
+                                   // ends no earlier than the one before it)
+                                   asm volatile("griddepcontrol.wait;" ::: "memory");
+                                 });
+}
+
+// At most 16 rows (the decoding step): one kernel joins the parts of cut
+// segments (its first `joins` blocks) and weighs the tokens; a block brings its
+// head's rows into the tensor core's order itself, and finds their L where the
+// parts say so (every block that needs an L sums it up from the parts: a few
+// numbers a row).
+template <class C>
+__global__ void __launch_bounds__(128) cache_finish_kernel(const __grid_constant__ DecParams p, int joins, int chunks) {
+  const CacheAttnParams& a = p.a;
+  constexpr int kD = C::kD, kE = kD / 32;
+  if ((int)blockIdx.x < joins) {
+    join_parts<C>(p, blockIdx.x % (C::kRows * kD / 512), blockIdx.x / (C::kRows * kD / 512) + 1);
+    return;
+  }
+  __shared__ uint4 s_q[kD / 16 * 32];
+  __shared__ float2 s_row[16];
+  const int nth = blockIdx.x - joins, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int h = nth / chunks % a.c.H, b = nth / chunks / a.c.H, tok0 = (nth % chunks * 4 + warp) * 32;
+  const DecSeq seq = dec_seq(a, b);
+  if ((nth % chunks) * 128 >= seq.len) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+#pragma unroll 1
+  for (int r = warp; r < 16; r += 4) {
+    const int i = r / a.group, head = h * a.group + r % a.group;
+    float f[kE], up = 1.0f, down = 1.0f;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) f[e] = 0.0f;
+    if (r < p.rows) {
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + b * a.qs[0] +
+                                                            head * a.qs[1] + i * a.qs[2]) + lane * (kE / 2);
+#pragma unroll
+      for (int e = 0; e < kE; e += 2) {
+        const uint32_t w = __ldg(q + e / 2);
+        f[e] = half_bits_to_f32<C::kF16>(w);
+        f[e + 1] = half_bits_to_f32<C::kF16>(w >> 16);
+      }
+    }
+    if constexpr (!C::kF16) {
+      float top = 0.0f;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) top = fmaxf(top, fabsf(f[e]));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      dec_row_scale(top, up, down);
+    }
+#pragma unroll
+    for (int e = 0; e < kE; e += 2)
+      reinterpret_cast<uint32_t*>(s_q)[dec_q_word<kD>(r, lane * kE + e)] = pack_f16x2(f[e] * up, f[e + 1] * up);
+    if (lane == 0) s_row[r].x = down;
+  }
+  const DecPlace at = dec_before<C>(p, b);
+  const int u0 = at.seg0 + h * dec_tiles<C>(p, seq, 0), u1 = u0 + dec_tiles<C>(p, seq, 0);
+  const int c0 = u0 / at.part, c1 = (u1 - 1) / at.part;
+  weigh_tokens<C::kKind, kD, true>(a, seq, b, h, tok0, s_q, s_row, [&] {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts, and the L of whole segments, are written
+    if (warp == 0 && lane < 16) {
+      float l2 = INFINITY;  // a row that sees nothing
+      if (lane < p.rows) {
+        float top = -INFINITY, sum = 0.0f;
+        if (c0 == c1) {
+          const int i = lane / a.group, head = h * a.group + lane % a.group;
+          top = __ldcg(a.lse + ((long long)b * a.Hq + head) * a.n + i) * kLog2eF;
+          sum = 1.0f;
+        } else {
+  #pragma unroll 4
+          for (int i = c0; i <= c1; ++i) {
+            const float2 ml = __ldcg(p.part_ml + (long long)(2 * i + (i == c0)) * C::kRows + lane);
+            const float m2 = fmaxf(top, ml.x), z = m2 == -INFINITY ? 0.0f : m2;
+            sum = fmaf(sum, ex2(top - z), ml.y * ex2(ml.x - z));
+            top = m2;
+          }
+        }
+        if (top > -INFINITY && sum > 0.0f) l2 = top + lg2(sum);
+      }
+      s_row[lane].y = l2;
+    }
+    __syncthreads();
+  });
 }
 
 }  // namespace fa

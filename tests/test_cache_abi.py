@@ -173,10 +173,10 @@ def test_null_args(fa):
 
 
 def test_evict_workspace_size(fa):
-    """Slots named per head twice (4 bytes each), a count and two scales per head."""
+    """Slots named per head twice (4 bytes each), and a count per head."""
     up = lambda x: -(-x // 256) * 256  # noqa: E731
     a = args_of(fa, "evict", B=3, keep=100, table_stride=4)
-    assert fa.fa_cache_evict_workspace_bytes(a) == 2 * up(3 * 2 * 100 * 4) + up(3 * 2 * 4) + up(3 * 2 * 8)
+    assert fa.fa_cache_evict_workspace_bytes(a) == 2 * up(3 * 2 * 100 * 4) + up(3 * 2 * 4)
 
 
 def test_python_refuses_cpu_tensors_and_bad_pools(fa):
