@@ -35,6 +35,7 @@ bool line_params(DecParams& p, const CacheAttnParams& a, int max_ctas, const Lau
   }
   p.part_o = reinterpret_cast<float*>(a.ws);
   p.part_ml = reinterpret_cast<float2*>(a.ws + 2LL * max_ctas * C::kRows * C::kD * 4);
+  p.scores = nullptr;
   p.max_ctas = ctx.max_ctas > 0 && ctx.max_ctas < max_ctas ? ctx.max_ctas : max_ctas;
   return true;
 }
@@ -45,11 +46,27 @@ template <int kD>
 constexpr int kPromptRows = 64;
 
 
-// The accumulated weights, after the attention; workspace behind `used` bytes.
+// With weights and one group of decode rows, the decode kernel keeps its
+// scores, unless a wide table would make them large (they take 4 bytes a row
+// for every token that the table could hold; the keys are then read twice):
+// 16 sequences of up to 4096 tokens, H 32/8, D 128: TIMES.
+constexpr long long kMostScores = 256LL << 20;
+inline long long score_bytes(const CacheAttnParams& a) {
+  return (long long)a.B * a.c.H * (((long long)a.c.M * a.c.page + 31) / 32) * a.n * a.group * 128;
+}
+template <int kD>
+bool keep_scores(const CacheAttnParams& a) {
+  return a.weights && (long long)a.n * a.group <= (kD <= 128 ? 32 : 16) &&
+         (double)a.B * a.c.H * a.c.M * a.c.page * a.n * a.group * 4 <= (double)kMostScores;
+}
+
+// Workspace of the accumulated weights, behind the attention's own.
 template <int kD>
 long long weights_workspace(const CacheAttnParams& a) {
+  if (!a.weights) return 0;
+  if (keep_scores<kD>(a)) return score_bytes(a);
   const long long groups = (long long)a.B * a.c.H * ((a.n * (long long)a.group + 15) / 16);
-  return a.weights && a.n * (long long)a.group > 16 ? groups * 16 * (kD * 2 + 8) : 0;
+  return groups * 16 * (kD * 2 + 8);
 }
 template <int kD>
 int launch_weights(const CacheAttnParams& a, int kind, bool f16, long long used, const LaunchCtx& ctx) {
@@ -85,11 +102,12 @@ int launch_decode(const CacheAttnParams& a, const LaunchCtx& ctx) {
   DecParams p;
   if (!allow_smem(kern, C::kSmem, ctx.dev, configured)) return FA_ERR_CUDA;
   if (!line_params<C>(p, a, ctx.num_sms * C::kCtas, ctx)) return FA_ERR_UNSUPPORTED;
+  if (keep_scores<C::kD>(a)) p.scores = reinterpret_cast<float*>(a.ws + line_workspace<C>(ctx.num_sms * C::kCtas));
   kern<<<p.max_ctas, C::kThreads, C::kSmem, ctx.stream>>>(tk, tv, p);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && a.weights && C::kMT == 1 && p.row_groups == 1) {
+  if (e == cudaSuccess && p.scores) {
     const int joins = (p.max_ctas - 1) * (C::kRows * C::kD / 512);
-    const long long chunks = ((long long)a.c.M * a.c.page + 127) / 128;
+    const long long chunks = ((long long)a.c.M * a.c.page + kFinishTokens - 1) / kFinishTokens;
     if (chunks * a.c.H * a.B > 0x7fffffffLL - joins) {
       set_error("B * H_kv * table width (%lld tokens) is beyond the weights' index range", (long long)a.c.M * a.c.page);
       return FA_ERR_UNSUPPORTED;
@@ -176,8 +194,7 @@ int launch_attn_d(const CacheAttnParams& a, int kind, bool f16, const LaunchCtx&
     rc = f16 ? launch_plan<kD, kKindE4m3, true>(a, ctx) : launch_plan<kD, kKindE4m3, false>(a, ctx);
   else
     rc = f16 ? launch_plan<kD, kKindInt8, true>(a, ctx) : launch_plan<kD, kKindInt8, false>(a, ctx);
-  // (16 rows at most: cache_finish_kernel has weighed the tokens)
-  if (rc != FA_OK || !a.weights || a.n * (long long)a.group <= 16) return rc;
+  if (rc != FA_OK || !a.weights || keep_scores<kD>(a)) return rc;
   return launch_weights<kD>(a, kind, f16, plan_workspace<kD>(a, ctx.num_sms), ctx);
 }
 

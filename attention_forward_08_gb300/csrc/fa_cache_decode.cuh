@@ -460,6 +460,21 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           }
         }
         const bool move = __any_sync(0xFFFFFFFFu, grow);
+        if (p.scores) {  // for cache_finish_kernel: 8 neighbouring tokens of a row a quad
+          float* out = p.scores + (((long long)b * c.H + h) * ((c.M * (c.page >> 4) + 1) / 2) + (tok0 >> 5)) * p.rows * 32 + 2 * t;
+#pragma unroll
+          for (int mt = 0; mt < C::kMT; ++mt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int r = mt * 16 + g + 8 * x;
+              if (r < p.rows) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  __stcg(reinterpret_cast<float2*>(out + r * 32 + 8 * j),
+                         make_float2(sc[mt][j][2 * x] * fa[mt][x][j >> 1], sc[mt][j][2 * x + 1] * fa[mt][x][j >> 1]));
+              }
+            }
+        }
         // Two halves of 16 tokens, each inside one block: O in that block's units.
 #pragma unroll
         for (int half = 0; half < 2; ++half) {

@@ -28,6 +28,7 @@ struct DecParams {
   int max_ctas;
   float* part_o;          // [2 * max_ctas, kRows, D]
   float2* part_ml;        // [2 * max_ctas, kRows]: maximum, sum
+  float* scores;          // [B, H, M * page / 32, rows, 32]: scores in base 2, for the weights (or NULL)
 };
 
 struct DecSeq {

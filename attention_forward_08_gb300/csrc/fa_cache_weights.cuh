@@ -3,17 +3,17 @@
 //   weights[b, kvh, j] += sum over rows r of the K/V head of 2^(s_rj - L2_r)
 //
 // with L2 the row's logsumexp in base 2, known once the attention itself has
-// run.  A warp owns 32 tokens, holds their keys in registers and goes over the
-// rows, 16 at a time; sums stay in its lanes, so that nothing is added twice
-// or in an order that changes.  Scores are computed again from the keys: to
-// keep them would take 4 bytes a row and token (and a workspace as wide as
-// the table), while a key is 1 byte an element for all rows of its head.
+// run.  Few rows: the attention leaves its scores, and cache_finish_kernel
+// sums them up.  Many: a warp owns 32 tokens, holds their keys in registers,
+// computes each score again and goes over the rows, 16 at a time (to keep the
+// scores would take 4 bytes a row and token, while a key is 1 byte an element
+// for all rows of its head); the query rows are brought into the tensor core's
+// order once, by a small kernel before it, together with each row's two
+// factors.  Either way sums stay in one thread, so that nothing is added twice
+// or in an order that changes.
 //
-// The query rows are brought into the tensor core's order once, by a small
-// kernel before this one, together with each row's two factors.
-//
-// Bound: the second reading of K (from L2 where it still is there) for few
-// rows, the tensor cores for many.
+// Bound: the scores' way through L2 for few rows; the second reading of K and
+// the tensor cores for many.
 #pragma once
 
 #include "fa_cache_decode.cuh"
@@ -68,13 +68,15 @@ __global__ void __launch_bounds__(256) cache_rows_kernel(const __grid_constant__
   }
 }
 
-// The weights of 32 tokens of a head, by one warp.  `q` (A operands) and `row`
-// hold the row groups' rows, in shared memory (kShared: one group) or global;
-// ready() returns once they are there, and is called with the keys on their way.
-template <int kKind, int kD, bool kShared, class Ready>
-__device__ __forceinline__ void weigh_tokens(const CacheAttnParams& a, const DecSeq& seq, int b, int h, int tok0,
-                                             const uint4* q, const float2* row, Ready ready) {
+template <int kKind, int kD>
+__global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constant__ WeightParams p) {
+  const CacheAttnParams& a = p.a;
   const CacheView& c = a.c;
+  const int h = blockIdx.y, b = blockIdx.z, tok0 = (blockIdx.x * 4 + (threadIdx.x >> 5)) * 32;
+  const long long bh = (long long)b * c.H + h;
+  const DecSeq seq = dec_seq(a, b);
+  const uint4* q = reinterpret_cast<const uint4*>(p.q) + bh * p.row_groups * (kD / 16) * 32;
+  const float2* row = p.row + bh * p.row_groups * 16;
   constexpr int kK = kD / 16;  // k-steps
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   // the query rows that see one of these tokens
@@ -108,7 +110,9 @@ __device__ __forceinline__ void weigh_tokens(const CacheAttnParams& a, const Dec
       }
     }
   }
-  ready();
+  // The rows are there (every block waits, also one that has nothing to do: a
+  // grid ends no earlier than the one before it).
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (none) return;
   const bool raw = a.cap_out == 0.0f;
   float sum[4][2] = {};
@@ -117,7 +121,7 @@ __device__ __forceinline__ void weigh_tokens(const CacheAttnParams& a, const Dec
     float sc[4][4] = {};
 #pragma unroll
     for (int kk = 0; kk < kK; ++kk) {
-      const uint4 x = kShared ? q[kk * 32 + lane] : __ldcg(q + ((long long)rg * kK + kk) * 32 + lane);
+      const uint4 x = __ldcg(q + ((long long)rg * kK + kk) * 32 + lane);
       const uint32_t qa[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -126,7 +130,7 @@ __device__ __forceinline__ void weigh_tokens(const CacheAttnParams& a, const Dec
         mma_f16(sc[j], qa, b0, b1);
       }
     }
-    const float2 r0 = kShared ? row[g] : __ldcg(row + rg * 16 + g), r1 = kShared ? row[g + 8] : __ldcg(row + rg * 16 + g + 8);
+    const float2 r0 = __ldcg(row + rg * 16 + g), r1 = __ldcg(row + rg * 16 + g + 8);
     const int ia = (rg * 16 + g) / a.group, ib = (rg * 16 + g + 8) / a.group;
     // tokens that rows g and g + 8 see (a row that is none has L2 = +inf)
     const int2 va = dec_span(a, seq, ia, ia), vb = dec_span(a, seq, ib, ib);
@@ -166,100 +170,63 @@ __device__ __forceinline__ void weigh_tokens(const CacheAttnParams& a, const Dec
   }
 }
 
-// Many rows: their operands come from cache_rows_kernel.
-template <int kKind, int kD>
-__global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constant__ WeightParams p) {
-  const CacheAttnParams& a = p.a;
-  const int h = blockIdx.y, b = blockIdx.z, tok0 = (blockIdx.x * 4 + (threadIdx.x >> 5)) * 32;
-  const long long bh = (long long)b * a.c.H + h;
-  weigh_tokens<kKind, kD, false>(a, dec_seq(a, b), b, h, tok0,
-                                 reinterpret_cast<const uint4*>(p.q) + bh * p.row_groups * (kD / 16) * 32,
-                                 p.row + bh * p.row_groups * 16, [] {
-                                   // (by every block, also one that has nothing to do: a grid
-                                   // ends no earlier than the one before it)
-                                   asm volatile("griddepcontrol.wait;" ::: "memory");
-                                 });
-}
+// Few rows (one row group of the decode kernel's): that kernel has left its
+// scores, 4 bytes a row and token, and one kernel joins the parts of cut
+// segments (its first `joins` blocks) and sums the weights, a thread a token.
+// A block finds the rows' L where the parts say so: a few numbers a row.
+constexpr int kFinishTokens = 512;  // a block
 
-// At most 16 rows (the decoding step): one kernel joins the parts of cut
-// segments (its first `joins` blocks) and weighs the tokens; a block brings its
-// head's rows into the tensor core's order itself, and finds their L where the
-// parts say so (every block that needs an L sums it up from the parts: a few
-// numbers a row).
 template <class C>
 __global__ void __launch_bounds__(128) cache_finish_kernel(const __grid_constant__ DecParams p, int joins, int chunks) {
   const CacheAttnParams& a = p.a;
-  constexpr int kD = C::kD, kE = kD / 32;
+  constexpr int kPieces = C::kRows * C::kD / 512;
   if ((int)blockIdx.x < joins) {
-    join_parts<C>(p, blockIdx.x % (C::kRows * kD / 512), blockIdx.x / (C::kRows * kD / 512) + 1);
+    join_parts<C>(p, blockIdx.x % kPieces, blockIdx.x / kPieces + 1);
     return;
   }
-  __shared__ uint4 s_q[kD / 16 * 32];
-  __shared__ float2 s_row[16];
-  const int nth = blockIdx.x - joins, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = nth / chunks % a.c.H, b = nth / chunks / a.c.H, tok0 = (nth % chunks * 4 + warp) * 32;
+  __shared__ float s_l2[C::kRows];
+  const int nth = blockIdx.x - joins, tid = threadIdx.x;
+  const int bh = nth / chunks, h = bh % a.c.H, b = bh / a.c.H, tok0 = nth % chunks * kFinishTokens;
   const DecSeq seq = dec_seq(a, b);
-  if ((nth % chunks) * 128 >= seq.len) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    return;
-  }
-#pragma unroll 1
-  for (int r = warp; r < 16; r += 4) {
-    const int i = r / a.group, head = h * a.group + r % a.group;
-    float f[kE], up = 1.0f, down = 1.0f;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) f[e] = 0.0f;
-    if (r < p.rows) {
-      const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + b * a.qs[0] +
-                                                            head * a.qs[1] + i * a.qs[2]) + lane * (kE / 2);
-#pragma unroll
-      for (int e = 0; e < kE; e += 2) {
-        const uint32_t w = __ldg(q + e / 2);
-        f[e] = half_bits_to_f32<C::kF16>(w);
-        f[e + 1] = half_bits_to_f32<C::kF16>(w >> 16);
-      }
-    }
-    if constexpr (!C::kF16) {
-      float top = 0.0f;
-#pragma unroll
-      for (int e = 0; e < kE; ++e) top = fmaxf(top, fabsf(f[e]));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-      dec_row_scale(top, up, down);
-    }
-#pragma unroll
-    for (int e = 0; e < kE; e += 2)
-      reinterpret_cast<uint32_t*>(s_q)[dec_q_word<kD>(r, lane * kE + e)] = pack_f16x2(f[e] * up, f[e + 1] * up);
-    if (lane == 0) s_row[r].x = down;
-  }
+  const int2 span = dec_group_span<C>(p, seq, 0);
   const DecPlace at = dec_before<C>(p, b);
-  const int u0 = at.seg0 + h * dec_tiles<C>(p, seq, 0), u1 = u0 + dec_tiles<C>(p, seq, 0);
+  const int tiles = dec_tiles<C>(p, seq, 0), u0 = at.seg0 + h * tiles, u1 = u0 + tiles;
   const int c0 = u0 / at.part, c1 = (u1 - 1) / at.part;
-  weigh_tokens<C::kKind, kD, true>(a, seq, b, h, tok0, s_q, s_row, [&] {
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts, and the L of whole segments, are written
-    if (warp == 0 && lane < 16) {
-      float l2 = INFINITY;  // a row that sees nothing
-      if (lane < p.rows) {
-        float top = -INFINITY, sum = 0.0f;
-        if (c0 == c1) {
-          const int i = lane / a.group, head = h * a.group + lane % a.group;
-          top = __ldcg(a.lse + ((long long)b * a.Hq + head) * a.n + i) * kLog2eF;
-          sum = 1.0f;
-        } else {
-  #pragma unroll 4
-          for (int i = c0; i <= c1; ++i) {
-            const float2 ml = __ldcg(p.part_ml + (long long)(2 * i + (i == c0)) * C::kRows + lane);
-            const float m2 = fmaxf(top, ml.x), z = m2 == -INFINITY ? 0.0f : m2;
-            sum = fmaf(sum, ex2(top - z), ml.y * ex2(ml.x - z));
-            top = m2;
-          }
-        }
-        if (top > -INFINITY && sum > 0.0f) l2 = top + lg2(sum);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // scores, parts, and the L of whole segments are written
+  if (tok0 >= span.y || tok0 + kFinishTokens <= span.x) return;
+  if (tid < p.rows) {
+    float top = -INFINITY, sum = 0.0f;
+    if (c0 == c1) {
+      const int i = tid / a.group, head = h * a.group + tid % a.group;
+      top = __ldcg(a.lse + ((long long)b * a.Hq + head) * a.n + i) * kLog2eF;
+      sum = 1.0f;
+    } else {
+#pragma unroll 4
+      for (int i = c0; i <= c1; ++i) {
+        const float2 ml = __ldcg(p.part_ml + (long long)(2 * i + (i == c0)) * C::kRows + tid);
+        const float m2 = fmaxf(top, ml.x), z = m2 == -INFINITY ? 0.0f : m2;
+        sum = fmaf(sum, ex2(top - z), ml.y * ex2(ml.x - z));
+        top = m2;
       }
-      s_row[lane].y = l2;
     }
-    __syncthreads();
-  });
+    s_l2[tid] = top > -INFINITY && sum > 0.0f ? top + lg2(sum) : INFINITY;  // (a row that sees nothing adds nothing)
+  }
+  __syncthreads();
+  const float* scores = p.scores + (long long)bh * ((a.c.M * (a.c.page >> 4) + 1) / 2) * p.rows * 32;
+  float* out = a.weights + (long long)bh * a.W;
+#pragma unroll
+  for (int i = 0; i < kFinishTokens / 128; ++i) {
+    const int tok = tok0 + i * 128 + tid;
+    if (tok < span.x || tok >= span.y) continue;
+    const float* s = scores + (long long)(tok >> 5) * p.rows * 32 + (tok & 31);
+    float sum = 0.0f;
+#pragma unroll 4
+    for (int r = 0; r < p.rows; ++r) sum += ex2(__ldcg(s + r * 32) - s_l2[r]);
+    if (tok < a.W)
+      out[tok] += sum;
+    else
+      flag_bad_index(a.c);
+  }
 }
 
 }  // namespace fa

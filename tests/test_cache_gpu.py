@@ -300,6 +300,22 @@ def test_full_machine(fa):
     attention_case(fa, Hq=32, Hkv=8, n=5, lens=(4000, 5000, 3001, 2500))
 
 
+@pytest.mark.parametrize("Hq,Hkv,n", [(16, 1, 1), (8, 2, 4), (4, 2, 40)])
+def test_wide_table(fa, Hq, Hkv, n):
+    """A table for 2^20 tokens of which a few are held: the tracked weights take their other way."""
+    g = torch.Generator().manual_seed(Hq)
+    lens, page, D = [300, 41], 64, 128
+    table, P, _ = R.make_table(g, lens, page, width=1 << 14)
+    pools = R.make_pools(g, P, Hkv, page, D, E4M3)
+    ref, cache = R.Cache(*pools), to_gpu(fa, pools)
+    q = torch.randn(2, Hq, n, D, generator=g).to(BF16)
+    w0 = torch.rand(2, Hkv, 310, generator=g)
+    w = w0.to(DEV)
+    got = fa.cache_attention(q.to(DEV), cache, i32(table), i32(lens), weights=w)
+    synced(fa)
+    check_attention(fa, ref, q, table, lens, got, w, w0)
+
+
 @pytest.mark.parametrize("n", [1, 5, 150])
 def test_attention_strided(fa, n):
     """Token-major q and output, pools interleaved, a table that is a slice of a wider one."""
