@@ -95,8 +95,10 @@ int launch_weights(const CacheAttnParams& a, int kind, bool f16, long long used,
 template <class C>
 int launch_decode(const CacheAttnParams& a, const LaunchCtx& ctx) {
   CUtensorMap tk, tv;
-  const int sub = a.c.page < C::kTile ? a.c.page : C::kTile;
-  if (!encode_pool(&tk, a.c, false, sub) || !encode_pool(&tv, a.c, true, sub)) return FA_ERR_CUDA;
+  if constexpr (C::kTma) {
+    const int rows = a.c.page < C::kTile ? a.c.page : C::kTile;
+    if (!encode_pool(&tk, a.c, false, rows) || !encode_pool(&tv, a.c, true, rows)) return FA_ERR_CUDA;
+  }
   auto kern = cache_decode_kernel<C>;
   static std::atomic<unsigned long long> configured{0};
   DecParams p;
@@ -170,9 +172,19 @@ long long plan_workspace(const CacheAttnParams& a, int num_sms) {
   switch (attn_plan<kD>(a)) {
     case AttnPlan::kPrompt: return line_workspace<PromptCfg<0, false, kD, 16>>(num_sms);
     case AttnPlan::kRows32:
-      if constexpr (kD <= 128) return line_workspace<DecCfg<0, false, kD, 2>>(num_sms * DecCfg<0, false, kD, 2>::kCtas);
-    default: return line_workspace<DecCfg<0, false, kD, 1>>(num_sms * DecCfg<0, false, kD, 1>::kCtas);
+      if constexpr (kD <= 128) return line_workspace<DecCfg<0, false, kD, 2, true>>(num_sms * DecCfg<0, false, kD, 2, true>::kCtas);
+    default: return line_workspace<DecCfg<0, false, kD, 1, true>>(num_sms * DecCfg<0, false, kD, 1, true>::kCtas);
   }
+}
+
+// TMA where a box holds 4 KB and more (16 sequences of 4608 tokens, 8 heads of
+// 64, blocks of 16: TIMES with boxes of 1 KB, TIMES with cp.async).
+template <int kD, int kKind, bool kF16, int kMT>
+int launch_decode_by(const CacheAttnParams& a, const LaunchCtx& ctx) {
+  if constexpr (kD >= 128) {
+    if (a.c.page >= 32) return launch_decode<DecCfg<kKind, kF16, kD, kMT, true>>(a, ctx);
+  }
+  return launch_decode<DecCfg<kKind, kF16, kD, kMT, false>>(a, ctx);
 }
 
 template <int kD, int kKind, bool kF16>
@@ -182,8 +194,8 @@ int launch_plan(const CacheAttnParams& a, const LaunchCtx& ctx) {
       return a.c.page >= 64 ? launch_prompt<PromptCfg<kKind, kF16, kD, 64>>(a, ctx)
                             : launch_prompt<PromptCfg<kKind, kF16, kD, 16>>(a, ctx);
     case AttnPlan::kRows32:
-      if constexpr (kD <= 128) return launch_decode<DecCfg<kKind, kF16, kD, 2>>(a, ctx);
-    default: return launch_decode<DecCfg<kKind, kF16, kD, 1>>(a, ctx);
+      if constexpr (kD <= 128) return launch_decode_by<kD, kKind, kF16, 2>(a, ctx);
+    default: return launch_decode_by<kD, kKind, kF16, 1>(a, ctx);
   }
 }
 

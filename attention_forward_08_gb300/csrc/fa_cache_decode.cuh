@@ -7,18 +7,24 @@
 // fp32 out), with an online softmax in base 2.  Nothing is lost on the way to
 // f16: stored values of both kinds are f16 numbers, and a bf16 query row is
 // scaled by a power of two so that its largest entry lies in [2^9, 2^10) (an
-// entry 2^-34 below that is lost at most).  A block's k_scale multiplies its
-// scores in fp32.  Its v_scale never touches a value: O is accumulated in the
-// units of the current block and multiplied by the ratio of the two scales
-// when a block with another one follows, together with the softmax's own
-// rescaling.  P is rounded to f16 (2^-11; the output has 2^-8 or 2^-11), its
-// sum is not.
+// entry 2^-34 below that is lost at most).  Over the 16 tokens of a step the
+// scales ks, vs are constant, and row i's weights are kept as
 //
-// Work.  A producer warp brings tiles of 32 tokens into a ring by TMA, with
-// their scales; the other warps take turns at the tiles, and each keeps a
+//   P'_ij = 2^(s_ij + log2 vs_j - m_i),   O = sum_j P'_ij v8_j / l_i,   l_i = sum_j P'_ij / vs_j
+//
+// with m_i the running maximum of s + log2 vs: v_scale costs an addition in
+// the exponent, and what counts most in O always has P' near 1, whatever the
+// scales of other blocks.  P' is rounded to f16 (2^-11; the output has 2^-8 or
+// 2^-11), the sums are not.
+//
+// Work.  A producer warp brings tiles of 32 tokens into a ring, with their
+// scales (two, one for K and one for V, where few wide tiles must keep the
+// memory busy); the other warps take turns at the tiles, and each keeps a
 // running maximum, sum and output of its own in registers, so that no barrier
-// stands between two tiles.  Tiles are shared out evenly over the machine
-// (fa_cache_line.cuh).
+// stands between two tiles.  The ring is filled by TMA where a tile's part of a
+// cache block is 4 KB and more, else by cp.async: a box costs its issuing
+// thread some 250 cycles whatever its size.  Tiles are shared out evenly over
+// the machine (fa_cache_line.cuh).
 //
 // Layout.  Neither product cares about the order of its summed index, nor
 // about the order of the columns it produces: lane (g, t) takes the bytes
@@ -34,8 +40,9 @@
 
 namespace fa {
 
-template <int kKind_, bool kF16_, int kD_, int kMT_>
+template <int kKind_, bool kF16_, int kD_, int kMT_, bool kTma_>
 struct DecCfg {
+  static constexpr bool kTma = kTma_;
   static constexpr int kKind = kKind_;
   static constexpr bool kF16 = kF16_;  // type of q and o
   static constexpr int kD = kD_, kMT = kMT_;
@@ -43,9 +50,9 @@ struct DecCfg {
   // Consumer warps a block, and blocks an SM: as many warps as the outputs
   // that each holds (kMT * D / 2 registers a lane) leave room for.
   static constexpr bool kWide = kMT * kD > 128;
-  static constexpr int kWarps = kD == 256 ? 6 : kWide ? 7 : 5;
+  static constexpr int kWarps = kWide ? 6 : 5, kProducers = kWide ? 2 : 1;
   static constexpr int kCtas = kWide ? 1 : 2;
-  static constexpr int kThreads = 32 * (kWarps + 1);        // and the producer warp
+  static constexpr int kThreads = 32 * (kWarps + kProducers);
   static constexpr int kCols = kD >= 128 ? kD / 128 : 1;    // 128-byte column blocks of a row
   static constexpr int kRowBytes = kD >= 128 ? 128 : 64;    // of one column block
   static constexpr int kTileBytes = kTile * kD;             // K; V alike
@@ -70,11 +77,12 @@ struct DecCfg {
   static constexpr int kSmem = 1024 + kOffTmp + 16;
 };
 
-// What a consumer needs beside a tile's bytes.
+// What a consumer needs beside a tile's bytes, for its two halves of 16
+// tokens: ks; log2 vs and 1 / vs (0 and 0 where values do not count: a zero
+// scale; 1 / vs is -1 where nothing is stored).
 struct DecMeta {
-  float ks[2], vs[2];  // scales of its two halves of 16 tokens
-  int ok[2];           // whether they are there
-  int pad[2];
+  float ks[2], lv[2], rv[2];
+  float pad[2];
 };
 
 // ------------------------------------------------------------------ tensor-core pieces
@@ -85,6 +93,15 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 16 bytes from the cache to shared memory; zeros if not `there`.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool there) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+// Arrive on `bar` once this thread's copies so far have landed.
+__device__ __forceinline__ void copy_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -183,13 +200,15 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   if (tid == 0) {
     for (int s = 0; s < kS; ++s) {
-      mbar_init(s_full + s, 1);
+      mbar_init(s_full + s, C::kProducers * (C::kTma ? 1 : 33));
       mbar_init(s_empty + s, 1);
     }
     fence_barrier_init();
     *s_abort = 0;
-    tma_prefetch_desc(&tk);
-    tma_prefetch_desc(&tv);
+    if constexpr (C::kTma) {
+      tma_prefetch_desc(&tk);
+      tma_prefetch_desc(&tv);
+    }
   }
 
   // The join kernel may take its place on the machine as soon as there is room.
@@ -216,8 +235,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     const int n_tiles = min(t1, at.seg0 + tiles) - pos;
     const bool whole = n_tiles == tiles;
 
-    if (warp == kW) {
+    if (warp >= kW) {
       // ---------------------------------------------------------- producer
+      const bool keys = C::kProducers == 1 || warp == kW, values = C::kProducers == 1 || warp > kW;
       // Parts of 32 tiles' (or 16) blocks at a time: lane l looks up part l's
       // block, one batch ahead, and writes its scales where the consumers of
       // tile k find them (entry k % 64: the ring is shorter than a batch, so
@@ -240,16 +260,20 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         const int blk = next_blk;
         float ks = 0.0f, vs = 0.0f;
         if (blk >= 0) {
-          ks = __ldg(c.k_scale + (long long)blk * c.H + h);
-          vs = __ldg(c.v_scale + (long long)blk * c.H + h);
+          if (keys) ks = __ldg(c.k_scale + (long long)blk * c.H + h);
+          if (values) vs = __ldg(c.v_scale + (long long)blk * c.H + h);
         }
         next_blk = look_up(k0 + per_batch);
         if (k0 + (lane >> shift) < n_tiles) {
           DecMeta* meta = s_meta + ((tile0 + k0 + (lane >> shift)) & 63);
-          meta->ks[sub_at] = ks;
-          meta->vs[sub_at] = vs;
-          meta->ok[sub_at] = blk >= 0;
-          if (subs == 1) meta->ks[1] = ks, meta->vs[1] = vs, meta->ok[1] = blk >= 0;
+          const bool counts = vs >= 1.17549435e-38f;
+          const float lv = counts ? lg2(vs) : 0.0f, rv = blk < 0 ? -1.0f : counts ? rcp_approx(vs) : 0.0f;
+          if (keys) meta->ks[sub_at] = ks;
+          if (values) meta->lv[sub_at] = lv, meta->rv[sub_at] = rv;
+          if (subs == 1) {
+            if (keys) meta->ks[1] = ks;
+            if (values) meta->lv[1] = lv, meta->rv[1] = rv;
+          }
         }
         __syncwarp();
         const int n = min(per_batch, n_tiles - k0);
@@ -261,26 +285,50 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
             ok = false;
             break;
           }
-          if (lane == 0) {
-            uint64_t* bar = s_full + stage;
-            uint8_t* dst = smem + stage * C::kStageBytes;
-            const int boxes = (b0 >= 0) + (b1 >= 0);
-            if (boxes == 0)
-              mbar_arrive(bar);
-            else
-              mbar_arrive_expect_tx(bar, (uint32_t)(boxes * sub * C::kD * 2));
+          uint64_t* bar = s_full + stage;
+          uint8_t* dst = smem + stage * C::kStageBytes;
+          if constexpr (C::kTma) {
+            if (lane == 0) {
+              const int boxes = (b0 >= 0) + (b1 >= 0);
+              if (boxes == 0)
+                mbar_arrive(bar);
+              else
+                mbar_arrive_expect_tx(bar, (uint32_t)(boxes * sub * C::kD * (3 - C::kProducers)));
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int from = u ? b1 : b0;
-              if (from >= 0) {
+              for (int u = 0; u < 2; ++u) {
+                const int from = u ? b1 : b0;
+                if (from >= 0) {
 #pragma unroll
-                for (int col = 0; col < C::kCols; ++col) {
-                  uint8_t* d = dst + (col * C::kTile + u * sub) * C::kRowBytes;
-                  tma_load_4d(d, &tk, bar, col * 128, y, h, from);
-                  tma_load_4d(d + C::kTileBytes, &tv, bar, col * 128, y, h, from);
+                  for (int col = 0; col < C::kCols; ++col) {
+                    uint8_t* d = dst + (col * C::kTile + u * sub) * C::kRowBytes;
+                    if (keys) tma_load_4d(d, &tk, bar, col * 128, y, h, from);
+                    if (values) tma_load_4d(d + C::kTileBytes, &tv, bar, col * 128, y, h, from);
+                  }
                 }
               }
             }
+          } else {
+            // 16-byte units, in the swizzle that a tensor map would give them
+            constexpr int kUnits = C::kRowBytes / 16, kRowsAtOnce = 32 / kUnits;
+            const int unit = lane % kUnits;
+            const uint32_t to = smem_u32(dst);
+#pragma unroll
+            for (int r0 = 0; r0 < C::kTile; r0 += kRowsAtOnce) {
+              const int r = r0 + lane / kUnits, from = subs == 2 && r >= 16 ? b1 : b0;
+              const int row = (y + r) & (c.page - 1);
+#pragma unroll
+              for (int col = 0; col < C::kCols; ++col) {
+                const uint32_t d = dec_unit<C>(to + col * C::kTile * C::kRowBytes, r, unit);
+                if (keys)
+                  copy16(d, c.k + max(from, 0) * c.ks[0] + h * c.ks[1] + row * c.ks[2] + col * 128 + unit * 16, from >= 0);
+                if (values)
+                  copy16(d + C::kTileBytes,
+                         c.v + max(from, 0) * c.vs[0] + h * c.vs[1] + row * c.vs[2] + col * 128 + unit * 16, from >= 0);
+              }
+            }
+            copy_arrive(bar);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);  // the scales
           }
           y = (y + C::kTile) & (c.page - 1);
           if (++stage == kS) stage = 0, phase ^= 1u;
@@ -343,7 +391,6 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       float m[C::kMT][2], l[C::kMT][2], rs[C::kMT][2];
       int hi_row[C::kMT][2], lo_row[C::kMT][2];  // the tokens that this lane's two rows see
       int lo_all = 0, hi_all = 0x7fffffff;       // ... that every row of the warp sees
-      float vs_unit = 1.0f;                      // O is in units of this scale
 #pragma unroll
       for (int mt = 0; mt < C::kMT; ++mt) {
 #pragma unroll
@@ -382,10 +429,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         const uint32_t tile_k = smem_u32(smem + stage * C::kStageBytes), tile_v = tile_k + C::kTileBytes;
         const int tok0 = (first_tile + k) * C::kTile;
         const DecMeta* meta_at = s_meta + ((tile0 + k) & 63);
-        const float4 meta = *reinterpret_cast<const float4*>(meta_at);
-        const int2 here = *reinterpret_cast<const int2*>(meta_at->ok);
-        const int ok_blk = here.x + 2 * here.y;
-        const bool full = ok_blk == 3 && lo_all <= tok0 && tok0 + C::kTile <= hi_all;
+        const float4 meta = *reinterpret_cast<const float4*>(meta_at);  // ks, ks, log2 vs, log2 vs
+        const float2 rv = *reinterpret_cast<const float2*>(meta_at->rv);
+        const bool full = rv.x >= 0.0f && rv.y >= 0.0f && lo_all <= tok0 && tok0 + C::kTile <= hi_all;
 
         // S = Q K^T: 4 column tiles of 8 tokens
         float sc[C::kMT][4][4];
@@ -413,7 +459,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           }
         }
 
-        // Masks, and the running maximum in base 2.
+        // Masks, and the running maximum of s + log2 vs in base 2.
         float fa[C::kMT][2][2];  // [row][half]: score to base 2
         float mx[C::kMT][2];
         bool grow = false;
@@ -444,7 +490,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const int tok = tok0 + j * 8 + 2 * t + (e & 1), x = e >> 1;
-                if (tok < lo_row[mt][x] || tok >= hi_row[mt][x] || !(ok_blk & (j < 2 ? 1 : 2)))
+                if (tok < lo_row[mt][x] || tok >= hi_row[mt][x] || (j < 2 ? rv.x : rv.y) < 0.0f)
                   sc[mt][j][e] = -INFINITY;
               }
           }
@@ -452,14 +498,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           for (int x = 0; x < 2; ++x) {
             const float va = fmaxf(fmax3(sc[mt][0][2 * x], sc[mt][0][2 * x + 1], sc[mt][1][2 * x]), sc[mt][1][2 * x + 1]);
             const float vb = fmaxf(fmax3(sc[mt][2][2 * x], sc[mt][2][2 * x + 1], sc[mt][3][2 * x]), sc[mt][3][2 * x + 1]);
-            float v = fmaxf(va * fa[mt][x][0], vb * fa[mt][x][1]);
+            float v = fmaxf(fmaf(va, fa[mt][x][0], meta.z), fmaf(vb, fa[mt][x][1], meta.w));
             v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
             v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
             mx[mt][x] = v;
             grow = grow || v > m[mt][x] + kDecLazy;
           }
         }
-        const bool move = __any_sync(0xFFFFFFFFu, grow);
         if (p.scores) {  // for cache_finish_kernel: 8 neighbouring tokens of a row a quad
           float* out = p.scores + (((long long)b * c.H + h) * ((c.M * (c.page >> 4) + 1) / 2) + (tok0 >> 5)) * p.rows * 32 + 2 * t;
 #pragma unroll
@@ -475,57 +520,50 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
               }
             }
         }
-        // Two halves of 16 tokens, each inside one block: O in that block's units.
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const float vs = half ? meta.w : meta.z;
-          const float unit = vs > 0.0f ? vs : vs_unit;  // a zero scale: its values do not count
-          const bool first = half == 0 && move;
-          if (first || unit != vs_unit) {
-            // (finite, so that an output of 0 stays 0)
-            const float by_unit = unit != vs_unit ? fminf(__fdividef(vs_unit, unit), 1e38f) : 1.0f;
-#pragma unroll
-            for (int mt = 0; mt < C::kMT; ++mt) {
-              float al[2] = {by_unit, by_unit};
-              if (first) {
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                  const float m2 = fmaxf(m[mt][x], mx[mt][x]);
-                  const float f = m2 == -INFINITY ? 1.0f : ex2(m[mt][x] - m2);
-                  l[mt][x] *= f;
-                  al[x] *= f;
-                  m[mt][x] = m2;
-                }
-              }
-#pragma unroll
-              for (int i = 0; i < C::kNTiles; ++i) {
-                fmul2(o[mt][i][0], o[mt][i][1], o[mt][i][0], o[mt][i][1], al[0], al[0]);
-                fmul2(o[mt][i][2], o[mt][i][3], o[mt][i][2], o[mt][i][3], al[1], al[1]);
-              }
-            }
-            vs_unit = unit;
-          }
-          uint32_t pa[C::kMT][4];  // P as the A operand
+        if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
           for (int mt = 0; mt < C::kMT; ++mt) {
-            const float m0 = m[mt][0] == -INFINITY ? 0.0f : m[mt][0], m1 = m[mt][1] == -INFINITY ? 0.0f : m[mt][1];
+            float al[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float m2 = fmaxf(m[mt][x], mx[mt][x]);
+              al[x] = m2 == -INFINITY ? 1.0f : ex2(m[mt][x] - m2);
+              l[mt][x] *= al[x];
+              m[mt][x] = m2;
+            }
+#pragma unroll
+            for (int i = 0; i < C::kNTiles; ++i) {
+              fmul2(o[mt][i][0], o[mt][i][1], o[mt][i][0], o[mt][i][1], al[0], al[0]);
+              fmul2(o[mt][i][2], o[mt][i][3], o[mt][i][2], o[mt][i][3], al[1], al[1]);
+            }
+          }
+        }
+        // Half by half (16 tokens, inside one cache block): P' and its sum.
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pa[C::kMT][4];  // P' as the A operand
+          const float lv = half ? meta.w : meta.z, rv_half = half ? rv.y : rv.x, by = rv_half > 0.0f ? rv_half : 1.0f;
+#pragma unroll
+          for (int mt = 0; mt < C::kMT; ++mt) {
+            const float m0 = lv - (m[mt][0] == -INFINITY ? 0.0f : m[mt][0]);
+            const float m1 = lv - (m[mt][1] == -INFINITY ? 0.0f : m[mt][1]);
             const float f0 = fa[mt][0][half], f1 = fa[mt][1][half];
             float pv[2][4];
 #pragma unroll
             for (int jj = 0; jj < 2; ++jj) {
               const float* x = sc[mt][2 * half + jj];
-              ffma2(pv[jj][0], pv[jj][1], x[0], x[1], f0, f0, -m0, -m0);
-              ffma2(pv[jj][2], pv[jj][3], x[2], x[3], f1, f1, -m1, -m1);
+              ffma2(pv[jj][0], pv[jj][1], x[0], x[1], f0, f0, m0, m0);
+              ffma2(pv[jj][2], pv[jj][3], x[2], x[3], f1, f1, m1, m1);
 #pragma unroll
               for (int e = 0; e < 4; ++e) pv[jj][e] = ex2(pv[jj][e]);
             }
-            l[mt][0] += (pv[0][0] + pv[0][1]) + (pv[1][0] + pv[1][1]);
-            l[mt][1] += (pv[0][2] + pv[0][3]) + (pv[1][2] + pv[1][3]);
+            l[mt][0] = fmaf((pv[0][0] + pv[0][1]) + (pv[1][0] + pv[1][1]), by, l[mt][0]);
+            l[mt][1] = fmaf((pv[0][2] + pv[0][3]) + (pv[1][2] + pv[1][3]), by, l[mt][1]);
             pa[mt][0] = pack_f16x2(pv[0][0], pv[0][1]);
             pa[mt][1] = pack_f16x2(pv[0][2], pv[0][3]);
             pa[mt][2] = pack_f16x2(pv[1][0], pv[1][1]);
             pa[mt][3] = pack_f16x2(pv[1][2], pv[1][3]);
-            if (!(vs > 0.0f)) pa[mt][0] = pa[mt][1] = pa[mt][2] = pa[mt][3] = 0u;
+            if (rv_half == 0.0f) pa[mt][0] = pa[mt][1] = pa[mt][2] = pa[mt][3] = 0u;
           }
           // O += P V over these 16 tokens: lane t takes tokens 2t, 2t+1, 2t+8, 2t+9
           const int row = half * 16 + 2 * t;
@@ -549,7 +587,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const int tok = tok0 + row + (e & 1) + 8 * (e >> 1);
-                if (tok < span.x || tok >= span.y || !(ok_blk & (half ? 2 : 1))) {
+                if (tok < span.x || tok >= span.y || rv_half < 0.0f) {
 #pragma unroll
                   for (int w = 0; w < kWords; ++w) v[e][w] = 0u;
                 }
@@ -577,7 +615,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         if (stage >= kS) stage -= kS, phase ^= 1u;
       }
 
-      // Join the warps: O in units of 1, at the block's common maximum.
+      // Join the warps: O at the block's common maximum.
 #pragma unroll
       for (int mt = 0; mt < C::kMT; ++mt)
 #pragma unroll
@@ -595,7 +633,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           const int r = mt * 16 + g + 8 * x;
           float top = -INFINITY;
           for (int w = 0; w < kW; ++w) top = fmaxf(top, s_ml[w * C::kRows + r].x);
-          const float f = m[mt][x] == -INFINITY ? 0.0f : ex2(m[mt][x] - top), fo = f * vs_unit;
+          const float f = m[mt][x] == -INFINITY ? 0.0f : ex2(m[mt][x] - top);
           if (t == 0) s_ml[warp * C::kRows + r].y = l[mt][x] * f;
           // four columns at a time, units rotated so that no two lanes meet in a bank
 #pragma unroll
@@ -605,7 +643,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
             const int d = dec_col<C>(i, 2 * t + (e & 1));
             static_assert(kRun % 4 == 0, "four neighbouring columns");
             *reinterpret_cast<float4*>(dec_join_at<C>(s_join, warp * C::kRows + r, d)) =
-                make_float4(o[mt][i][e] * fo, o[mt][i + 1][e] * fo, o[mt][i + 2][e] * fo, o[mt][i + 3][e] * fo);
+                make_float4(o[mt][i][e] * f, o[mt][i + 1][e] * f, o[mt][i + 2][e] * f, o[mt][i + 3][e] * f);
           }
         }
       named_bar_sync(1, 32 * kW);

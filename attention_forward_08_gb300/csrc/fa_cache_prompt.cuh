@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
         if (nth >= C::kStages && !(ok = prompt_warp_wait(&ctl->k_empty[stage], par ^ 1u, abort, a))) break;
         // (values of a zero scale are stored zeros for all that counts: they are
         // cleared below, and count with the scale 1)
-        const bool none = !(vs > 0.0f);
+        const bool none = !(vs >= 1.17549435e-38f);
         if (cw == 0 && lane / kG == j % kBatch)
           s_meta[(nth & 3) * kG + lane % kG] =
               make_float4(ks, none ? 0.0f : lg2(vs), none ? 1.0f : 1.0f / vs, blk >= 0 ? 1.0f : 0.0f);
