@@ -47,11 +47,11 @@ struct DecCfg {
   static constexpr bool kF16 = kF16_;  // type of q and o
   static constexpr int kD = kD_, kMT = kMT_;
   static constexpr int kTile = 32;  // tokens
-  // Consumer warps a block, and blocks an SM: as many warps as the outputs
-  // that each holds (kMT * D / 2 registers a lane) leave room for.
+  // As many consumer warps as the outputs that each holds (kMT * D / 2 registers
+  // a lane) leave room for, and two producers an SM: one block of 8 warps with
+  // 255 registers, or two of 6 with 168.
   static constexpr bool kWide = kMT * kD > 128;
-  static constexpr int kWarps = kWide ? 6 : 5, kProducers = kWide ? 2 : 1;
-  static constexpr int kCtas = kWide ? 1 : 2;
+  static constexpr int kWarps = kWide ? 6 : 5, kProducers = kWide ? 2 : 1, kCtas = kWide ? 1 : 2;
   static constexpr int kThreads = 32 * (kWarps + kProducers);
   static constexpr int kCols = kD >= 128 ? kD / 128 : 1;    // 128-byte column blocks of a row
   static constexpr int kRowBytes = kD >= 128 ? 128 : 64;    // of one column block
@@ -61,20 +61,26 @@ struct DecCfg {
   // kStages and warp k % kWarps, so that a stage's tiles all belong to one
   // warp: copies land in any order, and a warp that waited for one tile of a
   // stage cannot mistake its phase for the next one's.
-  static constexpr int kStages = (kWide ? 196608 : 98304) / kStageBytes / kWarps * kWarps;
+  static constexpr int kStages = kWide ? 196608 / kStageBytes / 6 * 6 : kD == 64 ? 20 : 10;
   static constexpr int kMinTiles = 2 * kWarps;  // of one block
   static constexpr int kRows = 16 * kMT;
   static constexpr int kKSteps = kD / 16, kNTiles = kD / 8;
   static constexpr int kQBytes = kRows * kD * 2;
   static constexpr int kRingBytes = kStages * kStageBytes;
-  // The warps join through the ring's memory: kWarps x (rows x D fp32).
-  static constexpr int kJoinBytes = kWarps * kRows * kD * 4;
-  static_assert(kJoinBytes <= kRingBytes && kWarps < kStages && kStages <= 24, "ring size");
+  // The warps join their outputs 8 rows at a time in memory of its own, so that
+  // the ring goes on to the next segment meanwhile; wide ones, all rows at once,
+  // in the ring's.
+  static constexpr int kJoinRows = kWide ? kRows : 8;
+  static constexpr int kJoinBytes = kWarps * kJoinRows * kD * 4;
+  static_assert((!kWide || kJoinBytes <= kRingBytes) && kStages % kWarps == 0 && kStages > kWarps && kStages <= 32,
+                "ring size");
   static_assert(kMT * kD <= 256, "32 rows of 256 columns do not fit the registers");
-  static constexpr int kOffQ = kRingBytes, kOffMl = kOffQ + kQBytes, kOffMeta = kOffMl + kWarps * kRows * 8;
+  static constexpr int kOffJoin = kWide ? 0 : kRingBytes;
+  static constexpr int kOffQ = kRingBytes + (kWide ? 0 : kJoinBytes), kOffMl = kOffQ + kQBytes, kOffMeta = kOffMl + kWarps * kRows * 8;
   static constexpr int kOffBar = kOffMeta + 64 * 32, kOffRs = kOffBar + kStages * 16;
   static constexpr int kOffTmp = kOffRs + kRows * 4;
   static constexpr int kSmem = 1024 + kOffTmp + 16;
+  static_assert(kSmem <= 232448, "shared memory");
 };
 
 // What a consumer needs beside a tile's bytes, for its two halves of 16
@@ -82,7 +88,7 @@ struct DecCfg {
 // scale; 1 / vs is -1 where nothing is stored).
 struct DecMeta {
   float ks[2], lv[2], rv[2];
-  float pad[2];
+  int blk[2];  // for the producer itself
 };
 
 // ------------------------------------------------------------------ tensor-core pieces
@@ -164,6 +170,19 @@ __device__ __forceinline__ float* dec_join_at(float* base, int r, int d) {
   return base + r * C::kD + (d & ~31) + ((((d >> 2) & 7) + 2 * (d >> 5) + r) & 7) * 4;
 }
 
+// A bounded wait by one thread; false once it ran out (or another did).
+__device__ __forceinline__ bool dec_wait_one(uint64_t* bar, uint32_t parity, volatile int* abort, const CacheAttnParams& a) {
+  const long long begin = clock64_now();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort) return false;
+    if (clock64_now() - begin > a.timeout_cycles) {
+      atomicOr(a.c.status, kStatusTimeout);
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
 // A bounded wait by a whole warp; false once it ran out (or another did).
 __device__ __forceinline__ bool dec_wait(uint64_t* bar, uint32_t parity, volatile int* abort, const CacheAttnParams& a) {
   bool ok = mbar_try_wait(bar, parity);
@@ -196,7 +215,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   uint64_t* s_empty = s_full + kS;
   float* s_rs = reinterpret_cast<float*>(smem + C::kOffRs);  // [row]: 2^-(scaling of the query row)
   volatile int* s_abort = reinterpret_cast<int*>(smem + C::kOffTmp);
-  float* s_join = reinterpret_cast<float*>(smem);
+  float* s_join = reinterpret_cast<float*>(smem + C::kOffJoin);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   if (tid == 0) {
     for (int s = 0; s < kS; ++s) {
@@ -274,69 +293,103 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
             if (keys) meta->ks[1] = ks;
             if (values) meta->lv[1] = lv, meta->rv[1] = rv;
           }
+          meta->blk[values ? 0 : 1] = blk;  // (two producers: one each)
         }
         __syncwarp();
         const int n = min(per_batch, n_tiles - k0);
+        if constexpr (C::kTma) {
+          // One thread, four tiles at a time: look-ups and first tries of the
+          // four go together (this loop is what a tile costs the block at least).
+          if (lane == 0) {
 #pragma unroll 1
-        for (int i = 0; i < n; ++i, ++issued) {
-          const int b0 = __shfl_sync(0xFFFFFFFFu, blk, i << shift);
-          const int b1 = subs == 2 ? __shfl_sync(0xFFFFFFFFu, blk, 2 * i + 1) : -1;
-          if (tile0 + issued >= kS && !dec_wait(s_empty + stage, phase ^ 1u, s_abort, a)) {
-            ok = false;
-            break;
-          }
-          uint64_t* bar = s_full + stage;
-          uint8_t* dst = smem + stage * C::kStageBytes;
-          if constexpr (C::kTma) {
-            if (lane == 0) {
-              const int boxes = (b0 >= 0) + (b1 >= 0);
-              if (boxes == 0)
-                mbar_arrive(bar);
-              else
-                mbar_arrive_expect_tx(bar, (uint32_t)(boxes * sub * C::kD * (3 - C::kProducers)));
+            for (int i = 0; i < n && ok; i += 4) {
+              int from[4], at_stage[4];
+              uint32_t par[4];
+              bool ready[4];
 #pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const int from = u ? b1 : b0;
-                if (from >= 0) {
+              for (int u = 0; u < 4; ++u) {
+                from[u] = s_meta[(tile0 + issued + u) & 63].blk[values ? 0 : 1];
+                at_stage[u] = stage + u < kS ? stage + u : stage + u - kS;
+                par[u] = stage + u < kS ? phase : phase ^ 1u;
+                ready[u] = tile0 + issued + u < kS || (i + u < n && mbar_try_wait(s_empty + at_stage[u], par[u] ^ 1u));
+              }
+              const int m = min(4, n - i);
 #pragma unroll
-                  for (int col = 0; col < C::kCols; ++col) {
-                    uint8_t* d = dst + (col * C::kTile + u * sub) * C::kRowBytes;
-                    if (keys) tma_load_4d(d, &tk, bar, col * 128, y, h, from);
-                    if (values) tma_load_4d(d + C::kTileBytes, &tv, bar, col * 128, y, h, from);
+              for (int u = 0; u < 4; ++u) {
+                if (u < m && ok) {
+                  ok = ready[u] || dec_wait_one(s_empty + at_stage[u], par[u] ^ 1u, s_abort, a);
+                  if (ok) {
+                    uint64_t* bar = s_full + at_stage[u];
+                    uint8_t* dst = smem + at_stage[u] * C::kStageBytes;
+                    if (from[u] < 0) {
+                      mbar_arrive(bar);
+                    } else {
+                      mbar_arrive_expect_tx(bar, (uint32_t)(C::kStageBytes / C::kProducers));
+#pragma unroll
+                      for (int col = 0; col < C::kCols; ++col) {
+                        uint8_t* d = dst + col * C::kTile * C::kRowBytes;
+                        if (keys) tma_load_4d(d, &tk, bar, col * 128, y, h, from[u]);
+                        if (values) tma_load_4d(d + C::kTileBytes, &tv, bar, col * 128, y, h, from[u]);
+                      }
+                    }
+                    ++issued;
+                    y = (y + C::kTile) & (c.page - 1);
                   }
                 }
               }
+              stage += m;
+              if (stage >= kS) stage -= kS, phase ^= 1u;
             }
-          } else {
-            // 16-byte units, in the swizzle that a tensor map would give them
-            constexpr int kUnits = C::kRowBytes / 16, kRowsAtOnce = 32 / kUnits;
-            const int unit = lane % kUnits;
-            const uint32_t to = smem_u32(dst);
+          }
+          issued = __shfl_sync(0xFFFFFFFFu, issued, 0);
+          stage = __shfl_sync(0xFFFFFFFFu, stage, 0);
+          phase = __shfl_sync(0xFFFFFFFFu, phase, 0);
+          y = __shfl_sync(0xFFFFFFFFu, y, 0);
+          ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+        } else {
+          // 16-byte units, in the swizzle that a tensor map would give them; the
+          // warp copies kRowsAtOnce rows at a time.
+          constexpr int kUnits = C::kRowBytes / 16, kRowsAtOnce = 32 / kUnits;
+          const int unit = lane % kUnits, r_lane = lane / kUnits;
+#pragma unroll 1
+          for (int i = 0; i < n; ++i, ++issued) {
+            const int b0 = __shfl_sync(0xFFFFFFFFu, blk, i << shift);
+            const int b1 = subs == 2 ? __shfl_sync(0xFFFFFFFFu, blk, 2 * i + 1) : b0;
+            // a half's first row of this lane
+            const uint8_t *k_from[2], *v_from[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const long long at_blk = max(half ? b1 : b0, 0), row = ((y + 16 * half) & (c.page - 1)) + r_lane;
+              k_from[half] = c.k + at_blk * c.ks[0] + h * c.ks[1] + row * c.ks[2] + unit * 16;
+              v_from[half] = c.v + at_blk * c.vs[0] + h * c.vs[1] + row * c.vs[2] + unit * 16;
+            }
+            if (tile0 + issued >= kS && !dec_wait(s_empty + stage, phase ^ 1u, s_abort, a)) {
+              ok = false;
+              break;
+            }
+            const uint32_t to = smem_u32(smem + stage * C::kStageBytes);
 #pragma unroll
             for (int r0 = 0; r0 < C::kTile; r0 += kRowsAtOnce) {
-              const int r = r0 + lane / kUnits, from = subs == 2 && r >= 16 ? b1 : b0;
-              const int row = (y + r) & (c.page - 1);
+              const bool there = (r0 < 16 ? b0 : b1) >= 0;
 #pragma unroll
               for (int col = 0; col < C::kCols; ++col) {
-                const uint32_t d = dec_unit<C>(to + col * C::kTile * C::kRowBytes, r, unit);
-                if (keys)
-                  copy16(d, c.k + max(from, 0) * c.ks[0] + h * c.ks[1] + row * c.ks[2] + col * 128 + unit * 16, from >= 0);
-                if (values)
-                  copy16(d + C::kTileBytes,
-                         c.v + max(from, 0) * c.vs[0] + h * c.vs[1] + row * c.vs[2] + col * 128 + unit * 16, from >= 0);
+                const uint32_t d = dec_unit<C>(to + col * C::kTile * C::kRowBytes, r0 + r_lane, unit);
+                if (keys) copy16(d, k_from[r0 / 16] + (r0 & 15) * c.ks[2] + col * 128, there);
+                if (values) copy16(d + C::kTileBytes, v_from[r0 / 16] + (r0 & 15) * c.vs[2] + col * 128, there);
               }
             }
+            uint64_t* bar = s_full + stage;
             copy_arrive(bar);
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);  // the scales
+            y = (y + C::kTile) & (c.page - 1);
+            if (++stage == kS) stage = 0, phase ^= 1u;
           }
-          y = (y + C::kTile) & (c.page - 1);
-          if (++stage == kS) stage = 0, phase ^= 1u;
         }
       }
       // After an expired wait: the copies in flight land first (a bounded wait
       // again), then the block ends.
-      if (__syncthreads_or(0)) {
+      if (C::kWide ? __syncthreads_or(!ok) : !ok) {
         for (int k = max(0, tile0 + issued - kS); k < tile0 + issued; ++k) {
           const long long begin = clock64_now();
           while (!mbar_try_wait(s_full + k % kS, (uint32_t)(k / kS) & 1u) && clock64_now() - begin < kDecDrainCycles) {
@@ -624,53 +677,60 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           l[mt][x] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][x], 2);
           if (t == 0) s_ml[warp * C::kRows + mt * 16 + g + 8 * x] = make_float2(m[mt][x], l[mt][x]);
         }
-      // Every warp is done with the ring, and the maxima are there.
-      if (__syncthreads_or(dead)) return;
+      // The maxima are there (and every warp is done with the ring).
+      if (C::kWide ? __syncthreads_or(dead) : named_bar_or(1, 32 * kW, dead)) return;
+      const int slot = 2 * blockIdx.x + (pos > at.seg0 ? 0 : 1);
 #pragma unroll
-      for (int mt = 0; mt < C::kMT; ++mt)
+      for (int pass = 0; pass < C::kRows / C::kJoinRows; ++pass) {
+        if (r0 + pass * C::kJoinRows >= r1) break;
+        if (pass > 0) named_bar_sync(1, 32 * kW);  // the rows before have been read
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int r = mt * 16 + g + 8 * x;
-          float top = -INFINITY;
-          for (int w = 0; w < kW; ++w) top = fmaxf(top, s_ml[w * C::kRows + r].x);
-          const float f = m[mt][x] == -INFINITY ? 0.0f : ex2(m[mt][x] - top);
-          if (t == 0) s_ml[warp * C::kRows + r].y = l[mt][x] * f;
-          // four columns at a time, units rotated so that no two lanes meet in a bank
+        for (int mt = 0; mt < C::kMT; ++mt)
 #pragma unroll
-          for (int q = 0; q < C::kNTiles / 2; ++q) {  // 2 * D / 8 values a row: columns of n = 2t, then 2t + 1
-            constexpr int kRun = C::kD == 64 ? 8 : 16;
-            const int i = (q * 4) % C::kNTiles, e = 2 * x + (q * 4) / C::kNTiles;
-            const int d = dec_col<C>(i, 2 * t + (e & 1));
-            static_assert(kRun % 4 == 0, "four neighbouring columns");
-            *reinterpret_cast<float4*>(dec_join_at<C>(s_join, warp * C::kRows + r, d)) =
-                make_float4(o[mt][i][e] * f, o[mt][i + 1][e] * f, o[mt][i + 2][e] * f, o[mt][i + 3][e] * f);
+          for (int x = 0; x < 2; ++x) {
+            if (!C::kWide && 2 * mt + x != pass) continue;
+            const int r = mt * 16 + g + 8 * x;
+            float top = -INFINITY;
+            for (int w = 0; w < kW; ++w) top = fmaxf(top, s_ml[w * C::kRows + r].x);
+            const float f = m[mt][x] == -INFINITY ? 0.0f : ex2(m[mt][x] - top);
+            if (t == 0) s_ml[warp * C::kRows + r].y = l[mt][x] * f;
+            // four columns at a time, units rotated so that no two lanes meet in a bank
+#pragma unroll
+            for (int q = 0; q < C::kNTiles / 2; ++q) {  // 2 * D / 8 values a row: columns of n = 2t, then 2t + 1
+              const int i = (q * 4) % C::kNTiles, e = 2 * x + (q * 4) / C::kNTiles;
+              const int d = dec_col<C>(i, 2 * t + (e & 1));
+              *reinterpret_cast<float4*>(dec_join_at<C>(s_join, warp * C::kJoinRows + r - pass * C::kJoinRows, d)) =
+                  make_float4(o[mt][i][e] * f, o[mt][i + 1][e] * f, o[mt][i + 2][e] * f, o[mt][i + 3][e] * f);
+            }
+          }
+        named_bar_sync(1, 32 * kW);
+#pragma unroll 1
+        for (int v = tid; v < min(r1 - r0 - pass * C::kJoinRows, C::kJoinRows) * (C::kD / 4); v += 32 * kW) {
+          const int rj = v / (C::kD / 4), r = pass * C::kJoinRows + rj, d = (v % (C::kD / 4)) * 4;
+          float top = -INFINITY, sum = 0.0f;
+          float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+          for (int w = 0; w < kW; ++w) {
+            const float2 ml = s_ml[w * C::kRows + r];
+            const float4 y = *reinterpret_cast<const float4*>(dec_join_at<C>(s_join, w * C::kJoinRows + rj, d));
+            top = fmaxf(top, ml.x);
+            sum += ml.y;
+            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+          }
+          if (whole) {
+            dec_write<C>(a, b, h, r0 + r, d, x, top, sum);
+          } else {
+            *reinterpret_cast<float4*>(p.part_o + ((long long)slot * C::kRows + r) * C::kD + d) = x;
+            if (d == 0) p.part_ml[(long long)slot * C::kRows + r] = make_float2(top, sum);
           }
         }
-      named_bar_sync(1, 32 * kW);
-      const int slot = 2 * blockIdx.x + (pos > at.seg0 ? 0 : 1);
-#pragma unroll 1
-      for (int v = tid; v < (r1 - r0) * (C::kD / 4); v += 32 * kW) {
-        const int r = v / (C::kD / 4), d = (v % (C::kD / 4)) * 4;
-        float top = -INFINITY, sum = 0.0f;
-        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int w = 0; w < kW; ++w) {
-          const float2 ml = s_ml[w * C::kRows + r];
-          const float4 y = *reinterpret_cast<const float4*>(dec_join_at<C>(s_join, w * C::kRows + r, d));
-          top = fmaxf(top, ml.x);
-          sum += ml.y;
-          x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-        }
-        if (whole) {
-          dec_write<C>(a, b, h, r0 + r, d, x, top, sum);
-        } else {
-          *reinterpret_cast<float4*>(p.part_o + ((long long)slot * C::kRows + r) * C::kD + d) = x;
-          if (d == 0) p.part_ml[(long long)slot * C::kRows + r] = make_float2(top, sum);
-        }
       }
-      fence_proxy_async_smem();  // what was written into the ring's memory goes before the next copies into it
+      if constexpr (C::kWide)
+        fence_proxy_async_smem();  // what was written into the ring's memory goes before the next copies into it
+      else
+        named_bar_sync(1, 32 * kW);  // the maxima and the query rows are free again
     }
-    __syncthreads();  // the ring's memory and the maxima are free again
+    if constexpr (C::kWide) __syncthreads();  // the ring's memory and the maxima are free again
     tile0 += n_tiles;
     pos += n_tiles;
     dec_next(p, at, tiles);

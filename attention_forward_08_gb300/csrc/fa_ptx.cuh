@@ -111,6 +111,18 @@ __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// ... and whether any of the threads had `mine`.
+__device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool mine) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(nthreads), "r"((uint32_t)mine)
+      : "memory");
+  return any != 0;
+}
+
 // ------------------------------------------------------------------ tcgen05: TMEM
 
 // Whole-warp: allocate `ncols` TMEM columns, the base address is written to smem.

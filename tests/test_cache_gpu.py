@@ -563,3 +563,27 @@ def test_cached_matches_dense_attention(fa, n):
     o2, l2 = fa.attention(q, *x, causal=True, q_offset=L - n)
     synced(fa)
     assert (o.float() - o2.float()).abs().max() <= 2e-2 and (l - l2).abs().max() <= 1e-2
+
+
+@pytest.mark.parametrize("n,D", [(1, 64), (1, 128), (5, 128), (1, 256), (64, 128), (64, 256)])
+def test_wait_bound_expires_or_not_then_recovers(fa, n, D):
+    """With a one-cycle wait bound a kernel unwinds at the first wait that it expires in (its copies and MMAs drained),
+    and the status tells; the hardware may hold a waiting thread until its copy has landed, and then none does.  Either
+    way the next run is right."""
+    g = torch.Generator().manual_seed(1)
+    lens = [3000, 700]
+    table, P, _ = R.make_table(g, lens, 64)
+    pools = R.make_pools(g, P, 2, 64, D, E4M3)
+    q = torch.randn(2, 8, n, D, generator=g).to(BF16)
+    cache, qd, t, ln = to_gpu(fa, pools), q.to(DEV), i32(table), i32(lens)
+    torch.cuda.synchronize()
+    try:
+        fa.fa_set_timeout_cycles(1)
+        fa.cache_attention(qd, cache, t, ln)
+        rc = fa.fa_sync_status(None)
+    finally:
+        fa.fa_set_timeout_cycles(0)
+    assert rc in (fa.fa.FA_OK, fa.fa.FA_ERR_DEVICE_TIMEOUT), fa.fa_last_error()
+    got = fa.cache_attention(qd, cache, t, ln)
+    synced(fa)
+    check_attention(fa, R.Cache(*pools), q, table, lens, got)
