@@ -116,14 +116,24 @@ __global__ void __launch_bounds__(512) cache_append_kernel(const AppendParams p)
   const float s = fmaxf(old, pow2_scale<kKind>(amax));
   __syncthreads();  // everybody has read the old scale
   if (tid == 0) *scale_at = s;
+  // x / s; where s is a power of two with a normal inverse (always, but for a
+  // caller's own scales), x times its inverse is the same number.
+  const uint32_t s_bits = __float_as_uint(s);
+  const bool pow2 = (s_bits & 0x7FFFFFu) == 0u && s_bits - 0x00800000u < 0x7E000000u;
+  const float inv = __uint_as_float(0x7F000000u - s_bits);
 #pragma unroll
   for (int i = 0; i < kMaxVec; ++i) {
     const int v = tid + i * blockDim.x;
     if (v < nv) {
       float f[8];
       x[i].get(f);
+      if (pow2) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = __fdiv_rn(f[e], s);
+        for (int e = 0; e < 8; ++e) f[e] *= inv;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = __fdiv_rn(f[e], s);
+      }
       uint2 r;
       r.x = round8x4<kKind>(f[0], f[1], f[2], f[3]);
       r.y = round8x4<kKind>(f[4], f[5], f[6], f[7]);

@@ -108,16 +108,17 @@ int launch_decode(const CacheAttnParams& a, const LaunchCtx& ctx) {
   kern<<<p.max_ctas, C::kThreads, C::kSmem, ctx.stream>>>(tk, tv, p);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && p.scores) {
-    const int joins = (p.max_ctas - 1) * (C::kRows * C::kD / 512);
+    const int joins = (p.max_ctas - 1) * join_pieces<C>(p);
     const long long chunks = ((long long)a.c.M * a.c.page + kFinishTokens - 1) / kFinishTokens;
     if (chunks * a.c.H * a.B > 0x7fffffffLL - joins) {
       set_error("B * H_kv * table width (%lld tokens) is beyond the weights' index range", (long long)a.c.M * a.c.page);
       return FA_ERR_UNSUPPORTED;
     }
-    e = launch_after(cache_finish_kernel<C>, dim3((unsigned)(joins + chunks * a.c.H * a.B)), 128, ctx.stream, p, joins,
-                     (int)chunks);
+    e = launch_after(cache_finish_kernel<C>, dim3((unsigned)(joins + chunks * a.c.H * a.B)), kJoinThreads, ctx.stream, p,
+                     joins, (int)chunks);
   } else if (e == cudaSuccess && p.max_ctas > 1) {
-    e = launch_after(cache_join_kernel<C>, dim3(C::kRows * C::kD / 512, (unsigned)p.max_ctas - 1), 128, ctx.stream, p);
+    e = launch_after(cache_join_kernel<C>, dim3((unsigned)join_pieces<C>(p), (unsigned)p.max_ctas - 1), kJoinThreads,
+                     ctx.stream, p);
   }
   if (e != cudaSuccess) {
     set_error("cache attention launch failed: %s", cudaGetErrorString(e));
@@ -147,7 +148,8 @@ int launch_prompt(const CacheAttnParams& a, const LaunchCtx& ctx) {
   kern<<<p.max_ctas, C::kThreads, C::kSmem, ctx.stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && p.max_ctas > 1)
-    e = launch_after(cache_join_kernel<C>, dim3(C::kRows * C::kD / 512, (unsigned)p.max_ctas - 1), 128, ctx.stream, p);
+    e = launch_after(cache_join_kernel<C>, dim3((unsigned)join_pieces<C>(p), (unsigned)p.max_ctas - 1), kJoinThreads,
+                     ctx.stream, p);
   if (e != cudaSuccess) {
     set_error("cache attention launch failed: %s", cudaGetErrorString(e));
     return FA_ERR_CUDA;

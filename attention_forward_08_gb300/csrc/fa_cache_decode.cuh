@@ -399,44 +399,41 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       }
     } else {
       // ---------------------------------------------------------- consumers
-      // The query rows, scaled to f16 and laid out as the tensor core's operand.
-#pragma unroll 1
-      for (int r = warp; r < C::kRows; r += kW) {
-        constexpr int kE = C::kD / 32;  // elements a lane
-        float f[kE];
-        const int row = r0 + r, i = row / a.group, head = h * a.group + row % a.group;
-        const bool in = row < r1 && i < seq.nq;
-        if (in) {
-          const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + b * a.qs[0] +
-                                                                head * a.qs[1] + i * a.qs[2]) + lane * (kE / 2);
+      // The query rows, scaled to f16 and laid out as the tensor core's operand:
+      // all of this warp's on their way at once.
+      constexpr int kE = C::kD / 32, kMine = (C::kRows + kW - 1) / kW;  // elements a lane; rows a warp
+      uint32_t qw[kMine][kE / 2];
 #pragma unroll
-          for (int e = 0; e < kE; e += 2) {
-            const uint32_t w = __ldg(q + e / 2);
-            f[e] = half_bits_to_f32<C::kF16>(w);
-            f[e + 1] = half_bits_to_f32<C::kF16>(w >> 16);
-          }
-        } else {
+      for (int i = 0; i < kMine; ++i) {
+        const int row = r0 + warp + i * kW, qi = row / a.group, head = h * a.group + row % a.group;
+        const bool in = warp + i * kW < C::kRows && row < r1 && qi < seq.nq;
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + b * a.qs[0] +
+                                                              head * a.qs[1] + qi * a.qs[2]) + lane * (kE / 2);
 #pragma unroll
-          for (int e = 0; e < kE; ++e) f[e] = 0.0f;
+        for (int e = 0; e < kE / 2; ++e) qw[i][e] = in ? __ldg(q + e) : 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int r = warp + i * kW;
+        if (r >= C::kRows) break;
+        float f[kE], up = 1.0f, down = 1.0f;
+#pragma unroll
+        for (int e = 0; e < kE / 2; ++e) {
+          f[2 * e] = half_bits_to_f32<C::kF16>(qw[i][e]);
+          f[2 * e + 1] = half_bits_to_f32<C::kF16>(qw[i][e] >> 16);
         }
-        float up = 1.0f;
-        if constexpr (!C::kF16) {
+        if (!C::kF16 && r0 + r < r1) {
           float top = 0.0f;
 #pragma unroll
           for (int e = 0; e < kE; ++e) top = fmaxf(top, fabsf(f[e]));
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-          float down;
+          top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)));  // (the order of bits, for floats >= 0)
           dec_row_scale(top, up, down);
-          if (lane == 0) s_rs[r] = down;
-        } else if (lane == 0) {
-          s_rs[r] = 1.0f;
         }
+        if (lane == 0) s_rs[r] = down;
 #pragma unroll
-        for (int e = 0; e < kE; e += 2) {
-          const int at_word = (r >> 4) * C::kKSteps * 128 + dec_q_word<C::kD>(r & 15, lane * kE + e);
-          reinterpret_cast<uint32_t*>(s_q)[at_word] = pack_f16x2(f[e] * up, f[e + 1] * up);
-        }
+        for (int e = 0; e < kE; e += 2)
+          reinterpret_cast<uint32_t*>(s_q)[(r >> 4) * C::kKSteps * 128 + dec_q_word<C::kD>(r & 15, lane * kE + e)] =
+              pack_f16x2(f[e] * up, f[e + 1] * up);
       }
       named_bar_sync(1, 32 * kW);
 

@@ -1,12 +1,15 @@
 // fa_cache_evict.cu -- keep the heaviest and latest tokens (include/fa_cache.h).
 //
-// The choice: one thread block per sequence and head finds, byte by byte, the
-// key of the last token that is kept (a radix selection: four passes over the
-// weights' keys, each counting one byte of those that match the bytes found so
-// far; the keys stay in shared memory where they fit), and writes for every
-// slot below `keep` which slot's token ends there.  A copy into other blocks
-// then moves by a second launch, one thread block per (sequence, head,
-// receiving block of K or of V).
+// The choice: one thread block per sequence and head searches the key above
+// which `keep` tokens lie, by counting: every pass counts the keys at and above
+// three values that quarter the range left, until one has exactly `keep` (after
+// 8 or 9 passes where weights differ, 17 at most), and then writes for every
+// slot below `keep` which slot's token ends there.  The keys stay in shared
+// memory where they fit.  (A radix selection, 8 bits a pass, took 15,000 cycles
+// for 2049 tokens and 21,000 for 16000, nearly all of it in atomics on the few
+// counters that float exponents share; this takes TIMES.)  A copy into other
+// blocks then moves by a second launch, one thread block per (sequence, head,
+// receiving block).
 //
 // In place, only tokens in slots at `keep` and behind move, and only into
 // slots below `keep`: no slot is both read and written, so the moves need no
@@ -44,8 +47,9 @@ __device__ __forceinline__ int warp_sum(int v) {
   return v;
 }
 
-// Tokens whose keys fit shared memory (192 KB).
-constexpr int kCachedKeys = 49152;
+constexpr int kFewMoves = 1024;  // in place: lists in shared memory, else in the workspace
+// Tokens whose keys fit shared memory (184 KB).
+constexpr int kCachedKeys = 47104;
 
 // Sixteen stored bytes of scale `from`, rounded to scale `to`.
 template <int kKind>
@@ -62,15 +66,23 @@ __device__ __forceinline__ uint4 rescale16(uint4 w, float from, float to) {
   return w;
 }
 
+__device__ int block_count(int v, uint2 (*tmp)[kPlanWarps]) {
+  v = __reduce_add_sync(0xFFFFFFFFu, v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) tmp[0][threadIdx.x >> 5].x = (uint32_t)v;
+  __syncthreads();
+  return __reduce_add_sync(0xFFFFFFFFu, (int)tmp[0][threadIdx.x & 31].x);
+}
+
 template <int kKind>
 __global__ void __launch_bounds__(kPlanThreads) cache_evict_plan_kernel(const EvictParams p, int cached) {
   const CacheView& c = p.c;
   const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long bh = (long long)b * c.H + h;
   extern __shared__ uint32_t s_key[];
-  __shared__ int hist[256];
+  __shared__ uint2 s_count[2][kPlanWarps];
   __shared__ int part[kPlanWarps][4];
-  __shared__ int s_max, s_digit, s_need;
+  __shared__ int s_max;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int n = checked_len(c, p.lens[b]);
   if (n > p.W) {
@@ -102,7 +114,6 @@ __global__ void __launch_bounds__(kPlanThreads) cache_evict_plan_kernel(const Ev
     most = __reduce_max_sync(0xFFFFFFFFu, most);
     if (lane == 0) atomicMax(&s_max, most);
   }
-  if (tid < 256) hist[tid] = 0;
   __syncthreads();
   // Positions above the bound are kept first (long: the bound may lie below INT_MIN).
   const long long late = p.recent > 0 ? (long long)s_max - p.recent : LLONG_MAX;
@@ -111,64 +122,62 @@ __global__ void __launch_bounds__(kPlanThreads) cache_evict_plan_kernel(const Ev
     const long long pos = p.recent > 0 && position ? position[j] : j;
     return pos > late ? first : weight_key(weight[j]);
   };
-  uint32_t found = 0;  // the bytes found so far
-  int need = p.keep;   // tokens still to take among those that match them
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    const uint32_t mask = shift == 24 ? 0u : ~0u << (shift + 8);
-    const int stop = (n + kPlanThreads - 1) / kPlanThreads * kPlanThreads;
+  if (in_smem && p.recent > 0) {
 #pragma unroll 4
-    for (int j = tid; j < stop; j += kPlanThreads) {
-      uint32_t k = 0;
-      bool in = j < n;
-      if (in) {
-        if (!in_smem) {
-          k = key_of(j);
-        } else if (shift == 24) {
-          k = s_key[j];
-          if (p.recent > 0 && (position ? position[j] : j) > late) s_key[j] = k = first;
-        } else {
-          k = s_key[j];
-        }
-        in = (k & mask) == found;
-      }
-      // Weights crowd into few exponents: lanes that agree count once.
-      const uint32_t live = __ballot_sync(0xFFFFFFFFu, in);
-      if (in) {
-        const int digit = (k >> shift) & 255;
-        const uint32_t same = __match_any_sync(live, digit);
-        if (__ffs(same) - 1 == lane) atomicAdd(&hist[digit], __popc(same));
-      }
-    }
-    __syncthreads();
-    if (warp == 0) {  // the digit at which the count from above reaches `need`
-      int mine = 0, at[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) mine += at[i] = hist[255 - (lane * 8 + i)];
-      int upto = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-        if (lane >= o) upto += t;
-      }
-      int before = upto - mine;
-      if (before < need && upto >= need) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (before < need && before + at[i] >= need) {
-            s_digit = 255 - (lane * 8 + i);
-            s_need = need - before;
-          }
-          before += at[i];
-        }
-      }
-    }
-    __syncthreads();
-    found |= (uint32_t)s_digit << shift;
-    need = s_need;
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
+    for (int j = tid; j < n; j += kPlanThreads)
+      if ((position ? position[j] : j) > late) s_key[j] = first;
   }
+  if (in_smem) __syncthreads();
   auto key = [&](int j) -> uint32_t { return in_smem ? s_key[j] : key_of(j); };
+  // At least `keep` keys are >= lo, fewer (`over`) are >= hi.
+  uint32_t lo = 0, hi = first + 1, found;
+  int over = 0, need = 0;
+#pragma unroll 1
+  for (int pass = 0;; ++pass) {
+    const uint32_t step = (hi - lo) / 4;
+    if (hi - lo == 1) {  // the last key that is kept, not all of it perhaps
+      found = lo;
+      need = p.keep - over;
+      break;
+    }
+    const uint32_t m1 = lo + max(step, 1u), m2 = step ? m1 + step : m1, m3 = step ? m2 + step : m1;
+    uint32_t c12 = 0, c3 = 0;
+#pragma unroll 4
+    for (int j = tid; j < n; j += kPlanThreads) {
+      const uint32_t k = key(j);
+      c12 += (k >= m1 ? 1u : 0u) + (k >= m2 ? 0x10000u : 0u);
+      c3 += k >= m3 ? 1u : 0u;
+    }
+    // (n of up to 47104 counts in 16 bits; more, whose keys are not in shared
+    // memory, one by one)
+    int n1, n2, n3;
+    if (in_smem) {
+      c12 = __reduce_add_sync(0xFFFFFFFFu, c12);
+      c3 = __reduce_add_sync(0xFFFFFFFFu, c3);
+      if (lane == 0) s_count[pass & 1][warp] = make_uint2(c12, c3);
+      __syncthreads();
+      const uint2 c = s_count[pass & 1][lane];
+      c12 = __reduce_add_sync(0xFFFFFFFFu, c.x);
+      n1 = c12 & 0xFFFF, n2 = c12 >> 16, n3 = __reduce_add_sync(0xFFFFFFFFu, c.y);
+    } else {
+      n1 = block_count(c12 & 0xFFFF, s_count);
+      n2 = block_count(c12 >> 16, s_count);
+      n3 = block_count(c3, s_count);
+    }
+    // (in order: m1 <= m2 <= m3, n1 >= n2 >= n3)
+    const uint32_t m[3] = {m1, m2, m3};
+    const int c[3] = {n1, n2, n3};
+    bool exact = false;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      if (c[i] == p.keep) exact = true, found = m[i] - 1;
+      if (c[i] >= p.keep) lo = m[i];
+    }
+#pragma unroll
+    for (int i = 2; i >= 0; --i)
+      if (c[i] < p.keep) hi = m[i], over = c[i];
+    if (exact) break;  // all above `found`, none of it
+  }
   // Kept: keys above `found`, and the first `need` slots whose key equals it.
   // Every warp owns a run of slots; a first sweep counts what lies before it.
   // In place, with `kept_lo` of the slots below `keep` kept: the slot j that
@@ -178,6 +187,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_evict_plan_kernel(const Ev
   const int run = ((n + kPlanThreads - 1) / kPlanThreads) * 32;
   const int j0 = warp * run, j1 = min(n, j0 + run);
   int above = 0, equal = 0, above_lo = 0, equal_lo = 0;
+#pragma unroll 4
   for (int j = j0 + lane; j < j1; j += 32) {
     const uint32_t k = key(j);
     const bool lo = j < p.keep;
@@ -204,6 +214,10 @@ __global__ void __launch_bounds__(kPlanThreads) cache_evict_plan_kernel(const Ev
   kept_n += min(eq, need);
   kept_lo += min(eq_lo, need);
   int* mover = p.mover + bh * p.keep;
+  // In place, the receiving slots in order (the movers' list has as many).
+  __shared__ int s_hole[kFewMoves], s_mover[kFewMoves];
+  const int moves = p.keep - kept_lo;
+  const bool few = moves <= kFewMoves;
   const uint32_t below = (1u << lane) - 1;
   for (int base = j0; base < j1; base += 32) {
     const int j = base + lane;
@@ -215,8 +229,11 @@ __global__ void __launch_bounds__(kPlanThreads) cache_evict_plan_kernel(const Ev
     const int at = kept_n + __popc(kb & below);  // kept slots before j
     if (p.into) {
       if (kept) src[at] = j;
+    } else if (few) {
+      if (in && j < p.keep && !kept) s_hole[j - at] = j;
+      if (kept && j >= p.keep) s_mover[at - kept_lo] = j;
     } else if (in && j < p.keep) {
-      src[j] = kept ? j : -1 - (j - at);
+      if (!kept) src[j - at] = j;
     } else if (kept) {
       mover[at - kept_lo] = j;
     }
@@ -232,110 +249,131 @@ __global__ void __launch_bounds__(kPlanThreads) cache_evict_plan_kernel(const Ev
     s_edge[tid] = blk < 0 ? 0.0f : (tid ? c.v_scale : c.k_scale)[(long long)blk * c.H + h];
   }
   __syncthreads();
-  const int blocks = (p.keep + c.page - 1) >> c.page_log2;
-  for (int m = warp; m < blocks; m += kPlanWarps) {
-    const int m0 = m << c.page_log2, tokens = min(c.page, p.keep - m0);
-    bool moves = false;
-    for (int t = lane; t < tokens; t += 32) moves = moves || src[m0 + t] < 0;
-    if (!__any_sync(0xFFFFFFFFu, moves)) continue;
+  auto hole_at = [&](int i) { return few ? s_hole[i] : src[i]; };
+  auto mover_at = [&](int i) { return few ? s_mover[i] : mover[i]; };
+  // A warp takes the moves into one block, of K or of V, from the first of them.
+  for (int w = warp; w < 2 * moves; w += kPlanWarps) {
+    const int i0 = w >> 1, is_v = w & 1, m = hole_at(i0) >> c.page_log2;
+    if (i0 > 0 && hole_at(i0 - 1) >> c.page_log2 == m) continue;
     const int to = checked_block(c, c.table, c.table_stride, b, m);
     if (to < 0) continue;
-#pragma unroll 1
-    for (int is_v = 0; is_v < 2; ++is_v) {
-      float* scales = is_v ? c.v_scale : c.k_scale;
-      const float old = scales[(long long)to * c.H + h];
-      float top = 0.0f;
-      for (int t = lane; t < tokens; t += 32) {  // the largest scale of the blocks that the tokens come from
-        const int s = src[m0 + t];
-        float sc = old;
-        if (s < 0) {
-          const int blk = checked_block(c, c.table, c.table_stride, b, mover[-1 - s] >> c.page_log2);
-          sc = blk < 0 ? 0.0f
-               : mover[-1 - s] >> c.page_log2 == p.keep >> c.page_log2 ? s_edge[is_v]
-                                                                         : scales[(long long)blk * c.H + h];
-        }
-        top = fmaxf(top, sc);
-      }
+    float* scales = is_v ? c.v_scale : c.k_scale;
+    const float old = scales[(long long)to * c.H + h];
+    // A mover's scale; of the block of slot `keep`, the one from before.
+    auto scale_of = [&](int from, int& blk) -> float {
+      const int fm = from >> c.page_log2;
+      blk = checked_block(c, c.table, c.table_stride, b, fm);
+      return blk < 0 ? 0.0f : fm == p.keep >> c.page_log2 ? s_edge[is_v] : scales[(long long)blk * c.H + h];
+    };
+    // The largest scale of the blocks that the block's tokens come from, its
+    // own among them unless all its tokens are new.
+    const int m0 = m << c.page_log2, tokens = min(c.page, p.keep - m0);
+    int n = 0;  // moves into it
+    float top = 0.0f;
+    for (int base = i0;; base += 32) {
+      const int i = base + lane;
+      const bool here = i < moves && hole_at(i) >> c.page_log2 == m;
+      int blk;
+      if (here) top = fmaxf(top, scale_of(mover_at(i), blk));
+      const int got = __popc(__ballot_sync(0xFFFFFFFFu, here));
+      n += got;
+      if (got < 32) break;
+    }
+    if (n < tokens) top = fmaxf(top, old);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-      const long long* cs = is_v ? c.vs : c.ks;
-      uint8_t* pool = (is_v ? c.v : c.k) + h * cs[1];
-      const int vd = c.D >> 4, vd_log2 = 31 - __clz(vd);  // 16-byte vectors a token
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    const long long* cs = is_v ? c.vs : c.ks;
+    uint8_t* pool = (is_v ? c.v : c.k) + h * cs[1];
+    uint8_t* out = pool + to * cs[0];
+    const int vd = c.D >> 4, vd_log2 = 31 - __clz(vd);  // 16-byte vectors a token
+    if (n < tokens && top != old) {  // what stays (and what is about to be overwritten) moves to the larger scale
       for (int v = lane; v < tokens * vd; v += 32) {
-        const int t = v >> vd_log2, at = (v & (vd - 1)) * 16, s = src[m0 + t];
-        uint4* dst = reinterpret_cast<uint4*>(pool + to * cs[0] + t * cs[2] + at);
-        if (s >= 0) {  // stays; rounded anew where the scale grows
-          if (old != top) *dst = rescale16<kKind>(*dst, old, top);
-          continue;
-        }
-        const int from = mover[-1 - s], fm = from >> c.page_log2;
-        const int blk = checked_block(c, c.table, c.table_stride, b, fm);
-        if (blk < 0) continue;
-        const float sc = fm == p.keep >> c.page_log2 ? s_edge[is_v] : scales[(long long)blk * c.H + h];
-        *dst = rescale16<kKind>(
-            *reinterpret_cast<const uint4*>(pool + blk * cs[0] + (from & (c.page - 1)) * cs[2] + at), sc, top);
+        uint4* at = reinterpret_cast<uint4*>(out + (v >> vd_log2) * cs[2] + (v & (vd - 1)) * 16);
+        *at = rescale16<kKind>(*at, old, top);
       }
       __syncwarp();
-      if (lane == 0) scales[(long long)to * c.H + h] = top;
     }
-    for (int t = lane; t < tokens; t += 32) {
-      const int s = src[m0 + t];
-      if (s >= 0) continue;
-      p.weights[bh * p.W + m0 + t] = weight[mover[-1 - s]];
-      p.positions[bh * p.W + m0 + t] = position[mover[-1 - s]];
+    for (int v = lane; v < n * vd; v += 32) {
+      const int i = i0 + (v >> vd_log2), at = (v & (vd - 1)) * 16, from = mover_at(i);
+      int blk;
+      const float sc = scale_of(from, blk);
+      if (blk < 0) continue;
+      *reinterpret_cast<uint4*>(out + (hole_at(i) - m0) * cs[2] + at) = rescale16<kKind>(
+          *reinterpret_cast<const uint4*>(pool + blk * cs[0] + (from & (c.page - 1)) * cs[2] + at), sc, top);
     }
+    __syncwarp();
+    if (lane == 0) scales[(long long)to * c.H + h] = top;
+  }
+  for (int i = tid; i < moves; i += kPlanThreads) {
+    p.weights[bh * p.W + hole_at(i)] = weight[mover_at(i)];
+    p.positions[bh * p.W + hole_at(i)] = position[mover_at(i)];
   }
 }
 
-// Copies the tokens of one receiving block, or (past them) the lengths.
+// Copies the tokens of one receiving block, K and V.
 template <int kKind>
 __global__ void __launch_bounds__(256) cache_evict_copy_kernel(const EvictParams p) {
   const CacheView& c = p.c;
-  const int m = blockIdx.x, h = blockIdx.y % c.H, is_v = blockIdx.y / c.H, b = blockIdx.z, tid = threadIdx.x;
+  const int m = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long bh = (long long)b * c.H + h;
   const int j0 = m << c.page_log2;
-  __shared__ const uint8_t* s_from[128];
-  __shared__ float s_scale[128];
-  __shared__ float s_top[4];
+  __shared__ int s_blk[128], s_row[128];
+  __shared__ float2 s_scale[128];
+  __shared__ float2 s_top[4];
+  const int to = m < p.M_into ? checked_block_quiet(c, p.into, p.into_stride, b, m) : -1;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the choice is made
   const int count = p.count[bh];
-  if (m == 0 && blockIdx.y == 0 && tid == 0) p.lens_out[b] = count;
+  if (m == 0 && h == 0 && tid == 0) p.lens_out[b] = count;
   if (j0 >= count) return;
-  const int tokens = min(c.page, count - j0);
-  float* scales = is_v ? c.v_scale : c.k_scale;
-  const long long* cs = is_v ? c.vs : c.ks;
-  uint8_t* pool = (is_v ? c.v : c.k) + h * cs[1];
-  float top = 0.0f;
-  if (tid < tokens) {
-    const int s = p.src[bh * p.keep + j0 + tid];
-    const int blk = checked_block(c, c.table, c.table_stride, b, s >> c.page_log2);
-    s_from[tid] = blk >= 0 ? pool + blk * cs[0] + (s & (c.page - 1)) * cs[2] : nullptr;
-    s_scale[tid] = top = blk >= 0 ? scales[(long long)blk * c.H + h] : 0.0f;
-    if (!is_v) {
-      const long long at = bh * p.W_out + j0 + tid, from = bh * p.W + s;
-      if (p.weights_out) p.weights_out[at] = p.weights[from];
-      if (p.positions_out) p.positions_out[at] = p.positions ? p.positions[from] : s;
-    }
+  if (to < 0) {
+    if (tid == 0) flag_bad_index(c);
+    return;
   }
-  if (tid < 128) {
+  const int tokens = min(c.page, count - j0);
+  float2 top = make_float2(0.0f, 0.0f);
+  int from = 0;
+  if (tid < tokens) {
+    from = p.src[bh * p.keep + j0 + tid];
+    const int blk = checked_block(c, c.table, c.table_stride, b, from >> c.page_log2);
+    s_blk[tid] = blk;
+    s_row[tid] = from & (c.page - 1);
+    if (blk >= 0) top = make_float2(c.k_scale[(long long)blk * c.H + h], c.v_scale[(long long)blk * c.H + h]);
+    s_scale[tid] = top;
+  }
+  if (warp < 4) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    if ((tid & 31) == 0) s_top[tid >> 5] = top;
+    for (int o = 16; o > 0; o >>= 1) {
+      top.x = fmaxf(top.x, __shfl_xor_sync(0xFFFFFFFFu, top.x, o));
+      top.y = fmaxf(top.y, __shfl_xor_sync(0xFFFFFFFFu, top.y, o));
+    }
+    if (lane == 0) s_top[warp] = top;
   }
   __syncthreads();
-  top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
-  const int to = checked_block(c, p.into, p.into_stride, b, m);
-  if (to < 0) return;
-  uint8_t* out = pool + to * cs[0];
+  top = s_top[0];
+#pragma unroll
+  for (int w = 1; w < 4; ++w) top = make_float2(fmaxf(top.x, s_top[w].x), fmaxf(top.y, s_top[w].y));
+  const uint8_t *k_in = c.k + h * c.ks[1], *v_in = c.v + h * c.vs[1];
+  uint8_t *k_out = c.k + to * c.ks[0] + h * c.ks[1], *v_out = c.v + to * c.vs[0] + h * c.vs[1];
   const int vd = c.D >> 4, vd_log2 = 31 - __clz(vd);  // 16-byte vectors a token
-#pragma unroll 4
+#pragma unroll 2
   for (int v = tid; v < tokens * vd; v += 256) {
     const int t = v >> vd_log2, at = (v & (vd - 1)) * 16;
-    if (!s_from[t]) continue;
-    const uint4 w = *reinterpret_cast<const uint4*>(s_from[t] + at);
-    *reinterpret_cast<uint4*>(out + t * cs[2] + at) = rescale16<kKind>(w, s_scale[t], top);
+    const long long blk = s_blk[t], row = s_row[t];
+    if (blk < 0) continue;
+    const uint4 x = *reinterpret_cast<const uint4*>(k_in + blk * c.ks[0] + row * c.ks[2] + at);
+    const uint4 y = *reinterpret_cast<const uint4*>(v_in + blk * c.vs[0] + row * c.vs[2] + at);
+    *reinterpret_cast<uint4*>(k_out + t * c.ks[2] + at) = rescale16<kKind>(x, s_scale[t].x, top.x);
+    *reinterpret_cast<uint4*>(v_out + t * c.vs[2] + at) = rescale16<kKind>(y, s_scale[t].y, top.y);
   }
-  if (tid == 0) scales[(long long)to * c.H + h] = top;
+  if (tid == 0) {
+    c.k_scale[(long long)to * c.H + h] = top.x;
+    c.v_scale[(long long)to * c.H + h] = top.y;
+  }
+  if (tid < tokens) {
+    const long long at = bh * p.W_out + j0 + tid, src = bh * p.W + from;
+    if (p.weights_out) p.weights_out[at] = p.weights[src];
+    if (p.positions_out) p.positions_out[at] = p.positions ? p.positions[src] : from;
+  }
 }
 
 // In place, and lens itself is to change: once every head has read it.
@@ -358,7 +396,7 @@ int launch(const EvictParams& p, const LaunchCtx& ctx) {
   if (e == cudaSuccess) {
     if (p.into)
       e = launch_after(cache_evict_copy_kernel<kKind>,
-                       dim3((unsigned)((p.keep + p.c.page - 1) / p.c.page), (unsigned)(2 * p.c.H), (unsigned)p.B), 256,
+                       dim3((unsigned)((p.keep + p.c.page - 1) / p.c.page), (unsigned)p.c.H, (unsigned)p.B), 256,
                        ctx.stream, p);
     else if (p.lens_out == p.lens)
       e = launch_after(cache_evict_lens_kernel, dim3((unsigned)((p.B + 127) / 128)), 128, ctx.stream, p);

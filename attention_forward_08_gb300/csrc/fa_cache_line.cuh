@@ -225,39 +225,67 @@ __device__ __forceinline__ DecPlace dec_before(const DecParams& p, int b) {
   return at;
 }
 
-// Joins the parts of a cut segment: the block of the first cut inside it sums
-// them, in order, four columns of a row a thread (128 threads: 512 / D rows,
-// `piece` of the segment's).
+// Joins the parts of a cut segment, by the block of the first cut inside it:
+// four columns a thread.  Of few rows a block takes 512 / D (`piece` of the
+// segment's), every fourth part a quarter of the block, whose sums are added in
+// order (38 parts a segment: one sequence of 131071 tokens in all 57.7 us with
+// one thread a column for all parts, 52.4 so); of many, four times as many.
+constexpr int kJoinThreads = 512;
+template <class C>
+constexpr bool kJoinByParts = C::kRows <= 32;
+
 template <class C>
 __device__ __forceinline__ void join_parts(const DecParams& p, int piece, int cut) {
   const CacheAttnParams& a = p.a;
-  constexpr int kRowsHere = 512 / C::kD;  // rows a block
-  const int tid = threadIdx.x;
+  constexpr int kRowsHere = 512 / C::kD;  // rows a quarter
+  constexpr bool kByParts = kJoinByParts<C>;
+  const int tid = threadIdx.x % 128, quarter = threadIdx.x / 128;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   DecPlace at;
   const bool in = dec_find<C>(p, cut, at);
   const int t = at.part * cut;
-  const int r = piece * kRowsHere + tid / (C::kD / 4), row = at.rg * C::kRows + r, d = tid % (C::kD / 4) * 4;
+  const int r = (kByParts ? piece : piece * 4 + quarter) * kRowsHere + tid / (C::kD / 4), row = at.rg * C::kRows + r, d = tid % (C::kD / 4) * 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
-  if (!in || at.seg0 == t || at.seg0 < t - at.part || row >= p.rows) return;
+  if (!in || at.seg0 == t || at.seg0 < t - at.part) return;
   const int c1 = (at.seg0 + dec_tiles<C>(p, at.seq, at.rg) - 1) / at.part;
   float top = -INFINITY, sum = 0.0f;
   float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-  for (int i = cut - 1; i <= c1; ++i) {
-    const long long slot = (long long)(2 * i + (i == cut - 1)) * C::kRows + r;
-    const float2 ml = __ldcg(p.part_ml + slot);
-    const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part_o + slot * C::kD + d));
+  auto add = [&](float2 ml, float4 y) {
     const float m2 = fmaxf(top, ml.x), z = m2 == -INFINITY ? 0.0f : m2;
     const float f = ex2(top - z), g = ex2(ml.x - z);
     top = m2;
     sum = fmaf(sum, f, ml.y * g);
     x.x = fmaf(x.x, f, y.x * g), x.y = fmaf(x.y, f, y.y * g), x.z = fmaf(x.z, f, y.z * g), x.w = fmaf(x.w, f, y.w * g);
+  };
+  if (row < p.rows) {
+#pragma unroll 4
+    for (int i = cut - 1 + (kByParts ? quarter : 0); i <= c1; i += kByParts ? 4 : 1) {
+      const long long slot = (long long)(2 * i + (i == cut - 1)) * C::kRows + r;
+      add(__ldcg(p.part_ml + slot), __ldcg(reinterpret_cast<const float4*>(p.part_o + slot * C::kD + d)));
+    }
   }
-  dec_write<C>(a, at.b, at.h, row, d, x, top, sum);
+  if constexpr (kByParts) {
+    __shared__ float4 s_x[3][128];
+    __shared__ float2 s_ml[3][128];
+    if (quarter > 0) {
+      s_x[quarter - 1][tid] = x;
+      s_ml[quarter - 1][tid] = make_float2(top, sum);
+    }
+    __syncthreads();
+    if (quarter > 0) return;
+#pragma unroll
+    for (int q = 0; q < 3; ++q) add(s_ml[q][tid], s_x[q][tid]);
+  }
+  if (row < p.rows) dec_write<C>(a, at.b, at.h, row, d, x, top, sum);
+}
+// Blocks of one cut: no more rows than a segment can have.
+template <class C>
+__host__ __device__ __forceinline__ int join_pieces(const DecParams& p) {
+  const int rows = p.rows < C::kRows ? p.rows : C::kRows, here = 512 / C::kD * (kJoinByParts<C> ? 1 : 4);
+  return (rows + here - 1) / here;
 }
 template <class C>
-__global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__ DecParams p) {
+__global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ DecParams p) {
   join_parts<C>(p, blockIdx.x, blockIdx.y + 1);
 }
 

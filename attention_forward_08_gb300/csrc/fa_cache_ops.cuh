@@ -95,7 +95,12 @@ __device__ __forceinline__ int checked_len(const CacheView& c, int len) {
   return len;
 }
 
-// The block of sequence b's tokens m * page .., or -1 for an entry out of range.
+// A table's entry, or -1 for one out of range: without telling, or telling.
+__device__ __forceinline__ int checked_block_quiet(const CacheView& c, const int* table, long long stride, int b, int m) {
+  const int at = table[b * stride + m];
+  return at < 0 || at >= c.P ? -1 : at;
+}
+// The block of sequence b's tokens m * page ..
 __device__ __forceinline__ int checked_block(const CacheView& c, const int* table, long long stride, int b, int m) {
   const int at = table[b * stride + m];
   if (at < 0 || at >= c.P) {

@@ -62,8 +62,8 @@ struct EvictParams {
   int B, W, M_into, W_out;
   int keep, recent;
   // Workspace: what the choice tells the moves.
-  int* src;         // [B, H, keep]: the slot whose token ends in slot j; -1 - i: that of mover i (in place)
-  int* mover;       // [B, H, keep]: kept slots at `keep` and behind, in order (in place)
+  int* src;         // [B, H, keep]: a copy: the slot whose token ends in slot j; in place: the receiving slots, in order
+  int* mover;       // [B, H, keep]: in place: kept slots at `keep` and behind, in order
   int* count;       // [B, H]: tokens kept
 };
 

@@ -174,14 +174,14 @@ __global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constan
 // scores, 4 bytes a row and token, and one kernel joins the parts of cut
 // segments (its first `joins` blocks) and sums the weights, a thread a token.
 // A block finds the rows' L where the parts say so: a few numbers a row.
-constexpr int kFinishTokens = 512;  // a block
+constexpr int kFinishTokens = kJoinThreads;  // a block
 
 template <class C>
-__global__ void __launch_bounds__(128) cache_finish_kernel(const __grid_constant__ DecParams p, int joins, int chunks) {
+__global__ void __launch_bounds__(kJoinThreads) cache_finish_kernel(const __grid_constant__ DecParams p, int joins, int chunks) {
   const CacheAttnParams& a = p.a;
-  constexpr int kPieces = C::kRows * C::kD / 512;
   if ((int)blockIdx.x < joins) {
-    join_parts<C>(p, blockIdx.x % kPieces, blockIdx.x / kPieces + 1);
+    const int pieces = join_pieces<C>(p);
+    join_parts<C>(p, blockIdx.x % pieces, blockIdx.x / pieces + 1);
     return;
   }
   __shared__ float s_l2[C::kRows];
@@ -214,19 +214,16 @@ __global__ void __launch_bounds__(128) cache_finish_kernel(const __grid_constant
   __syncthreads();
   const float* scores = p.scores + (long long)bh * ((a.c.M * (a.c.page >> 4) + 1) / 2) * p.rows * 32;
   float* out = a.weights + (long long)bh * a.W;
-#pragma unroll
-  for (int i = 0; i < kFinishTokens / 128; ++i) {
-    const int tok = tok0 + i * 128 + tid;
-    if (tok < span.x || tok >= span.y) continue;
-    const float* s = scores + (long long)(tok >> 5) * p.rows * 32 + (tok & 31);
-    float sum = 0.0f;
+  const int tok = tok0 + tid;
+  if (tok < span.x || tok >= span.y) return;
+  const float* s = scores + (long long)(tok >> 5) * p.rows * 32 + (tok & 31);
+  float sum = 0.0f;
 #pragma unroll 4
-    for (int r = 0; r < p.rows; ++r) sum += ex2(__ldcg(s + r * 32) - s_l2[r]);
-    if (tok < a.W)
-      out[tok] += sum;
-    else
-      flag_bad_index(a.c);
-  }
+  for (int r = 0; r < p.rows; ++r) sum += ex2(__ldcg(s + r * 32) - s_l2[r]);
+  if (tok < a.W)
+    out[tok] += sum;
+  else
+    flag_bad_index(a.c);
 }
 
 }  // namespace fa
