@@ -1,15 +1,16 @@
 // fa_cache_evict.cu -- keep the heaviest and latest tokens (include/fa_cache.h).
 //
-// The choice: one thread block per sequence and head searches the key above
-// which `keep` tokens lie, by counting: every pass counts the keys at and above
-// three values that quarter the range left, until one has exactly `keep` (after
-// 8 or 9 passes where weights differ, 17 at most), and then writes for every
-// slot below `keep` which slot's token ends there.  The keys stay in shared
-// memory where they fit.  (A radix selection, 8 bits a pass, took 15,000 cycles
-// for 2049 tokens and 21,000 for 16000, nearly all of it in atomics on the few
-// counters that float exponents share; this takes TIMES.)  A copy into other
-// blocks then moves by a second launch, one thread block per (sequence, head,
-// receiving block).
+// The choice: one thread block per sequence and head finds the key of the last
+// token that is kept, and writes for every slot below `keep` which slot's token
+// ends there.  Keys that are not protected are counted in 2048 classes that
+// split their own range evenly, so that weights spread over the classes
+// whatever their size (classes by leading bits would hold a few exponents, and
+// their counters cost 15,000 cycles in atomics at 2049 tokens); the class in
+// which the count from above reaches `keep` is settled by comparing its keys
+// with one another where they are few, else split again (three times at most:
+// 11 of 32 bits each).  The keys stay in shared memory where they fit.  A copy
+// into other blocks then moves by a second launch, one thread block per
+// (sequence, head, receiving block).
 //
 // In place, only tokens in slots at `keep` and behind move, and only into
 // slots below `keep`: no slot is both read and written, so the moves need no
@@ -41,12 +42,6 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__device__ __forceinline__ int warp_sum(int v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
-}
-
 constexpr int kFewMoves = 1024;  // in place: lists in shared memory, else in the workspace
 // Tokens whose keys fit shared memory (184 KB).
 constexpr int kCachedKeys = 47104;
@@ -66,119 +61,162 @@ __device__ __forceinline__ uint4 rescale16(uint4 w, float from, float to) {
   return w;
 }
 
-__device__ int block_count(int v, uint2 (*tmp)[kPlanWarps]) {
-  v = __reduce_add_sync(0xFFFFFFFFu, v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) tmp[0][threadIdx.x >> 5].x = (uint32_t)v;
-  __syncthreads();
-  return __reduce_add_sync(0xFFFFFFFFu, (int)tmp[0][threadIdx.x & 31].x);
-}
+constexpr int kClasses = 2048, kFewKeys = 256;
 
-template <int kKind>
-__global__ void __launch_bounds__(kPlanThreads) cache_evict_plan_kernel(const EvictParams p, int cached) {
-  const CacheView& c = p.c;
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const long long bh = (long long)b * c.H + h;
-  extern __shared__ uint32_t s_key[];
-  __shared__ uint2 s_count[2][kPlanWarps];
-  __shared__ int part[kPlanWarps][4];
-  __shared__ int s_max;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int n = checked_len(c, p.lens[b]);
-  if (n > p.W) {
-    if (tid == 0) flag_bad_index(c);
-    n = p.W;
-  }
-  int* src = p.src + bh * p.keep;
+struct PlanShared {
+  int count[kClasses];
+  uint32_t few[kFewKeys];
+  int part[kPlanWarps][4];
+  int hole[kFewMoves], mover[kFewMoves];
+  int latest, n_few, total;
+  uint32_t least, most, digit_over;  // range of the keys; the class found
+  int over, inside;
+  uint32_t found;
+  int need;
+  float edge[2];
+};
+
+// The choice for one head of n > keep tokens; kCached: the keys fit `s_key`.
+// Returns the number of moves (in place), whose slots are in `s` if few, else
+// in `src` and `mover`; of a copy, `src` is the answer.
+template <bool kCached>
+__device__ __forceinline__ int choose(const EvictParams& p, PlanShared& s, uint32_t* s_key, int n, const float* weight,
+                                      const int* position, int* src, int* mover) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t first = weight_key(INFINITY);
+  const int stop = (n + 31) & ~31;  // (whole warps stay together)
+  for (int i = tid; i < kClasses; i += kPlanThreads) s.count[i] = 0;
   if (tid == 0) {
-    p.count[bh] = min(n, p.keep);
-    if (!p.into && p.lens_out != p.lens && h == 0) p.lens_out[b] = min(n, p.keep);
-    s_max = INT_MIN;
+    s.latest = INT_MIN;
+    s.n_few = s.total = 0;
+    s.least = ~0u;
+    s.most = 0u;
   }
-  if (n <= p.keep) {  // all stay (a copy takes them all, in order)
-    if (p.into)
-      for (int j = tid; j < n; j += kPlanThreads) src[j] = j;
-    return;
-  }
-  const float* weight = p.weights + bh * p.W;
-  const int* position = p.positions ? p.positions + bh * p.W : nullptr;
   __syncthreads();
-  const bool in_smem = n <= cached;
-  if (p.recent > 0 || in_smem) {
+  if (kCached || p.recent > 0) {
     int most = position ? INT_MIN : n - 1;
 #pragma unroll 4
     for (int j = tid; j < n; j += kPlanThreads) {
-      if (in_smem) s_key[j] = weight_key(weight[j]);
+      if (kCached) s_key[j] = weight_key(weight[j]);
       if (p.recent > 0 && position) most = max(most, position[j]);
     }
     most = __reduce_max_sync(0xFFFFFFFFu, most);
-    if (lane == 0) atomicMax(&s_max, most);
+    if (lane == 0) atomicMax(&s.latest, most);
+    __syncthreads();
   }
-  __syncthreads();
   // Positions above the bound are kept first (long: the bound may lie below INT_MIN).
-  const long long late = p.recent > 0 ? (long long)s_max - p.recent : LLONG_MAX;
-  const uint32_t first = weight_key(INFINITY);
+  const long long late = p.recent > 0 ? (long long)s.latest - p.recent : LLONG_MAX;
   auto key_of = [&](int j) -> uint32_t {
     const long long pos = p.recent > 0 && position ? position[j] : j;
     return pos > late ? first : weight_key(weight[j]);
   };
-  if (in_smem && p.recent > 0) {
-#pragma unroll 4
-    for (int j = tid; j < n; j += kPlanThreads)
-      if ((position ? position[j] : j) > late) s_key[j] = first;
-  }
-  if (in_smem) __syncthreads();
-  auto key = [&](int j) -> uint32_t { return in_smem ? s_key[j] : key_of(j); };
-  // At least `keep` keys are >= lo, fewer (`over`) are >= hi.
-  uint32_t lo = 0, hi = first + 1, found;
-  int over = 0, need = 0;
-#pragma unroll 1
-  for (int pass = 0;; ++pass) {
-    const uint32_t step = (hi - lo) / 4;
-    if (hi - lo == 1) {  // the last key that is kept, not all of it perhaps
-      found = lo;
-      need = p.keep - over;
-      break;
-    }
-    const uint32_t m1 = lo + max(step, 1u), m2 = step ? m1 + step : m1, m3 = step ? m2 + step : m1;
-    uint32_t c12 = 0, c3 = 0;
+  auto key = [&](int j) -> uint32_t { return kCached ? s_key[j] : key_of(j); };
+  {  // protected tokens, and the others' range
+    uint32_t least = ~0u, most = 0u;
+    int sure = 0;
 #pragma unroll 4
     for (int j = tid; j < n; j += kPlanThreads) {
-      const uint32_t k = key(j);
-      c12 += (k >= m1 ? 1u : 0u) + (k >= m2 ? 0x10000u : 0u);
-      c3 += k >= m3 ? 1u : 0u;
+      uint32_t k;
+      if (kCached) {
+        k = s_key[j];
+        if (p.recent > 0 && (position ? position[j] : j) > late) s_key[j] = k = first;
+      } else {
+        k = key_of(j);
+      }
+      if (k == first) {
+        ++sure;
+      } else {
+        least = min(least, k);
+        most = max(most, k);
+      }
     }
-    // (n of up to 47104 counts in 16 bits; more, whose keys are not in shared
-    // memory, one by one)
-    int n1, n2, n3;
-    if (in_smem) {
-      c12 = __reduce_add_sync(0xFFFFFFFFu, c12);
-      c3 = __reduce_add_sync(0xFFFFFFFFu, c3);
-      if (lane == 0) s_count[pass & 1][warp] = make_uint2(c12, c3);
-      __syncthreads();
-      const uint2 c = s_count[pass & 1][lane];
-      c12 = __reduce_add_sync(0xFFFFFFFFu, c.x);
-      n1 = c12 & 0xFFFF, n2 = c12 >> 16, n3 = __reduce_add_sync(0xFFFFFFFFu, c.y);
-    } else {
-      n1 = block_count(c12 & 0xFFFF, s_count);
-      n2 = block_count(c12 >> 16, s_count);
-      n3 = block_count(c3, s_count);
+    least = __reduce_min_sync(0xFFFFFFFFu, least);
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
+    sure = __reduce_add_sync(0xFFFFFFFFu, sure);
+    if (lane == 0) {
+      atomicMin(&s.least, least);
+      atomicMax(&s.most, most);
+      atomicAdd(&s.total, sure);
     }
-    // (in order: m1 <= m2 <= m3, n1 >= n2 >= n3)
-    const uint32_t m[3] = {m1, m2, m3};
-    const int c[3] = {n1, n2, n3};
-    bool exact = false;
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      if (c[i] == p.keep) exact = true, found = m[i] - 1;
-      if (c[i] >= p.keep) lo = m[i];
-    }
-#pragma unroll
-    for (int i = 2; i >= 0; --i)
-      if (c[i] < p.keep) hi = m[i], over = c[i];
-    if (exact) break;  // all above `found`, none of it
+    __syncthreads();
   }
   // Kept: keys above `found`, and the first `need` slots whose key equals it.
+  uint32_t found = first;
+  int need = p.keep;
+  if (s.total < p.keep) {
+    uint32_t lo = s.least;                               // the key sought lies in lo .. lo + width
+    int bits = 32 - __clz(s.most - lo), over = s.total;  // width < 2^bits; keys above the range
+#pragma unroll 1
+    while (true) {
+      const int shift = max(bits - 11, 0);
+      const uint32_t width = bits == 32 ? ~0u : (1u << bits) - 1u;
+#pragma unroll 4
+      for (int j = tid; j < stop; j += kPlanThreads) {
+        const uint32_t k = j < n ? key(j) : first, at = (k - lo) >> shift;
+        const bool in = k >= lo && k - lo <= width && k != first;
+        // (ties crowd into a class: lanes that all agree count once)
+        const uint32_t here = in ? at : ~0u, lead = __shfl_sync(0xFFFFFFFFu, here, 0);
+        if (__all_sync(0xFFFFFFFFu, here == lead)) {
+          if (lane == 0 && in) atomicAdd(&s.count[at], 32);
+        } else if (in) {
+          atomicAdd(&s.count[at], 1);
+        }
+      }
+      __syncthreads();
+      // The class at which the count from above reaches `keep`: two a thread.
+      const int c1 = kClasses - 1 - 2 * tid, upper = s.count[c1], lower = s.count[c1 - 1];
+      int upto = upper + lower;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o) upto += t;
+      }
+      if (lane == 31) s.part[warp][0] = upto;
+      __syncthreads();
+      s.count[c1] = s.count[c1 - 1] = 0;
+      const int before = over + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? s.part[lane][0] : 0) + upto - upper - lower;
+      if (before < p.keep && before + upper + lower >= p.keep) {
+        const bool second = before + upper < p.keep;
+        s.digit_over = (uint32_t)(second ? c1 - 1 : c1);
+        s.over = second ? before + upper : before;
+        s.inside = second ? lower : upper;
+      }
+      __syncthreads();
+      lo += s.digit_over << shift;
+      over = s.over;
+      const int inside = s.inside;
+      bits = shift;
+      if (bits == 0) {  // one key is left
+        found = lo;
+        need = p.keep - over;
+        break;
+      }
+      if (inside <= kFewKeys) {  // compare its keys with one another
+#pragma unroll 4
+        for (int j = tid; j < n; j += kPlanThreads) {
+          const uint32_t k = key(j);
+          if (k >= lo && k != first && (k - lo) >> shift == 0u) s.few[atomicAdd(&s.n_few, 1)] = k;
+        }
+        __syncthreads();
+        if (tid < inside) {
+          const uint32_t k = s.few[tid];
+          int above = 0, equal = 0;
+          for (int i = 0; i < inside; ++i) {
+            above += s.few[i] > k;
+            equal += s.few[i] == k;
+          }
+          if (over + above < p.keep && over + above + equal >= p.keep) {  // (all that find it find the same)
+            s.found = k;
+            s.need = p.keep - over - above;
+          }
+        }
+        __syncthreads();
+        found = s.found;
+        need = s.need;
+        break;
+      }
+    }
+  }
   // Every warp owns a run of slots; a first sweep counts what lies before it.
   // In place, with `kept_lo` of the slots below `keep` kept: the slot j that
   // becomes free is hole number j - (kept slots before j), and a kept slot at
@@ -190,67 +228,90 @@ __global__ void __launch_bounds__(kPlanThreads) cache_evict_plan_kernel(const Ev
 #pragma unroll 4
   for (int j = j0 + lane; j < j1; j += 32) {
     const uint32_t k = key(j);
-    const bool lo = j < p.keep;
-    above += k > found;
-    equal += k == found;
-    above_lo += lo && k > found;
-    equal_lo += lo && k == found;
+    const int lo = j < p.keep ? 1 : 0, a = k > found ? 1 : 0, e = k == found ? 1 : 0;
+    above += a;
+    equal += e;
+    above_lo += a & lo;
+    equal_lo += e & lo;
   }
-  above = warp_sum(above);
-  equal = warp_sum(equal);
-  above_lo = warp_sum(above_lo);
-  equal_lo = warp_sum(equal_lo);
-  if (lane == 0) part[warp][0] = above, part[warp][1] = equal, part[warp][2] = above_lo, part[warp][3] = equal_lo;
+  above = __reduce_add_sync(0xFFFFFFFFu, above);
+  equal = __reduce_add_sync(0xFFFFFFFFu, equal);
+  above_lo = __reduce_add_sync(0xFFFFFFFFu, above_lo);
+  equal_lo = __reduce_add_sync(0xFFFFFFFFu, equal_lo);
+  if (lane == 0) *reinterpret_cast<int4*>(s.part[warp]) = make_int4(above, equal, above_lo, equal_lo);
   __syncthreads();
-  int eq = 0, kept_n = 0, kept_lo = 0, eq_lo = 0;
-  for (int w = 0; w < kPlanWarps; ++w) {
-    if (w < warp) {
-      kept_n += part[w][0];
-      eq += part[w][1];
-    }
-    kept_lo += part[w][2];
-    eq_lo += part[w][3];
-  }
-  kept_n += min(eq, need);
-  kept_lo += min(eq_lo, need);
-  int* mover = p.mover + bh * p.keep;
-  // In place, the receiving slots in order (the movers' list has as many).
-  __shared__ int s_hole[kFewMoves], s_mover[kFewMoves];
+  const int4 their = *reinterpret_cast<const int4*>(s.part[lane]);
+  int eq = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? their.y : 0);
+  int kept_n = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? their.x : 0) + min(eq, need);
+  const int kept_lo = __reduce_add_sync(0xFFFFFFFFu, their.z) + min(__reduce_add_sync(0xFFFFFFFFu, their.w), need);
   const int moves = p.keep - kept_lo;
   const bool few = moves <= kFewMoves;
   const uint32_t below = (1u << lane) - 1;
-  for (int base = j0; base < j1; base += 32) {
-    const int j = base + lane;
-    const bool in = j < j1;
-    const uint32_t k = in ? key(j) : 0;
-    const uint32_t e = __ballot_sync(0xFFFFFFFFu, in && k == found);
-    const bool kept = in && (k > found || (k == found && eq + __popc(e & below) < need));
-    const uint32_t kb = __ballot_sync(0xFFFFFFFFu, kept);
-    const int at = kept_n + __popc(kb & below);  // kept slots before j
-    if (p.into) {
-      if (kept) src[at] = j;
-    } else if (few) {
-      if (in && j < p.keep && !kept) s_hole[j - at] = j;
-      if (kept && j >= p.keep) s_mover[at - kept_lo] = j;
-    } else if (in && j < p.keep) {
-      if (!kept) src[j - at] = j;
-    } else if (kept) {
-      mover[at - kept_lo] = j;
+  for (int base = j0; base < j1; base += 128) {
+    uint32_t k4[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) k4[u] = base + 32 * u + lane < j1 ? key(base + 32 * u + lane) : 0u;  // (0: below all)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = base + 32 * u + lane;
+      const bool in = j < j1;
+      const uint32_t k = k4[u], e = __ballot_sync(0xFFFFFFFFu, in && k == found);
+      const bool kept = in && (k > found || (k == found && eq + __popc(e & below) < need));
+      const uint32_t kb = __ballot_sync(0xFFFFFFFFu, kept);
+      const int at = kept_n + __popc(kb & below);  // kept slots before j
+      if (p.into) {
+        if (kept) src[at] = j;
+      } else if (in && j < p.keep) {
+        if (!kept) (few ? s.hole : src)[j - at] = j;
+      } else if (kept) {
+        (few ? s.mover : mover)[at - kept_lo] = j;
+      }
+      kept_n += __popc(kb);
+      eq += __popc(e);
     }
-    kept_n += __popc(kb);
-    eq += __popc(e);
   }
+  return moves;
+}
+
+template <int kKind>
+__global__ void __launch_bounds__(kPlanThreads) cache_evict_plan_kernel(const EvictParams p, int cached) {
+  const CacheView& c = p.c;
+  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const long long bh = (long long)b * c.H + h;
+  extern __shared__ uint32_t s_key[];
+  __shared__ __align__(16) PlanShared s;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int n = checked_len(c, p.lens[b]);
+  if (n > p.W) {
+    if (tid == 0) flag_bad_index(c);
+    n = p.W;
+  }
+  int* src = p.src + bh * p.keep;
+  int* mover = p.mover + bh * p.keep;
+  if (tid == 0) {
+    p.count[bh] = min(n, p.keep);
+    if (!p.into && p.lens_out != p.lens && h == 0) p.lens_out[b] = min(n, p.keep);
+  }
+  if (n <= p.keep) {  // all stay (a copy takes them all, in order)
+    if (p.into)
+      for (int j = tid; j < n; j += kPlanThreads) src[j] = j;
+    return;
+  }
+  const float* weight = p.weights + bh * p.W;
+  const int* position = p.positions ? p.positions + bh * p.W : nullptr;
+  const int moves = n <= cached ? choose<true>(p, s, s_key, n, weight, position, src, mover)
+                                : choose<false>(p, s, s_key, n, weight, position, src, mover);
   if (p.into) return;
   // The moves in place.  The block of slot `keep` may hold sources and receive
   // as well: its scales from before.
-  __shared__ float s_edge[2];
   if (tid < 2) {
     const int blk = checked_block(c, c.table, c.table_stride, b, p.keep >> c.page_log2);
-    s_edge[tid] = blk < 0 ? 0.0f : (tid ? c.v_scale : c.k_scale)[(long long)blk * c.H + h];
+    s.edge[tid] = blk < 0 ? 0.0f : (tid ? c.v_scale : c.k_scale)[(long long)blk * c.H + h];
   }
   __syncthreads();
-  auto hole_at = [&](int i) { return few ? s_hole[i] : src[i]; };
-  auto mover_at = [&](int i) { return few ? s_mover[i] : mover[i]; };
+  const bool few = moves <= kFewMoves;
+  auto hole_at = [&](int i) { return few ? s.hole[i] : src[i]; };
+  auto mover_at = [&](int i) { return few ? s.mover[i] : mover[i]; };
   // A warp takes the moves into one block, of K or of V, from the first of them.
   for (int w = warp; w < 2 * moves; w += kPlanWarps) {
     const int i0 = w >> 1, is_v = w & 1, m = hole_at(i0) >> c.page_log2;
@@ -263,7 +324,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_evict_plan_kernel(const Ev
     auto scale_of = [&](int from, int& blk) -> float {
       const int fm = from >> c.page_log2;
       blk = checked_block(c, c.table, c.table_stride, b, fm);
-      return blk < 0 ? 0.0f : fm == p.keep >> c.page_log2 ? s_edge[is_v] : scales[(long long)blk * c.H + h];
+      return blk < 0 ? 0.0f : fm == p.keep >> c.page_log2 ? s.edge[is_v] : scales[(long long)blk * c.H + h];
     };
     // The largest scale of the blocks that the block's tokens come from, its
     // own among them unless all its tokens are new.
