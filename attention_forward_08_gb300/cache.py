@@ -138,26 +138,56 @@ def kv_cache(pages, H_kv, D, *, page=64, dtype=None, device="cuda") -> KVCache:
     return KVCache(k, v, ks, vs)
 
 
+# The checks below run on every call of a decoding loop: each reads an attribute once.
+
 def _on(device, name, t, dtype, shape=None):
     """An argument tensor: dtype, shape, contiguous, on the cache's device."""
-    if t.dtype != dtype or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name} must be {dtype}" + (f" {shape}" if shape is not None else "") +
+    if t.dtype is not dtype or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be {dtype}" + (f" {tuple(shape)}" if shape is not None else "") +
                          f" (got {t.dtype} {tuple(t.shape)})")
     if t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor on {device}")
     return t.data_ptr()
 
 
-def _table(a, cache, table, lens, B):
+def _table(device, name, table, B, width):
+    """An int32 [B, M] table, unit inner stride: (pointer, row stride, M)."""
     import torch
-    if table.dim() != 2 or table.shape[0] != B or table.dtype != torch.int32 or table.device != cache.device:
-        raise ValueError(f"table must be an int32 [B = {B}, M] tensor on {cache.device} "
-                         f"(got {table.dtype} {tuple(table.shape)})")
-    if table.shape[1] > 1 and table.stride(1) != 1:
-        raise ValueError("table must have unit stride along its last dimension")
-    a.cache = cache.c
-    a.table, a.table_stride, a.B, a.M = table.data_ptr(), table.stride(0), B, table.shape[1]
-    a.lens = _on(cache.device, "lens", lens, torch.int32, (B,))
+    shape = table.shape
+    if len(shape) != 2 or shape[0] != B or table.dtype is not torch.int32 or table.device != device:
+        raise ValueError(f"{name} must be an int32 [B = {B}, {width}] tensor on {device} "
+                         f"(got {table.dtype} {tuple(shape)})")
+    strides = table.stride()
+    if strides[1] != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    return table.data_ptr(), strides[0], shape[1]
+
+
+def _rows(name, t):
+    """Strides {batch, head, row} of a 4-D tensor with unit inner stride."""
+    strides = t.stride()
+    if strides[3] != 1:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    return strides[:3]
+
+
+def _trackers(device, H, weights, positions, B):
+    """(weights pointer, positions pointer, W) of fp32 and int32 [B, H_kv, W] trackers, each of which may be None."""
+    import torch
+    w = p = None
+    W = 0
+    if weights is not None:
+        if weights.dim() != 3:
+            raise ValueError(f"weights must be [B, H_kv, W] (got {tuple(weights.shape)})")
+        W = weights.shape[2]
+        w = _on(device, "weights", weights, torch.float32, (B, H, W))
+    if positions is not None:
+        if positions.dim() != 3 or (weights is not None and positions.shape[2] != W):
+            raise ValueError(f"positions must be [B, H_kv, W], W common to weights and positions "
+                             f"(got {tuple(positions.shape)})")
+        W = positions.shape[2]
+        p = _on(device, "positions", positions, torch.int32, (B, H, W))
+    return w, p, W
 
 
 _DTYPES = {}
@@ -168,9 +198,10 @@ def _dtype(t, name):
     if not _DTYPES:
         _DTYPES.update({torch.float32: _fa.FA_DTYPE_F32, torch.bfloat16: _fa.FA_DTYPE_BF16,
                         torch.float16: _fa.FA_DTYPE_F16})
-    if t.dtype not in _DTYPES:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
         raise ValueError(f"{name} dtype {t.dtype} is not bfloat16, float16 or float32")
-    return _DTYPES[t.dtype]
+    return code
 
 
 @contextlib.contextmanager
@@ -195,23 +226,29 @@ def _call(device, stream, work):
         return work(torch.cuda.current_stream(device).cuda_stream)
 
 
-def _scratch(a, need, workspace, device):
-    """Attach ``need`` bytes of scratch: ``workspace`` if given, else new memory of the current stream."""
+def _with_scratch(a, need, workspace, device, call):
+    """Run ``call(a)`` with ``need`` bytes of scratch: ``workspace`` if given, else memory of the stream, taken straight
+    from torch's caching allocator (a tensor around it would cost a decoding loop more than the memory does) and given
+    back behind the call: the allocator hands it out again only to work queued later on the same stream."""
     import torch
     if need < 0:
         _fa._check(_fa.FA_ERR_INVALID_ARGUMENT)
-    if need == 0 and workspace is None:
-        return None
-    if workspace is None:
-        workspace = torch.empty(need + 256, dtype=torch.uint8, device=device)
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
-    base = workspace.data_ptr()
-    start = (base + 255) // 256 * 256
-    if workspace.numel() * workspace.element_size() - (start - base) < need:
-        raise ValueError(f"workspace holds fewer than the {need} bytes (256-byte aligned) required")
-    a.workspace, a.workspace_bytes = start, need
-    return workspace
+    if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
+        base = workspace.data_ptr()
+        start = (base + 255) // 256 * 256
+        if workspace.numel() * workspace.element_size() - (start - base) < need:
+            raise ValueError(f"workspace holds fewer than the {need} bytes (256-byte aligned) required")
+        a.workspace, a.workspace_bytes = start, need
+        _fa._check(call(a))
+        return
+    base = torch._C._cuda_cudaCachingAllocator_raw_alloc(need + 256, a.stream or 0)
+    try:
+        a.workspace, a.workspace_bytes = (base + 255) // 256 * 256, need
+        _fa._check(call(a))
+    finally:
+        torch._C._cuda_cudaCachingAllocator_raw_delete(base)
 
 
 def cache_append(cache, k, v, table, lens, *, n_new=None, weights=None, positions=None, seen=None, stream=None):
@@ -226,44 +263,30 @@ def cache_append(cache, k, v, table, lens, *, n_new=None, weights=None, position
     larger; where it grows, the block's older tokens are rounded to it.  ``lens`` is not changed.
     """
     import torch
-    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+    shape, device, c = k.shape, cache.device, cache.c
+    if len(shape) != 4 or shape != v.shape or k.dtype is not v.dtype:
         raise ValueError(f"k and v must be 4-D [B, H_kv, n, D] and alike (got {tuple(k.shape)} {k.dtype}, "
                          f"{tuple(v.shape)} {v.dtype})")
-    B, H, n, D = k.shape
-    if (H, D) != (cache.c.H_kv, cache.c.D):
-        raise ValueError(f"k has {H} heads of {D}, the cache {cache.c.H_kv} of {cache.c.D}")
-    if k.device != cache.device or v.device != cache.device:
-        raise ValueError(f"k and v must be CUDA tensors on {cache.device}")
+    B, H, n, D = shape
+    if H != c.H_kv or D != c.D:
+        raise ValueError(f"k has {H} heads of {D}, the cache {c.H_kv} of {c.D}")
+    if k.device != device or v.device != device:
+        raise ValueError(f"k and v must be CUDA tensors on {device}")
+    t_ptr, t_stride, M = _table(device, "table", table, B, "M")
+    l_ptr = _on(device, "lens", lens, torch.int32, (B,))
+    n_ptr = None if n_new is None else _on(device, "n_new", n_new, torch.int32, (B,))
+    s_ptr = None if seen is None else _on(device, "seen", seen, torch.int32, (B,))
+    w_ptr, p_ptr, W = _trackers(device, H, weights, positions, B)
+    dtype, ks, vs = _dtype(k, "k"), _rows("k", k), _rows("v", v)
     if B == 0 or n == 0:
         return
-    a = FaCacheAppendArgs()
-    _table(a, cache, table, lens, B)
-    a.k, a.v, a.n, a.dtype = k.data_ptr(), v.data_ptr(), n, _dtype(k, "k")
-    a.k_strides[:], a.v_strides[:] = _fa._strides_bhs(k, "k"), _fa._strides_bhs(v, "v")
-    if n_new is not None:
-        a.n_new = _on(cache.device, "n_new", n_new, torch.int32, (B,))
-    _trackers(a, cache, weights, positions, B)
-    if seen is not None:
-        a.seen = _on(cache.device, "seen", seen, torch.int32, (B,))
 
     def work(raw):
-        a.stream = raw
-        _fa._check(fa_cache_append(a))
+        _fa._check(fa_cache_append(FaCacheAppendArgs(
+            c, k.data_ptr(), v.data_ptr(), ks, vs, t_ptr, t_stride, l_ptr, n_ptr, w_ptr, p_ptr, s_ptr, B, n, M, W, dtype,
+            raw)))
 
-    _call(cache.device, stream, work)
-
-
-def _trackers(a, cache, weights, positions, B):
-    import torch
-    W = None
-    for name, t, dtype in (("weights", weights, torch.float32), ("positions", positions, torch.int32)):
-        if t is None:
-            continue
-        if t.dim() != 3 or (W is not None and t.shape[2] != W):
-            raise ValueError(f"{name} must be [B, H_kv, W], W common to weights and positions (got {tuple(t.shape)})")
-        W = t.shape[2]
-        setattr(a, name, _on(cache.device, name, t, dtype, (B, cache.c.H_kv, W)))
-    a.W = 0 if W is None else W
+    _call(device, stream, work)
 
 
 def cache_attention(q, cache, table, lens, *, n_q=None, scale=None, causal=True, window=0, softcap=0.0, weights=None,
@@ -281,39 +304,36 @@ def cache_attention(q, cache, table, lens, *, n_q=None, scale=None, causal=True,
     (allocated here if None).
     """
     import torch
-    if q.dim() != 4 or q.shape[3] != cache.c.D:
-        raise ValueError(f"q must be 4-D [B, H_q, n, D = {cache.c.D}] (got {tuple(q.shape)})")
-    B, Hq, n, D = q.shape
-    if q.dtype not in (torch.bfloat16, torch.float16):
+    shape, device, c = q.shape, cache.device, cache.c
+    if len(shape) != 4 or shape[3] != c.D:
+        raise ValueError(f"q must be 4-D [B, H_q, n, D = {c.D}] (got {tuple(shape)})")
+    B, Hq, n, D = shape
+    dtype = _dtype(q, "q")
+    if dtype == _fa.FA_DTYPE_F32:
         raise ValueError(f"q dtype {q.dtype} is not bfloat16 or float16")
-    if q.device != cache.device:
-        raise ValueError(f"q must be a CUDA tensor on {cache.device}")
-    a = FaCacheAttnArgs()
-    _table(a, cache, table, lens, B)
-    a.q, a.H_q, a.n, a.dtype = q.data_ptr(), Hq, n, _dtype(q, "q")
-    a.q_strides[:] = _fa._strides_bhs(q, "q")
-    if n_q is not None:
-        a.n_q = _on(cache.device, "n_q", n_q, torch.int32, (B,))
-    _trackers(a, cache, weights, None, B)
-    a.scale = 1.0 / math.sqrt(D) if scale is None else scale
-    a.causal, a.window, a.softcap = bool(causal), window, softcap
-    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or out.device != q.device):
-        raise ValueError(f"out must be {q.dtype} {tuple(q.shape)} on {q.device}")
+    if q.device != device:
+        raise ValueError(f"q must be a CUDA tensor on {device}")
+    t_ptr, t_stride, M = _table(device, "table", table, B, "M")
+    l_ptr = _on(device, "lens", lens, torch.int32, (B,))
+    n_ptr = None if n_q is None else _on(device, "n_q", n_q, torch.int32, (B,))
+    w_ptr, _, W = (None, None, 0) if weights is None else _trackers(device, c.H_kv, weights, None, B)
+    qs = _rows("q", q)
+    if out is not None and (out.shape != shape or out.dtype is not q.dtype or out.device != device):
+        raise ValueError(f"out must be {q.dtype} {tuple(shape)} on {device}")
     if lse is not None:
-        _on(cache.device, "lse", lse, torch.float32, (B, Hq, n))
+        _on(device, "lse", lse, torch.float32, (B, Hq, n))
 
     def work(raw):
-        o = torch.empty((B, Hq, n, D), dtype=q.dtype, device=q.device) if out is None else out
-        l = torch.empty((B, Hq, n), dtype=torch.float32, device=q.device) if lse is None else lse
-        if o.numel():
-            a.o, a.lse, a.stream = o.data_ptr(), l.data_ptr(), raw
-            a.o_strides[:] = _fa._strides_bhs(o, "out")
-            ws = _scratch(a, fa_cache_attn_workspace_bytes(a), workspace, q.device)
-            _fa._check(fa_cache_attn(a))
-            del ws  # torch hands the block out again only to work queued later on the same stream
+        o = torch.empty(shape, dtype=q.dtype, device=device) if out is None else out
+        l = torch.empty((B, Hq, n), dtype=torch.float32, device=device) if lse is None else lse
+        if B and Hq and n:
+            a = FaCacheAttnArgs(c, q.data_ptr(), o.data_ptr(), l.data_ptr(), w_ptr, qs, _rows("out", o), t_ptr, t_stride,
+                                l_ptr, n_ptr, B, Hq, n, M, W, 1.0 / math.sqrt(D) if scale is None else scale,
+                                bool(causal), window, softcap, dtype, None, 0, raw)
+            _with_scratch(a, fa_cache_attn_workspace_bytes(a), workspace, device, fa_cache_attn)
         return o, l
 
-    return _call(cache.device, stream, work)
+    return _call(device, stream, work)
 
 
 def cache_evict(cache, table, lens, weights, positions=None, *, keep, recent=0, into=None, weights_out=None,
@@ -330,37 +350,25 @@ def cache_evict(cache, table, lens, weights, positions=None, *, keep, recent=0, 
     lens_out: where the new lengths go (may be ``lens``); allocated here if None.
     """
     import torch
-    B = table.shape[0]
-    a = FaCacheEvictArgs()
-    _table(a, cache, table, lens, B)
-    _trackers(a, cache, weights, positions, B)
-    a.keep, a.recent = keep, recent
+    device, c, B = cache.device, cache.c, table.shape[0]
+    t_ptr, t_stride, M = _table(device, "table", table, B, "M")
+    l_ptr = _on(device, "lens", lens, torch.int32, (B,))
+    w_ptr, p_ptr, W = _trackers(device, c.H_kv, weights, positions, B)
+    i_ptr, i_stride, M_into, wo_ptr, po_ptr, W_out = None, 0, 0, None, None, 0
     if into is not None:
-        if into.dim() != 2 or into.shape[0] != B or into.dtype != torch.int32 or into.device != cache.device:
-            raise ValueError(f"into must be an int32 [B = {B}, M_into] tensor on {cache.device}")
-        if into.shape[1] > 1 and into.stride(1) != 1:
-            raise ValueError("into must have unit stride along its last dimension")
-        a.into, a.into_stride, a.M_into = into.data_ptr(), into.stride(0), into.shape[1]
-        for name, t, dtype in (("weights_out", weights_out, torch.float32),
-                               ("positions_out", positions_out, torch.int32)):
-            if t is None:
-                continue
-            if t.dim() != 3 or (a.W_out and t.shape[2] != a.W_out):
-                raise ValueError(f"{name} must be [B, H_kv, W_out], W_out common to both (got {tuple(t.shape)})")
-            a.W_out = t.shape[2]
-            setattr(a, name, _on(cache.device, name, t, dtype, (B, cache.c.H_kv, a.W_out)))
+        i_ptr, i_stride, M_into = _table(device, "into", into, B, "M_into")
+        wo_ptr, po_ptr, W_out = _trackers(device, c.H_kv, weights_out, positions_out, B)
     elif weights_out is not None or positions_out is not None:
         raise ValueError("weights_out and positions_out go with into; in place, weights and positions are changed")
     if lens_out is not None:
-        _on(cache.device, "lens_out", lens_out, torch.int32, (B,))
+        _on(device, "lens_out", lens_out, torch.int32, (B,))
 
     def work(raw):
-        n = torch.empty(B, dtype=torch.int32, device=cache.device) if lens_out is None else lens_out
+        n = torch.empty(B, dtype=torch.int32, device=device) if lens_out is None else lens_out
         if B:
-            a.lens_out, a.stream = n.data_ptr(), raw
-            ws = _scratch(a, fa_cache_evict_workspace_bytes(a), workspace, cache.device)
-            _fa._check(fa_cache_evict(a))
-            del ws
+            a = FaCacheEvictArgs(c, t_ptr, t_stride, l_ptr, w_ptr, p_ptr, i_ptr, i_stride, wo_ptr, po_ptr, n.data_ptr(),
+                                 B, M, W, M_into, W_out, keep, recent, None, 0, raw)
+            _with_scratch(a, fa_cache_evict_workspace_bytes(a), workspace, device, fa_cache_evict)
         return n
 
-    return _call(cache.device, stream, work)
+    return _call(device, stream, work)
