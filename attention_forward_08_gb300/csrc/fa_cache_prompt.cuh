@@ -172,92 +172,88 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
       const uint64_t dQ = make_sdesc_sw128(smem_u32(smem + t * C::kQBytes), 16, 1024);
       const uint64_t dK = make_sdesc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
       const uint64_t dV = make_sdesc_sw128(smem_u32(smem + C::kOffV), 128 * 128, 1024);
-      const uint32_t q_lo = (uint32_t)dQ, q_hi = (uint32_t)(dQ >> 32), k_lo = (uint32_t)dK, k_hi = (uint32_t)(dK >> 32),
-                     v_lo = (uint32_t)dV, v_hi = (uint32_t)(dV >> 32);
+      const uint32_t lead = elect_lead();
       auto issue_S = [&](int buf, int stage) {
-        const uint32_t ka = k_lo + ((stage * C::kKvBytes) >> 4), dst = tmem + buf * 128;
-        mma_ss_lh<false, 0>(dst, q_lo, q_hi, ka, k_hi, idS, 0u);
+        const uint64_t k0 = dK + ((stage * C::kKvBytes) >> 4);
+        const uint32_t dst = tmem + buf * 128;
 #pragma unroll
-        for (int kk = 1; kk < C::kD / 16; ++kk) {
+        for (int kk = 0; kk < C::kD / 16; ++kk) {
           const uint32_t off = (kk / 4) * ((128 * 128) >> 4) + (kk % 4) * 2;
-          mma_ss_lh<false, 1>(dst, q_lo + off, q_hi, ka + off, k_hi, idS, 1u);
+          mma_f16_ss_by(lead, dst, dQ + off, k0 + off, idS, kk > 0 ? 1u : 0u);
         }
       };
       auto issue_PV = [&](int buf, int stage, bool first) {
-        const uint32_t va = v_lo + ((stage * C::kKvBytes) >> 4), src = tmem + buf * 128;
-        const uint32_t dst = tmem + C::kColO + (C::kTiles == 2 ? t * C::kD : 0);
-        mma_ts_lh<false, 0>(dst, src, va, v_hi, idPV, first ? 0u : 1u);
+        const uint64_t v0 = dV + ((stage * C::kKvBytes) >> 4);
+        const uint32_t src = tmem + buf * 128, dst = tmem + C::kColO + (C::kTiles == 2 ? t * C::kD : 0);
 #pragma unroll
-        for (int kk = 1; kk < 8; ++kk) mma_ts_lh<false, 1>(dst, src + kk * 8, va + ((kk * 16 * 128) >> 4), v_hi, idPV, 1u);
+        for (int kk = 0; kk < 8; ++kk)
+          mma_f16_ts_by(lead, dst, src + kk * 8, v0 + ((kk * 16 * 128) >> 4), idPV, first && kk == 0 ? 0u : 1u);
       };
       int groups = 0;
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return prompt_warp_wait(bar, parity, abort, a); };
       auto wait_turn = [&]() -> bool {
         if (C::kIssuers == 1 || (t == 0 && groups == 0)) return true;
-        return prompt_wait(&ctl->turn[t], (t == 0 ? groups - 1 : groups) & 1, abort, a);
+        return wait(&ctl->turn[t], (t == 0 ? groups - 1 : groups) & 1);
       };
       auto pass_turn = [&]() {
         if (C::kIssuers == 2) {
-          mbar_arrive(&ctl->turn[1 - t]);
+          if (lead) mbar_arrive(&ctl->turn[1 - t]);
           ++groups;
         }
       };
-      if (lane == 0) {
-        int nth = 0, stage = 0;  // blocks done, and the next one's stage
-        uint32_t par = 0;        // parity of the stage's use
-        bool ok = true;
+      int nth = 0, stage = 0;  // blocks done, and the next one's stage
+      uint32_t par = 0;        // parity of the stage's use
+      bool ok = true;
 #pragma unroll 1
-        for (int pieces = 0; ok; ++pieces) {
-          ok = prompt_wait(&ctl->q_full[t], pieces & 1, abort, a);
-          if (!ok) break;
-          const int n = ctl->n[t][pieces & 1];
-          if (n == 0) break;
-          ok = prompt_wait(&ctl->k_full[stage], par, abort, a) && wait_turn();
+      for (int pieces = 0; ok; ++pieces) {
+        ok = wait(&ctl->q_full[t], pieces & 1);
+        if (!ok) break;
+        const int n = ctl->n[t][pieces & 1];
+        if (n == 0) break;
+        ok = wait(&ctl->k_full[stage], par) && wait_turn();
+        if (!ok) break;
+        tc_fence_after();
+        // buffers: two tiles: tile t's; one: alternating over all blocks
+        issue_S(C::kTiles == 2 ? t : nth & 1, stage);
+        mma_commit_by(lead, &ctl->s_full[C::kTiles == 2 ? t : nth & 1]);
+        pass_turn();
+        mma_commit_by(lead, &ctl->k_empty[stage]);
+#pragma unroll 1
+        for (int j = 0; j < n; ++j, ++nth) {
+          const int next = stage + 1 == C::kStages ? 0 : stage + 1;
+          const uint32_t next_par = par ^ (next == 0 ? 1u : 0u);
+          const bool more = j + 1 < n;
+          if constexpr (C::kTiles == 1) {  // the next S goes before this PV
+            if (more) {
+              ok = wait(&ctl->k_full[next], next_par);
+              if (!ok) break;
+              tc_fence_after();
+              issue_S((nth + 1) & 1, next);
+              mma_commit_by(lead, &ctl->s_full[(nth + 1) & 1]);
+              mma_commit_by(lead, &ctl->k_empty[next]);
+            }
+          }
+          ok = wait(&ctl->v_full[stage], par) && (C::kTiles == 1 || !more || wait(&ctl->k_full[next], next_par)) &&
+               wait(&ctl->p_ready[t], (uint32_t)nth & 1u) && wait_turn();
           if (!ok) break;
           tc_fence_after();
-          // buffers: two tiles: tile t's; one: alternating over all blocks
-          issue_S(C::kTiles == 2 ? t : nth & 1, stage);
-          mma_commit(&ctl->s_full[C::kTiles == 2 ? t : nth & 1]);
-          pass_turn();
-          mma_commit(&ctl->k_empty[stage]);
-#pragma unroll 1
-          for (int j = 0; j < n; ++j, ++nth) {
-            const int next = stage + 1 == C::kStages ? 0 : stage + 1;
-            const uint32_t next_par = par ^ (next == 0 ? 1u : 0u);
-            const bool more = j + 1 < n;
-            if constexpr (C::kTiles == 1) {  // the next S goes before this PV
-              if (more) {
-                ok = prompt_wait(&ctl->k_full[next], next_par, abort, a);
-                if (!ok) break;
-                tc_fence_after();
-                issue_S((nth + 1) & 1, next);
-                mma_commit(&ctl->s_full[(nth + 1) & 1]);
-                mma_commit(&ctl->k_empty[next]);
-              }
-            }
-            ok = prompt_wait(&ctl->v_full[stage], par, abort, a) &&
-                 (C::kTiles == 1 || !more || prompt_wait(&ctl->k_full[next], next_par, abort, a)) &&
-                 prompt_wait(&ctl->p_ready[t], (uint32_t)nth & 1u, abort, a) && wait_turn();
-            if (!ok) break;
-            tc_fence_after();
-            issue_PV(C::kTiles == 2 ? t : nth & 1, stage, j == 0);
-            if (C::kTiles == 1 || !more) mma_commit(&ctl->o_ready[t]);
-            if (C::kTiles == 2 && more) {
-              issue_S(t, next);
-              mma_commit(&ctl->s_full[t]);
-            }
-            pass_turn();
-            mma_commit(&ctl->v_empty[stage]);
-            if (C::kTiles == 2 && more) mma_commit(&ctl->k_empty[next]);
-            stage = next;
-            par = next_par;
+          issue_PV(C::kTiles == 2 ? t : nth & 1, stage, j == 0);
+          if (C::kTiles == 1 || !more) mma_commit_by(lead, &ctl->o_ready[t]);
+          if (C::kTiles == 2 && more) {
+            issue_S(t, next);
+            mma_commit_by(lead, &ctl->s_full[t]);
           }
+          pass_turn();
+          mma_commit_by(lead, &ctl->v_empty[stage]);
+          if (C::kTiles == 2 && more) mma_commit_by(lead, &ctl->k_empty[next]);
+          stage = next;
+          par = next_par;
         }
       }
-      __syncwarp();
       // Every MMA issued here has completed before the block lets go of its
       // memory (after an expired wait too; bounded).
-      if (lane == 0) {
-        mma_commit(&ctl->drain[t]);
+      mma_commit_by(lead, &ctl->drain[t]);
+      if (lead) {
         const long long begin = clock64_now();
         while (!mbar_try_wait(&ctl->drain[t], 0) && clock64_now() - begin < kDecDrainCycles) {
         }
