@@ -46,6 +46,9 @@ struct PromptCfg {
   static constexpr int kMinTiles = 4;
   static constexpr int kStages = kD == 64 ? 3 : kD == 128 ? 2 : 1;  // of K; of V alike
   static constexpr int kIssuers = kTiles;
+  // Keys a score buffer; a row tile has two, so that the next scores are being
+  // computed while a softmax runs.
+  static constexpr int kKeys = kTiles == 2 ? 64 : 128, kParts = 128 / kKeys;
   static constexpr int kConvWarps = kTiles == 2 ? 4 : 8;
   static constexpr int kThreads = 128 + 32 * kConvWarps + 128 * kTiles;  // 512
   static constexpr int kQBytes = 128 * kD * 2;       // one row tile
@@ -53,10 +56,10 @@ struct PromptCfg {
   static constexpr int kOffK = kTiles * kQBytes, kOffV = kOffK + kStages * kKvBytes;
   static constexpr int kOffMeta = kOffV + kStages * kKvBytes, kOffCtl = kOffMeta + 4 * kGroups * 16;
   static constexpr int kSmem = 1024 + kOffCtl + 512;
-  static constexpr int kColO = 256;                  // S: two buffers of 128 columns; P over S
+  static constexpr int kColO = 256;                  // S: two buffers of kKeys columns a tile; P over S
   // Registers: 512 threads x 128 at launch; the softmax warps, which hold a
   // row of scores each, take the others'.
-  static constexpr int kRegsCtrl = 40, kRegsConv = kTiles == 2 ? 72 : 104, kRegsSoft = kTiles == 2 ? 200 : 208;
+  static constexpr int kRegsCtrl = 40, kRegsConv = 104, kRegsSoft = kTiles == 2 ? 184 : 208;
   static_assert(kRegsCtrl < 128 && kRegsConv < 128 && kRegsSoft > 128, "which warps give, which take");
   static_assert(128 * kRegsCtrl + 32 * kConvWarps * kRegsConv + 128 * kTiles * kRegsSoft <= 512 * 128,
                 "register split exceeds the launch allocation");
@@ -67,10 +70,9 @@ struct PromptCtl {
   uint64_t q_full[2];              // 4 softmax warps: query tile written
   uint64_t k_full[3], k_empty[3];  // converters / MMAs (one arrival an issuer)
   uint64_t v_full[3], v_empty[3];
-  uint64_t s_full[2];              // S computed (two tiles: of tile t; one tile: in buffer j & 1)
+  uint64_t s_full[2][2];           // [tile][buffer]: S computed
   uint64_t p_ready[2];             // softmax wrote P (and rescaled O)
-  uint64_t o_ready[2];             // two tiles: a piece's last PV done; one tile: each PV done
-  uint64_t turn[2];
+  uint64_t o_ready[2];             // each PV done
   uint64_t drain[2];
   int n[2][2];                     // [tile][piece & 1]: blocks of a piece (0: no more), beside q_full
   uint32_t tmem;
@@ -107,9 +109,9 @@ __device__ __forceinline__ void widen16(const uint4& w, uint4& lo, uint4& hi) {
 
 // A row's scores to base 2 where one positive factor cannot do it.
 template <class C>
-__device__ __forceinline__ void prompt_scale(uint32_t (&x)[128], const CacheAttnParams& a, const float4* meta, float rs) {
+__device__ __forceinline__ void prompt_scale(uint32_t (&x)[C::kKeys], const CacheAttnParams& a, const float4* meta, float rs) {
 #pragma unroll
-  for (int g = 0; g < C::kGroups; ++g) {
+  for (int g = 0; g < C::kKeys / C::kGroup; ++g) {
     const float ks = meta[g].x * rs, ci = ks * a.cap_in * 2.8853900817779268f;
 #pragma unroll
     for (int k = C::kGroup * g; k < C::kGroup * (g + 1); ++k) {
@@ -137,10 +139,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->q_full[i], 4);
-      mbar_init(&ctl->s_full[i], 1);
+      mbar_init(&ctl->s_full[i][0], 1);
+      mbar_init(&ctl->s_full[i][1], 1);
       mbar_init(&ctl->p_ready[i], 4);
       mbar_init(&ctl->o_ready[i], 1);
-      mbar_init(&ctl->turn[i], 1);
       mbar_init(&ctl->drain[i], 1);
     }
     for (int i = 0; i < 3; ++i) {
@@ -167,41 +169,35 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
     regs_dec<C::kRegsCtrl>();
     if (warp < C::kIssuers) {
       const int t = warp;  // row tile
-      constexpr uint32_t idS = make_idesc_fmt(kFmtF16, 128, 128, false, false);
+      constexpr uint32_t idS = make_idesc_fmt(kFmtF16, 128, C::kKeys, false, false);
       constexpr uint32_t idPV = make_idesc_fmt(kFmtF16, 128, C::kD, false, true);
       const uint64_t dQ = make_sdesc_sw128(smem_u32(smem + t * C::kQBytes), 16, 1024);
       const uint64_t dK = make_sdesc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
       const uint64_t dV = make_sdesc_sw128(smem_u32(smem + C::kOffV), 128 * 128, 1024);
       const uint32_t lead = elect_lead();
-      auto issue_S = [&](int buf, int stage) {
-        const uint64_t k0 = dK + ((stage * C::kKvBytes) >> 4);
-        const uint32_t dst = tmem + buf * 128;
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return prompt_warp_wait(bar, parity, abort, a); };
+      // Scores (part of the block in `stage`) into buffer `buf`.
+      auto issue_S = [&](int buf, int stage, int part) {
+        const uint64_t k0 = dK + ((stage * C::kKvBytes + part * (C::kKeys * 128)) >> 4);
+        const uint32_t dst = tmem + t * 128 + buf * C::kKeys;
 #pragma unroll
         for (int kk = 0; kk < C::kD / 16; ++kk) {
           const uint32_t off = (kk / 4) * ((128 * 128) >> 4) + (kk % 4) * 2;
           mma_f16_ss_by(lead, dst, dQ + off, k0 + off, idS, kk > 0 ? 1u : 0u);
         }
+        mma_commit_by(lead, &ctl->s_full[t][buf]);
+        if (part == C::kParts - 1) mma_commit_by(lead, &ctl->k_empty[stage]);
       };
-      auto issue_PV = [&](int buf, int stage, bool first) {
-        const uint64_t v0 = dV + ((stage * C::kKvBytes) >> 4);
-        const uint32_t src = tmem + buf * 128, dst = tmem + C::kColO + (C::kTiles == 2 ? t * C::kD : 0);
+      auto issue_PV = [&](int buf, int stage, int part, bool first) {
+        const uint64_t v0 = dV + ((stage * C::kKvBytes + part * (C::kKeys * 128)) >> 4);
+        const uint32_t src = tmem + t * 128 + buf * C::kKeys, dst = tmem + C::kColO + t * C::kD;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
+        for (int kk = 0; kk < C::kKeys / 16; ++kk)
           mma_f16_ts_by(lead, dst, src + kk * 8, v0 + ((kk * 16 * 128) >> 4), idPV, first && kk == 0 ? 0u : 1u);
+        mma_commit_by(lead, &ctl->o_ready[t]);
+        if (part == C::kParts - 1) mma_commit_by(lead, &ctl->v_empty[stage]);
       };
-      int groups = 0;
-      auto wait = [&](uint64_t* bar, uint32_t parity) { return prompt_warp_wait(bar, parity, abort, a); };
-      auto wait_turn = [&]() -> bool {
-        if (C::kIssuers == 1 || (t == 0 && groups == 0)) return true;
-        return wait(&ctl->turn[t], (t == 0 ? groups - 1 : groups) & 1);
-      };
-      auto pass_turn = [&]() {
-        if (C::kIssuers == 2) {
-          if (lead) mbar_arrive(&ctl->turn[1 - t]);
-          ++groups;
-        }
-      };
-      int nth = 0, stage = 0;  // blocks done, and the next one's stage
+      int nth = 0, stage = 0;  // score buffers filled, and the block's stage
       uint32_t par = 0;        // parity of the stage's use
       bool ok = true;
 #pragma unroll 1
@@ -210,42 +206,31 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
         if (!ok) break;
         const int n = ctl->n[t][pieces & 1];
         if (n == 0) break;
-        ok = wait(&ctl->k_full[stage], par) && wait_turn();
+        ok = wait(&ctl->k_full[stage], par);
         if (!ok) break;
         tc_fence_after();
-        // buffers: two tiles: tile t's; one: alternating over all blocks
-        issue_S(C::kTiles == 2 ? t : nth & 1, stage);
-        mma_commit_by(lead, &ctl->s_full[C::kTiles == 2 ? t : nth & 1]);
-        pass_turn();
-        mma_commit_by(lead, &ctl->k_empty[stage]);
+        issue_S(nth & 1, stage, 0);
 #pragma unroll 1
-        for (int j = 0; j < n; ++j, ++nth) {
+        for (int j = 0; j < n && ok; ++j) {
           const int next = stage + 1 == C::kStages ? 0 : stage + 1;
           const uint32_t next_par = par ^ (next == 0 ? 1u : 0u);
-          const bool more = j + 1 < n;
-          if constexpr (C::kTiles == 1) {  // the next S goes before this PV
-            if (more) {
+#pragma unroll
+          for (int part = 0; part < C::kParts; ++part) {
+            // the next scores go before this PV
+            if (part + 1 < C::kParts) {
+              issue_S((nth + 1) & 1, stage, part + 1);
+            } else if (j + 1 < n) {
               ok = wait(&ctl->k_full[next], next_par);
               if (!ok) break;
               tc_fence_after();
-              issue_S((nth + 1) & 1, next);
-              mma_commit_by(lead, &ctl->s_full[(nth + 1) & 1]);
-              mma_commit_by(lead, &ctl->k_empty[next]);
+              issue_S((nth + 1) & 1, next, 0);
             }
+            ok = (part > 0 || wait(&ctl->v_full[stage], par)) && wait(&ctl->p_ready[t], (uint32_t)nth & 1u);
+            if (!ok) break;
+            tc_fence_after();
+            issue_PV(nth & 1, stage, part, j == 0 && part == 0);
+            ++nth;
           }
-          ok = wait(&ctl->v_full[stage], par) && (C::kTiles == 1 || !more || wait(&ctl->k_full[next], next_par)) &&
-               wait(&ctl->p_ready[t], (uint32_t)nth & 1u) && wait_turn();
-          if (!ok) break;
-          tc_fence_after();
-          issue_PV(C::kTiles == 2 ? t : nth & 1, stage, j == 0);
-          if (C::kTiles == 1 || !more) mma_commit_by(lead, &ctl->o_ready[t]);
-          if (C::kTiles == 2 && more) {
-            issue_S(t, next);
-            mma_commit_by(lead, &ctl->s_full[t]);
-          }
-          pass_turn();
-          mma_commit_by(lead, &ctl->v_empty[stage]);
-          if (C::kTiles == 2 && more) mma_commit_by(lead, &ctl->k_empty[next]);
           stage = next;
           par = next_par;
         }
@@ -395,10 +380,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
     const int t = C::kTiles == 2 ? (warp - 8) >> 2 : 0;
     const int tl = tid - (512 - 128 * C::kTiles) - 128 * t;  // row of the tile = TMEM lane
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tO = tmem + lane_addr + C::kColO + (C::kTiles == 2 ? t * C::kD : 0);
+    const uint32_t tO = tmem + lane_addr + C::kColO + t * C::kD;
     uint8_t* q_tile = smem + t * C::kQBytes;
     const bool raw = a.cap_out == 0.0f && a.scale_log2 > 0.0f;
-    int blocks = 0, pieces = 0;
+    constexpr int kGroups = C::kKeys / C::kGroup;  // groups a score buffer
+    int nth = 0, pieces = 0;  // score buffers and pieces before this one
     bool ok = true;
 #pragma unroll 1
     for (int pos = t0; pos < t1 && ok; ++pieces) {
@@ -409,39 +395,42 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
       const int row = at.rg * C::kRows + t * 128 + tl, i = row / a.group, head = at.h * a.group + row % a.group;
       const bool real = row < p.rows;
       const int2 see = real ? dec_span(a, at.seq, i, i) : make_int2(0, 0);
-      // The query row, twice over: its largest entry, then its f16 form.  (S of
-      // the piece before is done: the tile may be written.)
+      // The warp's query rows, kLanes lanes a row, all loads under way at once:
+      // the row's largest entry, then its f16 form.  (S of the piece before is
+      // done: the tile may be written.)
       float rs = 1.0f;
       {
-        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at.b * a.qs[0] +
-                                                        head * a.qs[1] + i * a.qs[2]);
-        const bool in = see.x < see.y;
-        float up = 1.0f;
-        if constexpr (!C::kF16) {
-          float top = 0.0f;
-          if (in) {
-#pragma unroll 4
-            for (int u = 0; u < C::kD / 8; ++u) {
-              const uint4 w = __ldg(q + u);
-              const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+        constexpr int kLanes = C::kD / 8, kAtOnce = 32 / kLanes;  // rows a load
+        const uint16_t* mine = see.x < see.y
+                                   ? static_cast<const uint16_t*>(a.q) + at.b * a.qs[0] + head * a.qs[1] + i * a.qs[2]
+                                   : nullptr;
+        uint4 w[kLanes];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                top = fmax3(top, fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xFFFF0000u)));
-            }
-          }
-          dec_row_scale(top, up, rs);
+        for (int u = 0; u < kLanes; ++u) {
+          const uint16_t* q = reinterpret_cast<const uint16_t*>(
+              __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(mine), u * kAtOnce + lane / kLanes));
+          w[u] = make_uint4(0, 0, 0, 0);
+          if (q) w[u] = __ldg(reinterpret_cast<const uint4*>(q) + lane % kLanes);
         }
-#pragma unroll 4
-        for (int u = 0; u < C::kD / 8; ++u) {
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (in) w = __ldg(q + u);
+#pragma unroll
+        for (int u = 0; u < kLanes; ++u) {
           if constexpr (!C::kF16) {
-            uint32_t* x = &w.x;
+            uint32_t* x = &w[u].x;
+            float top = 0.0f, up, down;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              top = fmax3(top, fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xFFFF0000u)));
+#pragma unroll
+            for (int o = 1; o < kLanes; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            dec_row_scale(top, up, down);
+            const float got = __shfl_sync(0xFFFFFFFFu, down, (lane % kAtOnce) * kLanes);
+            if (lane / kAtOnce == u) rs = got;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               x[e] = pack_f16x2(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xFFFF0000u) * up);
           }
-          *reinterpret_cast<uint4*>(q_tile + (u / 8) * (128 * 128) + tl * 128 + (((u % 8) ^ (tl & 7)) << 4)) = w;
+          const int r = (warp & 3) * 32 + u * kAtOnce + lane / kLanes, c16 = lane % kLanes;
+          *reinterpret_cast<uint4*>(q_tile + (c16 / 8) * (128 * 128) + r * 128 + (((c16 % 8) ^ (r & 7)) << 4)) = w[u];
         }
       }
       fence_proxy_async_smem();
@@ -454,37 +443,37 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
       const float f_row = rs * a.scale_log2;
       float m = -INFINITY, l = 0.0f;
 #pragma unroll 1
-      for (int j = 0; j < n; ++j) {
-        const int nth = blocks + j, buf = C::kTiles == 2 ? t : nth & 1;
-        const uint32_t s_par = (uint32_t)(C::kTiles == 2 ? nth : nth >> 1) & 1u;
-        ok = prompt_warp_wait(&ctl->s_full[buf], s_par, abort, a);
+      for (int j = 0; j < n * C::kParts; ++j, ++nth) {
+        const int buf = nth & 1;
+        ok = prompt_warp_wait(&ctl->s_full[t][buf], (uint32_t)(nth >> 1) & 1u, abort, a);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t tS = tmem + lane_addr + buf * 128;
-        const float4* meta = s_meta + (nth & 3) * C::kGroups;
-        const int key0 = (first + j) * 128, lo = see.x - key0, hi = see.y - key0;
-        uint32_t x[128];  // the row's scores (fp32 bits)
+        const uint32_t tS = tmem + lane_addr + t * 128 + buf * C::kKeys;
+        const float4* meta = s_meta + ((nth / C::kParts) & 3) * C::kGroups + (nth % C::kParts) * kGroups;
+        const int key0 = first * 128 + j * C::kKeys, lo = see.x - key0, hi = see.y - key0;
+        uint32_t x[C::kKeys];  // the row's scores (fp32 bits)
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) tmem_ld32(tS + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[cc * 32]));
+        for (int cc = 0; cc < C::kKeys / 32; ++cc)
+          tmem_ld32(tS + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[cc * 32]));
         tmem_wait_ld();
         reg_fence(x);
         if (!raw) prompt_scale<C>(x, a, meta, rs);
-        if (lo > 0 || hi < 128) {
+        if (lo > 0 || hi < C::kKeys) {
 #pragma unroll
-          for (int k = 0; k < 128; ++k)
+          for (int k = 0; k < C::kKeys; ++k)
             if (k < lo || k >= hi) x[k] = 0xFF800000u;
         }
         // Group by group: a raw score times f plus y is the score's weight in
         // base 2 (s + log2 vs); y = -inf where nothing is stored.
-        float f[C::kGroups], y[C::kGroups], mx = -INFINITY;
+        float f[kGroups], y[kGroups], mx = -INFINITY;
 #pragma unroll
-        for (int g = 0; g < C::kGroups; ++g) {
+        for (int g = 0; g < kGroups; ++g) {
           const float4 q = meta[g];
           f[g] = raw ? fmaxf(q.x * f_row, 1e-37f) : 1.0f;  // (not 0: a hidden score stays -inf)
           y[g] = q.w == 0.0f ? -INFINITY : q.y;
         }
 #pragma unroll
-        for (int g = 0; g < C::kGroups; ++g) {
+        for (int g = 0; g < kGroups; ++g) {
           float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int k = 0; k < C::kGroup; k += 2)
@@ -501,7 +490,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
         }
         const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-        for (int g = 0; g < C::kGroups; ++g) {
+        for (int g = 0; g < kGroups; ++g) {
           const float off = y[g] - base;
           float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -520,11 +509,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
           }
           l = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), meta[g].z, l);
         }
-        if constexpr (C::kTiles == 1) {  // PV of the block before has landed (each phase is consumed, in order)
-          if (nth > 0) {
-            ok = prompt_warp_wait(&ctl->o_ready[0], (uint32_t)(nth - 1) & 1u, abort, a);
-            if (!ok) break;
-          }
+        if (j > 0) {  // the PV before has landed (each phase is consumed, in order)
+          ok = prompt_warp_wait(&ctl->o_ready[t], (uint32_t)(nth - 1) & 1u, abort, a);
+          if (!ok) break;
         }
         if (j > 0 && __any_sync(0xFFFFFFFFu, resc)) {
           tc_fence_after();
@@ -550,11 +537,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
         if (lane == 0) mbar_arrive(&ctl->p_ready[t]);
       }
       if (!ok) break;
-      blocks += n;
-      if constexpr (C::kTiles == 2)
-        ok = prompt_warp_wait(&ctl->o_ready[t], pieces & 1, abort, a);
-      else
-        ok = prompt_warp_wait(&ctl->o_ready[0], (uint32_t)(blocks - 1) & 1u, abort, a);
+      ok = prompt_warp_wait(&ctl->o_ready[t], (uint32_t)(nth - 1) & 1u, abort, a);
       if (!ok) break;
       tc_fence_after();
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
