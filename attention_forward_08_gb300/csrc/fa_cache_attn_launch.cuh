@@ -172,7 +172,7 @@ AttnPlan attn_plan(const CacheAttnParams& a) {
 template <int kD>
 long long plan_workspace(const CacheAttnParams& a, int num_sms) {
   switch (attn_plan<kD>(a)) {
-    case AttnPlan::kPrompt: return line_workspace<PromptCfg<0, false, kD, 16>>(num_sms);
+    case AttnPlan::kPrompt: return line_workspace<PromptCfg<0, false, kD, 16, true>>(num_sms);
     case AttnPlan::kRows32:
       if constexpr (kD <= 128) return line_workspace<DecCfg<0, false, kD, 2, true>>(num_sms * DecCfg<0, false, kD, 2, true>::kCtas);
     default: return line_workspace<DecCfg<0, false, kD, 1, true>>(num_sms * DecCfg<0, false, kD, 1, true>::kCtas);
@@ -193,8 +193,10 @@ template <int kD, int kKind, bool kF16>
 int launch_plan(const CacheAttnParams& a, const LaunchCtx& ctx) {
   switch (attn_plan<kD>(a)) {
     case AttnPlan::kPrompt:
-      return a.c.page >= 64 ? launch_prompt<PromptCfg<kKind, kF16, kD, 64>>(a, ctx)
-                            : launch_prompt<PromptCfg<kKind, kF16, kD, 16>>(a, ctx);
+      if (a.cap_out == 0.0f && a.scale_log2 > 0.0f)
+        return a.c.page >= 64 ? launch_prompt<PromptCfg<kKind, kF16, kD, 64, true>>(a, ctx)
+                              : launch_prompt<PromptCfg<kKind, kF16, kD, 16, true>>(a, ctx);
+      return launch_prompt<PromptCfg<kKind, kF16, kD, 16, false>>(a, ctx);
     case AttnPlan::kRows32:
       if constexpr (kD <= 128) return launch_decode_by<kD, kKind, kF16, 2>(a, ctx);
     default: return launch_decode_by<kD, kKind, kF16, 1>(a, ctx);

@@ -34,8 +34,9 @@ namespace fa {
 // kGroup_: tokens that surely share a cache block, and so a scale: 16, or 64
 // where blocks have 64 tokens and more (a quarter of the operations by group:
 // TIMES).
-template <int kKind_, bool kF16_, int kD_, int kGroup_>
+template <int kKind_, bool kF16_, int kD_, int kGroup_, bool kRaw_>
 struct PromptCfg {
+  static constexpr bool kRaw = kRaw_;  // scores need no more than a positive factor
   static constexpr int kGroup = kGroup_, kGroups = 128 / kGroup;  // groups a block of keys
   static constexpr int kKind = kKind_;
   static constexpr bool kF16 = kF16_;
@@ -59,7 +60,7 @@ struct PromptCfg {
   static constexpr int kColO = 256;                  // S: two buffers of kKeys columns a tile; P over S
   // Registers: 512 threads x 128 at launch; the softmax warps, which hold a
   // row of scores each, take the others'.
-  static constexpr int kRegsCtrl = 40, kRegsConv = 104, kRegsSoft = kTiles == 2 ? 184 : 208;
+  static constexpr int kRegsCtrl = 40, kRegsConv = kTiles == 2 ? 72 : 104, kRegsSoft = kTiles == 2 ? 200 : 208;
   static_assert(kRegsCtrl < 128 && kRegsConv < 128 && kRegsSoft > 128, "which warps give, which take");
   static_assert(128 * kRegsCtrl + 32 * kConvWarps * kRegsConv + 128 * kTiles * kRegsSoft <= 512 * 128,
                 "register split exceeds the launch allocation");
@@ -382,7 +383,6 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tO = tmem + lane_addr + C::kColO + t * C::kD;
     uint8_t* q_tile = smem + t * C::kQBytes;
-    const bool raw = a.cap_out == 0.0f && a.scale_log2 > 0.0f;
     constexpr int kGroups = C::kKeys / C::kGroup;  // groups a score buffer
     int nth = 0, pieces = 0;  // score buffers and pieces before this one
     bool ok = true;
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
           tmem_ld32(tS + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[cc * 32]));
         tmem_wait_ld();
         reg_fence(x);
-        if (!raw) prompt_scale<C>(x, a, meta, rs);
+        if constexpr (!C::kRaw) prompt_scale<C>(x, a, meta, rs);
         if (lo > 0 || hi < C::kKeys) {
 #pragma unroll
           for (int k = 0; k < C::kKeys; ++k)
@@ -465,55 +465,59 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
         }
         // Group by group: a raw score times f plus y is the score's weight in
         // base 2 (s + log2 vs); y = -inf where nothing is stored.
-        float f[kGroups], y[kGroups], mx = -INFINITY;
+        float f[kGroups], y[kGroups], inv_vs[kGroups], mx;
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
           const float4 q = meta[g];
-          f[g] = raw ? fmaxf(q.x * f_row, 1e-37f) : 1.0f;  // (not 0: a hidden score stays -inf)
+          f[g] = C::kRaw ? fmaxf(q.x * f_row, 1e-37f) : 1.0f;  // (not 0: a hidden score stays -inf)
           y[g] = q.w == 0.0f ? -INFINITY : q.y;
+          inv_vs[g] = q.z;
         }
+        // The weights against the maximum so far, and the new maximum beside
+        // them: neither waits for the other.  Where a row's maximum has grown
+        // too far for that, once more against the new one.
+        float corr = 1.0f, part;
+        bool moved = false;
+#pragma unroll 1
+        while (true) {
+          const float base = m == -INFINITY ? 0.0f : m;
+          mx = -INFINITY, part = 0.0f;
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          for (int g = 0; g < kGroups; ++g) {
+            const float off = y[g] - base;
+            float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int k = 0; k < C::kGroup; k += 2)
-            v[(k >> 1) & 3] = fmax3(v[(k >> 1) & 3], __uint_as_float(x[C::kGroup * g + k]),
-                                    __uint_as_float(x[C::kGroup * g + k + 1]));
-          mx = fmaxf(mx, fmaf(fmax3(fmaxf(v[0], v[1]), v[2], v[3]), f[g], y[g]));
-        }
-        float corr = 1.0f;
-        const bool resc = mx > m + kDecLazy;
-        if (resc) {
-          corr = ex2(m - mx);  // 0 when m = -inf
-          m = mx;
-          l *= corr;
-        }
-        const float base = m == -INFINITY ? 0.0f : m;
+            for (int c0 = 0; c0 < C::kGroup; c0 += 16) {
+              uint32_t pk[8];
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          const float off = y[g] - base;
-          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int c0 = 0; c0 < C::kGroup; c0 += 16) {
-            uint32_t pk[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int k = C::kGroup * g + c0 + 2 * e;
-              float x0, x1;
-              ffma2(x0, x1, __uint_as_float(x[k]), __uint_as_float(x[k + 1]), f[g], f[g], off, off);
-              x0 = ex2(x0), x1 = ex2(x1);
-              fadd2(sum[(e & 1) * 2], sum[(e & 1) * 2 + 1], x0, x1);
-              pk[e] = pack_f16x2(x0, x1);
+              for (int e = 0; e < 8; ++e) {
+                const int k = C::kGroup * g + c0 + 2 * e;
+                float x0 = __uint_as_float(x[k]), x1 = __uint_as_float(x[k + 1]);
+                v[e & 3] = fmax3(v[e & 3], x0, x1);
+                ffma2(x0, x1, x0, x1, f[g], f[g], off, off);
+                x0 = ex2(x0), x1 = ex2(x1);
+                fadd2(sum[(e & 1) * 2], sum[(e & 1) * 2 + 1], x0, x1);
+                pk[e] = pack_f16x2(x0, x1);
+              }
+              tmem_st8(tS + (C::kGroup * g + c0) / 2, pk);
             }
-            tmem_st8(tS + (C::kGroup * g + c0) / 2, pk);
+            mx = fmaxf(mx, fmaf(fmax3(fmaxf(v[0], v[1]), v[2], v[3]), f[g], y[g]));
+            part = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), inv_vs[g], part);
           }
-          l = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), meta[g].z, l);
+          const bool resc = mx > m + kDecLazy;
+          if (!__any_sync(0xFFFFFFFFu, resc)) break;
+          moved = true;
+          if (resc) {
+            corr = ex2(m - mx);  // 0 when m = -inf
+            m = mx;
+          }
         }
+        l = fmaf(l, corr, part);
         if (j > 0) {  // the PV before has landed (each phase is consumed, in order)
           ok = prompt_warp_wait(&ctl->o_ready[t], (uint32_t)(nth - 1) & 1u, abort, a);
           if (!ok) break;
         }
-        if (j > 0 && __any_sync(0xFFFFFFFFu, resc)) {
+        if (j > 0 && moved) {
           tc_fence_after();
 #pragma unroll
           for (int cc = 0; cc < C::kD / 32; ++cc) {
