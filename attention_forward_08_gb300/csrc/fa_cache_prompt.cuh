@@ -276,7 +276,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
       // scales.
       constexpr int kG = C::kGroups, kBatch = 32 / kG;
       int blk = -1, next_blk;
-      float ks = 0.0f, vs = 0.0f;
+      float4 mine;           // the group's scales, as the softmax reads them
+      uint32_t there, none;  // bit by lane: a block is there; its values' scale is 0
       auto look_up = [&](int j0) {
         const int j = j0 + lane / kG, tok = (first + j) * 128 + C::kGroup * (lane % kG);
         return j < n && tok < span.y && tok + C::kGroup > span.x
@@ -286,39 +287,45 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
       next_blk = look_up(0);
       auto turn_over = [&](int j0) {  // the batch of blocks j0 .. becomes the one in the lanes
         blk = next_blk;
-        ks = vs = 0.0f;
+        float ks = 0.0f, vs = 0.0f;
         if (blk >= 0) {
           ks = __ldg(c.k_scale + (long long)blk * c.H + h);
           vs = __ldg(c.v_scale + (long long)blk * c.H + h);
         }
+        // (values of a zero scale are stored zeros for all that counts: they are
+        // cleared below, and count with the scale 1)
+        const bool zero = !(vs >= 1.17549435e-38f);
+        mine = make_float4(ks, zero ? 0.0f : lg2(vs), zero ? 1.0f : 1.0f / vs, blk >= 0 ? 1.0f : 0.0f);
+        there = __ballot_sync(0xFFFFFFFFu, blk >= 0);
+        none = __ballot_sync(0xFFFFFFFFu, zero);
         next_blk = look_up(j0 + kBatch);
       };
-      // One set of registers, always on its way: as soon as a unit of K_j is
-      // widened and stored, its register takes that unit of V_j, and then of
-      // K_{j+1}, so that every load has half a block's time to arrive.
+      auto of_block = [&](uint32_t bits, int j) { return (bits >> (kG * (j % kBatch))) & ((1u << kG) - 1u); };
+      // One set of registers, always on its way: as soon as K_j is widened and
+      // stored, the registers take V_j, and then K_{j+1}, so that every load has
+      // half a block's time to arrive.
       uint4 x[kPer];
-      // Where this thread's keys of a block lie: by unit where groups are as
-      // short as a step between units, else by group.
-      auto load_at = [&](int i, int j, const uint8_t* from, long long row) {
-        const int tok = (first + j) * 128 + key0 + i * kKeysStep;
-        x[i] = make_uint4(0, 0, 0, 0);  // where nobody sees them or nothing is stored
-        if (from && tok >= span.x && tok < span.y)
-          x[i] = __ldg(reinterpret_cast<const uint4*>(from + ((key0 + i * kKeysStep) & (c.page - 1)) * row));
-      };
-      const uint8_t* from[kG];
-      auto find = [&](int j, const uint8_t* pool, const long long* st) {
+      auto load = [&](int j, const uint8_t* pool, const long long* st) {
+        const long long step = kKeysStep * st[2];
+        const int tok0 = (first + j) * 128;
+        if (C::kGroup == 64 && of_block(there, j) == (1u << kG) - 1u && tok0 >= span.x && tok0 + 128 <= span.y) {
 #pragma unroll
-        for (int g = 0; g < kG; ++g) {
-          const int at_blk = __shfl_sync(0xFFFFFFFFu, blk, (j % kBatch) * kG + g);
-          from[g] = at_blk >= 0 ? pool + at_blk * st[0] : nullptr;
-        }
-      };
-      auto load = [&](int i, int j, const uint8_t* pool, const long long* st) {
-        if constexpr (C::kGroup == 64) {
-          load_at(i, j, from[i * kKeysStep / 64], st[2]);
+          for (int g = 0; g < kG; ++g) {
+            const uint8_t* from = pool + __shfl_sync(0xFFFFFFFFu, blk, (j % kBatch) * kG + g) * st[0] +
+                                  (key0 + ((g * C::kGroup) & (c.page - 1))) * st[2];
+#pragma unroll
+            for (int i = g * (kPer / kG); i < (g + 1) * (kPer / kG); ++i, from += step)
+              x[i] = __ldg(reinterpret_cast<const uint4*>(from));
+          }
         } else {
-          const int at_blk = __shfl_sync(0xFFFFFFFFu, blk, (j % kBatch) * kG + ((key0 + i * kKeysStep) >> 4));
-          load_at(i, j, at_blk >= 0 ? pool + at_blk * st[0] : nullptr, st[2]);
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const int key = key0 + i * kKeysStep, tok = tok0 + key;
+            const int at_blk = __shfl_sync(0xFFFFFFFFu, blk, (j % kBatch) * kG + key / C::kGroup);
+            x[i] = make_uint4(0, 0, 0, 0);  // where nobody sees them or nothing is stored
+            if (at_blk >= 0 && tok >= span.x && tok < span.y)
+              x[i] = __ldg(reinterpret_cast<const uint4*>(pool + at_blk * st[0] + (key & (c.page - 1)) * st[2]));
+          }
         }
       };
       auto store = [&](int i, uint8_t* tile) {
@@ -333,42 +340,31 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
       const uint8_t* const k_pool = c.k + h * c.ks[1] + unit * 16;
       const uint8_t* const v_pool = c.v + h * c.vs[1] + unit * 16;
       turn_over(0);
-      if constexpr (C::kGroup == 64) find(0, k_pool, c.ks);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) load(i, 0, k_pool, c.ks);
+      load(0, k_pool, c.ks);
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
         if (nth >= C::kStages && !(ok = prompt_warp_wait(&ctl->k_empty[stage], par ^ 1u, abort, a))) break;
-        // (values of a zero scale are stored zeros for all that counts: they are
-        // cleared below, and count with the scale 1)
-        const bool none = !(vs >= 1.17549435e-38f);
-        if (cw == 0 && lane / kG == j % kBatch)
-          s_meta[(nth & 3) * kG + lane % kG] =
-              make_float4(ks, none ? 0.0f : lg2(vs), none ? 1.0f : 1.0f / vs, blk >= 0 ? 1.0f : 0.0f);
-        const uint32_t zero = (__ballot_sync(0xFFFFFFFFu, none) >> (kG * (j % kBatch))) & ((1u << kG) - 1u);  // groups of this block
+        if (cw == 0 && lane / kG == j % kBatch) s_meta[(nth & 3) * kG + lane % kG] = mine;
+        const uint32_t zero = of_block(none, j);
         uint8_t* tile = smem + C::kOffK + stage * C::kKvBytes;
-        if constexpr (C::kGroup == 64) find(j, v_pool, c.vs);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          store(i, tile);
-          load(i, j, v_pool, c.vs);
-        }
+        for (int i = 0; i < kPer; ++i) store(i, tile);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->k_full[stage]);
+        load(j, v_pool, c.vs);
         if (j % kBatch == kBatch - 1) turn_over(j + 1);
         if (nth >= C::kStages && !(ok = prompt_warp_wait(&ctl->v_empty[stage], par ^ 1u, abort, a))) break;
         tile = smem + C::kOffV + stage * C::kKvBytes;
-        if constexpr (C::kGroup == 64) find(j + 1, k_pool, c.ks);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           if ((zero >> ((key0 + i * kKeysStep) / C::kGroup)) & 1u) x[i] = make_uint4(0, 0, 0, 0);
           store(i, tile);
-          load(i, j + 1, k_pool, c.ks);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->v_full[stage]);
+        if (j + 1 < n) load(j + 1, k_pool, c.ks);
         ++nth;
         if (++stage == C::kStages) stage = 0, par ^= 1u;
       }
