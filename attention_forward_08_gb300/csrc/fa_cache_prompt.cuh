@@ -60,7 +60,7 @@ struct PromptCfg {
   static constexpr int kColO = 256;                  // S: two buffers of kKeys columns a tile; P over S
   // Registers: 512 threads x 128 at launch; the softmax warps, which hold a
   // row of scores each, take the others'.
-  static constexpr int kRegsCtrl = 40, kRegsConv = kTiles == 2 ? 72 : 104, kRegsSoft = kTiles == 2 ? 200 : 208;
+  static constexpr int kRegsCtrl = kTiles == 2 ? 56 : 64, kRegsConv = 104, kRegsSoft = kTiles == 2 ? 176 : 232;
   static_assert(kRegsCtrl < 128 && kRegsConv < 128 && kRegsSoft > 128, "which warps give, which take");
   static_assert(128 * kRegsCtrl + 32 * kConvWarps * kRegsConv + 128 * kTiles * kRegsSoft <= 512 * 128,
                 "register split exceeds the launch allocation");
