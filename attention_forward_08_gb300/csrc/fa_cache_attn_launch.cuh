@@ -40,23 +40,26 @@ bool line_params(DecParams& p, const CacheAttnParams& a, int max_ctas, const Lau
   return true;
 }
 
-
-// Rows of a K/V head behind which a call is a prompt's.
+// Rows of a K/V head behind which a call is a prompt's: what the decode kernel
+// holds at once.  (Several such groups, each reading every key, lose from the
+// second on: 4 sequences of 8192 tokens, 8 heads, D 64: 48 rows 56.0 us against
+// 51.4, 128 rows 74.5 against 49.2; D 128: 69.9 against 57.6 and 102.6 against
+// 58.2; D 256: 32 rows 78.4 against 77.9, 128 rows 194 against 97.  Just below:
+// D 128, 32 rows 37.0 us here, 55.3 there.)
 template <int kD>
-constexpr int kPromptRows = 64;
+constexpr int kPromptRows = kD <= 128 ? 32 : 16;
 
-
-// With weights and one group of decode rows, the decode kernel keeps its
-// scores, unless a wide table would make them large (they take 4 bytes a row
-// for every token that the table could hold; the keys are then read twice):
-// 16 sequences of up to 4096 tokens, H 32/8, D 128: TIMES.
+// With weights, the decode kernel keeps its scores, unless a wide table would
+// make them large (they take 4 bytes a row for every token that the table could
+// hold; the keys are then read twice).  16 sequences of up to 4096 tokens, H
+// 32/8, D 128: 32.5 us kept, 46 us read twice.
 constexpr long long kMostScores = 256LL << 20;
 inline long long score_bytes(const CacheAttnParams& a) {
   return (long long)a.B * a.c.H * (((long long)a.c.M * a.c.page + 31) / 32) * a.n * a.group * 128;
 }
 template <int kD>
 bool keep_scores(const CacheAttnParams& a) {
-  return a.weights && (long long)a.n * a.group <= (kD <= 128 ? 32 : 16) &&
+  return a.weights && (long long)a.n * a.group <= kPromptRows<kD> &&
          (double)a.B * a.c.H * a.c.M * a.c.page * a.n * a.group * 4 <= (double)kMostScores;
 }
 
@@ -94,7 +97,7 @@ int launch_weights(const CacheAttnParams& a, int kind, bool f16, long long used,
 
 template <class C>
 int launch_decode(const CacheAttnParams& a, const LaunchCtx& ctx) {
-  CUtensorMap tk, tv;
+  CUtensorMap tk{}, tv{};
   if constexpr (C::kTma) {
     const int rows = a.c.page < C::kTile ? a.c.page : C::kTile;
     if (!encode_pool(&tk, a.c, false, rows) || !encode_pool(&tv, a.c, true, rows)) return FA_ERR_CUDA;
@@ -158,9 +161,8 @@ int launch_prompt(const CacheAttnParams& a, const LaunchCtx& ctx) {
 }
 
 // Which kernel: by the rows of a K/V head.  Up to 16 (the decoding step), 32
-// where the registers hold them, and several groups of these up to a bound
-// behind which the tensor memory kernel, which always computes 128 * kTiles
-// rows, is faster.
+// where the registers hold them; else the tensor memory kernel, which always
+// computes 128 * kTiles rows.
 enum class AttnPlan { kRows16, kRows32, kPrompt };
 template <int kD>
 AttnPlan attn_plan(const CacheAttnParams& a) {
@@ -179,8 +181,9 @@ long long plan_workspace(const CacheAttnParams& a, int num_sms) {
   }
 }
 
-// TMA where a box holds 4 KB and more (16 sequences of 4608 tokens, 8 heads of
-// 64, blocks of 16: TIMES with boxes of 1 KB, TIMES with cp.async).
+// TMA where a box holds 4 KB and more.  (Blocks of 16 tokens of D 64, int8, 75 MB
+// of cache: 36.1 us with boxes of 1 KB, 32.3 with cp.async.  Blocks of 64 of D 128,
+// 361 MB: 67.6 us with boxes of 4 KB, 83.7 with cp.async.)
 template <int kD, int kKind, bool kF16, int kMT>
 int launch_decode_by(const CacheAttnParams& a, const LaunchCtx& ctx) {
   if constexpr (kD >= 128) {

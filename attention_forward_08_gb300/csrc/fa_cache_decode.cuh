@@ -1,7 +1,7 @@
 // fa_cache_decode.cuh -- attention of few query rows over the 8-bit cache.
 //
 // The rows of a K/V head share every key and value that is read; a thread
-// block takes up to 16 * kMT of them at a time (fa_cache_line.cuh).
+// block takes all of them, up to 16 * kMT.
 //
 // Mathematics.  S = Q K^T and O += P V on the tensor cores (m16n8k16, f16 in,
 // fp32 out), with an online softmax in base 2.  Nothing is lost on the way to
@@ -22,9 +22,8 @@
 // memory busy); the other warps take turns at the tiles, and each keeps a
 // running maximum, sum and output of its own in registers, so that no barrier
 // stands between two tiles.  The ring is filled by TMA where a tile's part of a
-// cache block is 4 KB and more, else by cp.async: a box costs its issuing
-// thread some 250 cycles whatever its size.  Tiles are shared out evenly over
-// the machine (fa_cache_line.cuh).
+// cache block is 4 KB and more, else by cp.async (fa_cache_attn_launch.cuh).
+// Tiles are shared out evenly over the machine (fa_cache_line.cuh).
 //
 // Layout.  Neither product cares about the order of its summed index, nor
 // about the order of the columns it produces: lane (g, t) takes the bytes
@@ -33,7 +32,11 @@
 // 128-byte swizzle, free of conflicts; the matching permutation is applied to
 // Q once, and undone by where O is written.
 //
-// Bound: memory; 2 * D bytes a token and K/V head, read once per row group.
+// Bound: memory; 2 * D bytes a token and K/V head, read once.  32 sequences of up to 8192 tokens, H 32/8, D 128, e4m3:
+// 66.6 us, 5.4 TB/s; one of 131072: 52.3 us, 5.1 TB/s.  (The loop itself moves
+// 7.5 TB/s; the rest is its start, the join and two launches.)  Tried and
+// slower: loads straight to registers (79.9 us on the first), a cp.async queue
+// a lane (83.7 us), one block of 10 + 2 warps an SM (102 us).
 #pragma once
 
 #include "fa_cache_line.cuh"
@@ -244,12 +247,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 
 #pragma unroll 1
   for (int pos = t0; pos < t1;) {
-    const int b = at.b, h = at.h, r0 = at.rg * C::kRows, r1 = min(p.rows, r0 + C::kRows);
+    const int b = at.b, h = at.h;
     const DecSeq seq = at.seq;
     // the first tile of a sequence tells about its length
-    if (tid == 0 && h == 0 && at.rg == 0 && pos == at.seg0) (void)checked_len(c, a.lens[b]);
-    const int tiles = dec_tiles<C>(p, seq, at.rg);
-    const int2 span = dec_group_span<C>(p, seq, at.rg);
+    if (tid == 0 && h == 0 && pos == at.seg0) (void)checked_len(c, a.lens[b]);
+    const int tiles = dec_tiles<C>(p, seq, 0);
+    const int2 span = dec_group_span<C>(p, seq, 0);
     const int first_tile = span.x / C::kTile + pos - at.seg0;
     const int n_tiles = min(t1, at.seg0 + tiles) - pos;
     const bool whole = n_tiles == tiles;
@@ -405,8 +408,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       uint32_t qw[kMine][kE / 2];
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
-        const int row = r0 + warp + i * kW, qi = row / a.group, head = h * a.group + row % a.group;
-        const bool in = warp + i * kW < C::kRows && row < r1 && qi < seq.nq;
+        const int row = warp + i * kW, qi = row / a.group, head = h * a.group + row % a.group;
+        const bool in = row < p.rows && qi < seq.nq;
         const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + b * a.qs[0] +
                                                               head * a.qs[1] + qi * a.qs[2]) + lane * (kE / 2);
 #pragma unroll
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           f[2 * e] = half_bits_to_f32<C::kF16>(qw[i][e]);
           f[2 * e + 1] = half_bits_to_f32<C::kF16>(qw[i][e] >> 16);
         }
-        if (!C::kF16 && r0 + r < r1) {
+        if (!C::kF16 && r < p.rows) {
           float top = 0.0f;
 #pragma unroll
           for (int e = 0; e < kE; ++e) top = fmaxf(top, fabsf(f[e]));
@@ -449,14 +452,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         for (int x = 0; x < 2; ++x) {
           m[mt][x] = -INFINITY;
           l[mt][x] = 0.0f;
-          const int r = mt * 16 + g + 8 * x, row = r0 + r;
-          rs[mt][x] = s_rs[r];
+          const int row = mt * 16 + g + 8 * x;
+          rs[mt][x] = s_rs[row];
           const int i = row / a.group;
-          const bool real = row < r1 && i < seq.nq;
+          const bool real = row < p.rows && i < seq.nq;
           const int2 v = real ? dec_span(a, seq, i, i) : make_int2(0, 0x7fffffff);
           // a row of the tile that is no query row may see anything: nothing of it is written
           lo_row[mt][x] = v.x;
-          hi_row[mt][x] = row < r1 && !real ? 0 : v.y;
+          hi_row[mt][x] = row < p.rows && !real ? 0 : v.y;
           lo_all = max(lo_all, lo_row[mt][x]);
           hi_all = min(hi_all, hi_row[mt][x]);
         }
@@ -679,7 +682,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       const int slot = 2 * blockIdx.x + (pos > at.seg0 ? 0 : 1);
 #pragma unroll
       for (int pass = 0; pass < C::kRows / C::kJoinRows; ++pass) {
-        if (r0 + pass * C::kJoinRows >= r1) break;
+        if (pass * C::kJoinRows >= p.rows) break;
         if (pass > 0) named_bar_sync(1, 32 * kW);  // the rows before have been read
 #pragma unroll
         for (int mt = 0; mt < C::kMT; ++mt)
@@ -702,7 +705,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           }
         named_bar_sync(1, 32 * kW);
 #pragma unroll 1
-        for (int v = tid; v < min(r1 - r0 - pass * C::kJoinRows, C::kJoinRows) * (C::kD / 4); v += 32 * kW) {
+        for (int v = tid; v < min(p.rows - pass * C::kJoinRows, C::kJoinRows) * (C::kD / 4); v += 32 * kW) {
           const int rj = v / (C::kD / 4), r = pass * C::kJoinRows + rj, d = (v % (C::kD / 4)) * 4;
           float top = -INFINITY, sum = 0.0f;
           float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -715,7 +718,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
             x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
           }
           if (whole) {
-            dec_write<C>(a, b, h, r0 + r, d, x, top, sum);
+            dec_write<C>(a, b, h, r, d, x, top, sum);
           } else {
             *reinterpret_cast<float4*>(p.part_o + ((long long)slot * C::kRows + r) * C::kD + d) = x;
             if (d == 0) p.part_ml[(long long)slot * C::kRows + r] = make_float2(top, sum);
