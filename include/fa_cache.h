@@ -107,13 +107,20 @@ int fa_cache_append(const fa_cache_append_args* args);
  *
  * A row that sees no key, and the rows i >= n_q[b] that pad a sequence, get
  * O = 0 and L = -inf and add no weight.  Keys that no row sees get weight
- * added 0.  Stored bytes behind lens[b] may be anything, NaN included.
+ * added 0.  Stored bytes behind lens[b] may be anything, NaN included.  (A NaN
+ * or an infinite score that a row sees makes that row NaN, as the formula does;
+ * a NaN among the values of a token may also reach the rows of its sequence and
+ * K/V head that do not see that token, where another row of the call does: a
+ * weight of 0 times NaN is NaN.)
  *
  * q, o: [B, H_q, n, D] bf16 or fp16, element strides {batch, head, row}, unit
  * inner stride, 16-byte aligned; lse: fp32 contiguous [B, H_q, n]; weights:
  * NULL or fp32 contiguous [B, H_kv, W], W >= every lens[b] (tokens at W and
  * behind get none and set the status above).  Sums over rows and heads are
- * taken in a fixed order: results do not change from run to run.
+ * taken in a fixed order: results do not change from run to run.  The order
+ * depends on how the work is shared out, so on the device's SM count and on
+ * fa_set_max_ctas, which caps this call's thread blocks too (SMs, or pairs an SM
+ * for few rows): results with another cap differ by fp32 rounding.
  * workspace: 256-byte aligned, fa_cache_attn_workspace_bytes(args) bytes.
  */
 typedef struct fa_cache_attn_args {
