@@ -150,6 +150,12 @@ def _on(device, name, t, dtype, shape=None):
     return t.data_ptr()
 
 
+def _int32(name, x):
+    """A count for the C ABI, which would take a longer one's low 32 bits."""
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise ValueError(f"{name} ({x}) must fit 32 bits")
+
+
 def _table(device, name, table, B, width):
     """An int32 [B, M] table, unit inner stride: (pointer, row stride, M)."""
     import torch
@@ -318,6 +324,8 @@ def cache_attention(q, cache, table, lens, *, n_q=None, scale=None, causal=True,
     n_ptr = None if n_q is None else _on(device, "n_q", n_q, torch.int32, (B,))
     w_ptr, _, W = (None, None, 0) if weights is None else _trackers(device, c.H_kv, weights, None, B)
     qs = _rows("q", q)
+    if window:
+        _int32("window", window)
     if out is not None and (out.shape != shape or out.dtype is not q.dtype or out.device != device):
         raise ValueError(f"out must be {q.dtype} {tuple(shape)} on {device}")
     if lse is not None:
@@ -360,6 +368,8 @@ def cache_evict(cache, table, lens, weights, positions=None, *, keep, recent=0, 
         wo_ptr, po_ptr, W_out = _trackers(device, c.H_kv, weights_out, positions_out, B)
     elif weights_out is not None or positions_out is not None:
         raise ValueError("weights_out and positions_out go with into; in place, weights and positions are changed")
+    _int32("keep", keep)
+    _int32("recent", recent)
     if lens_out is not None:
         _on(device, "lens_out", lens_out, torch.int32, (B,))
 

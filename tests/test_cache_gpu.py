@@ -517,6 +517,87 @@ def test_budget_loop_against_the_definition(fa):
     assert (weights[:, :, :24] >= 0).all()
 
 
+@pytest.mark.parametrize("kind,page,D,Hq", [(E4M3, 16, 64, 4), (I8, 32, 128, 8), (E4M3, 64, 256, 2)])
+def test_budget_loop_operator_by_operator(fa, kind, page, D, Hq):
+    """Each operator of each step against its definition on the state that the one before left: bytes, scales,
+    trackers and lengths to the bit, outputs and weights within the attention's tolerances."""
+    g = torch.Generator().manual_seed(page + D)
+    B, H, keep, recent, news = 3, 2, 40, 9, [[50, 7, 33], [1, 1, 1], [1, 1, 1], [5, 0, 2], [1, 1, 1], [40, 40, 1]]
+    M = -(-(keep + 50) // page)
+    cache = fa.kv_cache(B * M, H, D, page=page, dtype=kind)
+    rows = [list(range(b * M, b * M + M)) for b in range(B)]
+    table, W = i32(rows), M * page
+    weights, positions = torch.zeros(B, H, W, device=DEV), torch.zeros(B, H, W, dtype=torch.int32, device=DEV)
+    held, seen = [0] * B, [0] * B
+
+    def here():
+        return R.Cache(cache.k.cpu(), cache.v.cpu(), cache.k_scale.cpu(), cache.v_scale.cpu())
+
+    for new in news:
+        n = max(new)
+        q, k, v = (torch.randn(B, h, n, D, generator=g).to(BF16) for h in (Hq, H, H))
+        ref, w0, p0 = here(), weights.cpu(), positions.cpu()
+        fa.cache_append(cache, k.to(DEV), v.to(DEV), table, i32(held), n_new=i32(new), weights=weights,
+                        positions=positions, seen=i32(seen))
+        R.append(ref, {"k": k, "v": v}, rows, held, new)
+        same_pools(cache, ref, "append")
+        for b in range(B):
+            for t in range(new[b]):
+                w0[b, :, held[b] + t], p0[b, :, held[b] + t] = 0.0, seen[b] + t
+        assert torch.equal(weights.cpu(), w0) and torch.equal(positions.cpu(), p0)
+        held, seen = [x + y for x, y in zip(held, new)], [x + y for x, y in zip(seen, new)]
+        w0 = weights.clone()
+        got = fa.cache_attention(q.to(DEV), cache, table, i32(held), n_q=i32(new), weights=weights)
+        check_attention(fa, ref, q, rows, held, got, weights, w0, n_q=new)
+        rw, rp = weights.cpu().numpy().copy(), positions.cpu().numpy().copy()
+        lens = i32(held)
+        fa.cache_evict(cache, table, lens, weights, positions, keep=keep, recent=recent, lens_out=lens)
+        held, _ = R.evict(ref, rows, held, rw, rp, keep, recent)
+        assert lens.tolist() == held
+        same_pools(cache, ref, "evict")
+        np.testing.assert_array_equal(weights.cpu().numpy(), rw)
+        np.testing.assert_array_equal(positions.cpu().numpy(), rp)
+    synced(fa)
+
+
+def test_counts_beyond_32_bits_are_refused(fa):
+    cache = fa.kv_cache(2, 1, 64, page=16)
+    table, lens = i32([[0, 1]]), i32([4])
+    w, p = torch.zeros(1, 1, 32, device=DEV), torch.zeros(1, 1, 32, dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError, match="window"):
+        fa.cache_attention(torch.zeros(1, 1, 1, 64, dtype=BF16, device=DEV), cache, table, lens, window=2 ** 32 + 1)
+    with pytest.raises(ValueError, match="keep"):
+        fa.cache_evict(cache, table, lens, w, p, keep=2 ** 32 + 1)
+    with pytest.raises(ValueError, match="recent"):
+        fa.cache_evict(cache, table, lens, w, p, keep=4, recent=2 ** 32)
+
+
+@pytest.mark.parametrize("n,H,lens", [(8, 8, [128]), (16, 8, [128, 1, 0, 33]), (1, 3, [1, 2, 3]), (16, 1, [5])])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_short_segments(fa, n, H, lens, D):
+    """Segments shorter than a thread block's least part: one block each, some cut."""
+    attention_case(fa, D=D, Hq=4 * H, Hkv=H, lens=lens, n=n, n_q=[min(n, x) for x in lens], track=True)
+
+
+@pytest.mark.parametrize("softcap,scale", [(0.0, None), (5.0, None), (0.0, -0.1)])
+@pytest.mark.parametrize("page,D", [(16, 64), (64, 128), (128, 256), (16, 256), (128, 128)])
+def test_maximum_that_grows(fa, page, D, softcap, scale):
+    """Later keys far larger than earlier ones, for some rows: weights are taken again against a new maximum."""
+    g = torch.Generator().manual_seed(D + page)
+    lens = [700, 257]
+    table, P, _ = R.make_table(g, lens, page)
+    pools = R.make_pools(g, P, 2, page, D, E4M3)
+    for b in range(2):
+        for j, blk in enumerate(x for x in table[b] if x >= 0):
+            pools[2][blk] = 2.0 ** (-9 + j * page // 64)
+    q = torch.randn(2, 4, 150, D, generator=g).to(BF16)
+    q[:, :, ::3] *= 0.01
+    kw = {"softcap": softcap} if scale is None else {"softcap": softcap, "scale": scale}
+    got = fa.cache_attention(q.to(DEV), to_gpu(fa, pools), i32(table), i32(lens), **kw)
+    synced(fa)
+    check_attention(fa, R.Cache(*pools), q, table, lens, got, **kw)
+
+
 def test_budget_loop_captured_and_replayed(fa):
     a, sa = budget_loop(fa)
     b, sb = budget_loop(fa, graph=True)
