@@ -15,6 +15,8 @@ import math
 
 from . import fa as _fa
 
+torch = None  # imported with the first cache: not for those who only build, and not once a call
+
 FA_CACHE_E4M3, FA_CACHE_INT8 = 0, 1
 
 CACHE_EXPORTED = ("fa_cache_append", "fa_cache_attn", "fa_cache_attn_workspace_bytes", "fa_cache_evict",
@@ -97,6 +99,11 @@ def fa_cache_evict_workspace_bytes(args: FaCacheEvictArgs) -> int:
 
 # ----------------------------------------------------------------- torch convenience layer
 
+def _import_torch():
+    global torch
+    import torch
+
+
 class KVCache:
     """The pools of a paged cache: k, v [P, H_kv, page, D] in ``torch.float8_e4m3fn`` or ``torch.int8`` (unit inner
     stride, the other strides multiples of 16), and one fp32 scale for each block and head, [P, H_kv].  A key is its
@@ -105,7 +112,7 @@ class KVCache:
     __slots__ = ("k", "v", "k_scale", "v_scale", "c", "device")
 
     def __init__(self, k, v, k_scale, v_scale):
-        import torch
+        _import_torch()
         if k.dim() != 4:
             raise ValueError(f"k must be [P, H_kv, page, D] (got {tuple(k.shape)})")
         if k.dtype not in (torch.float8_e4m3fn, torch.int8):
@@ -131,7 +138,7 @@ class KVCache:
 
 def kv_cache(pages, H_kv, D, *, page=64, dtype=None, device="cuda") -> KVCache:
     """A new, empty cache of ``pages`` blocks (``dtype``: torch.float8_e4m3fn, the default, or torch.int8)."""
-    import torch
+    _import_torch()
     dtype = torch.float8_e4m3fn if dtype is None else dtype
     k, v = (torch.zeros((pages, H_kv, page, D), dtype=torch.uint8, device=device).view(dtype) for _ in range(2))
     ks, vs = (torch.zeros((pages, H_kv), dtype=torch.float32, device=device) for _ in range(2))
@@ -158,7 +165,6 @@ def _int32(name, x):
 
 def _table(device, name, table, B, width):
     """An int32 [B, M] table, unit inner stride: (pointer, row stride, M)."""
-    import torch
     shape = table.shape
     if len(shape) != 2 or shape[0] != B or table.dtype is not torch.int32 or table.device != device:
         raise ValueError(f"{name} must be an int32 [B = {B}, {width}] tensor on {device} "
@@ -179,7 +185,6 @@ def _rows(name, t):
 
 def _trackers(device, H, weights, positions, B):
     """(weights pointer, positions pointer, W) of fp32 and int32 [B, H_kv, W] trackers, each of which may be None."""
-    import torch
     w = p = None
     W = 0
     if weights is not None:
@@ -200,7 +205,6 @@ _DTYPES = {}
 
 
 def _dtype(t, name):
-    import torch
     if not _DTYPES:
         _DTYPES.update({torch.float32: _fa.FA_DTYPE_F32, torch.bfloat16: _fa.FA_DTYPE_BF16,
                         torch.float16: _fa.FA_DTYPE_F16})
@@ -214,7 +218,6 @@ def _dtype(t, name):
 def _foreign(device, stream):
     """The cache's device, and ``stream`` as torch's current one: what is allocated meanwhile belongs to the stream
     that uses it."""
-    import torch
     with torch.cuda.device(device):
         if stream is None:
             yield
@@ -225,7 +228,6 @@ def _foreign(device, stream):
 
 def _call(device, stream, work):
     """Run ``work(raw stream)`` on the cache's device and on the given or the current stream."""
-    import torch
     if stream is None and torch._C._cuda_getDevice() == device.index:
         return work(torch._C._cuda_getCurrentRawStream(device.index))
     with _foreign(device, stream):
@@ -236,7 +238,6 @@ def _with_scratch(a, need, workspace, device, call):
     """Run ``call(a)`` with ``need`` bytes of scratch: ``workspace`` if given, else memory of the stream, taken straight
     from torch's caching allocator (a tensor around it would cost a decoding loop more than the memory does) and given
     back behind the call: the allocator hands it out again only to work queued later on the same stream."""
-    import torch
     if need < 0:
         _fa._check(_fa.FA_ERR_INVALID_ARGUMENT)
     if workspace is not None:
@@ -268,7 +269,6 @@ def cache_append(cache, k, v, table, lens, *, n_new=None, weights=None, position
     A block's scale is the least power of two that its new values fit under, or the one that it had if that is
     larger; where it grows, the block's older tokens are rounded to it.  ``lens`` is not changed.
     """
-    import torch
     shape, device, c = k.shape, cache.device, cache.c
     if len(shape) != 4 or shape != v.shape or k.dtype is not v.dtype:
         raise ValueError(f"k and v must be 4-D [B, H_kv, n, D] and alike (got {tuple(k.shape)} {k.dtype}, "
@@ -309,7 +309,6 @@ def cache_attention(q, cache, table, lens, *, n_q=None, scale=None, causal=True,
     workspace: optional device tensor of at least ``fa_cache_attn_workspace_bytes`` bytes, 256-byte aligned
     (allocated here if None).
     """
-    import torch
     shape, device, c = q.shape, cache.device, cache.c
     if len(shape) != 4 or shape[3] != c.D:
         raise ValueError(f"q must be 4-D [B, H_q, n, D = {c.D}] (got {tuple(shape)})")
@@ -332,10 +331,15 @@ def cache_attention(q, cache, table, lens, *, n_q=None, scale=None, causal=True,
         _on(device, "lse", lse, torch.float32, (B, Hq, n))
 
     def work(raw):
-        o = torch.empty(shape, dtype=q.dtype, device=device) if out is None else out
+        o, os = out, None
+        if o is None:
+            if q.is_contiguous():
+                o, os = torch.empty_like(q), qs
+            else:
+                o = torch.empty(shape, dtype=q.dtype, device=device)
         l = torch.empty((B, Hq, n), dtype=torch.float32, device=device) if lse is None else lse
         if B and Hq and n:
-            a = FaCacheAttnArgs(c, q.data_ptr(), o.data_ptr(), l.data_ptr(), w_ptr, qs, _rows("out", o), t_ptr, t_stride,
+            a = FaCacheAttnArgs(c, q.data_ptr(), o.data_ptr(), l.data_ptr(), w_ptr, qs, os or _rows("out", o), t_ptr, t_stride,
                                 l_ptr, n_ptr, B, Hq, n, M, W, 1.0 / math.sqrt(D) if scale is None else scale,
                                 bool(causal), window, softcap, dtype, None, 0, raw)
             _with_scratch(a, fa_cache_attn_workspace_bytes(a), workspace, device, fa_cache_attn)
@@ -357,7 +361,6 @@ def cache_evict(cache, table, lens, weights, positions=None, *, keep, recent=0, 
     then be None (a token's position is its slot).
     lens_out: where the new lengths go (may be ``lens``); allocated here if None.
     """
-    import torch
     device, c, B = cache.device, cache.c, table.shape[0]
     t_ptr, t_stride, M = _table(device, "table", table, B, "M")
     l_ptr = _on(device, "lens", lens, torch.int32, (B,))
