@@ -14,7 +14,7 @@
 #include <cuda.h>
 
 #include "fa_cache_ops.cuh"
-#include "fa_ptx.cuh"
+#include "fa_cache_ptx.cuh"
 
 namespace fa {
 

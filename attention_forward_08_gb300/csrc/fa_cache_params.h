@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "fa_device.h"
 #include "fa_params.h"
 
 namespace fa {

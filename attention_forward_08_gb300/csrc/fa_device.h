@@ -4,6 +4,10 @@
 
 namespace fa {
 
+// A bit of the device status word beside kStatusTimeout (fa_params.h): a cache
+// length or table entry was out of range, and the tokens behind it skipped.
+constexpr unsigned int kStatusBadIndex = 1u << 1;
+
 struct DeviceInfo {
   int dev;
   int num_sms;

@@ -9,7 +9,6 @@ namespace fa {
 // Device status word bits (the library keeps one static word per device).
 enum : unsigned int {
   kStatusTimeout = 1u << 0,  // a bounded wait ran out; the kernel unwound early
-  kStatusBadIndex = 1u << 1, // a cache length or table entry out of range: the tokens behind it were skipped
 };
 
 struct FaParams {
