@@ -393,8 +393,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       // After an expired wait: the copies in flight land first (a bounded wait
       // again), then the block ends.
       if (C::kWide ? __syncthreads_or(!ok) : !ok) {
+        if constexpr (!C::kTma) {
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          return;
+        }
+        const long long begin = clock64_now();
         for (int k = max(0, tile0 + issued - kS); k < tile0 + issued; ++k) {
-          const long long begin = clock64_now();
           while (!mbar_try_wait(s_full + k % kS, (uint32_t)(k / kS) & 1u) && clock64_now() - begin < kDecDrainCycles) {
           }
         }
