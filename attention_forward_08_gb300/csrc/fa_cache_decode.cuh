@@ -202,6 +202,22 @@ __device__ __forceinline__ bool dec_wait(uint64_t* bar, uint32_t parity, volatil
   return false;
 }
 
+// The way out of a producer that has issued tiles 0 .. issued - 1: its copies
+// land before the block ends (a bounded wait; older tiles than the ring holds
+// have been consumed).
+template <class C>
+__device__ __forceinline__ void dec_drain(uint64_t* s_full, int issued) {
+  if constexpr (C::kTma) {
+    const long long begin = clock64_now();
+    for (int k = max(0, issued - C::kStages); k < issued; ++k)
+      while (!mbar_try_wait(s_full + k % C::kStages, (uint32_t)(k / C::kStages) & 1u) &&
+             clock64_now() - begin < kDecDrainCycles) {
+      }
+  } else {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     cache_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
@@ -390,18 +406,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           }
         }
       }
-      // After an expired wait: the copies in flight land first (a bounded wait
-      // again), then the block ends.
+      // After an expired wait the block ends here.
       if (C::kWide ? __syncthreads_or(!ok) : !ok) {
-        if constexpr (!C::kTma) {
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          return;
-        }
-        const long long begin = clock64_now();
-        for (int k = max(0, tile0 + issued - kS); k < tile0 + issued; ++k) {
-          while (!mbar_try_wait(s_full + k % kS, (uint32_t)(k / kS) & 1u) && clock64_now() - begin < kDecDrainCycles) {
-          }
-        }
+        dec_drain<C>(s_full, tile0 + issued);
         return;
       }
     } else {
@@ -739,6 +746,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     pos += n_tiles;
     dec_next(p, at, tiles);
   }
+  // Consumers whose wait expired have left without looking at the last copies.
+  // (Wide heads' producers leave with the consumers, above.)
+  if (!C::kWide && warp >= kW) dec_drain<C>(s_full, tile0);
 }
 
 }  // namespace fa

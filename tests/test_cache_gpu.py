@@ -668,3 +668,31 @@ def test_wait_bound_expires_or_not_then_recovers(fa, n, D):
     got = fa.cache_attention(qd, cache, t, ln)
     synced(fa)
     check_attention(fa, R.Cache(*pools), q, table, lens, got)
+
+
+@pytest.mark.parametrize("ctas", [0, 1])
+@pytest.mark.parametrize("cycles", [1, 300, 3000, 30000])
+@pytest.mark.parametrize("n,D,page,lens", [(1, 128, 64, [300, 40]), (1, 64, 16, [600]), (5, 128, 64, [3000, 31]),
+                                           (1, 256, 64, [150]), (5, 128, 16, [300, 2000])])
+def test_wait_bounds_of_any_length_then_the_next_call_is_right(fa, n, D, page, lens, cycles, ctas):
+    """Waits that expire while all of a short sequence's copies are under way: they land before the thread block ends,
+    so that whoever gets its shared memory next finds it its own."""
+    g = torch.Generator().manual_seed(D + n)
+    table, P, _ = R.make_table(g, lens, page)
+    pools = R.make_pools(g, P, 2, page, D, E4M3)
+    q = torch.randn(len(lens), 8, n, D, generator=g).to(BF16)
+    cache, qd, t, ln = to_gpu(fa, pools), q.to(DEV), i32(table), i32(lens)
+    torch.cuda.synchronize()
+    try:
+        fa.fa_set_max_ctas(ctas)
+        for _ in range(3):
+            fa.fa_set_timeout_cycles(cycles)
+            fa.cache_attention(qd, cache, t, ln)
+            fa.fa_set_timeout_cycles(0)
+            got = fa.cache_attention(qd, cache, t, ln)
+            rc = fa.fa_sync_status(None)
+            assert rc in (fa.fa.FA_OK, fa.fa.FA_ERR_DEVICE_TIMEOUT), fa.fa_last_error()
+            check_attention(fa, R.Cache(*pools), q, table, lens, got)
+    finally:
+        fa.fa_set_timeout_cycles(0)
+        fa.fa_set_max_ctas(0)
