@@ -49,7 +49,9 @@ __device__ __forceinline__ int2 dec_span(const CacheAttnParams& a, const DecSeq&
   if (i0 > i1) return make_int2(0, 0);
   const int p0 = s.len - s.nq + i0, p1 = s.len - s.nq + i1;
   const int hi = a.causal ? min(s.len, p1 + 1) : s.len;
-  const int lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
+  // (Where a call has more rows than tokens, the first stand before token 0: as
+  // far as the window's begin goes, at 0, so that no window leaves 32 bits.)
+  const int lo = a.window > 0 ? max(0, max(0, p0) - a.window + 1) : 0;
   return lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
 }
 // ... and the query rows of row group rg.

@@ -696,3 +696,12 @@ def test_wait_bounds_of_any_length_then_the_next_call_is_right(fa, n, D, page, l
     finally:
         fa.fa_set_timeout_cycles(0)
         fa.fa_set_max_ctas(0)
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 3, 2 ** 30])
+@pytest.mark.parametrize("n,lens", [(4, (1, 2, 9)), (8, (5, 0)), (40, (7, 39, 300)), (200, (100, 3, 199, 150))])
+@pytest.mark.parametrize("causal", [True, False])
+def test_window_wider_than_any_cache(fa, n, lens, window, causal):
+    """More rows than tokens, so that the first rows stand before the first token, and a window that means none."""
+    attention_case(fa, n=n, lens=lens, window=window, causal=causal, track=True)
+    attention_case(fa, n=n, lens=lens, window=window, causal=causal, D=64, page=16, kind=I8)
