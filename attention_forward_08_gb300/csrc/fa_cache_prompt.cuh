@@ -594,6 +594,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
       if ((warp & 3) == 0) ctl->n[t][pieces & 1] = 0;
       mbar_arrive(&ctl->q_full[t]);
     }
+    tmem_wait_st();  // (behind an expired wait, weights may be on their way to memory that is given back below)
   }
   tc_fence_before();
   __syncthreads();

@@ -705,3 +705,11 @@ def test_window_wider_than_any_cache(fa, n, lens, window, causal):
     """More rows than tokens, so that the first rows stand before the first token, and a window that means none."""
     attention_case(fa, n=n, lens=lens, window=window, causal=causal, track=True)
     attention_case(fa, n=n, lens=lens, window=window, causal=causal, D=64, page=16, kind=I8)
+
+
+@pytest.mark.parametrize("ctas", [0, 1])
+@pytest.mark.parametrize("cycles", [1, 300, 3000, 30000])
+@pytest.mark.parametrize("n,D,page,lens", [(64, 128, 64, [700, 300]), (70, 256, 64, [400]), (200, 64, 16, [900, 201])])
+def test_wait_bounds_of_many_rows_then_the_next_call_is_right(fa, n, D, page, lens, cycles, ctas):
+    """Stores to tensor memory that are under way when a wait expires are done before the memory is given back."""
+    test_wait_bounds_of_any_length_then_the_next_call_is_right(fa, n, D, page, lens, cycles, ctas)
