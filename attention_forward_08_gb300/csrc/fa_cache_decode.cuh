@@ -173,32 +173,35 @@ __device__ __forceinline__ float* dec_join_at(float* base, int r, int d) {
   return base + r * C::kD + (d & ~31) + ((((d >> 2) & 7) + 2 * (d >> 5) + r) & 7) * 4;
 }
 
-// A bounded wait by one thread; false once it ran out (or another did).
+// A bounded wait by one thread; false once it ran out (or another did).  The
+// bound is looked at before the hardware may suspend the thread: a bound of a
+// cycle expires wherever there is something to wait for.
 __device__ __forceinline__ bool dec_wait_one(uint64_t* bar, uint32_t parity, volatile int* abort, const CacheAttnParams& a) {
+  if (mbar_test(bar, parity)) return true;
   const long long begin = clock64_now();
-  while (!mbar_try_wait(bar, parity)) {
+  do {
     if (*abort) return false;
     if (clock64_now() - begin > a.timeout_cycles) {
       atomicOr(a.c.status, kStatusTimeout);
       *abort = 1;
       return false;
     }
-  }
+  } while (!mbar_try_wait(bar, parity));
   return true;
 }
 // A bounded wait by a whole warp; false once it ran out (or another did).
 __device__ __forceinline__ bool dec_wait(uint64_t* bar, uint32_t parity, volatile int* abort, const CacheAttnParams& a) {
-  bool ok = mbar_try_wait(bar, parity);
+  bool ok = mbar_test(bar, parity);
   if (!ok) {
     const long long begin = clock64_now();
-    while (!ok) {
-      ok = mbar_try_wait(bar, parity);
-      if (!ok && (*abort || clock64_now() - begin > a.timeout_cycles)) break;
+    while (!*abort && clock64_now() - begin <= a.timeout_cycles && !(ok = mbar_try_wait(bar, parity))) {
     }
   }
   if (__all_sync(0xFFFFFFFFu, ok)) return true;
-  if (!*abort && (threadIdx.x & 31) == 0) atomicOr(a.c.status, kStatusTimeout);
-  *abort = 1;
+  if ((threadIdx.x & 31) == 0) {
+    if (!*abort) atomicOr(a.c.status, kStatusTimeout);
+    *abort = 1;
+  }
   return false;
 }
 

@@ -95,16 +95,16 @@ struct PromptCtl {
 
 __device__ __forceinline__ bool prompt_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
                                             const CacheAttnParams& a) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_test(bar, parity)) return true;
   const long long begin = clock64_now();
-  while (!mbar_try_wait(bar, parity)) {
+  do {  // the bound is looked at before the hardware may suspend the thread
     if (*abort) return false;
     if (clock64_now() - begin > a.timeout_cycles) {
       *abort = 1;
       atomicOr(a.c.status, kStatusTimeout);
       return false;
     }
-  }
+  } while (!mbar_try_wait(bar, parity));
   return true;
 }
 __device__ __forceinline__ bool prompt_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,

@@ -18,6 +18,19 @@ __device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool mine) {
   return any != 0;
 }
 
+// A probe that never suspends the thread: has the phase of this parity completed?
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Issue by a whole warp: every lane runs the same code, one of them (`lead`,
 // from elect_lead) issues.  Control flow and operands stay uniform, so that the
 // operands live in uniform registers; a branch on the lane would move each of

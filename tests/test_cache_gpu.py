@@ -1,4 +1,6 @@
 """GPU parity of the 8-bit cache operators with their definition in 64 bits (tests/cache_reference.py)."""
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -713,3 +715,31 @@ def test_window_wider_than_any_cache(fa, n, lens, window, causal):
 def test_wait_bounds_of_many_rows_then_the_next_call_is_right(fa, n, D, page, lens, cycles, ctas):
     """Stores to tensor memory that are under way when a wait expires are done before the memory is given back."""
     test_wait_bounds_of_any_length_then_the_next_call_is_right(fa, n, D, page, lens, cycles, ctas)
+
+
+@pytest.mark.parametrize("n,D,page", [(1, 64, 16), (1, 128, 64), (1, 128, 16), (5, 128, 64), (1, 256, 64), (1, 256, 16),
+                                      (64, 64, 64), (64, 128, 64), (64, 256, 64)])
+def test_wait_bound_expires_then_recovers(fa, n, D, page):
+    """A wait looks at its bound before the hardware may suspend it: with a bound of one cycle the first wait whose
+    copy or product is not there yet expires, every role unwinds at once, and the status tells."""
+    g = torch.Generator().manual_seed(1)
+    lens = [3000, 700]
+    table, P, _ = R.make_table(g, lens, page)
+    pools = R.make_pools(g, P, 2, page, D, E4M3)
+    q = torch.randn(2, 8, n, D, generator=g).to(BF16)
+    cache, qd, t, ln = to_gpu(fa, pools), q.to(DEV), i32(table), i32(lens)
+    fa.cache_attention(qd, cache, t, ln)
+    torch.cuda.synchronize()
+    try:
+        fa.fa_set_timeout_cycles(1)
+        begin = time.monotonic()
+        fa.cache_attention(qd, cache, t, ln)
+        rc = fa.fa_sync_status(None)
+        took = time.monotonic() - begin
+    finally:
+        fa.fa_set_timeout_cycles(0)
+    assert rc == fa.fa.FA_ERR_DEVICE_TIMEOUT, fa.fa_last_error()
+    assert took < 1.0, f"unwinding took {took:.2f} s"
+    got = fa.cache_attention(qd, cache, t, ln)
+    synced(fa)
+    check_attention(fa, R.Cache(*pools), q, table, lens, got)
