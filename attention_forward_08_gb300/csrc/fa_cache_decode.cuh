@@ -10,12 +10,15 @@
 // entry 2^-34 below that is lost at most).  Over the 16 tokens of a step the
 // scales ks, vs are constant, and row i's weights are kept as
 //
-//   P'_ij = 2^(s_ij + log2 vs_j - m_i),   O = sum_j P'_ij v8_j / l_i,   l_i = sum_j P'_ij / vs_j
+//   P'_ij = 2^(s_ij + log2 vs_j - r_i),   O = sum_j P'_ij v8_j / l_i,   l_i = sum_j P'_ij / vs_j
 //
-// with m_i the running maximum of s + log2 vs: v_scale costs an addition in
-// the exponent, and what counts most in O always has P' near 1, whatever the
-// scales of other blocks.  P' is rounded to f16 (2^-11; the output has 2^-8 or
-// 2^-11), the sums are not.
+// with r_i 2^11 below the running maximum of s + log2 vs (fa_cache_line.cuh):
+// v_scale costs an addition in the exponent.  P' is rounded to f16: by 2^-11
+// (the output has 2^-8 or 2^-11) down to weights 2^-25 of the row's largest, by
+// 2^-36 of the largest below, "largest" in units of value, weight * v_scale.
+// So a first token that holds nearly all of a row's weight, with a value near 0,
+// leaves the others' sum right, and an outlier's large v_scale hides other
+// blocks only past that range.  The sums are not rounded to f16.
 //
 // Work.  A producer warp brings tiles of 32 tokens into a ring, with their
 // scales (two, one for K and one for V, where few wide tiles must keep the
@@ -50,6 +53,7 @@ struct DecCfg {
   static constexpr bool kF16 = kF16_;  // type of q and o
   static constexpr int kD = kD_, kMT = kMT_;
   static constexpr int kTile = 32;  // tokens
+  static constexpr int kLift = 11;  // of the weights (a reference that moves costs little here)
   // As many consumer warps as the outputs that each holds (kMT * D / 2 registers
   // a lane) leave room for, and two producers an SM: one block of 8 warps with
   // 255 registers, or two of 6 with 168.
@@ -87,8 +91,8 @@ struct DecCfg {
 };
 
 // What a consumer needs beside a tile's bytes, for its two halves of 16
-// tokens: ks; log2 vs and 1 / vs (0 and 0 where values do not count: a zero
-// scale; 1 / vs is -1 where nothing is stored).
+// tokens: ks; log2 vs and 1 / vs, less the weights' lift (0 and 0 where values
+// do not count: a zero scale; 1 / vs is -1 where nothing is stored).
 struct DecMeta {
   float ks[2], lv[2], rv[2];
   int blk[2];  // for the producer itself
@@ -231,7 +235,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* s_q = smem + C::kOffQ;
-  float2* s_ml = reinterpret_cast<float2*>(smem + C::kOffMl);        // [warp][row]: maximum, sum
+  float2* s_ml = reinterpret_cast<float2*>(smem + C::kOffMl);        // [warp][row]: reference, sum
   DecMeta* s_meta = reinterpret_cast<DecMeta*>(smem + C::kOffMeta);  // [tile % 64]
   uint64_t* s_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* s_empty = s_full + kS;
@@ -308,7 +312,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         if (k0 + (lane >> shift) < n_tiles) {
           DecMeta* meta = s_meta + ((tile0 + k0 + (lane >> shift)) & 63);
           const bool counts = vs >= 1.17549435e-38f;
-          const float lv = counts ? lg2(vs) : 0.0f, rv = blk < 0 ? -1.0f : counts ? rcp_approx(vs) : 0.0f;
+          const float lv = counts ? lg2(vs) : 0.0f, rv = blk < 0 ? -1.0f : counts ? rcp_approx(vs) * dec_unlift(C::kLift) : 0.0f;
           if (keys) meta->ks[sub_at] = ks;
           if (values) meta->lv[sub_at] = lv, meta->rv[sub_at] = rv;
           if (subs == 1) {
@@ -455,7 +459,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       named_bar_sync(1, 32 * kW);
 
       float o[C::kMT][C::kNTiles][4];
-      float m[C::kMT][2], l[C::kMT][2], rs[C::kMT][2];
+      float m[C::kMT][2], l[C::kMT][2], rs[C::kMT][2];  // m: the reference
       int hi_row[C::kMT][2], lo_row[C::kMT][2];  // the tokens that this lane's two rows see
       int lo_all = 0, hi_all = 0x7fffffff;       // ... that every row of the warp sees
 #pragma unroll
@@ -569,7 +573,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
             v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
             v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
             mx[mt][x] = v;
-            grow = grow || v > m[mt][x] + kDecLazy;
+            grow = grow || dec_grown(v, m[mt][x]);
           }
         }
         if (p.scores) {  // for cache_finish_kernel: 8 neighbouring tokens of a row a quad
@@ -593,7 +597,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
             float al[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const float m2 = fmaxf(m[mt][x], mx[mt][x]);
+              const float m2 = fmaxf(m[mt][x], dec_reference<C>(mx[mt][x]));
               al[x] = m2 == -INFINITY ? 1.0f : ex2(m[mt][x] - m2);
               l[mt][x] *= al[x];
               m[mt][x] = m2;
@@ -609,7 +613,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t pa[C::kMT][4];  // P' as the A operand
-          const float lv = half ? meta.w : meta.z, rv_half = half ? rv.y : rv.x, by = rv_half > 0.0f ? rv_half : 1.0f;
+          const float lv = half ? meta.w : meta.z, rv_half = half ? rv.y : rv.x, by = rv_half > 0.0f ? rv_half : dec_unlift(C::kLift);
 #pragma unroll
           for (int mt = 0; mt < C::kMT; ++mt) {
             const float m0 = lv - (m[mt][0] == -INFINITY ? 0.0f : m[mt][0]);
@@ -682,7 +686,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         if (stage >= kS) stage -= kS, phase ^= 1u;
       }
 
-      // Join the warps: O at the block's common maximum.
+      // Join the warps: O at the block's common reference.
 #pragma unroll
       for (int mt = 0; mt < C::kMT; ++mt)
 #pragma unroll

@@ -19,15 +19,28 @@
 namespace fa {
 
 constexpr float kDecLn2 = 0.6931471805599453f, kLog2eF = 1.4426950408889634f;
-constexpr float kDecLazy = 8.0f;  // the running maximum moves when it grows by more than 2^8: p stays below 2^8 in f16
 constexpr long long kDecDrainCycles = 1LL << 33;
+
+// Weights in f16.  A row's reference r is set 2^lift below its largest weight so
+// far, which is then 2^lift, and set again when one would be more than 2^14 (f16
+// ends at 2^16; the rest is room for the rounding of an exponent).  A weight
+// keeps all of its f16's 11 bits down to 2^-(14 + lift) of the largest, and is
+// lost below 2^-(25 + lift).
+constexpr float kDecMost = 14.0f;
+constexpr float dec_unlift(int lift) { return 1.0f / (float)(1 << lift); }
+// Has a row's largest score left the reference's range?  (The difference of
+// two neighbours is exact; false where there is no score yet.)
+__device__ __forceinline__ bool dec_grown(float top, float r) { return top - r > kDecMost; }
+// The reference for `top`: rounded up, so that top - r is never above the lift.
+template <class C>
+__device__ __forceinline__ float dec_reference(float top) { return __fsub_ru(top, (float)C::kLift); }
 
 struct DecParams {
   CacheAttnParams a;
   int rows, row_groups;   // rows of a K/V head; groups of kRows
   int max_ctas;
   float* part_o;          // [2 * max_ctas, kRows, D]
-  float2* part_ml;        // [2 * max_ctas, kRows]: maximum, sum
+  float2* part_ml;        // [2 * max_ctas, kRows]: reference, sum
   float* scores;          // [B, H, M * page / 32, rows, 32]: scores in base 2, for the weights (or NULL)
 };
 
@@ -199,17 +212,18 @@ __device__ __forceinline__ void dec_row_scale(float top, float& up, float& down)
   down = __uint_as_float((uint32_t)(ex - 9 + 127) << 23);
 }
 
-// Four columns of one output row, and its L.
+// Four columns of one output row, and its L: `x` are sums of lifted weights,
+// `sum` of weights as they are, both against the reference `top`.
 template <class C>
 __device__ __forceinline__ void dec_write(const CacheAttnParams& a, int b, int h, int row, int d, const float4& x,
                                           float top, float sum) {
   const int i = row / a.group, head = h * a.group + row % a.group;
-  const float inv = sum > 0.0f ? rcp_approx(sum) : 0.0f;
+  const float inv = sum > 0.0f ? rcp_approx(sum) * dec_unlift(C::kLift) : 0.0f;
   uint2 y;
   y.x = C::kF16 ? pack_f16x2(x.x * inv, x.y * inv) : pack_bf16x2(x.x * inv, x.y * inv);
   y.y = C::kF16 ? pack_f16x2(x.z * inv, x.w * inv) : pack_bf16x2(x.z * inv, x.w * inv);
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + b * a.os[0] + head * a.os[1] + i * a.os[2] + d) = y;
-  if (d == 0) a.lse[((long long)b * a.Hq + head) * a.n + i] = sum > 0.0f ? (top + lg2(sum)) * kDecLn2 : -INFINITY;
+  if (d == 0) a.lse[((long long)b * a.Hq + head) * a.n + i] = sum > 0.0f ? ((top + C::kLift) + lg2(sum)) * kDecLn2 : -INFINITY;
 }
 
 // The line's length, and the first tile (seg0) of sequence b; one row group.

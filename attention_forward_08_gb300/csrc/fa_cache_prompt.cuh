@@ -9,12 +9,13 @@
 // an f16 number, a bf16 query row is scaled by a power of two.  With k_scale
 // and v_scale constant over groups of 16 or 64 tokens (ks, vs), row i's weights are kept as
 //
-//   P'_ij = 2^(s_ij + log2 vs_j - m_i),   O = sum_j P'_ij v8_j / l_i,   l_i = sum_j P'_ij / vs_j
+//   P'_ij = 2^(s_ij + log2 vs_j - r_i),   O = sum_j P'_ij v8_j / l_i,   l_i = sum_j P'_ij / vs_j
 //
-// with m_i the running maximum of s + log2 vs: one FMA and one exponential a
-// score, the scales cost an operation per group, and what counts most in O
-// always has P' near 1, whatever the scales of other blocks.  P' is rounded to
-// f16 (2^-11), the sums are not.
+// with r_i 2^7 below the running maximum of s + log2 vs (fa_cache_line.cuh):
+// one FMA and one exponential a score, and the scales cost an operation per
+// group.  P' is rounded to f16, by 2^-11 down to 2^-21 of the row's largest
+// (weight * v_scale) and by 2^-32 of the largest below (fa_cache_decode.cuh);
+// the sums are not.
 //
 // Roles.  Warps 0 and 1 issue MMAs, one per row tile; the converter warps load
 // stored bytes straight from global memory into registers, half a block of 128
@@ -28,7 +29,7 @@
 // this one.  (With one buffer of 128 keys a tile, the tiles taking turns, each
 // block's scores, softmax and P V ran one after the other: 908 us against 865 on
 // the workload below.)  The softmax weighs a row against the maximum so far while
-// it finds the new one, and does it again where that has grown by more than 2^8.
+// it finds the new one, and does it again where that has grown by more than 2^7.
 //
 // Bound: the softmax warps' chains of dependent instructions, two warps a
 // scheduler, then the tensor cores (59% busy) and shared memory (the widened
@@ -58,6 +59,10 @@ struct PromptCfg {
   static constexpr int kRows = 128 * kTiles;
   static constexpr int kTile = 128;                  // keys a block of the line
   static constexpr int kMinTiles = 4;
+  // Of the weights: half of what f16 has room for, since a row whose maximum
+  // leaves the other half does its softmax twice (prompt piece: 802 us with 7,
+  // 815 with 10, 821 with 11).
+  static constexpr int kLift = 7;
   static constexpr int kStages = kD == 64 ? 3 : kD == 128 ? 2 : 1;  // of K; of V alike
   static constexpr int kIssuers = kTiles;
   // Keys a score buffer; a row tile has two, so that the next scores are being
@@ -143,7 +148,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
   const CacheView& c = a.c;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  float4* s_meta = reinterpret_cast<float4*>(smem + C::kOffMeta);  // [block % 4][group]: ks, log2 vs, 1 / vs, there
+  float4* s_meta = reinterpret_cast<float4*>(smem + C::kOffMeta);  // [block % 4][group]: ks, log2 vs, 1 / vs less the lift, there
   PromptCtl* ctl = reinterpret_cast<PromptCtl*>(smem + C::kOffCtl);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -308,7 +313,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
         // (values of a zero scale are stored zeros for all that counts: they are
         // cleared below, and count with the scale 1)
         const bool zero = !(vs >= 1.17549435e-38f);
-        mine = make_float4(ks, zero ? 0.0f : lg2(vs), zero ? 1.0f : 1.0f / vs, blk >= 0 ? 1.0f : 0.0f);
+        mine = make_float4(ks, zero ? 0.0f : lg2(vs), dec_unlift(C::kLift) * (zero ? 1.0f : 1.0f / vs), blk >= 0 ? 1.0f : 0.0f);
         there = __ballot_sync(0xFFFFFFFFu, blk >= 0);
         none = __ballot_sync(0xFFFFFFFFu, zero);
         next_blk = look_up(j0 + kBatch);
@@ -450,7 +455,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
       }
 
       const float f_row = rs * a.scale_log2;
-      float m = -INFINITY, l = 0.0f;
+      float m = -INFINITY, l = 0.0f;  // m: the reference
 #pragma unroll 1
       for (int j = 0; j < n * C::kParts; ++j, ++nth) {
         const int buf = nth & 1;
@@ -513,12 +518,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
             mx = fmaxf(mx, fmaf(fmax3(fmaxf(v[0], v[1]), v[2], v[3]), f[g], y[g]));
             part = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), inv_vs[g], part);
           }
-          const bool resc = mx > m + kDecLazy;
+          const bool resc = dec_grown(mx, m);  // (not twice: from its own reference a maximum is no further than the lift)
           if (!__any_sync(0xFFFFFFFFu, resc)) break;
           moved = true;
           if (resc) {
-            corr = ex2(m - mx);  // 0 when m = -inf
-            m = mx;
+            const float r = dec_reference<C>(mx);
+            corr = ex2(m - r);  // 0 when m = -inf
+            m = r;
           }
         }
         l = fmaf(l, corr, part);
@@ -553,7 +559,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
       ok = prompt_warp_wait(&ctl->o_ready[t], (uint32_t)(nth - 1) & 1u, abort, a);
       if (!ok) break;
       tc_fence_after();
-      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      const float inv = l > 0.0f ? dec_unlift(C::kLift) / l : 0.0f;
       const long long slot = (long long)(2 * blockIdx.x + (head_cut ? 0 : 1)) * C::kRows + t * 128 + tl;
       uint8_t* dst = static_cast<uint8_t*>(a.o) + (at.b * a.os[0] + head * a.os[1] + i * a.os[2]) * 2;
 #pragma unroll 1
@@ -583,7 +589,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
       tc_fence_before();
       if (real) {
         if (whole)
-          a.lse[((long long)at.b * a.Hq + head) * a.n + i] = l > 0.0f ? (m + lg2(l)) * kDecLn2 : -INFINITY;
+          a.lse[((long long)at.b * a.Hq + head) * a.n + i] = l > 0.0f ? ((m + C::kLift) + lg2(l)) * kDecLn2 : -INFINITY;
         else
           p.part_ml[slot] = make_float2(m, l);
       }

@@ -195,12 +195,12 @@ __global__ void __launch_bounds__(kJoinThreads) cache_finish_kernel(const __grid
   asm volatile("griddepcontrol.wait;" ::: "memory");  // scores, parts, and the L of whole segments are written
   if (tok0 >= span.y || tok0 + kFinishTokens <= span.x) return;
   if (tid < p.rows) {
-    float top = -INFINITY, sum = 0.0f;
+    float l2;
     if (c0 == c1) {
       const int i = tid / a.group, head = h * a.group + tid % a.group;
-      top = __ldcg(a.lse + ((long long)b * a.Hq + head) * a.n + i) * kLog2eF;
-      sum = 1.0f;
+      l2 = __ldcg(a.lse + ((long long)b * a.Hq + head) * a.n + i) * kLog2eF;
     } else {
+      float top = -INFINITY, sum = 0.0f;
 #pragma unroll 4
       for (int i = c0; i <= c1; ++i) {
         const float2 ml = __ldcg(p.part_ml + (long long)(2 * i + (i == c0)) * C::kRows + tid);
@@ -208,8 +208,9 @@ __global__ void __launch_bounds__(kJoinThreads) cache_finish_kernel(const __grid
         sum = fmaf(sum, ex2(top - z), ml.y * ex2(ml.x - z));
         top = m2;
       }
+      l2 = sum > 0.0f ? (top + C::kLift) + lg2(sum) : -INFINITY;
     }
-    s_l2[tid] = top > -INFINITY && sum > 0.0f ? top + lg2(sum) : INFINITY;  // (a row that sees nothing adds nothing)
+    s_l2[tid] = l2 > -INFINITY ? l2 : INFINITY;  // (a row that sees nothing adds nothing)
   }
   __syncthreads();
   const float* scores = p.scores + (long long)bh * ((a.c.M * (a.c.page >> 4) + 1) / 2) * p.rows * 32;

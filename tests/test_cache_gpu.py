@@ -743,3 +743,85 @@ def test_wait_bound_expires_then_recovers(fa, n, D, page):
     got = fa.cache_attention(qd, cache, t, ln)
     synced(fa)
     check_attention(fa, R.Cache(*pools), q, table, lens, got)
+
+
+def check_small_weights(q, got, ref, table, lens, floor):
+    """O against the definition: half a step of the output, 2^-11 of every weight's size (its f16 form), and what the
+    weights below f16's normal numbers lose at most, `floor`."""
+    ro, rl, _, a, sabs = R.attention(ref, q, table, lens)
+    o, lse = (t.double().cpu().numpy() for t in got)
+    tol_l = 2.0 ** -18 * sabs.max() + 1e-6
+    assert np.all(np.abs(lse - rl) <= tol_l)
+    tol = HALF[q.dtype] * np.abs(ro) + (HALF[F16] + 2 * tol_l) * a + floor + 1e-7
+    d = np.abs(o - ro)
+    assert np.all(d <= tol), f"max |dO| {d.max():.3e}, {(d / tol).max():.2f} of the tolerance, sum p |v| {a.mean():.3e}"
+
+
+def least_weight(rows):
+    """A row's largest weight is at least 2^lift in f16, whose numbers are 2^-24 apart at least, rounded by half that;
+    the lift is 11 where a K/V head has at most 32 rows, else 7."""
+    return 2.0 ** -(25 + (11 if rows <= 32 else 7))
+
+
+@pytest.mark.parametrize("ctas", [0, 1])
+@pytest.mark.parametrize("n,L,key,value", [(1, 16384, 24.0, 0.0), (5, 16384, 24.0, 0.0), (40, 16384, 24.0, 0.0),
+                                           (1, 16384, 24.0, 1.0), (40, 16384, 24.0, 1.0),
+                                           (1, 131071, 28.0, 0.0), (5, 131071, 28.0, 0.0)])
+def test_a_first_token_that_holds_nearly_all_the_weight(fa, n, ctas, L, key, value):
+    """As trained heads have it: 99.9% of each row's weight on one token whose value is (nearly) zero, so that the
+    output is made of weights 2^-24 of the largest."""
+    g = torch.Generator().manual_seed(L + n)
+    page, D, Hq, H = 64, 128, 4, 1
+    table, P, _ = R.make_table(g, [L], page)
+    k, v, ks, vs = R.make_pools(g, P, H, page, D, E4M3)
+    ks.fill_(1.0)
+    vs.fill_(2.0 ** -7)
+    k = (torch.randn(P, H, page, D, generator=g) * 0.25).to(E4M3)
+    k.view(torch.uint8)[..., 0] = 0
+    first = table[0][0]
+    k[first, 0, 0] = torch.zeros(D).to(E4M3)
+    k[first, 0, 0, 0] = torch.tensor(key).to(E4M3)
+    v[first, 0, 0] = torch.full((D,), value).to(E4M3)
+    q = torch.randn(1, Hq, n, D, generator=g) * 0.5
+    q[..., 0] = 8.0
+    q = q.to(BF16)
+    try:
+        fa.fa_set_max_ctas(ctas)
+        got = fa.cache_attention(q.to(DEV), to_gpu(fa, (k, v, ks, vs)), i32(table), i32([L]))
+        synced(fa)
+    finally:
+        fa.fa_set_max_ctas(0)
+    floor = least_weight(n * Hq) * 2.0 ** -7 * v.float().abs().sum((0, 1, 2)).double().numpy()
+    check_small_weights(q, got, R.Cache(k, v, ks, vs), table, [L], floor)
+
+
+@pytest.mark.parametrize("ctas", [0, 1])
+@pytest.mark.parametrize("n", [1, 5, 64])
+def test_an_outlier_block_hides_nothing_in_columns_where_it_is_zero(fa, n, ctas):
+    """A token with 90% of the weight in a block whose values have a scale 2^10 times the others', zero in half of the
+    columns: there the output is made of the other tokens alone."""
+    g = torch.Generator().manual_seed(n)
+    page, D, Hq, H, L = 16, 128, 4, 1, 8192
+    table, P, _ = R.make_table(g, [L], page)
+    k, v, ks, vs = R.make_pools(g, P, H, page, D, E4M3)
+    ks.fill_(1.0)
+    vs.fill_(2.0 ** -7)
+    k = (torch.randn(P, H, page, D, generator=g) * 0.25).to(E4M3)
+    k.view(torch.uint8)[..., 0] = 0
+    big = table[0][0]
+    vs[big] = 2.0 ** 3
+    k[big, 0, 3] = torch.zeros(D).to(E4M3)
+    k[big, 0, 3, 0] = torch.tensor(16.0).to(E4M3)
+    v.view(torch.uint8)[big] = 0
+    v[big, 0, 3, D // 2:] = torch.full((D // 2,), 448.0).to(E4M3)
+    q = torch.randn(1, Hq, n, D, generator=g) * 0.5
+    q[..., 0] = 8.0
+    q = q.to(BF16)
+    try:
+        fa.fa_set_max_ctas(ctas)
+        got = fa.cache_attention(q.to(DEV), to_gpu(fa, (k, v, ks, vs)), i32(table), i32([L]))
+        synced(fa)
+    finally:
+        fa.fa_set_max_ctas(0)
+    floor = least_weight(n * Hq) * 2.0 ** 3 * v.float().abs().sum((0, 1, 2)).double().numpy()
+    check_small_weights(q, got, R.Cache(k, v, ks, vs), table, [L], floor)
