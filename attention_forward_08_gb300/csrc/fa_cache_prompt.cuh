@@ -98,12 +98,13 @@ struct PromptCtl {
   int abort;
 };
 
+// kStrict: the bound is looked at before the hardware may suspend the thread
+// at all, as in dec_wait_one (everywhere, that made the prompt piece 0.7% slower);
+// else before it may do so twice.
+template <bool kStrict = false>
 __device__ __forceinline__ bool prompt_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
                                             const CacheAttnParams& a) {
-  // The first probe may suspend the thread for a while (a plain test, as in
-  // dec_wait_one, made the prompt piece 0.7% slower); the bound is looked at
-  // before any other may.
-  if (mbar_try_wait(bar, parity)) return true;
+  if (kStrict ? mbar_test(bar, parity) : mbar_try_wait(bar, parity)) return true;
   const long long begin = clock64_now();
   do {
     if (*abort) return false;
@@ -115,9 +116,10 @@ __device__ __forceinline__ bool prompt_wait(uint64_t* bar, uint32_t parity, vola
   } while (!mbar_try_wait(bar, parity));
   return true;
 }
+template <bool kStrict = false>
 __device__ __forceinline__ bool prompt_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
                                                  const CacheAttnParams& a) {
-  return __all_sync(0xFFFFFFFFu, prompt_wait(bar, parity, abort, a));
+  return __all_sync(0xFFFFFFFFu, prompt_wait<kStrict>(bar, parity, abort, a));
 }
 
 // 16 stored bytes -> 16 f16.
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
       bool ok = true;
 #pragma unroll 1
       for (int pieces = 0; ok; ++pieces) {
-        ok = wait(&ctl->q_full[t], pieces & 1);
+        ok = prompt_warp_wait<true>(&ctl->q_full[t], pieces & 1, abort, a);  // (query rows take a while to come)
         if (!ok) break;
         const int n = ctl->n[t][pieces & 1];
         if (n == 0) break;
