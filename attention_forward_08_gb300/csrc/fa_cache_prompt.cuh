@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
       ok = prompt_warp_wait(&ctl->o_ready[t], (uint32_t)(nth - 1) & 1u, abort, a);
       if (!ok) break;
       tc_fence_after();
-      const float inv = l > 0.0f ? dec_unlift(C::kLift) / l : 0.0f;
+      const float inv = l == 0.0f ? 0.0f : dec_unlift(C::kLift) / l;  // (a NaN row stays one)
       const long long slot = (long long)(2 * blockIdx.x + (head_cut ? 0 : 1)) * C::kRows + t * 128 + tl;
       uint8_t* dst = static_cast<uint8_t*>(a.o) + (at.b * a.os[0] + head * a.os[1] + i * a.os[2]) * 2;
 #pragma unroll 1
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
       tc_fence_before();
       if (real) {
         if (whole)
-          a.lse[((long long)at.b * a.Hq + head) * a.n + i] = l > 0.0f ? ((m + C::kLift) + lg2(l)) * kDecLn2 : -INFINITY;
+          a.lse[((long long)at.b * a.Hq + head) * a.n + i] = l == 0.0f ? -INFINITY : ((m + C::kLift) + lg2(l)) * kDecLn2;
         else
           p.part_ml[slot] = make_float2(m, l);
       }

@@ -208,9 +208,9 @@ __global__ void __launch_bounds__(kJoinThreads) cache_finish_kernel(const __grid
         sum = fmaf(sum, ex2(top - z), ml.y * ex2(ml.x - z));
         top = m2;
       }
-      l2 = sum > 0.0f ? (top + C::kLift) + lg2(sum) : -INFINITY;
+      l2 = sum == 0.0f ? -INFINITY : (top + C::kLift) + lg2(sum);
     }
-    s_l2[tid] = l2 > -INFINITY ? l2 : INFINITY;  // (a row that sees nothing adds nothing)
+    s_l2[tid] = l2 == -INFINITY ? INFINITY : l2;  // (a row that sees nothing adds nothing)
   }
   __syncthreads();
   const float* scores = p.scores + (long long)bh * ((a.c.M * (a.c.page >> 4) + 1) / 2) * p.rows * 32;
@@ -221,6 +221,13 @@ __global__ void __launch_bounds__(kJoinThreads) cache_finish_kernel(const __grid
   float sum = 0.0f;
 #pragma unroll 4
   for (int r = 0; r < p.rows; ++r) sum += ex2(__ldcg(s + r * 32) - s_l2[r]);
+  if (sum != sum) {  // a NaN row among them: only for the tokens that it sees
+    sum = 0.0f;
+    for (int r = 0; r < p.rows; ++r) {
+      const int2 see = dec_span(a, seq, r / a.group, r / a.group);
+      if (tok >= see.x && tok < see.y) sum += ex2(__ldcg(s + r * 32) - s_l2[r]);
+    }
+  }
   if (tok < a.W)
     out[tok] += sum;
   else

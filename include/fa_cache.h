@@ -108,8 +108,10 @@ int fa_cache_append(const fa_cache_append_args* args);
  * A row that sees no key, and the rows i >= n_q[b] that pad a sequence, get
  * O = 0 and L = -inf and add no weight.  Keys that no row sees get weight
  * added 0.  Stored bytes behind lens[b] may be anything, NaN included.  (A NaN
- * or an infinite score that a row sees makes that row NaN, as the formula does;
- * a NaN among the values of a token may also reach the rows of its sequence and
+ * or a +infinite score that a row sees makes that row's O and L NaN, and the
+ * weights of the tokens that it sees, as the formula does; a row whose scores
+ * are all -infinite counts as one that sees no key.
+ * A NaN among the values of a token may also reach the rows of its sequence and
  * K/V head that do not see that token, where another row of the call does: a
  * weight of 0 times NaN is NaN.)
  *

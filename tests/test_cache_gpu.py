@@ -825,3 +825,56 @@ def test_an_outlier_block_hides_nothing_in_columns_where_it_is_zero(fa, n, ctas)
         fa.fa_set_max_ctas(0)
     floor = least_weight(n * Hq) * 2.0 ** 3 * v.float().abs().sum((0, 1, 2)).double().numpy()
     check_small_weights(q, got, R.Cache(k, v, ks, vs), table, [L], floor)
+
+
+@pytest.mark.parametrize("ctas", [0, 1])
+@pytest.mark.parametrize("track", [False, True])
+@pytest.mark.parametrize("where", ["query", "key", "infinity"])
+@pytest.mark.parametrize("n,D,page,lens", [(1, 128, 64, [700, 40]), (5, 64, 16, [9, 300]), (6, 256, 64, [900, 33]),
+                                           (150, 128, 64, [150, 700]), (150, 64, 16, [400, 200])])
+def test_not_a_number_is_told(fa, n, D, page, lens, where, track, ctas):
+    """A row that sees a NaN score, or an infinite one, is NaN, its L too, and so is the weight of each token that it
+    sees; the other rows, and the tokens that no such row sees, are as if nothing was wrong."""
+    g = torch.Generator().manual_seed(n + D)
+    B, Hq, H = len(lens), 4, 2
+    table, P, _ = R.make_table(g, lens, page)
+    pools = R.make_pools(g, P, H, page, D, E4M3)
+    q = torch.randn(B, Hq, n, D, generator=g).to(F16 if where == "infinity" else BF16)
+    bad = np.zeros((B, Hq, n), bool)
+    at = lens[0] - 1 - n // 2  # a token that the later half of sequence 0's rows sees
+    qd = q.clone()
+    raw = [t.clone() for t in pools]
+    if where == "key":
+        raw[0].view(torch.uint8)[table[0][at // page], 1, at % page, 5] = 0x7F
+        bad[0, 2:] = lens[0] - n + np.arange(n) >= at
+    else:
+        bad[0, 1, n - 1] = bad[1, 3, 0] = True
+        qd[0, 1, n - 1, 7] = qd[1, 3, 0, 7] = float("nan" if where == "query" else "inf")
+        for b, h, i in ((0, 0, n - 1), (1, 1, 0)):  # (an infinite entry makes some score NaN or +inf)
+            blocks = [x for x in table[b] if x >= 0]
+            col = raw[0].float()[blocks, h // 2, :, 7].reshape(-1)[:lens[b] - n + i + 1]
+            assert (col >= 0).any()
+    w = w0 = None
+    if track:
+        w0 = torch.rand(B, H, max(lens), generator=g)
+        w = w0.to(DEV)
+    try:
+        fa.fa_set_max_ctas(ctas)
+        o, lse = fa.cache_attention(qd.to(DEV), to_gpu(fa, raw), i32(table), i32(lens), weights=w)
+        synced(fa)
+    finally:
+        fa.fa_set_max_ctas(0)
+    ref = R.Cache(*pools)
+    ro, rl, rw, _, _ = R.attention(ref, q, table, lens)
+    o, lse, there = o.cpu(), lse.cpu(), torch.from_numpy(bad)
+    assert torch.isnan(o[there]).all() and torch.isnan(lse[there]).all()
+    o[there], lse[there] = torch.from_numpy(ro)[there].to(o.dtype), torch.from_numpy(rl)[there].float()
+    if track:
+        w = w.cpu()
+        for b in range(B):
+            for h in range(H):
+                rows = np.nonzero(bad[b, 2 * h:2 * h + 2].any(0))[0]
+                seen = lens[b] - n + int(rows.max()) + 1 if len(rows) else 0
+                assert torch.isnan(w[b, h, :seen]).all()
+                w[b, h, :seen] = w0[b, h, :seen] + torch.from_numpy(rw)[b, h, :seen].float()
+    check_attention(fa, ref, q, table, lens, (o, lse), w, w0)
