@@ -218,10 +218,12 @@ template <class C>
 __device__ __forceinline__ void dec_write(const CacheAttnParams& a, int b, int h, int row, int d, const float4& x,
                                           float top, float sum) {
   const int i = row / a.group, head = h * a.group + row % a.group;
-  const float inv = sum == 0.0f ? 0.0f : rcp_approx(sum) * dec_unlift(C::kLift);  // (a NaN row stays one)
-  uint2 y;
-  y.x = C::kF16 ? pack_f16x2(x.x * inv, x.y * inv) : pack_bf16x2(x.x * inv, x.y * inv);
-  y.y = C::kF16 ? pack_f16x2(x.z * inv, x.w * inv) : pack_bf16x2(x.z * inv, x.w * inv);
+  const float inv = rcp_approx(sum) * dec_unlift(C::kLift);
+  uint2 y = make_uint2(0u, 0u);  // a row that sees nothing (another's NaN value may be in its x)
+  if (sum != 0.0f) {             // (a NaN row stays one)
+    y.x = C::kF16 ? pack_f16x2(x.x * inv, x.y * inv) : pack_bf16x2(x.x * inv, x.y * inv);
+    y.y = C::kF16 ? pack_f16x2(x.z * inv, x.w * inv) : pack_bf16x2(x.z * inv, x.w * inv);
+  }
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + b * a.os[0] + head * a.os[1] + i * a.os[2] + d) = y;
   if (d == 0) a.lse[((long long)b * a.Hq + head) * a.n + i] = sum == 0.0f ? -INFINITY : ((top + C::kLift) + lg2(sum)) * kDecLn2;
 }

@@ -564,7 +564,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
       ok = prompt_warp_wait(&ctl->o_ready[t], (uint32_t)(nth - 1) & 1u, abort, a);
       if (!ok) break;
       tc_fence_after();
-      const float inv = l == 0.0f ? 0.0f : dec_unlift(C::kLift) / l;  // (a NaN row stays one)
+      const bool none = l == 0.0f;  // sees nothing (another row's NaN value may be in its O; a NaN row stays one)
+      const float inv = dec_unlift(C::kLift) / l;
       const long long slot = (long long)(2 * blockIdx.x + (head_cut ? 0 : 1)) * C::kRows + t * 128 + tl;
       uint8_t* dst = static_cast<uint8_t*>(a.o) + (at.b * a.os[0] + head * a.os[1] + i * a.os[2]) * 2;
 #pragma unroll 1
@@ -580,7 +581,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float o0 = __uint_as_float(rr[8 * u + 2 * e]) * inv, o1 = __uint_as_float(rr[8 * u + 2 * e + 1]) * inv;
-              y[e] = C::kF16 ? pack_f16x2(o0, o1) : pack_bf16x2(o0, o1);
+              y[e] = none ? 0u : C::kF16 ? pack_f16x2(o0, o1) : pack_bf16x2(o0, o1);
             }
             *reinterpret_cast<uint4*>(dst + cc * 64 + u * 16) = make_uint4(y[0], y[1], y[2], y[3]);
           }
@@ -594,7 +595,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
       tc_fence_before();
       if (real) {
         if (whole)
-          a.lse[((long long)at.b * a.Hq + head) * a.n + i] = l == 0.0f ? -INFINITY : ((m + C::kLift) + lg2(l)) * kDecLn2;
+          a.lse[((long long)at.b * a.Hq + head) * a.n + i] = none ? -INFINITY : ((m + C::kLift) + lg2(l)) * kDecLn2;
         else
           p.part_ml[slot] = make_float2(m, l);
       }

@@ -112,8 +112,8 @@ int fa_cache_append(const fa_cache_append_args* args);
  * weights of the tokens that it sees, as the formula does; a row whose scores
  * are all -infinite counts as one that sees no key.
  * A NaN among the values of a token may also reach the rows of its sequence and
- * K/V head that do not see that token, where another row of the call does: a
- * weight of 0 times NaN is NaN.)
+ * K/V head that see other tokens but not that one, where another row of the
+ * call does: a weight of 0 times NaN is NaN.)
  *
  * q, o: [B, H_q, n, D] bf16 or fp16, element strides {batch, head, row}, unit
  * inner stride, 16-byte aligned; lse: fp32 contiguous [B, H_q, n]; weights:

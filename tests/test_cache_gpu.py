@@ -878,3 +878,26 @@ def test_not_a_number_is_told(fa, n, D, page, lens, where, track, ctas):
                 assert torch.isnan(w[b, h, :seen]).all()
                 w[b, h, :seen] = w0[b, h, :seen] + torch.from_numpy(rw)[b, h, :seen].float()
     check_attention(fa, ref, q, table, lens, (o, lse), w, w0)
+
+
+@pytest.mark.parametrize("ctas", [0, 1])
+@pytest.mark.parametrize("n,D", [(6, 64), (6, 256), (40, 128), (150, 64)])
+def test_rows_that_see_nothing_are_zero_beside_a_nan_value(fa, n, D, ctas):
+    """More rows than tokens, and padding behind n_q, in one row group with rows that see a NaN value."""
+    g = torch.Generator().manual_seed(n)
+    page, lens, n_q = 16, [n - 2, 60], [n, 3]
+    table, P, _ = R.make_table(g, lens, page)
+    pools = R.make_pools(g, P, 2, page, D, E4M3)
+    for b in range(2):
+        pools[1].view(torch.uint8)[table[b][0], :, 0] = 0x7F
+    q = torch.randn(2, 4, n, D, generator=g).to(BF16)
+    try:
+        fa.fa_set_max_ctas(ctas)
+        o, lse = fa.cache_attention(q.to(DEV), to_gpu(fa, pools), i32(table), i32(lens), n_q=i32(n_q))
+        synced(fa)
+    finally:
+        fa.fa_set_max_ctas(0)
+    assert (o[0, :, :2] == 0).all() and torch.isneginf(lse[0, :, :2]).all()
+    assert (o[1, :, 3:] == 0).all() and torch.isneginf(lse[1, :, 3:]).all()
+    assert torch.isnan(o[0, :, 2:]).all() and torch.isfinite(lse[0, :, 2:]).all()
+    assert torch.isnan(o[1, :, :3]).all() and torch.isfinite(lse[1, :, :3]).all()
