@@ -85,7 +85,7 @@ template <bool kCached>
 __device__ __forceinline__ int choose(const EvictParams& p, PlanShared& s, uint32_t* s_key, int n, const float* weight,
                                       const int* position, int* src, int* mover) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t first = weight_key(INFINITY);
+  const uint32_t first = ~0u;  // of protected tokens: above any weight's, +inf's too
   const int stop = (n + 31) & ~31;  // (whole warps stay together)
   for (int i = tid; i < kClasses; i += kPlanThreads) s.count[i] = 0;
   if (tid == 0) {

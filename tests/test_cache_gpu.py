@@ -901,3 +901,36 @@ def test_rows_that_see_nothing_are_zero_beside_a_nan_value(fa, n, D, ctas):
     assert (o[1, :, 3:] == 0).all() and torch.isneginf(lse[1, :, 3:]).all()
     assert torch.isnan(o[0, :, 2:]).all() and torch.isfinite(lse[0, :, 2:]).all()
     assert torch.isnan(o[1, :, :3]).all() and torch.isfinite(lse[1, :, :3]).all()
+
+
+@pytest.mark.parametrize("into", [True, False])
+@pytest.mark.parametrize("L", [20, 5000, 50000])
+@pytest.mark.parametrize("order", ["slots", "turned"])
+def test_evict_keeps_the_latest_before_infinite_weights(fa, into, L, order):
+    """Tokens pinned by an infinite weight, more of them than there is room beside the latest: the latest stay, then
+    the pinned ones of the lowest slots; with room for all pins, all stay."""
+    page, D, keep, recent, pins = 16, 64, 6, 3, 8
+    inf = float("inf")
+    M, extra = -(-L // page), 1
+    cache = fa.kv_cache(M + extra, 1, D, page=page)
+    w = torch.rand(1, 1, M * page, generator=torch.Generator().manual_seed(L))
+    p = torch.arange(M * page, dtype=torch.int32)
+    if order == "turned":  # the latest positions in the lowest slots
+        p = (L - 1 - p).contiguous()
+    p = p.view(1, 1, -1)
+    latest = list(range(3)) if order == "turned" else list(range(L - 3, L))
+    pinned = list(range(4, 4 + pins))
+    w[0, 0, pinned] = inf
+    w[0, 0, latest] = -inf  # (their weight does not count)
+    wd, pd = w.to(DEV), p.to(DEV)
+    table = i32([list(range(M))])
+    kept = sorted(latest + pinned[:keep - recent])
+    if into:
+        wo, po = torch.zeros(1, 1, keep, device=DEV), torch.zeros(1, 1, keep, dtype=torch.int32, device=DEV)
+        fa.cache_evict(cache, table, i32([L]), wd, pd, keep=keep, recent=recent, into=i32([[M]]), weights_out=wo, positions_out=po)
+    else:
+        fa.cache_evict(cache, table, i32([L]), wd, pd, keep=keep, recent=recent)
+        wo, po = wd[:, :, :keep], pd[:, :, :keep]
+    synced(fa)
+    assert sorted(po[0, 0].tolist()) == sorted(p[0, 0, kept].tolist())
+    assert sorted(wo[0, 0].tolist()) == sorted(w[0, 0, kept].tolist())
