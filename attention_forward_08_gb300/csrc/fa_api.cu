@@ -633,8 +633,9 @@ int fa_sync_status(void* stream) {
   unsigned int word = 0;
   e = cudaMemcpy(&word, g_status_ptr[dev], sizeof(word), cudaMemcpyDeviceToHost);
   if (e == cudaSuccess && word != 0) {
-    const unsigned int zero = 0;
-    e = cudaMemcpy(g_status_ptr[dev], &zero, sizeof(zero), cudaMemcpyHostToDevice);
+    // A timeout goes first; what else there is to tell waits for the next call.
+    const unsigned int rest = word & kStatusTimeout ? word & ~kStatusTimeout : 0;
+    e = cudaMemcpy(g_status_ptr[dev], &rest, sizeof(rest), cudaMemcpyHostToDevice);
   }
   if (e != cudaSuccess) {
     set_error("status word read: %s", cudaGetErrorString(e));

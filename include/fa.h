@@ -155,9 +155,12 @@ const char* fa_last_error(void);
 
 /*
  * fa_sync_status -- synchronise `stream`, then read and clear the device
- * status word of the current device.  FA_OK if no kernel stopped early since
- * the last call, FA_ERR_DEVICE_TIMEOUT if one did, FA_ERR_CUDA on a CUDA
- * error (including an earlier asynchronous kernel fault).
+ * status word of the current device.  FA_OK if there is nothing to tell since
+ * the last call, FA_ERR_DEVICE_TIMEOUT if a kernel stopped early,
+ * FA_ERR_INVALID_ARGUMENT if a cache call (fa_cache.h) met a length or a table
+ * entry out of range, FA_ERR_CUDA on a CUDA error (including an earlier
+ * asynchronous kernel fault).  Of both a timeout and a bad index, the timeout is
+ * told by this call and the index by the next.
  */
 int fa_sync_status(void* stream);
 

@@ -934,3 +934,20 @@ def test_evict_keeps_the_latest_before_infinite_weights(fa, into, L, order):
     synced(fa)
     assert sorted(po[0, 0].tolist()) == sorted(p[0, 0, kept].tolist())
     assert sorted(wo[0, 0].tolist()) == sorted(w[0, 0, kept].tolist())
+
+
+def test_status_tells_of_a_bad_index_behind_a_timeout(fa):
+    """Both since the last call: one is reported, and the other by the next call."""
+    cache = fa.kv_cache(2, 1, 64, page=16)
+    x = torch.ones(1, 1, 1, 64, dtype=BF16, device=DEV)
+    q = torch.randn(1, 4, 640, 128, device=DEV).to(BF16)
+    try:
+        fa.fa_set_timeout_cycles(1)
+        fa.cache_append(cache, x, x, i32([[99]]), i32([0]))
+        fa.attention(q, q, q, causal=True)
+        first = fa.fa_sync_status(None)
+    finally:
+        fa.fa_set_timeout_cycles(0)
+    assert first == fa.fa.FA_ERR_DEVICE_TIMEOUT
+    assert fa.fa_sync_status(None) == fa.fa.FA_ERR_INVALID_ARGUMENT and "out of range" in fa.fa_last_error()
+    assert fa.fa_sync_status(None) == fa.fa.FA_OK
