@@ -107,7 +107,8 @@ def _import_torch():
 class KVCache:
     """The pools of a paged cache: k, v [P, H_kv, page, D] in ``torch.float8_e4m3fn`` or ``torch.int8`` (unit inner
     stride, the other strides multiples of 16), and one fp32 scale for each block and head, [P, H_kv].  A key is its
-    stored value times its block's scale.  The tensors are the caller's; this object only keeps them together."""
+    stored value times its block's scale.  The tensors are the caller's; this object only keeps them together, with
+    their addresses: it cannot be given others later."""
 
     __slots__ = ("k", "v", "k_scale", "v_scale", "c", "device")
 
@@ -133,7 +134,14 @@ class KVCache:
         c.k_strides[:], c.v_strides[:] = k.stride()[:3], v.stride()[:3]
         c.P, c.H_kv, c.page, c.D = k.shape
         c.kind = FA_CACHE_INT8 if k.dtype == torch.int8 else FA_CACHE_E4M3
-        self.k, self.v, self.k_scale, self.v_scale, self.c, self.device = k, v, k_scale, v_scale, c, k.device
+        for name, x in zip(self.__slots__, (k, v, k_scale, v_scale, c, k.device)):
+            object.__setattr__(self, name, x)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"KVCache.{name} cannot be set: calls use the tensors that the cache was made of")
+
+    def __copy__(self):
+        return self
 
 
 def kv_cache(pages, H_kv, D, *, page=64, dtype=None, device="cuda") -> KVCache:

@@ -158,9 +158,10 @@ long long fa_cache_attn_workspace_bytes(const fa_cache_attn_args* args);
  * fa_cache_evict -- keep at most `keep` tokens of every sequence, chosen per
  * K/V head: the `recent` latest ones (positions > the head's largest position
  * - recent), then those with the largest accumulated weight, +infinity the
- * largest; ties go to the lowest slot, a NaN weight counts as -infinity.  A sequence with no more than `keep`
- * tokens keeps all.  The heads of a sequence may keep different tokens; all
- * keep equally many, so table and lens stay common.
+ * largest; ties go to the lowest slot, a NaN weight counts as -infinity.  A
+ * sequence with no more than `keep` tokens keeps all.  The heads of a sequence
+ * may keep different tokens; all keep equally many, so table and lens stay
+ * common.
  *
  * into == NULL: in place.  Kept tokens in slots below `keep` stay where they
  * are; those at `keep` and behind move, in ascending order, into the slots

@@ -1,5 +1,6 @@
 """Host-side tests of the serving operators' C ABI and Python layer (no GPU needed): include/fa_cache.h and the
 library agree, argument structs match the header, and bad arguments are refused before any CUDA call."""
+import copy
 import ctypes
 import os
 import re
@@ -192,6 +193,14 @@ def test_python_refuses_cpu_tensors_and_bad_pools(fa):
         fa.KVCache(k, k, s[:, :1], s)
     with pytest.raises(ValueError, match="unit stride"):
         fa.KVCache(k.transpose(2, 3), k.transpose(2, 3), s, s)
+
+def test_python_cache_keeps_its_tensors(fa):
+    """Calls use the addresses that the cache was made with: other tensors are refused, not ignored."""
+    cache = fa.KVCache.__new__(fa.KVCache)
+    for name in ("k", "v", "k_scale", "v_scale", "c", "device"):
+        with pytest.raises(AttributeError, match="KVCache"):
+            setattr(cache, name, torch.zeros(1))
+    assert copy.copy(cache) is cache
 
 
 # ----------------------------------------------------------------- the reference itself
