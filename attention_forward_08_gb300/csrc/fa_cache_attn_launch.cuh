@@ -52,7 +52,7 @@ constexpr int kPromptRows = kD <= 128 ? 32 : 16;
 // With weights, the decode kernel keeps its scores, unless a wide table would
 // make them large (they take 4 bytes a row for every token that the table could
 // hold; the keys are then read twice).  16 sequences of up to 4096 tokens, H
-// 32/8, D 128: 32.5 us kept, 46 us read twice.
+// 32/8, D 128: 33.6 us kept, 46 us read twice.
 constexpr long long kMostScores = 256LL << 20;
 inline long long score_bytes(const CacheAttnParams& a) {
   return (long long)a.B * a.c.H * (((long long)a.c.M * a.c.page + 31) / 32) * a.n * a.group * 128;

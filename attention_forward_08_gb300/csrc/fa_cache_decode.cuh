@@ -18,7 +18,9 @@
 // 2^-36 of the largest below, "largest" in units of value, weight * v_scale.
 // So a first token that holds nearly all of a row's weight, with a value near 0,
 // leaves the others' sum right, and an outlier's large v_scale hides other
-// blocks only past that range.  The sums are not rounded to f16.
+// blocks only past that range.  The sums are not rounded to f16.  1 / l, 1 / vs,
+// exponentials, logarithms and the softcap's quotient are the special function
+// unit's, 2^-22 off: a two-thousandth of what f16 weights are.
 //
 // Work.  A producer warp brings tiles of 32 tokens into a ring, with their
 // scales (two, one for K and one for V, where few wide tiles must keep the
@@ -35,11 +37,11 @@
 // 128-byte swizzle, free of conflicts; the matching permutation is applied to
 // Q once, and undone by where O is written.
 //
-// Bound: memory; 2 * D bytes a token and K/V head, read once.  32 sequences of up to 8192 tokens, H 32/8, D 128, e4m3:
-// 66.6 us, 5.4 TB/s; one of 131072: 52.3 us, 5.1 TB/s.  (The loop itself moves
-// 7.5 TB/s; the rest is its start, the join and two launches.)  Tried and
-// slower: loads straight to registers (79.9 us on the first), a cp.async queue
-// a lane (83.7 us), one block of 10 + 2 warps an SM (102 us).
+// Bound: memory; 2 * D bytes a token and K/V head, read once.  32 sequences of
+// up to 8192 tokens, H 32/8, D 128, e4m3: 66.7 us, 5.4 TB/s; one of 131072: 52.7
+// us, 5.1 TB/s; its start, the join and the second launch among them.  Tried and
+// slower: loads straight to registers (79.9 us on the first), a cp.async queue a
+// lane (83.7 us), one block of 10 + 2 warps an SM (102 us).
 #pragma once
 
 #include "fa_cache_line.cuh"

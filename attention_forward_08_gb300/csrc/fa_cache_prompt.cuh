@@ -32,9 +32,9 @@
 // it finds the new one, and does it again where that has grown by more than 2^7.
 //
 // Bound: the softmax warps' chains of dependent instructions, two warps a
-// scheduler, then the tensor cores (59% busy) and shared memory (the widened
+// scheduler, then the tensor cores (58% busy) and shared memory (the widened
 // tiles are written once for 256 rows).  2 x 2048 rows at the end of 16384
-// tokens, H 32/8, D 128, e4m3: 790 us, 1304 TFLOP/s.  Leaving out, in a copy,
+// tokens, H 32/8, D 128, e4m3: 795 us, 1297 TFLOP/s.  Leaving out, in a copy,
 // the exponentials, the maximum or half the MMAs gained 10%, 6% and 4%.
 #pragma once
 

@@ -176,7 +176,8 @@ void fa_set_timeout_cycles(long long cycles);
  * one CTA per SM and each CTA walks a balanced share of the (query block,
  * batch, head) work units.  n > 0 caps the number of CTAs (for example to
  * leave SMs to work on other streams); n <= 0 restores one per SM.  Results
- * do not depend on it.
+ * do not depend on it, but for those of fa_cache_attn (fa_cache.h), which it
+ * caps too and whose sums are cut where its thread blocks' parts end.
  */
 void fa_set_max_ctas(int n);
 
