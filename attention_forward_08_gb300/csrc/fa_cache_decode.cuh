@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   uint64_t* s_empty = s_full + kS;
   float* s_rs = reinterpret_cast<float*>(smem + C::kOffRs);  // [row]: 2^-(scaling of the query row)
   volatile int* s_abort = reinterpret_cast<int*>(smem + C::kOffTmp);
+  volatile int* s_issued = s_abort + 1;  // [producer], where there are two
   float* s_join = reinterpret_cast<float*>(smem + C::kOffJoin);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   if (tid == 0) {
@@ -415,9 +416,19 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           }
         }
       }
-      // After an expired wait the block ends here.
+      // After an expired wait the block ends here.  Of two producers, one may
+      // have stopped at an earlier tile: it arrives for the tiles that only the
+      // other issued (no more than a ring's length), so that both see those land.
+      int end = tile0 + issued;
+      if (C::kProducers == 2 && lane == 0) s_issued[warp - kW] = end;
       if (C::kWide ? __syncthreads_or(!ok) : !ok) {
-        dec_drain<C>(s_full, tile0 + issued);
+        if constexpr (C::kProducers == 2 && C::kTma) {
+          const int other = s_issued[kW + 1 - warp];
+          if (lane == 0)
+            for (int k = end; k < other; ++k) mbar_arrive(s_full + k % kS);
+          end = max(end, other);
+        }
+        dec_drain<C>(s_full, end);
         return;
       }
     } else {

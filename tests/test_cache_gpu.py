@@ -951,3 +951,32 @@ def test_status_tells_of_a_bad_index_behind_a_timeout(fa):
     assert first == fa.fa.FA_ERR_DEVICE_TIMEOUT
     assert fa.fa_sync_status(None) == fa.fa.FA_ERR_INVALID_ARGUMENT and "out of range" in fa.fa_last_error()
     assert fa.fa_sync_status(None) == fa.fa.FA_OK
+
+
+@pytest.mark.parametrize("D,page,n,lens", [(256, 64, 1, [9000, 4000]), (128, 64, 5, [9000, 4000]), (256, 32, 2, [30000])])
+def test_two_producers_unwind_at_once(fa, D, page, n, lens):
+    """Two producers that stop at different tiles: neither waits for copies that the other never issues."""
+    g = torch.Generator().manual_seed(D)
+    table, P, _ = R.make_table(g, lens, page)
+    pools = R.make_pools(g, P, 2, page, D, E4M3)
+    q = torch.randn(len(lens), 8, n, D, generator=g).to(BF16)
+    cache, qd, t, ln = to_gpu(fa, pools), q.to(DEV), i32(table), i32(lens)
+    fa.cache_attention(qd, cache, t, ln)
+    torch.cuda.synchronize()
+    longest, told = 0.0, 0
+    try:
+        for ctas in (0, 1, 8):
+            fa.fa_set_max_ctas(ctas)
+            for cycles in list(range(1, 4000, 100)) * 3:
+                fa.fa_set_timeout_cycles(cycles)
+                begin = time.monotonic()
+                fa.cache_attention(qd, cache, t, ln)
+                told += fa.fa_sync_status(None) == fa.fa.FA_ERR_DEVICE_TIMEOUT
+                longest = max(longest, time.monotonic() - begin)
+    finally:
+        fa.fa_set_timeout_cycles(0)
+        fa.fa_set_max_ctas(0)
+    assert told > 0 and longest < 1.0, f"{told} expired, the longest took {longest:.2f} s"
+    got = fa.cache_attention(qd, cache, t, ln)
+    synced(fa)
+    check_attention(fa, R.Cache(*pools), q, table, lens, got)
