@@ -1,7 +1,8 @@
 """Serving operators over a paged key/value cache held in 8 bits (C ABI: ``include/fa_cache.h``).
 
 ``KVCache`` holds the pools and their scales; ``cache_append`` writes new tokens, ``cache_attention`` attends to the
-cached ones, ``cache_evict`` keeps the heaviest and latest.  Like the dense operators in ``fa``, these functions
+cached ones (a tree of drafted tokens among them), ``cache_evict`` keeps the heaviest and latest; ``verify_drafts``
+decides which drafts stay, and ``cache_accept`` brings those together.  Like the dense operators in ``fa``, these functions
 check device, dtype, shape and strides, allocate what they return (and the scratch) if it is not given, and call the
 C ABI on the current torch stream, or on ``stream`` (a raw cudaStream_t); every step of the computation runs in the
 CUDA library.  Lengths and page tables stay on the device: no call synchronises, and each can be captured into a CUDA
@@ -19,8 +20,9 @@ torch = None  # imported with the first cache: not for those who only build, and
 
 FA_CACHE_E4M3, FA_CACHE_INT8 = 0, 1
 
-CACHE_EXPORTED = ("fa_cache_append", "fa_cache_attn", "fa_cache_attn_workspace_bytes", "fa_cache_evict",
-                  "fa_cache_evict_workspace_bytes")
+CACHE_EXPORTED = ("fa_cache_accept", "fa_cache_append", "fa_cache_attn", "fa_cache_attn_tree",
+                  "fa_cache_attn_tree_workspace_bytes", "fa_cache_attn_workspace_bytes", "fa_cache_evict",
+                  "fa_cache_evict_workspace_bytes", "fa_verify_drafts")
 
 _P, _LL, _I, _F = ctypes.c_void_p, ctypes.c_longlong, ctypes.c_int, ctypes.c_float
 
@@ -47,6 +49,26 @@ class FaCacheAttnArgs(ctypes.Structure):
                 ("softcap", _F), ("dtype", _I), ("workspace", _P), ("workspace_bytes", _LL), ("stream", _P)]
 
 
+class FaCacheAttnTreeArgs(ctypes.Structure):
+    """Layout of ``fa_cache_attn_tree_args`` in include/fa_cache.h."""
+    _fields_ = [("attn", FaCacheAttnArgs), ("tree", _P), ("tree_stride", _LL)]
+
+
+class FaVerifyDraftsArgs(ctypes.Structure):
+    """Layout of ``fa_verify_drafts_args`` in include/fa_cache.h."""
+    _fields_ = [("p", _P), ("q", _P), ("p_strides", _LL * 2), ("q_strides", _LL * 2), ("tokens", _P),
+                ("tokens_stride", _LL), ("tree", _P), ("tree_stride", _LL), ("u", _P), ("u_stride", _LL),
+                ("u_next", _P), ("n_q", _P), ("path", _P), ("count", _P), ("token", _P), ("B", _I), ("n", _I),
+                ("V", _I), ("dtype", _I), ("stream", _P)]
+
+
+class FaCacheAcceptArgs(ctypes.Structure):
+    """Layout of ``fa_cache_accept_args`` in include/fa_cache.h."""
+    _fields_ = [("cache", FaCache), ("table", _P), ("table_stride", _LL), ("lens", _P), ("n_q", _P), ("path", _P),
+                ("path_stride", _LL), ("count", _P), ("weights", _P), ("lens_out", _P), ("B", _I), ("n", _I),
+                ("M", _I), ("W", _I), ("stream", _P)]
+
+
 class FaCacheEvictArgs(ctypes.Structure):
     """Layout of ``fa_cache_evict_args`` in include/fa_cache.h."""
     _fields_ = [("cache", FaCache), ("table", _P), ("table_stride", _LL), ("lens", _P), ("weights", _P),
@@ -63,10 +85,11 @@ def _library():
     if _lib is None:
         lib = _fa.load_library()
         for name, args in (("fa_cache_append", FaCacheAppendArgs), ("fa_cache_attn", FaCacheAttnArgs),
-                           ("fa_cache_evict", FaCacheEvictArgs)):
+                           ("fa_cache_attn_tree", FaCacheAttnTreeArgs), ("fa_verify_drafts", FaVerifyDraftsArgs),
+                           ("fa_cache_accept", FaCacheAcceptArgs), ("fa_cache_evict", FaCacheEvictArgs)):
             getattr(lib, name).argtypes = [ctypes.POINTER(args)]
             getattr(lib, name).restype = ctypes.c_int
-            if name != "fa_cache_append":
+            if name + "_workspace_bytes" in CACHE_EXPORTED:
                 size = getattr(lib, name + "_workspace_bytes")
                 size.argtypes, size.restype = [ctypes.POINTER(args)], ctypes.c_longlong
         _lib = lib
@@ -86,6 +109,23 @@ def fa_cache_attn(args: FaCacheAttnArgs) -> int:
 def fa_cache_attn_workspace_bytes(args: FaCacheAttnArgs) -> int:
     """``fa_cache_attn_workspace_bytes`` of include/fa_cache.h (-1: invalid arguments)."""
     return _library().fa_cache_attn_workspace_bytes(ctypes.byref(args))
+
+
+def fa_cache_attn_tree(args: FaCacheAttnTreeArgs) -> int:
+    return _library().fa_cache_attn_tree(ctypes.byref(args))
+
+
+def fa_cache_attn_tree_workspace_bytes(args: FaCacheAttnTreeArgs) -> int:
+    """``fa_cache_attn_tree_workspace_bytes`` of include/fa_cache.h (-1: invalid arguments)."""
+    return _library().fa_cache_attn_tree_workspace_bytes(ctypes.byref(args))
+
+
+def fa_verify_drafts(args: FaVerifyDraftsArgs) -> int:
+    return _library().fa_verify_drafts(ctypes.byref(args))
+
+
+def fa_cache_accept(args: FaCacheAcceptArgs) -> int:
+    return _library().fa_cache_accept(ctypes.byref(args))
 
 
 def fa_cache_evict(args: FaCacheEvictArgs) -> int:
@@ -181,6 +221,18 @@ def _table(device, name, table, B, width):
     if strides[1] != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have unit stride along its last dimension")
     return table.data_ptr(), strides[0], shape[1]
+
+
+def _tree(device, tree, B, n):
+    """An int32 [B, n] tree, or [n] for all sequences: (pointer, stride between sequences)."""
+    shape = tree.shape
+    if shape != (n,) and shape != (B, n) or tree.dtype is not torch.int32 or tree.device != device:
+        raise ValueError(f"tree must be an int32 [B, n] = [{B}, {n}] or [{n}] tensor on {device} "
+                         f"(got {tree.dtype} {tuple(shape)})")
+    strides = tree.stride()
+    if strides[-1] != 1 and n > 1:
+        raise ValueError("tree must have unit stride along its last dimension")
+    return tree.data_ptr(), strides[0] if len(shape) == 2 else 0
 
 
 def _rows(name, t):
@@ -304,7 +356,7 @@ def cache_append(cache, k, v, table, lens, *, n_new=None, weights=None, position
 
 
 def cache_attention(q, cache, table, lens, *, n_q=None, scale=None, causal=True, window=0, softcap=0.0, weights=None,
-                    out=None, lse=None, workspace=None, stream=None):
+                    out=None, lse=None, workspace=None, stream=None, tree=None):
     """O and L of the query rows q [B, H_q, n, D] (bf16 or fp16, unit inner stride) over the cached tokens; returns
     (o, lse).
 
@@ -314,8 +366,11 @@ def cache_attention(q, cache, table, lens, *, n_q=None, scale=None, causal=True,
     scale (1 / sqrt(D)), causal, window, softcap: as in ``attention``, the causal diagonal at the rows' positions.
     weights: fp32 [B, H_kv, W], W >= every length: the attention weight that each cached token got, summed over rows
     and the heads of its group, is added.
-    workspace: optional device tensor of at least ``fa_cache_attn_workspace_bytes`` bytes, 256-byte aligned
-    (allocated here if None).
+    tree: int32 [B, n] (or [n], one tree for all sequences): the rows are drafts, row i behind row tree[b, i] < i, or
+    behind the last token before the drafts if that is -1.  A draft sees the tokens before the drafts, itself and the
+    drafts above it; its position, for the window, is that of a sequence that ends with it.  At most 1024 rows.
+    workspace: optional device tensor of at least ``fa_cache_attn_workspace_bytes`` (with a tree,
+    ``fa_cache_attn_tree_workspace_bytes``) bytes, 256-byte aligned (allocated here if None).
     """
     shape, device, c = q.shape, cache.device, cache.c
     if len(shape) != 4 or shape[3] != c.D:
@@ -337,6 +392,10 @@ def cache_attention(q, cache, table, lens, *, n_q=None, scale=None, causal=True,
         raise ValueError(f"out must be {q.dtype} {tuple(shape)} on {device}")
     if lse is not None:
         _on(device, "lse", lse, torch.float32, (B, Hq, n))
+    if tree is not None:
+        if not causal:
+            raise ValueError("a tree's rows see no row behind them: causal must be True")
+        nodes = _tree(device, tree, B, n)  # (beside `tree`, which has to live until the call is queued)
 
     def work(raw):
         o, os = out, None
@@ -350,7 +409,12 @@ def cache_attention(q, cache, table, lens, *, n_q=None, scale=None, causal=True,
             a = FaCacheAttnArgs(c, q.data_ptr(), o.data_ptr(), l.data_ptr(), w_ptr, qs, os or _rows("out", o), t_ptr, t_stride,
                                 l_ptr, n_ptr, B, Hq, n, M, W, 1.0 / math.sqrt(D) if scale is None else scale,
                                 bool(causal), window, softcap, dtype, None, 0, raw)
-            _with_scratch(a, fa_cache_attn_workspace_bytes(a), workspace, device, fa_cache_attn)
+            if tree is None:
+                _with_scratch(a, fa_cache_attn_workspace_bytes(a), workspace, device, fa_cache_attn)
+            else:
+                t = FaCacheAttnTreeArgs(a, *nodes)
+                _with_scratch(t.attn, fa_cache_attn_tree_workspace_bytes(t), workspace, device,
+                              lambda _: fa_cache_attn_tree(t))
         return o, l
 
     return _call(device, stream, work)
@@ -391,5 +455,99 @@ def cache_evict(cache, table, lens, weights, positions=None, *, keep, recent=0, 
                                  B, M, W, M_into, W_out, keep, recent, None, 0, raw)
             _with_scratch(a, fa_cache_evict_workspace_bytes(a), workspace, device, fa_cache_evict)
         return n
+
+    return _call(device, stream, work)
+
+
+def _nodes(device, name, t, dtype, B, n):
+    """A [B, n] argument, unit inner stride: (pointer, row stride)."""
+    if t.dtype is not dtype or t.shape != (B, n) or t.device != device:
+        raise ValueError(f"{name} must be {dtype} [B, n] = [{B}, {n}] on {device} (got {t.dtype} {tuple(t.shape)})")
+    strides = t.stride()
+    if strides[1] != 1 and n > 1:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    return t.data_ptr(), strides[0]
+
+
+def verify_drafts(p, tokens, tree, u, u_next, *, p_draft=None, n_q=None, stream=None):
+    """Which drafts of a tree stay, and the token behind them: so that both are distributed as the target's
+    probabilities p [B, n, V] (bf16, fp16 or fp32, unit inner stride) say.  Returns (path, count, token), int32 [B, n],
+    [B] and [B].
+
+    Node 0 of each sequence is its last token, which stays; node i is a draft of ``tokens[b, i]`` behind node
+    ``tree[b, i]`` (int32 [B, n] each; a tree [n] serves all), and p[b, i] are the target's probabilities behind it.
+    p_draft: [B, n, V] like p: row i the probabilities that node i's children were drawn from, independently; None if
+    the children of a node are distinct candidates that were not drawn (the most likely tokens, say).
+    u, u_next: fp32 [B, n] and [B], uniform random numbers in [0, 1).
+    n_q: int32 [B], the nodes of each sequence (all n if None).
+
+    From node 0 the path goes on to the first child that is accepted, one with probability p / p_draft (at most 1), the
+    next ones against what the rejected ones left of p, until no child is; ``token`` is drawn from what is left there.
+    path[b]: the path's nodes, ascending from 0, then -1; count[b]: how many.  A one-hot p keeps the drafts that are
+    its tokens.
+    """
+    if torch is None:
+        _import_torch()
+    shape, device = p.shape, p.device
+    if len(shape) != 3 or not p.is_cuda:
+        raise ValueError(f"p must be a 3-D CUDA tensor [B, n, V] (got {tuple(shape)} on {device})")
+    B, n, V = shape
+    dtype = _dtype(p, "p")
+    for name, t in (("p", p), ("p_draft", p_draft)):
+        if t is not None and V > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name} must have unit stride along its last dimension")
+    if p_draft is not None and (p_draft.shape != shape or p_draft.dtype is not p.dtype or p_draft.device != device):
+        raise ValueError(f"p_draft must be {p.dtype} {tuple(shape)} on {device}")
+    k_ptr, k_stride = _nodes(device, "tokens", tokens, torch.int32, B, n)
+    t_ptr, t_stride = _tree(device, tree, B, n)
+    u_ptr, u_stride = _nodes(device, "u", u, torch.float32, B, n)
+    x_ptr = _on(device, "u_next", u_next, torch.float32, (B,))
+    n_ptr = None if n_q is None else _on(device, "n_q", n_q, torch.int32, (B,))
+    if n == 0 or V == 0:
+        raise ValueError("n and V must be > 0")
+
+    def work(raw):
+        path, count, token = (torch.empty(s, dtype=torch.int32, device=device) for s in ((B, n), (B,), (B,)))
+        if B:
+            _fa._check(fa_verify_drafts(FaVerifyDraftsArgs(
+                p.data_ptr(), None if p_draft is None else p_draft.data_ptr(), p.stride()[:2],
+                (0, 0) if p_draft is None else p_draft.stride()[:2], k_ptr, k_stride, t_ptr, t_stride, u_ptr, u_stride,
+                x_ptr, n_ptr, path.data_ptr(), count.data_ptr(), token.data_ptr(), B, n, V, dtype, raw)))
+        return path, count, token
+
+    return _call(device, stream, work)
+
+
+def cache_accept(cache, table, lens, path, count, *, n_q=None, weights=None, lens_out=None, stream=None):
+    """Of the drafts that end each sequence's ``lens`` (int32 [B]) tokens, those of a path become its next tokens, the
+    others are dropped.  Returns the new lengths, int32 [B].
+
+    path, count: int32 [B, n] and [B] as ``verify_drafts`` gives them: the rows that stay, ascending, and how many.
+    n_q: int32 [B], the drafts of each sequence (all n if None).
+    weights: fp32 [B, H_kv, W], moved along; positions need no change.
+    lens_out: where the new lengths go (may be ``lens``); allocated here if None.  With caches of several layers,
+    each call is given the lengths that the drafts are counted in.
+    """
+    device, c, B = cache.device, cache.c, table.shape[0]
+    t_ptr, t_stride, M = _table(device, "table", table, B, "M")
+    l_ptr = _on(device, "lens", lens, torch.int32, (B,))
+    if path.dim() != 2:
+        raise ValueError(f"path must be [B, n] (got {tuple(path.shape)})")
+    n = path.shape[1]
+    p_ptr, p_stride = _nodes(device, "path", path, torch.int32, B, n)
+    k_ptr = _on(device, "count", count, torch.int32, (B,))
+    n_ptr = None if n_q is None else _on(device, "n_q", n_q, torch.int32, (B,))
+    w_ptr, _, W = (None, None, 0) if weights is None else _trackers(device, c.H_kv, weights, None, B)
+    if n == 0:
+        raise ValueError("path must hold at least one row")
+    if lens_out is not None:
+        _on(device, "lens_out", lens_out, torch.int32, (B,))
+
+    def work(raw):
+        out = torch.empty(B, dtype=torch.int32, device=device) if lens_out is None else lens_out
+        if B:
+            _fa._check(fa_cache_accept(FaCacheAcceptArgs(c, t_ptr, t_stride, l_ptr, n_ptr, p_ptr, p_stride, k_ptr,
+                                                         w_ptr, out.data_ptr(), B, n, M, W, raw)))
+        return out
 
     return _call(device, stream, work)

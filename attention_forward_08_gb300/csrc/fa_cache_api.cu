@@ -14,6 +14,7 @@ namespace fa {
 namespace {
 
 constexpr long long kIntMax = 0x7fffffffLL;
+constexpr int kMostVocabulary = 1 << 20;
 
 bool aligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 long long align256(long long bytes) { return (bytes + 255) / 256 * 256; }
@@ -213,6 +214,8 @@ CacheAttnParams attn_params(const fa_cache_attn_args* a, unsigned int* status, l
   for (int i = 0; i < 3; ++i) p.qs[i] = a->q_strides[i], p.os[i] = a->o_strides[i];
   p.lens = a->lens;
   p.n_q = a->n_q;
+  p.tree = nullptr;
+  p.tree_stride = 0;
   p.B = a->B;
   p.Hq = a->H_q;
   p.group = a->H_q / a->cache.H_kv;
@@ -226,6 +229,93 @@ CacheAttnParams attn_params(const fa_cache_attn_args* a, unsigned int* status, l
   p.timeout_cycles = timeout;
   p.ws = static_cast<uint8_t*>(a->workspace);
   return p;
+}
+
+CacheAttnParams tree_params(const fa_cache_attn_tree_args* a, unsigned int* status, long long timeout) {
+  CacheAttnParams p = attn_params(&a->attn, status, timeout);
+  p.tree = a->tree;
+  p.tree_stride = a->tree_stride;
+  return p;
+}
+
+int check_tree(const int* tree, long long stride, int B, int n) {
+  if (!tree) return invalid("tree must be non-NULL");
+  if (n > kMostDrafts) {
+    set_error("a tree of %d drafts is not supported (at most %d)", n, kMostDrafts);
+    return FA_ERR_UNSUPPORTED;
+  }
+  if (stride != 0 && stride < n && B > 1) {
+    set_error("the tree's row stride (%lld) is neither 0 (one tree for all) nor at least n (%d)", stride, n);
+    return FA_ERR_INVALID_ARGUMENT;
+  }
+  if (!aligned(tree, 4)) {
+    set_error("tree must be 4-byte aligned");
+    return FA_ERR_MISALIGNED;
+  }
+  return FA_OK;
+}
+
+int check_attn_tree(const fa_cache_attn_tree_args* a) {
+  if (!a) return invalid("args is NULL");
+  int rc = check_attn(&a->attn);
+  if (rc == FA_OK) rc = check_tree(a->tree, a->tree_stride, a->attn.B, a->attn.n);
+  if (rc == FA_OK && !a->attn.causal) return invalid("a tree's rows see no row behind them: causal must be set");
+  return rc;
+}
+
+int check_accept(const fa_cache_accept_args* a) {
+  if (!a) return invalid("args is NULL");
+  int rc = check_cache(a->cache);
+  if (rc == FA_OK) rc = check_table(a->table, a->table_stride, a->lens, a->B, a->M, a->cache.page);
+  if (rc != FA_OK) return rc;
+  if (!a->path || !a->count || !a->lens_out) return invalid("path, count and lens_out must be non-NULL");
+  if (a->n <= 0) {
+    set_error("n (%d) must be > 0", a->n);
+    return FA_ERR_INVALID_ARGUMENT;
+  }
+  if (a->n > kMostDrafts) {
+    set_error("%d drafts are not supported (at most %d)", a->n, kMostDrafts);
+    return FA_ERR_UNSUPPORTED;
+  }
+  if (a->path_stride < a->n && a->B > 1) return invalid("path's row stride is smaller than n");
+  if (a->weights && a->W <= 0) return invalid("W must be > 0 with weights");
+  if (!aligned(a->path, 4) || !aligned(a->count, 4) || !aligned(a->lens_out, 4) || !aligned(a->weights, 4) ||
+      !aligned(a->n_q, 4)) {
+    set_error("path, count, n_q, weights and lens_out must be 4-byte aligned");
+    return FA_ERR_MISALIGNED;
+  }
+  return FA_OK;
+}
+
+int check_verify(const fa_verify_drafts_args* a) {
+  if (!a) return invalid("args is NULL");
+  if (!a->p || !a->tokens || !a->u || !a->u_next) return invalid("p, tokens, u and u_next must be non-NULL");
+  if (!a->path || !a->count || !a->token) return invalid("path, count and token must be non-NULL");
+  if (a->B <= 0 || a->n <= 0 || a->V <= 0) {
+    set_error("B (%d), n (%d) and V (%d) must be > 0", a->B, a->n, a->V);
+    return FA_ERR_INVALID_ARGUMENT;
+  }
+  if (a->dtype != FA_DTYPE_F32 && a->dtype != FA_DTYPE_BF16 && a->dtype != FA_DTYPE_F16) {
+    set_error("dtype %d is not FA_DTYPE_F32 (0), FA_DTYPE_BF16 (1) or FA_DTYPE_F16 (2)", a->dtype);
+    return FA_ERR_INVALID_ARGUMENT;
+  }
+  if (a->B > 65535 || a->V > kMostVocabulary) {
+    set_error("B (%d) must be at most 65535 and V (%d) at most %d", a->B, a->V, kMostVocabulary);
+    return FA_ERR_UNSUPPORTED;
+  }
+  const int rc = check_tree(a->tree, a->tree_stride, a->B, a->n);
+  if (rc != FA_OK) return rc;
+  const unsigned esz = a->dtype == FA_DTYPE_F32 ? 4 : 2;
+  if (!aligned(a->p, esz) || !aligned(a->q, esz)) {
+    set_error("p and q must be aligned to their elements");
+    return FA_ERR_MISALIGNED;
+  }
+  if (!aligned(a->tokens, 4) || !aligned(a->u, 4) || !aligned(a->u_next, 4) || !aligned(a->n_q, 4) ||
+      !aligned(a->path, 4) || !aligned(a->count, 4) || !aligned(a->token, 4)) {
+    set_error("tokens, u, u_next, n_q, path, count and token must be 4-byte aligned");
+    return FA_ERR_MISALIGNED;
+  }
+  return FA_OK;
 }
 
 long long attn_workspace(const CacheAttnParams& p, int num_sms) {
@@ -322,6 +412,88 @@ int fa_cache_attn(const fa_cache_attn_args* a) {
   return p.c.D == 64    ? launch_cache_attn_d64(p, a->cache.kind, f16, ctx)
          : p.c.D == 128 ? launch_cache_attn_d128(p, a->cache.kind, f16, ctx)
                         : launch_cache_attn_d256(p, a->cache.kind, f16, ctx);
+}
+
+int fa_cache_attn_tree(const fa_cache_attn_tree_args* a) {
+  using namespace fa;
+  clear_error();
+  int rc = check_attn_tree(a);
+  if (rc != FA_OK) return rc;
+  DeviceInfo dev;
+  rc = current_device(&dev);
+  if (rc != FA_OK) return rc;
+  const CacheAttnParams p = tree_params(a, dev.status, dev.timeout_cycles);
+  rc = check_workspace(a->attn.workspace, a->attn.workspace_bytes, attn_workspace(p, dev.num_sms),
+                       "fa_cache_attn_tree_workspace_bytes");
+  if (rc != FA_OK) return rc;
+  const LaunchCtx ctx = {static_cast<cudaStream_t>(a->attn.stream), dev.num_sms, dev.dev, dev.max_ctas};
+  const int kind = a->attn.cache.kind;
+  const bool f16 = a->attn.dtype == FA_DTYPE_F16;
+  return p.c.D == 64    ? launch_cache_tree_d64(p, kind, f16, ctx)
+         : p.c.D == 128 ? launch_cache_tree_d128(p, kind, f16, ctx)
+                        : launch_cache_tree_d256(p, kind, f16, ctx);
+}
+
+long long fa_cache_attn_tree_workspace_bytes(const fa_cache_attn_tree_args* a) {
+  using namespace fa;
+  clear_error();
+  if (check_attn_tree(a) != FA_OK) return -1;
+  DeviceInfo dev;
+  if (current_device(&dev) != FA_OK) return -1;
+  return attn_workspace(tree_params(a, dev.status, dev.timeout_cycles), dev.num_sms);
+}
+
+int fa_verify_drafts(const fa_verify_drafts_args* a) {
+  using namespace fa;
+  clear_error();
+  int rc = check_verify(a);
+  if (rc != FA_OK) return rc;
+  DeviceInfo dev;
+  rc = current_device(&dev);
+  if (rc != FA_OK) return rc;
+  VerifyParams p = {};
+  p.p = a->p;
+  p.q = a->q;
+  for (int i = 0; i < 2; ++i) p.ps[i] = a->p_strides[i], p.qs[i] = a->q_strides[i];
+  p.tokens = a->tokens;
+  p.tokens_stride = a->tokens_stride;
+  p.tree = a->tree;
+  p.tree_stride = a->tree_stride;
+  p.u = a->u;
+  p.u_stride = a->u_stride;
+  p.u_next = a->u_next;
+  p.n_q = a->n_q;
+  p.path = a->path;
+  p.count = a->count;
+  p.token = a->token;
+  p.B = a->B;
+  p.n = a->n;
+  p.V = a->V;
+  p.status = dev.status;
+  return launch_verify(p, a->dtype, {static_cast<cudaStream_t>(a->stream), dev.num_sms, dev.dev, dev.max_ctas});
+}
+
+int fa_cache_accept(const fa_cache_accept_args* a) {
+  using namespace fa;
+  clear_error();
+  int rc = check_accept(a);
+  if (rc != FA_OK) return rc;
+  DeviceInfo dev;
+  rc = current_device(&dev);
+  if (rc != FA_OK) return rc;
+  AcceptParams p;
+  p.c = view_of(a->cache, a->table, a->table_stride, a->M, dev.status);
+  p.lens = a->lens;
+  p.n_q = a->n_q;
+  p.path = a->path;
+  p.path_stride = a->path_stride;
+  p.count = a->count;
+  p.weights = a->weights;
+  p.lens_out = a->lens_out;
+  p.B = a->B;
+  p.n = a->n;
+  p.W = a->W;
+  return launch_cache_accept(p, a->cache.kind, {static_cast<cudaStream_t>(a->stream), dev.num_sms, dev.dev, dev.max_ctas});
 }
 
 long long fa_cache_attn_workspace_bytes(const fa_cache_attn_args* a) {

@@ -3,7 +3,7 @@
 
 namespace fa {
 int launch_cache_attn_d64(const CacheAttnParams& a, int kind, bool f16, const LaunchCtx& ctx) {
-  return launch_attn_d<64>(a, kind, f16, ctx);
+  return launch_attn_d<64, false>(a, kind, f16, ctx);
 }
 long long cache_attn_workspace_d64(const CacheAttnParams& a, int num_sms) { return attn_workspace_d<64>(a, num_sms); }
 }  // namespace fa

@@ -71,7 +71,7 @@ long long weights_workspace(const CacheAttnParams& a) {
   const long long groups = (long long)a.B * a.c.H * ((a.n * (long long)a.group + 15) / 16);
   return groups * 16 * (kD * 2 + 8);
 }
-template <int kD>
+template <int kD, bool kTree>
 int launch_weights(const CacheAttnParams& a, int kind, bool f16, long long used, const LaunchCtx& ctx) {
   WeightParams p;
   p.a = a;
@@ -85,8 +85,8 @@ int launch_weights(const CacheAttnParams& a, int kind, bool f16, long long used,
   if (e == cudaSuccess) {
     const long long tokens = (long long)a.c.M * a.c.page;
     const dim3 by_tile((unsigned)((tokens + 127) / 128), (unsigned)a.c.H, (unsigned)a.B);
-    e = kind == FA_CACHE_E4M3 ? launch_after(cache_weights_kernel<kKindE4m3, kD>, by_tile, 128, ctx.stream, p)
-                              : launch_after(cache_weights_kernel<kKindInt8, kD>, by_tile, 128, ctx.stream, p);
+    e = kind == FA_CACHE_E4M3 ? launch_after(cache_weights_kernel<kKindE4m3, kD, kTree>, by_tile, 128, ctx.stream, p)
+                              : launch_after(cache_weights_kernel<kKindInt8, kD, kTree>, by_tile, 128, ctx.stream, p);
   }
   if (e != cudaSuccess) {
     set_error("cache weights launch failed: %s", cudaGetErrorString(e));
@@ -184,37 +184,38 @@ long long plan_workspace(const CacheAttnParams& a, int num_sms) {
 // TMA where a box holds 4 KB and more.  (Blocks of 16 tokens of D 64, int8, 75 MB
 // of cache: 36.1 us with boxes of 1 KB, 32.3 with cp.async.  Blocks of 64 of D 128,
 // 361 MB: 67.6 us with boxes of 4 KB, 83.7 with cp.async.)
-template <int kD, int kKind, bool kF16, int kMT>
+template <int kD, int kKind, bool kF16, int kMT, bool kTree>
 int launch_decode_by(const CacheAttnParams& a, const LaunchCtx& ctx) {
   if constexpr (kD >= 128) {
-    if (a.c.page >= 32) return launch_decode<DecCfg<kKind, kF16, kD, kMT, true>>(a, ctx);
+    if (a.c.page >= 32) return launch_decode<DecCfg<kKind, kF16, kD, kMT, true, kTree>>(a, ctx);
   }
-  return launch_decode<DecCfg<kKind, kF16, kD, kMT, false>>(a, ctx);
+  return launch_decode<DecCfg<kKind, kF16, kD, kMT, false, kTree>>(a, ctx);
 }
 
-template <int kD, int kKind, bool kF16>
+template <int kD, int kKind, bool kF16, bool kTree>
 int launch_plan(const CacheAttnParams& a, const LaunchCtx& ctx) {
   switch (attn_plan<kD>(a)) {
     case AttnPlan::kPrompt:
       if (a.cap_out == 0.0f && a.scale_log2 > 0.0f)
-        return a.c.page >= 64 ? launch_prompt<PromptCfg<kKind, kF16, kD, 64, true>>(a, ctx)
-                              : launch_prompt<PromptCfg<kKind, kF16, kD, 16, true>>(a, ctx);
-      return launch_prompt<PromptCfg<kKind, kF16, kD, 16, false>>(a, ctx);
+        return a.c.page >= 64 ? launch_prompt<PromptCfg<kKind, kF16, kD, 64, true, kTree>>(a, ctx)
+                              : launch_prompt<PromptCfg<kKind, kF16, kD, 16, true, kTree>>(a, ctx);
+      return launch_prompt<PromptCfg<kKind, kF16, kD, 16, false, kTree>>(a, ctx);
     case AttnPlan::kRows32:
-      if constexpr (kD <= 128) return launch_decode_by<kD, kKind, kF16, 2>(a, ctx);
-    default: return launch_decode_by<kD, kKind, kF16, 1>(a, ctx);
+      if constexpr (kD <= 128) return launch_decode_by<kD, kKind, kF16, 2, kTree>(a, ctx);
+    default: return launch_decode_by<kD, kKind, kF16, 1, kTree>(a, ctx);
   }
 }
 
-template <int kD>
+// kTree: a.tree is there.
+template <int kD, bool kTree>
 int launch_attn_d(const CacheAttnParams& a, int kind, bool f16, const LaunchCtx& ctx) {
   int rc;
   if (kind == FA_CACHE_E4M3)
-    rc = f16 ? launch_plan<kD, kKindE4m3, true>(a, ctx) : launch_plan<kD, kKindE4m3, false>(a, ctx);
+    rc = f16 ? launch_plan<kD, kKindE4m3, true, kTree>(a, ctx) : launch_plan<kD, kKindE4m3, false, kTree>(a, ctx);
   else
-    rc = f16 ? launch_plan<kD, kKindInt8, true>(a, ctx) : launch_plan<kD, kKindInt8, false>(a, ctx);
+    rc = f16 ? launch_plan<kD, kKindInt8, true, kTree>(a, ctx) : launch_plan<kD, kKindInt8, false, kTree>(a, ctx);
   if (rc != FA_OK || !a.weights || keep_scores<kD>(a)) return rc;
-  return launch_weights<kD>(a, kind, f16, plan_workspace<kD>(a, ctx.num_sms), ctx);
+  return launch_weights<kD, kTree>(a, kind, f16, plan_workspace<kD>(a, ctx.num_sms), ctx);
 }
 
 template <int kD>

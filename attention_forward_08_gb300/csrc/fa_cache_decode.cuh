@@ -45,11 +45,14 @@
 #pragma once
 
 #include "fa_cache_line.cuh"
+#include "fa_cache_tree.cuh"
 
 namespace fa {
 
-template <int kKind_, bool kF16_, int kD_, int kMT_, bool kTma_>
+// kTree_: the rows are the drafts of a tree (fa_cache_tree.cuh).
+template <int kKind_, bool kF16_, int kD_, int kMT_, bool kTma_, bool kTree_ = false>
 struct DecCfg {
+  static constexpr bool kTree = kTree_;
   static constexpr bool kTma = kTma_;
   static constexpr int kKind = kKind_;
   static constexpr bool kF16 = kF16_;  // type of q and o
@@ -475,6 +478,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       float m[C::kMT][2], l[C::kMT][2], rs[C::kMT][2];  // m: the reference
       int hi_row[C::kMT][2], lo_row[C::kMT][2];  // the tokens that this lane's two rows see
       int lo_all = 0, hi_all = 0x7fffffff;       // ... that every row of the warp sees
+      uint32_t drafts[C::kTree ? C::kMT : 1][2];  // of a tree: the drafts that they see, beside those tokens
+      const int base = seq.len - seq.nq;
+      uint32_t line = 0;  // of lane i: node i and the nodes above it
+      if constexpr (C::kTree) line = tree_lines(a, b, seq.nq);
 #pragma unroll
       for (int mt = 0; mt < C::kMT; ++mt) {
 #pragma unroll
@@ -487,7 +494,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           rs[mt][x] = s_rs[row];
           const int i = row / a.group;
           const bool real = row < p.rows && i < seq.nq;
-          const int2 v = real ? dec_span(a, seq, i, i) : make_int2(0, 0x7fffffff);
+          int2 v = make_int2(0, 0x7fffffff);
+          if constexpr (C::kTree) {
+            drafts[mt][x] = __shfl_sync(0xFFFFFFFFu, line, i & 31);
+            if (real) v = make_int2(tree_window(a, base, drafts[mt][x]), base);
+            else drafts[mt][x] = 0u;
+          } else if (real) {
+            v = dec_span(a, seq, i, i);
+          }
           // a row of the tile that is no query row may see anything: nothing of it is written
           lo_row[mt][x] = v.x;
           hi_row[mt][x] = row < p.rows && !real ? 0 : v.y;
@@ -574,8 +588,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const int tok = tok0 + j * 8 + 2 * t + (e & 1), x = e >> 1;
-                if (tok < lo_row[mt][x] || tok >= hi_row[mt][x] || (j < 2 ? rv.x : rv.y) < 0.0f)
-                  sc[mt][j][e] = -INFINITY;
+                bool hidden = tok < lo_row[mt][x] || tok >= hi_row[mt][x];
+                if constexpr (C::kTree) hidden = hidden && !tree_bit(drafts[mt][x], tok - base);
+                if (hidden || (j < 2 ? rv.x : rv.y) < 0.0f) sc[mt][j][e] = -INFINITY;
               }
           }
 #pragma unroll

@@ -30,6 +30,7 @@
 #include "fa_cache.h"
 #include "fa_cache_launch.cuh"
 #include "fa_cache_ops.cuh"
+#include "fa_cache_rescale.cuh"
 #include "fa_device.h"
 
 namespace fa {
@@ -47,21 +48,6 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 constexpr int kFewMoves = 1024;  // in place: lists in shared memory, else in the workspace
 // Tokens whose keys fit shared memory (184 KB).
 constexpr int kCachedKeys = 47104;
-
-// Sixteen stored bytes of scale `from`, rounded to scale `to`.
-template <int kKind>
-__device__ __forceinline__ uint4 rescale16(uint4 w, float from, float to) {
-  if (from == to) return w;
-  const float ratio = __fdiv_rn(from, to);
-  uint32_t* u = &w.x;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float f[4];
-    load8x4<kKind>(u[i], f);
-    u[i] = round8x4<kKind>(__fmul_rn(f[0], ratio), __fmul_rn(f[1], ratio), __fmul_rn(f[2], ratio), __fmul_rn(f[3], ratio));
-  }
-  return w;
-}
 
 constexpr int kClasses = 2048, kFewKeys = 256;
 

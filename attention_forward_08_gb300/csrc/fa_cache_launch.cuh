@@ -25,10 +25,12 @@ bool allow_smem(K kern, int bytes, int dev, std::atomic<unsigned long long>& con
 // Programmatic launch: the blocks come up while the kernel before ends, and
 // wait for it (griddepcontrol.wait) before they read what it wrote.
 template <class... P>
-cudaError_t launch_after(void (*kern)(P...), dim3 grid, unsigned threads, cudaStream_t stream, const P&... p) {
+cudaError_t launch_after_with(size_t smem, void (*kern)(P...), dim3 grid, unsigned threads, cudaStream_t stream,
+                              const P&... p) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -36,6 +38,10 @@ cudaError_t launch_after(void (*kern)(P...), dim3 grid, unsigned threads, cudaSt
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, p...);
+}
+template <class... P>
+cudaError_t launch_after(void (*kern)(P...), dim3 grid, unsigned threads, cudaStream_t stream, const P&... p) {
+  return launch_after_with(0, kern, grid, threads, stream, p...);
 }
 
 }  // namespace fa

@@ -56,11 +56,14 @@ __device__ __forceinline__ DecSeq dec_seq(const CacheAttnParams& a, int b) {
   return s;
 }
 
-// Tokens that query rows i0 .. i1 see: [lo, hi), empty as {0, 0}.
+// Tokens that query rows i0 .. i1 see: [lo, hi), empty as {0, 0}.  (Of a tree's:
+// what they see lies in there; a node stands no later than its row, and no
+// earlier than the first.)
+template <bool kTree = false>
 __device__ __forceinline__ int2 dec_span(const CacheAttnParams& a, const DecSeq& s, int i0, int i1) {
   i1 = min(i1, s.nq - 1);
   if (i0 > i1) return make_int2(0, 0);
-  const int p0 = s.len - s.nq + i0, p1 = s.len - s.nq + i1;
+  const int p0 = s.len - s.nq + (kTree ? 0 : i0), p1 = s.len - s.nq + i1;
   const int hi = a.causal ? min(s.len, p1 + 1) : s.len;
   // (Where a call has more rows than tokens, the first stand before token 0: as
   // far as the window's begin goes, at 0, so that no window leaves 32 bits.)
@@ -70,8 +73,8 @@ __device__ __forceinline__ int2 dec_span(const CacheAttnParams& a, const DecSeq&
 // ... and the query rows of row group rg.
 template <class C>
 __device__ __forceinline__ int2 dec_group_span(const DecParams& p, const DecSeq& s, int rg) {
-  if (p.row_groups == 1) return dec_span(p.a, s, 0, p.a.n - 1);
-  return dec_span(p.a, s, rg * C::kRows / p.a.group, (min(p.rows, (rg + 1) * C::kRows) - 1) / p.a.group);
+  if (p.row_groups == 1) return dec_span<C::kTree>(p.a, s, 0, p.a.n - 1);
+  return dec_span<C::kTree>(p.a, s, rg * C::kRows / p.a.group, (min(p.rows, (rg + 1) * C::kRows) - 1) / p.a.group);
 }
 
 // Tiles of one segment: at least one, so that empty rows are written too.

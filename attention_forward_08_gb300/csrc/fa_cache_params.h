@@ -42,6 +42,8 @@ struct CacheAttnParams {
   float* weights;
   long long qs[3], os[3];  // element strides: batch, head, row
   const int *lens, *n_q;
+  const int* tree;         // [B, n], row stride tree_stride: the rows' parents; NULL: each row follows the one before
+  long long tree_stride;
   int B, Hq, group, n, W;
   int causal, window;
   float scale_log2;             // scale * log2(e)
@@ -68,6 +70,33 @@ struct EvictParams {
   int* count;       // [B, H]: tokens kept
 };
 
+constexpr int kMostDrafts = 1024;  // nodes of a sequence's tree
+
+struct AcceptParams {
+  CacheView c;
+  const int *lens, *n_q;
+  const int* path;  // [B, n], row stride path_stride
+  long long path_stride;
+  const int* count;
+  float* weights;
+  int* lens_out;
+  int B, n, W;
+};
+
+struct VerifyParams {
+  const void *p, *q;              // probabilities; q may be NULL
+  long long ps[2], qs[2];         // element strides: batch, row
+  const int *tokens, *tree;
+  long long tokens_stride, tree_stride;
+  const float *u, *u_next;
+  long long u_stride;
+  const int* n_q;
+  int *path, *count, *token;      // path [B, n] contiguous
+  int B, n, V;
+  int seg;                        // vocabulary entries a warp takes (set by the launch)
+  unsigned int* status;
+};
+
 struct LaunchCtx {
   cudaStream_t stream;
   int num_sms;
@@ -80,9 +109,14 @@ int launch_cache_append(const AppendParams& p, int kind, int dtype, const Launch
 int launch_cache_attn_d64(const CacheAttnParams& p, int kind, bool f16, const LaunchCtx& ctx);
 int launch_cache_attn_d128(const CacheAttnParams& p, int kind, bool f16, const LaunchCtx& ctx);
 int launch_cache_attn_d256(const CacheAttnParams& p, int kind, bool f16, const LaunchCtx& ctx);
+int launch_cache_tree_d64(const CacheAttnParams& p, int kind, bool f16, const LaunchCtx& ctx);  // (fa_cache_tree_d*.cu)
+int launch_cache_tree_d128(const CacheAttnParams& p, int kind, bool f16, const LaunchCtx& ctx);
+int launch_cache_tree_d256(const CacheAttnParams& p, int kind, bool f16, const LaunchCtx& ctx);
 long long cache_attn_workspace_d64(const CacheAttnParams& p, int num_sms);
 long long cache_attn_workspace_d128(const CacheAttnParams& p, int num_sms);
 long long cache_attn_workspace_d256(const CacheAttnParams& p, int num_sms);
 int launch_cache_evict(const EvictParams& p, int kind, const LaunchCtx& ctx);
+int launch_cache_accept(const AcceptParams& p, int kind, const LaunchCtx& ctx);
+int launch_verify(VerifyParams p, int dtype, const LaunchCtx& ctx);
 
 }  // namespace fa

@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(256) cache_rows_kernel(const __grid_constant__
   }
 }
 
-template <int kKind, int kD>
+template <int kKind, int kD, bool kTree>
 __global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constant__ WeightParams p) {
   const CacheAttnParams& a = p.a;
   const CacheView& c = a.c;
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constan
   int i0 = 0, i1 = seq.nq - 1;
   const int pos0 = seq.len - seq.nq;
   if (a.causal) i0 = max(0, tok0 - pos0);
-  if (a.window > 0) i1 = (int)min((long long)i1, (long long)tok0 + 31 + a.window - 1 - pos0);
+  if (!kTree && a.window > 0) i1 = (int)min((long long)i1, (long long)tok0 + 31 + a.window - 1 - pos0);
   const bool none = tok0 >= seq.len || i0 > i1;
   const int rg0 = i0 * a.group / 16, rg1 = (i1 * a.group + a.group - 1) / 16;
 
@@ -133,7 +133,13 @@ __global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constan
     const float2 r0 = __ldcg(row + rg * 16 + g), r1 = __ldcg(row + rg * 16 + g + 8);
     const int ia = (rg * 16 + g) / a.group, ib = (rg * 16 + g + 8) / a.group;
     // tokens that rows g and g + 8 see (a row that is none has L2 = +inf)
-    const int2 va = dec_span(a, seq, ia, ia), vb = dec_span(a, seq, ib, ib);
+    int2 va = make_int2(0, 0), vb = va;
+    if constexpr (kTree) {  // (of a tree's, those before the drafts)
+      if (ia < seq.nq) va = make_int2(a.window > 0 ? tree_first(a, pos0, tree_depth(a, b, ia)) : 0, pos0);
+      if (ib < seq.nq) vb = make_int2(a.window > 0 ? tree_first(a, pos0, tree_depth(a, b, ib)) : 0, pos0);
+    } else {
+      va = dec_span(a, seq, ia, ia), vb = dec_span(a, seq, ib, ib);
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -144,7 +150,9 @@ __global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constan
         s = raw ? s * a.scale_log2
                 : fmaf(-2.0f * a.cap_out, rcp_approx(ex2(s * a.cap_in * 2.8853900817779268f) + 1.0f), a.cap_out);
         const int tok = tok0 + 8 * j + 2 * t + (e & 1);
-        if (tok >= v.x && tok < v.y) sum[j][e & 1] += ex2(s - r.y);
+        bool seen = tok >= v.x && tok < v.y;
+        if constexpr (kTree) seen = seen || tree_sees_draft(a, seq, b, e < 2 ? ia : ib, tok);
+        if (seen) sum[j][e & 1] += ex2(s - r.y);
       }
   }
 #pragma unroll
@@ -224,8 +232,14 @@ __global__ void __launch_bounds__(kJoinThreads) cache_finish_kernel(const __grid
   if (sum != sum) {  // a NaN row among them: only for the tokens that it sees
     sum = 0.0f;
     for (int r = 0; r < p.rows; ++r) {
-      const int2 see = dec_span(a, seq, r / a.group, r / a.group);
-      if (tok >= see.x && tok < see.y) sum += ex2(__ldcg(s + r * 32) - s_l2[r]);
+      bool seen;
+      if constexpr (C::kTree) {
+        seen = tree_sees(a, seq, b, r / a.group, tok);
+      } else {
+        const int2 see = dec_span(a, seq, r / a.group, r / a.group);
+        seen = tok >= see.x && tok < see.y;
+      }
+      if (seen) sum += ex2(__ldcg(s + r * 32) - s_l2[r]);
     }
   }
   if (tok < a.W)

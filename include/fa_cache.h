@@ -1,7 +1,8 @@
 /*
  * fa_cache.h -- C ABI of the GB300 (sm_103a) library's serving operators: a
- * paged key/value cache held in 8 bits, attention over it, and eviction from
- * it by accumulated attention weight.  Statuses, error messages, streams and
+ * paged key/value cache held in 8 bits, attention over it, eviction from it by
+ * accumulated attention weight, and decoding with a tree of drafted tokens
+ * (attention, verification, acceptance).  Statuses, error messages, streams and
  * the bounded-wait contract are those of fa.h.
  *
  * The cache.  Keys and values live in blocks ("pages") of `page` tokens; a
@@ -12,7 +13,7 @@
  * Sequence b's token j is slot j % page of block table[b, j / page].  Every
  * table entry that a sequence's tokens need must lie in [0, P); the others are
  * never read (-1 is customary).  One block serves one sequence where a call
- * writes it (fa_cache_append, fa_cache_evict); sequences that are only read
+ * writes it (fa_cache_append, fa_cache_accept, fa_cache_evict); sequences that are only read
  * may share blocks.
  *
  * A length past the table (lens[b] > M * page), a negative one, or an entry
@@ -153,6 +154,128 @@ int fa_cache_attn(const fa_cache_attn_args* args);
 /* Bytes of scratch fa_cache_attn needs (it depends on shapes alone); -1 (with
  * the message set) when the arguments are invalid. */
 long long fa_cache_attn_workspace_bytes(const fa_cache_attn_args* args);
+
+/*
+ * fa_cache_attn_tree -- fa_cache_attn where the rows are the drafts of a tree:
+ * row i of n_q[b] is a node, its token in slot base + i, base = lens[b] -
+ * n_q[b] (all appended before, as any tokens), and tree[b, i] the row of its
+ * parent, which is less than i; -1: the node follows the last token before the
+ * drafts.  Then
+ *
+ *   depth(i) = depth(tree[b, i]) + 1, 0 for a node without parent
+ *   row i stands at position base + depth(i) and sees the tokens before slot
+ *   base, itself and the nodes above it; of these, with window > 0, those whose
+ *   position is more than its own - window
+ *
+ * A chain (tree[b, i] = i - 1) is fa_cache_attn.  Rows need not have one root.
+ * An entry that is no earlier row counts as -1 (entries of the rows i < n_q[b]
+ * alone are read), and fa_sync_status() then reports FA_ERR_INVALID_ARGUMENT
+ * once.  Scores, O, L, weights (of all rows; fa_cache_accept moves them with
+ * their tokens), paddings and NaN as fa_cache_attn has them; `attn.causal` must
+ * be set, and n at most 1024.
+ * attn.workspace: 256-byte aligned, fa_cache_attn_tree_workspace_bytes(args) bytes.
+ */
+typedef struct fa_cache_attn_tree_args {
+  fa_cache_attn_args attn;
+  const int* tree;       /* [B, n] */
+  long long tree_stride; /* between sequences; 0: one tree for all */
+} fa_cache_attn_tree_args;
+
+int fa_cache_attn_tree(const fa_cache_attn_tree_args* args);
+long long fa_cache_attn_tree_workspace_bytes(const fa_cache_attn_tree_args* args);
+
+/*
+ * fa_verify_drafts -- which drafted tokens stay, so that what is kept, and the
+ * token behind it, are distributed as the target's probabilities say.
+ *
+ * Node 0 of a sequence's n_q[b] nodes (n when n_q is NULL) is its last token,
+ * which stays; node i > 0 is a draft of token tokens[b, i], behind its parent
+ * tree[b, i] (as in fa_cache_attn_tree; nodes without parent but node 0 are
+ * never reached).  p[b, i, :] are the target's probabilities behind node i,
+ * q[b, i, :] those that node i's children were drawn from, independently and in
+ * the order of their rows; with q NULL the children of a node are distinct
+ * candidates chosen without chance.  From node 0 the path goes on as follows.
+ * At its last node c, with r = p[c], Z = 1, for each child i in order, t its token:
+ *
+ *   u[b, i] * q[c, t] * Z < r[t]   (1 for q[c, t] where q is NULL):
+ *       the path goes on at i; else
+ *   r = max(r - Z q[c], 0), Z = sum of r   (q NULL: Z -= r[t], r[t] = 0)
+ *
+ * Where no child is left, or none was taken, the next token is the least t with
+ * r[0] + .. + r[t] > u_next[b] * (r[0] + r[1] + ..).  If all of r is 0, p[c]
+ * takes its place (and token 0, if that is 0 too).
+ *
+ * path[b, :] are the path's nodes, ascending, path[b, 0] = 0, then -1;
+ * count[b] how many they are (node 0 among them); token[b] the next token.  A
+ * sequence of no nodes gets count 0 and token -1.
+ *
+ * p, q: `dtype` (f32, bf16, f16), element strides {batch, node}, unit inner
+ * stride; rows sum to 1 up to their rounding.  What is no positive finite
+ * number counts as 0.  u, u_next: fp32 in [0, 1), the caller's random numbers.
+ * Sums are taken in 48 bits and more, in a fixed order.
+ * A tree entry out of range counts as -1, a token outside [0, V) is rejected
+ * (its q is 0), n_q[b] outside [0, n] is cut, and fa_sync_status() then reports
+ * FA_ERR_INVALID_ARGUMENT once.  n at most 1024, V at most 2^20.
+ */
+typedef struct fa_verify_drafts_args {
+  const void* p; /* [B, n, V] */
+  const void* q; /* [B, n, V] or NULL */
+  long long p_strides[2];
+  long long q_strides[2];
+  const int* tokens;       /* [B, n] */
+  long long tokens_stride; /* between sequences */
+  const int* tree;         /* [B, n] */
+  long long tree_stride;   /* between sequences; 0: one tree for all */
+  const float* u;          /* [B, n] */
+  long long u_stride;      /* between sequences */
+  const float* u_next;     /* [B] */
+  const int* n_q;          /* [B] or NULL */
+  int* path;               /* [B, n] contiguous */
+  int* count;              /* [B] */
+  int* token;              /* [B] */
+  int B, n, V;
+  int dtype;
+  void* stream;
+} fa_verify_drafts_args;
+
+int fa_verify_drafts(const fa_verify_drafts_args* args);
+
+/*
+ * fa_cache_accept -- of the n_q[b] drafts (n when n_q is NULL) that end the
+ * lens[b] tokens of a sequence, those of a path become its next tokens, the
+ * others are dropped: with base = lens[b] - n_q[b], the token in slot base +
+ * path[b, i] moves to slot base + i, for i < count[b], and lens_out[b] = base +
+ * count[b].  Paths ascend; fa_verify_drafts makes them.  For every layer's cache
+ * alike, with the same path.
+ *
+ * A block that receives tokens gets the largest scale s' of the blocks that
+ * its tokens come from (its own among them where tokens stay before those that
+ * come); a token from a block of scale s becomes round(stored * (s / s')).
+ * weights: NULL or fp32 contiguous [B, H_kv, W], moved along.  (A slot's position
+ * is that of the path's token that it receives: fa_cache_append's numbers stay.)
+ * Slots behind lens_out[b] keep what they held.
+ * lens_out may be lens itself.
+ * A path that does not ascend, or leaves [0, n_q[b]), ends before that entry;
+ * count[b] is cut to [0, n_q[b]]; a sequence with fewer tokens than drafts, or
+ * n_q[b] outside [0, n], stays as it is; fa_sync_status() then reports
+ * FA_ERR_INVALID_ARGUMENT once.  n at most 1024.
+ */
+typedef struct fa_cache_accept_args {
+  fa_cache cache;
+  const int* table; /* [B, M], row stride table_stride */
+  long long table_stride;
+  const int* lens; /* [B]: tokens held, the drafts among them */
+  const int* n_q;  /* [B] or NULL */
+  const int* path; /* [B, n], row stride path_stride */
+  long long path_stride;
+  const int* count; /* [B] */
+  float* weights;
+  int* lens_out; /* [B] */
+  int B, n, M, W;
+  void* stream;
+} fa_cache_accept_args;
+
+int fa_cache_accept(const fa_cache_accept_args* args);
 
 /*
  * fa_cache_evict -- keep at most `keep` tokens of every sequence, chosen per
