@@ -7,6 +7,7 @@
 #include "fa.h"
 #include "fa_cache.h"
 #include "fa_cache_decode.cuh"
+#include "fa_cache_drafts.cuh"
 #include "fa_cache_launch.cuh"
 #include "fa_cache_prompt.cuh"
 #include "fa_cache_weights.cuh"
@@ -160,14 +161,44 @@ int launch_prompt(const CacheAttnParams& a, const LaunchCtx& ctx) {
   return FA_OK;
 }
 
+template <class C>
+int launch_drafts(const CacheAttnParams& a, const LaunchCtx& ctx) {
+  auto kern = cache_drafts_kernel<C>;
+  static std::atomic<unsigned long long> configured{0};
+  if (!((configured.load(std::memory_order_acquire) >> ctx.dev) & 1ull)) {
+    cudaFuncAttributes attr;  // (as for the prompt kernel)
+    const cudaError_t e = cudaFuncGetAttributes(&attr, kern);
+    if (e != cudaSuccess || attr.numRegs != 128) {
+      set_error("kernel register count %d differs from the 128 its register split assumes",
+                e == cudaSuccess ? attr.numRegs : -1);
+      return FA_ERR_CUDA;
+    }
+  }
+  DecParams p;
+  if (!allow_smem(kern, kDraftSmem<C>, ctx.dev, configured)) return FA_ERR_CUDA;
+  if (!line_params<C>(p, a, ctx.num_sms, ctx)) return FA_ERR_UNSUPPORTED;
+  kern<<<p.max_ctas, C::kThreads, kDraftSmem<C>, ctx.stream>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess && p.max_ctas > 1)
+    e = launch_after(cache_join_kernel<C>, dim3((unsigned)join_pieces<C>(p), (unsigned)p.max_ctas - 1), kJoinThreads,
+                     ctx.stream, p);
+  if (e != cudaSuccess) {
+    set_error("cache attention launch failed: %s", cudaGetErrorString(e));
+    return FA_ERR_CUDA;
+  }
+  return FA_OK;
+}
+
 // Which kernel: by the rows of a K/V head.  Up to 16 (the decoding step), 32
 // where the registers hold them; else the tensor memory kernel, which always
 // computes 128 * kTiles rows.
-enum class AttnPlan { kRows16, kRows32, kPrompt };
+// A tree's rows beyond those take the drafts' kernel, 128 or 256 at a time.
+enum class AttnPlan { kRows16, kRows32, kDrafts128, kDrafts256, kPrompt };
 template <int kD>
 AttnPlan attn_plan(const CacheAttnParams& a) {
   const long long rows = (long long)a.n * a.group;
-  if (rows > kPromptRows<kD>) return AttnPlan::kPrompt;
+  if (rows > kPromptRows<kD>)
+    return !a.tree ? AttnPlan::kPrompt : kD == 256 || rows <= 128 ? AttnPlan::kDrafts128 : AttnPlan::kDrafts256;
   return kD <= 128 && rows > 16 ? AttnPlan::kRows32 : AttnPlan::kRows16;
 }
 
@@ -175,6 +206,8 @@ template <int kD>
 long long plan_workspace(const CacheAttnParams& a, int num_sms) {
   switch (attn_plan<kD>(a)) {
     case AttnPlan::kPrompt: return line_workspace<PromptCfg<0, false, kD, 16, true>>(num_sms);
+    case AttnPlan::kDrafts128: return line_workspace<DraftCfg<0, false, kD, 16, true, kD <= 128>>(num_sms);
+    case AttnPlan::kDrafts256: return line_workspace<DraftCfg<0, false, kD, 16, true, false>>(num_sms);
     case AttnPlan::kRows32:
       if constexpr (kD <= 128) return line_workspace<DecCfg<0, false, kD, 2, true>>(num_sms * DecCfg<0, false, kD, 2, true>::kCtas);
     default: return line_workspace<DecCfg<0, false, kD, 1, true>>(num_sms * DecCfg<0, false, kD, 1, true>::kCtas);
@@ -192,18 +225,33 @@ int launch_decode_by(const CacheAttnParams& a, const LaunchCtx& ctx) {
   return launch_decode<DecCfg<kKind, kF16, kD, kMT, false, kTree>>(a, ctx);
 }
 
+// (The variants are the prompt kernel's.)
+template <int kD, int kKind, bool kF16, bool kSplit>
+int launch_drafts_by(const CacheAttnParams& a, const LaunchCtx& ctx) {
+  if (a.cap_out == 0.0f && a.scale_log2 > 0.0f)
+    return a.c.page >= 64 ? launch_drafts<DraftCfg<kKind, kF16, kD, 64, true, kSplit>>(a, ctx)
+                          : launch_drafts<DraftCfg<kKind, kF16, kD, 16, true, kSplit>>(a, ctx);
+  return launch_drafts<DraftCfg<kKind, kF16, kD, 16, false, kSplit>>(a, ctx);
+}
+
 template <int kD, int kKind, bool kF16, bool kTree>
 int launch_plan(const CacheAttnParams& a, const LaunchCtx& ctx) {
-  switch (attn_plan<kD>(a)) {
-    case AttnPlan::kPrompt:
-      if (a.cap_out == 0.0f && a.scale_log2 > 0.0f)
-        return a.c.page >= 64 ? launch_prompt<PromptCfg<kKind, kF16, kD, 64, true, kTree>>(a, ctx)
-                              : launch_prompt<PromptCfg<kKind, kF16, kD, 16, true, kTree>>(a, ctx);
-      return launch_prompt<PromptCfg<kKind, kF16, kD, 16, false, kTree>>(a, ctx);
-    case AttnPlan::kRows32:
-      if constexpr (kD <= 128) return launch_decode_by<kD, kKind, kF16, 2, kTree>(a, ctx);
-    default: return launch_decode_by<kD, kKind, kF16, 1, kTree>(a, ctx);
+  const AttnPlan plan = attn_plan<kD>(a);
+  if constexpr (kTree) {
+    if constexpr (kD <= 128) {
+      if (plan == AttnPlan::kDrafts256) return launch_drafts_by<kD, kKind, kF16, false>(a, ctx);
+    }
+    if (plan == AttnPlan::kDrafts128) return launch_drafts_by<kD, kKind, kF16, kD <= 128>(a, ctx);
+  } else if (plan == AttnPlan::kPrompt) {
+    if (a.cap_out == 0.0f && a.scale_log2 > 0.0f)
+      return a.c.page >= 64 ? launch_prompt<PromptCfg<kKind, kF16, kD, 64, true>>(a, ctx)
+                            : launch_prompt<PromptCfg<kKind, kF16, kD, 16, true>>(a, ctx);
+    return launch_prompt<PromptCfg<kKind, kF16, kD, 16, false>>(a, ctx);
   }
+  if constexpr (kD <= 128) {
+    if (plan == AttnPlan::kRows32) return launch_decode_by<kD, kKind, kF16, 2, kTree>(a, ctx);
+  }
+  return launch_decode_by<kD, kKind, kF16, 1, kTree>(a, ctx);
 }
 
 // kTree: a.tree is there.

@@ -39,7 +39,6 @@
 #pragma once
 
 #include "fa_cache_line.cuh"
-#include "fa_cache_tree.cuh"
 
 namespace fa {
 
@@ -49,10 +48,9 @@ namespace fa {
 // with 16, D 128 144.8 and 157.7, D 256 350 and 381).
 // kRaw_: no softcap and a positive scale, so that a score's FMA scales it too
 // (with one, and 16: 198, 238 and 418 us).
-// kTree_: the rows are the drafts of a tree (fa_cache_tree.cuh).
-template <int kKind_, bool kF16_, int kD_, int kGroup_, bool kRaw_, bool kTree_ = false>
+template <int kKind_, bool kF16_, int kD_, int kGroup_, bool kRaw_>
 struct PromptCfg {
-  static constexpr bool kTree = kTree_;
+  static constexpr bool kTree = false;
   static constexpr bool kRaw = kRaw_;  // scores need no more than a positive factor
   static constexpr int kGroup = kGroup_, kGroups = 128 / kGroup;  // groups a block of keys
   static constexpr int kKind = kKind_;
@@ -77,8 +75,7 @@ struct PromptCfg {
   static constexpr int kKvBytes = 128 * kD * 2;
   static constexpr int kOffK = kTiles * kQBytes, kOffV = kOffK + kStages * kKvBytes;
   static constexpr int kOffMeta = kOffV + kStages * kKvBytes, kOffCtl = kOffMeta + 4 * kGroups * 16;
-  static constexpr int kOffTree = kOffCtl + 512;     // [word][row]: the drafts that a row sees
-  static constexpr int kSmem = 1024 + kOffTree + (kTree ? kTreeWords * kRows * 4 : 0);
+  static constexpr int kSmem = 1024 + kOffCtl + 512;
   static constexpr int kColO = 256;                  // S: two buffers of kKeys columns a tile; P over S
   // Registers: 512 threads x 128 at launch; the softmax warps, which hold a
   // row of scores each, take the others'.
@@ -417,25 +414,14 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
       const bool whole = n == tiles, head_cut = pos > at.seg0;
       const int row = at.rg * C::kRows + t * 128 + tl, i = row / a.group, head = at.h * a.group + row % a.group;
       const bool real = row < p.rows;
-      const int base = at.seq.len - at.seq.nq;  // (trees) the first draft's slot
-      int2 see = make_int2(0, 0);               // tokens; of a tree's row, those before the drafts
-      bool some;
-      if constexpr (C::kTree) {
-        some = real && i < at.seq.nq && base + i >= 0;
-        if (some) see = make_int2(a.window > 0 ? tree_first(a, base, tree_depth(a, at.b, i)) : 0, base);
-      } else {
-        if (real) see = dec_span(a, at.seq, i, i);
-        some = see.x < see.y;
-      }
-      bool have_drafts = false;  // (trees) the row's drafts are in shared memory
-      uint32_t* const s_drafts = reinterpret_cast<uint32_t*>(smem + C::kOffTree) + t * 128 + tl;
+      const int2 see = real ? dec_span(a, at.seq, i, i) : make_int2(0, 0);
       // The warp's query rows, kLanes lanes a row, all loads under way at once:
       // the row's largest entry, then its f16 form.  (S of the piece before is
       // done: the tile may be written.)
       float rs = 1.0f;
       {
         constexpr int kLanes = C::kD / 8, kAtOnce = 32 / kLanes;  // rows a load
-        const uint16_t* mine = some
+        const uint16_t* mine = see.x < see.y
                                    ? static_cast<const uint16_t*>(a.q) + at.b * a.qs[0] + head * a.qs[1] + i * a.qs[2]
                                    : nullptr;
         uint4 w[kLanes];
@@ -479,19 +465,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
 #pragma unroll 1
       for (int j = 0; j < n * C::kParts; ++j, ++nth) {
         const int buf = nth & 1;
-        const int key0 = first * 128 + j * C::kKeys, lo = see.x - key0, hi = see.y - key0;
-        if constexpr (C::kTree) {
-          if (some && hi < C::kKeys && !have_drafts) {
-            tree_write_line<C::kRows>(a, at.b, i, s_drafts);
-            have_drafts = true;
-          }
-          __syncwarp();
-        }
         ok = prompt_warp_wait(&ctl->s_full[t][buf], (uint32_t)(nth >> 1) & 1u, abort, a);
         if (!ok) break;
         tc_fence_after();
         const uint32_t tS = tmem + lane_addr + t * 128 + buf * C::kKeys;
         const float4* meta = s_meta + ((nth / C::kParts) & 3) * C::kGroups + (nth % C::kParts) * kGroups;
+        const int key0 = first * 128 + j * C::kKeys, lo = see.x - key0, hi = see.y - key0;
         uint32_t x[C::kKeys];  // the row's scores (fp32 bits)
 #pragma unroll
         for (int cc = 0; cc < C::kKeys / 32; ++cc)
@@ -500,20 +479,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_prompt_kernel(const __gr
         reg_fence(x);
         if constexpr (!C::kRaw) prompt_scale<C>(x, a, meta, rs);
         if (lo > 0 || hi < C::kKeys) {
-          if constexpr (C::kTree) {
-            uint32_t drafts[C::kKeys / 32] = {};
-            if (some && hi < C::kKeys) {
 #pragma unroll
-              for (int w = 0; w < C::kKeys / 32; ++w) drafts[w] = tree_read_line<C::kRows>(s_drafts, a.n, 32 * w - hi);
-            }
-#pragma unroll
-            for (int k = 0; k < C::kKeys; ++k)
-              if ((k < lo || k >= hi) && !((drafts[k / 32] >> (k & 31)) & 1u)) x[k] = 0xFF800000u;
-          } else {
-#pragma unroll
-            for (int k = 0; k < C::kKeys; ++k)
-              if (k < lo || k >= hi) x[k] = 0xFF800000u;
-          }
+          for (int k = 0; k < C::kKeys; ++k)
+            if (k < lo || k >= hi) x[k] = 0xFF800000u;
         }
         // Group by group: a raw score times f plus y is the score's weight in
         // base 2 (s + log2 vs); y = -inf where nothing is stored.

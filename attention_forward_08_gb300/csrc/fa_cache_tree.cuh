@@ -14,8 +14,6 @@
 
 namespace fa {
 
-constexpr int kTreeWords = kMostDrafts / 32;
-
 // The row above `node` (-1: none).  An entry that is no earlier row counts as -1, and is told.
 __device__ __forceinline__ int tree_parent(const CacheAttnParams& a, int b, int node) {
   const int up = __ldg(a.tree + b * a.tree_stride + node);
@@ -72,7 +70,16 @@ __device__ __noinline__ void tree_write_line(const CacheAttnParams& a, int b, in
     i = tree_parent(a, b, i);
   }
 }
-// Bits `from` .. from + 31 of a line of n nodes (from may be negative).
+// Bits `from` .. from + 31 of row i's line (from may be negative), by walking up;
+__device__ inline __noinline__ uint32_t tree_walk(const CacheAttnParams& a, int b, int i, int from) {
+  uint32_t bits = 0u;
+  for (int n = a.window > 0 ? a.window : INT_MAX; i >= from && i >= 0 && n > 0; --n) {
+    if (i < from + 32) bits |= 1u << (i - from);
+    i = tree_parent(a, b, i);
+  }
+  return bits;
+}
+// ... or of a line of n nodes that was written.
 template <int kStride>
 __device__ __forceinline__ uint32_t tree_read_line(const uint32_t* words, int n, int from) {
   const int w = from >> 5, most = (n + 31) / 32;
