@@ -168,16 +168,19 @@ int launch_drafts(const CacheAttnParams& a, const LaunchCtx& ctx) {
   if (!((configured.load(std::memory_order_acquire) >> ctx.dev) & 1ull)) {
     cudaFuncAttributes attr;  // (as for the prompt kernel)
     const cudaError_t e = cudaFuncGetAttributes(&attr, kern);
-    if (e != cudaSuccess || attr.numRegs != 128) {
-      set_error("kernel register count %d differs from the 128 its register split assumes",
-                e == cudaSuccess ? attr.numRegs : -1);
+    if (e != cudaSuccess || attr.numRegs != C::kRegsLaunch) {
+      set_error("kernel register count %d differs from the %d its register split assumes",
+                e == cudaSuccess ? attr.numRegs : -1, C::kRegsLaunch);
       return FA_ERR_CUDA;
     }
   }
   DecParams p;
   if (!allow_smem(kern, kDraftSmem<C>, ctx.dev, configured)) return FA_ERR_CUDA;
   if (!line_params<C>(p, a, ctx.num_sms, ctx)) return FA_ERR_UNSUPPORTED;
-  kern<<<p.max_ctas, C::kThreads, kDraftSmem<C>, ctx.stream>>>(p);
+  CUtensorMap tk, tv;
+  const int rows = a.c.page < C::kPieceKeys ? a.c.page : C::kPieceKeys;
+  if (!encode_pool_rows(&tk, a.c, false, rows) || !encode_pool_rows(&tv, a.c, true, rows)) return FA_ERR_CUDA;
+  kern<<<p.max_ctas, C::kThreads, kDraftSmem<C>, ctx.stream>>>(tk, tv, p);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && p.max_ctas > 1)
     e = launch_after(cache_join_kernel<C>, dim3((unsigned)join_pieces<C>(p), (unsigned)p.max_ctas - 1), kJoinThreads,

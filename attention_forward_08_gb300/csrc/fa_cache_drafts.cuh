@@ -9,19 +9,23 @@
 // them from HBM, once.
 //
 // Loads.  One warp looks up blocks and scales, up to 16 blocks of 128 keys
-// ahead, and leaves addresses in shared memory; the converter warps keep 48 KB
-// (D = 256: 64 KB) of stored bytes on their way into registers.
+// ahead; one keeps 48 KB of stored bytes on their way, by TMA into a ring of
+// their own (in registers of the converter warps the compiler waits for the last
+// of several loads where the first is needed); the converter warps widen what
+// has landed.
 //
 // Streams.  Up to 128 rows (kSplit) are one row tile, and the two softmax
 // warpgroups take the blocks of keys in turn, each with its own maximum, sum
 // and output in tensor memory, which are joined at a piece's end: as many
 // blocks are in work at a time as with two row tiles.  Up to 256 rows are two
-// tiles as in the prompt kernel.  D = 256 has room for one tile and one stream.
+// tiles as in the prompt kernel.  D = 256 has room for one stream, and for 64 rows
+// (half of a tile; its other half computes what lies behind, which nobody reads).
 //
 // Bound: memory, 2 * D bytes a token and K/V head; then the converters and the
 // softmax warps' chains.
 #pragma once
 
+#include "fa_cache_decode.cuh"
 #include "fa_cache_prompt.cuh"
 #include "fa_cache_tree.cuh"
 
@@ -39,24 +43,30 @@ struct DraftCfg {
   static_assert(kD <= 128 || !kSplit, "no room for two outputs");
   static constexpr int kTiles = kD <= 128 && !kSplit ? 2 : 1;  // 128-row tiles
   static constexpr int kSoft = kD <= 128 ? 2 : 1;              // softmax warpgroups, issuers
-  static constexpr int kRows = 128 * kTiles;
+  static constexpr int kRows = kD == 256 ? 64 : 128 * kTiles;
+  static constexpr int kQRows = kD == 256 ? 64 : 128;          // of a tile in shared memory
   static constexpr int kTile = 128;  // keys a block of the line
   static constexpr int kMinTiles = 4;
   static constexpr int kLift = 7;
-  static constexpr int kStages = kD == 64 ? 4 : kD == 128 ? 2 : 1;  // of K; of V alike
+  // Stages of the widened K and V, and the ring of stored bytes: pieces of 128
+  // keys (D = 256: 64).
+  static constexpr int kStagesK = kD == 64 ? 4 : kD == 128 ? 2 : 1, kStagesV = kD == 128 && !kSplit ? 1 : kStagesK;
+  static constexpr int kPieceKeys = kD == 256 ? 64 : 128, kPieceBytes = kPieceKeys * kD, kPieces = 128 / kPieceKeys;
+  static constexpr int kRing = 49152 / kPieceBytes;
   static constexpr int kKeys = kD <= 128 ? 64 : 128, kParts = 128 / kKeys;  // keys a score buffer
-  static constexpr int kConvWarps = kD <= 128 ? 4 : 8;
+  static constexpr int kConvWarps = 8;
   static constexpr int kThreads = 128 + 32 * kConvWarps + 128 * kSoft;
-  // Registers: 512 threads x 128 at launch.
-  static constexpr int kRegsCtrl = 56, kRegsConv = kD <= 128 ? 136 : 112, kRegsSoft = kD <= 128 ? 160 : 224;
-  static_assert(kThreads == 512 && 128 * kRegsCtrl + 32 * kConvWarps * kRegsConv + 128 * kSoft * kRegsSoft <= 512 * 128,
+  // Registers: at launch 640 threads x 96 or 512 x 128.
+  static constexpr int kRegsLaunch = kThreads == 640 ? 96 : 128;
+  static constexpr int kRegsCtrl = kD <= 128 ? 48 : 56, kRegsConv = kD <= 128 ? 64 : 72, kRegsSoft = kD <= 128 ? 152 : 240;
+  static_assert(kRegsCtrl < kRegsLaunch && kRegsConv < kRegsLaunch && kRegsSoft > kRegsLaunch, "which warps give, which take");
+  static_assert(128 * kRegsCtrl + 32 * kConvWarps * kRegsConv + 128 * kSoft * kRegsSoft <= kThreads * kRegsLaunch,
                 "register split exceeds the launch allocation");
   static constexpr int kUnits = kD / 16;                            // 16-byte units a key
-  static constexpr int kSet = 128 * kUnits / (32 * kConvWarps);     // a converter's units of a block's K, or V: 4 or 8
-  static constexpr int kSets = kD == 64 ? 6 : kD == 128 ? 3 : 2;    // sets of registers that are on their way
-  static constexpr int kQBytes = 128 * kD * 2, kKvBytes = 128 * kD * 2;
-  static constexpr int kOffK = kTiles * kQBytes, kOffV = kOffK + kStages * kKvBytes;
-  static constexpr int kOffInfo = kOffV + kStages * kKvBytes;
+  static constexpr int kSet = kPieceKeys * kUnits / (32 * kConvWarps);  // a converter's units of a piece: 2 or 4
+  static constexpr int kQBytes = kQRows * kD * 2, kKvBytes = 128 * kD * 2;
+  static constexpr int kOffK = kTiles * kQBytes, kOffV = kOffK + kStagesK * kKvBytes;
+  static constexpr int kOffRing = kOffV + kStagesV * kKvBytes, kOffInfo = kOffRing + 49152;
   static constexpr int kColO = 256;  // S: two buffers of kKeys columns a stream; P over S
 };
 
@@ -66,9 +76,10 @@ constexpr int kDraftWords = 8;    // of a row's drafts that are kept (more are l
 template <class C>
 struct DraftInfo {
   float4 meta[kDraftAhead][8];          // by 16 keys: ks, log2 vs, 1 / vs less the lift, there
-  long long k_from[kDraftAhead][8];     // bytes from the pool's begin to the first of 16 keys
-  long long v_from[kDraftAhead][8];
+  int2 from[kDraftAhead][8];            // cache block (-1: none), head
   int range[kDraftAhead][8];            // keys that are stored and seen: lo | hi << 8; values that count: lo << 16 | hi << 24
+  int tok[kDraftAhead];                 // a block's first token
+  uint32_t all[kDraftAhead];            // 1: all keys are stored and seen; 2: all values count
   uint32_t line[kDraftWords][128 * C::kSoft];  // the drafts that a softmax thread's row sees
   float2 ml[2][128];                    // (streams) references and sums
   uint64_t q_full[2];                   // 4 softmax warps: query tile written
@@ -76,7 +87,7 @@ struct DraftInfo {
   uint64_t s_full[2][2];                // [stream][buffer]: S computed
   uint64_t p_ready[2];                  // softmax wrote P (and rescaled O)
   uint64_t o_ready[2];                  // each PV done
-  uint64_t info_full[4], info_empty[4], drain[2];
+  uint64_t info_full[4], info_empty[4], ring_full[6], ring_empty[6], drain[2];
   int n[2][2];                          // [stream][piece & 1]: blocks of a piece (0: no more), beside q_full
   uint32_t tmem;
   int abort;
@@ -84,17 +95,6 @@ struct DraftInfo {
 
 template <class C>
 constexpr int kDraftSmem = 1024 + C::kOffInfo + (int)sizeof(DraftInfo<C>);
-
-// 16 bytes that are read once; zeros if not `there`.
-__device__ __forceinline__ uint4 draft_load(const uint8_t* p, bool there) {
-  uint4 v;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
-      "mov.u32 %3, 0;\n\t@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-      : "l"(p), "r"((uint32_t)there));
-  return v;
-}
 
 // A row's scores to base 2 where one positive factor cannot do it.
 template <class C>
@@ -123,7 +123,8 @@ __device__ __forceinline__ uint32_t draft_seen(const CacheAttnParams& a, int b, 
 }
 
 template <class C>
-__global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __grid_constant__ DecParams p) {
+__global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(
+    const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const __grid_constant__ DecParams p) {
   static_assert(kDraftSmem<C> <= 232448, "shared memory");
   const CacheAttnParams& a = p.a;
   const CacheView& c = a.c;
@@ -152,8 +153,14 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
       mbar_init(&info->info_full[i], 1);
       mbar_init(&info->info_empty[i], C::kSoft);
     }
+    for (int i = 0; i < C::kRing; ++i) {
+      mbar_init(&info->ring_full[i], 1);
+      mbar_init(&info->ring_empty[i], C::kConvWarps);
+    }
     info->abort = 0;
     fence_barrier_init();
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
   }
   if (warp == 1) {
     tmem_alloc(&info->tmem, 512);
@@ -165,8 +172,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
   const uint32_t tmem = info->tmem;
   volatile int* abort = &info->abort;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return prompt_warp_wait(bar, parity, abort, a); };
-  // Block nb of this thread block's has stage nb % kStages; stream t takes every
-  // block, or those with nb % 2 == t.
+  // Block nb of this thread block's has stages nb % kStagesK and nb % kStagesV;
+  // stream t takes every block, or those with nb % 2 == t.
   constexpr int kStep = C::kSplit ? 2 : 1;
 
   if (warp < 4) {
@@ -186,8 +193,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
         const uint32_t dst = tmem + t * 128 + buf * C::kKeys;
 #pragma unroll
         for (int kk = 0; kk < C::kD / 16; ++kk) {
-          const uint32_t off = (kk / 4) * ((128 * 128) >> 4) + (kk % 4) * 2;
-          mma_f16_ss_by(lead, dst, dQ + off, k0 + off, idS, kk > 0 ? 1u : 0u);
+          mma_f16_ss_by(lead, dst, dQ + (kk / 4) * ((C::kQRows * 128) >> 4) + (kk % 4) * 2,
+                        k0 + (kk / 4) * ((128 * 128) >> 4) + (kk % 4) * 2, idS, kk > 0 ? 1u : 0u);
         }
         mma_commit_by(lead, &info->s_full[t][buf]);
         if (part == C::kParts - 1) mma_commit_by(lead, &info->k_empty[stage]);
@@ -201,8 +208,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
         mma_commit_by(lead, &info->o_ready[t]);
         if (part == C::kParts - 1) mma_commit_by(lead, &info->v_empty[stage]);
       };
-      auto stage_of = [](int nb) { return nb & (C::kStages - 1); };
-      auto par_of = [](int nb) { return (uint32_t)(nb / C::kStages) & 1u; };
+      auto stage_of = [](int nb) { return nb & (C::kStagesK - 1); };
+      auto par_of = [](int nb) { return (uint32_t)(nb / C::kStagesK) & 1u; };
       int nth = 0, before = 0;  // this stream's score buffers; all blocks of earlier pieces
       bool ok = true;
 #pragma unroll 1
@@ -221,7 +228,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
         issue_S(nth & 1, stage_of(begin), 0);
 #pragma unroll 1
         for (int nb = begin; nb < end && ok; nb += kStep) {
-          const int stage = stage_of(nb), next = nb + kStep;
+          const int stage = stage_of(nb), next = nb + kStep, stage_v = nb & (C::kStagesV - 1);
 #pragma unroll
           for (int part = 0; part < C::kParts; ++part) {
             // the next scores go before this PV
@@ -233,10 +240,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
               tc_fence_after();
               issue_S((nth + 1) & 1, stage_of(next), 0);
             }
-            ok = (part > 0 || wait(&info->v_full[stage], par_of(nb))) && wait(&info->p_ready[t], (uint32_t)nth & 1u);
+            ok = (part > 0 || wait(&info->v_full[stage_v], (uint32_t)(nb / C::kStagesV) & 1u)) && wait(&info->p_ready[t], (uint32_t)nth & 1u);
             if (!ok) break;
             tc_fence_after();
-            issue_PV(nth & 1, stage, part, nb == begin && part == 0);
+            issue_PV(nth & 1, stage_v, part, nb == begin && part == 0);
             ++nth;
           }
           if (!ok) break;
@@ -293,85 +300,134 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
         // (values of a zero scale are zeros, and count with the scale 1)
         const bool zero = !(vs >= 1.17549435e-38f);
         info->meta[slot][g] = make_float4(ks, zero ? 0.0f : lg2(vs), dec_unlift(C::kLift) * (zero ? 1.0f : 1.0f / vs), blk >= 0 ? 1.0f : 0.0f);
-        const long long row = mine & (c.page - 1);
-        info->k_from[slot][g] = blk >= 0 ? blk * c.ks[0] + h * c.ks[1] + row * c.ks[2] : 0;
-        info->v_from[slot][g] = blk >= 0 ? blk * c.vs[0] + h * c.vs[1] + row * c.vs[2] : 0;
+        info->from[slot][g] = make_int2(blk, h);
+        if (g == 0) info->tok[slot] = mine;
         const int keys = blk >= 0 && lo < hi ? lo | (hi << 8) : 0;
         info->range[slot][g] = keys | (zero ? 0 : keys << 16);
+        const uint32_t k_all = __ballot_sync(0xFFFFFFFFu, keys == 16 << 8), v_all = __ballot_sync(0xFFFFFFFFu, keys == 16 << 8 && !zero);
+        const int shift = lane & 24;
+        if (g == 0) info->all[slot] = (((k_all >> shift) & 255u) == 255u ? 1u : 0u) | (((v_all >> shift) & 255u) == 255u ? 2u : 0u);
         __syncwarp();
         if (lane == 0) mbar_arrive(&info->info_full[batch & 3]);
       }
+    } else if (warp == 3) {
+      // ---------------------------------------------------------- stored bytes
+      // A lane a 16-key group; one of those that share a box of the tensor map
+      // copies it (its block, if any of them has one).
+      constexpr int kGroupsHere = C::kPieceKeys / 16;
+      const int rows = min(c.page, C::kPieceKeys), share = rows / 16;
+      int slot = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (int nb = 0; nb < t1 - t0 && ok; ++nb) {
+        if ((nb & 3) == 0) ok = wait(&info->info_full[(nb >> 2) & 3], (uint32_t)(nb >> 4) & 1u);
+        if (!ok) break;
+        const int at_info = nb & (kDraftAhead - 1), tok = info->tok[at_info];
+#pragma unroll 1
+        for (int i = 0; i < 2 * C::kPieces; ++i) {
+          const bool is_v = i >= C::kPieces;
+          const int g0 = (is_v ? i - C::kPieces : i) * kGroupsHere, g = g0 + lane % kGroupsHere;
+          const int2 from = info->from[at_info][g];
+          int blk = lane < kGroupsHere ? from.x : -1;
+#pragma unroll
+          for (int o = 1; o < kGroupsHere; o <<= 1) {
+            const int other = __shfl_xor_sync(0xFFFFFFFFu, blk, o);
+            if (o < share) blk = max(blk, other);
+          }
+          const bool box = lane < kGroupsHere && (lane & (share - 1)) == 0 && blk >= 0;
+          const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, box));
+          if (issued >= C::kRing) ok = wait(&info->ring_empty[slot], phase ^ 1u);
+          if (!ok) break;
+          uint64_t* const bar = &info->ring_full[slot];
+          if (lane == 0) {
+            if (boxes > 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * rows * C::kD));
+            else mbar_arrive(bar);
+          }
+          __syncwarp();
+          if (box)
+            tma_load_4d(smem + C::kOffRing + slot * C::kPieceBytes + lane * 16 * C::kD, is_v ? &tv : &tk, bar, 0,
+                        (tok + 16 * g) & (c.page - 1), from.y, blk);
+          __syncwarp();
+          ++issued;
+          if (++slot == C::kRing) slot = 0, phase ^= 1u;
+        }
+      }
+      // Copies land before the block ends (also where nobody looked at them; bounded).
+      const long long begin = clock64_now();
+      for (int k = max(0, issued - C::kRing); k < issued; ++k)
+        while (!mbar_try_wait(&info->ring_full[k % C::kRing], (uint32_t)(k / C::kRing) & 1u) &&
+               clock64_now() - begin < kDecDrainCycles) {
+        }
     }
   } else if (warp < 4 + C::kConvWarps) {
     // ============================================================ converters
-    if constexpr (C::kRegsConv > 128) regs_inc<C::kRegsConv>();
-    else regs_dec<C::kRegsConv>();
+    regs_dec<C::kRegsConv>();
     const int cw = warp - 4;
     // Lane bits 0-1: unit, 2: key, then units, then keys: eight neighbours
     // write eight different 16-byte columns of the swizzled rows.
     constexpr int kHigh = C::kUnits / 4;
-    constexpr int kKeysWarp = 32 / C::kUnits, kKeysStep = kKeysWarp * C::kConvWarps;  // 16, or 32 (D = 64)
+    constexpr int kKeysWarp = 32 / C::kUnits, kKeysStep = kKeysWarp * C::kConvWarps;  // 64, 32, 16
     const int unit = (lane & 3) + 4 * ((lane >> 3) % kHigh);
     const int key0 = cw * kKeysWarp + ((lane >> 2) & 1) + 2 * ((lane >> 3) / kHigh);
-    const int g0 = key0 >> 4, r = key0 & 15;  // its keys are key r of groups g0, g0 + kKeysStep / 16, ..
+    const int g0 = key0 >> 4, r = key0 & 15;  // its keys of a piece are key r of groups g0, g0 + kKeysStep / 16, ..
     uint8_t* const to = smem + C::kOffK + (uint32_t)(unit / 4) * (128 * 128) + key0 * 128;
-    const uint32_t lo16 = ((unit % 4) * 2 ^ (key0 & 7)) << 4, hi16 = ((unit % 4) * 2 + 1 ^ (key0 & 7)) << 4;
-    const uint8_t *const k_pool = c.k + unit * 16 + r * c.ks[2], *const v_pool = c.v + unit * 16 + r * c.vs[2];
-    const int sets = 2 * (t1 - t0);  // K's, then V's, of one block after the other
-    uint4 x[C::kSets][C::kSet];
-    int from = 0, set = 0;  // the next set to be loaded; to be stored
+    const uint32_t lo16 = (((unit % 4) * 2) ^ (key0 & 7)) << 4, hi16 = (((unit % 4) * 2 + 1) ^ (key0 & 7)) << 4;
+    const uint32_t from = smem_u32(smem + C::kOffRing) + key0 * C::kD + unit * 16;
+    int slot = 0;
+    uint32_t phase = 0;
     bool ok = true;
-    auto load = [&](uint4 (&w)[C::kSet]) {
-      if (from >= sets || !ok) return;
-      const int nb = from >> 1, slot = nb & (kDraftAhead - 1);
-      const bool is_v = from & 1;
-      if ((from & 7) == 0 && !(ok = wait(&info->info_full[(nb >> 2) & 3], (uint32_t)(nb >> 4) & 1u))) return;
-      const long long* off = (is_v ? info->v_from[slot] : info->k_from[slot]) + g0;
-      const int* range = info->range[slot] + g0;
-      const uint8_t* const pool = is_v ? v_pool : k_pool;
-      const int shift = is_v ? 16 : 0;
-#pragma unroll
-      for (int i = 0; i < C::kSet; ++i) {
-        const int keys = range[i * (kKeysStep / 16)] >> shift;
-        w[i] = draft_load(pool + off[i * (kKeysStep / 16)], r >= (keys & 255) && r < ((keys >> 8) & 255));
-      }
-      ++from;
-    };
-    auto store = [&](const uint4 (&w)[C::kSet]) {
-      const int nb = set >> 1, stage = nb & (C::kStages - 1);
-      const bool is_v = set & 1;
-      if (nb >= C::kStages) ok = ok && wait(is_v ? &info->v_empty[stage] : &info->k_empty[stage], (uint32_t)(nb / C::kStages + 1) & 1u);
-      if (!ok) return;
-      uint8_t* row = to + (is_v ? C::kOffV - C::kOffK : 0) + stage * C::kKvBytes;
-#pragma unroll
-      for (int i = 0; i < C::kSet; ++i) {  // (a step of kKeysStep keys leaves the swizzle as it is)
-        uint4 lo, hi;
-        widen16<C::kKind>(w[i], lo, hi);
-        *reinterpret_cast<uint4*>(row + i * (kKeysStep * 128) + lo16) = lo;
-        *reinterpret_cast<uint4*>(row + i * (kKeysStep * 128) + hi16) = hi;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(is_v ? &info->v_full[stage] : &info->k_full[stage]);
-      ++set;
-    };
-#pragma unroll
-    for (int s = 0; s < C::kSets; ++s) load(x[s]);
 #pragma unroll 1
-    while (set < sets && ok) {
+    for (int nb = 0; nb < t1 - t0 && ok; ++nb) {
+      const int at_info = nb & (kDraftAhead - 1);
 #pragma unroll
-      for (int s = 0; s < C::kSets; ++s) {
-        if (set < sets && ok) {
-          store(x[s]);
-          load(x[s]);
+      for (int i = 0; i < 2 * C::kPieces; ++i) {
+        const bool is_v = i >= C::kPieces;
+        const int piece = is_v ? i - C::kPieces : i;
+        ok = wait(&info->ring_full[slot], phase);
+        if (!ok) break;
+        uint4 x[C::kSet];
+#pragma unroll
+        for (int u = 0; u < C::kSet; ++u) x[u] = lds128(from + slot * C::kPieceBytes + u * (kKeysStep * C::kD));
+        if (!(info->all[at_info] & (is_v ? 2u : 1u))) {  // where nobody sees them or nothing is stored: zeros
+          const int* range = info->range[at_info] + piece * (C::kPieceKeys / 16) + g0;
+#pragma unroll
+          for (int u = 0; u < C::kSet; ++u) {
+            const int keys = range[u * (kKeysStep / 16)] >> (is_v ? 16 : 0);
+            if (!(r >= (keys & 255) && r < ((keys >> 8) & 255))) x[u] = make_uint4(0, 0, 0, 0);
+          }
         }
+        constexpr int kStages[2] = {C::kStagesK, C::kStagesV};
+        const int stages = kStages[is_v], stage = nb & (stages - 1);
+        if (piece == 0 && nb >= stages) {
+          ok = wait(is_v ? &info->v_empty[stage] : &info->k_empty[stage], (uint32_t)(nb / stages + 1) & 1u);
+          if (!ok) break;
+        }
+        uint8_t* const row = to + (is_v ? C::kOffV - C::kOffK : 0) + stage * C::kKvBytes + piece * (C::kPieceKeys * 128);
+#pragma unroll
+        for (int u = 0; u < C::kSet; ++u) {  // (a step of kKeysStep keys leaves the swizzle as it is)
+          uint4 lo, hi;
+          widen16<C::kKind>(x[u], lo, hi);
+          *reinterpret_cast<uint4*>(row + u * (kKeysStep * 128) + lo16) = lo;
+          *reinterpret_cast<uint4*>(row + u * (kKeysStep * 128) + hi16) = hi;
+        }
+        if (piece == C::kPieces - 1) fence_proxy_async_smem();
+        __syncwarp();
+        // (The slot is free once what was read has been used: given back right behind
+        // the loads, it was filled again before a warp that waited for its stage
+        // had its bytes.)
+        if (lane == 0) {
+          if (piece == C::kPieces - 1) mbar_arrive(is_v ? &info->v_full[stage] : &info->k_full[stage]);
+          mbar_arrive(&info->ring_empty[slot]);
+        }
+        if (++slot == C::kRing) slot = 0, phase ^= 1u;
       }
     }
   } else {
     // ============================================================ softmax
     regs_inc<C::kRegsSoft>();
-    const int t = C::kSoft == 2 ? (warp - 8) >> 2 : 0;
-    const int tl = tid - (512 - 128 * C::kSoft) - 128 * t;  // row of the tile = TMEM lane
+    const int t = (warp - 4 - C::kConvWarps) >> 2;
+    const int tl = tid - (C::kThreads - 128 * C::kSoft) - 128 * t;  // row of the tile = TMEM lane
     const int row_tile = C::kSplit ? 0 : t;
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tO = tmem + lane_addr + C::kColO + t * C::kD;
@@ -386,7 +442,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
       const int first = span.x / 128 + pos - at.seg0;
       const bool whole = n == tiles, head_cut = pos > at.seg0;
       const int row = at.rg * C::kRows + row_tile * 128 + tl, i = row / a.group, head = at.h * a.group + row % a.group;
-      const bool real = row < p.rows;
+      const bool real = tl < C::kQRows && row < p.rows;
       const int base = at.seq.len - at.seq.nq;  // the first draft's slot
       const bool some = real && i < at.seq.nq && base + i >= 0;
       // Does any row of this warp's count?  (Rows are those of whole tiles.)
@@ -428,8 +484,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
                 x[e] = pack_f16x2(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xFFFF0000u) * up);
             }
             const int r = (warp & 3) * 32 + (u0 + u) * kAtOnce + lane / kLanes, c16 = lane % kLanes;
-            if (!C::kSplit || t == 0)
-              *reinterpret_cast<uint4*>(q_tile + (c16 / 8) * (128 * 128) + r * 128 + (((c16 % 8) ^ (r & 7)) << 4)) = w[u];
+            if (r < C::kQRows && (!C::kSplit || t == 0))
+              *reinterpret_cast<uint4*>(q_tile + (c16 / 8) * (C::kQRows * 128) + r * 128 + (((c16 % 8) ^ (r & 7)) << 4)) = w[u];
           }
         }
       }
