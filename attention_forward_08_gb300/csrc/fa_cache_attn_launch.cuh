@@ -162,7 +162,7 @@ int launch_prompt(const CacheAttnParams& a, const LaunchCtx& ctx) {
 }
 
 template <class C>
-int launch_drafts(const CacheAttnParams& a, const LaunchCtx& ctx) {
+int launch_drafts(const CacheAttnParams& a, int kind, bool f16, const LaunchCtx& ctx) {
   auto kern = cache_drafts_kernel<C>;
   static std::atomic<unsigned long long> configured{0};
   if (!((configured.load(std::memory_order_acquire) >> ctx.dev) & 1ull)) {
@@ -177,14 +177,18 @@ int launch_drafts(const CacheAttnParams& a, const LaunchCtx& ctx) {
   DecParams p;
   if (!allow_smem(kern, kDraftSmem<C>, ctx.dev, configured)) return FA_ERR_CUDA;
   if (!line_params<C>(p, a, ctx.num_sms, ctx)) return FA_ERR_UNSUPPORTED;
+  p.kind = kind;
+  p.f16 = f16;
   CUtensorMap tk, tv;
   const int rows = a.c.page < C::kPieceKeys ? a.c.page : C::kPieceKeys;
   if (!encode_pool_rows(&tk, a.c, false, rows) || !encode_pool_rows(&tv, a.c, true, rows)) return FA_ERR_CUDA;
   kern<<<p.max_ctas, C::kThreads, kDraftSmem<C>, ctx.stream>>>(tk, tv, p);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && p.max_ctas > 1)
-    e = launch_after(cache_join_kernel<C>, dim3((unsigned)join_pieces<C>(p), (unsigned)p.max_ctas - 1), kJoinThreads,
-                     ctx.stream, p);
+  if (e == cudaSuccess && p.max_ctas > 1) {
+    const dim3 grid((unsigned)join_pieces<C>(p), (unsigned)p.max_ctas - 1);
+    e = f16 ? launch_after(cache_join_kernel<DraftF16<C>>, grid, kJoinThreads, ctx.stream, p)
+            : launch_after(cache_join_kernel<C>, grid, kJoinThreads, ctx.stream, p);
+  }
   if (e != cudaSuccess) {
     set_error("cache attention launch failed: %s", cudaGetErrorString(e));
     return FA_ERR_CUDA;
@@ -209,8 +213,8 @@ template <int kD>
 long long plan_workspace(const CacheAttnParams& a, int num_sms) {
   switch (attn_plan<kD>(a)) {
     case AttnPlan::kPrompt: return line_workspace<PromptCfg<0, false, kD, 16, true>>(num_sms);
-    case AttnPlan::kDrafts128: return line_workspace<DraftCfg<0, false, kD, 16, true, kD <= 128>>(num_sms);
-    case AttnPlan::kDrafts256: return line_workspace<DraftCfg<0, false, kD, 16, true, false>>(num_sms);
+    case AttnPlan::kDrafts128: return line_workspace<DraftCfg<kD, 16, true, kD <= 128, 1>>(num_sms);
+    case AttnPlan::kDrafts256: return line_workspace<DraftCfg<kD, 16, true, false, 1>>(num_sms);
     case AttnPlan::kRows32:
       if constexpr (kD <= 128) return line_workspace<DecCfg<0, false, kD, 2, true>>(num_sms * DecCfg<0, false, kD, 2, true>::kCtas);
     default: return line_workspace<DecCfg<0, false, kD, 1, true>>(num_sms * DecCfg<0, false, kD, 1, true>::kCtas);
@@ -228,23 +232,34 @@ int launch_decode_by(const CacheAttnParams& a, const LaunchCtx& ctx) {
   return launch_decode<DecCfg<kKind, kF16, kD, kMT, false, kTree>>(a, ctx);
 }
 
-// (The variants are the prompt kernel's.)
-template <int kD, int kKind, bool kF16, bool kSplit>
-int launch_drafts_by(const CacheAttnParams& a, const LaunchCtx& ctx) {
-  if (a.cap_out == 0.0f && a.scale_log2 > 0.0f)
-    return a.c.page >= 64 ? launch_drafts<DraftCfg<kKind, kF16, kD, 64, true, kSplit>>(a, ctx)
-                          : launch_drafts<DraftCfg<kKind, kF16, kD, 16, true, kSplit>>(a, ctx);
-  return launch_drafts<DraftCfg<kKind, kF16, kD, 16, false, kSplit>>(a, ctx);
+template <int kD>
+int launch_drafts_by(const CacheAttnParams& a, AttnPlan plan, int kind, bool f16, const LaunchCtx& ctx) {
+  const bool raw = a.cap_out == 0.0f && a.scale_log2 > 0.0f;
+  if constexpr (kD <= 128) {
+    if (plan == AttnPlan::kDrafts128) {
+      const int rows = a.n * a.group;
+      if (rows <= 32)
+        return raw ? launch_drafts<DraftCfg<kD, 16, true, true, 4>>(a, kind, f16, ctx)
+                   : launch_drafts<DraftCfg<kD, 16, false, true, 4>>(a, kind, f16, ctx);
+      if (rows <= 64)
+        return raw ? launch_drafts<DraftCfg<kD, 16, true, true, 2>>(a, kind, f16, ctx)
+                   : launch_drafts<DraftCfg<kD, 16, false, true, 2>>(a, kind, f16, ctx);
+      return raw ? launch_drafts<DraftCfg<kD, 16, true, true, 1>>(a, kind, f16, ctx)
+                 : launch_drafts<DraftCfg<kD, 16, false, true, 1>>(a, kind, f16, ctx);
+    }
+  }
+  // (The variants are the prompt kernel's.)
+  if (!raw) return launch_drafts<DraftCfg<kD, 16, false, false, 1>>(a, kind, f16, ctx);
+  return a.c.page >= 64 ? launch_drafts<DraftCfg<kD, 64, true, false, 1>>(a, kind, f16, ctx)
+                        : launch_drafts<DraftCfg<kD, 16, true, false, 1>>(a, kind, f16, ctx);
 }
 
 template <int kD, int kKind, bool kF16, bool kTree>
 int launch_plan(const CacheAttnParams& a, const LaunchCtx& ctx) {
   const AttnPlan plan = attn_plan<kD>(a);
   if constexpr (kTree) {
-    if constexpr (kD <= 128) {
-      if (plan == AttnPlan::kDrafts256) return launch_drafts_by<kD, kKind, kF16, false>(a, ctx);
-    }
-    if (plan == AttnPlan::kDrafts128) return launch_drafts_by<kD, kKind, kF16, kD <= 128>(a, ctx);
+    if (plan == AttnPlan::kDrafts128 || plan == AttnPlan::kDrafts256)
+      return launch_drafts_by<kD>(a, plan, kKind, kF16, ctx);
   } else if (plan == AttnPlan::kPrompt) {
     if (a.cap_out == 0.0f && a.scale_log2 > 0.0f)
       return a.c.page >= 64 ? launch_prompt<PromptCfg<kKind, kF16, kD, 64, true>>(a, ctx)

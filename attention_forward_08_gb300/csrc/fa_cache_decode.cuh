@@ -481,7 +481,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       uint32_t drafts[C::kTree ? C::kMT : 1][2];  // of a tree: the drafts that they see, beside those tokens
       const int base = seq.len - seq.nq;
       uint32_t line = 0;  // of lane i: node i and the nodes above it
-      if constexpr (C::kTree) line = tree_lines(a, b, seq.nq);
+      const TreeOf tree = tree_of(a, b);
+      if constexpr (C::kTree) line = tree_lines(lane < seq.nq ? tree_parent(tree, lane) : -1);
 #pragma unroll
       for (int mt = 0; mt < C::kMT; ++mt) {
 #pragma unroll
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           int2 v = make_int2(0, 0x7fffffff);
           if constexpr (C::kTree) {
             drafts[mt][x] = __shfl_sync(0xFFFFFFFFu, line, i & 31);
-            if (real) v = make_int2(tree_window(a, base, drafts[mt][x]), base);
+            if (real) v = make_int2(tree_window(tree, base, drafts[mt][x]), base);
             else drafts[mt][x] = 0u;
           } else if (real) {
             v = dec_span(a, seq, i, i);

@@ -9,17 +9,21 @@
 // them from HBM, once.
 //
 // Loads.  One warp looks up blocks and scales, up to 16 blocks of 128 keys
-// ahead; one keeps 48 KB of stored bytes on their way, by TMA into a ring of
-// their own (in registers of the converter warps the compiler waits for the last
-// of several loads where the first is needed); the converter warps widen what
-// has landed.
+// ahead; one keeps 48 KB of stored bytes on their way, by TMA into two rings, of K
+// and of V (loads to registers of the converter warps: the compiler waits for the
+// last of several where the first is needed); four converter warps widen K and
+// four V, so that neither waits for the other's place.
 //
-// Streams.  Up to 128 rows (kSplit) are one row tile, and the two softmax
-// warpgroups take the blocks of keys in turn, each with its own maximum, sum
-// and output in tensor memory, which are joined at a piece's end: as many
-// blocks are in work at a time as with two row tiles.  Up to 256 rows are two
-// tiles as in the prompt kernel.  D = 256 has room for one stream, and for 64 rows
-// (half of a tile; its other half computes what lies behind, which nobody reads).
+// Streams.  Up to 128 rows (kSplit) are one row tile, and of every block of keys
+// each of the two softmax warpgroups takes one half, with its own maximum, sum
+// and output in tensor memory, which are joined at a piece's end: as many keys
+// are in work at a time as with two row tiles.  Up to 64 rows (32) are in the
+// tile twice (four times), and a copy weighs every second (fourth) run of keys,
+// with a maximum, sum and output of its own: the tensor cores compute the whole
+// tile anyhow, and a softmax thread has half (a quarter) of the work.
+// Up to 256 rows are two tiles as in the prompt kernel.  D = 256 has room for one
+// stream, and for 64 rows (half of a tile; its other half computes what lies
+// behind, which nobody reads).
 //
 // Bound: memory, 2 * D bytes a token and K/V head; then the converters and the
 // softmax warps' chains.
@@ -31,16 +35,17 @@
 
 namespace fa {
 
-template <int kKind_, bool kF16_, int kD_, int kGroup_, bool kRaw_, bool kSplit_>
+// kDup_: copies of the rows in the row tile, each with its share of the keys.
+template <int kD_, int kGroup_, bool kRaw_, bool kSplit_, int kDup_>
 struct DraftCfg {
   static constexpr bool kTree = true;
+  static constexpr bool kF16 = false;      // (the join's; the kernel itself asks at run time)
+  static constexpr int kDup = kDup_;
   static constexpr bool kRaw = kRaw_;      // scores need no more than a positive factor
   static constexpr bool kSplit = kSplit_;  // two streams of keys for one row tile
   static constexpr int kGroup = kGroup_;   // tokens that surely share a cache block: 16, or 64
-  static constexpr int kKind = kKind_;
-  static constexpr bool kF16 = kF16_;
   static constexpr int kD = kD_;
-  static_assert(kD <= 128 || !kSplit, "no room for two outputs");
+  static_assert(kSplit ? kD <= 128 && kGroup == 16 : kDup == 1, "copies of rows are joined as streams are");
   static constexpr int kTiles = kD <= 128 && !kSplit ? 2 : 1;  // 128-row tiles
   static constexpr int kSoft = kD <= 128 ? 2 : 1;              // softmax warpgroups, issuers
   static constexpr int kRows = kD == 256 ? 64 : 128 * kTiles;
@@ -48,13 +53,18 @@ struct DraftCfg {
   static constexpr int kTile = 128;  // keys a block of the line
   static constexpr int kMinTiles = 4;
   static constexpr int kLift = 7;
-  // Stages of the widened K and V, and the ring of stored bytes: pieces of 128
-  // keys (D = 256: 64).
-  static constexpr int kStagesK = kD == 64 ? 4 : kD == 128 ? 2 : 1, kStagesV = kD == 128 && !kSplit ? 1 : kStagesK;
-  static constexpr int kPieceKeys = kD == 256 ? 64 : 128, kPieceBytes = kPieceKeys * kD, kPieces = 128 / kPieceKeys;
-  static constexpr int kRing = 49152 / kPieceBytes;
-  static constexpr int kKeys = kD <= 128 ? 64 : 128, kParts = 128 / kKeys;  // keys a score buffer
-  static constexpr int kConvWarps = 8;
+  static constexpr int kKeys = 64;   // keys a score buffer: a unit
+  // Widened K and V: stages of 16 KB (D = 256: 32).  Stored bytes: rings of three
+  // pieces of 8 KB, of K and of V.
+  static constexpr int kStageKeys = kD == 64 ? 128 : 64, kStageBytes = kStageKeys * kD * 2;
+  static constexpr int kStagesK = kD == 256 ? 2 : 4, kStagesV = kD == 128 && !kSplit ? 2 : kStagesK;
+  static constexpr int kPieceKeys = 8192 / kD, kPieceBytes = 8192, kRing = 3;
+  static constexpr int kPieces = kStageKeys > kPieceKeys ? kStageKeys / kPieceKeys : 1;  // a stage
+  static_assert(kPieces * kPieceKeys == kStageKeys, "stages are whole pieces");
+  static constexpr int kStageUnits = kStageKeys / kKeys;
+  // Issuers that are done with a stage, one after the other.
+  static constexpr int kReaders = kSplit ? kStageUnits : kTiles;
+  static constexpr int kConvWarps = 8;  // half of them for K, half for V
   static constexpr int kThreads = 128 + 32 * kConvWarps + 128 * kSoft;
   // Registers: at launch 640 threads x 96 or 512 x 128.
   static constexpr int kRegsLaunch = kThreads == 640 ? 96 : 128;
@@ -62,12 +72,23 @@ struct DraftCfg {
   static_assert(kRegsCtrl < kRegsLaunch && kRegsConv < kRegsLaunch && kRegsSoft > kRegsLaunch, "which warps give, which take");
   static_assert(128 * kRegsCtrl + 32 * kConvWarps * kRegsConv + 128 * kSoft * kRegsSoft <= kThreads * kRegsLaunch,
                 "register split exceeds the launch allocation");
-  static constexpr int kUnits = kD / 16;                            // 16-byte units a key
-  static constexpr int kSet = kPieceKeys * kUnits / (32 * kConvWarps);  // a converter's units of a piece: 2 or 4
-  static constexpr int kQBytes = kQRows * kD * 2, kKvBytes = 128 * kD * 2;
-  static constexpr int kOffK = kTiles * kQBytes, kOffV = kOffK + kStagesK * kKvBytes;
-  static constexpr int kOffRing = kOffV + kStagesV * kKvBytes, kOffInfo = kOffRing + 49152;
+  static constexpr int kVecs = kD / 16;                              // 16-byte vectors a key
+  static constexpr int kSet = kPieceBytes / 16 / (16 * kConvWarps);  // a converter's of a piece: 4
+  static constexpr int kQBytes = kQRows * kD * 2;
+  // 32 columns of the copies' outputs, for each stream: over the query rows (the
+  // second's behind the rings where those have too little room).
+  static constexpr int kHand = (128 - 128 / kDup) * 128;
+  static constexpr int kOffK = kTiles * kQBytes, kOffV = kOffK + kStagesK * kStageBytes;
+  static constexpr int kOffRing = kOffV + kStagesV * kStageBytes;
+  static constexpr int kOffHand1 = 2 * kHand <= kQBytes ? kHand : kOffRing + 2 * kRing * kPieceBytes;
+  static constexpr int kOffInfo = kOffRing + 2 * kRing * kPieceBytes + (kOffHand1 > kHand ? kHand : 0);
+  static_assert(kHand <= kQBytes, "room for the copies' outputs");
   static constexpr int kColO = 256;  // S: two buffers of kKeys columns a stream; P over S
+};
+
+template <class C>
+struct DraftF16 : C {
+  static constexpr bool kF16 = true;
 };
 
 constexpr int kDraftAhead = 16;   // blocks of keys that are looked up ahead, in batches of 4
@@ -83,11 +104,11 @@ struct DraftInfo {
   uint32_t line[kDraftWords][128 * C::kSoft];  // the drafts that a softmax thread's row sees
   float2 ml[2][128];                    // (streams) references and sums
   uint64_t q_full[2];                   // 4 softmax warps: query tile written
-  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t full[2][4], empty[2][4];     // [K, V][stage]
   uint64_t s_full[2][2];                // [stream][buffer]: S computed
-  uint64_t p_ready[2];                  // softmax wrote P (and rescaled O)
-  uint64_t o_ready[2];                  // each PV done
-  uint64_t info_full[4], info_empty[4], ring_full[6], ring_empty[6], drain[2];
+  uint64_t p_ready[2][2];               // softmax wrote P (and rescaled O); a warp may be a unit ahead of another
+  uint64_t o_ready[2][2];               // PV done, by buffer: nobody is two phases of one behind
+  uint64_t info_full[4], info_empty[4], ring_full[2][C::kRing], ring_empty[2][C::kRing], drain[2];
   int n[2][2];                          // [stream][piece & 1]: blocks of a piece (0: no more), beside q_full
   uint32_t tmem;
   int abort;
@@ -98,9 +119,9 @@ constexpr int kDraftSmem = 1024 + C::kOffInfo + (int)sizeof(DraftInfo<C>);
 
 // A row's scores to base 2 where one positive factor cannot do it.
 template <class C>
-__device__ __forceinline__ void draft_scale(uint32_t (&x)[C::kKeys], const CacheAttnParams& a, const float4* meta, float rs) {
+__device__ __forceinline__ void draft_scale(uint32_t (&x)[C::kKeys / C::kDup], const CacheAttnParams& a, const float4* meta, float rs) {
 #pragma unroll
-  for (int g = 0; g < C::kKeys / C::kGroup; ++g) {
+  for (int g = 0; g < C::kKeys / C::kDup / C::kGroup; ++g) {
     const float ks = meta[g * (C::kGroup / 16)].x * rs, ci = ks * a.cap_in * 2.8853900817779268f;
 #pragma unroll
     for (int k = C::kGroup * g; k < C::kGroup * (g + 1); ++k) {
@@ -113,12 +134,17 @@ __device__ __forceinline__ void draft_scale(uint32_t (&x)[C::kKeys], const Cache
 }
 
 // Of 32 keys, those that row i sees: the ones from lo to hi - 1, where the drafts
-// begin, and its drafts.
+// begin, and its drafts: bits of `line` where there are up to 32, else of `lines`.
 template <class C>
-__device__ __forceinline__ uint32_t draft_seen(const CacheAttnParams& a, int b, int i, const uint32_t* line, int lo, int hi) {
+__device__ __forceinline__ uint32_t draft_seen(const TreeOf& tree, int i, uint32_t line, const uint32_t* lines, int lo, int hi) {
   const int from = min(max(lo, 0), 32), to = min(max(hi, 0), 32);
   uint32_t seen = from < to ? (0xFFFFFFFFu >> (32 - (to - from))) << from : 0u;
-  if (hi < 32) seen |= a.n <= 32 * kDraftWords ? tree_read_line<128 * C::kSoft>(line, a.n, -hi) : tree_walk(a, b, i, -hi);
+  if (hi < 32) {
+    if (tree.n <= 32)
+      seen |= hi >= 0 ? line << hi : hi > -32 ? line >> -hi : 0u;
+    else
+      seen |= tree.n <= 32 * kDraftWords ? tree_read_line<128 * C::kSoft>(lines, tree.n, -hi) : tree_walk(tree, i, -hi);
+  }
   return seen;
 }
 
@@ -141,21 +167,25 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(
       mbar_init(&info->q_full[i], 4);
       mbar_init(&info->s_full[i][0], 1);
       mbar_init(&info->s_full[i][1], 1);
-      mbar_init(&info->p_ready[i], 4);
-      mbar_init(&info->o_ready[i], 1);
+      mbar_init(&info->p_ready[i][0], 4);
+      mbar_init(&info->p_ready[i][1], 4);
+      mbar_init(&info->o_ready[i][0], 1);
+      mbar_init(&info->o_ready[i][1], 1);
       mbar_init(&info->drain[i], 1);
     }
+    for (int kv = 0; kv < 2; ++kv) {
+      for (int i = 0; i < 4; ++i) {
+        mbar_init(&info->full[kv][i], C::kConvWarps / 2);
+        mbar_init(&info->empty[kv][i], C::kReaders);
+      }
+      for (int i = 0; i < C::kRing; ++i) {
+        mbar_init(&info->ring_full[kv][i], 1);
+        mbar_init(&info->ring_empty[kv][i], C::kConvWarps / 2);
+      }
+    }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&info->k_full[i], C::kConvWarps);
-      mbar_init(&info->v_full[i], C::kConvWarps);
-      mbar_init(&info->k_empty[i], C::kTiles);
-      mbar_init(&info->v_empty[i], C::kTiles);
       mbar_init(&info->info_full[i], 1);
       mbar_init(&info->info_empty[i], C::kSoft);
-    }
-    for (int i = 0; i < C::kRing; ++i) {
-      mbar_init(&info->ring_full[i], 1);
-      mbar_init(&info->ring_empty[i], C::kConvWarps);
     }
     info->abort = 0;
     fence_barrier_init();
@@ -172,9 +202,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(
   const uint32_t tmem = info->tmem;
   volatile int* abort = &info->abort;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return prompt_warp_wait(bar, parity, abort, a); };
-  // Block nb of this thread block's has stages nb % kStagesK and nb % kStagesV;
-  // stream t takes every block, or those with nb % 2 == t.
-  constexpr int kStep = C::kSplit ? 2 : 1;
+  // Units: halves of this thread block's blocks of keys.  Stream t takes unit t of
+  // every block, or all.
+  constexpr int kUnitStep = C::kSplit ? 2 : 1;
 
   if (warp < 4) {
     // ============================================================ control
@@ -186,31 +216,38 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(
       constexpr uint32_t idPV = make_idesc_fmt(kFmtF16, 128, C::kD, false, true);
       const uint64_t dQ = make_sdesc_sw128(smem_u32(smem + (C::kSplit ? 0 : t * C::kQBytes)), 16, 1024);
       const uint64_t dK = make_sdesc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
-      const uint64_t dV = make_sdesc_sw128(smem_u32(smem + C::kOffV), 128 * 128, 1024);
+      const uint64_t dV = make_sdesc_sw128(smem_u32(smem + C::kOffV), C::kStageKeys * 128, 1024);
       const uint32_t lead = elect_lead();
-      auto issue_S = [&](int buf, int stage, int part) {
-        const uint64_t k0 = dK + ((stage * C::kKvBytes + part * (C::kKeys * 128)) >> 4);
+      // Unit u's bytes in its stage; and is it the last unit that this stream takes of it?
+      auto at_stage = [](int u, int stages) {
+        return (uint32_t)((u / C::kStageUnits) & (stages - 1)) * C::kStageBytes + (u % C::kStageUnits) * (C::kKeys * 128);
+      };
+      constexpr int kLast = C::kStageUnits - 1;
+      auto leaves = [&](int u) { return C::kSplit || u % C::kStageUnits == kLast; };
+      auto issue_S = [&](int buf, int u) {
+        const uint64_t k0 = dK + (at_stage(u, C::kStagesK) >> 4);
         const uint32_t dst = tmem + t * 128 + buf * C::kKeys;
 #pragma unroll
-        for (int kk = 0; kk < C::kD / 16; ++kk) {
+        for (int kk = 0; kk < C::kD / 16; ++kk)
           mma_f16_ss_by(lead, dst, dQ + (kk / 4) * ((C::kQRows * 128) >> 4) + (kk % 4) * 2,
-                        k0 + (kk / 4) * ((128 * 128) >> 4) + (kk % 4) * 2, idS, kk > 0 ? 1u : 0u);
-        }
+                        k0 + (kk / 4) * ((C::kStageKeys * 128) >> 4) + (kk % 4) * 2, idS, kk > 0 ? 1u : 0u);
         mma_commit_by(lead, &info->s_full[t][buf]);
-        if (part == C::kParts - 1) mma_commit_by(lead, &info->k_empty[stage]);
+        if (leaves(u)) mma_commit_by(lead, &info->empty[0][(u / C::kStageUnits) & (C::kStagesK - 1)]);
       };
-      auto issue_PV = [&](int buf, int stage, int part, bool first) {
-        const uint64_t v0 = dV + ((stage * C::kKvBytes + part * (C::kKeys * 128)) >> 4);
+      auto issue_PV = [&](int buf, int u, bool first) {
+        const uint64_t v0 = dV + (at_stage(u, C::kStagesV) >> 4);
         const uint32_t src = tmem + t * 128 + buf * C::kKeys, dst = tmem + C::kColO + t * C::kD;
 #pragma unroll
         for (int kk = 0; kk < C::kKeys / 16; ++kk)
           mma_f16_ts_by(lead, dst, src + kk * 8, v0 + ((kk * 16 * 128) >> 4), idPV, first && kk == 0 ? 0u : 1u);
-        mma_commit_by(lead, &info->o_ready[t]);
-        if (part == C::kParts - 1) mma_commit_by(lead, &info->v_empty[stage]);
+        mma_commit_by(lead, &info->o_ready[t][buf]);
+        if (leaves(u)) mma_commit_by(lead, &info->empty[1][(u / C::kStageUnits) & (C::kStagesV - 1)]);
       };
-      auto stage_of = [](int nb) { return nb & (C::kStagesK - 1); };
-      auto par_of = [](int nb) { return (uint32_t)(nb / C::kStagesK) & 1u; };
-      int nth = 0, before = 0;  // this stream's score buffers; all blocks of earlier pieces
+      auto full = [&](int kv, int stages, int u) {
+        const int nth = u / C::kStageUnits;
+        return wait(&info->full[kv][nth & (stages - 1)], (uint32_t)(nth / stages) & 1u);
+      };
+      int nth = 0, before = 0;  // this stream's units; all blocks of earlier pieces
       bool ok = true;
 #pragma unroll 1
       for (int pieces = 0; ok; ++pieces) {
@@ -219,35 +256,26 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(
         if (!ok) break;
         const int n = info->n[C::kSplit ? 0 : t][pieces & 1];
         if (n == 0) break;
-        const int begin = C::kSplit && (before & 1) != t ? before + 1 : before, end = before + n;
-        before = end;
-        if (begin >= end) continue;
-        ok = wait(&info->k_full[stage_of(begin)], par_of(begin));
+        const int begin = 2 * before + (C::kSplit ? t : 0), end = 2 * (before + n);
+        before += n;
+        ok = full(0, C::kStagesK, begin);
         if (!ok) break;
         tc_fence_after();
-        issue_S(nth & 1, stage_of(begin), 0);
+        issue_S(nth & 1, begin);
 #pragma unroll 1
-        for (int nb = begin; nb < end && ok; nb += kStep) {
-          const int stage = stage_of(nb), next = nb + kStep, stage_v = nb & (C::kStagesV - 1);
-#pragma unroll
-          for (int part = 0; part < C::kParts; ++part) {
-            // the next scores go before this PV
-            if (part + 1 < C::kParts) {
-              issue_S((nth + 1) & 1, stage, part + 1);
-            } else if (next < end) {
-              ok = wait(&info->k_full[stage_of(next)], par_of(next));
-              if (!ok) break;
-              tc_fence_after();
-              issue_S((nth + 1) & 1, stage_of(next), 0);
-            }
-            ok = (part > 0 || wait(&info->v_full[stage_v], (uint32_t)(nb / C::kStagesV) & 1u)) && wait(&info->p_ready[t], (uint32_t)nth & 1u);
+        for (int u = begin; u < end; u += kUnitStep, ++nth) {
+          if (u + kUnitStep < end) {  // the next scores go before this PV
+            ok = full(0, C::kStagesK, u + kUnitStep);
             if (!ok) break;
             tc_fence_after();
-            issue_PV(nth & 1, stage_v, part, nb == begin && part == 0);
-            ++nth;
+            issue_S((nth + 1) & 1, u + kUnitStep);
           }
+          ok = full(1, C::kStagesV, u) && wait(&info->p_ready[t][nth & 1], (uint32_t)(nth >> 1) & 1u);
           if (!ok) break;
-          if ((nb & 3) == (C::kSplit ? 2 + t : 3)) mma_commit_by(lead, &info->info_empty[(nb >> 2) & 3]);
+          tc_fence_after();
+          issue_PV(nth & 1, u, u == begin);
+          // (the last unit that this stream takes of four blocks that were looked up together)
+          if ((u & 7) == (C::kSplit ? 6 + t : 7)) mma_commit_by(lead, &info->info_empty[(u >> 3) & 3]);
         }
       }
       // Every MMA issued here has completed before the block lets go of its
@@ -312,22 +340,31 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(
       }
     } else if (warp == 3) {
       // ---------------------------------------------------------- stored bytes
-      // A lane a 16-key group; one of those that share a box of the tensor map
-      // copies it (its block, if any of them has one).
-      constexpr int kGroupsHere = C::kPieceKeys / 16;
-      const int rows = min(c.page, C::kPieceKeys), share = rows / 16;
-      int slot = 0, issued = 0;
-      uint32_t phase = 0;
+      // Both rings, whichever has room.  A lane a 16-key group; one of those that
+      // share a box of the tensor map copies it (its block, if any of them has one).
+      constexpr int kGroupsHere = C::kPieceKeys / 16, kPiecesBlock = 128 / C::kPieceKeys;
+      const int rows = min(c.page, C::kPieceKeys), share = rows / 16, pieces = kPiecesBlock * (t1 - t0);
+      int done[2] = {0, 0}, slot[2] = {0, 0};  // pieces of K, V
+      uint32_t phase[2] = {0, 0};
+      int known = 0;                           // blocks that are looked up
       bool ok = true;
+      long long begin = clock64_now();         // since when nothing has moved
 #pragma unroll 1
-      for (int nb = 0; nb < t1 - t0 && ok; ++nb) {
-        if ((nb & 3) == 0) ok = wait(&info->info_full[(nb >> 2) & 3], (uint32_t)(nb >> 4) & 1u);
-        if (!ok) break;
-        const int at_info = nb & (kDraftAhead - 1), tok = info->tok[at_info];
-#pragma unroll 1
-        for (int i = 0; i < 2 * C::kPieces; ++i) {
-          const bool is_v = i >= C::kPieces;
-          const int g0 = (is_v ? i - C::kPieces : i) * kGroupsHere, g = g0 + lane % kGroupsHere;
+      while (ok && (done[0] < pieces || done[1] < pieces)) {
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          if (done[kv] == pieces) continue;
+          const int nb = done[kv] / kPiecesBlock;
+          if (nb == known) {
+            ok = wait(&info->info_full[(nb >> 2) & 3], (uint32_t)(nb >> 4) & 1u);
+            if (!ok) break;
+            known += 4;
+          }
+          uint64_t* const bar = &info->ring_full[kv][slot[kv]];
+          if (done[kv] >= C::kRing && !__all_sync(0xFFFFFFFFu, mbar_test(&info->ring_empty[kv][slot[kv]], phase[kv] ^ 1u)))
+            continue;
+          const int at_info = nb & (kDraftAhead - 1), tok = info->tok[at_info];
+          const int g = done[kv] % kPiecesBlock * kGroupsHere + lane % kGroupsHere;
           const int2 from = info->from[at_info][g];
           int blk = lane < kGroupsHere ? from.x : -1;
 #pragma unroll
@@ -337,91 +374,89 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(
           }
           const bool box = lane < kGroupsHere && (lane & (share - 1)) == 0 && blk >= 0;
           const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, box));
-          if (issued >= C::kRing) ok = wait(&info->ring_empty[slot], phase ^ 1u);
-          if (!ok) break;
-          uint64_t* const bar = &info->ring_full[slot];
           if (lane == 0) {
             if (boxes > 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * rows * C::kD));
             else mbar_arrive(bar);
           }
           __syncwarp();
           if (box)
-            tma_load_4d(smem + C::kOffRing + slot * C::kPieceBytes + lane * 16 * C::kD, is_v ? &tv : &tk, bar, 0,
+            tma_load_4d(smem + C::kOffRing + (kv * C::kRing + slot[kv]) * C::kPieceBytes + lane * 16 * C::kD, kv ? &tv : &tk, bar, 0,
                         (tok + 16 * g) & (c.page - 1), from.y, blk);
           __syncwarp();
-          ++issued;
-          if (++slot == C::kRing) slot = 0, phase ^= 1u;
+          ++done[kv];
+          if (++slot[kv] == C::kRing) slot[kv] = 0, phase[kv] ^= 1u;
+          begin = clock64_now();
+        }
+        // (bounded as the other waits are)
+        if (ok && __any_sync(0xFFFFFFFFu, *abort || clock64_now() - begin > a.timeout_cycles)) {
+          if (lane == 0 && !*abort) {
+            *abort = 1;
+            atomicOr(c.status, kStatusTimeout);
+          }
+          ok = false;
         }
       }
       // Copies land before the block ends (also where nobody looked at them; bounded).
-      const long long begin = clock64_now();
-      for (int k = max(0, issued - C::kRing); k < issued; ++k)
-        while (!mbar_try_wait(&info->ring_full[k % C::kRing], (uint32_t)(k / C::kRing) & 1u) &&
-               clock64_now() - begin < kDecDrainCycles) {
-        }
+      begin = clock64_now();
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv)
+        for (int k = max(0, done[kv] - C::kRing); k < done[kv]; ++k)
+          while (!mbar_try_wait(&info->ring_full[kv][k % C::kRing], (uint32_t)(k / C::kRing) & 1u) &&
+                 clock64_now() - begin < kDecDrainCycles) {
+          }
     }
   } else if (warp < 4 + C::kConvWarps) {
     // ============================================================ converters
     regs_dec<C::kRegsConv>();
-    const int cw = warp - 4;
-    // Lane bits 0-1: unit, 2: key, then units, then keys: eight neighbours
+    const int kv = (warp - 4) / (C::kConvWarps / 2), cw = (warp - 4) % (C::kConvWarps / 2);
+    // Lane bits 0-1: vector, 2: key, then vectors, then keys: eight neighbours
     // write eight different 16-byte columns of the swizzled rows.
-    constexpr int kHigh = C::kUnits / 4;
-    constexpr int kKeysWarp = 32 / C::kUnits, kKeysStep = kKeysWarp * C::kConvWarps;  // 64, 32, 16
-    const int unit = (lane & 3) + 4 * ((lane >> 3) % kHigh);
+    constexpr int kHigh = C::kVecs / 4;
+    constexpr int kKeysWarp = 32 / C::kVecs, kKeysStep = kKeysWarp * C::kConvWarps / 2;  // 32, 16, 8
+    static_assert(kKeysStep * C::kSet == C::kPieceKeys, "a piece is a set");
+    const int vec = (lane & 3) + 4 * ((lane >> 3) % kHigh);
     const int key0 = cw * kKeysWarp + ((lane >> 2) & 1) + 2 * ((lane >> 3) / kHigh);
-    const int g0 = key0 >> 4, r = key0 & 15;  // its keys of a piece are key r of groups g0, g0 + kKeysStep / 16, ..
-    uint8_t* const to = smem + C::kOffK + (uint32_t)(unit / 4) * (128 * 128) + key0 * 128;
-    const uint32_t lo16 = (((unit % 4) * 2) ^ (key0 & 7)) << 4, hi16 = (((unit % 4) * 2 + 1) ^ (key0 & 7)) << 4;
-    const uint32_t from = smem_u32(smem + C::kOffRing) + key0 * C::kD + unit * 16;
+    uint8_t* const to = smem + (kv ? C::kOffV : C::kOffK) + (uint32_t)(vec / 4) * (C::kStageKeys * 128) + key0 * 128;
+    const uint32_t lo16 = (((vec % 4) * 2) ^ (key0 & 7)) << 4, hi16 = (((vec % 4) * 2 + 1) ^ (key0 & 7)) << 4;
+    const uint32_t from = smem_u32(smem + C::kOffRing + kv * C::kRing * C::kPieceBytes) + key0 * C::kD + vec * 16;
+    const int stages = kv ? C::kStagesV : C::kStagesK, pieces = 128 / C::kPieceKeys * (t1 - t0);
     int slot = 0;
     uint32_t phase = 0;
-    bool ok = true;
 #pragma unroll 1
-    for (int nb = 0; nb < t1 - t0 && ok; ++nb) {
-      const int at_info = nb & (kDraftAhead - 1);
+    for (int k = 0; k < pieces; ++k) {
+      const int nth = k / C::kPieces, part = k % C::kPieces, stage = nth & (stages - 1);  // of the stage
+      if (!wait(&info->ring_full[kv][slot], phase)) break;
+      uint4 x[C::kSet];
 #pragma unroll
-      for (int i = 0; i < 2 * C::kPieces; ++i) {
-        const bool is_v = i >= C::kPieces;
-        const int piece = is_v ? i - C::kPieces : i;
-        ok = wait(&info->ring_full[slot], phase);
-        if (!ok) break;
-        uint4 x[C::kSet];
+      for (int u = 0; u < C::kSet; ++u) x[u] = lds128(from + slot * C::kPieceBytes + u * (kKeysStep * C::kD));
+      const int at_info = (k * C::kPieceKeys / 128) & (kDraftAhead - 1);
+      if (!((info->all[at_info] >> kv) & 1u)) {  // where nobody sees them or nothing is stored: zeros
 #pragma unroll
-        for (int u = 0; u < C::kSet; ++u) x[u] = lds128(from + slot * C::kPieceBytes + u * (kKeysStep * C::kD));
-        if (!(info->all[at_info] & (is_v ? 2u : 1u))) {  // where nobody sees them or nothing is stored: zeros
-          const int* range = info->range[at_info] + piece * (C::kPieceKeys / 16) + g0;
-#pragma unroll
-          for (int u = 0; u < C::kSet; ++u) {
-            const int keys = range[u * (kKeysStep / 16)] >> (is_v ? 16 : 0);
-            if (!(r >= (keys & 255) && r < ((keys >> 8) & 255))) x[u] = make_uint4(0, 0, 0, 0);
-          }
+        for (int u = 0; u < C::kSet; ++u) {
+          const int key = (k * C::kPieceKeys) % 128 + key0 + u * kKeysStep, keys = info->range[at_info][key >> 4] >> (16 * kv);
+          if (!((key & 15) >= (keys & 255) && (key & 15) < ((keys >> 8) & 255))) x[u] = make_uint4(0, 0, 0, 0);
         }
-        constexpr int kStages[2] = {C::kStagesK, C::kStagesV};
-        const int stages = kStages[is_v], stage = nb & (stages - 1);
-        if (piece == 0 && nb >= stages) {
-          ok = wait(is_v ? &info->v_empty[stage] : &info->k_empty[stage], (uint32_t)(nb / stages + 1) & 1u);
-          if (!ok) break;
-        }
-        uint8_t* const row = to + (is_v ? C::kOffV - C::kOffK : 0) + stage * C::kKvBytes + piece * (C::kPieceKeys * 128);
-#pragma unroll
-        for (int u = 0; u < C::kSet; ++u) {  // (a step of kKeysStep keys leaves the swizzle as it is)
-          uint4 lo, hi;
-          widen16<C::kKind>(x[u], lo, hi);
-          *reinterpret_cast<uint4*>(row + u * (kKeysStep * 128) + lo16) = lo;
-          *reinterpret_cast<uint4*>(row + u * (kKeysStep * 128) + hi16) = hi;
-        }
-        if (piece == C::kPieces - 1) fence_proxy_async_smem();
-        __syncwarp();
-        // (The slot is free once what was read has been used: given back right behind
-        // the loads, it was filled again before a warp that waited for its stage
-        // had its bytes.)
-        if (lane == 0) {
-          if (piece == C::kPieces - 1) mbar_arrive(is_v ? &info->v_full[stage] : &info->k_full[stage]);
-          mbar_arrive(&info->ring_empty[slot]);
-        }
-        if (++slot == C::kRing) slot = 0, phase ^= 1u;
       }
+      if (part == 0 && nth >= stages && !wait(&info->empty[kv][stage], (uint32_t)(nth / stages + 1) & 1u)) break;
+      uint8_t* const row = to + stage * C::kStageBytes + part * (C::kPieceKeys * 128);
+#pragma unroll
+      for (int u = 0; u < C::kSet; ++u) {  // (a step of kKeysStep keys leaves the swizzle as it is)
+        uint4 lo, hi;
+        if (p.kind == kKindE4m3) widen16<kKindE4m3>(x[u], lo, hi);
+        else widen16<kKindInt8>(x[u], lo, hi);
+        *reinterpret_cast<uint4*>(row + u * (kKeysStep * 128) + lo16) = lo;
+        *reinterpret_cast<uint4*>(row + u * (kKeysStep * 128) + hi16) = hi;
+      }
+      if (part == C::kPieces - 1) fence_proxy_async_smem();
+      __syncwarp();
+      // (The slot is free once what was read has been used: given back right behind
+      // the loads, it was filled again before a warp that waited for its stage
+      // had its bytes.)
+      if (lane == 0) {
+        if (part == C::kPieces - 1) mbar_arrive(&info->full[kv][stage]);
+        mbar_arrive(&info->ring_empty[kv][slot]);
+      }
+      if (++slot == C::kRing) slot = 0, phase ^= 1u;
     }
   } else {
     // ============================================================ softmax
@@ -430,23 +465,31 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(
     const int tl = tid - (C::kThreads - 128 * C::kSoft) - 128 * t;  // row of the tile = TMEM lane
     const int row_tile = C::kSplit ? 0 : t;
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tO = tmem + lane_addr + C::kColO + t * C::kD;
+    const uint32_t tO = tmem + lane_addr + C::kColO + t * C::kD;  // the stream's output
     uint8_t* q_tile = smem + row_tile * C::kQBytes;
-    constexpr int kGroups = C::kKeys / C::kGroup;  // groups a score buffer
-    int nth = 0, before = 0, pieces = 0;  // the stream's score buffers, all blocks, and pieces before this one
+    constexpr int kMine = C::kKeys / C::kDup, kGroups = kMine / C::kGroup;  // keys of a score buffer a thread weighs; groups
+    constexpr int kCopy = 128 / C::kDup;                                    // rows of a copy
+    const int copy = C::kDup > 1 ? tl / kCopy : 0;                          // (a warp's)
+    int nth = 0, before = 0, pieces = 0;  // the stream's units, all blocks, and pieces before this one
     bool ok = true;
+    // The product of a unit's weights has landed.
+    auto landed = [&](int unit) { return wait(&info->o_ready[t][unit & 1], (uint32_t)(unit >> 1) & 1u); };
 #pragma unroll 1
     for (int pos = t0; pos < t1; ++pieces) {
       const int tiles = dec_tiles<C>(p, at.seq, at.rg), n = min(t1, at.seg0 + tiles) - pos;
       const int2 span = dec_group_span<C>(p, at.seq, at.rg);
       const int first = span.x / 128 + pos - at.seg0;
       const bool whole = n == tiles, head_cut = pos > at.seg0;
-      const int row = at.rg * C::kRows + row_tile * 128 + tl, i = row / a.group, head = at.h * a.group + row % a.group;
+      const int row = C::kDup > 1 ? tl & (kCopy - 1) : at.rg * C::kRows + row_tile * 128 + tl, i = row / a.group, head = at.h * a.group + row % a.group;
       const bool real = tl < C::kQRows && row < p.rows;
       const int base = at.seq.len - at.seq.nq;  // the first draft's slot
       const bool some = real && i < at.seq.nq && base + i >= 0;
-      // Does any row of this warp's count?  (Rows are those of whole tiles.)
-      const bool work = __any_sync(0xFFFFFFFFu, real);
+      // Does any row of this warp's count?  (With copies, all warps go on together.)
+      const bool work = C::kDup > 1 || __any_sync(0xFFFFFFFFu, real);
+      // Up to 32 nodes' parents are on their way with the rows, a lane a node.
+      const TreeOf tree = tree_of(a, at.b);
+      int up = -1;
+      if (tree.n <= 32 && lane < at.seq.nq) up = tree_parent(tree, lane);
       // The warp's query rows, kLanes lanes a row, all loads under way at once:
       // the row's largest entry, then its f16 form.  (S of the piece before is
       // done: the tile may be written.  Both streams load, the first writes.)
@@ -468,7 +511,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(
           }
 #pragma unroll
           for (int u = 0; u < kPass; ++u) {
-            if constexpr (!C::kF16) {
+            if (!p.f16) {
               uint32_t* x = &w[u].x;
               float top = 0.0f, up, down;
 #pragma unroll
@@ -495,131 +538,145 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(
         if ((warp & 3) == 0) info->n[t][pieces & 1] = n;
         mbar_arrive(&info->q_full[t]);
       }
-      int lo_row = 0;  // the first token before the drafts that the row sees
-      if (some && a.window > 0) lo_row = tree_first(a, base, tree_depth(a, at.b, i));
-      uint32_t* const line = &info->line[0][t * 128 + tl];
-      if (some && a.n <= 32 * kDraftWords && (first + n) * 128 > base) tree_write_line<128 * C::kSoft>(a, at.b, i, line);
+      // What the row sees: tokens from lo_row on before the drafts, and its line.
+      int lo_row = 0;
+      uint32_t line = 0u;
+      uint32_t* const lines = &info->line[0][t * 128 + tl];
+      if (tree.n <= 32) {
+        line = __shfl_sync(0xFFFFFFFFu, tree_lines(up), i & 31);
+        if (some) lo_row = tree_window(tree, base, line);
+      } else if (some) {
+        if (tree.window > 0) lo_row = tree_first(tree, base, tree_depth(tree, i));
+        if (tree.n <= 32 * kDraftWords && (first + n) * 128 > base) tree_write_line<128 * C::kSoft>(tree, i, lines);
+      }
       __syncwarp();
 
       const float f_row = rs * a.scale_log2;
       float m = -INFINITY, l = 0.0f;  // m: the reference
-      int done = 0;                   // score buffers of this piece
+      bool fresh = true;              // no unit of this piece yet
 #pragma unroll 1
-      for (int nb = C::kSplit && (before & 1) != t ? before + 1 : before; nb < before + n && ok; nb += kStep) {
-#pragma unroll 1
-        for (int part_at = 0; part_at < C::kParts; ++part_at, ++nth, ++done) {
-          const int buf = nth & 1;
-          ok = wait(&info->s_full[t][buf], (uint32_t)(nth >> 1) & 1u);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t tS = tmem + lane_addr + t * 128 + buf * C::kKeys;
-          const float4* meta = info->meta[nb & (kDraftAhead - 1)] + part_at * (C::kKeys / 16);
-          const int key0 = (first + nb - before) * 128 + part_at * C::kKeys, lo = lo_row - key0, hi = base - key0;
-          float corr = 1.0f;
-          bool moved = false;
-          if (work) {
-            uint32_t x[C::kKeys];  // the row's scores (fp32 bits)
+      for (int u = 2 * before + (C::kSplit ? t : 0); u < 2 * (before + n); u += kUnitStep, ++nth, fresh = false) {
+        const int buf = nth & 1, nb = u >> 1, part_at = u & 1;
+        ok = wait(&info->s_full[t][buf], (uint32_t)(nth >> 1) & 1u);
+        if (!ok) break;
+        if (nth > 1 && !(ok = landed(nth - 2))) break;
+        tc_fence_after();
+        const uint32_t tS = tmem + lane_addr + t * 128 + buf * C::kKeys;
+        const float4* meta = info->meta[nb & (kDraftAhead - 1)] + (part_at * C::kKeys + copy * kMine) / 16;
+        const int key0 = (first + nb - before) * 128 + part_at * C::kKeys + copy * kMine, lo = lo_row - key0, hi = base - key0;
+        float corr = 1.0f;
+        bool moved = false;
+        if (work) {
+          uint32_t x[kMine];  // the row's scores (fp32 bits)
+          if constexpr (kMine == 16) {
+            tmem_ld16(tS + copy * kMine, x);
+          } else {
 #pragma unroll
-            for (int cc = 0; cc < C::kKeys / 32; ++cc)
-              tmem_ld32(tS + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[cc * 32]));
-            tmem_wait_ld();
-            reg_fence(x);
-            if constexpr (!C::kRaw) draft_scale<C>(x, a, meta, rs);
-            if (lo > 0 || hi < C::kKeys) {
-              uint32_t seen[C::kKeys / 32] = {};
-              if (some) {
+            for (int cc = 0; cc < kMine / 32; ++cc)
+              tmem_ld32(tS + copy * kMine + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[cc * 32]));
+          }
+          tmem_wait_ld();
+          reg_fence(x);
+          if constexpr (!C::kRaw) draft_scale<C>(x, a, meta, rs);
+          if (lo > 0 || hi < kMine) {
+            uint32_t seen[(kMine + 31) / 32] = {};
+            if (some) {
 #pragma unroll
-                for (int w = 0; w < C::kKeys / 32; ++w) seen[w] = draft_seen<C>(a, at.b, i, line, lo - 32 * w, hi - 32 * w);
-              }
-#pragma unroll
-              for (int k = 0; k < C::kKeys; ++k)
-                if (!((seen[k / 32] >> (k & 31)) & 1u)) x[k] = 0xFF800000u;
+              for (int w = 0; w < (kMine + 31) / 32; ++w) seen[w] = draft_seen<C>(tree, i, line, lines, lo - 32 * w, hi - 32 * w);
             }
-            // Group by group: a raw score times f plus y is the score's weight in
-            // base 2 (s + log2 vs); y = -inf where nothing is stored.
-            float f[kGroups], y[kGroups], inv_vs[kGroups], mx, part;
+#pragma unroll
+            for (int k = 0; k < kMine; ++k)
+              if (!((seen[k / 32] >> (k & 31)) & 1u)) x[k] = 0xFF800000u;
+          }
+          // Group by group: a raw score times f plus y is the score's weight in
+          // base 2 (s + log2 vs); y = -inf where nothing is stored.
+          float f[kGroups], y[kGroups], inv_vs[kGroups], mx, part;
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) {
+            const float4 q = meta[g * (C::kGroup / 16)];
+            f[g] = C::kRaw ? fmaxf(q.x * f_row, 1e-37f) : 1.0f;  // (not 0: a hidden score stays -inf)
+            y[g] = q.w == 0.0f ? -INFINITY : q.y;
+            inv_vs[g] = q.z;
+          }
+          // The weights against the maximum so far, and the new maximum beside
+          // them: neither waits for the other.  Where a row's maximum has grown
+          // too far for that, once more against the new one.
+#pragma unroll 1
+          while (true) {
+            const float from = m == -INFINITY ? 0.0f : m;
+            mx = -INFINITY, part = 0.0f;
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) {
-              const float4 q = meta[g * (C::kGroup / 16)];
-              f[g] = C::kRaw ? fmaxf(q.x * f_row, 1e-37f) : 1.0f;  // (not 0: a hidden score stays -inf)
-              y[g] = q.w == 0.0f ? -INFINITY : q.y;
-              inv_vs[g] = q.z;
-            }
-            // The weights against the maximum so far, and the new maximum beside
-            // them: neither waits for the other.  Where a row's maximum has grown
-            // too far for that, once more against the new one.
-#pragma unroll 1
-            while (true) {
-              const float from = m == -INFINITY ? 0.0f : m;
-              mx = -INFINITY, part = 0.0f;
+              const float off = y[g] - from;
+              float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-              for (int g = 0; g < kGroups; ++g) {
-                const float off = y[g] - from;
-                float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+              for (int c0 = 0; c0 < C::kGroup; c0 += 16) {
+                uint32_t pk[8];
 #pragma unroll
-                for (int c0 = 0; c0 < C::kGroup; c0 += 16) {
-                  uint32_t pk[8];
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) {
-                    const int k = C::kGroup * g + c0 + 2 * e;
-                    float x0 = __uint_as_float(x[k]), x1 = __uint_as_float(x[k + 1]);
-                    v[e & 3] = fmax3(v[e & 3], x0, x1);
-                    ffma2(x0, x1, x0, x1, f[g], f[g], off, off);
-                    x0 = ex2(x0), x1 = ex2(x1);
-                    fadd2(sum[(e & 1) * 2], sum[(e & 1) * 2 + 1], x0, x1);
-                    pk[e] = pack_f16x2(x0, x1);
-                  }
-                  tmem_st8(tS + (C::kGroup * g + c0) / 2, pk);
+                for (int e = 0; e < 8; ++e) {
+                  const int k = C::kGroup * g + c0 + 2 * e;
+                  float x0 = __uint_as_float(x[k]), x1 = __uint_as_float(x[k + 1]);
+                  v[e & 3] = fmax3(v[e & 3], x0, x1);
+                  ffma2(x0, x1, x0, x1, f[g], f[g], off, off);
+                  x0 = ex2(x0), x1 = ex2(x1);
+                  fadd2(sum[(e & 1) * 2], sum[(e & 1) * 2 + 1], x0, x1);
+                  pk[e] = pack_f16x2(x0, x1);
                 }
-                mx = fmaxf(mx, fmaf(fmax3(fmaxf(v[0], v[1]), v[2], v[3]), f[g], y[g]));
-                part = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), inv_vs[g], part);
+                tmem_st8(tS + (copy * kMine + C::kGroup * g + c0) / 2, pk);
               }
-              const bool resc = dec_grown(mx, m);  // (not twice: from its own reference a maximum is no further than the lift)
-              if (!__any_sync(0xFFFFFFFFu, resc)) break;
-              moved = true;
-              if (resc) {
-                const float r = dec_reference<C>(mx);
-                corr = ex2(m - r);  // 0 when m = -inf
-                m = r;
-              }
+              mx = fmaxf(mx, fmaf(fmax3(fmaxf(v[0], v[1]), v[2], v[3]), f[g], y[g]));
+              part = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), inv_vs[g], part);
             }
-            l = fmaf(l, corr, part);
-          }
-          if (done > 0) {  // the PV before has landed (each phase is consumed, in order)
-            ok = wait(&info->o_ready[t], (uint32_t)(nth - 1) & 1u);
-            if (!ok) break;
-          }
-          if (done > 0 && moved) {
-            tc_fence_after();
-#pragma unroll
-            for (int cc = 0; cc < C::kD / 32; ++cc) {
-              uint32_t rr[32];
-              tmem_ld32(tO + cc * 32, rr);
-              tmem_wait_ld();
-              reg_fence(rr);
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                float o0, o1;
-                fmul2(o0, o1, __uint_as_float(rr[e]), __uint_as_float(rr[e + 1]), corr, corr);
-                rr[e] = __float_as_uint(o0);
-                rr[e + 1] = __float_as_uint(o1);
-              }
-              tmem_st32(tO + cc * 32, rr);
+            const bool resc = dec_grown(mx, m);  // (not twice: from its own reference a maximum is no further than the lift)
+            if (!__any_sync(0xFFFFFFFFu, resc)) break;
+            moved = true;
+            if (resc) {
+              const float r = dec_reference<C>(mx);
+              corr = ex2(m - r);  // 0 when m = -inf
+              m = r;
             }
           }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&info->p_ready[t]);
+          l = fmaf(l, corr, part);
+          if constexpr (C::kDup > 1) {  // the other copies' keys weigh nothing here
+            const uint32_t none[8] = {};
+#pragma unroll
+            for (int q = 1; q < C::kDup; ++q)
+#pragma unroll
+              for (int c0 = 0; c0 < kMine / 2; c0 += 8) tmem_st8(tS + ((copy + q) % C::kDup) * (kMine / 2) + c0, none);
+          }
         }
+        // (The product that read this buffer's weights has landed: its scores were
+        // issued behind that.  Outputs that are to be rescaled have one more to come.)
+        if (!fresh && moved) {
+          if (!(ok = landed(nth - 1))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int cc = 0; cc < C::kD / 32; ++cc) {
+            uint32_t rr[32];
+            tmem_ld32(tO + cc * 32, rr);
+            tmem_wait_ld();
+            reg_fence(rr);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float o0, o1;
+              fmul2(o0, o1, __uint_as_float(rr[e]), __uint_as_float(rr[e + 1]), corr, corr);
+              rr[e] = __float_as_uint(o0);
+              rr[e + 1] = __float_as_uint(o1);
+            }
+            tmem_st32(tO + cc * 32, rr);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&info->p_ready[t][buf]);
       }
-      if (ok && done > 0) ok = wait(&info->o_ready[t], (uint32_t)(nth - 1) & 1u);
+      if (ok) ok = landed(nth - 1);
       // (a NaN row stays one; one that is none, or that sees nothing, has no sum)
       if (!some) l = 0.0f;
-      const long long slot = (long long)(2 * blockIdx.x + (head_cut ? 0 : 1)) * C::kRows + row_tile * 128 + tl;
+      const long long slot = (long long)(2 * blockIdx.x + (head_cut ? 0 : 1)) * C::kRows + (C::kDup > 1 ? row : row_tile * 128 + tl);
       uint8_t* dst = static_cast<uint8_t*>(a.o) + (at.b * a.os[0] + head * a.os[1] + i * a.os[2]) * 2;
-      float f0 = 1.0f, f1 = 0.0f;  // of this stream's output, and the other's
-      bool mine = true, other = false;
+      float f0 = 1.0f, f1 = 0.0f;  // of the two streams' outputs
       if constexpr (C::kSplit) {
         info->ml[t][tl] = make_float2(m, l);
         tc_fence_before();
@@ -627,12 +684,21 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(
           ok = false;
           break;
         }
-        const float2 ml = info->ml[t ^ 1][tl];
-        mine = done > 0, other = n > 1 || !mine;
-        const float top = fmaxf(m, ml.x), z = top == -INFINITY ? 0.0f : top;
-        f0 = ex2(m - z), f1 = ex2(ml.x - z);
-        l = t == 0 ? fmaf(l, f0, ml.y * f1) : fmaf(ml.y, f1, l * f0);  // (alike in both)
-        m = top;
+        // The row's sum over its copies and streams, always in the same order.
+        float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int q = 0; q < C::kDup; ++q)
+          top = fmax3(top, info->ml[0][q * kCopy + (tl & (kCopy - 1))].x, info->ml[1][q * kCopy + (tl & (kCopy - 1))].x);
+        const float z = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+        for (int q = 0; q < C::kDup; ++q)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float2 ml = info->ml[u][q * kCopy + (tl & (kCopy - 1))];
+            sum = fmaf(ml.y, ex2(ml.x - z), sum);
+          }
+        f0 = ex2(info->ml[0][tl].x - z), f1 = ex2(info->ml[1][tl].x - z);
+        m = top, l = sum;
       } else if (!ok) {
         break;
       }
@@ -640,50 +706,69 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(
       const bool none = l == 0.0f;  // sees nothing (another row's NaN value may be in its O)
       const float inv = whole ? dec_unlift(C::kLift) / l : 1.0f;
       f0 *= inv, f1 *= inv;
-      // (of two streams' outputs each warpgroup writes half of the columns)
+      // Of two streams' outputs each warpgroup writes half of the columns; copies
+      // but the first hand theirs over where the query rows have been.
       constexpr int kCols = C::kSplit ? C::kD / 2 : C::kD;
-      const uint32_t tOther = tmem + lane_addr + C::kColO + (t ^ 1) * C::kD;
+      const uint32_t tO0 = C::kSplit ? tmem + lane_addr + C::kColO : tO, tO1 = tO0 + C::kD;
       const int d0 = C::kSplit ? t * kCols : 0;
+      uint8_t* const hand = smem + t * C::kOffHand1;
       if (work) {
 #pragma unroll 1
         for (int d = d0; d < d0 + kCols; d += 32) {
           uint32_t rr[32], ro[C::kSplit ? 32 : 1] = {};
-          if (mine) tmem_ld32(tO + d, rr);
-          if constexpr (C::kSplit) {
-            if (other) tmem_ld32(tOther + d, ro);
-          }
+          tmem_ld32(tO0 + d, rr);
+          if constexpr (C::kSplit) tmem_ld32(tO1 + d, ro);
           tmem_wait_ld();
           reg_fence(rr);
           reg_fence(ro);
+          float o[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            float o = mine ? __uint_as_float(rr[e]) * f0 : 0.0f;
-            if constexpr (C::kSplit) {
-              if (other) o = fmaf(__uint_as_float(ro[e]), f1, o);
-            }
-            rr[e] = none ? 0u : __float_as_uint(o);
+            o[e] = __uint_as_float(rr[e]) * f0;
+            if constexpr (C::kSplit) o[e] = fmaf(__uint_as_float(ro[e]), f1, o[e]);
           }
-          if (real && whole) {
+          if constexpr (C::kDup > 1) {
+            if (copy > 0) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              uint32_t y[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float o0 = __uint_as_float(rr[8 * u + 2 * e]), o1 = __uint_as_float(rr[8 * u + 2 * e + 1]);
-                y[e] = C::kF16 ? pack_f16x2(o0, o1) : pack_bf16x2(o0, o1);
-              }
-              *reinterpret_cast<uint4*>(dst + d * 2 + u * 16) = make_uint4(y[0], y[1], y[2], y[3]);
+              for (int u = 0; u < 8; ++u)
+                *reinterpret_cast<float4*>(hand + (tl - kCopy) * 128 + ((u ^ (tl & 7)) << 4)) =
+                    make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
             }
-          } else if (real) {
-            uint4* part = reinterpret_cast<uint4*>(p.part_o + slot * C::kD + d);
+            named_bar_sync(1 + t, 128);
+            if (copy == 0) {
 #pragma unroll
-            for (int u = 0; u < 8; ++u) part[u] = make_uint4(rr[4 * u], rr[4 * u + 1], rr[4 * u + 2], rr[4 * u + 3]);
+              for (int q = 0; q < C::kDup - 1; ++q)
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                  const float4 y = *reinterpret_cast<const float4*>(hand + (q * kCopy + tl) * 128 + ((u ^ (tl & 7)) << 4));
+                  o[4 * u] += y.x, o[4 * u + 1] += y.y, o[4 * u + 2] += y.z, o[4 * u + 3] += y.w;
+                }
+            }
+            named_bar_sync(1 + t, 128);
+          }
+          if (real && copy == 0) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = none ? 0.0f : o[e];
+            if (whole) {
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                uint32_t y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  y[e] = p.f16 ? pack_f16x2(o[8 * u + 2 * e], o[8 * u + 2 * e + 1]) : pack_bf16x2(o[8 * u + 2 * e], o[8 * u + 2 * e + 1]);
+                *reinterpret_cast<uint4*>(dst + d * 2 + u * 16) = make_uint4(y[0], y[1], y[2], y[3]);
+              }
+            } else {
+              float4* part = reinterpret_cast<float4*>(p.part_o + slot * C::kD + d);
+#pragma unroll
+              for (int u = 0; u < 8; ++u) part[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+            }
           }
           __syncwarp();
         }
       }
       tc_fence_before();
-      if (real && (!C::kSplit || t == 0)) {
+      if (real && copy == 0 && (!C::kSplit || t == 0)) {
         if (whole)
           a.lse[((long long)at.b * a.Hq + head) * a.n + i] = none ? -INFINITY : ((m + C::kLift) + lg2(l)) * kDecLn2;
         else

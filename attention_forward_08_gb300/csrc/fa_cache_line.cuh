@@ -39,6 +39,8 @@ struct DecParams {
   CacheAttnParams a;
   int rows, row_groups;   // rows of a K/V head; groups of kRows
   int max_ctas;
+  int kind;               // of the stored values, and is q f16: where a kernel asks at run time
+  bool f16;
   float* part_o;          // [2 * max_ctas, kRows, D]
   float2* part_ml;        // [2 * max_ctas, kRows]: reference, sum
   float* scores;          // [B, H, M * page / 32, rows, 32]: scores in base 2, for the weights (or NULL)

@@ -115,6 +115,7 @@ __global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constan
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (none) return;
   const bool raw = a.cap_out == 0.0f;
+  const TreeOf tree = tree_of(a, b);
   float sum[4][2] = {};
 #pragma unroll 1
   for (int rg = rg0; rg <= rg1; ++rg) {
@@ -135,8 +136,8 @@ __global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constan
     // tokens that rows g and g + 8 see (a row that is none has L2 = +inf)
     int2 va = make_int2(0, 0), vb = va;
     if constexpr (kTree) {  // (of a tree's, those before the drafts)
-      if (ia < seq.nq) va = make_int2(a.window > 0 ? tree_first(a, pos0, tree_depth(a, b, ia)) : 0, pos0);
-      if (ib < seq.nq) vb = make_int2(a.window > 0 ? tree_first(a, pos0, tree_depth(a, b, ib)) : 0, pos0);
+      if (ia < seq.nq) va = make_int2(a.window > 0 ? tree_first(tree, pos0, tree_depth(tree, ia)) : 0, pos0);
+      if (ib < seq.nq) vb = make_int2(a.window > 0 ? tree_first(tree, pos0, tree_depth(tree, ib)) : 0, pos0);
     } else {
       va = dec_span(a, seq, ia, ia), vb = dec_span(a, seq, ib, ib);
     }
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constan
                 : fmaf(-2.0f * a.cap_out, rcp_approx(ex2(s * a.cap_in * 2.8853900817779268f) + 1.0f), a.cap_out);
         const int tok = tok0 + 8 * j + 2 * t + (e & 1);
         bool seen = tok >= v.x && tok < v.y;
-        if constexpr (kTree) seen = seen || tree_sees_draft(a, seq, b, e < 2 ? ia : ib, tok);
+        if constexpr (kTree) seen = seen || tree_sees_draft(tree, seq.nq, e < 2 ? ia : ib, tok - pos0);
         if (seen) sum[j][e & 1] += ex2(s - r.y);
       }
   }
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_finish_kernel(const __grid
     for (int r = 0; r < p.rows; ++r) {
       bool seen;
       if constexpr (C::kTree) {
-        seen = tree_sees(a, seq, b, r / a.group, tok);
+        seen = tree_sees(tree_of(a, b), seq, r / a.group, tok);
       } else {
         const int2 see = dec_span(a, seq, r / a.group, r / a.group);
         seen = tok >= see.x && tok < see.y;
