@@ -179,10 +179,7 @@ int launch_drafts(const CacheAttnParams& a, int kind, bool f16, const LaunchCtx&
   if (!line_params<C>(p, a, ctx.num_sms, ctx)) return FA_ERR_UNSUPPORTED;
   p.kind = kind;
   p.f16 = f16;
-  CUtensorMap tk, tv;
-  const int rows = a.c.page < C::kPieceKeys ? a.c.page : C::kPieceKeys;
-  if (!encode_pool_rows(&tk, a.c, false, rows) || !encode_pool_rows(&tv, a.c, true, rows)) return FA_ERR_CUDA;
-  kern<<<p.max_ctas, C::kThreads, kDraftSmem<C>, ctx.stream>>>(tk, tv, p);
+  kern<<<p.max_ctas, C::kThreads, kDraftSmem<C>, ctx.stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && p.max_ctas > 1) {
     const dim3 grid((unsigned)join_pieces<C>(p), (unsigned)p.max_ctas - 1);

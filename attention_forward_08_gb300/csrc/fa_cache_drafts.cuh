@@ -9,10 +9,14 @@
 // them from HBM, once.
 //
 // Loads.  One warp looks up blocks and scales, up to 16 blocks of 128 keys
-// ahead; one keeps 48 KB of stored bytes on their way, by TMA into two rings, of K
-// and of V (loads to registers of the converter warps: the compiler waits for the
-// last of several where the first is needed); four converter warps widen K and
-// four V, so that neither waits for the other's place.
+// ahead.  Four converter warps take K and four V, so that neither waits for the
+// other's place, and each works alone: a lane copies 16 bytes a time into a place
+// of its own (cp.async; three pieces of 2 KB a warp, 48 KB in all), widens them and
+// writes them where the tensor core reads.  No barrier stands between the copy
+// and the use.  (Loads to registers: the compiler waits for the last of several
+// where the first is needed.  TMA into common rings: the barriers of a piece cost as
+// much as its conversion, 94 us for 16 sequences of up to 8192 tokens with pieces of
+// 8 KB, 132 with 4.)
 //
 // Streams.  Up to 128 rows (kSplit) are one row tile, and of every block of keys
 // each of the two softmax warpgroups takes one half, with its own maximum, sum
@@ -54,13 +58,12 @@ struct DraftCfg {
   static constexpr int kMinTiles = 4;
   static constexpr int kLift = 7;
   static constexpr int kKeys = 64;   // keys a score buffer: a unit
-  // Widened K and V: stages of 16 KB (D = 256: 32).  Stored bytes: rings of three
-  // pieces of 8 KB, of K and of V.
+  // Widened K and V: stages of 16 KB (D = 256: 32).  Stored bytes: three pieces of
+  // 2 KB a converter warp.
   static constexpr int kStageKeys = kD == 64 ? 128 : 64, kStageBytes = kStageKeys * kD * 2;
   static constexpr int kStagesK = kD == 256 ? 2 : 4, kStagesV = kD == 128 && !kSplit ? 2 : kStagesK;
-  static constexpr int kPieceKeys = 8192 / kD, kPieceBytes = 8192, kRing = 3;
-  static constexpr int kPieces = kStageKeys > kPieceKeys ? kStageKeys / kPieceKeys : 1;  // a stage
-  static_assert(kPieces * kPieceKeys == kStageKeys, "stages are whole pieces");
+  static constexpr int kPieceKeys = 2048 / kD, kPieceBytes = 2048, kRing = 3;
+  static constexpr int kPieces = kStageKeys / kPieceKeys;  // a stage: 4, 4, 8
   static constexpr int kStageUnits = kStageKeys / kKeys;
   // Issuers that are done with a stage, one after the other.
   static constexpr int kReaders = kSplit ? kStageUnits : kTiles;
@@ -73,15 +76,15 @@ struct DraftCfg {
   static_assert(128 * kRegsCtrl + 32 * kConvWarps * kRegsConv + 128 * kSoft * kRegsSoft <= kThreads * kRegsLaunch,
                 "register split exceeds the launch allocation");
   static constexpr int kVecs = kD / 16;                              // 16-byte vectors a key
-  static constexpr int kSet = kPieceBytes / 16 / (16 * kConvWarps);  // a converter's of a piece: 4
+  static constexpr int kSet = kPieceBytes / 16 / 32;  // a lane's of a piece: 4
   static constexpr int kQBytes = kQRows * kD * 2;
   // 32 columns of the copies' outputs, for each stream: over the query rows (the
   // second's behind the rings where those have too little room).
   static constexpr int kHand = (128 - 128 / kDup) * 128;
   static constexpr int kOffK = kTiles * kQBytes, kOffV = kOffK + kStagesK * kStageBytes;
   static constexpr int kOffRing = kOffV + kStagesV * kStageBytes;
-  static constexpr int kOffHand1 = 2 * kHand <= kQBytes ? kHand : kOffRing + 2 * kRing * kPieceBytes;
-  static constexpr int kOffInfo = kOffRing + 2 * kRing * kPieceBytes + (kOffHand1 > kHand ? kHand : 0);
+  static constexpr int kOffHand1 = 2 * kHand <= kQBytes ? kHand : kOffRing + kConvWarps * kRing * kPieceBytes;
+  static constexpr int kOffInfo = kOffRing + kConvWarps * kRing * kPieceBytes + (kOffHand1 > kHand ? kHand : 0);
   static_assert(kHand <= kQBytes, "room for the copies' outputs");
   static constexpr int kColO = 256;  // S: two buffers of kKeys columns a stream; P over S
 };
@@ -97,10 +100,8 @@ constexpr int kDraftWords = 8;    // of a row's drafts that are kept (more are l
 template <class C>
 struct DraftInfo {
   float4 meta[kDraftAhead][8];          // by 16 keys: ks, log2 vs, 1 / vs less the lift, there
-  int2 from[kDraftAhead][8];            // cache block (-1: none), head
+  long long from[2][kDraftAhead][8];    // K, V: bytes from the pool's begin to the first of 16 keys
   int range[kDraftAhead][8];            // keys that are stored and seen: lo | hi << 8; values that count: lo << 16 | hi << 24
-  int tok[kDraftAhead];                 // a block's first token
-  uint32_t all[kDraftAhead];            // 1: all keys are stored and seen; 2: all values count
   uint32_t line[kDraftWords][128 * C::kSoft];  // the drafts that a softmax thread's row sees
   float2 ml[2][128];                    // (streams) references and sums
   uint64_t q_full[2];                   // 4 softmax warps: query tile written
@@ -108,7 +109,7 @@ struct DraftInfo {
   uint64_t s_full[2][2];                // [stream][buffer]: S computed
   uint64_t p_ready[2][2];               // softmax wrote P (and rescaled O); a warp may be a unit ahead of another
   uint64_t o_ready[2][2];               // PV done, by buffer: nobody is two phases of one behind
-  uint64_t info_full[4], info_empty[4], ring_full[2][C::kRing], ring_empty[2][C::kRing], drain[2];
+  uint64_t info_full[4], info_empty[4], drain[2];
   int n[2][2];                          // [stream][piece & 1]: blocks of a piece (0: no more), beside q_full
   uint32_t tmem;
   int abort;
@@ -149,8 +150,7 @@ __device__ __forceinline__ uint32_t draft_seen(const TreeOf& tree, int i, uint32
 }
 
 template <class C>
-__global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(
-    const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const __grid_constant__ DecParams p) {
+__global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __grid_constant__ DecParams p) {
   static_assert(kDraftSmem<C> <= 232448, "shared memory");
   const CacheAttnParams& a = p.a;
   const CacheView& c = a.c;
@@ -175,12 +175,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(
     }
     for (int kv = 0; kv < 2; ++kv) {
       for (int i = 0; i < 4; ++i) {
-        mbar_init(&info->full[kv][i], C::kConvWarps / 2);
+        mbar_init(&info->full[kv][i], C::kPieces);
         mbar_init(&info->empty[kv][i], C::kReaders);
-      }
-      for (int i = 0; i < C::kRing; ++i) {
-        mbar_init(&info->ring_full[kv][i], 1);
-        mbar_init(&info->ring_empty[kv][i], C::kConvWarps / 2);
       }
     }
     for (int i = 0; i < 4; ++i) {
@@ -189,8 +185,6 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(
     }
     info->abort = 0;
     fence_barrier_init();
-    tma_prefetch_desc(&tk);
-    tma_prefetch_desc(&tv);
   }
   if (warp == 1) {
     tmem_alloc(&info->tmem, 512);
@@ -328,136 +322,81 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(
         // (values of a zero scale are zeros, and count with the scale 1)
         const bool zero = !(vs >= 1.17549435e-38f);
         info->meta[slot][g] = make_float4(ks, zero ? 0.0f : lg2(vs), dec_unlift(C::kLift) * (zero ? 1.0f : 1.0f / vs), blk >= 0 ? 1.0f : 0.0f);
-        info->from[slot][g] = make_int2(blk, h);
-        if (g == 0) info->tok[slot] = mine;
+        const long long row = mine & (c.page - 1);
+        info->from[0][slot][g] = blk >= 0 ? blk * c.ks[0] + h * c.ks[1] + row * c.ks[2] : 0;
+        info->from[1][slot][g] = blk >= 0 ? blk * c.vs[0] + h * c.vs[1] + row * c.vs[2] : 0;
         const int keys = blk >= 0 && lo < hi ? lo | (hi << 8) : 0;
         info->range[slot][g] = keys | (zero ? 0 : keys << 16);
-        const uint32_t k_all = __ballot_sync(0xFFFFFFFFu, keys == 16 << 8), v_all = __ballot_sync(0xFFFFFFFFu, keys == 16 << 8 && !zero);
-        const int shift = lane & 24;
-        if (g == 0) info->all[slot] = (((k_all >> shift) & 255u) == 255u ? 1u : 0u) | (((v_all >> shift) & 255u) == 255u ? 2u : 0u);
         __syncwarp();
         if (lane == 0) mbar_arrive(&info->info_full[batch & 3]);
       }
-    } else if (warp == 3) {
-      // ---------------------------------------------------------- stored bytes
-      // Both rings, whichever has room.  A lane a 16-key group; one of those that
-      // share a box of the tensor map copies it (its block, if any of them has one).
-      constexpr int kGroupsHere = C::kPieceKeys / 16, kPiecesBlock = 128 / C::kPieceKeys;
-      const int rows = min(c.page, C::kPieceKeys), share = rows / 16, pieces = kPiecesBlock * (t1 - t0);
-      int done[2] = {0, 0}, slot[2] = {0, 0};  // pieces of K, V
-      uint32_t phase[2] = {0, 0};
-      int known = 0;                           // blocks that are looked up
-      bool ok = true;
-      long long begin = clock64_now();         // since when nothing has moved
-#pragma unroll 1
-      while (ok && (done[0] < pieces || done[1] < pieces)) {
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          if (done[kv] == pieces) continue;
-          const int nb = done[kv] / kPiecesBlock;
-          if (nb == known) {
-            ok = wait(&info->info_full[(nb >> 2) & 3], (uint32_t)(nb >> 4) & 1u);
-            if (!ok) break;
-            known += 4;
-          }
-          uint64_t* const bar = &info->ring_full[kv][slot[kv]];
-          if (done[kv] >= C::kRing && !__all_sync(0xFFFFFFFFu, mbar_test(&info->ring_empty[kv][slot[kv]], phase[kv] ^ 1u)))
-            continue;
-          const int at_info = nb & (kDraftAhead - 1), tok = info->tok[at_info];
-          const int g = done[kv] % kPiecesBlock * kGroupsHere + lane % kGroupsHere;
-          const int2 from = info->from[at_info][g];
-          int blk = lane < kGroupsHere ? from.x : -1;
-#pragma unroll
-          for (int o = 1; o < kGroupsHere; o <<= 1) {
-            const int other = __shfl_xor_sync(0xFFFFFFFFu, blk, o);
-            if (o < share) blk = max(blk, other);
-          }
-          const bool box = lane < kGroupsHere && (lane & (share - 1)) == 0 && blk >= 0;
-          const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, box));
-          if (lane == 0) {
-            if (boxes > 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * rows * C::kD));
-            else mbar_arrive(bar);
-          }
-          __syncwarp();
-          if (box)
-            tma_load_4d(smem + C::kOffRing + (kv * C::kRing + slot[kv]) * C::kPieceBytes + lane * 16 * C::kD, kv ? &tv : &tk, bar, 0,
-                        (tok + 16 * g) & (c.page - 1), from.y, blk);
-          __syncwarp();
-          ++done[kv];
-          if (++slot[kv] == C::kRing) slot[kv] = 0, phase[kv] ^= 1u;
-          begin = clock64_now();
-        }
-        // (bounded as the other waits are)
-        if (ok && __any_sync(0xFFFFFFFFu, *abort || clock64_now() - begin > a.timeout_cycles)) {
-          if (lane == 0 && !*abort) {
-            *abort = 1;
-            atomicOr(c.status, kStatusTimeout);
-          }
-          ok = false;
-        }
-      }
-      // Copies land before the block ends (also where nobody looked at them; bounded).
-      begin = clock64_now();
-#pragma unroll 1
-      for (int kv = 0; kv < 2; ++kv)
-        for (int k = max(0, done[kv] - C::kRing); k < done[kv]; ++k)
-          while (!mbar_try_wait(&info->ring_full[kv][k % C::kRing], (uint32_t)(k / C::kRing) & 1u) &&
-                 clock64_now() - begin < kDecDrainCycles) {
-          }
     }
   } else if (warp < 4 + C::kConvWarps) {
     // ============================================================ converters
     regs_dec<C::kRegsConv>();
-    const int kv = (warp - 4) / (C::kConvWarps / 2), cw = (warp - 4) % (C::kConvWarps / 2);
+    constexpr int kTeam = C::kConvWarps / 2;  // of K, of V: piece k is warp k % kTeam's
+    const int kv = (warp - 4) / kTeam, cw = (warp - 4) % kTeam;
     // Lane bits 0-1: vector, 2: key, then vectors, then keys: eight neighbours
     // write eight different 16-byte columns of the swizzled rows.
     constexpr int kHigh = C::kVecs / 4;
-    constexpr int kKeysWarp = 32 / C::kVecs, kKeysStep = kKeysWarp * C::kConvWarps / 2;  // 32, 16, 8
-    static_assert(kKeysStep * C::kSet == C::kPieceKeys, "a piece is a set");
+    constexpr int kKeysWarp = 32 / C::kVecs;  // keys at once: 8, 4, 2
+    static_assert(kKeysWarp * C::kSet == C::kPieceKeys, "a piece is a set");
     const int vec = (lane & 3) + 4 * ((lane >> 3) % kHigh);
-    const int key0 = cw * kKeysWarp + ((lane >> 2) & 1) + 2 * ((lane >> 3) / kHigh);
+    const int key0 = ((lane >> 2) & 1) + 2 * ((lane >> 3) / kHigh);
     uint8_t* const to = smem + (kv ? C::kOffV : C::kOffK) + (uint32_t)(vec / 4) * (C::kStageKeys * 128) + key0 * 128;
-    const uint32_t lo16 = (((vec % 4) * 2) ^ (key0 & 7)) << 4, hi16 = (((vec % 4) * 2 + 1) ^ (key0 & 7)) << 4;
-    const uint32_t from = smem_u32(smem + C::kOffRing + kv * C::kRing * C::kPieceBytes) + key0 * C::kD + vec * 16;
+    const uint32_t lo16 = (((vec % 4) * 2) ^ key0) << 4, hi16 = (((vec % 4) * 2 + 1) ^ key0) << 4;
+    const uint32_t mine = smem_u32(smem + C::kOffRing + (warp - 4) * C::kRing * C::kPieceBytes) + lane * 16;
+    const uint8_t* const pool = (kv ? c.v : c.k) + vec * 16;
+    const long long stride = kv ? c.vs[2] : c.ks[2];
     const int stages = kv ? C::kStagesV : C::kStagesK, pieces = 128 / C::kPieceKeys * (t1 - t0);
-    int slot = 0;
-    uint32_t phase = 0;
-#pragma unroll 1
-    for (int k = 0; k < pieces; ++k) {
-      const int nth = k / C::kPieces, part = k % C::kPieces, stage = nth & (stages - 1);  // of the stage
-      if (!wait(&info->ring_full[kv][slot], phase)) break;
-      uint4 x[C::kSet];
-#pragma unroll
-      for (int u = 0; u < C::kSet; ++u) x[u] = lds128(from + slot * C::kPieceBytes + u * (kKeysStep * C::kD));
-      const int at_info = (k * C::kPieceKeys / 128) & (kDraftAhead - 1);
-      if (!((info->all[at_info] >> kv) & 1u)) {  // where nobody sees them or nothing is stored: zeros
+    int known = 0;  // blocks that are looked up
+    bool ok = true;
+    auto copy = [&](int k, int slot) {  // of piece k, as one group
+      const int nb = k * C::kPieceKeys / 128, at = nb & (kDraftAhead - 1);
+      if (k < pieces && nb >= known) {
+        ok = wait(&info->info_full[(nb >> 2) & 3], (uint32_t)(nb >> 4) & 1u);
+        known += 4;
+      }
+      if (k < pieces && ok) {
 #pragma unroll
         for (int u = 0; u < C::kSet; ++u) {
-          const int key = (k * C::kPieceKeys) % 128 + key0 + u * kKeysStep, keys = info->range[at_info][key >> 4] >> (16 * kv);
-          if (!((key & 15) >= (keys & 255) && (key & 15) < ((keys >> 8) & 255))) x[u] = make_uint4(0, 0, 0, 0);
+          const int key = (k * C::kPieceKeys) % 128 + key0 + u * kKeysWarp, r = key & 15, keys = info->range[at][key >> 4] >> (16 * kv);
+          // (zeros where nobody sees them or nothing is stored)
+          copy16(mine + slot * C::kPieceBytes + u * 512, pool + info->from[kv][at][key >> 4] + r * stride,
+                 r >= (keys & 255) && r < ((keys >> 8) & 255));
         }
       }
-      if (part == 0 && nth >= stages && !wait(&info->empty[kv][stage], (uint32_t)(nth / stages + 1) & 1u)) break;
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    copy(cw, 0);
+    copy(cw + kTeam, 1);
+    int slot = 0;
+#pragma unroll 1
+    for (int k = cw; k < pieces && ok; k += kTeam) {
+      const int nth = k / C::kPieces, part = k % C::kPieces, stage = nth & (stages - 1);
+      copy(k + 2 * kTeam, slot + 2 >= C::kRing ? slot + 2 - C::kRing : slot + 2);
+      asm volatile("cp.async.wait_group 2;" ::: "memory");
+      uint4 x[C::kSet];
+#pragma unroll
+      for (int u = 0; u < C::kSet; ++u) x[u] = lds128(mine + slot * C::kPieceBytes + u * 512);
+      if (nth >= stages) ok = ok && wait(&info->empty[kv][stage], (uint32_t)(nth / stages + 1) & 1u);
+      if (!ok) break;
       uint8_t* const row = to + stage * C::kStageBytes + part * (C::kPieceKeys * 128);
 #pragma unroll
-      for (int u = 0; u < C::kSet; ++u) {  // (a step of kKeysStep keys leaves the swizzle as it is)
+      for (int u = 0; u < C::kSet; ++u) {
         uint4 lo, hi;
         if (p.kind == kKindE4m3) widen16<kKindE4m3>(x[u], lo, hi);
         else widen16<kKindInt8>(x[u], lo, hi);
-        *reinterpret_cast<uint4*>(row + u * (kKeysStep * 128) + lo16) = lo;
-        *reinterpret_cast<uint4*>(row + u * (kKeysStep * 128) + hi16) = hi;
+        const uint32_t turn = (u * (kKeysWarp << 4)) & 0x70u;  // (the swizzle goes by the key's low three bits)
+        *reinterpret_cast<uint4*>(row + u * (kKeysWarp * 128) + (lo16 ^ turn)) = lo;
+        *reinterpret_cast<uint4*>(row + u * (kKeysWarp * 128) + (hi16 ^ turn)) = hi;
       }
-      if (part == C::kPieces - 1) fence_proxy_async_smem();
+      fence_proxy_async_smem();
       __syncwarp();
-      // (The slot is free once what was read has been used: given back right behind
-      // the loads, it was filled again before a warp that waited for its stage
-      // had its bytes.)
-      if (lane == 0) {
-        if (part == C::kPieces - 1) mbar_arrive(&info->full[kv][stage]);
-        mbar_arrive(&info->ring_empty[kv][slot]);
-      }
-      if (++slot == C::kRing) slot = 0, phase ^= 1u;
+      if (lane == 0) mbar_arrive(&info->full[kv][stage]);
+      if (++slot == C::kRing) slot = 0;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // (after an expired wait copies may be on their way)
   } else {
     // ============================================================ softmax
     regs_inc<C::kRegsSoft>();
