@@ -33,6 +33,8 @@
 // softmax warps' chains.
 #pragma once
 
+#include <type_traits>
+
 #include "fa_cache_decode.cuh"
 #include "fa_cache_prompt.cuh"
 #include "fa_cache_tree.cuh"
@@ -104,6 +106,7 @@ struct DraftInfo {
   int range[kDraftAhead][8];            // keys that are stored and seen: lo | hi << 8; values that count: lo << 16 | hi << 24
   uint32_t line[kDraftWords][128 * C::kSoft];  // the drafts that a softmax thread's row sees
   float2 ml[2][128];                    // (streams) references and sums
+  float rs[128];                        // (streams) a row's factor back
   uint64_t q_full[2];                   // 4 softmax warps: query tile written
   uint64_t full[2][4], empty[2][4];     // [K, V][stage]
   uint64_t s_full[2][2];                // [stream][buffer]: S computed
@@ -349,6 +352,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
     const uint8_t* const pool = (kv ? c.v : c.k) + vec * 16;
     const long long stride = kv ? c.vs[2] : c.ks[2];
     const int stages = kv ? C::kStagesV : C::kStagesK, pieces = 128 / C::kPieceKeys * (t1 - t0);
+    const bool e4m3 = p.kind == kKindE4m3;
     int known = 0;  // blocks that are looked up
     bool ok = true;
     auto copy = [&](int k, int slot) {  // of piece k, as one group
@@ -358,12 +362,22 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
         known += 4;
       }
       if (k < pieces && ok) {
+        // (a piece's keys lie in one 16-key group, or two; what is known about them is read before the first copy)
+        constexpr int kGroupsHere = C::kPieceKeys > 16 ? C::kPieceKeys / 16 : 1;
+        const int first = (k * C::kPieceKeys) % 128;
+        long long off[kGroupsHere];
+        int keys[kGroupsHere];
+#pragma unroll
+        for (int g = 0; g < kGroupsHere; ++g) {
+          off[g] = info->from[kv][at][first / 16 + g];
+          keys[g] = info->range[at][first / 16 + g] >> (16 * kv);
+        }
 #pragma unroll
         for (int u = 0; u < C::kSet; ++u) {
-          const int key = (k * C::kPieceKeys) % 128 + key0 + u * kKeysWarp, r = key & 15, keys = info->range[at][key >> 4] >> (16 * kv);
+          const int g = u * kKeysWarp / 16, r = first % 16 + key0 + u * kKeysWarp - 16 * g;
           // (zeros where nobody sees them or nothing is stored)
-          copy16(mine + slot * C::kPieceBytes + u * 512, pool + info->from[kv][at][key >> 4] + r * stride,
-                 r >= (keys & 255) && r < ((keys >> 8) & 255));
+          copy16(mine + slot * C::kPieceBytes + u * 512, pool + off[g] + r * stride,
+                 r >= (keys[g] & 255) && r < ((keys[g] >> 8) & 255));
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -374,23 +388,26 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
 #pragma unroll 1
     for (int k = cw; k < pieces && ok; k += kTeam) {
       const int nth = k / C::kPieces, part = k % C::kPieces, stage = nth & (stages - 1);
-      copy(k + 2 * kTeam, slot + 2 >= C::kRing ? slot + 2 - C::kRing : slot + 2);
-      asm volatile("cp.async.wait_group 2;" ::: "memory");
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
       uint4 x[C::kSet];
 #pragma unroll
       for (int u = 0; u < C::kSet; ++u) x[u] = lds128(mine + slot * C::kPieceBytes + u * 512);
+      copy(k + 2 * kTeam, slot + 2 >= C::kRing ? slot + 2 - C::kRing : slot + 2);
       if (nth >= stages) ok = ok && wait(&info->empty[kv][stage], (uint32_t)(nth / stages + 1) & 1u);
       if (!ok) break;
       uint8_t* const row = to + stage * C::kStageBytes + part * (C::kPieceKeys * 128);
+      auto widen = [&](auto kind) {
 #pragma unroll
-      for (int u = 0; u < C::kSet; ++u) {
-        uint4 lo, hi;
-        if (p.kind == kKindE4m3) widen16<kKindE4m3>(x[u], lo, hi);
-        else widen16<kKindInt8>(x[u], lo, hi);
-        const uint32_t turn = (u * (kKeysWarp << 4)) & 0x70u;  // (the swizzle goes by the key's low three bits)
-        *reinterpret_cast<uint4*>(row + u * (kKeysWarp * 128) + (lo16 ^ turn)) = lo;
-        *reinterpret_cast<uint4*>(row + u * (kKeysWarp * 128) + (hi16 ^ turn)) = hi;
-      }
+        for (int u = 0; u < C::kSet; ++u) {
+          uint4 lo, hi;
+          widen16<decltype(kind)::value>(x[u], lo, hi);
+          const uint32_t turn = (u * (kKeysWarp << 4)) & 0x70u;  // (the swizzle goes by the key's low three bits)
+          *reinterpret_cast<uint4*>(row + u * (kKeysWarp * 128) + (lo16 ^ turn)) = lo;
+          *reinterpret_cast<uint4*>(row + u * (kKeysWarp * 128) + (hi16 ^ turn)) = hi;
+        }
+      };
+      if (e4m3) widen(std::integral_constant<int, kKindE4m3>());
+      else widen(std::integral_constant<int, kKindInt8>());
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&info->full[kv][stage]);
@@ -429,53 +446,60 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
       const TreeOf tree = tree_of(a, at.b);
       int up = -1;
       if (tree.n <= 32 && lane < at.seq.nq) up = tree_parent(tree, lane);
-      // The warp's query rows, kLanes lanes a row, all loads under way at once:
-      // the row's largest entry, then its f16 form.  (S of the piece before is
-      // done: the tile may be written.  Both streams load, the first writes.)
+      // The warp's query rows, kLanes lanes a row, straight to their place in the
+      // tile; then, a thread a row, their f16 form.  (S of the piece before is done: the
+      // tile may be written.  With two streams, the first does it.  The loops are
+      // rolled: what runs once a piece costs the fetching of its instructions.)
       float rs = 1.0f;
-      {
-        constexpr int kLanes = C::kD / 8, kAtOnce = 32 / kLanes;  // rows a load
-        const uint16_t* mine = some ? static_cast<const uint16_t*>(a.q) + at.b * a.qs[0] + head * a.qs[1] + i * a.qs[2]
-                                    : nullptr;
-        constexpr int kPass = kLanes < 16 ? kLanes : 16;
-#pragma unroll
-        for (int u0 = 0; u0 < kLanes; u0 += kPass) {
-          uint4 w[kPass];
-#pragma unroll
-          for (int u = 0; u < kPass; ++u) {
-            const uint16_t* q = reinterpret_cast<const uint16_t*>(
-                __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(mine), (u0 + u) * kAtOnce + lane / kLanes));
-            w[u] = make_uint4(0, 0, 0, 0);
-            if (q) w[u] = __ldg(reinterpret_cast<const uint4*>(q) + lane % kLanes);
+      if (!C::kSplit || t == 0) {
+        constexpr int kLanes = C::kD / 8, kAtOnce = 32 / kLanes;  // rows a copy
+        const long long from = some ? (at.b * a.qs[0] + head * a.qs[1] + i * a.qs[2]) * 2 : -1;
+        const int r0 = (warp & 3) * 32, c16 = lane % kLanes;
+        if (r0 < C::kQRows) {
+          uint8_t* const col = q_tile + (c16 / 8) * (C::kQRows * 128);
+#pragma unroll 2
+          for (int r = lane / kLanes; r < 32; r += kAtOnce) {
+            const long long off = __shfl_sync(0xFFFFFFFFu, from, r);
+            copy16(smem_u32(col + (r0 + r) * 128 + (((c16 % 8) ^ (r & 7)) << 4)),
+                   static_cast<const uint8_t*>(a.q) + max(off, 0LL) + c16 * 16, off >= 0);
           }
-#pragma unroll
-          for (int u = 0; u < kPass; ++u) {
-            if (!p.f16) {
-              uint32_t* x = &w[u].x;
-              float top = 0.0f, up, down;
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          __syncwarp();
+          if (!p.f16) {
+            uint8_t* const mine = q_tile + tl * 128;
+            float top = 0.0f, up;
+#pragma unroll 4
+            for (int c = 0; c < kLanes; ++c) {
+              const uint4 w = *reinterpret_cast<const uint4*>(mine + (c / 8) * (C::kQRows * 128) + (((c % 8) ^ (tl & 7)) << 4));
+              const uint32_t* x = &w.x;
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 top = fmax3(top, fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xFFFF0000u)));
-#pragma unroll
-              for (int o = 1; o < kLanes; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-              dec_row_scale(top, up, down);
-              const float got = __shfl_sync(0xFFFFFFFFu, down, (lane % kAtOnce) * kLanes);
-              if (lane / kAtOnce == u0 + u) rs = got;
+            }
+            dec_row_scale(top, up, rs);
+#pragma unroll 4
+            for (int c = 0; c < kLanes; ++c) {
+              uint4* const at16 = reinterpret_cast<uint4*>(mine + (c / 8) * (C::kQRows * 128) + (((c % 8) ^ (tl & 7)) << 4));
+              uint4 w = *at16;
+              uint32_t* x = &w.x;
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 x[e] = pack_f16x2(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xFFFF0000u) * up);
+              *at16 = w;
             }
-            const int r = (warp & 3) * 32 + (u0 + u) * kAtOnce + lane / kLanes, c16 = lane % kLanes;
-            if (r < C::kQRows && (!C::kSplit || t == 0))
-              *reinterpret_cast<uint4*>(q_tile + (c16 / 8) * (C::kQRows * 128) + r * 128 + (((c16 % 8) ^ (r & 7)) << 4)) = w[u];
           }
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if ((warp & 3) == 0) info->n[t][pieces & 1] = n;
+          mbar_arrive(&info->q_full[t]);
+        }
+        if constexpr (C::kSplit) info->rs[tl] = rs;
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0 && (!C::kSplit || t == 0)) {
-        if ((warp & 3) == 0) info->n[t][pieces & 1] = n;
-        mbar_arrive(&info->q_full[t]);
+      if constexpr (C::kSplit) {
+        named_bar_sync(3, 256);
+        rs = info->rs[tl];
       }
       // What the row sees: tokens from lo_row on before the drafts, and its line.
       int lo_row = 0;
