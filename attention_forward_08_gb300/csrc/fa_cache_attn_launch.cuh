@@ -179,12 +179,14 @@ int launch_drafts(const CacheAttnParams& a, int kind, bool f16, const LaunchCtx&
   if (!line_params<C>(p, a, ctx.num_sms, ctx)) return FA_ERR_UNSUPPORTED;
   p.kind = kind;
   p.f16 = f16;
+  p.cuts = reinterpret_cast<int4*>(a.ws + line_workspace<C>(ctx.num_sms));
   kern<<<p.max_ctas, C::kThreads, kDraftSmem<C>, ctx.stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && p.max_ctas > 1) {
-    const dim3 grid((unsigned)join_pieces<C>(p), (unsigned)p.max_ctas - 1);
-    e = f16 ? launch_after(cache_join_kernel<DraftF16<C>>, grid, kJoinThreads, ctx.stream, p)
-            : launch_after(cache_join_kernel<C>, grid, kJoinThreads, ctx.stream, p);
+    const int rows = p.rows < C::kRows ? p.rows : C::kRows, at_once = kJoinThreads / (C::kD / 4);
+    const dim3 grid((unsigned)((rows + at_once - 1) / at_once), (unsigned)p.max_ctas - 1);
+    e = f16 ? launch_after(cache_drafts_join_kernel<C, true>, grid, kJoinThreads, ctx.stream, p)
+            : launch_after(cache_drafts_join_kernel<C, false>, grid, kJoinThreads, ctx.stream, p);
   }
   if (e != cudaSuccess) {
     set_error("cache attention launch failed: %s", cudaGetErrorString(e));
@@ -196,13 +198,12 @@ int launch_drafts(const CacheAttnParams& a, int kind, bool f16, const LaunchCtx&
 // Which kernel: by the rows of a K/V head.  Up to 16 (the decoding step), 32
 // where the registers hold them; else the tensor memory kernel, which always
 // computes 128 * kTiles rows.
-// A tree's rows beyond those take the drafts' kernel, 128 or 256 at a time.
-enum class AttnPlan { kRows16, kRows32, kDrafts128, kDrafts256, kPrompt };
+// A tree's rows beyond those take the drafts' kernel.
+enum class AttnPlan { kRows16, kRows32, kDrafts, kPrompt };
 template <int kD>
 AttnPlan attn_plan(const CacheAttnParams& a) {
   const long long rows = (long long)a.n * a.group;
-  if (rows > kPromptRows<kD>)
-    return !a.tree ? AttnPlan::kPrompt : kD == 256 || rows <= 128 ? AttnPlan::kDrafts128 : AttnPlan::kDrafts256;
+  if (rows > kPromptRows<kD>) return a.tree ? AttnPlan::kDrafts : AttnPlan::kPrompt;
   return kD <= 128 && rows > 16 ? AttnPlan::kRows32 : AttnPlan::kRows16;
 }
 
@@ -210,8 +211,7 @@ template <int kD>
 long long plan_workspace(const CacheAttnParams& a, int num_sms) {
   switch (attn_plan<kD>(a)) {
     case AttnPlan::kPrompt: return line_workspace<PromptCfg<0, false, kD, 16, true>>(num_sms);
-    case AttnPlan::kDrafts128: return line_workspace<DraftCfg<kD, 16, true, kD <= 128, 1>>(num_sms);
-    case AttnPlan::kDrafts256: return line_workspace<DraftCfg<kD, 16, true, false, 1>>(num_sms);
+    case AttnPlan::kDrafts: return line_workspace<DraftCfg<kD, 16, true, 1>>(num_sms) + 16LL * num_sms;
     case AttnPlan::kRows32:
       if constexpr (kD <= 128) return line_workspace<DecCfg<0, false, kD, 2, true>>(num_sms * DecCfg<0, false, kD, 2, true>::kCtas);
     default: return line_workspace<DecCfg<0, false, kD, 1, true>>(num_sms * DecCfg<0, false, kD, 1, true>::kCtas);
@@ -230,33 +230,28 @@ int launch_decode_by(const CacheAttnParams& a, const LaunchCtx& ctx) {
 }
 
 template <int kD>
-int launch_drafts_by(const CacheAttnParams& a, AttnPlan plan, int kind, bool f16, const LaunchCtx& ctx) {
+int launch_drafts_by(const CacheAttnParams& a, int kind, bool f16, const LaunchCtx& ctx) {
   const bool raw = a.cap_out == 0.0f && a.scale_log2 > 0.0f;
   if constexpr (kD <= 128) {
-    if (plan == AttnPlan::kDrafts128) {
-      const int rows = a.n * a.group;
-      if (rows <= 32)
-        return raw ? launch_drafts<DraftCfg<kD, 16, true, true, 4>>(a, kind, f16, ctx)
-                   : launch_drafts<DraftCfg<kD, 16, false, true, 4>>(a, kind, f16, ctx);
-      if (rows <= 64)
-        return raw ? launch_drafts<DraftCfg<kD, 16, true, true, 2>>(a, kind, f16, ctx)
-                   : launch_drafts<DraftCfg<kD, 16, false, true, 2>>(a, kind, f16, ctx);
-      return raw ? launch_drafts<DraftCfg<kD, 16, true, true, 1>>(a, kind, f16, ctx)
-                 : launch_drafts<DraftCfg<kD, 16, false, true, 1>>(a, kind, f16, ctx);
-    }
+    const long long rows = (long long)a.n * a.group;
+    if (rows <= 32)
+      return raw ? launch_drafts<DraftCfg<kD, 16, true, 4>>(a, kind, f16, ctx)
+                 : launch_drafts<DraftCfg<kD, 16, false, 4>>(a, kind, f16, ctx);
+    if (rows <= 64)
+      return raw ? launch_drafts<DraftCfg<kD, 16, true, 2>>(a, kind, f16, ctx)
+                 : launch_drafts<DraftCfg<kD, 16, false, 2>>(a, kind, f16, ctx);
+  } else if (raw && a.c.page >= 64) {
+    return launch_drafts<DraftCfg<kD, 64, true, 1>>(a, kind, f16, ctx);
   }
-  // (The variants are the prompt kernel's.)
-  if (!raw) return launch_drafts<DraftCfg<kD, 16, false, false, 1>>(a, kind, f16, ctx);
-  return a.c.page >= 64 ? launch_drafts<DraftCfg<kD, 64, true, false, 1>>(a, kind, f16, ctx)
-                        : launch_drafts<DraftCfg<kD, 16, true, false, 1>>(a, kind, f16, ctx);
+  return raw ? launch_drafts<DraftCfg<kD, 16, true, 1>>(a, kind, f16, ctx)
+             : launch_drafts<DraftCfg<kD, 16, false, 1>>(a, kind, f16, ctx);
 }
 
 template <int kD, int kKind, bool kF16, bool kTree>
 int launch_plan(const CacheAttnParams& a, const LaunchCtx& ctx) {
   const AttnPlan plan = attn_plan<kD>(a);
   if constexpr (kTree) {
-    if (plan == AttnPlan::kDrafts128 || plan == AttnPlan::kDrafts256)
-      return launch_drafts_by<kD>(a, plan, kKind, kF16, ctx);
+    if (plan == AttnPlan::kDrafts) return launch_drafts_by<kD>(a, kKind, kF16, ctx);
   } else if (plan == AttnPlan::kPrompt) {
     if (a.cap_out == 0.0f && a.scale_log2 > 0.0f)
       return a.c.page >= 64 ? launch_prompt<PromptCfg<kKind, kF16, kD, 64, true>>(a, ctx)

@@ -25,9 +25,9 @@
 // tile twice (four times), and a copy weighs every second (fourth) run of keys,
 // with a maximum, sum and output of its own: the tensor cores compute the whole
 // tile anyhow, and a softmax thread has half (a quarter) of the work.
-// Up to 256 rows are two tiles as in the prompt kernel.  D = 256 has room for one
-// stream, and for 64 rows (half of a tile; its other half computes what lies
-// behind, which nobody reads).
+// D = 256 has room for one stream, and for 64 rows (half of a tile; its other half
+// computes what lies behind, which nobody reads).  More rows are several row
+// groups, whose second finds the keys in L2.
 //
 // Bound: memory, 2 * D bytes a token and K/V head; then the converters and the
 // softmax warps' chains.
@@ -42,20 +42,17 @@
 namespace fa {
 
 // kDup_: copies of the rows in the row tile, each with its share of the keys.
-template <int kD_, int kGroup_, bool kRaw_, bool kSplit_, int kDup_>
+template <int kD_, int kGroup_, bool kRaw_, int kDup_>
 struct DraftCfg {
   static constexpr bool kTree = true;
-  static constexpr bool kF16 = false;      // (the join's; the kernel itself asks at run time)
   static constexpr int kDup = kDup_;
   static constexpr bool kRaw = kRaw_;      // scores need no more than a positive factor
-  static constexpr bool kSplit = kSplit_;  // two streams of keys for one row tile
   static constexpr int kGroup = kGroup_;   // tokens that surely share a cache block: 16, or 64
   static constexpr int kD = kD_;
-  static_assert(kSplit ? kD <= 128 && kGroup == 16 : kDup == 1, "copies of rows are joined as streams are");
-  static constexpr int kTiles = kD <= 128 && !kSplit ? 2 : 1;  // 128-row tiles
-  static constexpr int kSoft = kD <= 128 ? 2 : 1;              // softmax warpgroups, issuers
-  static constexpr int kRows = kD == 256 ? 64 : 128 * kTiles;
-  static constexpr int kQRows = kD == 256 ? 64 : 128;          // of a tile in shared memory
+  static constexpr bool kSplit = kD <= 128;  // two streams of keys
+  static_assert(kSplit ? kGroup == 16 : kDup == 1, "copies of rows are joined as streams are");
+  static constexpr int kSoft = kSplit ? 2 : 1;             // softmax warpgroups, issuers
+  static constexpr int kRows = kD == 256 ? 64 : 128;       // of a row group
   static constexpr int kTile = 128;  // keys a block of the line
   static constexpr int kMinTiles = 4;
   static constexpr int kLift = 7;
@@ -63,12 +60,12 @@ struct DraftCfg {
   // Widened K and V: stages of 16 KB (D = 256: 32).  Stored bytes: three pieces of
   // 2 KB a converter warp.
   static constexpr int kStageKeys = kD == 64 ? 128 : 64, kStageBytes = kStageKeys * kD * 2;
-  static constexpr int kStagesK = kD == 256 ? 2 : 4, kStagesV = kD == 128 && !kSplit ? 2 : kStagesK;
+  static constexpr int kStages = kD == 256 ? 2 : 4;  // of K; of V alike
   static constexpr int kPieceKeys = 2048 / kD, kPieceBytes = 2048, kRing = 3;
   static constexpr int kPieces = kStageKeys / kPieceKeys;  // a stage: 4, 4, 8
   static constexpr int kStageUnits = kStageKeys / kKeys;
   // Issuers that are done with a stage, one after the other.
-  static constexpr int kReaders = kSplit ? kStageUnits : kTiles;
+  static constexpr int kReaders = kSplit ? kStageUnits : 1;
   static constexpr int kConvWarps = 8;  // half of them for K, half for V
   static constexpr int kThreads = 128 + 32 * kConvWarps + 128 * kSoft;
   // Registers: at launch 640 threads x 96 or 512 x 128.
@@ -79,21 +76,19 @@ struct DraftCfg {
                 "register split exceeds the launch allocation");
   static constexpr int kVecs = kD / 16;                              // 16-byte vectors a key
   static constexpr int kSet = kPieceBytes / 16 / 32;  // a lane's of a piece: 4
-  static constexpr int kQBytes = kQRows * kD * 2;
-  // 32 columns of the copies' outputs, for each stream: over the query rows (the
-  // second's behind the rings where those have too little room).
-  static constexpr int kHand = (128 - 128 / kDup) * 128;
-  static constexpr int kOffK = kTiles * kQBytes, kOffV = kOffK + kStagesK * kStageBytes;
-  static constexpr int kOffRing = kOffV + kStagesV * kStageBytes;
-  static constexpr int kOffHand1 = 2 * kHand <= kQBytes ? kHand : kOffRing + kConvWarps * kRing * kPieceBytes;
-  static constexpr int kOffInfo = kOffRing + kConvWarps * kRing * kPieceBytes + (kOffHand1 > kHand ? kHand : 0);
-  static_assert(kHand <= kQBytes, "room for the copies' outputs");
+  static constexpr int kQBytes = kRows * kD * 2;
+  // 16 columns of the copies' outputs, for each stream, over the query rows.
+  static constexpr int kHand = (128 - 128 / kDup) * 64;
+  static constexpr int kOffK = kQBytes, kOffV = kOffK + kStages * kStageBytes;
+  static constexpr int kOffRing = kOffV + kStages * kStageBytes;
+  static constexpr int kOffInfo = kOffRing + kConvWarps * kRing * kPieceBytes;
+  static_assert(2 * kHand <= kQBytes, "room for the copies' outputs");
   static constexpr int kColO = 256;  // S: two buffers of kKeys columns a stream; P over S
 };
 
-template <class C>
-struct DraftF16 : C {
-  static constexpr bool kF16 = true;
+template <class C, bool kF16_>
+struct DraftJoin : C {
+  static constexpr bool kF16 = kF16_;
 };
 
 constexpr int kDraftAhead = 16;   // blocks of keys that are looked up ahead, in batches of 4
@@ -107,13 +102,13 @@ struct DraftInfo {
   uint32_t line[kDraftWords][128 * C::kSoft];  // the drafts that a softmax thread's row sees
   float2 ml[2][128];                    // (streams) references and sums
   float rs[128];                        // (streams) a row's factor back
-  uint64_t q_full[2];                   // 4 softmax warps: query tile written
+  uint64_t q_full;                      // 4 softmax warps: query tile written
   uint64_t full[2][4], empty[2][4];     // [K, V][stage]
   uint64_t s_full[2][2];                // [stream][buffer]: S computed
   uint64_t p_ready[2][2];               // softmax wrote P (and rescaled O); a warp may be a unit ahead of another
   uint64_t o_ready[2][2];               // PV done, by buffer: nobody is two phases of one behind
   uint64_t info_full[4], info_empty[4], drain[2];
-  int n[2][2];                          // [stream][piece & 1]: blocks of a piece (0: no more), beside q_full
+  int n[2];                             // [piece & 1]: blocks of a piece (0: no more), beside q_full
   uint32_t tmem;
   int abort;
 };
@@ -163,11 +158,15 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   DecPlace at;
-  if (!dec_find<C>(p, blockIdx.x, at)) return;  // the whole block: nothing is set up yet
+  if (!dec_find<C>(p, blockIdx.x, at)) {  // the whole block: nothing is set up yet
+    if (tid == 0) p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    return;
+  }
   const int t0 = at.part * (int)blockIdx.x, t1 = (int)min((long long)at.total, (long long)t0 + at.part);
   if (tid == 0) {
+    p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    mbar_init(&info->q_full, 4);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&info->q_full[i], 4);
       mbar_init(&info->s_full[i][0], 1);
       mbar_init(&info->s_full[i][1], 1);
       mbar_init(&info->p_ready[i][0], 4);
@@ -211,7 +210,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
       const int t = warp;
       constexpr uint32_t idS = make_idesc_fmt(kFmtF16, 128, C::kKeys, false, false);
       constexpr uint32_t idPV = make_idesc_fmt(kFmtF16, 128, C::kD, false, true);
-      const uint64_t dQ = make_sdesc_sw128(smem_u32(smem + (C::kSplit ? 0 : t * C::kQBytes)), 16, 1024);
+      const uint64_t dQ = make_sdesc_sw128(smem_u32(smem), 16, 1024);
       const uint64_t dK = make_sdesc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
       const uint64_t dV = make_sdesc_sw128(smem_u32(smem + C::kOffV), C::kStageKeys * 128, 1024);
       const uint32_t lead = elect_lead();
@@ -222,23 +221,23 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
       constexpr int kLast = C::kStageUnits - 1;
       auto leaves = [&](int u) { return C::kSplit || u % C::kStageUnits == kLast; };
       auto issue_S = [&](int buf, int u) {
-        const uint64_t k0 = dK + (at_stage(u, C::kStagesK) >> 4);
+        const uint64_t k0 = dK + (at_stage(u, C::kStages) >> 4);
         const uint32_t dst = tmem + t * 128 + buf * C::kKeys;
 #pragma unroll
         for (int kk = 0; kk < C::kD / 16; ++kk)
-          mma_f16_ss_by(lead, dst, dQ + (kk / 4) * ((C::kQRows * 128) >> 4) + (kk % 4) * 2,
+          mma_f16_ss_by(lead, dst, dQ + (kk / 4) * ((C::kRows * 128) >> 4) + (kk % 4) * 2,
                         k0 + (kk / 4) * ((C::kStageKeys * 128) >> 4) + (kk % 4) * 2, idS, kk > 0 ? 1u : 0u);
         mma_commit_by(lead, &info->s_full[t][buf]);
-        if (leaves(u)) mma_commit_by(lead, &info->empty[0][(u / C::kStageUnits) & (C::kStagesK - 1)]);
+        if (leaves(u)) mma_commit_by(lead, &info->empty[0][(u / C::kStageUnits) & (C::kStages - 1)]);
       };
       auto issue_PV = [&](int buf, int u, bool first) {
-        const uint64_t v0 = dV + (at_stage(u, C::kStagesV) >> 4);
+        const uint64_t v0 = dV + (at_stage(u, C::kStages) >> 4);
         const uint32_t src = tmem + t * 128 + buf * C::kKeys, dst = tmem + C::kColO + t * C::kD;
 #pragma unroll
         for (int kk = 0; kk < C::kKeys / 16; ++kk)
           mma_f16_ts_by(lead, dst, src + kk * 8, v0 + ((kk * 16 * 128) >> 4), idPV, first && kk == 0 ? 0u : 1u);
         mma_commit_by(lead, &info->o_ready[t][buf]);
-        if (leaves(u)) mma_commit_by(lead, &info->empty[1][(u / C::kStageUnits) & (C::kStagesV - 1)]);
+        if (leaves(u)) mma_commit_by(lead, &info->empty[1][(u / C::kStageUnits) & (C::kStages - 1)]);
       };
       auto full = [&](int kv, int stages, int u) {
         const int nth = u / C::kStageUnits;
@@ -248,26 +247,25 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
       bool ok = true;
 #pragma unroll 1
       for (int pieces = 0; ok; ++pieces) {
-        uint64_t* const q_full = &info->q_full[C::kSplit ? 0 : t];
-        ok = prompt_warp_wait<true>(q_full, pieces & 1, abort, a);  // (query rows take a while to come)
+        ok = prompt_warp_wait<true>(&info->q_full, pieces & 1, abort, a);  // (query rows take a while to come)
         if (!ok) break;
-        const int n = info->n[C::kSplit ? 0 : t][pieces & 1];
+        const int n = info->n[pieces & 1];
         if (n == 0) break;
         const int begin = 2 * before + (C::kSplit ? t : 0), end = 2 * (before + n);
         before += n;
-        ok = full(0, C::kStagesK, begin);
+        ok = full(0, C::kStages, begin);
         if (!ok) break;
         tc_fence_after();
         issue_S(nth & 1, begin);
 #pragma unroll 1
         for (int u = begin; u < end; u += kUnitStep, ++nth) {
           if (u + kUnitStep < end) {  // the next scores go before this PV
-            ok = full(0, C::kStagesK, u + kUnitStep);
+            ok = full(0, C::kStages, u + kUnitStep);
             if (!ok) break;
             tc_fence_after();
             issue_S((nth + 1) & 1, u + kUnitStep);
           }
-          ok = full(1, C::kStagesV, u) && wait(&info->p_ready[t][nth & 1], (uint32_t)(nth >> 1) & 1u);
+          ok = full(1, C::kStages, u) && wait(&info->p_ready[t][nth & 1], (uint32_t)(nth >> 1) & 1u);
           if (!ok) break;
           tc_fence_after();
           issue_PV(nth & 1, u, u == begin);
@@ -351,7 +349,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
     const uint32_t mine = smem_u32(smem + C::kOffRing + (warp - 4) * C::kRing * C::kPieceBytes) + lane * 16;
     const uint8_t* const pool = (kv ? c.v : c.k) + vec * 16;
     const long long stride = kv ? c.vs[2] : c.ks[2];
-    const int stages = kv ? C::kStagesV : C::kStagesK, pieces = 128 / C::kPieceKeys * (t1 - t0);
+    const int stages = kv ? C::kStages : C::kStages, pieces = 128 / C::kPieceKeys * (t1 - t0);
     const bool e4m3 = p.kind == kKindE4m3;
     int known = 0;  // blocks that are looked up
     bool ok = true;
@@ -419,10 +417,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
     regs_inc<C::kRegsSoft>();
     const int t = (warp - 4 - C::kConvWarps) >> 2;
     const int tl = tid - (C::kThreads - 128 * C::kSoft) - 128 * t;  // row of the tile = TMEM lane
-    const int row_tile = C::kSplit ? 0 : t;
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tO = tmem + lane_addr + C::kColO + t * C::kD;  // the stream's output
-    uint8_t* q_tile = smem + row_tile * C::kQBytes;
     constexpr int kMine = C::kKeys / C::kDup, kGroups = kMine / C::kGroup;  // keys of a score buffer a thread weighs; groups
     constexpr int kCopy = 128 / C::kDup;                                    // rows of a copy
     const int copy = C::kDup > 1 ? tl / kCopy : 0;                          // (a warp's)
@@ -436,8 +432,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
       const int2 span = dec_group_span<C>(p, at.seq, at.rg);
       const int first = span.x / 128 + pos - at.seg0;
       const bool whole = n == tiles, head_cut = pos > at.seg0;
-      const int row = C::kDup > 1 ? tl & (kCopy - 1) : at.rg * C::kRows + row_tile * 128 + tl, i = row / a.group, head = at.h * a.group + row % a.group;
-      const bool real = tl < C::kQRows && row < p.rows;
+      const int row = C::kDup > 1 ? tl & (kCopy - 1) : at.rg * C::kRows + tl, i = row / a.group, head = at.h * a.group + row % a.group;
+      const bool real = tl < C::kRows && row < p.rows;
       const int base = at.seq.len - at.seq.nq;  // the first draft's slot
       const bool some = real && i < at.seq.nq && base + i >= 0;
       // Does any row of this warp's count?  (With copies, all warps go on together.)
@@ -455,8 +451,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
         constexpr int kLanes = C::kD / 8, kAtOnce = 32 / kLanes;  // rows a copy
         const long long from = some ? (at.b * a.qs[0] + head * a.qs[1] + i * a.qs[2]) * 2 : -1;
         const int r0 = (warp & 3) * 32, c16 = lane % kLanes;
-        if (r0 < C::kQRows) {
-          uint8_t* const col = q_tile + (c16 / 8) * (C::kQRows * 128);
+        if (r0 < C::kRows) {
+          uint8_t* const col = smem + (c16 / 8) * (C::kRows * 128);
 #pragma unroll 2
           for (int r = lane / kLanes; r < 32; r += kAtOnce) {
             const long long off = __shfl_sync(0xFFFFFFFFu, from, r);
@@ -466,11 +462,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
           asm volatile("cp.async.wait_all;" ::: "memory");
           __syncwarp();
           if (!p.f16) {
-            uint8_t* const mine = q_tile + tl * 128;
+            uint8_t* const mine = smem + tl * 128;
             float top = 0.0f, up;
 #pragma unroll 4
             for (int c = 0; c < kLanes; ++c) {
-              const uint4 w = *reinterpret_cast<const uint4*>(mine + (c / 8) * (C::kQRows * 128) + (((c % 8) ^ (tl & 7)) << 4));
+              const uint4 w = *reinterpret_cast<const uint4*>(mine + (c / 8) * (C::kRows * 128) + (((c % 8) ^ (tl & 7)) << 4));
               const uint32_t* x = &w.x;
 #pragma unroll
               for (int e = 0; e < 4; ++e)
@@ -479,7 +475,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
             dec_row_scale(top, up, rs);
 #pragma unroll 4
             for (int c = 0; c < kLanes; ++c) {
-              uint4* const at16 = reinterpret_cast<uint4*>(mine + (c / 8) * (C::kQRows * 128) + (((c % 8) ^ (tl & 7)) << 4));
+              uint4* const at16 = reinterpret_cast<uint4*>(mine + (c / 8) * (C::kRows * 128) + (((c % 8) ^ (tl & 7)) << 4));
               uint4 w = *at16;
               uint32_t* x = &w.x;
 #pragma unroll
@@ -492,8 +488,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if ((warp & 3) == 0) info->n[t][pieces & 1] = n;
-          mbar_arrive(&info->q_full[t]);
+          if ((warp & 3) == 0) info->n[pieces & 1] = n;
+          mbar_arrive(&info->q_full);
         }
         if constexpr (C::kSplit) info->rs[tl] = rs;
       }
@@ -637,7 +633,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
       if (ok) ok = landed(nth - 1);
       // (a NaN row stays one; one that is none, or that sees nothing, has no sum)
       if (!some) l = 0.0f;
-      const long long slot = (long long)(2 * blockIdx.x + (head_cut ? 0 : 1)) * C::kRows + (C::kDup > 1 ? row : row_tile * 128 + tl);
+      const long long slot = (long long)(2 * blockIdx.x + (head_cut ? 0 : 1)) * C::kRows + (C::kDup > 1 ? row : tl);
       uint8_t* dst = static_cast<uint8_t*>(a.o) + (at.b * a.os[0] + head * a.os[1] + i * a.os[2]) * 2;
       float f0 = 1.0f, f1 = 0.0f;  // of the two streams' outputs
       if constexpr (C::kSplit) {
@@ -674,27 +670,27 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
       constexpr int kCols = C::kSplit ? C::kD / 2 : C::kD;
       const uint32_t tO0 = C::kSplit ? tmem + lane_addr + C::kColO : tO, tO1 = tO0 + C::kD;
       const int d0 = C::kSplit ? t * kCols : 0;
-      uint8_t* const hand = smem + t * C::kOffHand1;
+      uint8_t* const hand = smem + t * C::kHand;
       if (work) {
 #pragma unroll 1
-        for (int d = d0; d < d0 + kCols; d += 32) {
-          uint32_t rr[32], ro[C::kSplit ? 32 : 1] = {};
-          tmem_ld32(tO0 + d, rr);
-          if constexpr (C::kSplit) tmem_ld32(tO1 + d, ro);
+        for (int d = d0; d < d0 + kCols; d += 16) {
+          uint32_t rr[16], ro[C::kSplit ? 16 : 1] = {};
+          tmem_ld16(tO0 + d, rr);
+          if constexpr (C::kSplit) tmem_ld16(tO1 + d, ro);
           tmem_wait_ld();
           reg_fence(rr);
           reg_fence(ro);
-          float o[32];
+          float o[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
+          for (int e = 0; e < 16; ++e) {
             o[e] = __uint_as_float(rr[e]) * f0;
             if constexpr (C::kSplit) o[e] = fmaf(__uint_as_float(ro[e]), f1, o[e]);
           }
           if constexpr (C::kDup > 1) {
             if (copy > 0) {
 #pragma unroll
-              for (int u = 0; u < 8; ++u)
-                *reinterpret_cast<float4*>(hand + (tl - kCopy) * 128 + ((u ^ (tl & 7)) << 4)) =
+              for (int u = 0; u < 4; ++u)
+                *reinterpret_cast<float4*>(hand + (tl - kCopy) * 64 + ((u ^ ((tl >> 1) & 3)) << 4)) =
                     make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
             }
             named_bar_sync(1 + t, 128);
@@ -702,8 +698,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
 #pragma unroll
               for (int q = 0; q < C::kDup - 1; ++q)
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                  const float4 y = *reinterpret_cast<const float4*>(hand + (q * kCopy + tl) * 128 + ((u ^ (tl & 7)) << 4));
+                for (int u = 0; u < 4; ++u) {
+                  const float4 y = *reinterpret_cast<const float4*>(hand + (q * kCopy + tl) * 64 + ((u ^ ((tl >> 1) & 3)) << 4));
                   o[4 * u] += y.x, o[4 * u + 1] += y.y, o[4 * u + 2] += y.z, o[4 * u + 3] += y.w;
                 }
             }
@@ -711,10 +707,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
           }
           if (real && copy == 0) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = none ? 0.0f : o[e];
+            for (int e = 0; e < 16; ++e) o[e] = none ? 0.0f : o[e];
             if (whole) {
 #pragma unroll
-              for (int u = 0; u < 4; ++u) {
+              for (int u = 0; u < 2; ++u) {
                 uint32_t y[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -724,7 +720,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
             } else {
               float4* part = reinterpret_cast<float4*>(p.part_o + slot * C::kD + d);
 #pragma unroll
-              for (int u = 0; u < 8; ++u) part[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+              for (int u = 0; u < 4; ++u) part[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
             }
           }
           __syncwarp();
@@ -736,6 +732,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
           a.lse[((long long)at.b * a.Hq + head) * a.n + i] = none ? -INFINITY : ((m + C::kLift) + lg2(l)) * kDecLn2;
         else
           p.part_ml[slot] = make_float2(none ? -INFINITY : m, l);
+        // (a segment that begins here and goes on in blocks up to the last one named)
+        if (tl == 0 && !whole && !head_cut)
+          p.cuts[blockIdx.x] = make_int4(at.b, at.h, at.rg, (at.seg0 + tiles - 1) / at.part);
       }
       if constexpr (C::kSplit) named_bar_sync(3, 256);  // both outputs have been read
       before += n;
@@ -743,8 +742,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
       dec_next(p, at, tiles);
     }
     if (ok && lane == 0 && (!C::kSplit || t == 0)) {
-      if ((warp & 3) == 0) info->n[t][pieces & 1] = 0;
-      mbar_arrive(&info->q_full[t]);
+      if ((warp & 3) == 0) info->n[pieces & 1] = 0;
+      mbar_arrive(&info->q_full);
     }
     tmem_wait_st();  // (behind an expired wait, weights may be on their way to memory that is given back below)
   }
@@ -754,6 +753,35 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+// Joins the parts of a cut segment, four columns a thread.  The block that began
+// it has left where it is and how far it goes: to find that again, as
+// cache_join_kernel does, took these grids 11 us and more, since none of their blocks
+// fits beside the attention's.
+template <class C, bool kF16>
+__global__ void __launch_bounds__(kJoinThreads) cache_drafts_join_kernel(const __grid_constant__ DecParams p) {
+  const CacheAttnParams& a = p.a;
+  constexpr int kAtOnce = kJoinThreads / (C::kD / 4);  // rows
+  const int c0 = blockIdx.y, r = blockIdx.x * kAtOnce + threadIdx.x / (C::kD / 4), d = threadIdx.x % (C::kD / 4) * 4;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
+  const int4 cut = __ldcg(p.cuts + c0);
+  const int row = cut.z * C::kRows + r;
+  if (cut.x < 0 || r >= C::kRows || row >= p.rows) return;
+  float top = -INFINITY, sum = 0.0f;
+  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int i = c0; i <= cut.w; ++i) {
+    const long long slot = (long long)(2 * i + (i == c0)) * C::kRows + r;
+    const float2 ml = __ldcg(p.part_ml + slot);
+    const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part_o + slot * C::kD + d));
+    const float m2 = fmaxf(top, ml.x), z = m2 == -INFINITY ? 0.0f : m2;
+    const float f = ex2(top - z), g = ex2(ml.x - z);
+    top = m2;
+    sum = fmaf(sum, f, ml.y * g);
+    x.x = fmaf(x.x, f, y.x * g), x.y = fmaf(x.y, f, y.y * g), x.z = fmaf(x.z, f, y.z * g), x.w = fmaf(x.w, f, y.w * g);
+  }
+  dec_write<DraftJoin<C, kF16>>(a, cut.x, cut.y, row, d, x, top, sum);
 }
 
 }  // namespace fa

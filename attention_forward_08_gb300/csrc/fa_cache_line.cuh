@@ -41,6 +41,7 @@ struct DecParams {
   int max_ctas;
   int kind;               // of the stored values, and is q f16: where a kernel asks at run time
   bool f16;
+  int4* cuts;             // [max_ctas] (drafts): the segment that a block begins and does not end: sequence, head, row group, last block
   float* part_o;          // [2 * max_ctas, kRows, D]
   float2* part_ml;        // [2 * max_ctas, kRows]: reference, sum
   float* scores;          // [B, H, M * page / 32, rows, 32]: scores in base 2, for the weights (or NULL)
@@ -72,11 +73,12 @@ __device__ __forceinline__ int2 dec_span(const CacheAttnParams& a, const DecSeq&
   const int lo = a.window > 0 ? max(0, max(0, p0) - a.window + 1) : 0;
   return lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
 }
-// ... and the query rows of row group rg.
+// ... and the query rows of row group rg.  (A tree's row groups see the same
+// tokens but for a few at the end, and all count as the last one.)
 template <class C>
 __device__ __forceinline__ int2 dec_group_span(const DecParams& p, const DecSeq& s, int rg) {
-  if (p.row_groups == 1) return dec_span<C::kTree>(p.a, s, 0, p.a.n - 1);
-  return dec_span<C::kTree>(p.a, s, rg * C::kRows / p.a.group, (min(p.rows, (rg + 1) * C::kRows) - 1) / p.a.group);
+  if (C::kTree || p.row_groups == 1) return dec_span<C::kTree>(p.a, s, 0, p.a.n - 1);
+  return dec_span(p.a, s, rg * C::kRows / p.a.group, (min(p.rows, (rg + 1) * C::kRows) - 1) / p.a.group);
 }
 
 // Tiles of one segment: at least one, so that empty rows are written too.
@@ -109,9 +111,11 @@ __device__ __forceinline__ int dec_part(const DecParams& p, int total);
 // take one load.  (The host keeps all counts below 2^31.)  False past the end.
 template <class C>
 __device__ __forceinline__ bool dec_find(const DecParams& p, int nth, DecPlace& at) {
-  const int lane = threadIdx.x & 31, B = p.a.B, H = p.a.c.H;
+  // (A tree's row groups are alike, as heads are.)
+  const bool alike = C::kTree || p.row_groups == 1;
+  const int lane = threadIdx.x & 31, B = p.a.B, H = C::kTree ? p.a.c.H * p.row_groups : p.a.c.H;
   int mine = 0, total = 0, head = 0;
-  if (p.row_groups == 1) {
+  if (alike) {
 #pragma unroll 1
     for (int i = lane; i < B; i += 32) {
       mine = dec_tiles<C>(p, dec_seq(p.a, i), 0) * H;
@@ -128,7 +132,7 @@ __device__ __forceinline__ bool dec_find(const DecParams& p, int nth, DecPlace& 
   if ((long long)at.part * nth >= total) return false;
   const int t = at.part * nth;
   int before = 0;
-  if (p.row_groups == 1) {
+  if (alike) {
 #pragma unroll 1
     for (int base = 0;; base += 32) {
       if (B > 32) mine = base + lane < B ? dec_tiles<C>(p, dec_seq(p.a, base + lane), 0) * H : 0;
@@ -161,7 +165,10 @@ __device__ __forceinline__ bool dec_find(const DecParams& p, int nth, DecPlace& 
   }
   at.h = (int)((unsigned)(t - before) / (unsigned)head);
   at.seg0 = before + at.h * head;
-  if (p.row_groups > 1) {
+  if constexpr (C::kTree) {
+    at.rg = at.h % p.row_groups;
+    at.h /= p.row_groups;
+  } else if (p.row_groups > 1) {
 #pragma unroll 1
     for (int base = 0;; base += 32) {  // row groups, 32 at a time
       const int n = base + lane < p.row_groups ? dec_tiles<C>(p, at.seq, base + lane) : 0;
