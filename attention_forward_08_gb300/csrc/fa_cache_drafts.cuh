@@ -77,12 +77,14 @@ struct DraftCfg {
   static constexpr int kVecs = kD / 16;                              // 16-byte vectors a key
   static constexpr int kSet = kPieceBytes / 16 / 32;  // a lane's of a piece: 4
   static constexpr int kQBytes = kRows * kD * 2;
-  // 16 columns of the copies' outputs, for each stream, over the query rows.
-  static constexpr int kHand = (128 - 128 / kDup) * 64;
+  // Columns of an output that are written at a time; the copies' for both streams
+  // over the query rows, as far as those go.
+  static constexpr int kChunk = kDup > 1 ? 32 : 16, kHand = (128 - 128 / kDup) * 128;
   static constexpr int kOffK = kQBytes, kOffV = kOffK + kStages * kStageBytes;
   static constexpr int kOffRing = kOffV + kStages * kStageBytes;
-  static constexpr int kOffInfo = kOffRing + kConvWarps * kRing * kPieceBytes;
-  static_assert(2 * kHand <= kQBytes, "room for the copies' outputs");
+  static constexpr int kOffHand1 = 2 * kHand <= kQBytes ? kHand : kOffRing + kConvWarps * kRing * kPieceBytes;
+  static constexpr int kOffInfo = kOffRing + kConvWarps * kRing * kPieceBytes + (kOffHand1 > kHand ? kHand : 0);
+  static_assert(kHand <= kQBytes, "room for the copies' outputs");
   static constexpr int kColO = 256;  // S: two buffers of kKeys columns a stream; P over S
 };
 
@@ -347,9 +349,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
     uint8_t* const to = smem + (kv ? C::kOffV : C::kOffK) + (uint32_t)(vec / 4) * (C::kStageKeys * 128) + key0 * 128;
     const uint32_t lo16 = (((vec % 4) * 2) ^ key0) << 4, hi16 = (((vec % 4) * 2 + 1) ^ key0) << 4;
     const uint32_t mine = smem_u32(smem + C::kOffRing + (warp - 4) * C::kRing * C::kPieceBytes) + lane * 16;
-    const uint8_t* const pool = (kv ? c.v : c.k) + vec * 16;
     const long long stride = kv ? c.vs[2] : c.ks[2];
-    const int stages = kv ? C::kStages : C::kStages, pieces = 128 / C::kPieceKeys * (t1 - t0);
+    const uint8_t* const pool = (kv ? c.v : c.k) + vec * 16 + key0 * stride;
+    const int pieces = 128 / C::kPieceKeys * (t1 - t0);
     const bool e4m3 = p.kind == kKindE4m3;
     int known = 0;  // blocks that are looked up
     bool ok = true;
@@ -371,11 +373,16 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
           keys[g] = info->range[at][first / 16 + g] >> (16 * kv);
         }
 #pragma unroll
-        for (int u = 0; u < C::kSet; ++u) {
-          const int g = u * kKeysWarp / 16, r = first % 16 + key0 + u * kKeysWarp - 16 * g;
-          // (zeros where nobody sees them or nothing is stored)
-          copy16(mine + slot * C::kPieceBytes + u * 512, pool + off[g] + r * stride,
-                 r >= (keys[g] & 255) && r < ((keys[g] >> 8) & 255));
+        for (int g = 0; g < kGroupsHere; ++g) {
+          constexpr int kOfGroup = C::kSet / kGroupsHere;
+          const uint8_t* from = pool + off[g] + first % 16 * stride;
+          const int lo = keys[g] & 255, hi = (keys[g] >> 8) & 255;
+#pragma unroll
+          for (int u = 0; u < kOfGroup; ++u, from += kKeysWarp * stride) {
+            const int r = first % 16 + key0 + u * kKeysWarp;
+            // (zeros where nobody sees them or nothing is stored)
+            copy16(mine + slot * C::kPieceBytes + (g * kOfGroup + u) * 512, from, r >= lo && r < hi);
+          }
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -385,13 +392,15 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
     int slot = 0;
 #pragma unroll 1
     for (int k = cw; k < pieces && ok; k += kTeam) {
-      const int nth = k / C::kPieces, part = k % C::kPieces, stage = nth & (stages - 1);
+      const int nth = k / C::kPieces, part = k % C::kPieces, stage = nth & (C::kStages - 1);
+      // (asked early, so that the answer is there when it is needed)
+      const bool room = nth < C::kStages || mbar_test(&info->empty[kv][stage], (uint32_t)(nth / C::kStages + 1) & 1u);
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       uint4 x[C::kSet];
 #pragma unroll
       for (int u = 0; u < C::kSet; ++u) x[u] = lds128(mine + slot * C::kPieceBytes + u * 512);
       copy(k + 2 * kTeam, slot + 2 >= C::kRing ? slot + 2 - C::kRing : slot + 2);
-      if (nth >= stages) ok = ok && wait(&info->empty[kv][stage], (uint32_t)(nth / stages + 1) & 1u);
+      if (!__all_sync(0xFFFFFFFFu, room)) ok = ok && wait(&info->empty[kv][stage], (uint32_t)(nth / C::kStages + 1) & 1u);
       if (!ok) break;
       uint8_t* const row = to + stage * C::kStageBytes + part * (C::kPieceKeys * 128);
       auto widen = [&](auto kind) {
@@ -670,27 +679,30 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
       constexpr int kCols = C::kSplit ? C::kD / 2 : C::kD;
       const uint32_t tO0 = C::kSplit ? tmem + lane_addr + C::kColO : tO, tO1 = tO0 + C::kD;
       const int d0 = C::kSplit ? t * kCols : 0;
-      uint8_t* const hand = smem + t * C::kHand;
+      uint8_t* const hand = smem + t * C::kOffHand1;
       if (work) {
 #pragma unroll 1
-        for (int d = d0; d < d0 + kCols; d += 16) {
-          uint32_t rr[16], ro[C::kSplit ? 16 : 1] = {};
-          tmem_ld16(tO0 + d, rr);
-          if constexpr (C::kSplit) tmem_ld16(tO1 + d, ro);
+        for (int d = d0; d < d0 + kCols; d += C::kChunk) {
+          constexpr int kN = C::kChunk;
+          uint32_t rr[kN], ro[C::kSplit ? kN : 1] = {};
+          if constexpr (kN == 16) tmem_ld16(tO0 + d, rr);
+          else tmem_ld32(tO0 + d, rr);
+          if constexpr (C::kSplit && kN == 16) tmem_ld16(tO1 + d, ro);
+          else if constexpr (C::kSplit) tmem_ld32(tO1 + d, ro);
           tmem_wait_ld();
           reg_fence(rr);
           reg_fence(ro);
-          float o[16];
+          float o[kN];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
+          for (int e = 0; e < kN; ++e) {
             o[e] = __uint_as_float(rr[e]) * f0;
             if constexpr (C::kSplit) o[e] = fmaf(__uint_as_float(ro[e]), f1, o[e]);
           }
           if constexpr (C::kDup > 1) {
             if (copy > 0) {
 #pragma unroll
-              for (int u = 0; u < 4; ++u)
-                *reinterpret_cast<float4*>(hand + (tl - kCopy) * 64 + ((u ^ ((tl >> 1) & 3)) << 4)) =
+              for (int u = 0; u < kN / 4; ++u)
+                *reinterpret_cast<float4*>(hand + (tl - kCopy) * 128 + ((u ^ (tl & 7)) << 4)) =
                     make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
             }
             named_bar_sync(1 + t, 128);
@@ -698,8 +710,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
 #pragma unroll
               for (int q = 0; q < C::kDup - 1; ++q)
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                  const float4 y = *reinterpret_cast<const float4*>(hand + (q * kCopy + tl) * 64 + ((u ^ ((tl >> 1) & 3)) << 4));
+                for (int u = 0; u < kN / 4; ++u) {
+                  const float4 y = *reinterpret_cast<const float4*>(hand + (q * kCopy + tl) * 128 + ((u ^ (tl & 7)) << 4));
                   o[4 * u] += y.x, o[4 * u + 1] += y.y, o[4 * u + 2] += y.z, o[4 * u + 3] += y.w;
                 }
             }
@@ -707,10 +719,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
           }
           if (real && copy == 0) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = none ? 0.0f : o[e];
+            for (int e = 0; e < kN; ++e) o[e] = none ? 0.0f : o[e];
             if (whole) {
 #pragma unroll
-              for (int u = 0; u < 2; ++u) {
+              for (int u = 0; u < kN / 8; ++u) {
                 uint32_t y[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -720,7 +732,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
             } else {
               float4* part = reinterpret_cast<float4*>(p.part_o + slot * C::kD + d);
 #pragma unroll
-              for (int u = 0; u < 4; ++u) part[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+              for (int u = 0; u < kN / 4; ++u) part[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
             }
           }
           __syncwarp();
