@@ -93,7 +93,7 @@ struct VerifyParams {
   const int* n_q;
   int *path, *count, *token;      // path [B, n] contiguous
   int B, n, V;
-  int seg;                        // vocabulary entries a warp takes (set by the launch)
+  int blocks, seg;                // blocks a sequence, vocabulary entries a warp (set by the launch)
   unsigned int* status;
 };
 
