@@ -13,9 +13,10 @@
 //
 // A token is the least t whose cumulative sum passes u Z.  With a vocabulary of
 // 10^5 two sums in 32 bits would disagree about t once in a hundred calls, so
-// terms and partial sums are pairs of floats (48 bits; error-free sums and
-// products), and 64 bits from a warp on: doubles for every term would take the
-// few FP64 units ten times the memory's time.  All orders are fixed.
+// terms and sums are pairs of floats (48 bits; error-free sums and products):
+// doubles for every term would take the few FP64 units ten times the memory's
+// time, and doubles for the walk and the sums of segments alone took half of a
+// single sequence's (12.4 us).  All orders are fixed.
 //
 // Work.  A cluster of 2 to 8 blocks a sequence.  Tests need two numbers a node, which
 // every block gathers for itself and walks over alike, so that decisions are
@@ -55,19 +56,20 @@ __device__ __forceinline__ uint32_t ver_rank() {
 __device__ __forceinline__ void ver_cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// A number of 48 bits: hi + lo.
+struct Pair {
+  float hi, lo;
+};
 // Writes x where `p` lies in block `rank` of the cluster.
-__device__ __forceinline__ void ver_send(double* p, uint32_t rank, double x) {
+__device__ __forceinline__ void ver_send(Pair* p, uint32_t rank, Pair x) {
   uint32_t at;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
                : "=r"(at)
                : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(at), "d"(x) : "memory");
+  asm volatile("st.shared::cluster.f32 [%0], %1;\n\tst.shared::cluster.f32 [%0 + 4], %2;" ::"r"(at), "f"(x.hi), "f"(x.lo)
+               : "memory");
 }
 
-// A sum of 48 bits: hi + lo.
-struct Pair {
-  float hi, lo;
-};
 // (intrinsics: nothing here may be contracted or reordered)
 __device__ __forceinline__ void pair_add(Pair& a, float hi, float lo) {
   const float s = __fadd_rn(a.hi, hi), b = __fsub_rn(s, a.hi);
@@ -75,6 +77,17 @@ __device__ __forceinline__ void pair_add(Pair& a, float hi, float lo) {
   a.hi = s;
   a.lo = __fadd_rn(a.lo, __fadd_rn(e, lo));
 }
+__device__ __forceinline__ Pair pair_sum(Pair a, Pair b) {  // normalised
+  pair_add(a, b.hi, b.lo);
+  const float s = __fadd_rn(a.hi, a.lo);
+  return {s, __fsub_rn(a.lo, __fsub_rn(s, a.hi))};
+}
+__device__ __forceinline__ Pair pair_minus(Pair a, Pair b) { return pair_sum(a, {-b.hi, -b.lo}); }
+__device__ __forceinline__ Pair pair_times(Pair a, float b) {
+  const float h = __fmul_rn(a.hi, b);
+  return pair_sum({h, 0.0f}, {__fmaf_rn(a.lo, b, __fmaf_rn(a.hi, b, -h)), 0.0f});
+}
+__device__ __forceinline__ bool pair_above(Pair a, Pair b) { return pair_minus(a, b).hi > 0.0f; }
 // max(p - c q, 0).
 __device__ __forceinline__ Pair ver_less(float p, float q, Pair c) {
   const float h = __fmul_rn(c.hi, q);
@@ -92,11 +105,14 @@ __device__ __forceinline__ Pair ver_warp_sum(Pair x) {
   }
   return x;
 }
-__device__ __forceinline__ double ver_upto(double x, int lane) {  // inclusive sum over the lanes
+__device__ __forceinline__ Pair ver_lane(Pair x, int lane) {
+  return {__shfl_sync(0xFFFFFFFFu, x.hi, lane), __shfl_sync(0xFFFFFFFFu, x.lo, lane)};
+}
+__device__ __forceinline__ Pair ver_upto(Pair x, int lane) {  // inclusive sum over the lanes
 #pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
-    const double y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-    if (lane >= o) x += y;
+    const Pair y = {__shfl_up_sync(0xFFFFFFFFu, x.hi, o), __shfl_up_sync(0xFFFFFFFFu, x.lo, o)};
+    if (lane >= o) x = pair_sum(x, y);
   }
   return x;
 }
@@ -104,23 +120,24 @@ __device__ __forceinline__ double ver_upto(double x, int lane) {  // inclusive s
 // Of values x in order, a lane each, `upto` their inclusive sums: the first whose
 // sum passes `rest` (the last that is not 0 where none does: u of 1, a rounding;
 // -1: all are 0).  What is left of `rest` before it.
-__device__ __forceinline__ int ver_find(double x, double upto, double& rest) {
-  const uint32_t some = __ballot_sync(0xFFFFFFFFu, x > 0.0), hit = __ballot_sync(0xFFFFFFFFu, x > 0.0 && upto > rest);
+__device__ __forceinline__ int ver_find(Pair x, Pair upto, Pair& rest) {
+  const bool is = x.hi > 0.0f;
+  const uint32_t some = __ballot_sync(0xFFFFFFFFu, is), hit = __ballot_sync(0xFFFFFFFFu, is && pair_above(upto, rest));
   if (!some) return -1;
   const int l = hit ? __ffs(hit) - 1 : 31 - __clz(some);
-  rest = __shfl_sync(0xFFFFFFFFu, rest - (upto - x), l);
+  const Pair before = ver_lane(upto, max(l - 1, 0));
+  if (l > 0) rest = pair_minus(rest, before);
   return l;
 }
 
 struct VerShared {
-  double sum[2][kVerWarps * kVerMostBlocks];  // of the segments, by pass & 1
-  double part[kVerWarps];                     // of the chosen segment's pieces
+  Pair sum[2][kVerWarps * kVerMostBlocks];  // of the segments, by pass & 1
+  Pair part[kVerWarps];                     // of the chosen segment's pieces
   // What comes next: a pass over r = max(p[cur] - c q[cur], 0), without the
   // candidates below cur where `gone`; or the path's length, the segment that
   // holds the token, and what is left of the sum sought there.
   int ends, cur, gone, count, seg;
-  Pair c;
-  double rest;
+  Pair c, rest;
 };
 
 // What is left of a row.
@@ -130,7 +147,6 @@ struct VerRow {
   Pair c;
   const uint32_t* gone;  // bit by entry - first: rejected candidates; or NULL
   int first;
-  static constexpr int kAtOnce = 8;
   __device__ __forceinline__ float left(int e, float x) const {
     return (gone[(e - first) >> 5] >> ((e - first) & 31)) & 1u ? 0.0f : x;
   }
@@ -139,8 +155,8 @@ struct VerRow {
     if (q) return ver_less(x, ver_prob(ver_load(q + e)), c);
     return {gone ? left(e, x) : x, 0.0f};
   }
-  // This lane's sum over entries e0 + lane, e0 + lane + 32, .. < e1.  (A wait of
-  // all entries' memory at once: 8 of a lane's at a time come from L2.)
+  // This lane's sum over entries e0 + lane, e0 + lane + 32, .. < e1.  (All are
+  // asked for at once, into L2.)
   __device__ __forceinline__ Pair sum(int e0, int e1) const {
     const int lane = threadIdx.x & 31;
     constexpr int kLine = 128 / sizeof(T);
@@ -150,12 +166,13 @@ struct VerRow {
       if (q) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + e));
     }
     Pair s = {0.0f, 0.0f};
+    if (q) {
+      constexpr int kAtOnce = 8;
 #pragma unroll 1
-    for (int e = e0 + lane; e < e1; e += 32 * kAtOnce) {
-      float x[kAtOnce], y[kAtOnce];
+      for (int e = e0 + lane; e < e1; e += 32 * kAtOnce) {
+        float x[kAtOnce], y[kAtOnce];
 #pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) x[u] = e + 32 * u < e1 ? ver_load(p + e + 32 * u) : 0.0f;
-      if (q) {
+        for (int u = 0; u < kAtOnce; ++u) x[u] = e + 32 * u < e1 ? ver_load(p + e + 32 * u) : 0.0f;
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) y[u] = e + 32 * u < e1 ? ver_load(q + e + 32 * u) : 0.0f;
 #pragma unroll
@@ -163,7 +180,14 @@ struct VerRow {
           const Pair r = ver_less(ver_prob(x[u]), ver_prob(y[u]), c);
           pair_add(s, r.hi, r.lo);
         }
-      } else {
+      }
+    } else {
+      constexpr int kAtOnce = 16;
+#pragma unroll 1
+      for (int e = e0 + lane; e < e1; e += 32 * kAtOnce) {
+        float x[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) x[u] = e + 32 * u < e1 ? ver_load(p + e + 32 * u) : 0.0f;
         if (gone) {
 #pragma unroll
           for (int u = 0; u < kAtOnce; ++u) x[u] = left(min(e + 32 * u, e1 - 1), x[u]);
@@ -235,19 +259,20 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyPara
   // next, nodes of the path; c, and the sum of what is left; whether the path
   // has ended, the last pass's sums are those of what is left, and they are p's.
   int cur = 0, next = 1, count = 1;
-  double c = 0.0, z = 1.0;
+  Pair c = {0.0f, 0.0f}, z = {1.0f, 0.0f};
   bool over = false, summed = false, bare = false;
+  bool taken = false;  // the last pass was without rejected candidates
   const int per = (kVerWarps * blocks + 31) / 32;  // segments a lane
-  double mine = 0.0, upto = 0.0;                   // of its segments, and with the lanes before
+  Pair mine, upto;                                 // of its segments, and with the lanes before
 #pragma unroll 1
   for (int passes = 0;; ++passes) {
-    const double* const sums = s.sum[(passes - 1) & 1];  // (the last pass's)
+    const Pair* const sums = s.sum[(passes - 1) & 1];  // (the last pass's)
     if (warp == 0) {
       if (passes > 0) {
-        mine = 0.0;
-        for (int i = lane * per; i < min((lane + 1) * per, kVerWarps * blocks); ++i) mine += sums[i];
+        mine = {0.0f, 0.0f};
+        for (int i = lane * per; i < min((lane + 1) * per, kVerWarps * blocks); ++i) mine = pair_sum(mine, sums[i]);
         upto = ver_upto(mine, lane);
-        z = __shfl_sync(0xFFFFFFFFu, upto, 31);
+        z = ver_lane(upto, 31);
       }
       // the walk, up to the path's end or to a sum that it needs
       bool gone = false, ends = false;
@@ -266,47 +291,49 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyPara
         over = i < 0;
         if (over) break;
         next = i + 1;
-        const double pi = (double)s_p[i], qi = drafts ? (double)s_q[i] : 1.0;
-        const double r = drafts ? fmax(pi - c * qi, 0.0) : pi;
-        if ((double)s_u[i] * qi * z < r) {
+        const float pi = s_p[i];
+        Pair r = {pi, 0.0f}, least = pair_times(z, s_u[i]);
+        if (drafts) {
+          const Pair d = pair_sum(r, pair_times(c, -s_q[i]));
+          r = d.hi > 0.0f ? d : Pair{0.0f, 0.0f};
+          least = pair_times(least, s_q[i]);
+        }
+        if (pair_above(r, least)) {
           if (rank == 0 && lane == 0) path[count] = i;
           ++count;
           cur = i;
-          c = 0.0;
-          z = 1.0;
+          c = {0.0f, 0.0f};
+          z = {1.0f, 0.0f};
           summed = false;
         } else if (drafts) {
-          c += z;
+          c = pair_sum(c, z);
           summed = true;
           break;
         } else {
-          z -= r;
+          z = pair_minus(z, r);
         }
       }
       if (over) {
         if (!summed) {  // (the path ended with an accepted node, or there is no q)
           gone = !drafts;
           summed = true;
-        } else if (z == 0.0 && !bare) {  // nothing is left: of p itself
-          c = 0.0;
+        } else if (z.hi == 0.0f && !bare) {  // nothing is left: of p itself
+          c = {0.0f, 0.0f};
           bare = true;
         } else {  // the segment that holds the token
           ends = true;
-          const double u = (double)p.u_next[b];
-          double rest = (u > 0.0 ? fmin(u, 1.0) : 0.0) * z;
+          const float u = p.u_next[b];
+          Pair rest = pair_times(z, u > 0.0f ? fminf(u, 1.0f) : 0.0f);
           int seg = ver_find(mine, upto, rest);
           if (seg >= 0) {
             const int i = seg * per + lane;
-            const double x = lane < per && i < kVerWarps * blocks ? sums[i] : 0.0;
+            const Pair x = lane < per && i < kVerWarps * blocks ? sums[i] : Pair{0.0f, 0.0f};
             seg = seg * per + max(ver_find(x, ver_upto(x, lane), rest), 0);
           }
           if (lane == 0) s.seg = seg, s.rest = rest;
         }
       }
-      if (lane == 0) {
-        const float hi = (float)c;
-        s.ends = ends, s.cur = cur, s.gone = gone, s.count = count, s.c = {hi, (float)(c - (double)hi)};
-      }
+      if (lane == 0) s.ends = ends, s.cur = cur, s.gone = gone, s.count = count, s.c = c;
     }
     __syncthreads();
     if (s.ends) break;
@@ -315,18 +342,23 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyPara
     row.c = s.c;
     row.p = probs + s.cur * p.ps[1];
     row.q = drafts && row.c.hi > 0.0f ? drafts + s.cur * p.qs[1] : nullptr;
-    row.gone = s.gone ? s_gone : nullptr;
-    if (s.gone) {  // (a warp's own bits)
+    row.gone = nullptr;
+    taken = s.gone;
+    if (taken) {  // (a warp's own bits)
       for (int w = lane; w < p.seg / 32; w += 32) s_gone[warp * (p.seg / 32) + w] = 0u;
       __syncwarp();
+      bool some = false;
       for (int j = s.cur + 1 + lane; j < nodes; j += 32) {
-        const int e = s_token[j] - first;
-        if (s_tree[j] == s.cur && s_token[j] >= e0 && s_token[j] < e1) atomicOr(s_gone + (e >> 5), 1u << (e & 31));
+        const int e = s_token[j];
+        if (s_tree[j] != s.cur || e < e0 || e >= e1) continue;
+        atomicOr(s_gone + ((e - first) >> 5), 1u << ((e - first) & 31));
+        some = true;
       }
       __syncwarp();
+      if (__any_sync(0xFFFFFFFFu, some)) row.gone = s_gone;
     }
     const Pair x = ver_warp_sum(row.sum(e0, e1));
-    if (lane < blocks) ver_send(&s.sum[passes & 1][rank * kVerWarps + warp], (uint32_t)lane, (double)x.hi + (double)x.lo);
+    if (lane < blocks) ver_send(&s.sum[passes & 1][rank * kVerWarps + warp], (uint32_t)lane, x);
     ver_cluster_sync();
   }
 
@@ -340,28 +372,25 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyPara
   if (seg < 0 || seg / kVerWarps != rank) return;
   const int run = p.seg / kVerThreads + (p.seg % kVerThreads != 0), s1 = min((seg + 1) * p.seg, p.V);
   const int r0 = min(seg * p.seg + tid * run, s1), r1 = min(r0 + run, s1);
+  row.gone = taken ? s_gone : nullptr;
   Pair x = {0.0f, 0.0f};
 #pragma unroll 4
-  for (int e = r0; e < r1; ++e) {
-    const Pair r = row.entry(e);
-    pair_add(x, r.hi, r.lo);
-  }
-  const double of = (double)x.hi + (double)x.lo, before = ver_upto(of, lane);
-  if (lane == 31) s.part[warp] = before;
+  for (int e = r0; e < r1; ++e) x = pair_sum(x, row.entry(e));
+  const Pair upto_lane = ver_upto(x, lane);
+  if (lane == 31) s.part[warp] = upto_lane;
   __syncthreads();
-  double rest = s.rest;
-  const double part = lane < kVerWarps ? s.part[lane] : 0.0;
+  Pair rest = s.rest;
+  const Pair part = lane < kVerWarps ? s.part[lane] : Pair{0.0f, 0.0f};
   if (max(ver_find(part, ver_upto(part, lane), rest), 0) != warp) return;
-  if (max(ver_find(of, before, rest), 0) != lane) return;
+  if (max(ver_find(x, upto_lane, rest), 0) != lane) return;
   int token = r0;
 #pragma unroll 1
   for (int e = r0; e < r1; ++e) {
     const Pair r = row.entry(e);
-    const double x = (double)r.hi + (double)r.lo;
-    if (x > 0.0) {
+    if (r.hi > 0.0f) {
       token = e;
-      if (x > rest) break;
-      rest -= x;
+      if (pair_above(r, rest)) break;
+      rest = pair_minus(rest, r);
     }
   }
   p.token[b] = token;
