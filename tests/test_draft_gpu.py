@@ -269,6 +269,58 @@ def test_tree_nan_and_infinite_scores(fa, n):
     assert not torch.isnan(w[0, 0, 100 + hidden.to(DEV)]).any() and torch.isnan(w[0, 0, :100]).all()
 
 
+def many_rows(fa, D, page, Hq, Hkv, n, lens, kind=E4M3):
+    g = torch.Generator().manual_seed(D + n)
+    rng = random.Random(n)
+    table, P, _ = R.make_table(g, lens, page)
+    pools = R.make_pools(g, P, Hkv, page, D, kind)
+    q = torch.randn(len(lens), Hq, n, D, generator=g).to(BF16)
+    trees = [T.random_tree(rng, n, SHAPES[b % 4]) for b in range(len(lens))]
+    cache, args = to_gpu(fa, pools), (i32(table), i32(lens))
+    qd, tree = q.to(DEV), i32(trees)
+    return (lambda: fa.cache_attention(qd, cache, *args, tree=tree)), (R.Cache(*pools), q, table, lens, trees)
+
+
+# (rows four times, twice and once in a tile, two row groups, and heads of 256; the decode kernel's two tiles)
+MANY_ROWS = [(128, 64, 8, 2, 5, [700, 300]), (64, 16, 8, 2, 12, [900, 201]), (128, 16, 4, 1, 30, [1000]),
+             (128, 64, 8, 1, 30, [400, 2000]), (256, 64, 8, 2, 9, [400, 90]), (128, 64, 4, 2, 2, [300, 40])]
+
+
+@pytest.mark.parametrize("ctas", [0, 1])
+@pytest.mark.parametrize("cycles", [1, 300, 3000, 30000])
+@pytest.mark.parametrize("D,page,Hq,Hkv,n,lens", MANY_ROWS)
+def test_tree_wait_bounds_then_the_next_call_is_right(fa, D, page, Hq, Hkv, n, lens, cycles, ctas):
+    """Copies, products and stores that are under way when a wait expires are done before the block gives back its
+    memory."""
+    call, ref = many_rows(fa, D, page, Hq, Hkv, n, lens)
+    torch.cuda.synchronize()
+    try:
+        fa.fa_set_max_ctas(ctas)
+        for _ in range(3):
+            fa.fa_set_timeout_cycles(cycles)
+            call()
+            fa.fa_set_timeout_cycles(0)
+            got = call()
+            assert fa.fa_sync_status(None) in (fa.fa.FA_OK, fa.fa.FA_ERR_DEVICE_TIMEOUT), fa.fa_last_error()
+            check_attention(*ref, got)
+    finally:
+        fa.fa_set_timeout_cycles(0)
+        fa.fa_set_max_ctas(0)
+
+
+@pytest.mark.parametrize("D,page,Hq,Hkv,n,lens", MANY_ROWS + [
+    (128, 64, 32, 8, 16, [5000 - 300 * b for b in range(16)]), (64, 16, 32, 32, 33, [900 + 7 * b for b in range(5)]),
+    (256, 16, 16, 2, 13, [3000 - 431 * b for b in range(7)]), (128, 64, 8, 1, 104, [9000])])
+def test_tree_results_do_not_change_from_run_to_run(fa, D, page, Hq, Hkv, n, lens):
+    call, ref = many_rows(fa, D, page, Hq, Hkv, n, lens)
+    o, lse = call()
+    check_attention(*ref, (o, lse))
+    for _ in range(6):
+        again = call()
+        assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    synced(fa)
+
+
 # ----------------------------------------------------------------- verification
 
 def verify_case(fa, *, n=6, V=1000, B=3, dtype=F32, drawn=True, shape="beam", seed=0, sharp=2.0, n_q=None, u=None,
@@ -328,6 +380,21 @@ def test_verify_tree_sizes(fa, drawn, n, shape):
 def test_verify_largest_vocabulary(fa):
     for drawn in (True, False):
         verify_case(fa, n=3, V=1 << 20, B=1, drawn=drawn, shape="star", sharp=4.0)
+    synced(fa)
+
+
+@pytest.mark.parametrize("B", [20, 40, 80])
+@pytest.mark.parametrize("n,V", [(2, 1 << 20), (7, 70001)])
+def test_verify_large_vocabularies_of_many(fa, B, n, V):
+    """The blocks of a sequence are as many as run at once, unless what is rejected has no room."""
+    verify_case(fa, n=n, V=V if B < 80 else V // 2, B=B, dtype=BF16, drawn=False, shape="star", sharp=3.0)
+    synced(fa)
+
+
+@pytest.mark.parametrize("drawn", [True, False])
+def test_verify_results_do_not_change_from_run_to_run(fa, drawn):
+    got = [verify_case(fa, n=12, V=30011, B=24, drawn=drawn, seed=3) for _ in range(3)]
+    assert got[0] == got[1] == got[2]
     synced(fa)
 
 
