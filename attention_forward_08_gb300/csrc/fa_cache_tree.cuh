@@ -80,7 +80,7 @@ __device__ __noinline__ void tree_write_line(TreeOf t, int i, uint32_t* words) {
   }
 }
 // Bits `from` .. from + 31 of row i's line (from may be negative), by walking up;
-__device__ inline __noinline__ uint32_t tree_walk(TreeOf t, int i, int from) {
+__device__ __forceinline__ uint32_t tree_walk_here(const TreeOf& t, int i, int from) {
   uint32_t bits = 0u;
   for (int n = t.window > 0 ? t.window : INT_MAX; i >= from && i >= 0 && n > 0; --n) {
     if (i < from + 32) bits |= 1u << (i - from);
@@ -88,6 +88,8 @@ __device__ inline __noinline__ uint32_t tree_walk(TreeOf t, int i, int from) {
   }
   return bits;
 }
+// (a call, where it is rare and its registers would be another's)
+__device__ inline __noinline__ uint32_t tree_walk(TreeOf t, int i, int from) { return tree_walk_here(t, i, from); }
 // ... or of a line of n nodes that was written.
 template <int kStride>
 __device__ __forceinline__ uint32_t tree_read_line(const uint32_t* words, int n, int from) {

@@ -68,6 +68,16 @@ __global__ void __launch_bounds__(256) cache_rows_kernel(const __grid_constant__
   }
 }
 
+// Of tokens tok0 .. + 31, those that row i of a tree sees.
+__device__ __forceinline__ uint32_t weight_seen(const TreeOf& tree, const DecSeq& seq, int pos0, int i, int tok0) {
+  if (i >= seq.nq) return 0u;
+  const int from = tree.window > 0 ? min(max(tree_first(tree, pos0, tree_depth(tree, i)) - tok0, 0), 32) : 0;
+  const int to = min(max(pos0 - tok0, 0), 32);
+  uint32_t seen = from < to ? (0xFFFFFFFFu >> (32 - (to - from))) << from : 0u;
+  if (to < 32) seen |= tree_walk_here(tree, i, tok0 - pos0);
+  return seen;
+}
+
 template <int kKind, int kD, bool kTree>
 __global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constant__ WeightParams p) {
   const CacheAttnParams& a = p.a;
@@ -133,11 +143,12 @@ __global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constan
     }
     const float2 r0 = __ldcg(row + rg * 16 + g), r1 = __ldcg(row + rg * 16 + g + 8);
     const int ia = (rg * 16 + g) / a.group, ib = (rg * 16 + g + 8) / a.group;
-    // tokens that rows g and g + 8 see (a row that is none has L2 = +inf)
+    // Tokens that rows g and g + 8 see (a row that is none has L2 = +inf): from .x
+    // to .y; of a tree's, bits from this lane's first token on.
     int2 va = make_int2(0, 0), vb = va;
-    if constexpr (kTree) {  // (of a tree's, those before the drafts)
-      if (ia < seq.nq) va = make_int2(a.window > 0 ? tree_first(tree, pos0, tree_depth(tree, ia)) : 0, pos0);
-      if (ib < seq.nq) vb = make_int2(a.window > 0 ? tree_first(tree, pos0, tree_depth(tree, ib)) : 0, pos0);
+    uint32_t sa = 0u, sb = 0u;
+    if constexpr (kTree) {
+      sa = weight_seen(tree, seq, pos0, ia, tok0) >> (2 * t), sb = weight_seen(tree, seq, pos0, ib, tok0) >> (2 * t);
     } else {
       va = dec_span(a, seq, ia, ia), vb = dec_span(a, seq, ib, ib);
     }
@@ -146,13 +157,17 @@ __global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constan
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 r = e < 2 ? r0 : r1;
-        const int2 v = e < 2 ? va : vb;
         float s = sc[j][e] * (ks[j >> 1] * r.x);
         s = raw ? s * a.scale_log2
                 : fmaf(-2.0f * a.cap_out, rcp_approx(ex2(s * a.cap_in * 2.8853900817779268f) + 1.0f), a.cap_out);
-        const int tok = tok0 + 8 * j + 2 * t + (e & 1);
-        bool seen = tok >= v.x && tok < v.y;
-        if constexpr (kTree) seen = seen || tree_sees_draft(tree, seq.nq, e < 2 ? ia : ib, tok - pos0);
+        bool seen;
+        if constexpr (kTree) {
+          seen = ((e < 2 ? sa : sb) >> (8 * j + (e & 1))) & 1u;
+        } else {
+          const int2 v = e < 2 ? va : vb;
+          const int tok = tok0 + 8 * j + 2 * t + (e & 1);
+          seen = tok >= v.x && tok < v.y;
+        }
         if (seen) sum[j][e & 1] += ex2(s - r.y);
       }
   }
