@@ -9,7 +9,8 @@
 // receive, and later sources are never behind earlier slots.
 //
 // Bound: latency; a chain of five loads (length and count, path, table, scales,
-// bytes) and few tokens.
+// bytes) and few tokens: 32 sequences of 16 drafts, 8 heads of 128, 7.1 us; 64 of 200,
+// 8 heads of 256, blocks of 16, 13.1 us (26.8 a receiving block at a time).
 #include "fa.h"
 #include "fa_cache.h"
 #include "fa_cache_launch.cuh"

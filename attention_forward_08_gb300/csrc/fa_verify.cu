@@ -18,15 +18,18 @@
 // time, and doubles for the walk and the sums of segments alone took half of a
 // single sequence's (12.4 us).  All orders are fixed.
 //
-// Work.  A cluster of 2 to 8 blocks a sequence.  Tests need two numbers a node, which
-// every block gathers for itself and walks over alike, so that decisions are
-// not sent around; a pass over a row is shared out by contiguous segments, one
-// a warp, whose sums go to all blocks (distributed shared memory).  The warp
-// sums tell the segment in which the cumulative sum passes u Z; its block alone
-// reads that again.
+// Work.  A cluster of 2 to 8 blocks a sequence, as many as run at once (64
+// sequences: 18.0 us with 4, 24 with 8, which take two turns).  Tests need two
+// numbers a node, which every block gathers for itself and walks over alike, so that
+// decisions are not sent around; a pass over a row is shared out by contiguous
+// segments, one a warp, whose sums go to all blocks (distributed shared memory).
+// These tell the segment in which the cumulative sum passes u Z; its block alone
+// reads that again, a run of entries a thread.
 //
-// Bound: latency (three dependent loads and two cluster barriers); then one row
-// of p and q a sequence, and one more for each rejected draft that has a sibling.
+// Bound: latency (three dependent loads and two cluster barriers: one sequence of 5
+// nodes, 32000 entries, 9.8 us); then the sums' instructions, some 30 an entry of p
+// and q (32 sequences of 128001 fp32 entries, up to three passes one after the
+// other, 28 us; 64 of 100000 bf16 entries without q, 18 us, 0.7 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -38,7 +41,7 @@ namespace fa {
 namespace {
 
 constexpr int kVerThreads = 512, kVerWarps = kVerThreads / 32, kVerMostBlocks = 8;
-constexpr size_t kVerSmem = 46 * 1024;  // dynamic shared memory that needs no opting in, beside VerShared
+constexpr size_t kVerSmem = 45 * 1024;  // dynamic shared memory that needs no opting in
 
 __device__ __forceinline__ float ver_load(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float ver_load(const __nv_bfloat16* p) {
@@ -139,6 +142,8 @@ struct VerShared {
   int ends, cur, gone, count, seg;
   Pair c, rest;
 };
+
+static_assert(kVerSmem + sizeof(VerShared) <= 48 * 1024, "shared memory");
 
 // What is left of a row.
 template <class T>
