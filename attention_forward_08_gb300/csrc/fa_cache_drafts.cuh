@@ -35,8 +35,8 @@
 // of 16 sequences of up to 8192 tokens 76 us, 2.4 TB/s (the prompt kernel on causal
 // rows: 122); 104 rows at 131071 tokens 105 us, 2.5 TB/s (164); 240 rows of 8 x up to
 // 6000 tokens 76 us (77).  Tried and slower: the stored bytes by bulk copies, a
-// barrier a piece (85 us on the first), three loads of the query's rows from all
-// softmax warps (118 on the second).
+// barrier a piece (85 us on the first); the query rows by way of all softmax warps'
+// registers (118 on the second).
 #pragma once
 
 #include <type_traits>
