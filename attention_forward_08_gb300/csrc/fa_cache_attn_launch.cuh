@@ -29,7 +29,7 @@ bool line_params(DecParams& p, const CacheAttnParams& a, int max_ctas, const Lau
   p.a = a;
   p.rows = a.n * a.group;
   p.row_groups = (p.rows + C::kRows - 1) / C::kRows;
-  if ((double)a.B * a.c.H * p.row_groups * ((double)a.c.M * a.c.page / C::kTile + 2) >= 2147483648.0) {
+  if ((double)a.B * a.c.H * p.row_groups * ((double)a.c.M * a.c.page / C::kTile + 2 + C::kLead) >= 2147483648.0) {
     set_error("B * H_kv * row groups (%d) * table width (%d tokens) is beyond the kernel's index range", p.row_groups,
               a.c.M * a.c.page);
     return false;

@@ -53,6 +53,7 @@ namespace fa {
 template <int kKind_, bool kF16_, int kD_, int kMT_, bool kTma_, bool kTree_ = false>
 struct DecCfg {
   static constexpr bool kTree = kTree_;
+  static constexpr int kLead = 0;
   static constexpr bool kTma = kTma_;
   static constexpr int kKind = kKind_;
   static constexpr bool kF16 = kF16_;  // type of q and o

@@ -61,6 +61,7 @@ struct DraftCfg {
   static constexpr int kRows = kD == 256 ? 64 : 128;       // of a row group
   static constexpr int kTile = 128;  // keys a block of the line
   static constexpr int kMinTiles = 4;
+  static constexpr int kLead = kD == 64 ? 10 : kD == 128 ? 8 : 5;
   static constexpr int kLift = 7;
   static constexpr int kKeys = 64;   // keys a score buffer: a unit
   // Widened K and V: stages of 16 KB (D = 256: 32).  Stored bytes: three pieces of
@@ -117,6 +118,7 @@ struct DraftInfo {
   uint64_t o_ready[2][2];               // PV done, by buffer: nobody is two phases of one behind
   uint64_t info_full[4], info_empty[4], drain[2];
   int n[2];                             // [piece & 1]: blocks of a piece (0: no more), beside q_full
+  int blocks;                           // of keys, of all pieces
   uint32_t tmem;
   int abort;
 };
@@ -153,6 +155,15 @@ __device__ __forceinline__ uint32_t draft_seen(const TreeOf& tree, int i, uint32
       seen |= tree.n <= 32 * kDraftWords ? tree_read_line<128 * C::kSoft>(lines, tree.n, -hi) : tree_walk(tree, i, -hi);
   }
   return seen;
+}
+
+// Of a segment of `tiles` places on the line, the blocks of keys before this part
+// of the line, t0 .. t1 - 1, and in it (none or less: it ends before the first).
+template <class C>
+__device__ __forceinline__ int draft_first(const DecPlace& seg, int t0) { return max(t0 - seg.seg0 - C::kLead, 0); }
+template <class C>
+__device__ __forceinline__ int draft_blocks(const DecPlace& seg, int tiles, int t0, int t1) {
+  return min(t1 - seg.seg0, tiles) - C::kLead - draft_first<C>(seg, t0);
 }
 
 template <class C>
@@ -199,6 +210,17 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
   if (warp == 1) {
     tmem_alloc(&info->tmem, 512);
     tmem_relinquish();
+  } else if (warp == 3) {  // the blocks of keys in this part of the line
+    DecPlace seg = at;
+    int blocks = 0;
+#pragma unroll 1
+    while (true) {
+      const int tiles = dec_tiles<C>(p, seg.seq, seg.rg);
+      blocks += max(draft_blocks<C>(seg, tiles, t0, t1), 0);
+      if (t1 <= seg.seg0 + tiles) break;
+      dec_next(p, seg, tiles);
+    }
+    info->blocks = blocks;
   }
   tc_fence_before();
   __syncthreads();
@@ -293,21 +315,25 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
     } else if (warp == 2) {
       // ---------------------------------------------------------- blocks and scales
       // Four blocks of keys at a time, a lane 16 keys.
-      int pos = t0, left = 0, tok = 0;  // of the piece: blocks left, the next one's first token
+      const int blocks = info->blocks;
+      int left = 0, tok = 0;  // of the piece: blocks left, the next one's first token
+      bool begun = false;
       int2 span = make_int2(0, 0);
       bool ok = true;
 #pragma unroll 1
-      for (int nb = 0; nb < t1 - t0 && ok; nb += 4) {
+      for (int nb = 0; nb < blocks && ok; nb += 4) {
         int b = 0, h = 0, mine = 0, lo = 0, hi = 0;  // this lane's keys: the first, and those that are seen
         bool any = false;                            // are some of its kGroup keys seen?
 #pragma unroll 1
-        for (int q = 0; q < min(4, t1 - t0 - nb); ++q) {
+        for (int q = 0; q < min(4, blocks - nb); ++q) {
           if (left == 0) {
-            if (pos > t0) dec_next(p, at, dec_tiles<C>(p, at.seq, at.rg));
-            if (lane == 0 && at.h == 0 && at.rg == 0 && pos == at.seg0) (void)checked_len(c, a.lens[at.b]);
+            if (begun) dec_next(p, at, dec_tiles<C>(p, at.seq, at.rg));
+            begun = true;
+            const int first = draft_first<C>(at, t0);
+            if (lane == 0 && at.h == 0 && at.rg == 0 && first == 0) (void)checked_len(c, a.lens[at.b]);
             span = dec_group_span<C>(p, at.seq, at.rg);
-            left = min(t1, at.seg0 + dec_tiles<C>(p, at.seq, at.rg)) - pos;
-            tok = (span.x / 128 + pos - at.seg0) * 128;
+            left = draft_blocks<C>(at, dec_tiles<C>(p, at.seq, at.rg), t0, t1);
+            tok = (span.x / 128 + first) * 128;
           }
           if ((lane >> 3) == q) {
             b = at.b, h = at.h;
@@ -317,7 +343,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
             any = of < span.y && of + C::kGroup > span.x;
           }
           tok += 128;
-          --left, ++pos;
+          --left;
         }
         const int slot = (nb + (lane >> 3)) & (kDraftAhead - 1), g = lane & 7, batch = nb >> 2;
         const int blk = any ? checked_block(c, c.table, c.table_stride, b, mine >> c.page_log2) : -1;
@@ -357,7 +383,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
     const uint32_t mine = smem_u32(smem + C::kOffRing + (warp - 4) * C::kRing * C::kPieceBytes) + lane * 16;
     const long long stride = kv ? c.vs[2] : c.ks[2];
     const uint8_t* const pool = (kv ? c.v : c.k) + vec * 16 + key0 * stride;
-    const int pieces = 128 / C::kPieceKeys * (t1 - t0);
+    const int pieces = 128 / C::kPieceKeys * info->blocks;
     const bool e4m3 = p.kind == kKindE4m3;
     int known = 0;  // blocks that are looked up
     bool ok = true;
@@ -443,10 +469,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
     auto landed = [&](int unit) { return wait(&info->o_ready[t][unit & 1], (uint32_t)(unit >> 1) & 1u); };
 #pragma unroll 1
     for (int pos = t0; pos < t1; ++pieces) {
-      const int tiles = dec_tiles<C>(p, at.seq, at.rg), n = min(t1, at.seg0 + tiles) - pos;
+      const int tiles = dec_tiles<C>(p, at.seq, at.rg), n = draft_blocks<C>(at, tiles, t0, t1), from_block = draft_first<C>(at, t0);
+      if (n <= 0) break;
       const int2 span = dec_group_span<C>(p, at.seq, at.rg);
-      const int first = span.x / 128 + pos - at.seg0;
-      const bool whole = n == tiles, head_cut = pos > at.seg0;
+      const int first = span.x / 128 + from_block;
+      const bool whole = n == tiles - C::kLead, head_cut = from_block > 0;
       const int row = C::kDup > 1 ? tl & (kCopy - 1) : at.rg * C::kRows + tl, i = row / a.group, head = at.h * a.group + row % a.group;
       const bool real = tl < C::kRows && row < p.rows;
       const int base = at.seq.len - at.seq.nq;  // the first draft's slot
@@ -756,7 +783,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
       }
       if constexpr (C::kSplit) named_bar_sync(3, 256);  // both outputs have been read
       before += n;
-      pos += n;
+      pos = at.seg0 + tiles;
       dec_next(p, at, tiles);
     }
     if (ok && lane == 0 && (!C::kSplit || t == 0)) {

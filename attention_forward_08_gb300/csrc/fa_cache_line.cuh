@@ -81,11 +81,12 @@ __device__ __forceinline__ int2 dec_group_span(const DecParams& p, const DecSeq&
   return dec_span(p.a, s, rg * C::kRows / p.a.group, (min(p.rows, (rg + 1) * C::kRows) - 1) / p.a.group);
 }
 
-// Tiles of one segment: at least one, so that empty rows are written too.
+// Tiles of one segment: at least one, so that empty rows are written too.  (With
+// kLead places on the line before them that hold none: what a segment costs to begin.)
 template <class C>
 __device__ __forceinline__ int dec_tiles(const DecParams& p, const DecSeq& s, int rg) {
   const int2 v = dec_group_span<C>(p, s, rg);
-  return max(1, (v.y + C::kTile - 1) / C::kTile - v.x / C::kTile);
+  return max(1, (v.y + C::kTile - 1) / C::kTile - v.x / C::kTile) + C::kLead;
 }
 // Tiles of a head's row groups 0 .. groups-1, by a whole warp (many groups).
 template <class C>

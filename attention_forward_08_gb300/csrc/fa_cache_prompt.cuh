@@ -51,6 +51,7 @@ namespace fa {
 template <int kKind_, bool kF16_, int kD_, int kGroup_, bool kRaw_>
 struct PromptCfg {
   static constexpr bool kTree = false;
+  static constexpr int kLead = 0;
   static constexpr bool kRaw = kRaw_;  // scores need no more than a positive factor
   static constexpr int kGroup = kGroup_, kGroups = 128 / kGroup;  // groups a block of keys
   static constexpr int kKind = kKind_;
