@@ -32,11 +32,11 @@
 // Bound: memory, 2 * D bytes a token and K/V head; now the converters' and the
 // softmax warps' chains (2300 cycles a block of 128 keys of D 128; issue slots half
 // busy) and what is done once a piece (20000 cycles).  8 heads of 128, e4m3: 64 rows
-// of 16 sequences of up to 8192 tokens 76 us, 2.4 TB/s (the prompt kernel on causal
-// rows: 122); 104 rows at 131071 tokens 105 us, 2.5 TB/s (164); 240 rows of 8 x up to
-// 6000 tokens 76 us (77).  Tried and slower: the stored bytes by bulk copies, a
-// barrier a piece (85 us on the first); the query rows by way of all softmax warps'
-// registers (118 on the second).
+// of 16 sequences of up to 8192 tokens 70 us, 2.6 TB/s (the prompt kernel on causal
+// rows: 122); 104 rows at 131071 tokens 99 us, 2.7 TB/s (164); 240 rows of 8 x up to
+// 6000 tokens 67 us (77).  Tried and slower, on the first and the second when they
+// took 76 and 105: the stored bytes by bulk copies, a barrier a piece (85 us); the
+// query rows by way of all softmax warps' registers (75, 118).
 #pragma once
 
 #include <type_traits>
@@ -61,6 +61,10 @@ struct DraftCfg {
   static constexpr int kRows = kD == 256 ? 64 : 128;       // of a row group
   static constexpr int kTile = 128;  // keys a block of the line
   static constexpr int kMinTiles = 4;
+  // What a piece costs before and behind its keys, in blocks of keys: parts of the line
+  // that begin more segments get fewer keys.  (64 rows of 16 sequences of up to 8192
+  // tokens, D 128: 76 us with 0, 70.4 with 6, 69.7 with 8, 74 with 12; 240 rows: 76, 67.5,
+  // 67.3, 72; D 256: 66, 65.2 with 3, 65.0 with 5, 71 with 8.)
   static constexpr int kLead = kD == 64 ? 10 : kD == 128 ? 8 : 5;
   static constexpr int kLift = 7;
   static constexpr int kKeys = 64;   // keys a score buffer: a unit
