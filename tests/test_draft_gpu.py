@@ -286,6 +286,31 @@ MANY_ROWS = [(128, 64, 8, 2, 5, [700, 300]), (64, 16, 8, 2, 12, [900, 201]), (12
              (128, 64, 8, 1, 30, [400, 2000]), (256, 64, 8, 2, 9, [400, 90]), (128, 64, 4, 2, 2, [300, 40])]
 
 
+@pytest.mark.parametrize("ctas", [0, 3, 40])
+@pytest.mark.parametrize("n,kw", [(12, {}), (40, dict(D=64, page=16, kind=I8)), (70, dict(track=True)),
+                                  (10, dict(D=256, window=90, track=True))])
+def test_tree_many_sequences(fa, n, kw, ctas):
+    """More sequences than a warp has lanes, most of them short: thread blocks with many segments, with a few keys, with
+    none; sequences without drafts and without tokens between them."""
+    lens = [(37 * b) % 300 + n if b % 5 else (b % 3) * n for b in range(75)]
+    n_q = [min(length, n if b % 4 else b % (n + 1)) for b, length in enumerate(lens)]
+    lens[40] = 9000
+    try:
+        fa.fa_set_max_ctas(ctas)
+        tree_case(fa, n=n, lens=lens, n_q=n_q, shape="all", **kw)
+    finally:
+        fa.fa_set_max_ctas(0)
+
+
+@pytest.mark.parametrize("n", [33, 130])
+@pytest.mark.parametrize("window", [1, 3, 40, 200])
+@pytest.mark.parametrize("D,page", [(64, 16), (256, 64)])
+def test_tree_weights_with_a_window(fa, n, window, D, page):
+    """Windows that end in a line of drafts, at their begin and before them, and what the tokens there got."""
+    tree_case(fa, n=n, D=D, page=page, Hq=2, Hkv=1, lens=(n, n + 1, n + 31, n + 32, n + 300), window=window, shape="all",
+              track=True, softcap=5.0 if window == 3 else 0.0)
+
+
 @pytest.mark.parametrize("ctas", [0, 1])
 @pytest.mark.parametrize("cycles", [1, 300, 3000, 30000])
 @pytest.mark.parametrize("D,page,Hq,Hkv,n,lens", MANY_ROWS)
