@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyPara
 
   // The nodes, and the two numbers of each that its test needs.
   const int told = p.n_q ? p.n_q[b] : n, nodes = min(max(told, 0), n);
+  const float u_next = p.u_next[b];
   bool bad = nodes != told;
   for (int i = tid; i < n; i += kVerThreads) {
     int up = p.tree[b * p.tree_stride + i], t = p.tokens[b * p.tokens_stride + i];
@@ -327,8 +328,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyPara
           bare = true;
         } else {  // the segment that holds the token
           ends = true;
-          const float u = p.u_next[b];
-          Pair rest = pair_times(z, u > 0.0f ? fminf(u, 1.0f) : 0.0f);
+          Pair rest = pair_times(z, u_next > 0.0f ? fminf(u_next, 1.0f) : 0.0f);
           int seg = ver_find(mine, upto, rest);
           if (seg >= 0) {
             const int i = seg * per + lane;
