@@ -157,9 +157,15 @@ __global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constan
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 r = e < 2 ? r0 : r1;
-        float s = sc[j][e] * (ks[j >> 1] * r.x);
-        s = raw ? s * a.scale_log2
-                : fmaf(-2.0f * a.cap_out, rcp_approx(ex2(s * a.cap_in * 2.8853900817779268f) + 1.0f), a.cap_out);
+        float s = sc[j][e];
+        if (kTree && raw) {
+          s = fmaf(s, ks[j >> 1] * (r.x * a.scale_log2), -r.y);
+        } else {
+          s *= ks[j >> 1] * r.x;
+          s = raw ? s * a.scale_log2
+                  : fmaf(-2.0f * a.cap_out, rcp_approx(ex2(s * a.cap_in * 2.8853900817779268f) + 1.0f), a.cap_out);
+          s -= r.y;
+        }
         bool seen;
         if constexpr (kTree) {
           seen = ((e < 2 ? sa : sb) >> (8 * j + (e & 1))) & 1u;
@@ -168,7 +174,7 @@ __global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constan
           const int tok = tok0 + 8 * j + 2 * t + (e & 1);
           seen = tok >= v.x && tok < v.y;
         }
-        if (seen) sum[j][e & 1] += ex2(s - r.y);
+        if (seen) sum[j][e & 1] += ex2(s);
       }
   }
 #pragma unroll
