@@ -94,7 +94,9 @@ __global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constan
   const int pos0 = seq.len - seq.nq;
   if (a.causal) i0 = max(0, tok0 - pos0);
   if (!kTree && a.window > 0) i1 = (int)min((long long)i1, (long long)tok0 + 31 + a.window - 1 - pos0);
-  const bool none = tok0 >= seq.len || i0 > i1;
+  // The first token that any row sees: blocks behind the window need not be there.
+  const int lo = dec_span<kTree>(a, seq, 0, a.n - 1).x;
+  const bool none = tok0 >= seq.len || tok0 + 31 < lo || i0 > i1;
   const int rg0 = i0 * a.group / 16, rg1 = (i1 * a.group + a.group - 1) / 16;
 
   // keys: lane (g, t) holds the bytes of token 8j + g that it multiplies
@@ -105,7 +107,7 @@ __global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constan
   for (int half = 0; half < 2; ++half) {
     const int tok = tok0 + 16 * half;
     int blk = -1;
-    if (!none && tok < seq.len) blk = checked_block(c, c.table, c.table_stride, b, tok >> c.page_log2);
+    if (!none && tok < seq.len && tok + 15 >= lo) blk = checked_block(c, c.table, c.table_stride, b, tok >> c.page_log2);
     here[half] = blk >= 0;
     ks[half] = here[half] ? __ldg(c.k_scale + (long long)blk * c.H + h) : 0.0f;
 #pragma unroll

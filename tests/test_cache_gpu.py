@@ -215,6 +215,26 @@ def test_window(fa, n, window):
     attention_case(fa, n=n, lens=(n, 3 + n, 130 + n, 777), window=window, track=window == 100)
 
 
+@pytest.mark.parametrize("D,page,Hq,Hkv,n", [(64, 16, 2, 1, 5), (64, 16, 2, 1, 40), (128, 16, 8, 2, 1), (128, 16, 8, 2, 9),
+                                            (128, 64, 8, 2, 20), (256, 16, 2, 1, 4), (256, 16, 2, 1, 9), (256, 32, 4, 2, 40)])
+@pytest.mark.parametrize("window", [3, 100])
+def test_weights_need_no_blocks_behind_the_window(fa, D, page, Hq, Hkv, n, window):
+    """Table entries of tokens that a window hides from every row may be anything, with scores that are kept and
+    without; the window begins at every place of 32 tokens."""
+    g = torch.Generator().manual_seed(n + D)
+    lens = [n + 160 + 7 * b for b in range(33)]
+    table, P, _ = R.make_table(g, lens, page)
+    pools = R.make_pools(g, P, Hkv, page, D, E4M3)
+    gone = [[P + 7 if (m + 1) * page <= length - n - window + 1 else x for m, x in enumerate(r)] for r, length in zip(table, lens)]
+    assert any(P + 7 in r for r in gone)
+    q = torch.randn(len(lens), Hq, n, D, generator=g).to(BF16)
+    w0 = torch.rand(len(lens), Hkv, max(lens) + 3, generator=g)
+    w = w0.to(DEV)
+    got = fa.cache_attention(q.to(DEV), to_gpu(fa, pools), i32(gone), i32(lens), weights=w, window=window)
+    synced(fa)
+    check_attention(fa, R.Cache(*pools), q, table, lens, got, w, w0, window=window)
+
+
 @pytest.mark.parametrize("n", [1, 6, 150])
 @pytest.mark.parametrize("softcap", [0.5, 20.0])
 @pytest.mark.parametrize("D", [64, 128, 256])

@@ -311,6 +311,29 @@ def test_tree_weights_with_a_window(fa, n, window, D, page):
               track=True, softcap=5.0 if window == 3 else 0.0)
 
 
+@pytest.mark.parametrize("D,page,Hq,Hkv,n,width", [
+    (64, 16, 2, 1, 5, 0), (64, 16, 2, 1, 16, 0), (64, 16, 2, 1, 17, 0), (64, 16, 2, 1, 60, 0), (64, 16, 1, 1, 130, 0),
+    (128, 16, 8, 2, 8, 0), (128, 16, 8, 2, 9, 0), (128, 64, 8, 2, 20, 0), (128, 32, 8, 2, 6, 1 << 20),
+    (256, 16, 2, 1, 8, 0), (256, 16, 2, 1, 9, 0), (256, 32, 4, 2, 40, 0), (256, 128, 4, 1, 3, 1 << 20)])
+@pytest.mark.parametrize("window", [3, 100])
+def test_tree_weights_need_no_blocks_behind_the_window(fa, D, page, Hq, Hkv, n, width, window):
+    """Table entries of tokens that a window hides from every draft may be anything, with scores that are kept and
+    without; the window begins at every place of 32 tokens."""
+    g = torch.Generator().manual_seed(n + D)
+    lens = [n + 160 + 7 * b for b in range(33)]
+    table, P, _ = R.make_table(g, lens, page, width=max(width // page, -(-max(lens) // page)))
+    pools = R.make_pools(g, P, Hkv, page, D, E4M3)
+    gone = [[P + 7 if (m + 1) * page <= length - n - window + 1 else x for m, x in enumerate(r)] for r, length in zip(table, lens)]
+    assert any(P + 7 in r for r in gone)
+    q = torch.randn(len(lens), Hq, n, D, generator=g).to(BF16)
+    trees = [T.random_tree(random.Random(b), n, SHAPES[b % 4]) for b in range(len(lens))]
+    w0 = torch.rand(len(lens), Hkv, max(lens) + 3, generator=g)
+    w = w0.to(DEV)
+    got = fa.cache_attention(q.to(DEV), to_gpu(fa, pools), i32(gone), i32(lens), tree=i32(trees), weights=w, window=window)
+    synced(fa)
+    check_attention(R.Cache(*pools), q, table, lens, trees, got, w, w0, window=window)
+
+
 @pytest.mark.parametrize("ctas", [0, 1])
 @pytest.mark.parametrize("cycles", [1, 300, 3000, 30000])
 @pytest.mark.parametrize("D,page,Hq,Hkv,n,lens", MANY_ROWS)
