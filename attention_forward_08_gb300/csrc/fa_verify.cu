@@ -85,19 +85,23 @@ __device__ __forceinline__ Pair pair_sum(Pair a, Pair b) {  // normalised
   const float s = __fadd_rn(a.hi, a.lo);
   return {s, __fsub_rn(a.lo, __fsub_rn(s, a.hi))};
 }
+__device__ __forceinline__ Pair pair_normal(Pair a) { return pair_sum(a, {0.0f, 0.0f}); }
 __device__ __forceinline__ Pair pair_minus(Pair a, Pair b) { return pair_sum(a, {-b.hi, -b.lo}); }
 __device__ __forceinline__ Pair pair_times(Pair a, float b) {
   const float h = __fmul_rn(a.hi, b);
   return pair_sum({h, 0.0f}, {__fmaf_rn(a.lo, b, __fmaf_rn(a.hi, b, -h)), 0.0f});
 }
 __device__ __forceinline__ bool pair_above(Pair a, Pair b) { return pair_minus(a, b).hi > 0.0f; }
-// max(p - c q, 0).
+// max(p - c q, 0).  (Not normalised: where p is within a step or two of c q, lo
+// may be the larger part, and the sign is that of both.)
 __device__ __forceinline__ Pair ver_less(float p, float q, Pair c) {
   const float h = __fmul_rn(c.hi, q);
   const float e = __fmaf_rn(c.lo, q, __fmaf_rn(c.hi, q, -h));
   const float s = __fsub_rn(p, h);
-  const float f = __fsub_rn(__fsub_rn(p, s), h);  // (what s lost, where p > h)
-  return {fmaxf(s, 0.0f), s > 0.0f ? __fsub_rn(f, e) : 0.0f};
+  const float f = __fsub_rn(__fsub_rn(p, s), h);  // (what s lost, where p > h; nothing where p is near h)
+  const float lo = __fsub_rn(f, e);
+  const bool some = __fadd_rn(s, lo) > 0.0f;
+  return {some ? s : 0.0f, some ? lo : 0.0f};
 }
 
 __device__ __forceinline__ Pair ver_warp_sum(Pair x) {
@@ -157,7 +161,7 @@ struct VerRow {
   }
   __device__ __forceinline__ Pair entry(int e) const {
     const float x = ver_prob(ver_load(p + e));
-    if (q) return ver_less(x, ver_prob(ver_load(q + e)), c);
+    if (q) return pair_normal(ver_less(x, ver_prob(ver_load(q + e)), c));
     return {gone ? left(e, x) : x, 0.0f};
   }
   // This lane's sum over entries e0 + lane, e0 + lane + 32, .. < e1.  (All are
@@ -362,7 +366,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyPara
       __syncwarp();
       if (__any_sync(0xFFFFFFFFu, some)) row.gone = s_gone;
     }
-    const Pair x = ver_warp_sum(row.sum(e0, e1));
+    const Pair x = pair_normal(ver_warp_sum(row.sum(e0, e1)));
     if (lane < blocks) ver_send(&s.sum[passes & 1][rank * kVerWarps + warp], (uint32_t)lane, x);
     ver_cluster_sync();
   }

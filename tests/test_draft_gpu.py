@@ -509,6 +509,39 @@ def test_verify_same_candidate_twice(fa):
     synced(fa)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_verify_what_two_rejections_leave_is_not_rounded_away(fa, dtype):
+    """Entry 0 of what two rejected drafts (of token 2, which the target never takes) leave is p - C q with a C of more
+    than 24 bits: a difference in the last place of p, or 0; u_next 0 takes the first token that has any.  (The terms
+    are fp32 numbers or less, so p - C q is off by 2^-46 of p at most with C in 48 bits; cases nearer to 0 are left out.)"""
+    B, V = 4000, 3
+    rng = np.random.default_rng(7)
+    p, q = np.zeros((B, V)), np.zeros((B, V))
+    f = lambda x: torch.tensor(x).to(dtype).double().numpy()
+    q[:, 0], q[:, 1] = f(rng.uniform(0.1, 0.4, B)), f(rng.uniform(0.1, 0.3, B))
+    q[:, 2] = f(1.0 - q[:, 0] - q[:, 1])
+    p[:, 1] = f(np.maximum(1.0 - q[:, 0] * (1.0 + q[:, 2]), q[:, 1]))
+    for _ in range(40):  # p[0] next to C q[0]
+        z = np.maximum(p[:, 0] - q[:, 0], 0.0) + (p[:, 1] - q[:, 1])
+        p[:, 0] = f((1.0 + z) * q[:, 0])
+    z = np.maximum(p[:, 0] - q[:, 0], 0.0) + (p[:, 1] - q[:, 1])
+    left = p[:, 0] - q[:, 0] - z * q[:, 0]
+    use = np.abs(left) > 2.0 ** -40
+    p, q, left = p[use], q[use], left[use]
+    B = len(p)
+    assert min((left > 0).mean(), (left < 0).mean()) > 0.1
+    tokens, tree = i32([[0, 2, 2]] * B), i32([-1, 0, 0])
+    dev = lambda x: torch.tensor(x).to(dtype).to(DEV)[:, None].expand(B, 3, V)
+    path, count, token = fa.verify_drafts(dev(p), tokens, tree, torch.full((B, 3), 0.5, device=DEV),
+                                          torch.zeros(B, device=DEV), p_draft=dev(q))
+    synced(fa)
+    assert (count == 1).all()
+    want = [T.verify(np.tile(p[b], (3, 1)), [0, 2, 2], [-1, 0, 0], [0.5] * 3, 0.0, np.tile(q[b], (3, 1)))[1] for b in range(B)]
+    assert np.array_equal(want, np.where(left > 0, 0, 1))
+    wrong = np.nonzero(token.cpu().numpy() != want)[0]
+    assert len(wrong) == 0, f"{len(wrong)} of {B}; the first, {wrong[0]}: {token[wrong[0]]} for {want[wrong[0]]}"
+
+
 def test_verify_padding_and_strides(fa):
     verify_case(fa, n=7, V=333, B=5, n_q=(7, 0, 1, 3, 6), pad=3)
     verify_case(fa, n=7, V=333, B=5, n_q=(7, 0, 1, 3, 6), drawn=False, dtype=BF16, pad=1)
