@@ -28,27 +28,30 @@ struct Accepted {
 };
 
 // Sequence b's numbers, and its path in shared memory; the whole thread block.
-// A path that does not ascend, or leaves the drafts, ends before that entry.
+// A path that does not ascend, or leaves the drafts, ends before that entry; so
+// does one that reaches a draft behind the table, which nothing has stored.
 __device__ __forceinline__ Accepted accepted(const AcceptParams& p, int b, int* s_path, int* s_end) {
   Accepted r;
-  r.held = checked_len(p.c, p.lens[b]);
+  const int len = p.lens[b];
+  r.held = checked_len(p.c, len);
   int nq = p.n_q ? p.n_q[b] : p.n, count = p.count[b];
-  if (nq < 0 || nq > p.n || nq > r.held || count < 0 || count > nq) {
+  if (nq < 0 || nq > p.n || nq > len || count < 0 || count > nq) {
     if (threadIdx.x == 0) flag_bad_index(p.c);
-    if (nq < 0 || nq > p.n || nq > r.held) {  // the drafts are not there: nothing is done
+    if (nq < 0 || nq > p.n || nq > len) {  // the drafts are not there: nothing is done
       r.base = r.held;
       r.count = 0;
       return r;
     }
     count = count < 0 ? 0 : nq;
   }
-  r.base = r.held - nq;
+  r.base = min(len - nq, r.held);
+  const int stored = r.held - r.base;  // drafts that the table has room for: all, but for a length past it
   if (threadIdx.x == 0) *s_end = count;
   __syncthreads();
   const int* path = p.path + b * p.path_stride;
   for (int i = threadIdx.x; i < count; i += kAcceptThreads) {
     const int at = path[i];
-    if (at >= nq || at <= (i ? path[i - 1] : -1)) atomicMin(s_end, i);
+    if (at >= stored || at <= (i ? path[i - 1] : -1)) atomicMin(s_end, i);
     s_path[i] = at;
   }
   __syncthreads();

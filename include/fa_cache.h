@@ -255,7 +255,8 @@ int fa_verify_drafts(const fa_verify_drafts_args* args);
  * is that of the path's token that it receives: fa_cache_append's numbers stay.)
  * Slots behind lens_out[b] keep what they held.
  * lens_out may be lens itself.
- * A path that does not ascend, or leaves [0, n_q[b]), ends before that entry;
+ * A path that does not ascend, leaves [0, n_q[b]), or (lens[b] past the table)
+ * reaches a draft that the table has no slot for, ends before that entry;
  * count[b] is cut to [0, n_q[b]]; a sequence with fewer tokens than drafts, or
  * n_q[b] outside [0, n], stays as it is; fa_sync_status() then reports
  * FA_ERR_INVALID_ARGUMENT once.  n at most 1024.

@@ -669,6 +669,30 @@ def test_accept_bad_entries(fa):
         assert torch.equal(a, t.view(torch.uint8))
 
 
+def test_accept_of_drafts_that_the_table_has_no_room_for(fa):
+    """Drafts behind the table were not appended: a path ends before the first of them, and the tokens before the drafts
+    stay where they are; told."""
+    g = torch.Generator().manual_seed(4)
+    lens, n, page = [68, 100, 64, 66, 70], 8, 16
+    table, P, _ = R.make_table(g, [64] * 5, page)
+    pools = R.make_pools(g, P, 2, page, 64, E4M3)
+    ref, cache = R.Cache(*pools), to_gpu(fa, pools)
+    rows = [[0, 2, 5, 6], [0, 1, 2, 3], [0, 3, 4, 7], [0, 1, 3, 5], [2, 3, 4, 5]]
+    path = torch.full((5, n), -1, dtype=torch.int32)
+    path[:, :4] = torch.tensor(rows)
+    n_q = [8, 8, 8, 7, 6]  # the drafts begin in slots 60, 92, 56, 59, 64
+    w = torch.rand(5, 2, 70, generator=g)
+    want_w, wd = w.numpy().copy(), w.to(DEV)
+    kept = [[0, 2], [], rows[2], [0, 1, 3], []]
+    want = T.accept(ref, table, [64] * 5, kept, [len(x) for x in kept], [4, 0, 8, 5, 0], want_w)
+    got = fa.cache_accept(cache, i32(table), i32(lens), path.to(DEV), i32([4] * 5), n_q=i32(n_q), weights=wd)
+    told(fa)
+    assert got.tolist() == want == [62, 64, 60, 62, 64]
+    np.testing.assert_array_equal(R.stored(cache.k.cpu()), ref.pool["k"])
+    np.testing.assert_array_equal(R.stored(cache.v.cpu()), ref.pool["v"])
+    np.testing.assert_array_equal(wd.cpu().numpy(), want_w)
+
+
 # ----------------------------------------------------------------- together
 
 def draft_loop(fa, steps=6, kind=E4M3, graph=False, stream=None):
