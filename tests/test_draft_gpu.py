@@ -269,6 +269,54 @@ def test_tree_nan_and_infinite_scores(fa, n):
     assert not torch.isnan(w[0, 0, 100 + hidden.to(DEV)]).any() and torch.isnan(w[0, 0, :100]).all()
 
 
+@pytest.mark.parametrize("D,page,kind,io,Hq,Hkv,n", [
+    (64, 16, E4M3, BF16, 2, 1, 6), (128, 64, I8, F16, 4, 2, 8), (128, 16, E4M3, BF16, 8, 2, 6), (64, 16, I8, F16, 2, 1, 20),
+    (128, 64, E4M3, BF16, 2, 1, 60), (256, 16, E4M3, F16, 2, 1, 9), (256, 64, I8, BF16, 4, 2, 40), (64, 32, E4M3, F16, 8, 4, 90)])
+@pytest.mark.parametrize("L", [0, 100, 900])
+@pytest.mark.parametrize("ctas", [0, 2])
+@pytest.mark.parametrize("track", [False, True])
+def test_tree_infinite_scores(fa, D, page, kind, io, Hq, Hkv, n, L, ctas, track):
+    """Node 2's key has a score of +infinity with the rows of a group's first head, all others -infinity: what sees it
+    is NaN, and the weights of the tokens that it sees; the head's other rows see as good as nothing, and the other
+    heads' are what they are."""
+    g = torch.Generator().manual_seed(n + L)
+    group, length = Hq // Hkv, L + n
+    table, P, _ = R.make_table(g, [length], page)
+    pools = R.make_pools(g, P, Hkv, page, D, kind)
+    tree = [-1, 0, 0, 2, 1, 2] + [4] * (n - 6)
+    pools[0][..., 0] = torch.tensor(-8.0).to(kind)
+    pools[0][table[0][(L + 2) // page], :, (L + 2) % page, 0] = torch.tensor(8.0).to(kind)
+    q = torch.randn(1, Hq, n, D, generator=g).to(io)
+    plain = q.clone()
+    q[:, ::group, :, 0] = float("inf")
+    w = torch.zeros(1, Hkv, length, device=DEV)
+    fa.fa_set_max_ctas(ctas)
+    try:
+        o, lse = fa.cache_attention(q.to(DEV), to_gpu(fa, pools), i32(table), i32([length]), tree=i32([tree]),
+                                    weights=w if track else None)
+    finally:
+        fa.fa_set_max_ctas(0)
+    synced(fa)
+    o, lse, w = o.double().cpu(), lse.double().cpu(), w.double().cpu()
+    sees = torch.tensor([2 in T.line(tree, i) for i in range(n)])
+    assert torch.isnan(lse[:, ::group, sees]).all() and torch.isnan(o[:, ::group, sees]).all()
+    assert torch.isneginf(lse[:, ::group, ~sees]).all() and (o[:, ::group, ~sees] == 0).all()
+    others = torch.arange(Hq) % group > 0
+    for h in range(Hkv):  # (each group's other heads, by themselves)
+        part = R.Cache(*(t[:, h:h + 1] for t in pools))
+        mine = others.clone()
+        mine[:h * group], mine[(h + 1) * group:] = False, False
+        ro, rl, rw, a, sabs = T.attention(part, plain[:, mine], table, [length], [tree])
+        tol_l = 2.0 ** -18 * sabs[0] + 1e-6  # (as in check_attention)
+        assert np.all(np.abs(lse[:, mine].numpy() - rl) <= tol_l)
+        assert np.all(np.abs(o[:, mine].numpy() - ro) <= HALF[io] * np.abs(ro) + (HALF[F16] + 2 * tol_l) * a + 1e-7)
+        if track:
+            seen = T.visible(tree, length, n)[sees.numpy()].any(0)
+            hidden = np.nonzero(~seen)[0]
+            assert 0 < len(hidden) < n and torch.isnan(w[0, h][torch.from_numpy(seen)]).all()
+            assert np.all(np.abs(w[0, h, hidden].numpy() - rw[0, 0, hidden]) <= (2.0 ** -22 + 2 * tol_l) * rw[0, 0, hidden])
+
+
 def many_rows(fa, D, page, Hq, Hkv, n, lens, kind=E4M3):
     g = torch.Generator().manual_seed(D + n)
     rng = random.Random(n)
