@@ -368,6 +368,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyPara
     }
     const Pair x = pair_normal(ver_warp_sum(row.sum(e0, e1)));
     if (lane < blocks) ver_send(&s.sum[passes & 1][rank * kVerWarps + warp], (uint32_t)lane, x);
+    __syncwarp();  // (the barrier takes whole warps)
     ver_cluster_sync();
   }
 
