@@ -540,6 +540,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
         if constexpr (C::kSplit) info->rs[tl] = rs;
       }
       if constexpr (C::kSplit) {
+        __syncwarp();  // (here and below: bar.sync and tcgen05's .aligned forms take whole warps)
         named_bar_sync(3, 256);
         rs = info->rs[tl];
       }
@@ -593,6 +594,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
             for (int k = 0; k < kMine; ++k)
               if (!((seen[k / 32] >> (k & 31)) & 1u)) x[k] = 0xFF800000u;
           }
+          __syncwarp();
           // Group by group: a raw score times f plus y is the score's weight in
           // base 2 (s + log2 vs); y = -inf where nothing is stored.
           float f[kGroups], y[kGroups], inv_vs[kGroups], mx, part;
@@ -640,6 +642,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
               corr = ex2(m - r);  // 0 when m = -inf
               m = r;
             }
+            __syncwarp();
           }
           l = fmaf(l, corr, part);
           if constexpr (C::kDup > 1) {  // the other copies' keys weigh nothing here
@@ -785,6 +788,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
         if (tl == 0 && !whole && !head_cut)
           p.cuts[blockIdx.x] = make_int4(at.b, at.h, at.rg, (at.seg0 + tiles - 1) / at.part);
       }
+      __syncwarp();
       if constexpr (C::kSplit) named_bar_sync(3, 256);  // both outputs have been read
       before += n;
       pos = at.seg0 + tiles;
@@ -794,6 +798,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) cache_drafts_kernel(const __gr
       if ((warp & 3) == 0) info->n[pieces & 1] = 0;
       mbar_arrive(&info->q_full);
     }
+    __syncwarp();
     tmem_wait_st();  // (behind an expired wait, weights may be on their way to memory that is given back below)
   }
   tc_fence_before();
