@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(128) cache_weights_kernel(const __grid_constan
     uint32_t sa = 0u, sb = 0u;
     if constexpr (kTree) {
       sa = weight_seen(tree, seq, pos0, ia, tok0) >> (2 * t), sb = weight_seen(tree, seq, pos0, ib, tok0) >> (2 * t);
+      __syncwarp();  // (each lane has walked for itself; the next rows' products take whole warps)
     } else {
       va = dec_span(a, seq, ia, ia), vb = dec_span(a, seq, ib, ib);
     }
