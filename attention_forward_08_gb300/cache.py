@@ -525,8 +525,8 @@ def cache_accept(cache, table, lens, path, count, *, n_q=None, weights=None, len
     path, count: int32 [B, n] and [B] as ``verify_drafts`` gives them: the rows that stay, ascending, and how many.
     n_q: int32 [B], the drafts of each sequence (all n if None).
     weights: fp32 [B, H_kv, W], moved along; positions need no change.
-    lens_out: where the new lengths go (may be ``lens``); allocated here if None.  With caches of several layers,
-    each call is given the lengths that the drafts are counted in.
+    lens_out: where the new lengths go (may be ``lens``, but no other argument's memory); allocated here if None.  With
+    caches of several layers, each call is given the lengths that the drafts are counted in.
     """
     device, c, B = cache.device, cache.c, table.shape[0]
     t_ptr, t_stride, M = _table(device, "table", table, B, "M")

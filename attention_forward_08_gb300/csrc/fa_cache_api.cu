@@ -263,6 +263,12 @@ int check_attn_tree(const fa_cache_attn_tree_args* a) {
   return rc;
 }
 
+// Do n ints at a and m ints at b (or none: NULL) share memory?
+bool overlap(const int* a, long long n, const int* b, long long m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return b && x < y + 4 * (uintptr_t)m && y < x + 4 * (uintptr_t)n;
+}
+
 int check_accept(const fa_cache_accept_args* a) {
   if (!a) return invalid("args is NULL");
   int rc = check_cache(a->cache);
@@ -284,6 +290,15 @@ int check_accept(const fa_cache_accept_args* a) {
     set_error("path, count, n_q, weights and lens_out must be 4-byte aligned");
     return FA_ERR_MISALIGNED;
   }
+  // One block of a sequence writes lens_out while its others still read (lens
+  // itself is written behind them, a sequence's by a block that has read its own).
+  const long long B = a->B;
+  const auto apart = [&](const int* x, long long n) {
+    return !overlap(a->lens_out, B, x, n) || (a->lens_out == a->lens && x == a->lens && n == B);
+  };
+  if (!apart(a->lens, B) || !apart(a->count, B) || !apart(a->n_q, B) || !apart(a->path, (B - 1) * a->path_stride + a->n) ||
+      !apart(a->table, (B - 1) * a->table_stride + a->M))
+    return invalid("lens_out must be lens itself, or share no memory with lens, n_q, path, count and table");
   return FA_OK;
 }
 

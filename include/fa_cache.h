@@ -254,7 +254,7 @@ int fa_verify_drafts(const fa_verify_drafts_args* args);
  * weights: NULL or fp32 contiguous [B, H_kv, W], moved along.  (A slot's position
  * is that of the path's token that it receives: fa_cache_append's numbers stay.)
  * Slots behind lens_out[b] keep what they held.
- * lens_out may be lens itself.
+ * lens_out may be lens itself; it shares no other memory with the inputs.
  * A path that does not ascend, leaves [0, n_q[b]), or (lens[b] past the table)
  * reaches a draft that the table has no slot for, ends before that entry;
  * count[b] is cut to [0, n_q[b]]; a sequence with fewer tokens than drafts, or

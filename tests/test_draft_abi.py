@@ -118,6 +118,27 @@ def test_refusals(fa, which, kw, status, needle):
         assert fa.fa_cache_attn_tree_workspace_bytes(a) == -1
 
 
+APART = dict(lens=P + 64, count=P + 4096, path=P + 8192, table=P + 12288)  # (2 sequences, 5 drafts, 4 blocks)
+
+
+@pytest.mark.parametrize("kw", [dict(lens_out=P + 64 + 4), dict(lens_out=P + 64 - 4), dict(lens_out=P + 4096),
+                                dict(lens_out=P + 4096 - 4), dict(n_q=P + 16384, lens_out=P + 16384 + 4),
+                                dict(lens_out=P + 8192 + 36), dict(path_stride=9, lens_out=P + 8192 + 52),
+                                dict(lens_out=P + 12288 + 28), dict(lens_out=P + 64, n_q=P + 68)])
+def test_accept_refuses_lengths_over_what_it_reads(fa, kw):
+    """Blocks of a sequence read its numbers while one of them writes lens_out."""
+    assert fa.fa_cache_accept(draft_args(fa, "accept", **{**APART, **kw})) == 1
+    assert "share no memory" in fa.fa_last_error()
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are stand-ins")
+@pytest.mark.parametrize("lens_out", [P + 64, P + 64 + 8, P + 64 - 8, P + 4096 - 8, P + 8192 + 40, P + 12288 + 32])
+def test_accept_takes_lengths_that_are_lens_or_apart(fa, lens_out):
+    for n_q in (None, P + 64):
+        fa.fa_cache_accept(draft_args(fa, "accept", **APART, lens_out=lens_out, n_q=n_q if lens_out == P + 64 else None))
+        assert "share no memory" not in fa.fa_last_error()  # (there is no device)
+
+
 def test_null_args(fa):
     lib = fa.cache._library()
     for name in ("fa_cache_attn_tree", "fa_verify_drafts", "fa_cache_accept"):
