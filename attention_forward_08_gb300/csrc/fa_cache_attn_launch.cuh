@@ -202,7 +202,8 @@ int launch_drafts(const CacheAttnParams& a, int kind, bool f16, const LaunchCtx&
 // (32 rows, 8 heads of 128: 1000 tokens 17.7 us against 20.6 with 32 rows in registers,
 // 4 sequences of 8192 33.3 against 38.6, 131071 tokens 82.6 against 85.1; 17 rows there
 // 83.3 against 82.2; 16 rows of 256: 53.4 against 41.9, 12 of 128, 16 sequences of 8192:
-// 83.1 against 59.5); with weights, behind what keeps its scores.
+// 83.1 against 59.5); with weights, behind the rows whose scores can be kept (where a
+// wide table alone forbids that, they stay with the decode kernel all the same).
 enum class AttnPlan { kRows16, kRows32, kDrafts, kPrompt };
 template <int kD>
 AttnPlan attn_plan(const CacheAttnParams& a) {

@@ -64,7 +64,9 @@ struct DraftCfg {
   // What a piece costs before and behind its keys, in blocks of keys: parts of the line
   // that begin more segments get fewer keys.  (64 rows of 16 sequences of up to 8192
   // tokens, D 128: 76 us with 0, 70.4 with 6, 69.7 with 8, 74 with 12; 240 rows: 76, 67.5,
-  // 67.3, 72; D 256: 66, 65.2 with 3, 65.0 with 5, 71 with 8.)
+  // 67.3, 72; D 256: 66, 65.2 with 3, 65.0 with 5, 71 with 8; D 64, 104 rows at 131071
+  // tokens: 92.7 with 0, 87.6 with 5, 86.7 with 10, 86.4 with 15, and 33 rows of 16
+  // sequences of up to 8192: 57.8, 53.4, 55.4, 58.3.)
   static constexpr int kLead = kD == 64 ? 10 : kD == 128 ? 8 : 5;
   static constexpr int kLift = 7;
   static constexpr int kKeys = 64;   // keys a score buffer: a unit

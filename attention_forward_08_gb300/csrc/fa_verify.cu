@@ -27,9 +27,10 @@
 // reads that again, a run of entries a thread.
 //
 // Bound: latency (three dependent loads and two cluster barriers: one sequence of 5
-// nodes, 32000 entries, 9.8 us); then the sums' instructions, some 30 an entry of p
-// and q (32 sequences of 128001 fp32 entries, up to three passes one after the
-// other, 28 us; 64 of 100000 bf16 entries without q, 18 us, 0.7 TB/s).
+// nodes, 32000 entries, 9.2 us); then the sums' instructions, some 30 an entry of p
+// and q (32 sequences of 16 nodes, 128001 bf16 entries, up to three passes one after
+// the other, 29 us; of 17 nodes other draws, 27 us in bf16, 30 in fp16 and in fp32;
+// 64 of 100000 bf16 entries without q, 18 us, 0.7 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

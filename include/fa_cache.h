@@ -19,7 +19,8 @@
  * A length past the table (lens[b] > M * page), a negative one, or an entry
  * outside [0, P) that a sequence needs is not followed: the tokens behind it
  * are skipped (not written; not seen by attention; not moved by eviction) and
- * fa_sync_status() then reports FA_ERR_INVALID_ARGUMENT once.
+ * fa_sync_status() then reports FA_ERR_INVALID_ARGUMENT once.  (Attention takes a
+ * length past the table as M * page, its rows' positions with it.)
  *
  * Memory: every pointer is caller-owned device memory on the current device;
  * nothing is allocated, and nothing is kept after the call's kernels have run.
